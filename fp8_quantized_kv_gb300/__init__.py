@@ -12,6 +12,7 @@ runs in the library's CUDA kernels.  torch provides device memory and streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from typing import Optional
@@ -25,7 +26,7 @@ DTYPES = {"k8v8": K8V8, "k16v8": K16V8, "k16v16": K16V16, "k8v16": K8V16, "mxk8v
 LAYOUT_CONTIGUOUS, LAYOUT_PAGED = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 
-DEVERR_SEQ_TOO_LONG, DEVERR_BAD_PAGE, DEVERR_TIMEOUT = 0x1, 0x2, 0x4
+DEVERR_SEQ_TOO_LONG, DEVERR_BAD_PAGE, DEVERR_TIMEOUT, DEVERR_NO_PAGES = 0x1, 0x2, 0x4, 0x8
 STEP_EARLY_CACHE_READ = 0x1
 KERNEL_AUTO, KERNEL_CUDA_CORES, KERNEL_TENSOR_CORES = 0, 1, 2
 KERNEL_TENSOR_CORES_K_F16, KERNEL_TENSOR_CORES_K_F16_PRODUCER = 3, 4
@@ -324,6 +325,139 @@ def fp8kv_prefill_attention(q: torch.Tensor, cache: Fp8KVCache, q_pos0: torch.Te
     return out
 
 
+# ----------------------------------------------------- serving-step calls --
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _here(t: torch.Tensor, dtype, name, shape=None, contiguous=True):
+    """A CUDA tensor of `dtype` on the current device (the launch goes to that
+    device's stream), contiguous unless said otherwise; returns its address."""
+    if t.dtype is not dtype or not t.is_cuda or (contiguous and not t.is_contiguous()):
+        raise ValueError(f"{name}: expected a {'contiguous ' if contiguous else ''}CUDA {dtype} tensor, got "
+                         f"{t.dtype} on {t.device} (contiguous={t.is_contiguous()})")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _cache_here(cache: Fp8KVCache):
+    if cache.k.get_device() != torch.cuda.current_device():
+        raise ValueError(f"cache: on {cache.k.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _on(stream):
+    """Allocations of a call that launches on `stream` belong to that stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _raw_stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def fp8kv_build_tables(cache: Fp8KVCache, cached_lens: torch.Tensor, new_lens: torch.Tensor, n_rows: int,
+                       free_pages: Optional[torch.Tensor] = None, free_head: Optional[torch.Tensor] = None,
+                       cu_new=None, seq_lens=None, seq_idx=None, pos=None, slots=None, free_head_out=None,
+                       stream=None):
+    """Page tables and slot maps of one step: sequence b holds cached_lens[b]
+    tokens and gets new_lens[b] more ([B] int32 each).  Fresh pages come from
+    free_pages[free_head:] ([F], [1] int32; paged caches only) and go into
+    cache.page_table in place.  Returns a dict of cu_new [B + 1], seq_lens [B],
+    seq_idx and pos [n_rows] (int32), slots [n_rows] (int64) and free_head [1]
+    (None for a contiguous cache); rows behind the last sequence hold -1.
+    Output tensors may be passed in and may not be input tensors."""
+    B, N = cache.batch, int(n_rows)
+    paged = cache.layout == LAYOUT_PAGED
+    if paged != (free_pages is not None) or paged != (free_head is not None):
+        raise ValueError("free_pages and free_head come with a paged cache, and only with one")
+    _cache_here(cache)
+    a_cached = _here(cached_lens, torch.int32, "cached_lens", (B,))
+    a_new = _here(new_lens, torch.int32, "new_lens", (B,))
+    F, a_free, a_head = 0, None, None
+    if paged:
+        F = free_pages.numel()
+        a_free, a_head = _here(free_pages, torch.int32, "free_pages", (F,)), _here(free_head, torch.int32, "free_head", (1,))
+    if cu_new is None or seq_lens is None or seq_idx is None or pos is None or slots is None or \
+            (paged and free_head_out is None):
+        with _on(stream):
+            def new(t, shape, dtype=torch.int32):
+                return torch.empty(shape, dtype=dtype, device=cache.k.device) if t is None else t
+            cu_new, seq_lens, seq_idx, pos = new(cu_new, B + 1), new(seq_lens, B), new(seq_idx, N), new(pos, N)
+            slots = new(slots, N, torch.int64)
+            free_head_out = new(free_head_out, 1) if paged else free_head_out
+    a_out = None if free_head_out is None else _here(free_head_out, torch.int32, "free_head_out", (1,))
+    _check(get_lib().fp8kv_build_tables(
+        cache.struct_ref, a_cached, a_new, a_free, F, a_head, N, _here(cu_new, torch.int32, "cu_new", (B + 1,)),
+        _here(seq_lens, torch.int32, "seq_lens", (B,)), _here(seq_idx, torch.int32, "seq_idx", (N,)),
+        _here(pos, torch.int32, "pos", (N,)), _here(slots, torch.int64, "slots", (N,)), a_out, _raw_stream(stream)),
+        "fp8kv_build_tables")
+    return {"cu_new": cu_new, "seq_lens": seq_lens, "seq_idx": seq_idx, "pos": pos, "slots": slots,
+            "free_head": free_head_out}
+
+
+def fp8kv_rope_tables(positions: int, rot_dim: int, base: float = 10000.0, factor: float = 1.0,
+                      original_positions: int = 0, ramp=(1.0, 4.0), amplitude: float = 1.0,
+                      cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, stream=None):
+    """cos and sin [positions, rot_dim / 2] fp32 of t * base^(-2 i / rot_dim).
+    factor > 1 stretches the context: every pair, or (original_positions > 0)
+    those that turn fewer than ramp[1] times within original_positions, fully
+    below ramp[0] turns.  amplitude scales both tables."""
+    if cos is None or sin is None:
+        with _on(stream):
+            shape = (int(positions), int(rot_dim) // 2)
+            cos = torch.empty(shape, device="cuda") if cos is None else cos
+            sin = torch.empty(shape, device="cuda") if sin is None else sin
+    shape = (positions, rot_dim // 2)
+    _check(get_lib().fp8kv_rope_tables(
+        positions, rot_dim, base, factor, original_positions, ramp[0], ramp[1], amplitude,
+        _here(cos, torch.float32, "cos", shape), _here(sin, torch.float32, "sin", shape), _raw_stream(stream)),
+        "fp8kv_rope_tables")
+    return cos, sin
+
+
+def _rows(t, heads, dim, n, name):
+    """[n, heads, dim] bf16 whose tokens may lie apart (a slice of a fused
+    projection): address and token stride."""
+    a = _here(t, torch.bfloat16, name, (n, heads, dim), contiguous=False)
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != dim):
+        raise ValueError(f"{name}: heads of a token must lie side by side, got strides {t.stride()}")
+    return a, (s0 if n > 1 else max(s0, heads * dim))
+
+
+def fp8kv_rope_append(cache: Fp8KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
+                      slots: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor, layout="half",
+                      q_out: Optional[torch.Tensor] = None, stream=None):
+    """Rotate q [n, Hq, D] and k [n, Hkv, D] (bf16; token strides as in a
+    slice of a fused projection) at positions pos [n] int32 with the tables
+    cos, sin [positions, R / 2], write k and v quantised into the cache at
+    slots [n] int64 (negative: padding, row skipped) and return the rotated
+    queries [n, Hq, D] bf16 (q_out; may be q)."""
+    n, Hq, D = q.shape
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout: expected one of {tuple(ROPE_LAYOUTS)}, got {layout!r}")
+    if cos.dim() != 2:
+        raise ValueError(f"cos: expected [positions, rot_dim / 2], got {tuple(cos.shape)}")
+    if D != cache.head_dim:
+        raise ValueError(f"q: head dim {D}, but the cache's is {cache.head_dim}")
+    _cache_here(cache)
+    a_q, s_q = _rows(q, Hq, D, n, "q")
+    a_k, s_k = _rows(k, cache.kv_heads, D, n, "k")
+    a_v, s_v = _rows(v, cache.kv_heads, D, n, "v")
+    if q_out is None:
+        with _on(stream):
+            q_out = torch.empty((n, Hq, D), dtype=torch.bfloat16, device=q.device)
+    T, half = cos.shape
+    _check(get_lib().fp8kv_rope_append(
+        cache.struct_ref, a_q, s_q, a_k, s_k, a_v, s_v, Hq, _here(pos, torch.int32, "pos", (n,)),
+        _here(slots, torch.int64, "slots", (n,)), n, _here(cos, torch.float32, "cos"),
+        _here(sin, torch.float32, "sin", (T, half)), T, 2 * half, ROPE_LAYOUTS[layout],
+        _here(q_out, torch.bfloat16, "q_out", (n, Hq, D)), _raw_stream(stream)), "fp8kv_rope_append")
+    return q_out
+
+
 def fp8kv_get_device_error(clear: bool = True) -> int:
     """Synchronise the device and return (optionally clearing) the device
     error word (bits DEVERR_*)."""
@@ -342,5 +476,6 @@ __all__ = ["Fp8KVCache", "Fp8KVError", "fp8kv_quantize", "fp8kv_quantize_mx", "f
            "fp8kv_decode_num_splits", "fp8kv_decode_workspace_bytes", "fp8kv_decode_split",
            "fp8kv_decode_merge", "fp8kv_decode_attention", "fp8kv_decode_step",
            "fp8kv_decode_step_workspace_bytes",
-           "fp8kv_prefill_attention", "fp8kv_get_device_error", "fp8kv_status_string",
+           "fp8kv_prefill_attention", "fp8kv_build_tables", "fp8kv_rope_tables", "fp8kv_rope_append",
+           "fp8kv_get_device_error", "fp8kv_status_string",
            "EXPORTS", "K8V8", "K16V8", "K16V16", "K8V16", "MXK8V8"]

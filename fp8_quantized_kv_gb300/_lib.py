@@ -24,6 +24,9 @@ EXPORTS = (
     "fp8kv_decode_attention_static",
     "fp8kv_decode_static_scratch_bytes",
     "fp8kv_prefill_attention",
+    "fp8kv_build_tables",
+    "fp8kv_rope_tables",
+    "fp8kv_rope_append",
     "fp8kv_get_device_error",
     "fp8kv_status_string",
 )
@@ -66,7 +69,7 @@ def get_lib() -> ctypes.CDLL:
             "(the FP8-KV kernels have no fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, f32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
-    u32 = ctypes.c_uint32
+    u32, f64 = ctypes.c_uint32, ctypes.c_double
     cp = ctypes.POINTER(CacheStruct)
     sig = {
         "fp8kv_quantize": (i32, [vp, i64, i32, vp, vp, vp]),
@@ -82,6 +85,9 @@ def get_lib() -> ctypes.CDLL:
         "fp8kv_decode_attention_static": (i32, [vp, cp, vp, i32, f32, i32, vp, i32, vp]),
         "fp8kv_decode_static_scratch_bytes": (sz, []),
         "fp8kv_prefill_attention": (i32, [vp, cp, vp, i32, i32, f32, i32, vp, i32, vp]),
+        "fp8kv_build_tables": (i32, [cp, vp, vp, vp, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp]),
+        "fp8kv_rope_tables": (i32, [i64, i32, f64, f64, i32, f64, f64, f64, vp, vp, vp]),
+        "fp8kv_rope_append": (i32, [cp, vp, i64, vp, i64, vp, i64, i32, vp, vp, i64, vp, vp, i32, i32, i32, vp, vp]),
         "fp8kv_get_device_error": (i32, [ctypes.POINTER(ctypes.c_uint32), i32]),
         "fp8kv_status_string": (ctypes.c_char_p, [i32]),
     }

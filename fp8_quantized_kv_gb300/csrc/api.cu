@@ -17,7 +17,7 @@ __device__ unsigned int g_device_error;
 // Per-device values looked up on first use and kept; atomics, so host
 // threads making their first call at once (each looking the value up and
 // storing the same result) do not race.
-static unsigned int* device_error_ptr() {
+unsigned int* device_error_ptr() {
   constexpr int kMaxDev = 64;
   static std::atomic<unsigned int*> ptrs[kMaxDev];
   int dev = 0;
@@ -33,7 +33,7 @@ static unsigned int* device_error_ptr() {
   return p;
 }
 
-static int sm_count() {
+int sm_count() {
   constexpr int kMaxDev = 64;
   static std::atomic<int> counts[kMaxDev];
   int dev = 0;
@@ -52,7 +52,7 @@ static int sm_count() {
 
 static bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
-static fp8kv_status check_cache(const fp8kv_cache* c, CacheView* view) {
+fp8kv_status check_cache(const fp8kv_cache* c, CacheView* view) {
   if (c == nullptr) return FP8KV_ERR_INVALID_ARG;
   if (c->dtype < FP8KV_K8V8 || c->dtype > FP8KV_MXK8V8) return FP8KV_ERR_INVALID_ARG;
   if (c->layout != FP8KV_LAYOUT_CONTIGUOUS && c->layout != FP8KV_LAYOUT_PAGED) return FP8KV_ERR_INVALID_ARG;
@@ -113,7 +113,7 @@ static fp8kv_status check_cache(const fp8kv_cache* c, CacheView* view) {
   return FP8KV_OK;
 }
 
-static int capacity_of(const fp8kv_cache* c) {
+int capacity_of(const fp8kv_cache* c) {
   return c->layout == FP8KV_LAYOUT_PAGED ? c->max_pages_per_seq * c->page_size : c->max_tokens;
 }
 
@@ -187,15 +187,15 @@ static SplitPlan plan_splits(const fp8kv_cache* c, int requested, int kernel, in
   return {splits, chunk, tile, kernel};
 }
 
-}  // namespace fp8kv
-
-using namespace fp8kv;
-
-static fp8kv_status cuda_status(cudaError_t e) {
+fp8kv_status cuda_status(cudaError_t e) {
   if (e == cudaSuccess) return FP8KV_OK;
   (void)cudaGetLastError();
   return FP8KV_ERR_CUDA;
 }
+
+}  // namespace fp8kv
+
+using namespace fp8kv;
 
 extern "C" {
 

@@ -1,0 +1,147 @@
+// api_step.cu -- the extern "C" boundary of the serving-step calls: argument
+// checks, launch plans, status codes.  As in api.cu, every entry validates on
+// the host, launches on the caller's stream and allocates nothing.
+#include <cmath>
+#include <cstdint>
+
+#include "params.cuh"
+
+using namespace fp8kv;
+
+namespace {
+
+struct Range { const void* p; size_t bytes; };
+
+bool overlap(const Range& a, const Range& b) {
+  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x < y + b.bytes && y < x + a.bytes;
+}
+
+bool misaligned(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; }
+
+}  // namespace
+
+extern "C" {
+
+fp8kv_status fp8kv_build_tables(const fp8kv_cache* cache, const int32_t* cached_lens, const int32_t* new_lens,
+                                const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
+                                int64_t n_rows, int32_t* cu_new, int32_t* seq_lens, int32_t* seq_idx, int32_t* pos,
+                                int64_t* slots, int32_t* free_head_out, fp8kv_stream_t stream) {
+  CacheView view;
+  const fp8kv_status st = check_cache(cache, &view);
+  if (st != FP8KV_OK) return st;
+  if (n_rows < 0 || num_free < 0 || cu_new == nullptr) return FP8KV_ERR_INVALID_ARG;
+  if (cache->batch > kTablesMaxBatch || n_rows > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
+  if (cache->batch > 0 && (!cached_lens || !new_lens || !seq_lens)) return FP8KV_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!seq_idx || !pos || !slots)) return FP8KV_ERR_INVALID_ARG;
+  if (view.paged) {
+    if (!free_head || !free_head_out || (num_free > 0 && !free_pages)) return FP8KV_ERR_INVALID_ARG;
+  } else if (free_pages || num_free || free_head || free_head_out) {
+    return FP8KV_ERR_INVALID_ARG;
+  }
+  const size_t B = (size_t)cache->batch, N = (size_t)n_rows;
+  const Range in[] = {{cached_lens, 4 * B}, {new_lens, 4 * B}, {free_pages, 4 * (size_t)num_free}, {free_head, 4},
+                      {view.page_table, 4 * B * (size_t)view.max_pages_per_seq}};
+  const Range out[] = {{cu_new, 4 * (B + 1)}, {seq_lens, 4 * B}, {seq_idx, 4 * N},
+                       {pos, 4 * N}, {slots, 8 * N}, {free_head_out, 4}};
+  for (int i = 0; i < 6; ++i) {
+    for (const Range& r : in)
+      if (overlap(r, out[i])) return FP8KV_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[j], out[i])) return FP8KV_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < 4; ++i)
+    if (overlap(in[i], in[4])) return FP8KV_ERR_INVALID_ARG;      // the page table is written in place
+  unsigned int* err = device_error_ptr();
+  if (!err) return FP8KV_ERR_CUDA;
+  return cuda_status(launch_build_tables(view, cached_lens, new_lens, free_pages, num_free, free_head, (int)n_rows,
+                                         cu_new, seq_lens, seq_idx, pos, slots, free_head_out, err,
+                                         (cudaStream_t)stream));
+}
+
+fp8kv_status fp8kv_rope_tables(int64_t positions, int32_t rot_dim, double base, double factor,
+                               int32_t original_positions, double ramp_low, double ramp_high, double amplitude,
+                               float* cos, float* sin, fp8kv_stream_t stream) {
+  if (positions < 0 || rot_dim <= 0 || original_positions < 0) return FP8KV_ERR_INVALID_ARG;
+  if (!(base > 0) || !std::isfinite(base) || !(factor > 0) || !std::isfinite(factor) || !std::isfinite(amplitude))
+    return FP8KV_ERR_INVALID_ARG;
+  if (original_positions > 0 && !(std::isfinite(ramp_low) && std::isfinite(ramp_high) && ramp_low < ramp_high))
+    return FP8KV_ERR_INVALID_ARG;
+  if (rot_dim % 2 != 0 || rot_dim > 2 * kRopeMaxPairs || positions > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
+  if (positions == 0) return FP8KV_OK;
+  if (!cos || !sin) return FP8KV_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)positions * (rot_dim / 2) * sizeof(float);
+  if (overlap({cos, bytes}, {sin, bytes})) return FP8KV_ERR_INVALID_ARG;
+  constexpr double kTwoPi = 6.283185307179586476925;
+  unsigned long long w[kRopeMaxPairs];
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (original_positions > 0) {
+      double g = (original_positions * f / kTwoPi - ramp_low) / (ramp_high - ramp_low);
+      g = g < 0 ? 0 : g > 1 ? 1 : g;
+      f *= g + (1 - g) / factor;
+    } else {
+      f /= factor;
+    }
+    // the frequency in turns per position, modulo one turn (positions are
+    // whole numbers), as a 64-bit binary fraction
+    double turns = f / kTwoPi;
+    turns -= std::floor(turns);
+    const double scaled = std::ldexp(turns, 64);
+    w[i] = scaled >= 18446744073709551616.0 ? 0 : (unsigned long long)scaled;
+  }
+  return cuda_status(launch_rope_tables((int)positions, rot_dim / 2, w, (float)amplitude, cos, sin,
+                                        (cudaStream_t)stream));
+}
+
+fp8kv_status fp8kv_rope_append(const fp8kv_cache* cache, const void* q, int64_t q_stride, const void* k,
+                               int64_t k_stride, const void* v, int64_t v_stride, int32_t q_heads,
+                               const int32_t* pos, const int64_t* slots, int64_t n_tokens, const float* cos,
+                               const float* sin, int32_t positions, int32_t rot_dim, int32_t layout, void* q_out,
+                               fp8kv_stream_t stream) {
+  RopeAppendParams p;
+  const fp8kv_status st = check_cache(cache, &p.c);
+  if (st != FP8KV_OK) return st;
+  if (n_tokens < 0 || q_heads <= 0 || positions < 0 || rot_dim <= 0) return FP8KV_ERR_INVALID_ARG;
+  if (layout != FP8KV_ROPE_HALF && layout != FP8KV_ROPE_INTERLEAVED) return FP8KV_ERR_INVALID_ARG;
+  if (rot_dim > cache->head_dim) return FP8KV_ERR_INVALID_ARG;
+  if (rot_dim % 8 != 0 || n_tokens > INT32_MAX || q_heads > 65535) return FP8KV_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return FP8KV_OK;
+  if (!q || !k || !v || !pos || !slots || !cos || !sin || !q_out) return FP8KV_ERR_INVALID_ARG;
+  const int64_t qw = (int64_t)q_heads * cache->head_dim, kw = (int64_t)cache->kv_heads * cache->head_dim;
+  if (q_stride < qw || k_stride < kw || v_stride < kw) return FP8KV_ERR_INVALID_ARG;
+  if (q_stride % 8 || k_stride % 8 || v_stride % 8) return FP8KV_ERR_INVALID_ARG;
+  for (const void* a : {q, k, v, (const void*)cos, (const void*)sin, (const void*)q_out})
+    if (misaligned(a, 16)) return FP8KV_ERR_INVALID_ARG;
+  if (misaligned(slots, 8) || misaligned(pos, 4)) return FP8KV_ERR_INVALID_ARG;
+  // q_out: a buffer of its own, or q rotated in place
+  const int64_t N = n_tokens;
+  const Range out = {q_out, (size_t)(2 * N * qw)};
+  if (!(q_out == q && q_stride == qw) && overlap(out, {q, (size_t)(2 * ((N - 1) * q_stride + qw))}))
+    return FP8KV_ERR_INVALID_ARG;
+  if (overlap(out, {k, (size_t)(2 * ((N - 1) * k_stride + kw))}) ||
+      overlap(out, {v, (size_t)(2 * ((N - 1) * v_stride + kw))}))
+    return FP8KV_ERR_INVALID_ARG;
+  p.err = device_error_ptr();
+  if (!p.err) return FP8KV_ERR_CUDA;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.pos = pos;
+  p.slots = slots;
+  p.cos = cos;
+  p.sin = sin;
+  p.n = n_tokens;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_heads = q_heads;
+  p.rot = rot_dim;
+  p.positions = positions;
+  p.interleaved = layout == FP8KV_ROPE_INTERLEAVED;
+  return cuda_status(launch_rope_append(p, cache->dtype, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -53,6 +53,24 @@ struct PrefillParams {
   float scale_log2;
 };
 
+// Limits of the step tables: sequences of one fp8kv_build_tables call (three
+// integers each in a CTA's shared memory), pairs of a rotary table.
+constexpr int kTablesMaxBatch = 16384;
+constexpr int kRopeMaxPairs = 128;
+
+struct RopeAppendParams {
+  CacheView c;
+  const __nv_bfloat16 *q, *k, *v;   // rows [n][heads][D], one token every *_stride elements
+  __nv_bfloat16* q_out;             // [n][Hq][D]
+  const int32_t* pos;               // [n]
+  const int64_t* slots;             // [n], negative: padding
+  const float *cos, *sin;           // [positions][rot / 2]
+  unsigned int* err;
+  int64_t n, q_stride, k_stride, v_stride;
+  int q_heads, rot, positions, interleaved;
+  int groups, per_group;            // warps per token, row passes per warp
+};
+
 cudaError_t launch_quantize(const void* x, int64_t rows, int head_dim, uint8_t* codes, float* scales,
                             cudaStream_t s);
 cudaError_t launch_quantize_mx(const void* x, int64_t rows, int head_dim, uint8_t* codes, uint8_t* scales,
@@ -68,5 +86,19 @@ cudaError_t launch_decode_merge(const float* part_o, const float* part_m, const 
                                 int64_t rows, int head_dim, void* out, int out_f32, cudaStream_t st);
 cudaError_t launch_prefill_fma(const PrefillParams& p, int dtype, int batch, cudaStream_t st);
 cudaError_t launch_prefill_tc(const PrefillParams& p, int batch, cudaStream_t st);
+cudaError_t launch_build_tables(const CacheView& c, const int32_t* cached, const int32_t* fresh,
+                                const int32_t* free_pages, int num_free, const int32_t* free_head, int rows,
+                                int32_t* cu, int32_t* seq_lens, int32_t* seq_idx, int32_t* pos, int64_t* slots,
+                                int32_t* head_out, unsigned int* err, cudaStream_t s);
+cudaError_t launch_rope_tables(int positions, int pairs, const unsigned long long* w, float amplitude, float* cos,
+                               float* sin, cudaStream_t s);
+cudaError_t launch_rope_append(RopeAppendParams& p, int dtype, cudaStream_t s);
+
+// Host-side pieces of the C-ABI layer (api.cu).
+unsigned int* device_error_ptr();
+int sm_count();
+fp8kv_status check_cache(const fp8kv_cache* c, CacheView* view);
+int capacity_of(const fp8kv_cache* c);
+fp8kv_status cuda_status(cudaError_t e);
 
 }  // namespace fp8kv

@@ -1,0 +1,237 @@
+// step_tables.cu -- what a serving step needs before its attention runs: the
+// page tables and slot maps of a ragged batch, built on the GPU from the
+// requests' lengths, and the rotary tables.
+//
+// Page tables and slot maps.  Sequence b holds c_b tokens and gets n_b more:
+//   cu_b    = sum of n_b' over b' < b              first row of the sequence
+//   first_b = ceil(c_b / P), last_b = ceil((c_b + n_b) / P)
+//   base_b  = sum of (last_b' - first_b') over b' < b
+//   page i of [first_b, last_b) = free_pages[head + base_b + i - first_b]
+//   row cu_b + j: position t = c_b + j, slot = page(t / P) P + t mod P
+// A row's page is either one that the sequence had before (read from the
+// table, at an entry this call does not write) or a fresh one (read from the
+// free list), so no thread reads what another writes and one launch does it
+// all.  Every CTA scans the lengths itself: 4 bytes a sequence, against the
+// second launch (about 2 us) that sharing one scan would take.
+#include "params.cuh"
+
+namespace fp8kv {
+
+constexpr int kTablesThreads = 256;
+
+// Inclusive sums over the CTA of two values per thread.
+__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long* wa, long long* wb) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, a, o);
+    const long long y = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) { a += x; b += y; }
+  }
+  if (lane == 31) { wa[warp] = a; wb[warp] = b; }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kTablesThreads / 32; ++w)
+    if (w < warp) { a += wa[w]; b += wb[w]; }
+}
+
+struct TablesParams {
+  const int32_t *cached, *fresh, *free_pages, *free_head;
+  int32_t* table;              // page table, written in place (null: contiguous cache)
+  int32_t *cu, *seq_lens, *seq_idx, *pos, *head_out;
+  int64_t* slots;
+  unsigned int* err;
+  int batch, num_free, rows, page_shift, num_pages, max_pages, max_tokens;
+};
+
+// Thread i places fresh page i (a fresh page holds at least one new row, so
+// there are no more of them than rows) and writes row i's entries.
+__global__ void __launch_bounds__(kTablesThreads) build_tables_kernel(const TablesParams p) {
+  extern __shared__ int32_t tsm[];
+  int32_t* cu = tsm;                                   // [batch + 1] first row of each sequence
+  int32_t* base = cu + p.batch + 1;                    // [batch + 1] first fresh page of each sequence
+  int32_t* cached = base + p.batch + 1;                // [batch] tokens before the step, -1: not placed
+  __shared__ long long wa[kTablesThreads / 32];
+  __shared__ long long wb[kTablesThreads / 32];
+  __shared__ long long tot_rows, tot_pages;
+  const int tid = threadIdx.x;
+  const bool paged = p.table != nullptr;
+  const int P1 = (1 << p.page_shift) - 1;
+  const long long cap = paged ? (long long)p.max_pages << p.page_shift : p.max_tokens;
+  const int head = paged ? *p.free_head : 0;
+  const int avail = paged ? (head < 0 || head > p.num_free ? 0 : p.num_free - head) : 0;
+  const bool lead = blockIdx.x == 0;
+  unsigned int bad = 0;
+  if (tid == 0) { tot_rows = 0; tot_pages = 0; cu[0] = 0; base[0] = 0; }
+  if (paged && (head < 0 || head > p.num_free)) bad |= FP8KV_DEVERR_NO_PAGES;
+  __syncthreads();
+  for (int b0 = 0; b0 < p.batch; b0 += kTablesThreads) {
+    const int b = b0 + tid;
+    int c = 0, n = 0, need = 0;
+    bool fits = true;
+    if (b < p.batch) {
+      c = p.cached[b];
+      n = p.fresh[b];
+      // a length below 0 or past the cache's capacity: the sequence keeps its
+      // rows (so that the others' rows stay where the caller has them) and
+      // gets no page
+      fits = c >= 0 && n >= 0 && (long long)c + n <= cap;
+      if (!fits) bad |= FP8KV_DEVERR_SEQ_TOO_LONG;
+      if (n < 0) n = 0;
+      if (fits && paged) need = ((c + n + P1) >> p.page_shift) - ((c + P1) >> p.page_shift);
+    }
+    long long a = n, f = need;
+    block_scan2(a, f, wa, wb);
+    const long long rows_end = tot_rows + a, pages_end = tot_pages + f;
+    if (b < p.batch) {
+      if (fits && need > 0 && pages_end > avail) { fits = false; bad |= FP8KV_DEVERR_NO_PAGES; }
+      cu[b + 1] = (int)min(rows_end, (long long)INT32_MAX);
+      base[b + 1] = (int)min(pages_end, (long long)INT32_MAX);
+      cached[b] = fits ? c : -1;
+      if (lead) p.seq_lens[b] = fits ? c + n : max(c, 0);
+      if (b == p.batch - 1 && rows_end > p.rows) bad |= FP8KV_DEVERR_SEQ_TOO_LONG;
+    }
+    __syncthreads();
+    if (tid == kTablesThreads - 1) { tot_rows = rows_end; tot_pages = pages_end; }
+    __syncthreads();
+  }
+  if (lead) {
+    for (int b = tid; b <= p.batch; b += kTablesThreads) p.cu[b] = cu[b];
+    if (tid == 0 && paged) {
+      // pages placed: sequences take them in order, so those that got theirs
+      // are the ones whose range ends within the list
+      int lo = 0, hi = p.batch;                        // largest b with base[b] <= avail
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (base[mid] <= avail) lo = mid; else hi = mid - 1;
+      }
+      *p.head_out = head + base[lo];
+    }
+  }
+  const int i = blockIdx.x * kTablesThreads + tid;
+  // fresh page f
+  for (long long f = i; paged && f < base[p.batch]; f += (long long)gridDim.x * kTablesThreads) {
+    int lo = 0, hi = p.batch - 1;                      // sequence with base[b] <= f < base[b + 1]
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (base[mid + 1] > f) hi = mid; else lo = mid + 1;
+    }
+    const int c = cached[lo];
+    if (c >= 0) {
+      int page = p.free_pages[head + f];
+      if (page < 0 || page >= p.num_pages) { page = -1; bad |= FP8KV_DEVERR_BAD_PAGE; }
+      p.table[(int64_t)lo * p.max_pages + ((c + P1) >> p.page_shift) + (f - base[lo])] = page;
+    }
+  }
+  // row i
+  if (i < p.rows) {
+    int b = -1, t = -1;
+    long long slot = -1;
+    if (i < cu[p.batch]) {
+      int lo = 0, hi = p.batch - 1;                    // sequence with cu[b] <= i < cu[b + 1]
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (cu[mid + 1] > i) hi = mid; else lo = mid + 1;
+      }
+      b = lo;
+      const int c = cached[lo];
+      if (c >= 0) {
+        t = c + (i - cu[lo]);
+        if (!paged) {
+          slot = (long long)lo * p.max_tokens + t;
+        } else {
+          const int pi = t >> p.page_shift, first = (c + P1) >> p.page_shift;
+          const int page = pi < first ? p.table[(int64_t)lo * p.max_pages + pi]
+                                      : p.free_pages[head + base[lo] + pi - first];
+          if (page < 0 || page >= p.num_pages) bad |= FP8KV_DEVERR_BAD_PAGE;
+          else slot = ((long long)page << p.page_shift) + (t & P1);
+        }
+      }
+    }
+    p.seq_idx[i] = b;
+    p.pos[i] = t;
+    p.slots[i] = slot;
+  }
+  if (bad) raise_error(p.err, bad);
+}
+
+cudaError_t launch_build_tables(const CacheView& c, const int32_t* cached, const int32_t* fresh,
+                                const int32_t* free_pages, int num_free, const int32_t* free_head, int rows,
+                                int32_t* cu, int32_t* seq_lens, int32_t* seq_idx, int32_t* pos, int64_t* slots,
+                                int32_t* head_out, unsigned int* err, cudaStream_t s) {
+  TablesParams p;
+  p.cached = cached;
+  p.fresh = fresh;
+  p.free_pages = free_pages;
+  p.free_head = free_head;
+  p.table = const_cast<int32_t*>(c.page_table);
+  p.cu = cu;
+  p.seq_lens = seq_lens;
+  p.seq_idx = seq_idx;
+  p.pos = pos;
+  p.slots = slots;
+  p.head_out = head_out;
+  p.err = err;
+  p.batch = c.batch;
+  p.num_free = num_free;
+  p.rows = rows;
+  p.page_shift = c.page_shift;
+  p.num_pages = c.num_pages;
+  p.max_pages = c.max_pages_per_seq;
+  p.max_tokens = c.max_tokens;
+  constexpr int most = (3 * kTablesMaxBatch + 2) * (int)sizeof(int32_t);
+  const int bytes = (3 * c.batch + 2) * (int)sizeof(int32_t);
+  if (bytes > 40 * 1024) {
+    const cudaError_t e = ensure_smem_optin((const void*)build_tables_kernel, most);
+    if (e != cudaSuccess) return e;
+  }
+  const int grid = rows > 0 ? (rows - 1) / kTablesThreads + 1 : 1;
+  build_tables_kernel<<<grid, kTablesThreads, bytes, s>>>(p);
+  return cudaGetLastError();
+}
+
+// Rotary tables.  cos and sin of theta = t w_i for positions t and pairs i.
+// With w_i in turns as a 64-bit binary fraction W_i (host, fp64), the phase
+// t W_i mod 2^64 is exact integer arithmetic: far positions lose nothing but
+// t 2^-56 turns, the rounding of W_i itself.  Its top two bits (after adding
+// an eighth of a turn) pick the quadrant, the rest is an angle in
+// [-pi/4, pi/4] whose sine and cosine are taken in fp32.
+struct RopeTablesParams {
+  unsigned long long w[kRopeMaxPairs];
+  float *cos, *sin;
+  float amplitude;
+  int positions, pairs;
+};
+
+__global__ void __launch_bounds__(256) rope_tables_kernel(const __grid_constant__ RopeTablesParams p) {
+  const long long n = (long long)p.positions * p.pairs;
+  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (long long)gridDim.x * blockDim.x) {
+    const int t = (int)(e / p.pairs), i = (int)(e - (long long)t * p.pairs);
+    const unsigned int phase = (unsigned int)(((unsigned long long)(unsigned int)t * p.w[i]) >> 32);
+    const unsigned int quad = (phase + 0x20000000u) >> 30;
+    const int rest = (int)(phase - (quad << 30));
+    float sn, cs;
+    sincosf((float)rest * 1.4629180792671596e-09f, &sn, &cs);      // 2 pi / 2^32
+    const float c = quad == 0 ? cs : quad == 1 ? -sn : quad == 2 ? -cs : sn;
+    const float s = quad == 0 ? sn : quad == 1 ? cs : quad == 2 ? -sn : -cs;
+    p.cos[e] = c * p.amplitude;
+    p.sin[e] = s * p.amplitude;
+  }
+}
+
+cudaError_t launch_rope_tables(int positions, int pairs, const unsigned long long* w, float amplitude, float* cos,
+                               float* sin, cudaStream_t s) {
+  if (positions == 0) return cudaSuccess;
+  RopeTablesParams p;
+  for (int i = 0; i < kRopeMaxPairs; ++i) p.w[i] = i < pairs ? w[i] : 0;
+  p.cos = cos;
+  p.sin = sin;
+  p.amplitude = amplitude;
+  p.positions = positions;
+  p.pairs = pairs;
+  const long long blocks = ((long long)positions * pairs + 255) / 256;
+  rope_tables_kernel<<<(unsigned)(blocks < 4864 ? blocks : 4864), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace fp8kv

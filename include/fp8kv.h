@@ -127,6 +127,7 @@ typedef enum {
 #define FP8KV_DEVERR_SEQ_TOO_LONG 0x1u   /* a length/position exceeds the cache */
 #define FP8KV_DEVERR_BAD_PAGE 0x2u       /* a page id outside [0, num_pages)    */
 #define FP8KV_DEVERR_TIMEOUT 0x4u        /* a bounded mbarrier wait ran out    */
+#define FP8KV_DEVERR_NO_PAGES 0x8u       /* a step needs more pages than are free */
 
 /* A KV cache.  The struct is read on the host at every call (pass it by
  * pointer; it may live on the stack).  All pointers are device pointers owned
@@ -350,6 +351,90 @@ FP8KV_API fp8kv_status fp8kv_prefill_attention(const void *q, const fp8kv_cache 
                                      const int32_t *q_pos0, int32_t n_q,
                                      int32_t q_heads, float sm_scale, int32_t kernel,
                                      void *out, int32_t out_dtype, fp8kv_stream_t stream);
+
+/* The tables of one serving step over a ragged batch, built on the GPU from
+ * the requests' lengths: sequence b holds cached_lens[b] tokens and gets
+ * new_lens[b] more (0 is allowed: an idle request).  Fresh pages come from
+ * free_pages in order, from index *free_head on, sequence by sequence.
+ *   cached_lens, new_lens: [batch] int32
+ *   free_pages:    [num_free] int32 page ids (paged cache; NULL, with num_free
+ *                  0 and both heads NULL, for a contiguous one)
+ *   free_head:     [1] int32, first entry of free_pages not yet handed out
+ *   n_rows:        rows of seq_idx, pos and slots; rows behind the last
+ *                  sequence's (padding) get -1 in all three
+ *   cu_new:        [batch + 1] int32, first row of each sequence
+ *   seq_lens:      [batch] int32, cached_lens + new_lens
+ *   seq_idx, pos:  [n_rows] int32, sequence and position of each row, as
+ *                  fp8kv_append takes them (without padding: it reports -1)
+ *   slots:         [n_rows] int64, where each row goes: page_id * page_size +
+ *                  t % page_size (paged), b * max_tokens + t (contiguous)
+ *   free_head_out: [1] int32, free_head plus the pages handed out
+ * The entries of cache->page_table for the fresh pages are written in place;
+ * all others stay.  Outputs may not overlap inputs (FP8KV_ERR_INVALID_ARG):
+ * to run steps from a graph, copy seq_lens and free_head_out back between
+ * two steps.  At most 16384 sequences (else FP8KV_ERR_UNSUPPORTED).
+ * A sequence that cannot be placed keeps its rows with slot and pos -1, gets
+ * no page, has seq_lens = cached_lens, and raises a device error bit:
+ * SEQ_TOO_LONG for a negative length or one past the capacity, NO_PAGES when
+ * the free list does not hold all of its pages (later sequences that need
+ * pages fail too).  An invalid page id gives slot -1 and BAD_PAGE; new rows
+ * past n_rows raise SEQ_TOO_LONG. */
+FP8KV_API fp8kv_status fp8kv_build_tables(const fp8kv_cache *cache, const int32_t *cached_lens,
+                                          const int32_t *new_lens, const int32_t *free_pages,
+                                          int32_t num_free, const int32_t *free_head, int64_t n_rows,
+                                          int32_t *cu_new, int32_t *seq_lens, int32_t *seq_idx,
+                                          int32_t *pos, int64_t *slots, int32_t *free_head_out,
+                                          fp8kv_stream_t stream);
+
+/* Rotary tables: cos and sin of t * w_i for positions t in [0, positions) and
+ * pairs i in [0, rot_dim / 2), times `amplitude`, as fp8kv_rope_append and
+ * fp8kv_cache.rope_cos / rope_sin read them.  w_i = base^(-2 i / rot_dim),
+ * changed for contexts longer than the model was trained on:
+ *   original_positions 0: w_i / factor for every pair;
+ *   else, with turns_i = original_positions * w_i / (2 pi) (how often the pair
+ *   turns within the trained length) and g_i = (turns_i - ramp_low) /
+ *   (ramp_high - ramp_low) clamped to [0, 1]: w_i (g_i + (1 - g_i) / factor),
+ *   so fast pairs stay and slow ones are stretched.
+ * The angle at position t is off by at most t * 2^-55 of a turn (w_i is held
+ * as a binary fraction of a turn, so far positions lose nothing else).
+ *   rot_dim:  even, 2 to 256 (else FP8KV_ERR_UNSUPPORTED)
+ *   cos, sin: [positions][rot_dim / 2] fp32 */
+FP8KV_API fp8kv_status fp8kv_rope_tables(int64_t positions, int32_t rot_dim, double base, double factor,
+                                         int32_t original_positions, double ramp_low, double ramp_high,
+                                         double amplitude, float *cos, float *sin, fp8kv_stream_t stream);
+
+/* Which elements of a head form rotary pair i (rot_dim = R). */
+typedef enum {
+  FP8KV_ROPE_HALF = 0,        /* dims i and i + R / 2 */
+  FP8KV_ROPE_INTERLEAVED = 1  /* dims 2 i and 2 i + 1 */
+} fp8kv_rope_layout;
+
+/* Rotate the new tokens' queries and keys and write keys and values into the
+ * cache, in one launch.  Row n at position pos[n]: the first rot_dim elements
+ * of every query and key head turn pairwise, (a, b) -> (a cos - b sin,
+ * b cos + a sin) in fp32 with each product and sum rounded once; the rest of
+ * the head stays.  Queries are rounded to bf16 into q_out.  Keys are quantised
+ * from fp32 as fp8kv_append quantises them (or rounded to bf16 for a bf16
+ * side; a k_bias is subtracted first), values likewise without rotation, and
+ * both are written to slot slots[n] (fp8kv_build_tables).
+ *   q:             [n][q_heads][head_dim] bf16, token n at q + n * q_stride
+ *   k, v:          [n][kv_heads][head_dim] bf16, at k_stride and v_stride
+ *                  (strides in elements, multiples of 8; pointers 16-byte
+ *                  aligned: slices of one projection's output qualify)
+ *   cos, sin:      [positions][rot_dim / 2] fp32, 16-byte aligned
+ *   rot_dim:       a multiple of 8 from 8 to head_dim (else UNSUPPORTED)
+ *   q_out:         [n][q_heads][head_dim] bf16; may be q itself if
+ *                  q_stride = q_heads * head_dim
+ * A row with a negative slot is padding: nothing of it is read or written.
+ * A row whose position has no table entry or whose slot lies outside the
+ * cache is skipped and raises SEQ_TOO_LONG or BAD_PAGE.  Two rows of one call
+ * may not share a slot (which row's codes and scale stay is not defined). */
+FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q, int64_t q_stride,
+                                         const void *k, int64_t k_stride, const void *v,
+                                         int64_t v_stride, int32_t q_heads, const int32_t *pos,
+                                         const int64_t *slots, int64_t n_tokens, const float *cos,
+                                         const float *sin, int32_t positions, int32_t rot_dim,
+                                         int32_t layout, void *q_out, fp8kv_stream_t stream);
 
 /* Read (and, if `clear` is non-zero, reset) the device error word of the
  * current device.  Synchronous: waits for all work on the device. */

@@ -1,0 +1,96 @@
+"""Refusals of the serving-step calls, on the host: every call below is turned
+down by its argument checks, before any CUDA call.  No GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import fp8_quantized_kv_gb300 as fk
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from fp8_quantized_kv_gb300 import build as kbuild
+    from fp8_quantized_kv_gb300._lib import get_lib
+    kbuild.build()
+    return get_lib()
+
+
+def _cache(**kw):
+    from fp8_quantized_kv_gb300._lib import CacheStruct
+    base = dict(dtype=0, layout=0, batch=4, kv_heads=2, head_dim=128, max_tokens=1024,
+                k=0x1000, v=0x2000, k_scale=0x3000, v_scale=0x4000)
+    base.update(kw)
+    return ctypes.byref(CacheStruct(**base))
+
+
+def _paged(**kw):
+    return _cache(**{**dict(layout=1, max_tokens=0, page_size=16, num_pages=64, max_pages_per_seq=8, page_table=0x5000), **kw})
+
+
+def _tables(lib, cache, **kw):
+    a = dict(cached=0x10000, new=0x11000, free=0x12000, num_free=16, head=0x13000, rows=8, cu=0x14000, lens=0x15000,
+             seq=0x16000, pos=0x17000, slots=0x18000, head_out=0x19000)
+    a.update(kw)
+    return lib.fp8kv_build_tables(cache, a["cached"], a["new"], a["free"], a["num_free"], a["head"], a["rows"], a["cu"], a["lens"],
+                                  a["seq"], a["pos"], a["slots"], a["head_out"], None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(rows=-1)), (INVALID, dict(num_free=-1)), (INVALID, dict(cached=None)), (INVALID, dict(new=None)),
+    (INVALID, dict(cu=None)), (INVALID, dict(lens=None)), (INVALID, dict(seq=None)), (INVALID, dict(slots=None)),
+    (INVALID, dict(free=None)), (INVALID, dict(head=None)), (INVALID, dict(head_out=None)),
+    (INVALID, dict(lens=0x10000)), (INVALID, dict(head_out=0x13000)),      # outputs over inputs
+    (INVALID, dict(pos=0x16004)), (INVALID, dict(cu=0x5000)), (INVALID, dict(cached=0x5000)),
+    (UNSUPPORTED, dict(rows=1 << 31)),
+])
+def test_tables_refusals(lib, want, kw):
+    assert _tables(lib, _paged(), **kw) == want
+
+
+def test_tables_refusals_by_cache(lib):
+    assert _tables(lib, _paged(batch=16385)) == UNSUPPORTED
+    assert _tables(lib, _paged(page_size=8)) == UNSUPPORTED
+    assert _tables(lib, _cache()) == INVALID                               # a free list with a contiguous cache
+    assert _tables(lib, None) == INVALID
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(positions=-1)), (INVALID, dict(rot=0)), (INVALID, dict(base=0.0)), (INVALID, dict(base=float("inf"))),
+    (INVALID, dict(factor=0.0)), (INVALID, dict(factor=float("nan"))), (INVALID, dict(amplitude=float("inf"))),
+    (INVALID, dict(original=-1)), (INVALID, dict(original=64, lo=2.0, hi=2.0)), (INVALID, dict(original=64, lo=float("nan"))),
+    (INVALID, dict(cos=None)), (INVALID, dict(sin=0x20010)), (UNSUPPORTED, dict(rot=7)), (UNSUPPORTED, dict(rot=258)),
+    (UNSUPPORTED, dict(positions=1 << 31)),
+])
+def test_rope_tables_refusals(lib, want, kw):
+    a = dict(positions=100, rot=64, base=1e4, factor=1.0, original=0, lo=1.0, hi=4.0, amplitude=1.0, cos=0x20000, sin=0x80000)
+    a.update(kw)
+    assert lib.fp8kv_rope_tables(*a.values(), None) == want
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(n=-1)), (INVALID, dict(q_heads=0)), (INVALID, dict(rot=0)), (INVALID, dict(rot=136)), (INVALID, dict(layout=2)),
+    (INVALID, dict(q=None)), (INVALID, dict(k=None)), (INVALID, dict(pos=None)), (INVALID, dict(slots=None)), (INVALID, dict(cos=None)),
+    (INVALID, dict(q_out=None)), (INVALID, dict(q=0x100008)), (INVALID, dict(qs=512 - 8)), (INVALID, dict(ks=252)),
+    (INVALID, dict(vs=260)), (INVALID, dict(q_out=0x100010)), (INVALID, dict(qs=1024, q_out=0x100000)), (INVALID, dict(q_out=0x200000)),
+    (INVALID, dict(slots=0x500004)), (UNSUPPORTED, dict(rot=12)), (UNSUPPORTED, dict(n=1 << 31)),
+])
+def test_rope_append_refusals(lib, want, kw):
+    a = dict(q=0x100000, qs=512, k=0x200000, ks=256, v=0x300000, vs=256, q_heads=4, pos=0x400000, slots=0x500000, n=16,
+             cos=0x600000, sin=0x700000, positions=64, rot=64, layout=0, q_out=0x800000)
+    a.update(kw)
+    assert lib.fp8kv_rope_append(_cache(), *a.values(), None) == want
+
+
+def test_python_argument_checks():
+    """The binding turns wrong tensors down by name."""
+    t = torch.zeros(4, dtype=torch.int32)
+    with pytest.raises(ValueError, match="pos: expected a contiguous CUDA"):
+        fk._here(t, torch.int32, "pos")
+    with pytest.raises(ValueError, match="free_pages and free_head"):
+        cache = type("C", (), dict(layout=fk.LAYOUT_PAGED, batch=4))()
+        fk.fp8kv_build_tables(cache, t, t, 4)
+    with pytest.raises(ValueError, match="layout"):
+        fk.fp8kv_rope_append(None, torch.zeros(1, 2, 64), None, None, t, t, t, t, layout="quarter")
