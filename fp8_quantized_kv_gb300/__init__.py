@@ -29,10 +29,10 @@ OUT_BF16, OUT_F32 = 0, 1
 DEVERR_SEQ_TOO_LONG, DEVERR_BAD_PAGE, DEVERR_TIMEOUT, DEVERR_NO_PAGES = 0x1, 0x2, 0x4, 0x8
 STEP_EARLY_CACHE_READ = 0x1
 KERNEL_AUTO, KERNEL_CUDA_CORES, KERNEL_TENSOR_CORES = 0, 1, 2
-KERNEL_TENSOR_CORES_K_F16, KERNEL_TENSOR_CORES_K_F16_PRODUCER = 3, 4
+KERNEL_TENSOR_CORES_K_F16, KERNEL_TENSOR_CORES_K_F16_PRODUCER, KERNEL_WARP_MMA = 3, 4, 5
 KERNELS = {"auto": KERNEL_AUTO, "cuda_cores": KERNEL_CUDA_CORES, "tensor_cores": KERNEL_TENSOR_CORES,
            "tensor_cores_k_f16": KERNEL_TENSOR_CORES_K_F16,
-           "tensor_cores_k_f16_producer": KERNEL_TENSOR_CORES_K_F16_PRODUCER}
+           "tensor_cores_k_f16_producer": KERNEL_TENSOR_CORES_K_F16_PRODUCER, "warp_mma": KERNEL_WARP_MMA}
 
 STATUS_NAMES = {0: "FP8KV_OK", 1: "FP8KV_ERR_INVALID_ARG", 2: "FP8KV_ERR_UNSUPPORTED",
                 3: "FP8KV_ERR_WORKSPACE", 4: "FP8KV_ERR_CUDA", 5: "FP8KV_ERR_TIMEOUT",
@@ -458,6 +458,52 @@ def fp8kv_rope_append(cache: Fp8KVCache, q: torch.Tensor, k: torch.Tensor, v: to
     return q_out
 
 
+def fp8kv_chunk_num_splits(cache: Fp8KVCache, total_q: int, q_heads: int, window: int = 0, sinks: int = 0,
+                           num_splits: int = 0, kernel=0) -> int:
+    return int(get_lib().fp8kv_chunk_num_splits(cache.struct_ref, total_q, q_heads, window, sinks, num_splits, _kernel(kernel)))
+
+
+def fp8kv_chunk_workspace_bytes(cache: Fp8KVCache, total_q: int, q_heads: int, window: int = 0, sinks: int = 0,
+                                num_splits: int = 0, kernel=0) -> int:
+    return int(get_lib().fp8kv_chunk_workspace_bytes(cache.struct_ref, total_q, q_heads, window, sinks, num_splits,
+                                                     _kernel(kernel)))
+
+
+def fp8kv_chunk_attention(q: torch.Tensor, cache: Fp8KVCache, cu_q: Optional[torch.Tensor], seq_lens: torch.Tensor,
+                          sm_scale: Optional[float] = None, window: int = 0, sinks: int = 0, num_splits: int = 0,
+                          out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                          workspace: Optional[torch.Tensor] = None, kernel="auto", stream=None):
+    """Ragged chunk attention: q [total_q, Hq, D] bf16, sequence b's queries in
+    rows cu_q[b]..cu_q[b+1]-1 (cu_q [B + 1] int32, or None: one query per
+    sequence), the last at position seq_lens[b] - 1 of its cached tokens.
+    window > 0: a query sees the last `window` tokens, its own among them, and
+    the first `sinks`.  Returns out [total_q, Hq, D]; rows outside every
+    sequence stay as they were (an `out` made here holds anything there).
+    kernel: "auto" or "warp_mma"."""
+    total_q, Hq, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError(f"q: head dim {D}, but the cache's is {cache.head_dim}")
+    _cache_here(cache)
+    a_q = _here(q, torch.bfloat16, "q")
+    k = _kernel(kernel)
+    if out is None or workspace is None:
+        with _on(stream):
+            if out is None:
+                out = torch.empty((total_q, Hq, D), dtype=out_dtype, device=q.device)
+            if workspace is None:
+                need = fp8kv_chunk_workspace_bytes(cache, total_q, Hq, window, sinks, num_splits, k)
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"out: expected bf16 or fp32, got {out.dtype}")
+    _check(get_lib().fp8kv_chunk_attention(
+        a_q, cache.struct_ref, None if cu_q is None else _here(cu_q, torch.int32, "cu_q", (cache.batch + 1,)),
+        _here(seq_lens, torch.int32, "seq_lens", (cache.batch,)), total_q, Hq,
+        1.0 / math.sqrt(D) if sm_scale is None else sm_scale, window, sinks, num_splits, k,
+        _here(workspace, torch.uint8, "workspace"), workspace.numel(), _here(out, out.dtype, "out", (total_q, Hq, D)),
+        OUT_F32 if out.dtype == torch.float32 else OUT_BF16, _raw_stream(stream)), "fp8kv_chunk_attention")
+    return out
+
+
 def fp8kv_get_device_error(clear: bool = True) -> int:
     """Synchronise the device and return (optionally clearing) the device
     error word (bits DEVERR_*)."""
@@ -477,5 +523,6 @@ __all__ = ["Fp8KVCache", "Fp8KVError", "fp8kv_quantize", "fp8kv_quantize_mx", "f
            "fp8kv_decode_merge", "fp8kv_decode_attention", "fp8kv_decode_step",
            "fp8kv_decode_step_workspace_bytes",
            "fp8kv_prefill_attention", "fp8kv_build_tables", "fp8kv_rope_tables", "fp8kv_rope_append",
+           "fp8kv_chunk_num_splits", "fp8kv_chunk_workspace_bytes", "fp8kv_chunk_attention",
            "fp8kv_get_device_error", "fp8kv_status_string",
            "EXPORTS", "K8V8", "K16V8", "K16V16", "K8V16", "MXK8V8"]

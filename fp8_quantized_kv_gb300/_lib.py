@@ -27,6 +27,9 @@ EXPORTS = (
     "fp8kv_build_tables",
     "fp8kv_rope_tables",
     "fp8kv_rope_append",
+    "fp8kv_chunk_num_splits",
+    "fp8kv_chunk_workspace_bytes",
+    "fp8kv_chunk_attention",
     "fp8kv_get_device_error",
     "fp8kv_status_string",
 )
@@ -88,6 +91,9 @@ def get_lib() -> ctypes.CDLL:
         "fp8kv_build_tables": (i32, [cp, vp, vp, vp, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp]),
         "fp8kv_rope_tables": (i32, [i64, i32, f64, f64, i32, f64, f64, f64, vp, vp, vp]),
         "fp8kv_rope_append": (i32, [cp, vp, i64, vp, i64, vp, i64, i32, vp, vp, i64, vp, vp, i32, i32, i32, vp, vp]),
+        "fp8kv_chunk_num_splits": (i32, [cp, i64, i32, i32, i32, i32, i32]),
+        "fp8kv_chunk_workspace_bytes": (sz, [cp, i64, i32, i32, i32, i32, i32]),
+        "fp8kv_chunk_attention": (i32, [vp, cp, vp, vp, i64, i32, f32, i32, i32, i32, i32, vp, sz, vp, i32, vp]),
         "fp8kv_get_device_error": (i32, [ctypes.POINTER(ctypes.c_uint32), i32]),
         "fp8kv_status_string": (ctypes.c_char_p, [i32]),
     }

@@ -20,6 +20,43 @@ bool overlap(const Range& a, const Range& b) {
 
 bool misaligned(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; }
 
+struct ChunkPlan { int kernel, row_warps, tile_tokens, tiles, splits; };
+
+// How a chunk call runs.  Tiles: rows per tile by the average number of query
+// rows (queries x heads of a group) a sequence has, so that short chunks do
+// not carry empty rows.  Splits: only when there are fewer tiles than the GPU
+// can hold CTAs.
+fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int window, int sinks, int num_splits,
+                        int kernel, ChunkPlan* plan) {
+  if (total_q < 0 || q_heads <= 0 || q_heads % c->kv_heads != 0 || window < 0 || sinks < 0 || num_splits < 0)
+    return FP8KV_ERR_INVALID_ARG;
+  if (kernel != FP8KV_KERNEL_AUTO && kernel != FP8KV_KERNEL_WARP_MMA) return FP8KV_ERR_INVALID_ARG;
+  const int G = q_heads / c->kv_heads;
+  if (G > 16 || c->rope_cos != nullptr || c->kv_heads > 65535 || num_splits > 4096) return FP8KV_ERR_UNSUPPORTED;
+  if (total_q > INT32_MAX || (double)total_q * q_heads > 8.0 * INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
+  const int64_t B = c->batch > 0 ? c->batch : 1;
+  const int64_t rows = (total_q + B - 1) / B * G;
+  plan->kernel = FP8KV_KERNEL_WARP_MMA;
+  plan->row_warps = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  plan->tile_tokens = 16 * plan->row_warps / G;
+  const int64_t tiles = total_q / plan->tile_tokens + c->batch;
+  if (tiles > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
+  plan->tiles = (int)tiles;
+  const int cap = capacity_of(c);
+  const int64_t seen = window > 0 && window < cap ? (int64_t)window + plan->tile_tokens + (sinks < cap ? sinks : cap) : cap;
+  const int64_t kv_tiles = ((seen < cap ? seen : cap) + 63) / 64 + 1;
+  int64_t want = num_splits;
+  if (want == 0) {
+    const int64_t units = tiles * c->kv_heads, target = 2 * (int64_t)sm_count();
+    want = units > 0 ? target / units : 1;
+    if (want > kv_tiles / 4) want = kv_tiles / 4;
+  }
+  if (want > kv_tiles) want = kv_tiles;
+  if (want > 4096) want = 4096;
+  plan->splits = want < 1 ? 1 : (int)want;
+  return FP8KV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -142,6 +179,66 @@ fp8kv_status fp8kv_rope_append(const fp8kv_cache* cache, const void* q, int64_t 
   p.positions = positions;
   p.interleaved = layout == FP8KV_ROPE_INTERLEAVED;
   return cuda_status(launch_rope_append(p, cache->dtype, (cudaStream_t)stream));
+}
+
+int32_t fp8kv_chunk_num_splits(const fp8kv_cache* cache, int64_t total_q, int32_t q_heads, int32_t window,
+                               int32_t sinks, int32_t num_splits, int32_t kernel) {
+  CacheView view;
+  ChunkPlan plan;
+  if (check_cache(cache, &view) != FP8KV_OK) return 0;
+  if (plan_chunk(cache, total_q, q_heads, window, sinks, num_splits, kernel, &plan) != FP8KV_OK) return 0;
+  return plan.splits;
+}
+
+size_t fp8kv_chunk_workspace_bytes(const fp8kv_cache* cache, int64_t total_q, int32_t q_heads, int32_t window,
+                                   int32_t sinks, int32_t num_splits, int32_t kernel) {
+  const int S = fp8kv_chunk_num_splits(cache, total_q, q_heads, window, sinks, num_splits, kernel);
+  if (S <= 1) return 0;
+  return (size_t)total_q * q_heads * S * ((size_t)cache->head_dim + 2) * sizeof(float);
+}
+
+fp8kv_status fp8kv_chunk_attention(const void* q, const fp8kv_cache* cache, const int32_t* cu_q,
+                                   const int32_t* seq_lens, int64_t total_q, int32_t q_heads, float sm_scale,
+                                   int32_t window, int32_t sinks, int32_t num_splits, int32_t kernel,
+                                   void* workspace, size_t workspace_bytes, void* out, int32_t out_dtype,
+                                   fp8kv_stream_t stream) {
+  ChunkParams p;
+  fp8kv_status st = check_cache(cache, &p.c);
+  if (st != FP8KV_OK) return st;
+  ChunkPlan plan;
+  st = plan_chunk(cache, total_q, q_heads, window, sinks, num_splits, kernel, &plan);
+  if (st != FP8KV_OK) return st;
+  if (out_dtype != FP8KV_OUT_BF16 && out_dtype != FP8KV_OUT_F32) return FP8KV_ERR_INVALID_ARG;
+  if (!std::isfinite(sm_scale)) return FP8KV_ERR_INVALID_ARG;
+  if (cu_q == nullptr && total_q != cache->batch) return FP8KV_ERR_INVALID_ARG;
+  if (cache->batch == 0 || total_q == 0) return FP8KV_OK;
+  if (!q || !seq_lens || !out || misaligned(q, 16) || misaligned(out, 16)) return FP8KV_ERR_INVALID_ARG;
+  const int64_t rows = total_q * q_heads;
+  const size_t need = fp8kv_chunk_workspace_bytes(cache, total_q, q_heads, window, sinks, num_splits, kernel);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FP8KV_ERR_WORKSPACE;
+  if (need > 0 && misaligned(workspace, 16)) return FP8KV_ERR_INVALID_ARG;
+  p.err = device_error_ptr();
+  if (!p.err) return FP8KV_ERR_CUDA;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.cu_q = cu_q;
+  p.seq_lens = seq_lens;
+  p.out = out;
+  p.part_o = plan.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  p.part_m = plan.splits > 1 ? p.part_o + rows * plan.splits * cache->head_dim : nullptr;
+  p.part_l = plan.splits > 1 ? p.part_m + rows * plan.splits : nullptr;
+  p.total_q = (int)total_q;
+  p.q_heads = q_heads;
+  p.group = q_heads / cache->kv_heads;
+  p.out_f32 = out_dtype == FP8KV_OUT_F32;
+  p.window = window < capacity_of(cache) ? window : 0;
+  p.sinks = sinks;
+  p.num_splits = plan.splits;
+  p.tile_tokens = plan.tile_tokens;
+  p.scale_log2 = sm_scale * kLog2e;
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = launch_chunk_mma(p, cache->dtype, plan.row_warps, cu_q ? plan.tiles : cache->batch, s);
+  if (e == cudaSuccess && plan.splits > 1) e = launch_chunk_merge(p, s);
+  return cuda_status(e);
 }
 
 }  // extern "C"

@@ -1,0 +1,659 @@
+// chunk_mma.cu -- ragged chunk attention over the cache on warp-level matrix
+// instructions, for every cache type and head dim: the form for few query
+// rows per sequence (single tokens, drafted tokens), where reading the cache
+// bounds the time, and for the types the tcgen05 kernel is not built for.
+//
+// One pass over the keys with a running maximum m, sum l and output O:
+//   s = (q . k) k_scale sm_scale log2(e),  m' = max(m, max s),
+//   l = l 2^(m - m') + sum 2^(s - m'),     O = O 2^(m - m') + 2^(s - m') V
+// 128 threads; a CTA owns 16 MW query rows of one KV head (rows = tokens x
+// heads of the group) and walks 64-key tiles through a ring of NS cp.async
+// stages.  MW = 4: a warp owns 16 rows and all keys of a tile.  MW = 1 and 2:
+// the warps split a tile's keys and join their (m, l, O) at the end, so a
+// tile with few rows still keeps four warps busy.
+//
+// Operands.  e4m3 codes convert to f16 exactly, so QK runs in f16 with each
+// bf16 query row scaled by a power of two to put its largest element in
+// [2^14, 2^15): elements 2^-29 and more below it lose bits, an error of 2^-39
+// of the largest.  The scale comes back in fp32.  bf16 keys meet the bf16
+// query as they are.  Block-scaled keys: the four 32-element partial products
+// are scaled in fp32 and added.  The order of a row's elements inside a dot
+// product is free, so a lane takes the 16 (or 8) bytes that lie together and
+// the query fragments use the same order: no shuffles, no transposition of K.
+// P (16 bits, the one rounding of the softmax) is f16 next to e4m3 values,
+// with the value scale folded in and a power of two 2^-kp that follows the
+// largest value scale the row sees (O is rescaled when it rises), and bf16 next to
+// bf16 values.  m, l and O are fp32.
+//
+// Keys that a query does not see get no weight, whatever their rows hold:
+// rows that no query of the tile sees are not read at all, and in a tile that
+// only some of the queries see, non-finite values are set aside and added
+// to the queries that see them (a zero weight times NaN would not be zero).
+#include "chunk_common.cuh"
+#include "tc_common.cuh"
+
+namespace fp8kv {
+
+constexpr int kChunkThreads = 128;
+
+template <int D, int KE, int VE>
+struct ChunkCfg {
+  static constexpr int KB = KE == ELEM_BF16 ? 2 * D : D;       // bytes of a K row
+  static constexpr int VB = VE == ELEM_BF16 ? 2 * D : D;
+  static constexpr int SC = KE == ELEM_BF16 && VE == ELEM_BF16 ? 0 : 2 * kChunkKeys * 4;
+  static constexpr int STAGE = kChunkKeys * (KB + VB) + SC;
+  static constexpr int NS = 3;
+  static constexpr int OS = D + 4;                             // fp32 row stride of the join buffer
+  static constexpr int JOIN = 64 * OS * 4 + 2 * 64 * 4;
+  static constexpr int BYTES = (NS * STAGE > JOIN ? NS * STAGE : JOIN) + 4 * kChunkKeys * 4;
+};
+
+// 16-byte chunk of a K row in shared memory.  A lane reads 16 (MX: 8) bytes of
+// row lane / 4, four lanes side by side: neighbouring rows swap their 64-byte
+// (MX: 32-byte) parts so that a quarter warp (half warp) meets every bank once.
+template <int KE, int KB>
+__device__ __forceinline__ int k_chunk(int ch, int row) {
+  if constexpr (KE == ELEM_MX) return ch ^ ((row & 3) << 1);
+  return KB >= 128 ? ch ^ ((row & 1) << 2) : ch;
+}
+// 16-byte chunk of a V row: eight rows' chunks of the same column lie in
+// different banks (ldmatrix).
+template <int VB>
+__device__ __forceinline__ int v_chunk(int ch, int row) {
+  return VB >= 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
+}
+
+__device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4_z(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float x, float y) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// Non-finite 16-bit values of a B fragment register: `clean` has zeros in
+// their place, the others 1.0 at each NaN, +inf or -inf.
+template <bool BF16>
+struct SetAside {
+  uint32_t clean, nan, pinf, ninf;
+  __device__ __forceinline__ explicit SetAside(uint32_t w) : clean(w), nan(0), pinf(0), ninf(0) {
+    constexpr uint32_t INF = BF16 ? 0x7F80u : 0x7C00u, ONE = BF16 ? 0x3F80u : 0x3C00u;
+#pragma unroll
+    for (int sh = 0; sh < 32; sh += 16) {
+      const uint32_t h = (w >> sh) & 0xFFFFu, m = h & 0x7FFFu;
+      if (m < INF) continue;
+      clean &= ~(0xFFFFu << sh);
+      if (m > INF) nan |= ONE << sh;
+      else if (h & 0x8000u) ninf |= ONE << sh;
+      else pinf |= ONE << sh;
+    }
+  }
+};
+
+template <int D, int KE, int VE, int MW>
+__global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) {
+  using C = ChunkCfg<D, KE, VE>;
+  constexpr int NKB = 4 / MW;                  // key blocks of a tile (warps that share rows)
+  constexpr int KPW = kChunkKeys / NKB;        // keys of a tile per warp
+  constexpr int NT = KPW / 8;                  // 8-key score tiles per warp
+  constexpr bool KB16 = KE == ELEM_BF16, VB16 = VE == ELEM_BF16;
+  extern __shared__ __align__(128) uint8_t csm[];
+  int* rows_sh = reinterpret_cast<int*>(csm + (C::BYTES - 4 * kChunkKeys * 4));   // [4][64] cache rows of coming tiles
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
+  const int wm = warp % MW, kb0 = (warp / MW) * KPW;
+  const int hk = blockIdx.y, split = blockIdx.z;
+  ChunkTile t;
+  // the last tiles of a sequence see the most keys: they start first
+  if (!chunk_tile(p, gridDim.x - 1 - blockIdx.x, tid == 0 && hk == 0 && split == 0, t)) return;
+  const int per = (t.n + p.num_splits - 1) / p.num_splits;
+  const int j0 = min(t.n, split * per), nt = min(t.n, j0 + per) - j0;
+  const int G = p.group;
+
+  auto find_rows = [&](int it) {               // threads 0..63
+    return it < nt ? chunk_row(p, t, hk, chunk_key0(t, j0 + it) + tid) : -1;
+  };
+  auto issue = [&](int it) {
+    if (it < nt) {
+      uint8_t* st = csm + (it % C::NS) * C::STAGE;
+      const uint32_t ks = umma::smem_u32(st), vs = ks + kChunkKeys * C::KB, sc = vs + kChunkKeys * C::VB;
+      const int* rows = rows_sh + (it & 3) * kChunkKeys;
+      constexpr int KC = C::KB / 16, VC = C::VB / 16;
+#pragma unroll
+      for (int i = 0; i < kChunkKeys * KC / kChunkThreads; ++i) {
+        const int e = tid + i * kChunkThreads, r = e / KC, ch = e % KC, row = rows[r];
+        cp_async16_z(ks + r * C::KB + k_chunk<KE, C::KB>(ch, r) * 16, p.c.k + (row < 0 ? 0 : (int64_t)row * C::KB + ch * 16),
+                     row >= 0);
+      }
+#pragma unroll
+      for (int i = 0; i < kChunkKeys * VC / kChunkThreads; ++i) {
+        const int e = tid + i * kChunkThreads, r = e / VC, ch = e % VC, row = rows[r];
+        cp_async16_z(vs + r * C::VB + v_chunk<C::VB>(ch, r) * 16, p.c.v + (row < 0 ? 0 : (int64_t)row * C::VB + ch * 16),
+                     row >= 0);
+      }
+      if constexpr (C::SC > 0) {
+        const int r = tid & 63, row = rows[r];
+        const float* src = tid < 64 ? p.c.k_scale : p.c.v_scale;
+        if (tid < 64 ? !KB16 : !VB16) cp_async4_z(sc + tid * 4, src + (row < 0 ? 0 : row), row >= 0);
+      }
+    }
+    cp_async_commit();
+  };
+
+  // prologue: cache rows of the first NS tiles, loads of the first NS - 1
+  if (tid < kChunkKeys)
+    for (int it = 0; it < C::NS; ++it) rows_sh[(it & 3) * kChunkKeys + tid] = find_rows(it);
+  __syncthreads();
+  for (int it = 0; it < C::NS - 1; ++it) issue(it);
+
+  // the warp's 16 query rows as A fragments: rows g and g + 8
+  int qpos[2];
+  int64_t qrow[2];                             // row of out (query row x heads + head), -1: none
+  const uint4* qsrc[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = wm * 16 + g + 8 * i, tok = r / G;
+    const bool live = tok < t.ntok && r < p.tile_tokens * G;
+    qpos[i] = live ? t.pos0 + tok : -1;
+    qrow[i] = live ? (int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G) : -1;
+    qsrc[i] = reinterpret_cast<const uint4*>(p.q + (live ? qrow[i] : 0) * D);
+  }
+  constexpr int KS = D / 16;                   // k steps
+  uint32_t qa[KS][4];
+  float qf[2] = {1.f, 1.f};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[KS][2];                         // four elements of each step
+    constexpr bool WIDE = KE == ELEM_E4M3;     // 16 elements together per lane (else 8)
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+      const int at = WIDE ? 8 * (u >> 1) + 2 * c4 + (u & 1) : 4 * u + c4;
+      const uint4 x = qrow[i] >= 0 ? qsrc[i][at] : make_uint4(0, 0, 0, 0);
+      w[2 * u][0] = x.x; w[2 * u][1] = x.y; w[2 * u + 1][0] = x.z; w[2 * u + 1][1] = x.w;
+    }
+    float sc = 1.f;
+    if constexpr (!KB16) {
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float f[2];
+          bf16x2_to_f32(w[k][u], f);
+          amax = fmaxf(amax, fmaxf(fabsf(f[0]), fabsf(f[1])));
+        }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int e = ((__float_as_int(amax) >> 23) & 0xFF) - 127;       // amax in [2^e, 2^(e+1))
+      const int up = min(14 - e, 126);
+      if (amax > 0.f && e < 128) { sc = pow2i(up); qf[i] = pow2i(-up); }
+    }
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t v = w[k][u];
+        if constexpr (!KB16) {
+          float f[2];
+          bf16x2_to_f32(v, f);
+          v = pack16<false>(f[0] * sc, f[1] * sc);
+        }
+        qa[k][2 * u + i] = v;
+      }
+  }
+
+  float o[D / 8][4];
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  int kp[2] = {-1000, -1000};                  // exponent of P of each row (e4m3 values; none yet)
+
+#pragma unroll 1
+  for (int it = 0; it < nt; ++it) {
+    cp_async_wait<C::NS - 2>();
+    __syncthreads();                           // tile `it` has landed; every warp is done with tile it - 1
+    issue(it + C::NS - 1);
+    const int next_row = tid < kChunkKeys ? find_rows(it + C::NS) : -1;
+    const uint8_t* st = csm + (it % C::NS) * C::STAGE;
+    const uint8_t* vst = st + kChunkKeys * C::KB;
+    const float* ksc = reinterpret_cast<const float*>(vst + kChunkKeys * C::VB);
+    const float* vsc = ksc + kChunkKeys;
+    const int key0 = chunk_key0(t, j0 + it);
+
+    // scores: s[n] holds rows g, g + 8 and keys kb0 + 8 n + 2 c4, + 1
+    float s[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int kr = kb0 + 8 * n + g, kc = kb0 + 8 * n + 2 * c4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+      if constexpr (KE == ELEM_E4M3) {
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          const uint4 w = *reinterpret_cast<const uint4*>(st + kr * C::KB + k_chunk<KE, C::KB>(4 * h + c4, kr) * 16);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            mma16816<false>(s[n], qa[4 * h + u], e4m3x2_to_f16x2((uint16_t)ww[u]), e4m3x2_to_f16x2((uint16_t)(ww[u] >> 16)));
+        }
+        const float2 sc = *reinterpret_cast<const float2*>(ksc + kc);
+        const float s0 = sc.x * p.scale_log2, s1 = sc.y * p.scale_log2;
+        s[n][0] *= s0 * qf[0]; s[n][1] *= s1 * qf[0];
+        s[n][2] *= s0 * qf[1]; s[n][3] *= s1 * qf[1];
+      } else if constexpr (KE == ELEM_MX) {
+        const uint2 e8 = *reinterpret_cast<const uint2*>(ksc + kc);
+#pragma unroll
+        for (int blk = 0; blk < D / 32; ++blk) {
+          const uint2 w = *reinterpret_cast<const uint2*>(st + kr * C::KB + k_chunk<KE, C::KB>(2 * blk + (c4 >> 1), kr) * 16 +
+                                                          (c4 & 1) * 8);
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816<false>(part, qa[2 * blk], e4m3x2_to_f16x2((uint16_t)w.x), e4m3x2_to_f16x2((uint16_t)(w.x >> 16)));
+          mma16816<false>(part, qa[2 * blk + 1], e4m3x2_to_f16x2((uint16_t)w.y), e4m3x2_to_f16x2((uint16_t)(w.y >> 16)));
+          const float b0 = pow2_exact((int)((e8.x >> (8 * blk)) & 0xFF) - 127);
+          const float b1 = pow2_exact((int)((e8.y >> (8 * blk)) & 0xFF) - 127);
+          s[n][0] = fmaf(part[0], b0, s[n][0]); s[n][1] = fmaf(part[1], b1, s[n][1]);
+          s[n][2] = fmaf(part[2], b0, s[n][2]); s[n][3] = fmaf(part[3], b1, s[n][3]);
+        }
+        s[n][0] *= p.scale_log2 * qf[0]; s[n][1] *= p.scale_log2 * qf[0];
+        s[n][2] *= p.scale_log2 * qf[1]; s[n][3] *= p.scale_log2 * qf[1];
+      } else {
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u) {
+          const uint4 w = *reinterpret_cast<const uint4*>(st + kr * C::KB + k_chunk<KE, C::KB>(4 * u + c4, kr) * 16);
+          mma16816<true>(s[n], qa[2 * u], w.x, w.y);
+          mma16816<true>(s[n], qa[2 * u + 1], w.z, w.w);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] *= p.scale_log2;
+      }
+    }
+    const bool part = !chunk_all_seen(p, t, key0);
+    if (part) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!chunk_sees(p, qpos[e >> 1], key0 + kb0 + 8 * n + 2 * c4 + (e & 1))) s[n][e] = -INFINITY;
+    }
+    // running maximum and weights
+    float alpha[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mt = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mt = fmaxf(mt, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+      const float mn = fmaxf(m[i], mt), ref = mn == -INFINITY ? 0.f : mn;
+      alpha[i] = m[i] == -INFINITY ? 1.f : ex2_ftz(m[i] - ref);   // (nothing yet: O and l are zero)
+      m[i] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        s[n][2 * i] = ex2_ftz(s[n][2 * i] - ref);
+        s[n][2 * i + 1] = ex2_ftz(s[n][2 * i + 1] - ref);
+        sum += s[n][2 * i] + s[n][2 * i + 1];
+      }
+      l[i] = l[i] * alpha[i] + sum;
+    }
+    if constexpr (!VB16) {
+      // the largest value scale among the keys that the row sees
+      auto finite = [](float v) { return v < INFINITY ? v : 0.f; };
+      float vm[2];
+      if (!part) {
+        float v = finite(vsc[kb0 + (lane & (KPW - 1))]);
+        if constexpr (KPW == 64) v = fmaxf(v, finite(vsc[lane + 32]));
+        vm[0] = vm[1] = warp_max_f32(v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          vm[i] = 0.f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int kc = kb0 + 8 * n + 2 * c4 + e;
+              if (chunk_sees(p, qpos[i], key0 + kc)) vm[i] = fmaxf(vm[i], finite(vsc[kc]));
+            }
+          vm[i] = fmaxf(vm[i], __shfl_xor_sync(0xffffffffu, vm[i], 1));
+          vm[i] = fmaxf(vm[i], __shfl_xor_sync(0xffffffffu, vm[i], 2));
+        }
+      }
+      float vf[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int need = max(-100, min(100, ((__float_as_int(vm[i]) >> 23) & 0xFF) - 127 - 14));   // vm 2^-need < 2^15
+        if (vm[i] > 0.f && need > kp[i]) {
+          if (kp[i] > -1000) alpha[i] *= pow2_diff((float)(kp[i] - need), 0);
+          kp[i] = need;
+        }
+        vf[i] = kp[i] > -1000 ? pow2i(-kp[i]) : 1.f;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float2 v = *reinterpret_cast<const float2*>(vsc + kb0 + 8 * n + 2 * c4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float w = s[n][e] * ((e & 1 ? v.y : v.x) * vf[e >> 1]);
+          // a scale that is not finite would turn an unseen key's zero into NaN
+          s[n][e] = part && !chunk_sees(p, qpos[e >> 1], key0 + kb0 + 8 * n + 2 * c4 + (e & 1)) ? 0.f : w;
+        }
+      }
+    }
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][0] *= alpha[0]; o[n][1] *= alpha[0];
+        o[n][2] *= alpha[1]; o[n][3] *= alpha[1];
+      }
+    }
+    // a tile seen by some of its queries only: are there values that must not
+    // meet the others' zero weights?
+    bool aside = false;
+    if (part && t.ntok > 1) {
+      constexpr int VC = C::VB / 16;
+      for (int e = lane; e < KPW * VC; e += 32) {
+        const uint4 w = *reinterpret_cast<const uint4*>(vst + (kb0 + e / VC) * C::VB + (e % VC) * 16);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if constexpr (VB16)
+            aside = aside || (ww[u] & 0x7F800000u) == 0x7F800000u || (ww[u] & 0x7F80u) == 0x7F80u;
+          else
+            aside = aside || ((((ww[u] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0);
+        }
+      }
+      aside = __any_sync(0xffffffffu, aside);
+    }
+    // O += P V: 16 keys at a time
+    const uint32_t vaddr = umma::smem_u32(vst);
+#pragma unroll
+    for (int j = 0; j < KPW / 16; ++j) {
+      const uint32_t pa[4] = {pack16<VB16>(s[2 * j][0], s[2 * j][1]), pack16<VB16>(s[2 * j][2], s[2 * j][3]),
+                              pack16<VB16>(s[2 * j + 1][0], s[2 * j + 1][1]), pack16<VB16>(s[2 * j + 1][2], s[2 * j + 1][3])};
+      const int vr = kb0 + 16 * j + (lane & 15);       // row this lane addresses for ldmatrix
+#pragma unroll
+      for (int u = 0; u < C::VB / 32; ++u) {
+        uint32_t r[4];
+        ldsm_x4_trans(vaddr + vr * C::VB + v_chunk<C::VB>(2 * u + (lane >> 4), vr) * 16, r);
+        if constexpr (VB16) {
+          if (aside) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = SetAside<true>(r[k]).clean;
+          }
+          mma16816<true>(o[2 * u], pa, r[0], r[1]);
+          mma16816<true>(o[2 * u + 1], pa, r[2], r[3]);
+        } else {
+          // two keys x two dims of e4m3 codes -> the two keys' pairs of each dim
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[k] = __byte_perm(r[k], 0, 0x3120);
+          uint32_t b[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            b[2 * k] = e4m3x2_to_f16x2((uint16_t)r[k]);
+            b[2 * k + 1] = e4m3x2_to_f16x2((uint16_t)(r[k] >> 16));
+          }
+          if (aside) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) b[k] = SetAside<false>(b[k]).clean;
+          }
+          mma16816<false>(o[4 * u], pa, b[0], b[2]);
+          mma16816<false>(o[4 * u + 1], pa, b[1], b[3]);
+          mma16816<false>(o[4 * u + 2], pa, b[4], b[6]);
+          mma16816<false>(o[4 * u + 3], pa, b[5], b[7]);
+        }
+      }
+    }
+    if (aside) {                               // rare: which queries see the values set aside
+#pragma unroll
+      for (int j = 0; j < KPW / 16; ++j) {
+        uint32_t see[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = key0 + kb0 + 16 * j + 8 * (k >> 1) + 2 * c4, pos = qpos[k & 1];
+          see[k] = pack16<VB16>(chunk_sees(p, pos, key) ? 1.f : 0.f, chunk_sees(p, pos, key + 1) ? 1.f : 0.f);
+        }
+        auto add = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
+          const SetAside<VB16> x(b0), y(b1);
+          float nan[4] = {0.f, 0.f, 0.f, 0.f}, pinf[4] = {0.f, 0.f, 0.f, 0.f}, ninf[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816<VB16>(nan, see, x.nan, y.nan);
+          mma16816<VB16>(pinf, see, x.pinf, y.pinf);
+          mma16816<VB16>(ninf, see, x.ninf, y.ninf);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (pinf[e] > 0.f) acc[e] += INFINITY;
+            if (ninf[e] > 0.f) acc[e] -= INFINITY;
+            if (nan[e] > 0.f) acc[e] = NAN;
+          }
+        };
+        const int vr = kb0 + 16 * j + (lane & 15);
+#pragma unroll
+        for (int u = 0; u < C::VB / 32; ++u) {
+          uint32_t r[4];
+          ldsm_x4_trans(vaddr + vr * C::VB + v_chunk<C::VB>(2 * u + (lane >> 4), vr) * 16, r);
+          if constexpr (VB16) {
+            add(o[2 * u], r[0], r[1]);
+            add(o[2 * u + 1], r[2], r[3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) r[k] = __byte_perm(r[k], 0, 0x3120);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              add(o[4 * u + 2 * k], e4m3x2_to_f16x2((uint16_t)r[2 * k]), e4m3x2_to_f16x2((uint16_t)r[2 * k + 1]));
+              add(o[4 * u + 2 * k + 1], e4m3x2_to_f16x2((uint16_t)(r[2 * k] >> 16)),
+                  e4m3x2_to_f16x2((uint16_t)(r[2 * k + 1] >> 16)));
+            }
+          }
+        }
+      }
+    }
+    if (tid < kChunkKeys) rows_sh[((it + C::NS) & 3) * kChunkKeys + tid] = next_row;
+  }
+
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+    l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+  }
+  if constexpr (!VB16) {
+    const float f[2] = {kp[0] > -1000 ? pow2i(kp[0]) : 1.f, kp[1] > -1000 ? pow2i(kp[1]) : 1.f};
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] *= f[e >> 1];
+  }
+  // four neighbouring elements of row g + 8 i: e4m3 values interleave two
+  // accumulator tiles, bf16 values have two neighbours in each
+  auto store = [&](int64_t row, int d, const float (&x)[4], float mm, float ll) {
+    if (p.num_splits > 1) {
+      const int64_t at = row * p.num_splits + split;
+      *reinterpret_cast<float4*>(p.part_o + at * D + d) = make_float4(x[0], x[1], x[2], x[3]);
+      if (d == 0) { p.part_m[at] = mm; p.part_l[at] = ll; }
+      return;
+    }
+    const float inv = ll > 0.f ? 1.f / ll : 0.f;
+    if (p.out_f32) {
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + row * D + d) =
+          make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    } else {
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + row * D + d) =
+          make_uint2(pack16<true>(x[0] * inv, x[1] * inv), pack16<true>(x[2] * inv, x[3] * inv));
+    }
+  };
+  if constexpr (MW == 4 && !VB16) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (qrow[i] >= 0)
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u) {
+          const float x[4] = {o[2 * u][2 * i], o[2 * u + 1][2 * i], o[2 * u][2 * i + 1], o[2 * u + 1][2 * i + 1]};
+          store(qrow[i], 16 * u + 4 * c4, x, m[i], l[i]);
+        }
+  } else {
+    cp_async_wait<0>();
+    __syncthreads();                           // the ring is free: rows of all warps meet in shared memory
+    float* osh = reinterpret_cast<float*>(csm);
+    float* msh = osh + 64 * C::OS;
+    float* lsh = msh + 64;
+    const int at = (warp / MW) * 16 * MW + wm * 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = at + g + 8 * i;
+      float* dst = osh + r * C::OS;
+      if (c4 == 0) { msh[r] = m[i]; lsh[r] = l[i]; }
+      if constexpr (VB16) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+          *reinterpret_cast<float2*>(dst + 8 * n + 2 * c4) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < D / 16; ++u)
+          *reinterpret_cast<float4*>(dst + 16 * u + 4 * c4) =
+              make_float4(o[2 * u][2 * i], o[2 * u + 1][2 * i], o[2 * u][2 * i + 1], o[2 * u + 1][2 * i + 1]);
+      }
+    }
+    __syncthreads();
+    for (int e = tid; e < 16 * MW * (D / 4); e += kChunkThreads) {
+      const int r = e / (D / 4), d = (e % (D / 4)) * 4, tok = r / G;
+      if (tok >= t.ntok || r >= p.tile_tokens * G) continue;
+      float M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < NKB; ++k) M = fmaxf(M, msh[k * 16 * MW + r]);
+      float L = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < NKB; ++k) {
+        const int kr = k * 16 * MW + r;
+        const float w = chunk_weight(msh[kr], lsh[kr], M);
+        const float4 v = *reinterpret_cast<const float4*>(osh + kr * C::OS + d);
+        L = fmaf(w, lsh[kr], L);
+        x[0] = fmaf(w, v.x, x[0]); x[1] = fmaf(w, v.y, x[1]);
+        x[2] = fmaf(w, v.z, x[2]); x[3] = fmaf(w, v.w, x[3]);
+      }
+      store((int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G), d, x, M, L);
+    }
+  }
+}
+
+// Joins the splits of each row: one warp per row of out.  Rows behind the
+// last sequence stay as they were.
+template <int D>
+__global__ void __launch_bounds__(256) chunk_merge(const ChunkParams p) {
+  const int lane = threadIdx.x & 31, S = p.num_splits;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= (int64_t)p.total_q * p.q_heads) return;
+  const int tok = (int)(row / p.q_heads);
+  if (p.cu_q != nullptr && (tok < p.cu_q[0] || tok >= p.cu_q[p.c.batch])) return;
+  const float* pm = p.part_m + row * S;
+  const float* pl = p.part_l + row * S;
+  constexpr int E = D / 32;
+  float M = -INFINITY, L = 0.f, x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = 0.f;
+  for (int s = lane; s < S; s += 32) M = fmaxf(M, pm[s]);
+  M = warp_max(M);
+  for (int s0 = 0; s0 < S; s0 += 32) {
+    const int s = s0 + lane;
+    float w = 0.f;
+    if (s < S) {
+      w = chunk_weight(pm[s], pl[s], M);
+      L = fmaf(w, pl[s], L);
+    }
+    const int n = min(32, S - s0);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+      const float* po = p.part_o + (row * S + s0 + k) * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(po);
+        x[0] = fmaf(wk, v.x, x[0]); x[1] = fmaf(wk, v.y, x[1]);
+        x[2] = fmaf(wk, v.z, x[2]); x[3] = fmaf(wk, v.w, x[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(po);
+        x[0] = fmaf(wk, v.x, x[0]); x[1] = fmaf(wk, v.y, x[1]);
+      }
+    }
+  }
+  L = warp_sum(L);
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] *= inv;
+  if (p.out_f32) {
+    float* dst = reinterpret_cast<float*>(p.out) + row * D + lane * E;
+    if constexpr (E == 4) *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+    else *reinterpret_cast<float2*>(dst) = make_float2(x[0], x[1]);
+  } else {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.out) + row * D + lane * E);
+    if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pack16<true>(x[0], x[1]), pack16<true>(x[2], x[3]));
+    else *dst = pack16<true>(x[0], x[1]);
+  }
+}
+
+cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t st) {
+  const int64_t rows = (int64_t)p.total_q * p.q_heads;
+  const unsigned grid = (unsigned)((rows + 7) / 8);
+  if (p.c.head_dim == 128) chunk_merge<128><<<grid, 256, 0, st>>>(p);
+  else chunk_merge<64><<<grid, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, int KE, int VE, int MW>
+static cudaError_t launch_one(const ChunkParams& p, dim3 grid, cudaStream_t st) {
+  constexpr int smem = ChunkCfg<D, KE, VE>::BYTES;
+  const cudaError_t e = ensure_smem_optin((const void*)chunk_mma<D, KE, VE, MW>, smem);
+  if (e != cudaSuccess) return e;
+  chunk_mma<D, KE, VE, MW><<<grid, kChunkThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D, int KE, int VE>
+static cudaError_t launch_rows(const ChunkParams& p, int row_warps, dim3 grid, cudaStream_t st) {
+  if (row_warps == 1) return launch_one<D, KE, VE, 1>(p, grid, st);
+  if (row_warps == 2) return launch_one<D, KE, VE, 2>(p, grid, st);
+  return launch_one<D, KE, VE, 4>(p, grid, st);
+}
+
+template <int D>
+static cudaError_t launch_types(const ChunkParams& p, int dtype, int row_warps, dim3 grid, cudaStream_t st) {
+  if constexpr (D == 128)     // (MXFP8 keys are built for head_dim 128)
+    if (dtype == FP8KV_MXK8V8) return launch_rows<D, ELEM_MX, ELEM_E4M3>(p, row_warps, grid, st);
+  if (dtype == FP8KV_K8V8) return launch_rows<D, ELEM_E4M3, ELEM_E4M3>(p, row_warps, grid, st);
+  if (dtype == FP8KV_K16V8) return launch_rows<D, ELEM_BF16, ELEM_E4M3>(p, row_warps, grid, st);
+  if (dtype == FP8KV_K8V16) return launch_rows<D, ELEM_E4M3, ELEM_BF16>(p, row_warps, grid, st);
+  return launch_rows<D, ELEM_BF16, ELEM_BF16>(p, row_warps, grid, st);
+}
+
+cudaError_t launch_chunk_mma(const ChunkParams& p, int dtype, int row_warps, int tiles, cudaStream_t st) {
+  const dim3 grid(tiles, p.c.kv_heads, p.num_splits);
+  return p.c.head_dim == 128 ? launch_types<128>(p, dtype, row_warps, grid, st)
+                             : launch_types<64>(p, dtype, row_warps, grid, st);
+}
+
+}  // namespace fp8kv

@@ -71,6 +71,23 @@ struct RopeAppendParams {
   int groups, per_group;            // warps per token, row passes per warp
 };
 
+struct ChunkParams {
+  CacheView c;
+  const __nv_bfloat16* q;    // [total_q][Hq][D]
+  const int32_t* cu_q;       // [B + 1], or null: one query per sequence
+  const int32_t* seq_lens;   // [B]
+  void* out;                 // [total_q][Hq][D]
+  float* part_o;             // [total_q * Hq][S][D]  unnormalised O of each split (S > 1)
+  float* part_m;             // [total_q * Hq][S]     its maximum, log2 domain
+  float* part_l;             // [total_q * Hq][S]     its sum
+  unsigned int* err;
+  int total_q, q_heads, group, out_f32;
+  int window, sinks;         // window 0: every key up to the query's position
+  int num_splits;            // CTAs that share a tile's keys
+  int tile_tokens;           // queries of a sequence per tile
+  float scale_log2;          // sm_scale * log2(e)
+};
+
 cudaError_t launch_quantize(const void* x, int64_t rows, int head_dim, uint8_t* codes, float* scales,
                             cudaStream_t s);
 cudaError_t launch_quantize_mx(const void* x, int64_t rows, int head_dim, uint8_t* codes, uint8_t* scales,
@@ -92,6 +109,8 @@ cudaError_t launch_build_tables(const CacheView& c, const int32_t* cached, const
                                 int32_t* head_out, unsigned int* err, cudaStream_t s);
 cudaError_t launch_rope_tables(int positions, int pairs, const unsigned long long* w, float amplitude, float* cos,
                                float* sin, cudaStream_t s);
+cudaError_t launch_chunk_mma(const ChunkParams& p, int dtype, int row_warps, int tiles, cudaStream_t st);
+cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t st);
 cudaError_t launch_rope_append(RopeAppendParams& p, int dtype, cudaStream_t s);
 
 // Host-side pieces of the C-ABI layer (api.cu).

@@ -120,7 +120,10 @@ typedef enum {
    * for other dtypes and head dims, and by the prefill
    * (FP8KV_ERR_INVALID_ARG). */
   FP8KV_KERNEL_TENSOR_CORES_K_F16 = 3,
-  FP8KV_KERNEL_TENSOR_CORES_K_F16_PRODUCER = 4
+  FP8KV_KERNEL_TENSOR_CORES_K_F16_PRODUCER = 4,
+  /* fp8kv_chunk_attention only: warp-level matrix instructions, every cache
+   * type and head dim (other calls: FP8KV_ERR_INVALID_ARG). */
+  FP8KV_KERNEL_WARP_MMA = 5
 } fp8kv_decode_kernel;
 
 /* Device error word bits (fp8kv_get_device_error). */
@@ -435,6 +438,55 @@ FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q
                                          const int64_t *slots, int64_t n_tokens, const float *cos,
                                          const float *sin, int32_t positions, int32_t rot_dim,
                                          int32_t layout, void *q_out, fp8kv_stream_t stream);
+
+/* Attention of a ragged chunk of new tokens over the cache, which must hold
+ * them already (append first), causal or under a sliding window.  Sequence b's
+ * queries are rows cu_q[b] .. cu_q[b+1] - 1; the last of them sits at position
+ * seq_lens[b] - 1.  A query at position p sees the keys j with j <= p and,
+ * under a window, j > p - window or j < sinks: the last `window` tokens, its
+ * own among them, and the first `sinks` tokens of the sequence.  Sequences may
+ * have no query, one (decode), some (drafted tokens) or many (a prompt's
+ * chunk), mixed in one call.
+ *   q:          [total_q][q_heads][head_dim] bf16, 16-byte aligned; query head
+ *               h reads KV head h / (q_heads / kv_heads)
+ *   cu_q:       [batch + 1] int32 device array, not decreasing; rows before
+ *               cu_q[0] and from cu_q[batch] on are neither read nor written.
+ *               NULL: one query per sequence (total_q = batch)
+ *   seq_lens:   [batch] int32 device array, tokens in the cache
+ *   window:     0: no window; else at least 1 (a window of the cache's
+ *               capacity or more is none)
+ *   sinks:      >= 0; no effect without a window
+ *   num_splits: CTAs that share the keys of one tile of queries, joined by a
+ *               second kernel; 0: chosen from the sizes (1 for long chunks)
+ *   kernel:     FP8KV_KERNEL_AUTO, or _WARP_MMA (every cache type but
+ *               rotated-bias residual keys, which return
+ *               FP8KV_ERR_UNSUPPORTED; group 1 to 16)
+ *   workspace:  fp8kv_chunk_workspace_bytes() bytes, 16-byte aligned, nothing
+ *               need be zero; NULL if that is 0.  Calls that may run at once
+ *               need one each.
+ *   out:        [total_q][q_heads][head_dim], bf16 or fp32 per out_dtype,
+ *               16-byte aligned
+ * A query that sees no key (its position is negative: seq_lens[b] is less than
+ * its sequence's queries) gets a zero row.  Keys that a query does not see
+ * have no influence on it, whatever they hold (NaN included).  A length below
+ * 0 or past the capacity raises SEQ_TOO_LONG and gives zero rows; offsets that
+ * decrease or pass total_q raise it and leave their rows as they were. */
+FP8KV_API fp8kv_status fp8kv_chunk_attention(const void *q, const fp8kv_cache *cache,
+                                             const int32_t *cu_q, const int32_t *seq_lens,
+                                             int64_t total_q, int32_t q_heads, float sm_scale,
+                                             int32_t window, int32_t sinks, int32_t num_splits,
+                                             int32_t kernel, void *workspace, size_t workspace_bytes,
+                                             void *out, int32_t out_dtype, fp8kv_stream_t stream);
+
+/* The split count that call will use (0 on invalid arguments), and the bytes
+ * of workspace it needs: the fp32 partials (O, m, l) of every (row, split), 0
+ * without splits. */
+FP8KV_API int32_t fp8kv_chunk_num_splits(const fp8kv_cache *cache, int64_t total_q, int32_t q_heads,
+                                         int32_t window, int32_t sinks, int32_t num_splits,
+                                         int32_t kernel);
+FP8KV_API size_t fp8kv_chunk_workspace_bytes(const fp8kv_cache *cache, int64_t total_q, int32_t q_heads,
+                                             int32_t window, int32_t sinks, int32_t num_splits,
+                                             int32_t kernel);
 
 /* Read (and, if `clear` is non-zero, reset) the device error word of the
  * current device.  Synchronous: waits for all work on the device. */

@@ -84,6 +84,46 @@ def test_rope_append_refusals(lib, want, kw):
     assert lib.fp8kv_rope_append(_cache(), *a.values(), None) == want
 
 
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(total=-1)), (INVALID, dict(q_heads=3)), (INVALID, dict(window=-1)), (INVALID, dict(sinks=-1)),
+    (INVALID, dict(splits=-1)), (INVALID, dict(kernel=1)), (INVALID, dict(kernel=7)), (INVALID, dict(out_dtype=2)),
+    (INVALID, dict(sm=float("nan"))), (INVALID, dict(q=None)), (INVALID, dict(lens=None)), (INVALID, dict(out=None)),
+    (INVALID, dict(q=0x10008)), (INVALID, dict(out=0x40008)), (INVALID, dict(cu=None)), (INVALID, dict(ws=0x30008)),
+    (WORKSPACE, dict(ws=None)), (WORKSPACE, dict(ws_bytes=100)), (UNSUPPORTED, dict(q_heads=34)), (UNSUPPORTED, dict(total=1 << 31)),
+    (UNSUPPORTED, dict(splits=5000)),
+])
+def test_chunk_refusals(lib, want, kw):
+    a = dict(q=0x10000, cu=0x20000, lens=0x21000, total=10, q_heads=4, sm=0.1, window=0, sinks=0, splits=2, kernel=0, ws=0x30000,
+             ws_bytes=1 << 30, out=0x40000, out_dtype=0)
+    a.update(kw)
+    v = list(a.values())
+    assert lib.fp8kv_chunk_attention(v[0], _paged(), *v[1:], None) == want
+
+
+def test_chunk_refusals_by_cache(lib):
+    args = (0x20000, 0x21000, 10, 4, 0.1, 0, 0, 0, 0, 0x30000, 1 << 30, 0x40000, 0, None)
+    turning = _cache(k_bias=0x8000, rope_cos=0x9000, rope_sin=0xA000, rope_positions=2048)
+    assert lib.fp8kv_chunk_attention(0x10000, turning, *args) == UNSUPPORTED
+    assert lib.fp8kv_chunk_attention(0x10000, None, *args) == INVALID
+    # other calls do not know the chunk kernel's name
+    assert lib.fp8kv_prefill_attention(0x10000, _cache(), 0x20000, 16, 4, 0.1, 5, 0x40000, 0, None) == INVALID
+    assert lib.fp8kv_decode_split(0x10000, _cache(), 0x20000, 4, 0.1, 0, 5, 0x30000, 1 << 30, None) == INVALID
+
+
+def test_chunk_plan(lib):
+    """Splits and workspace from the sizes alone: splits for few tiles of a
+    long cache, none for many tiles or a short window; never more than tiles."""
+    n = lib.fp8kv_chunk_num_splits
+    long = dict(batch=1, max_tokens=65536)
+    assert n(_cache(**long), 1, 4, 0, 0, 0, 0) > 8
+    assert n(_cache(**long), 1, 4, 128, 4, 0, 0) <= 2
+    assert n(_cache(**long), 4096, 4, 0, 0, 0, 0) == 1
+    assert n(_cache(max_tokens=64), 4, 4, 0, 0, 100, 0) == 2
+    assert n(_cache(), 4, 3, 0, 0, 0, 0) == 0
+    assert lib.fp8kv_chunk_workspace_bytes(_cache(), 4, 4, 0, 0, 3, 0) == 4 * 4 * 3 * 130 * 4
+    assert lib.fp8kv_chunk_workspace_bytes(_cache(), 4, 4, 0, 0, 1, 0) == 0
+
+
 def test_python_argument_checks():
     """The binding turns wrong tensors down by name."""
     t = torch.zeros(4, dtype=torch.int32)
