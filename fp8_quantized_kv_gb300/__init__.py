@@ -479,7 +479,8 @@ def fp8kv_chunk_attention(q: torch.Tensor, cache: Fp8KVCache, cu_q: Optional[tor
     window > 0: a query sees the last `window` tokens, its own among them, and
     the first `sinks`.  Returns out [total_q, Hq, D]; rows outside every
     sequence stay as they were (an `out` made here holds anything there).
-    kernel: "auto" or "warp_mma"."""
+    kernel: "auto", "warp_mma" or "tensor_cores" (head dim 128, not block-scaled
+    keys)."""
     total_q, Hq, D = q.shape
     if D != cache.head_dim:
         raise ValueError(f"q: head dim {D}, but the cache's is {cache.head_dim}")

@@ -30,14 +30,18 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
                         int kernel, ChunkPlan* plan) {
   if (total_q < 0 || q_heads <= 0 || q_heads % c->kv_heads != 0 || window < 0 || sinks < 0 || num_splits < 0)
     return FP8KV_ERR_INVALID_ARG;
-  if (kernel != FP8KV_KERNEL_AUTO && kernel != FP8KV_KERNEL_WARP_MMA) return FP8KV_ERR_INVALID_ARG;
+  if (kernel != FP8KV_KERNEL_AUTO && kernel != FP8KV_KERNEL_WARP_MMA && kernel != FP8KV_KERNEL_TENSOR_CORES)
+    return FP8KV_ERR_INVALID_ARG;
   const int G = q_heads / c->kv_heads;
   if (G > 16 || c->rope_cos != nullptr || c->kv_heads > 65535 || num_splits > 4096) return FP8KV_ERR_UNSUPPORTED;
   if (total_q > INT32_MAX || (double)total_q * q_heads > 8.0 * INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
   const int64_t B = c->batch > 0 ? c->batch : 1;
   const int64_t rows = (total_q + B - 1) / B * G;
-  plan->kernel = FP8KV_KERNEL_WARP_MMA;
-  plan->row_warps = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  const bool tc_built = c->head_dim == 128 && c->dtype != FP8KV_MXK8V8;
+  if (kernel == FP8KV_KERNEL_TENSOR_CORES && !tc_built) return FP8KV_ERR_UNSUPPORTED;
+  const bool tc = kernel == FP8KV_KERNEL_TENSOR_CORES || (kernel == FP8KV_KERNEL_AUTO && tc_built && rows > 32);
+  plan->kernel = tc ? FP8KV_KERNEL_TENSOR_CORES : FP8KV_KERNEL_WARP_MMA;
+  plan->row_warps = tc ? 8 : rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   plan->tile_tokens = 16 * plan->row_warps / G;
   const int64_t tiles = total_q / plan->tile_tokens + c->batch;
   if (tiles > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
@@ -49,7 +53,7 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   if (want == 0) {
     const int64_t units = tiles * c->kv_heads, target = 2 * (int64_t)sm_count();
     want = units > 0 ? target / units : 1;
-    if (want > kv_tiles / 4) want = kv_tiles / 4;
+    if (want > kv_tiles / (tc ? 8 : 4)) want = kv_tiles / (tc ? 8 : 4);
   }
   if (want > kv_tiles) want = kv_tiles;
   if (want > 4096) want = 4096;
@@ -236,7 +240,9 @@ fp8kv_status fp8kv_chunk_attention(const void* q, const fp8kv_cache* cache, cons
   p.tile_tokens = plan.tile_tokens;
   p.scale_log2 = sm_scale * kLog2e;
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = launch_chunk_mma(p, cache->dtype, plan.row_warps, cu_q ? plan.tiles : cache->batch, s);
+  const int tiles = cu_q ? plan.tiles : cache->batch;
+  cudaError_t e = plan.kernel == FP8KV_KERNEL_TENSOR_CORES ? launch_chunk_tc(p, cache->dtype, tiles, s)
+                                                            : launch_chunk_mma(p, cache->dtype, plan.row_warps, tiles, s);
   if (e == cudaSuccess && plan.splits > 1) e = launch_chunk_merge(p, s);
   return cuda_status(e);
 }

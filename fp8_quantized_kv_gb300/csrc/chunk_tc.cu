@@ -1,0 +1,653 @@
+// chunk_tc.cu -- ragged chunk attention over the cache on the tcgen05 tensor
+// cores (head_dim 128): the form for tiles with many query rows, where the
+// two matrix products and the softmax between them bound the time.
+//
+// A CTA owns up to 128 query rows of one KV head (tokens x heads of the
+// group: the heads share the K and V tiles) and walks the 64-key tiles that
+// any of them sees.  Per tile:
+//   S[128 x 64]   = Q . K^T        e4m3 keys: kind::f8f6f4 on the codes as they
+//                                  landed, the bf16 query as two e4m3 terms
+//                                  (hi, and what hi leaves over) after a
+//                                  power-of-two scaling of the row; bf16 keys:
+//                                  kind::f16 in bf16
+//   p = 2^(s - m), l += p          one thread per row, running maximum m moved
+//                                  only when it grows by more than 2^8
+//   O[128 x 128] += P . V          kind::f16; P is the A operand and stays in
+//                                  TMEM, written over the scores it came from;
+//                                  e4m3 values converted to f16 (exact), bf16
+//                                  values as they landed
+// P carries the value scale and a power of two 2^-kp per row, as in
+// chunk_mma.cu: 16 bits, the one rounding of the softmax.
+//
+// The CTA keeps to 256 TMEM columns (two score buffers, one O) and about 100
+// KB of shared memory, so two CTAs share an SM: one's softmax runs while the
+// other's products, prologue or epilogue do.
+//
+// Warp roles (registers moved between the warpgroups by setmaxnreg, 3 x 80):
+//   warps 0-3   softmax, one query row (TMEM lane) per thread; epilogue
+//   warps 4-7   preparation: per-key scales; e4m3 V codes -> f16 operand; in a
+//               tile that not every query sees whole, rows nobody sees are
+//               zeroed and a row with non-finite values is zeroed and its
+//               scale set to NaN: queries that see it get NaN, others nothing
+//   warp 8      TMA producer: K ring and V ring (with the scale rows)
+//   warp 9      TMEM owner and MMA issuer
+// Every wait is bounded; one that runs out raises FP8KV_DEVERR_TIMEOUT.
+#include "chunk_common.cuh"
+#include "tc_common.cuh"
+
+namespace fp8kv {
+
+constexpr int kCtRows = 128, kCtThreads = 384;
+
+template <int KE, int VE>
+struct CtCfg {
+  static constexpr bool K16 = KE == ELEM_BF16, V16 = VE == ELEM_BF16;
+  static constexpr int D = 128;
+  static constexpr int QOP = kCtRows * 2 * D;                       // [hi, lo][128][128 B], or [2 halves of D][128][128 B]
+  static constexpr int KT = kChunkKeys * D * (K16 ? 2 : 1);         // K tile
+  static constexpr int VT = kChunkKeys * D * (V16 ? 2 : 1);         // V tile as stored
+  static constexpr int SCALES = K16 && V16 ? 0 : 2 * kChunkKeys * 4;
+  static constexpr int KN = K16 ? 2 : 3, VN = K16 && !V16 ? 1 : 2;  // ring depths
+  static constexpr int NOP = V16 ? 0 : 2;                           // f16 V operand buffers
+  static constexpr int OPT = kChunkKeys * D * 2;
+  static constexpr int VST = VT + 1024 * (SCALES > 0);              // V stage: tile, scales (1024-byte aligned)
+  static constexpr int CST = 2 * kChunkKeys + 4;                    // floats: k, v column scales, largest v scale
+  static constexpr int NCOL = 4;
+  static constexpr int MISC = 512;
+  static constexpr int BYTES = 1024 + QOP + KN * KT + VN * VST + NOP * OPT + NCOL * CST * 4 + MISC;
+  static_assert(2 * (BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+struct ChunkTcParams {
+  CUtensorMap tmk, tmv;
+  ChunkParams p;
+};
+
+template <int N>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
+// D[tmem] (+)= A[tmem] x B[smem]^T, 16-bit operands; one thread issues.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(id), "r"(accumulate));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+template <int KE, int VE>
+__global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant__ ChunkTcParams tp) {
+  using C = CtCfg<KE, VE>;
+  constexpr int D = 128;
+  const ChunkParams& p = tp.p;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qop = smem;
+  uint8_t* kring = qop + C::QOP;
+  uint8_t* vring = kring + C::KN * C::KT;
+  uint8_t* vop = C::V16 ? vring : vring + C::VN * C::VST;
+  float* cols = reinterpret_cast<float*>(vring + C::VN * C::VST + C::NOP * C::OPT);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(cols) + C::NCOL * C::CST * 4);
+  constexpr int OPN = C::V16 ? C::VN : C::NOP;                // operand buffers of P.V
+  uint64_t* kfull = bars;                                     // [KN] K tile landed
+  uint64_t* kfree = kfull + C::KN;                            // [KN] QK has read it
+  uint64_t* vfull = kfree + C::KN;                            // [VN] V tile and scales landed
+  uint64_t* vfree = vfull + C::VN;                            // [VN] converted (bf16: read by P.V)
+  uint64_t* op_full = vfree + C::VN;                          // [OPN] operand of P.V ready
+  uint64_t* op_free = op_full + OPN;                          // [OPN] P.V has read it
+  uint64_t* col_full = op_free + OPN;                         // [NCOL] column scales written
+  uint64_t* s_full = col_full + C::NCOL;                      // [2] scores ready
+  uint64_t* p_full = s_full + 2;                              // P written
+  uint64_t* pv_done = p_full + 1;                             // P.V finished
+  uint64_t* drained = pv_done + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  static_assert(8 * (2 * C::KN + 2 * C::VN + 2 * OPN + C::NCOL + 5) + 8 <= C::MISC, "barriers fit");
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int hk = blockIdx.y, split = blockIdx.z;
+  ChunkTile t;
+  if (!chunk_tile(p, gridDim.x - 1 - blockIdx.x, tid == 0 && hk == 0 && split == 0, t)) return;
+  const int per = (t.n + p.num_splits - 1) / p.num_splits;
+  const int j0 = min(t.n, split * per), n = min(t.n, j0 + per) - j0;
+  const CacheView& c = p.c;
+  const int G = p.group;
+
+  // loads of K tile / V tile j (one thread)
+  const int64_t cont0 = ((int64_t)t.b * c.kv_heads + hk) * c.max_tokens;
+  auto page_needed = [&](int k0, int len) {                   // is any key of [k0, k0 + len) seen by a query?
+    return k0 < t.kv_end && (k0 + len > t.lo || k0 < p.sinks);
+  };
+  auto load_tile = [&](int j, bool is_v) {
+    const int key0 = chunk_key0(t, j0 + j);
+    uint8_t* st = is_v ? vring + (j % C::VN) * C::VST : kring + (j % C::KN) * C::KT;
+    uint64_t* bar = is_v ? &vfull[j % C::VN] : &kfull[j % C::KN];
+    const CUtensorMap* map = is_v ? &tp.tmv : &tp.tmk;
+    const bool wide = is_v ? C::V16 : C::K16;
+    const uint32_t half = kChunkKeys * 128;                   // bf16: dims 64..127 behind dims 0..63
+    float* ksc = reinterpret_cast<float*>(st + C::VT);
+    float* vsc = ksc + kChunkKeys;
+    if (!c.paged) {
+      const int row = (int)(cont0 + key0);
+      const int nsc = min(kChunkKeys, (t.kv_end - key0 + 15) & ~15);
+      const uint32_t sb = is_v ? (uint32_t)nsc * 4 * ((C::K16 ? 0 : 1) + (C::V16 ? 0 : 1)) : 0;
+      tma::arrive_expect_tx(bar, half * (wide ? 2 : 1) + sb);
+      tma::load_2d(st, map, 0, row, bar);
+      if (wide) tma::load_2d(st + half, map, 64, row, bar);
+      if (is_v && !C::K16) tma::load_1d(ksc, c.k_scale + cont0 + key0, nsc * 4, bar);
+      if (is_v && !C::V16) tma::load_1d(vsc, c.v_scale + cont0 + key0, nsc * 4, bar);
+    } else {
+      const int P = c.page_size;
+      int np = 0;
+      for (int k = 0; k < kChunkKeys / P; ++k) np += page_needed(key0 + k * P, P);
+      const uint32_t one = (uint32_t)P * 128 * (wide ? 2 : 1) +
+                           (is_v ? (uint32_t)P * 4 * ((C::K16 ? 0 : 1) + (C::V16 ? 0 : 1)) : 0);
+      tma::arrive_expect_tx(bar, np * one);
+      for (int k = 0; k < kChunkKeys / P; ++k) {
+        if (!page_needed(key0 + k * P, P)) continue;          // a page nobody sees may be gone
+        int page = c.page_table[(int64_t)t.b * c.max_pages_per_seq + ((key0 >> c.page_shift) + k)];
+        if (page < 0 || page >= c.num_pages) {
+          raise_error(p.err, FP8KV_DEVERR_BAD_PAGE);
+          page = 0;
+        }
+        const int64_t row = ((int64_t)page * c.kv_heads + hk) * P;
+        tma::load_2d(st + k * P * 128, map, 0, (int)row, bar);
+        if (wide) tma::load_2d(st + half + k * P * 128, map, 64, (int)row, bar);
+        if (is_v && !C::K16) tma::load_1d(ksc + k * P, c.k_scale + row, P * 4, bar);
+        if (is_v && !C::V16) tma::load_1d(vsc + k * P, c.v_scale + row, P * 4, bar);
+      }
+    }
+  };
+
+  // ---------------------------------------------------------------- setup
+  const int k_first = min(n, C::KN), v_first = min(n, C::VN);
+  if (warp == 8 && lane == 0) {
+    tma::prefetch_map(&tp.tmk);
+    tma::prefetch_map(&tp.tmv);
+    for (int i = 0; i < C::KN; ++i) { umma::mbar_init(&kfull[i], 1); umma::mbar_init(&kfree[i], 1); }
+    for (int i = 0; i < C::VN; ++i) { umma::mbar_init(&vfull[i], 1); umma::mbar_init(&vfree[i], C::V16 ? 1 : 4); }
+    for (int i = 0; i < OPN; ++i) { umma::mbar_init(&op_full[i], 4); umma::mbar_init(&op_free[i], 1); }
+    for (int i = 0; i < C::NCOL; ++i) umma::mbar_init(&col_full[i], 4);
+    umma::mbar_init(&s_full[0], 1);
+    umma::mbar_init(&s_full[1], 1);
+    umma::mbar_init(p_full, 4);
+    umma::mbar_init(pv_done, 1);
+    umma::mbar_init(drained, 1);
+    *abort_flag = 0;
+    umma::mbar_fence_init();
+    for (int j = 0; j < k_first; ++j) load_tile(j, false);
+    for (int j = 0; j < v_first; ++j) load_tile(j, true);
+  }
+  if (warp == 9) {
+    umma::tmem_alloc(tslot, 256);
+    umma::tmem_relinquish();
+  }
+  // softmax warps: this thread's query row -> QK operand
+  const int r = tid & 127;                        // row of the tile, TMEM lane
+  const int tok = r / G;
+  const bool live = warp < 4 && tok < t.ntok && r < p.tile_tokens * G;
+  const int64_t qrow = live ? (int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G) : -1;
+  const int qpos = live ? t.pos0 + tok : -1;
+  int kq = 0;
+  if (warp < 4) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (live ? qrow : 0) * D);
+    if constexpr (C::K16) {
+#pragma unroll
+      for (int ch = 0; ch < 16; ++ch) {
+        uint4 w = live && p.scale_log2 != 0.f ? src[ch] : make_uint4(0, 0, 0, 0);
+        if (p.scale_log2 < 0.f) w = make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
+        *reinterpret_cast<uint4*>(qop + (ch >> 3) * (kCtRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w;
+      }
+    } else {
+      float amax = 0.f;
+#pragma unroll
+      for (int ch = 0; ch < 16; ++ch) {
+        const uint4 w = live ? src[ch] : make_uint4(0, 0, 0, 0);
+        const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float f[2];
+          bf16x2_to_f32(w4[u], f);
+          amax = fmaxf(amax, fmaxf(fabsf(f[0]), fabsf(f[1])));
+        }
+      }
+      kq = amax < INFINITY ? max(-100, min(120, e4m3_row_exp(amax))) : 0;
+      const float qsc = pow2i(-kq);
+#pragma unroll 2
+      for (int ch = 0; ch < 8; ++ch) {             // 16 dims (one 16-byte e4m3 chunk) each
+        const uint4 a = live ? src[2 * ch] : make_uint4(0, 0, 0, 0), b = live ? src[2 * ch + 1] : make_uint4(0, 0, 0, 0);
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float f[2], g[2], hv[4];
+          bf16x2_to_f32(w[2 * u], f);
+          bf16x2_to_f32(w[2 * u + 1], g);
+          const float x0 = f[0] * qsc, x1 = f[1] * qsc, x2 = g[0] * qsc, x3 = g[1] * qsc;
+          hi[u] = e4m3x2_rn(x0, x1) | (e4m3x2_rn(x2, x3) << 16);
+          e4m3x4_to_f32_scaled(hi[u], hv);
+          lo[u] = e4m3x2_rn(x0 - hv[0] * kTwoPow120, x1 - hv[1] * kTwoPow120) |
+                  (e4m3x2_rn(x2 - hv[2] * kTwoPow120, x3 - hv[3] * kTwoPow120) << 16);
+        }
+        const int off = r * 128 + ((ch ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(qop + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(qop + kCtRows * 128 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+    umma::fence_proxy_async_smem();
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = *tslot;
+  const uint32_t o_col = tmem + 128;              // S and P: columns 0-63 and 64-127; O: 128-255
+
+  if (warp >= 8) {
+    reg_dec<32>();
+    if (warp == 8) {
+      // ---------------------------------------------------------- producer
+      if (lane == 0) {
+        int kdone = k_first, vdone = v_first;
+        for (int j = 0; j < n; ++j) {
+          const int jk = j + C::KN, jv = j + C::VN;
+          if (jk < n) {
+            if (!wait_fast(&kfree[jk % C::KN], (jk / C::KN - 1) & 1, abort_flag)) break;
+            load_tile(jk, false);
+            kdone = jk + 1;
+          }
+          if (jv < n) {
+            if (!wait_fast(&vfree[jv % C::VN], (jv / C::VN - 1) & 1, abort_flag)) break;
+            load_tile(jv, true);
+            vdone = jv + 1;
+          }
+        }
+        // no copy is in flight when the CTA ends (matters when a wait gave up)
+        for (int j = max(0, kdone - C::KN); j < kdone; ++j)
+          (void)umma::mbar_wait(&kfull[j % C::KN], (j / C::KN) & 1, 100000000ull);
+        for (int j = max(0, vdone - C::VN); j < vdone; ++j)
+          (void)umma::mbar_wait(&vfull[j % C::VN], (j / C::VN) & 1, 100000000ull);
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t ID_QK = C::K16 ? umma::idesc(umma::FMT_BF16, umma::FMT_BF16, umma::MAJOR_K, umma::MAJOR_K, 128, 64)
+                                          : umma::idesc(umma::FMT_E4M3, umma::FMT_E4M3, umma::MAJOR_K, umma::MAJOR_K, 128, 64);
+        constexpr uint32_t FV = C::V16 ? umma::FMT_BF16 : umma::FMT_F16;
+        constexpr uint32_t ID_PV = umma::idesc(FV, FV, umma::MAJOR_K, umma::MAJOR_MN, 128, 128);
+        const uint32_t qa = umma::smem_u32(qop);
+        auto issue_qk = [&](int j) {
+          if (!wait_fast(&kfull[j % C::KN], (j / C::KN) & 1, abort_flag)) return false;
+          umma::fence_after_sync();
+          const uint32_t ka = umma::smem_u32(kring + (j % C::KN) * C::KT), sd = tmem + 64 * (j & 1);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            // e4m3: 32 dims a step, the four steps of hi and of lo meet the same
+            // K; bf16: 16 dims a step, halves of 64 dims behind each other
+            const uint64_t a = umma::sdesc(qa + (kk >> 2) * (kCtRows * 128) + (kk & 3) * 32, 16, 1024, umma::SWIZZLE_128B);
+            const uint64_t b = umma::sdesc(ka + (C::K16 ? (kk >> 2) * (kChunkKeys * 128) : 0) + (kk & 3) * 32, 16, 1024,
+                                           umma::SWIZZLE_128B);
+            if constexpr (C::K16) umma::mma_f16_ss(sd, a, b, ID_QK, kk > 0);
+            else umma::mma_f8_ss(sd, a, b, ID_QK, kk > 0);
+          }
+          umma::mma_commit(&s_full[j & 1]);
+          umma::mma_commit(&kfree[j % C::KN]);
+          return true;
+        };
+        bool ok = n > 0 && issue_qk(0);
+        if (ok && n > 1) ok = issue_qk(1);
+        for (int j = 0; ok && j < n; ++j) {
+          const int ob = j % OPN;
+          if (!wait_fast(&op_full[ob], (j / OPN) & 1, abort_flag)) break;
+          if (!wait_fast(p_full, j & 1, abort_flag)) break;
+          umma::fence_after_sync();
+          const uint32_t va = umma::smem_u32(vop + ob * (C::V16 ? C::VST : C::OPT)), pa = tmem + 64 * (j & 1);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ts(o_col, pa + 8 * kk, umma::sdesc(va + kk * 2048, kChunkKeys * 128, 1024, umma::SWIZZLE_128B), ID_PV,
+                       (j > 0 || kk > 0) ? 1u : 0u);
+          umma::mma_commit(pv_done);
+          umma::mma_commit(&op_free[ob]);
+          if constexpr (C::V16) umma::mma_commit(&vfree[ob]);
+          if (j + 2 < n) {
+            // the scores of tile j + 2 go where P of tile j was
+            if (!wait_fast(pv_done, j & 1, abort_flag)) break;
+            ok = issue_qk(j + 2);
+          }
+        }
+        // all issued MMAs complete before TMEM is released
+        umma::mma_commit(drained);
+        (void)umma::mbar_wait(drained, 0, 100000000ull);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ preparation
+    reg_dec<56>();
+    const int pt = tid - 128;
+    bool failed = false;
+    for (int j = 0; j < n; ++j) {
+      const int vs = j % C::VN, cb = j % C::NCOL, key0 = chunk_key0(t, j0 + j);
+      bool ok = wait_fast(&vfull[vs], (j / C::VN) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) { failed = true; break; }
+      uint8_t* st = vring + vs * C::VST;
+      const float* ksc = reinterpret_cast<const float*>(st + C::VT);
+      const float* vsc = ksc + kChunkKeys;
+      const bool part = !chunk_all_seen(p, t, key0);
+      float* cc = cols + cb * C::CST;
+      auto seen = [&](int k) { return !part || (key0 + k < t.kv_end && (key0 + k >= t.lo || key0 + k < p.sinks)); };
+      // warp w of the four takes keys 16 w .. 16 w + 15: two lanes a key, each
+      // half of the row
+      const int kr = pt >> 1, hf = pt & 1;
+      const bool vis = seen(kr);
+      bool aside = false;                          // this key's V row holds something not finite
+      if constexpr (C::V16) {
+        if (part) {
+          uint8_t* row = st + hf * (kChunkKeys * 128) + kr * 128;
+          for (int ch = 0; ch < 8; ++ch) {
+            uint4* at = reinterpret_cast<uint4*>(row + (ch << 4));
+            uint4 w = *at;
+            uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            bool bad = false;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const bool b0 = (ww[u] & 0x7F80u) == 0x7F80u, b1 = (ww[u] & 0x7F800000u) == 0x7F800000u;
+              if (b0 || !vis) ww[u] &= 0xFFFF0000u;
+              if (b1 || !vis) ww[u] &= 0x0000FFFFu;
+              bad = bad || b0 || b1;
+            }
+            aside = aside || bad;
+            if (bad || !vis) *at = make_uint4(ww[0], ww[1], ww[2], ww[3]);
+          }
+          umma::fence_proxy_async_smem();
+        }
+      }
+      uint4 w[4];                                  // e4m3: 64 codes of the key
+      if constexpr (!C::V16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int ch = 4 * hf + i;
+          w[i] = *reinterpret_cast<const uint4*>(st + kr * 128 + ((ch ^ (kr & 7)) << 4));
+          if (part) {
+            uint32_t* u = &w[i].x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t nan = (((u[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 per NaN code
+              aside = aside || nan != 0;
+              u[k] = vis ? u[k] & ~(nan * 0xFFu) : 0u;
+            }
+          }
+        }
+      }
+      // (the exchange outside any condition: every lane takes part)
+      const bool other = __shfl_xor_sync(0xffffffffu, (int)aside, 1) != 0;
+      aside = aside || other;
+      if (hf == 0) {
+        const float vv = C::V16 ? 1.f : vis ? vsc[kr] : 0.f;
+        if constexpr (!C::K16) cc[kr] = vis ? ksc[kr] * p.scale_log2 : 0.f;
+        cc[kChunkKeys + kr] = aside && vis ? NAN : vv;
+      }
+      if (!C::V16 && warp == 4) {                  // the tile's largest finite value scale
+        const float a = vsc[lane], b = vsc[lane + 32];
+        const float vm = warp_max(fmaxf(seen(lane) && a < INFINITY ? a : 0.f, seen(lane + 32) && b < INFINITY ? b : 0.f));
+        if (lane == 0) cc[2 * kChunkKeys] = vm;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        umma::mbar_arrive(&col_full[cb]);
+        if constexpr (C::V16) umma::mbar_arrive(&op_full[vs]);
+        else umma::mbar_arrive(&vfree[vs]);
+      }
+      if constexpr (!C::V16) {
+        const int ob = j % C::NOP, ou = j / C::NOP;
+        if (ou > 0) {
+          ok = wait_fast(&op_free[ob], (ou - 1) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) { failed = true; break; }
+        }
+        uint8_t* dst = vop + ob * C::OPT + hf * (kChunkKeys * 128) + kr * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          uint32_t h[8];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            h[2 * u] = e4m3x2_to_f16x2((uint16_t)(ww[u] & 0xFFFF));
+            h[2 * u + 1] = e4m3x2_to_f16x2((uint16_t)(ww[u] >> 16));
+          }
+          *reinterpret_cast<uint4*>(dst + (((2 * i) ^ (kr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + (((2 * i + 1) ^ (kr & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        umma::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&op_full[ob]);
+      }
+    }
+    (void)failed;
+  } else {
+    // ---------------------------------------------------------------- softmax
+    reg_inc<152>();
+    const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
+    // what is left of the score's scale, positive (bf16 keys: the query operand
+    // carries the sign, and is zero for a scale of zero)
+    const float s2 = !C::K16 ? pow2i(kq) : p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1.f;
+    float m_used = -INFINITY, l = 0.f;
+    int kp = -1000;                               // this row's P exponent (none yet)
+    bool failed = false;
+    for (int j = 0; j < n; ++j) {
+      const int cb = j % C::NCOL, key0 = chunk_key0(t, j0 + j);
+      const uint32_t s_col = tmem + 64 * (j & 1) + lane_off;
+      bool ok = wait_fast(&col_full[cb], (j / C::NCOL) & 1, abort_flag);
+      ok = ok && wait_fast(&s_full[j & 1], (j >> 1) & 1, abort_flag);
+      ok = ok && !*abort_flag;
+      if (!__all_sync(0xffffffffu, ok)) { failed = true; break; }
+      umma::fence_after_sync();
+      float2 sv[32];
+      {
+        uint32_t rr[4][16];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) umma::tmem_ld16_nowait(s_col + 16 * k, rr[k]);
+        umma::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int u = 0; u < 8; ++u) sv[8 * k + u] = make_float2(__uint_as_float(rr[k][2 * u]), __uint_as_float(rr[k][2 * u + 1]));
+      }
+      const float4* kc4 = reinterpret_cast<const float4*>(cols + cb * C::CST);
+      const float4* vc4 = kc4 + kChunkKeys / 4;
+      const bool part = !chunk_all_seen(p, t, key0);
+      if constexpr (!C::K16) {
+#pragma unroll
+        for (int q4 = 0; q4 < 16; ++q4) {
+          const float4 kc = kc4[q4];
+          sv[2 * q4] = __fmul2_rn(sv[2 * q4], make_float2(kc.x, kc.y));
+          sv[2 * q4 + 1] = __fmul2_rn(sv[2 * q4 + 1], make_float2(kc.z, kc.w));
+        }
+      }
+      float vmt = C::V16 ? 0.f : cols[cb * C::CST + 2 * kChunkKeys];
+      unsigned long long hide = 0;                // keys this row does not see
+      if (part) {
+        float vm = 0.f;
+#pragma unroll
+        for (int k = 0; k < 64; ++k) {
+          const bool see = chunk_sees(p, qpos, key0 + k);
+          float& x = k & 1 ? sv[k >> 1].y : sv[k >> 1].x;
+          x = see ? x : -INFINITY;
+          if (!see) hide |= 1ull << k;
+          if constexpr (!C::V16) {
+            const float v = reinterpret_cast<const float*>(vc4)[k];
+            vm = fmaxf(vm, see && v < INFINITY ? v : 0.f);
+          }
+        }
+        vmt = vm;
+      }
+      // the row's maximum by three-input max
+      float m8[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        m8[k] = max3(max3(sv[k].x, sv[k].y, sv[k + 8].x), max3(sv[k + 8].y, sv[k + 16].x, sv[k + 16].y),
+                     fmaxf(sv[k + 24].x, sv[k + 24].y));
+      const float mt = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * s2;
+      float alpha = 1.f;
+      if (mt != -INFINITY && (m_used == -INFINITY || mt > m_used + 8.f)) {
+        alpha = m_used == -INFINITY ? 0.f : ex2(m_used - mt);
+        m_used = mt;
+      }
+      float alpha_o = alpha;
+      if constexpr (!C::V16) {
+        if (vmt > 0.f) {
+          const int need = max(-100, min(100, ((__float_as_int(vmt) >> 23) & 0xFF) - 127 - 6));   // vmt 2^-need < 128
+          if (need > kp) {
+            if (kp > -1000) alpha_o *= pow2_diff((float)(kp - need), 0);
+            kp = need;
+          }
+        }
+      }
+      const int kpr = kp > -1000 ? kp : 0;
+      const float neg_m = (m_used == -INFINITY ? 0.f : -m_used) - (float)kpr;
+      const float2 s22 = make_float2(s2, s2), nm2 = make_float2(neg_m, neg_m);
+      float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
+      uint32_t ph[32];
+#pragma unroll
+      for (int q4 = 0; q4 < 16; ++q4) {
+        const float2 a01 = __ffma2_rn(sv[2 * q4], s22, nm2), a23 = __ffma2_rn(sv[2 * q4 + 1], s22, nm2);
+        float2 p01 = make_float2(ex2_ftz(a01.x), ex2_ftz(a01.y));
+        float2 p23 = make_float2(ex2_ftz(a23.x), ex2_ftz(a23.y));
+        la = __fadd2_rn(la, p01);
+        lb = __fadd2_rn(lb, p23);
+        if (!C::V16 || part) {
+          const float4 vc = vc4[q4];
+          p01 = __fmul2_rn(p01, make_float2(vc.x, vc.y));
+          p23 = __fmul2_rn(p23, make_float2(vc.z, vc.w));
+        }
+        if (part) {                               // an unseen key's scale may be anything
+          const uint32_t h = (uint32_t)(hide >> (4 * q4)) & 15u;
+          p01.x = h & 1u ? 0.f : p01.x;
+          p01.y = h & 2u ? 0.f : p01.y;
+          p23.x = h & 4u ? 0.f : p23.x;
+          p23.y = h & 8u ? 0.f : p23.y;
+        }
+        if constexpr (C::V16) {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(p01.x, p01.y), y = __floats2bfloat162_rn(p23.x, p23.y);
+          ph[2 * q4] = *reinterpret_cast<const uint32_t*>(&x);
+          ph[2 * q4 + 1] = *reinterpret_cast<const uint32_t*>(&y);
+        } else {
+          const __half2 x = __floats2half2_rn(p01.x, p01.y), y = __floats2half2_rn(p23.x, p23.y);
+          ph[2 * q4] = *reinterpret_cast<const uint32_t*>(&x);
+          ph[2 * q4 + 1] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+      }
+      l = l * alpha + ((la.x + la.y) + (lb.x + lb.y)) * pow2i(kpr);
+      tmem_st16(s_col, ph);
+      tmem_st16(s_col + 16, ph + 16);
+      // O may be rescaled only when the previous P.V is done
+      if (j > 0) {
+        const bool done = wait_fast(pv_done, (j - 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, done)) { failed = true; break; }
+      }
+      if (__any_sync(0xffffffffu, alpha_o != 1.f && j > 0)) {
+        umma::fence_after_sync();
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          uint32_t rr[16];
+          umma::tmem_ld16_nowait(o_col + lane_off + 16 * k, rr);
+          umma::tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 16; ++u) rr[u] = __float_as_uint(__uint_as_float(rr[u]) * alpha_o);
+          tmem_st16(o_col + lane_off + 16 * k, rr);
+        }
+      }
+      tmem_wait_st();
+      umma::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(p_full);
+    }
+    // ---------------------------------------------------------------- epilogue
+    if (!failed && n > 0) {
+      const bool done = wait_or_abort(pv_done, (n - 1) & 1, abort_flag);
+      failed = !__all_sync(0xffffffffu, done);
+    }
+    if (failed) {
+      if (lane == 0) raise_error(p.err, FP8KV_DEVERR_TIMEOUT);
+    } else {
+      umma::fence_after_sync();
+      const float of = C::V16 || kp <= -1000 ? 1.f : pow2i(kp);
+      const bool whole = p.num_splits == 1;
+      const float f = whole ? (l > 0.f ? of / l : l == l ? 0.f : l) : of;
+      const int64_t at = whole ? qrow : qrow * p.num_splits + split;
+      if (!whole && live) { p.part_m[at] = m_used; p.part_l[at] = l; }
+#pragma unroll 1
+      for (int k = 0; k < 8; ++k) {
+        uint32_t rr[16];
+        if (n > 0) {
+          umma::tmem_ld16_nowait(o_col + lane_off + 16 * k, rr);
+          umma::tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int u = 0; u < 16; ++u) rr[u] = 0u;
+        }
+        if (!live) continue;
+        float o[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) o[u] = __uint_as_float(rr[u]) * f;
+        if (!whole || p.out_f32) {
+          float4* dst = reinterpret_cast<float4*>((whole ? reinterpret_cast<float*>(p.out) : p.part_o) + at * D + 16 * k);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+        } else {
+          uint32_t h[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(o[2 * u], o[2 * u + 1]);
+            h[u] = *reinterpret_cast<const uint32_t*>(&x);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at * D + 16 * k);
+          dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+          dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+      }
+    }
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (warp == 9) umma::tmem_dealloc(tmem, 256);
+}
+
+template <int KE, int VE>
+static cudaError_t launch_one_tc(const ChunkParams& p, int tiles, cudaStream_t st) {
+  using C = CtCfg<KE, VE>;
+  const cudaError_t e = ensure_smem_optin((const void*)chunk_tc<KE, VE>, C::BYTES);
+  if (e != cudaSuccess) return e;
+  ChunkTcParams tp;
+  const CacheView& c = p.c;
+  const int64_t rows = c.paged ? (int64_t)c.num_pages * c.kv_heads * c.page_size
+                               : (int64_t)c.batch * c.kv_heads * c.max_tokens;
+  const int box = c.paged ? c.page_size : kChunkKeys;
+  if (!make_map(&tp.tmk, c.k, C::K16, rows, box) || !make_map(&tp.tmv, c.v, C::V16, rows, box)) return cudaErrorInvalidValue;
+  tp.p = p;
+  chunk_tc<KE, VE><<<dim3(tiles, c.kv_heads, p.num_splits), kCtThreads, C::BYTES, st>>>(tp);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_chunk_tc(const ChunkParams& p, int dtype, int tiles, cudaStream_t st) {
+  if (dtype == FP8KV_K8V8) return launch_one_tc<ELEM_E4M3, ELEM_E4M3>(p, tiles, st);
+  if (dtype == FP8KV_K16V8) return launch_one_tc<ELEM_BF16, ELEM_E4M3>(p, tiles, st);
+  if (dtype == FP8KV_K8V16) return launch_one_tc<ELEM_E4M3, ELEM_BF16>(p, tiles, st);
+  return launch_one_tc<ELEM_BF16, ELEM_BF16>(p, tiles, st);
+}
+
+}  // namespace fp8kv

@@ -458,9 +458,10 @@ FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q
  *   sinks:      >= 0; no effect without a window
  *   num_splits: CTAs that share the keys of one tile of queries, joined by a
  *               second kernel; 0: chosen from the sizes (1 for long chunks)
- *   kernel:     FP8KV_KERNEL_AUTO, or _WARP_MMA (every cache type but
- *               rotated-bias residual keys, which return
- *               FP8KV_ERR_UNSUPPORTED; group 1 to 16)
+ *   kernel:     FP8KV_KERNEL_AUTO; _WARP_MMA (every cache type but rotated-bias
+ *               residual keys, which return FP8KV_ERR_UNSUPPORTED; group 1 to
+ *               16); or _TENSOR_CORES (128-row tiles on tcgen05: head_dim 128,
+ *               not FP8KV_MXK8V8, else FP8KV_ERR_UNSUPPORTED)
  *   workspace:  fp8kv_chunk_workspace_bytes() bytes, 16-byte aligned, nothing
  *               need be zero; NULL if that is 0.  Calls that may run at once
  *               need one each.
@@ -468,7 +469,10 @@ FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q
  *               16-byte aligned
  * A query that sees no key (its position is negative: seq_lens[b] is less than
  * its sequence's queries) gets a zero row.  Keys that a query does not see
- * have no influence on it, whatever they hold (NaN included).  A length below
+ * have no influence on it, whatever they hold (NaN included; pages that no
+ * query sees need not exist).  A seen value that is not finite makes that
+ * element of the row not finite; the tensor-core kernel may make the whole row
+ * NaN.  A length below
  * 0 or past the capacity raises SEQ_TOO_LONG and gives zero rows; offsets that
  * decrease or pass total_q raise it and leave their rows as they were. */
 FP8KV_API fp8kv_status fp8kv_chunk_attention(const void *q, const fp8kv_cache *cache,

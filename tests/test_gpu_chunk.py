@@ -120,8 +120,8 @@ def definition(q, kv, cu, lens, window, sinks, sm):
             w = torch.softmax(s, -1)
             o[r] = torch.einsum("hk,khd->hd", w, vv)
             pv[r] = torch.einsum("hk,khd->hd", w, vv.abs())
-            qk[r] = (torch.einsum("hd,khd->hk", q[r].abs(), kk.abs()) * sm).amax(-1)
-            qs[r] = q[r].abs().amax(-1) * kk.abs().sum(-1).amax(0) * sm
+            qk[r] = (torch.einsum("hd,khd->hk", q[r].abs(), kk.abs()) * abs(sm)).amax(-1)
+            qs[r] = q[r].abs().amax(-1) * kk.abs().sum(-1).amax(0) * abs(sm)
             keys[r], vmax[r] = len(j), vv.abs().amax((0, 2))
     return o, pv, qk, qs, keys, vmax
 
@@ -158,7 +158,7 @@ def run_case(dtype, D, Hq, Hkv, cached, new, page, seed, window=0, sinks=0, kern
 
 
 DTYPES = ["k8v8", "k16v8", "k8v16", "k16v16", "mxk8v8"]
-KERNELS = ["warp_mma"]
+KERNELS = ["warp_mma", "tensor_cores"]
 
 
 @pytest.mark.parametrize("page", [0, 16])
@@ -170,6 +170,28 @@ def test_types(dtype, D, page):
     if dtype == "mxk8v8" and D == 64:
         pytest.skip("block-scaled keys are built for head dim 128")
     run_case(dtype, D, 6, 2, [0, 37, 130, 64], [67, 0, 41, 1], page, seed=1, kernel="warp_mma")
+
+
+@pytest.mark.parametrize("page", [0, 16, 64])
+@pytest.mark.parametrize("dtype", ["k8v8", "k16v8", "k8v16", "k16v16"])
+def test_types_tensor_cores(dtype, page):
+    """The same on tcgen05, with 128-row tiles that are full, ragged, of one
+    token, and longer than the rings."""
+    run_case(dtype, 128, 6, 2, [0, 37, 130, 64, 700], [67, 0, 41, 1, 130], page, seed=1, kernel="tensor_cores")
+
+
+@pytest.mark.parametrize("dtype", ["k8v8", "k16v16"])
+@pytest.mark.parametrize("sm", [0.0, -0.11, 2.0])
+def test_score_scale(dtype, sm):
+    """A scale of zero (every seen key weighs the same), a negative and a large one."""
+    lens, cu = [90, 200], [0, 50, 200]
+    cache = make_cache(dtype, 128, 2, lens, 16, seed=21)
+    q = torch.randn(200, 4, 128, device="cuda").to(torch.bfloat16)
+    for kernel in KERNELS:
+        out = fk.fp8kv_chunk_attention(q, cache, _i32(cu), _i32(lens), sm_scale=sm, out_dtype=torch.float32, kernel=kernel)
+        assert fk.fp8kv_get_device_error() == 0
+        o, pv, qk, qs, keys, vmax = definition(q, cache_values(cache, lens), cu, lens, 0, 0, sm)
+        check(out, cache, (o, pv, qk, qs, keys, vmax), slice(0, 200), kernel)
 
 
 @pytest.mark.parametrize("dtype,D", [("k8v8", 128), ("k8v8", 64), ("k16v16", 128), ("mxk8v8", 128), ("k8v16", 64)])
@@ -244,12 +266,14 @@ def test_v_scales_spread(kernel):
     run_case("k8v8", 128, 8, 2, [900, 500], [1, 1], 16, seed=9, spread=9.0)
 
 
-@pytest.mark.parametrize("dtype,kernel", [("k8v8", "warp_mma"), ("k16v16", "warp_mma"), ("k16v8", "warp_mma")])
+@pytest.mark.parametrize("dtype,kernel", [("k8v8", "warp_mma"), ("k16v16", "warp_mma"), ("k16v8", "warp_mma"),
+                                          ("k8v8", "tensor_cores"), ("k16v16", "tensor_cores"), ("k8v16", "tensor_cores")])
 @pytest.mark.parametrize("what", ["k_row", "v_nan", "v_inf", "v_huge"])
 def test_unseen_poison(dtype, kernel, what):
     """Non-finite rows at some positions of the sequence itself: the queries
     that do not see them come out as if they were not there, those that do see
-    a value that is not finite get one in that element."""
+    a value that is not finite get one in that element (on the tensor-core
+    kernel perhaps in the others of the row too)."""
     lens, new, window, sinks = [200], [120], 40, 3
     D, Hkv, Hq = 128, 1, 2
     bad = [100, 150, 199]
@@ -283,7 +307,7 @@ def test_unseen_poison(dtype, kernel, what):
         assert (out[sees].abs() > 2.0 ** 60).all()
     else:
         assert not torch.isfinite(out[sees][..., 5]).any()
-    if what == "v_nan" and kernel == "warp_mma" or (what == "v_inf" and not coded):
+    if kernel == "warp_mma" and (what == "v_nan" or what == "v_inf" and not coded):
         rest = [d for d in range(D) if d != 5]
         assert torch.isfinite(out[sees][..., rest]).all()
 
@@ -312,6 +336,22 @@ def test_many_sequences():
     new = (rng.integers(0, 4, 1500) * (rng.random(1500) < 0.4)).tolist()
     cached = rng.integers(0, 40, 1500).tolist()
     run_case("k8v8", 64, 2, 1, cached, new, 16, seed=12)
+    run_case("k8v8", 128, 2, 1, cached, new, 16, seed=12, kernel="tensor_cores")
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_pages_behind_the_window_may_be_gone(kernel):
+    """A windowed sequence whose old pages were given back: their table entries
+    are out of range, and nothing reads them."""
+    lens, cu = [900, 400], [0, 100, 101]
+    cache = make_cache("k8v8", 128, 2, lens, 16, seed=22)
+    q = torch.randn(101, 8, 128, device="cuda").to(torch.bfloat16)
+    args = dict(window=50, sinks=4, out_dtype=torch.float32, kernel=kernel)
+    ref = fk.fp8kv_chunk_attention(q, cache, _i32(cu), _i32(lens), **args)
+    cache.page_table[0, 1:(900 - 100 - 50) // 16] = -5
+    cache.page_table[1, 1:(400 - 50) // 16] = 1 << 30
+    out = fk.fp8kv_chunk_attention(q, cache, _i32(cu), _i32(lens), **args)
+    assert fk.fp8kv_get_device_error() == 0 and torch.equal(out, ref)
 
 
 def test_offsets_past_32_bits():
@@ -327,8 +367,9 @@ def test_offsets_past_32_bits():
             src, dst = int(small.page_table[b, i]), int(table[b, i])
             big.k[dst], big.v[dst] = small.k[src], small.v[src]
     q = torch.randn(31, 8, D, device="cuda").to(torch.bfloat16)
-    args = (_i32([0, 30, 31]), _i32(lens))
-    assert torch.equal(fk.fp8kv_chunk_attention(q, big, *args), fk.fp8kv_chunk_attention(q, small, *args))
+    for kernel in KERNELS:
+        args = (_i32([0, 30, 31]), _i32(lens))
+        assert torch.equal(fk.fp8kv_chunk_attention(q, big, *args, kernel=kernel), fk.fp8kv_chunk_attention(q, small, *args, kernel=kernel))
     assert fk.fp8kv_get_device_error() == 0
 
 

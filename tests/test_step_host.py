@@ -105,6 +105,9 @@ def test_chunk_refusals_by_cache(lib):
     turning = _cache(k_bias=0x8000, rope_cos=0x9000, rope_sin=0xA000, rope_positions=2048)
     assert lib.fp8kv_chunk_attention(0x10000, turning, *args) == UNSUPPORTED
     assert lib.fp8kv_chunk_attention(0x10000, None, *args) == INVALID
+    tc = args[:8] + (2,) + args[9:]
+    for kw in (dict(head_dim=64), dict(dtype=4)):
+        assert lib.fp8kv_chunk_attention(0x10000, _cache(**kw), *tc) == UNSUPPORTED
     # other calls do not know the chunk kernel's name
     assert lib.fp8kv_prefill_attention(0x10000, _cache(), 0x20000, 16, 4, 0.1, 5, 0x40000, 0, None) == INVALID
     assert lib.fp8kv_decode_split(0x10000, _cache(), 0x20000, 4, 0.1, 0, 5, 0x30000, 1 << 30, None) == INVALID
@@ -117,7 +120,7 @@ def test_chunk_plan(lib):
     long = dict(batch=1, max_tokens=65536)
     assert n(_cache(**long), 1, 4, 0, 0, 0, 0) > 8
     assert n(_cache(**long), 1, 4, 128, 4, 0, 0) <= 2
-    assert n(_cache(**long), 4096, 4, 0, 0, 0, 0) == 1
+    assert n(_cache(**long), 16384, 4, 0, 0, 0, 0) == 1
     assert n(_cache(max_tokens=64), 4, 4, 0, 0, 100, 0) == 2
     assert n(_cache(), 4, 3, 0, 0, 0, 0) == 0
     assert lib.fp8kv_chunk_workspace_bytes(_cache(), 4, 4, 0, 0, 3, 0) == 4 * 4 * 3 * 130 * 4
