@@ -29,7 +29,7 @@
 //               tile that not every query sees whole, rows nobody sees are
 //               zeroed and a row with non-finite values is zeroed and its
 //               scale set to NaN: queries that see it get NaN, others nothing
-//   warp 8      TMA producer: K ring and V ring (with the scale rows)
+//   warps 8, 10 TMA producers: K ring, and V ring with the scale rows
 //   warp 9      TMEM owner and MMA issuer
 // Every wait is bounded; one that runs out raises FP8KV_DEVERR_TIMEOUT.
 #include "chunk_common.cuh"
@@ -134,7 +134,20 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   auto page_needed = [&](int k0, int len) {                   // is any key of [k0, k0 + len) seen by a query?
     return k0 < t.kv_end && (k0 + len > t.lo || k0 < p.sinks);
   };
-  auto load_tile = [&](int j, bool is_v) {
+  // One warp loads the K tiles, one the V tiles with the scale rows.  Paged:
+  // lane 4 i + k keeps the page id of page k of tile 8 q + i, fetched for eight
+  // tiles at once and one group ahead, so no copy waits for the page table.
+  const int pages = c.paged ? kChunkKeys / c.page_size : 0;
+  auto fetch_ids = [&](int group) {
+    const int j = 8 * group + (lane >> 2), k = lane & 3;
+    int page = 0;
+    if (k < pages && j < n) {
+      const int key = chunk_key0(t, j0 + j) + k * c.page_size;
+      if (page_needed(key, c.page_size)) page = c.page_table[(int64_t)t.b * c.max_pages_per_seq + (key >> c.page_shift)];
+    }
+    return page;
+  };
+  auto load_tile = [&](int j, bool is_v, int ids) {
     const int key0 = chunk_key0(t, j0 + j);
     uint8_t* st = is_v ? vring + (j % C::VN) * C::VST : kring + (j % C::KN) * C::KT;
     uint64_t* bar = is_v ? &vfull[j % C::VN] : &kfull[j % C::KN];
@@ -143,40 +156,43 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     const uint32_t half = kChunkKeys * 128;                   // bf16: dims 64..127 behind dims 0..63
     float* ksc = reinterpret_cast<float*>(st + C::VT);
     float* vsc = ksc + kChunkKeys;
+    const int sides = is_v ? (C::K16 ? 0 : 1) + (C::V16 ? 0 : 1) : 0;   // scale rows beside the tile
     if (!c.paged) {
+      if (lane != 0) return;
       const int row = (int)(cont0 + key0);
       const int nsc = min(kChunkKeys, (t.kv_end - key0 + 15) & ~15);
-      const uint32_t sb = is_v ? (uint32_t)nsc * 4 * ((C::K16 ? 0 : 1) + (C::V16 ? 0 : 1)) : 0;
-      tma::arrive_expect_tx(bar, half * (wide ? 2 : 1) + sb);
+      tma::arrive_expect_tx(bar, half * (wide ? 2 : 1) + (uint32_t)nsc * 4 * sides);
       tma::load_2d(st, map, 0, row, bar);
       if (wide) tma::load_2d(st + half, map, 64, row, bar);
       if (is_v && !C::K16) tma::load_1d(ksc, c.k_scale + cont0 + key0, nsc * 4, bar);
       if (is_v && !C::V16) tma::load_1d(vsc, c.v_scale + cont0 + key0, nsc * 4, bar);
     } else {
       const int P = c.page_size;
-      int np = 0;
-      for (int k = 0; k < kChunkKeys / P; ++k) np += page_needed(key0 + k * P, P);
-      const uint32_t one = (uint32_t)P * 128 * (wide ? 2 : 1) +
-                           (is_v ? (uint32_t)P * 4 * ((C::K16 ? 0 : 1) + (C::V16 ? 0 : 1)) : 0);
-      tma::arrive_expect_tx(bar, np * one);
-      for (int k = 0; k < kChunkKeys / P; ++k) {
-        if (!page_needed(key0 + k * P, P)) continue;          // a page nobody sees may be gone
-        int page = c.page_table[(int64_t)t.b * c.max_pages_per_seq + ((key0 >> c.page_shift) + k)];
+      int page = __shfl_sync(0xffffffffu, ids, (j & 7) * 4 + (lane & 3));
+      const bool mine = lane < pages && page_needed(key0 + lane * P, P);   // a page nobody sees may be gone
+      const int np = __popc(__ballot_sync(0xffffffffu, mine));
+      if (lane == 0) tma::arrive_expect_tx(bar, np * (uint32_t)P * (128 * (wide ? 2 : 1) + 4 * sides));
+      __syncwarp();
+      if (mine) {
         if (page < 0 || page >= c.num_pages) {
           raise_error(p.err, FP8KV_DEVERR_BAD_PAGE);
           page = 0;
         }
         const int64_t row = ((int64_t)page * c.kv_heads + hk) * P;
-        tma::load_2d(st + k * P * 128, map, 0, (int)row, bar);
-        if (wide) tma::load_2d(st + half + k * P * 128, map, 64, (int)row, bar);
-        if (is_v && !C::K16) tma::load_1d(ksc + k * P, c.k_scale + row, P * 4, bar);
-        if (is_v && !C::V16) tma::load_1d(vsc + k * P, c.v_scale + row, P * 4, bar);
+        tma::load_2d(st + lane * P * 128, map, 0, (int)row, bar);
+        if (wide) tma::load_2d(st + half + lane * P * 128, map, 64, (int)row, bar);
+        if (is_v && !C::K16) tma::load_1d(ksc + lane * P, c.k_scale + row, P * 4, bar);
+        if (is_v && !C::V16) tma::load_1d(vsc + lane * P, c.v_scale + row, P * 4, bar);
       }
     }
   };
 
   // ---------------------------------------------------------------- setup
-  const int k_first = min(n, C::KN), v_first = min(n, C::VN);
+  int ids = 0, next_ids = 0;                      // page ids of this group of eight tiles and of the next
+  if (warp == 8 || warp == 10) {
+    ids = fetch_ids(0);
+    next_ids = fetch_ids(1);
+  }
   if (warp == 8 && lane == 0) {
     tma::prefetch_map(&tp.tmk);
     tma::prefetch_map(&tp.tmv);
@@ -191,8 +207,6 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     umma::mbar_init(drained, 1);
     *abort_flag = 0;
     umma::mbar_fence_init();
-    for (int j = 0; j < k_first; ++j) load_tile(j, false);
-    for (int j = 0; j < v_first; ++j) load_tile(j, true);
   }
   if (warp == 9) {
     umma::tmem_alloc(tslot, 256);
@@ -260,29 +274,29 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
 
   if (warp >= 8) {
     reg_dec<32>();
-    if (warp == 8) {
-      // ---------------------------------------------------------- producer
-      if (lane == 0) {
-        int kdone = k_first, vdone = v_first;
-        for (int j = 0; j < n; ++j) {
-          const int jk = j + C::KN, jv = j + C::VN;
-          if (jk < n) {
-            if (!wait_fast(&kfree[jk % C::KN], (jk / C::KN - 1) & 1, abort_flag)) break;
-            load_tile(jk, false);
-            kdone = jk + 1;
-          }
-          if (jv < n) {
-            if (!wait_fast(&vfree[jv % C::VN], (jv / C::VN - 1) & 1, abort_flag)) break;
-            load_tile(jv, true);
-            vdone = jv + 1;
-          }
+    if (warp == 8 || warp == 10) {
+      // ---------------------------------------------------------- producers
+      const bool is_v = warp == 10;
+      const int depth = is_v ? C::VN : C::KN;
+      uint64_t* full = is_v ? vfull : kfull;
+      uint64_t* free_ = is_v ? vfree : kfree;
+      int done = 0;
+      for (int j = 0; j < n; ++j) {
+        if (j >= depth) {
+          const bool ok = wait_fast(&free_[j % depth], (j / depth - 1) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) break;
         }
-        // no copy is in flight when the CTA ends (matters when a wait gave up)
-        for (int j = max(0, kdone - C::KN); j < kdone; ++j)
-          (void)umma::mbar_wait(&kfull[j % C::KN], (j / C::KN) & 1, 100000000ull);
-        for (int j = max(0, vdone - C::VN); j < vdone; ++j)
-          (void)umma::mbar_wait(&vfull[j % C::VN], (j / C::VN) & 1, 100000000ull);
+        if (j > 0 && (j & 7) == 0) {
+          ids = next_ids;
+          next_ids = fetch_ids((j >> 3) + 1);
+        }
+        load_tile(j, is_v, ids);
+        done = j + 1;
       }
+      // no copy is in flight when the CTA ends (matters when a wait gave up)
+      if (lane == 0)
+        for (int j = max(0, done - depth); j < done; ++j)
+          (void)umma::mbar_wait(&full[j % depth], (j / depth) & 1, 100000000ull);
     } else if (warp == 9) {
       // ---------------------------------------------------------- MMA issuer
       if (lane == 0) {
