@@ -23,21 +23,22 @@
 // KB of shared memory, so two CTAs share an SM: one's softmax runs while the
 // other's products, prologue or epilogue do.
 //
-// Warp roles (registers moved between the warpgroups by setmaxnreg, 3 x 80):
+// Warp roles (256 threads, so that a thread has 128 registers at two CTAs):
 //   warps 0-3   softmax, one query row (TMEM lane) per thread; epilogue
-//   warps 4-7   preparation: per-key scales; e4m3 V codes -> f16 operand; in a
-//               tile that not every query sees whole, rows nobody sees are
-//               zeroed and a row with non-finite values is zeroed and its
-//               scale set to NaN: queries that see it get NaN, others nothing
-//   warps 8, 10 TMA producers: K ring, and V ring with the scale rows
-//   warp 9      TMEM owner and MMA issuer
+//   warps 4-5   preparation, one key per thread: per-key scales; e4m3 V codes
+//               -> f16 operand; in a tile that not every query sees whole,
+//               rows nobody sees are zeroed, and a row with non-finite values
+//               is cleared of them and its key scale set to NaN: queries that
+//               see it get NaN, the others nothing
+//   warp 6      TMA producer: K ring, and V ring with the scale rows
+//   warp 7      TMEM owner and MMA issuer
 // Every wait is bounded; one that runs out raises FP8KV_DEVERR_TIMEOUT.
 #include "chunk_common.cuh"
 #include "tc_common.cuh"
 
 namespace fp8kv {
 
-constexpr int kCtRows = 128, kCtThreads = 384;
+constexpr int kCtRows = 128, kCtThreads = 256;
 
 template <int KE, int VE>
 struct CtCfg {
@@ -62,11 +63,6 @@ struct ChunkTcParams {
   CUtensorMap tmk, tmv;
   ChunkParams p;
 };
-
-template <int N>
-__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
 
 // D[tmem] (+)= A[tmem] x B[smem]^T, 16-bit operands; one thread issues.
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t accumulate) {
@@ -134,8 +130,8 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   auto page_needed = [&](int k0, int len) {                   // is any key of [k0, k0 + len) seen by a query?
     return k0 < t.kv_end && (k0 + len > t.lo || k0 < p.sinks);
   };
-  // One warp loads the K tiles, one the V tiles with the scale rows.  Paged:
-  // lane 4 i + k keeps the page id of page k of tile 8 q + i, fetched for eight
+  // The producer warp loads the K tiles and the V tiles with the scale rows.
+  // Paged: lane 4 i + k keeps the page id of page k of tile 8 q + i, fetched for eight
   // tiles at once and one group ahead, so no copy waits for the page table.
   const int pages = c.paged ? kChunkKeys / c.page_size : 0;
   auto fetch_ids = [&](int group) {
@@ -189,17 +185,17 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
 
   // ---------------------------------------------------------------- setup
   int ids = 0, next_ids = 0;                      // page ids of this group of eight tiles and of the next
-  if (warp == 8 || warp == 10) {
+  if (warp == 6) {
     ids = fetch_ids(0);
     next_ids = fetch_ids(1);
   }
-  if (warp == 8 && lane == 0) {
+  if (warp == 6 && lane == 0) {
     tma::prefetch_map(&tp.tmk);
     tma::prefetch_map(&tp.tmv);
     for (int i = 0; i < C::KN; ++i) { umma::mbar_init(&kfull[i], 1); umma::mbar_init(&kfree[i], 1); }
-    for (int i = 0; i < C::VN; ++i) { umma::mbar_init(&vfull[i], 1); umma::mbar_init(&vfree[i], C::V16 ? 1 : 4); }
-    for (int i = 0; i < OPN; ++i) { umma::mbar_init(&op_full[i], 4); umma::mbar_init(&op_free[i], 1); }
-    for (int i = 0; i < C::NCOL; ++i) umma::mbar_init(&col_full[i], 4);
+    for (int i = 0; i < C::VN; ++i) { umma::mbar_init(&vfull[i], 1); umma::mbar_init(&vfree[i], C::V16 ? 1 : 2); }
+    for (int i = 0; i < OPN; ++i) { umma::mbar_init(&op_full[i], 2); umma::mbar_init(&op_free[i], 1); }
+    for (int i = 0; i < C::NCOL; ++i) umma::mbar_init(&col_full[i], 2);
     umma::mbar_init(&s_full[0], 1);
     umma::mbar_init(&s_full[1], 1);
     umma::mbar_init(p_full, 4);
@@ -208,7 +204,7 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     *abort_flag = 0;
     umma::mbar_fence_init();
   }
-  if (warp == 9) {
+  if (warp == 7) {
     umma::tmem_alloc(tslot, 256);
     umma::tmem_relinquish();
   }
@@ -272,32 +268,45 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   const uint32_t tmem = *tslot;
   const uint32_t o_col = tmem + 128;              // S and P: columns 0-63 and 64-127; O: 128-255
 
-  if (warp >= 8) {
-    reg_dec<32>();
-    if (warp == 8 || warp == 10) {
-      // ---------------------------------------------------------- producers
-      const bool is_v = warp == 10;
-      const int depth = is_v ? C::VN : C::KN;
-      uint64_t* full = is_v ? vfull : kfull;
-      uint64_t* free_ = is_v ? vfree : kfree;
-      int done = 0;
-      for (int j = 0; j < n; ++j) {
-        if (j >= depth) {
-          const bool ok = wait_fast(&free_[j % depth], (j / depth - 1) & 1, abort_flag);
-          if (!__all_sync(0xffffffffu, ok)) break;
+  if (warp >= 6) {
+    if (warp == 6) {
+      // ---------------------------------------------------------- producer
+      // V tile j goes out behind K tile j + KN - VN (the K ring is the deeper
+      // one); a V tile's page ids may be those of the group before
+      constexpr int LEAD = C::KN - C::VN;
+      int old_ids = ids, kdone = 0, vdone = 0;
+      for (int i = 0; i < n + LEAD; ++i) {
+        if (i < n) {
+          if (i >= C::KN) {
+            const bool ok = wait_fast(&kfree[i % C::KN], (i / C::KN - 1) & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
+          }
+          if (i > 0 && (i & 7) == 0) {
+            old_ids = ids;
+            ids = next_ids;
+            next_ids = fetch_ids((i >> 3) + 1);
+          }
+          load_tile(i, false, ids);
+          kdone = i + 1;
         }
-        if (j > 0 && (j & 7) == 0) {
-          ids = next_ids;
-          next_ids = fetch_ids((j >> 3) + 1);
+        const int j = i - LEAD;
+        if (j >= 0) {
+          if (j >= C::VN) {
+            const bool ok = wait_fast(&vfree[j % C::VN], (j / C::VN - 1) & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) break;
+          }
+          load_tile(j, true, (j >> 3) == (min(i, n - 1) >> 3) ? ids : old_ids);
+          vdone = j + 1;
         }
-        load_tile(j, is_v, ids);
-        done = j + 1;
       }
       // no copy is in flight when the CTA ends (matters when a wait gave up)
-      if (lane == 0)
-        for (int j = max(0, done - depth); j < done; ++j)
-          (void)umma::mbar_wait(&full[j % depth], (j / depth) & 1, 100000000ull);
-    } else if (warp == 9) {
+      if (lane == 0) {
+        for (int j = max(0, kdone - C::KN); j < kdone; ++j)
+          (void)umma::mbar_wait(&kfull[j % C::KN], (j / C::KN) & 1, 100000000ull);
+        for (int j = max(0, vdone - C::VN); j < vdone; ++j)
+          (void)umma::mbar_wait(&vfull[j % C::VN], (j / C::VN) & 1, 100000000ull);
+      }
+    } else {
       // ---------------------------------------------------------- MMA issuer
       if (lane == 0) {
         constexpr uint32_t ID_QK = C::K16 ? umma::idesc(umma::FMT_BF16, umma::FMT_BF16, umma::MAJOR_K, umma::MAJOR_K, 128, 64)
@@ -351,30 +360,24 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ preparation
-    reg_dec<56>();
-    const int pt = tid - 128;
-    bool failed = false;
+    const int kr = tid - 128;                     // this thread's key of the tile
     for (int j = 0; j < n; ++j) {
       const int vs = j % C::VN, cb = j % C::NCOL, key0 = chunk_key0(t, j0 + j);
       bool ok = wait_fast(&vfull[vs], (j / C::VN) & 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) { failed = true; break; }
+      if (!__all_sync(0xffffffffu, ok)) break;
       uint8_t* st = vring + vs * C::VST;
       const float* ksc = reinterpret_cast<const float*>(st + C::VT);
       const float* vsc = ksc + kChunkKeys;
       const bool part = !chunk_all_seen(p, t, key0);
       float* cc = cols + cb * C::CST;
       auto seen = [&](int k) { return !part || (key0 + k < t.kv_end && (key0 + k >= t.lo || key0 + k < p.sinks)); };
-      // warp w of the four takes keys 16 w .. 16 w + 15: two lanes a key, each
-      // half of the row
-      const int kr = pt >> 1, hf = pt & 1;
       const bool vis = seen(kr);
       bool aside = false;                          // this key's V row holds something not finite
       if constexpr (C::V16) {
         if (part) {
-          uint8_t* row = st + hf * (kChunkKeys * 128) + kr * 128;
-          for (int ch = 0; ch < 8; ++ch) {
-            uint4* at = reinterpret_cast<uint4*>(row + (ch << 4));
-            uint4 w = *at;
+          for (int ch = 0; ch < 16; ++ch) {
+            uint4* at = reinterpret_cast<uint4*>(st + (ch >> 3) * (kChunkKeys * 128) + kr * 128 + (((ch & 7) ^ (kr & 7)) << 4));
+            const uint4 w = *at;
             uint32_t ww[4] = {w.x, w.y, w.z, w.w};
             bool bad = false;
 #pragma unroll
@@ -390,34 +393,29 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
           umma::fence_proxy_async_smem();
         }
       }
-      uint4 w[4];                                  // e4m3: 64 codes of the key
+      uint32_t w[C::V16 ? 1 : 32];                 // e4m3: the key's 128 codes
       if constexpr (!C::V16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ch = 4 * hf + i;
-          w[i] = *reinterpret_cast<const uint4*>(st + kr * 128 + ((ch ^ (kr & 7)) << 4));
-          if (part) {
-            uint32_t* u = &w[i].x;
+        for (int ch = 0; ch < 8; ++ch) {
+          const uint4 x = *reinterpret_cast<const uint4*>(st + kr * 128 + ((ch ^ (kr & 7)) << 4));
+          w[4 * ch] = x.x; w[4 * ch + 1] = x.y; w[4 * ch + 2] = x.z; w[4 * ch + 3] = x.w;
+        }
+        if (part) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t nan = (((u[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 per NaN code
-              aside = aside || nan != 0;
-              u[k] = vis ? u[k] & ~(nan * 0xFFu) : 0u;
-            }
+          for (int k = 0; k < 32; ++k) {
+            const uint32_t nan = (((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 per NaN code
+            aside = aside || nan != 0;
+            w[k] = vis ? w[k] & ~(nan * 0xFFu) : 0u;
           }
         }
       }
-      // (the exchange outside any condition: every lane takes part)
-      const bool other = __shfl_xor_sync(0xffffffffu, (int)aside, 1) != 0;
-      aside = aside || other;
-      if (hf == 0) {
-        const float vv = C::V16 ? 1.f : vis ? vsc[kr] : 0.f;
-        if constexpr (!C::K16) cc[kr] = vis ? ksc[kr] * p.scale_log2 : 0.f;
-        cc[kChunkKeys + kr] = aside && vis ? NAN : vv;
-      }
+      const float vv = C::V16 || !vis ? 0.f : vsc[kr];
+      aside = (aside || !(fabsf(vv) < INFINITY)) && part && vis;
+      cc[kr] = aside ? NAN : C::K16 ? 1.f : vis ? ksc[kr] * p.scale_log2 : 0.f;
+      if constexpr (!C::V16) cc[kChunkKeys + kr] = aside ? 0.f : vv;
       if (!C::V16 && warp == 4) {                  // the tile's largest finite value scale
         const float a = vsc[lane], b = vsc[lane + 32];
-        const float vm = warp_max(fmaxf(seen(lane) && a < INFINITY ? a : 0.f, seen(lane + 32) && b < INFINITY ? b : 0.f));
+        const float vm = warp_max_f32(fmaxf(seen(lane) && a < INFINITY ? a : 0.f, seen(lane + 32) && b < INFINITY ? b : 0.f));
         if (lane == 0) cc[2 * kChunkKeys] = vm;
       }
       __syncwarp();
@@ -430,30 +428,21 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
         const int ob = j % C::NOP, ou = j / C::NOP;
         if (ou > 0) {
           ok = wait_fast(&op_free[ob], (ou - 1) & 1, abort_flag);
-          if (!__all_sync(0xffffffffu, ok)) { failed = true; break; }
+          if (!__all_sync(0xffffffffu, ok)) break;
         }
-        uint8_t* dst = vop + ob * C::OPT + hf * (kChunkKeys * 128) + kr * 128;
+        uint8_t* dst = vop + ob * C::OPT + kr * 128;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          uint32_t h[8];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            h[2 * u] = e4m3x2_to_f16x2((uint16_t)(ww[u] & 0xFFFF));
-            h[2 * u + 1] = e4m3x2_to_f16x2((uint16_t)(ww[u] >> 16));
-          }
-          *reinterpret_cast<uint4*>(dst + (((2 * i) ^ (kr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + (((2 * i + 1) ^ (kr & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-        }
+        for (int ch = 0; ch < 16; ++ch)            // 8 dims each; 64 dims a half
+          *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kChunkKeys * 128) + (((ch & 7) ^ (kr & 7)) << 4)) =
+              make_uint4(e4m3x2_to_f16x2((uint16_t)(w[2 * ch] & 0xFFFF)), e4m3x2_to_f16x2((uint16_t)(w[2 * ch] >> 16)),
+                         e4m3x2_to_f16x2((uint16_t)(w[2 * ch + 1] & 0xFFFF)), e4m3x2_to_f16x2((uint16_t)(w[2 * ch + 1] >> 16)));
         umma::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) umma::mbar_arrive(&op_full[ob]);
       }
     }
-    (void)failed;
   } else {
     // ---------------------------------------------------------------- softmax
-    reg_inc<152>();
     const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
     // what is left of the score's scale, positive (bf16 keys: the query operand
     // carries the sign, and is zero for a scale of zero)
@@ -480,9 +469,9 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
 #pragma unroll
           for (int u = 0; u < 8; ++u) sv[8 * k + u] = make_float2(__uint_as_float(rr[k][2 * u]), __uint_as_float(rr[k][2 * u + 1]));
       }
-      const float4* kc4 = reinterpret_cast<const float4*>(cols + cb * C::CST);
+      const float* cc = cols + cb * C::CST;
+      const float4* kc4 = reinterpret_cast<const float4*>(cc);
       const float4* vc4 = kc4 + kChunkKeys / 4;
-      const bool part = !chunk_all_seen(p, t, key0);
       if constexpr (!C::K16) {
 #pragma unroll
         for (int q4 = 0; q4 < 16; ++q4) {
@@ -491,22 +480,23 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
           sv[2 * q4 + 1] = __fmul2_rn(sv[2 * q4 + 1], make_float2(kc.z, kc.w));
         }
       }
-      float vmt = C::V16 ? 0.f : cols[cb * C::CST + 2 * kChunkKeys];
-      unsigned long long hide = 0;                // keys this row does not see
-      if (part) {
-        float vm = 0.f;
+      float vmt = C::V16 ? 0.f : cc[2 * kChunkKeys];
+      if (!chunk_all_seen(p, t, key0)) {          // some query of the tile does not see all of its keys
+        vmt = 0.f;
 #pragma unroll
-        for (int k = 0; k < 64; ++k) {
-          const bool see = chunk_sees(p, qpos, key0 + k);
-          float& x = k & 1 ? sv[k >> 1].y : sv[k >> 1].x;
-          x = see ? x : -INFINITY;
-          if (!see) hide |= 1ull << k;
-          if constexpr (!C::V16) {
-            const float v = reinterpret_cast<const float*>(vc4)[k];
-            vm = fmaxf(vm, see && v < INFINITY ? v : 0.f);
+        for (int q4 = 0; q4 < 16; ++q4) {
+          const float4 kc = C::K16 ? kc4[q4] : make_float4(1.f, 1.f, 1.f, 1.f);
+          const float4 vc = C::V16 ? make_float4(0.f, 0.f, 0.f, 0.f) : vc4[q4];
+          const float kk[4] = {kc.x, kc.y, kc.z, kc.w}, vv[4] = {vc.x, vc.y, vc.z, vc.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const bool see = chunk_sees(p, qpos, key0 + 4 * q4 + u);
+            float& x = u & 1 ? sv[2 * q4 + (u >> 1)].y : sv[2 * q4 + (u >> 1)].x;
+            x = see ? x * kk[u] : -INFINITY;
+            vmt = fmaxf(vmt, see ? vv[u] : 0.f);
           }
+          asm volatile("" ::: "memory");          // (the scales are read again below: nothing to keep)
         }
-        vmt = vm;
       }
       // the row's maximum by three-input max
       float m8[8];
@@ -542,17 +532,10 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
         float2 p23 = make_float2(ex2_ftz(a23.x), ex2_ftz(a23.y));
         la = __fadd2_rn(la, p01);
         lb = __fadd2_rn(lb, p23);
-        if (!C::V16 || part) {
+        if constexpr (!C::V16) {
           const float4 vc = vc4[q4];
           p01 = __fmul2_rn(p01, make_float2(vc.x, vc.y));
           p23 = __fmul2_rn(p23, make_float2(vc.z, vc.w));
-        }
-        if (part) {                               // an unseen key's scale may be anything
-          const uint32_t h = (uint32_t)(hide >> (4 * q4)) & 15u;
-          p01.x = h & 1u ? 0.f : p01.x;
-          p01.y = h & 2u ? 0.f : p01.y;
-          p23.x = h & 4u ? 0.f : p23.x;
-          p23.y = h & 8u ? 0.f : p23.y;
         }
         if constexpr (C::V16) {
           const __nv_bfloat162 x = __floats2bfloat162_rn(p01.x, p01.y), y = __floats2bfloat162_rn(p23.x, p23.y);
@@ -638,7 +621,7 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  if (warp == 9) umma::tmem_dealloc(tmem, 256);
+  if (warp == 7) umma::tmem_dealloc(tmem, 256);
 }
 
 template <int KE, int VE>
