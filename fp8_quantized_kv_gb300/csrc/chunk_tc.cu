@@ -10,8 +10,9 @@
 //                                  (hi, and what hi leaves over) after a
 //                                  power-of-two scaling of the row; bf16 keys:
 //                                  kind::f16 in bf16
-//   p = 2^(s - m), l += p          one thread per row, running maximum m moved
-//                                  only when it grows by more than 2^8
+//   p = 2^(s - m), l += p          a quad of threads per two rows, running
+//                                  maximum m moved only when it grows by
+//                                  more than 2^8
 //   O[128 x 128] += P . V          kind::f16; P is the A operand and stays in
 //                                  TMEM, written over the scores it came from;
 //                                  e4m3 values converted to f16 (exact), bf16
@@ -23,22 +24,24 @@
 // KB of shared memory, so two CTAs share an SM: one's softmax runs while the
 // other's products, prologue or epilogue do.
 //
-// Warp roles (256 threads, so that a thread has 128 registers at two CTAs):
-//   warps 0-3   softmax, one query row (TMEM lane) per thread; epilogue
-//   warps 4-5   preparation, one key per thread: per-key scales; e4m3 V codes
+// Warp roles (384 threads, 80 registers each at two CTAs):
+//   warps 0-7   softmax of 16 query rows (TMEM lanes) each; epilogue
+//   warps 8-9   preparation, one key per thread: per-key scales; e4m3 V codes
 //               -> f16 operand; in a tile that not every query sees whole,
 //               rows nobody sees are zeroed, and a row with non-finite values
 //               is cleared of them and its key scale set to NaN: queries that
 //               see it get NaN, the others nothing
-//   warp 6      TMA producer: K ring, and V ring with the scale rows
-//   warp 7      TMEM owner and MMA issuer
+//   warp 10     TMA producer: K ring, and V ring with the scale rows
+//   warp 11     TMEM owner and MMA issuer
 // Every wait is bounded; one that runs out raises FP8KV_DEVERR_TIMEOUT.
+#include <cfloat>
+
 #include "chunk_common.cuh"
 #include "tc_common.cuh"
 
 namespace fp8kv {
 
-constexpr int kCtRows = 128, kCtThreads = 256;
+constexpr int kCtRows = 128, kCtThreads = 384;
 
 template <int KE, int VE>
 struct CtCfg {
@@ -72,15 +75,50 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b), "r"(id), "r"(accumulate));
 }
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+// TMEM access of 16 lanes (rows) in the fragment shape of a matrix product:
+// thread 4 g + c of the warp holds rows g and g + 8.  256-bit columns (8 fp32):
+// registers 4 n .. 4 n + 3 are columns 8 n + 2 c, + 1 of row g, then of row
+// g + 8; 128-bit columns (4 words): registers 2 n, 2 n + 1 are word 4 n + c of
+// row g and of row g + 8.  A thread then meets only a quarter of the keys, and
+// loads a quarter of their scales: with a whole row per thread, bringing 64 key
+// and 64 value scales to every thread took half of the shared-memory bandwidth.
+__device__ __forceinline__ void tmem_ld_256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_256b_x2(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+// OR of `pred` over the 256 softmax threads (named barrier 1).
+__device__ __forceinline__ bool softmax_any(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)pred)
+      : "memory");
+  return r != 0;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -114,7 +152,8 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   uint64_t* drained = pv_done + 1;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-  static_assert(8 * (2 * C::KN + 2 * C::VN + 2 * OPN + C::NCOL + 5) + 8 <= C::MISC, "barriers fit");
+  int8_t* kq_sh = reinterpret_cast<int8_t*>(bars) + 256;      // [128] exponent of each row's query operand
+  static_assert(8 * (2 * C::KN + 2 * C::VN + 2 * OPN + C::NCOL + 5) + 8 <= 256 && 256 + kCtRows <= C::MISC, "they fit");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hk = blockIdx.y, split = blockIdx.z;
@@ -185,11 +224,11 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
 
   // ---------------------------------------------------------------- setup
   int ids = 0, next_ids = 0;                      // page ids of this group of eight tiles and of the next
-  if (warp == 6) {
+  if (warp == 10) {
     ids = fetch_ids(0);
     next_ids = fetch_ids(1);
   }
-  if (warp == 6 && lane == 0) {
+  if (warp == 10 && lane == 0) {
     tma::prefetch_map(&tp.tmk);
     tma::prefetch_map(&tp.tmv);
     for (int i = 0; i < C::KN; ++i) { umma::mbar_init(&kfull[i], 1); umma::mbar_init(&kfree[i], 1); }
@@ -198,28 +237,27 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     for (int i = 0; i < C::NCOL; ++i) umma::mbar_init(&col_full[i], 2);
     umma::mbar_init(&s_full[0], 1);
     umma::mbar_init(&s_full[1], 1);
-    umma::mbar_init(p_full, 4);
+    umma::mbar_init(p_full, 8);
     umma::mbar_init(pv_done, 1);
     umma::mbar_init(drained, 1);
     *abort_flag = 0;
     umma::mbar_fence_init();
   }
-  if (warp == 7) {
+  if (warp == 11) {
     umma::tmem_alloc(tslot, 256);
     umma::tmem_relinquish();
   }
-  // softmax warps: this thread's query row -> QK operand
+  // softmax warps: half of this thread's query row -> QK operand
   const int r = tid & 127;                        // row of the tile, TMEM lane
   const int tok = r / G;
-  const bool live = warp < 4 && tok < t.ntok && r < p.tile_tokens * G;
+  const bool live = warp < 8 && tok < t.ntok && r < p.tile_tokens * G;
   const int64_t qrow = live ? (int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G) : -1;
-  const int qpos = live ? t.pos0 + tok : -1;
-  int kq = 0;
-  if (warp < 4) {
+  const int hf = (tid >> 7) & 1;                  // softmax warps: dims 64 hf .. of the query, of O
+  if (warp < 8) {
     const uint4* src = reinterpret_cast<const uint4*>(p.q + (live ? qrow : 0) * D);
     if constexpr (C::K16) {
 #pragma unroll
-      for (int ch = 0; ch < 16; ++ch) {
+      for (int ch = 8 * hf; ch < 8 * hf + 8; ++ch) {
         uint4 w = live && p.scale_log2 != 0.f ? src[ch] : make_uint4(0, 0, 0, 0);
         if (p.scale_log2 < 0.f) w = make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
         *reinterpret_cast<uint4*>(qop + (ch >> 3) * (kCtRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w;
@@ -237,10 +275,11 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
           amax = fmaxf(amax, fmaxf(fabsf(f[0]), fabsf(f[1])));
         }
       }
-      kq = amax < INFINITY ? max(-100, min(120, e4m3_row_exp(amax))) : 0;
+      const int kq = amax < INFINITY ? max(-100, min(120, e4m3_row_exp(amax))) : 0;
+      kq_sh[r] = (int8_t)kq;
       const float qsc = pow2i(-kq);
 #pragma unroll 2
-      for (int ch = 0; ch < 8; ++ch) {             // 16 dims (one 16-byte e4m3 chunk) each
+      for (int ch = 4 * hf; ch < 4 * hf + 4; ++ch) {   // 16 dims (one 16-byte e4m3 chunk) each
         const uint4 a = live ? src[2 * ch] : make_uint4(0, 0, 0, 0), b = live ? src[2 * ch + 1] : make_uint4(0, 0, 0, 0);
         const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         uint32_t hi[4], lo[4];
@@ -268,8 +307,8 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   const uint32_t tmem = *tslot;
   const uint32_t o_col = tmem + 128;              // S and P: columns 0-63 and 64-127; O: 128-255
 
-  if (warp >= 6) {
-    if (warp == 6) {
+  if (warp >= 10) {
+    if (warp == 10) {
       // ---------------------------------------------------------- producer
       // V tile j goes out behind K tile j + KN - VN (the K ring is the deeper
       // one); a V tile's page ids may be those of the group before
@@ -358,9 +397,9 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
         (void)umma::mbar_wait(drained, 0, 100000000ull);
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     // ------------------------------------------------------------ preparation
-    const int kr = tid - 128;                     // this thread's key of the tile
+    const int kr = tid - 256;                     // this thread's key of the tile
     for (int j = 0; j < n; ++j) {
       const int vs = j % C::VN, cb = j % C::NCOL, key0 = chunk_key0(t, j0 + j);
       bool ok = wait_fast(&vfull[vs], (j / C::VN) & 1, abort_flag);
@@ -413,7 +452,7 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       aside = (aside || !(fabsf(vv) < INFINITY)) && part && vis;
       cc[kr] = aside ? NAN : C::K16 ? 1.f : vis ? ksc[kr] * p.scale_log2 : 0.f;
       if constexpr (!C::V16) cc[kChunkKeys + kr] = aside ? 0.f : vv;
-      if (!C::V16 && warp == 4) {                  // the tile's largest finite value scale
+      if (!C::V16 && warp == 8) {                  // the tile's largest finite value scale
         const float a = vsc[lane], b = vsc[lane + 32];
         const float vm = warp_max_f32(fmaxf(seen(lane) && a < INFINITY ? a : 0.f, seen(lane + 32) && b < INFINITY ? b : 0.f));
         if (lane == 0) cc[2 * kChunkKeys] = vm;
@@ -443,12 +482,27 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
-    // what is left of the score's scale, positive (bf16 keys: the query operand
-    // carries the sign, and is zero for a scale of zero)
-    const float s2 = !C::K16 ? pow2i(kq) : p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1.f;
-    float m_used = -INFINITY, l = 0.f;
-    int kp = -1000;                               // this row's P exponent (none yet)
+    // a warp reaches the 32 TMEM lanes of its quarter: warps w and w + 4 share
+    // them, 16 rows each; this thread's rows are row0 + g + 8 i, with its quad
+    const int row0 = 32 * (warp & 3) + 16 * hf;
+    const uint32_t lane_off = (uint32_t)row0 << 16;
+    const int g = lane >> 2, c2 = 2 * (lane & 3);
+    int qpos[2];                                  // position (-1: no query)
+    float s2[2], m_used[2], l[2], neg_m[2];
+    float up[2];                                  // 2^kp
+    float vm_top[2];                              // value scales below it need no larger kp
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int row = row0 + g + 8 * i, tk = row / G;
+      qpos[i] = tk < t.ntok && row < p.tile_tokens * G ? t.pos0 + tk : -1;
+      // what is left of the score's scale, positive (bf16 keys: the query
+      // operand carries the sign, and is zero for a scale of zero)
+      s2[i] = !C::K16 ? pow2i(kq_sh[row]) : p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1.f;
+      up[i] = 1.f;
+      m_used[i] = -INFINITY;
+      l[i] = neg_m[i] = 0.f;
+      vm_top[i] = FLT_MIN;
+    }
     bool failed = false;
     for (int j = 0; j < n; ++j) {
       const int cb = j % C::NCOL, key0 = chunk_key0(t, j0 + j);
@@ -458,113 +512,128 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       ok = ok && !*abort_flag;
       if (!__all_sync(0xffffffffu, ok)) { failed = true; break; }
       umma::fence_after_sync();
-      float2 sv[32];
+      float2 sv[2][8];                            // row i, keys 8 k + c2, + 1
       {
-        uint32_t rr[4][16];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) umma::tmem_ld16_nowait(s_col + 16 * k, rr[k]);
+        uint32_t rr[32];
+        tmem_ld_256b_x8(s_col, rr);
         umma::tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int u = 0; u < 8; ++u) sv[8 * k + u] = make_float2(__uint_as_float(rr[k][2 * u]), __uint_as_float(rr[k][2 * u + 1]));
+          for (int k = 0; k < 8; ++k)
+            sv[i][k] = make_float2(__uint_as_float(rr[4 * k + 2 * i]), __uint_as_float(rr[4 * k + 2 * i + 1]));
       }
-      const float* cc = cols + cb * C::CST;
-      const float4* kc4 = reinterpret_cast<const float4*>(cc);
-      const float4* vc4 = kc4 + kChunkKeys / 4;
+      const float* kc = cols + cb * C::CST + c2;
+      const float* vc = kc + kChunkKeys;
       if constexpr (!C::K16) {
 #pragma unroll
-        for (int q4 = 0; q4 < 16; ++q4) {
-          const float4 kc = kc4[q4];
-          sv[2 * q4] = __fmul2_rn(sv[2 * q4], make_float2(kc.x, kc.y));
-          sv[2 * q4 + 1] = __fmul2_rn(sv[2 * q4 + 1], make_float2(kc.z, kc.w));
+        for (int k = 0; k < 8; ++k) {
+          const float2 x = *reinterpret_cast<const float2*>(kc + 8 * k);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) sv[i][k] = __fmul2_rn(sv[i][k], x);
         }
       }
-      float vmt = C::V16 ? 0.f : cc[2 * kChunkKeys];
+      const float vmt = C::V16 ? 0.f : cols[cb * C::CST + 2 * kChunkKeys];
+      float vm[2] = {vmt, vmt};                   // largest value scale that the row sees
       if (!chunk_all_seen(p, t, key0)) {          // some query of the tile does not see all of its keys
-        vmt = 0.f;
 #pragma unroll
-        for (int q4 = 0; q4 < 16; ++q4) {
-          const float4 kc = C::K16 ? kc4[q4] : make_float4(1.f, 1.f, 1.f, 1.f);
-          const float4 vc = C::V16 ? make_float4(0.f, 0.f, 0.f, 0.f) : vc4[q4];
-          const float kk[4] = {kc.x, kc.y, kc.z, kc.w}, vv[4] = {vc.x, vc.y, vc.z, vc.w};
+        for (int i = 0; i < 2; ++i) vm[i] = 0.f;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const bool see = chunk_sees(p, qpos, key0 + 4 * q4 + u);
-            float& x = u & 1 ? sv[2 * q4 + (u >> 1)].y : sv[2 * q4 + (u >> 1)].x;
-            x = see ? x * kk[u] : -INFINITY;
-            vmt = fmaxf(vmt, see ? vv[u] : 0.f);
-          }
-          asm volatile("" ::: "memory");          // (the scales are read again below: nothing to keep)
-        }
-      }
-      // the row's maximum by three-input max
-      float m8[8];
+        for (int k = 0; k < 8; ++k) {
+          const float2 x = C::K16 ? *reinterpret_cast<const float2*>(kc + 8 * k) : make_float2(1.f, 1.f);
+          const float2 v = C::V16 ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(vc + 8 * k);
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        m8[k] = max3(max3(sv[k].x, sv[k].y, sv[k + 8].x), max3(sv[k + 8].y, sv[k + 16].x, sv[k + 16].y),
-                     fmaxf(sv[k + 24].x, sv[k + 24].y));
-      const float mt = max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * s2;
-      float alpha = 1.f;
-      if (mt != -INFINITY && (m_used == -INFINITY || mt > m_used + 8.f)) {
-        alpha = m_used == -INFINITY ? 0.f : ex2(m_used - mt);
-        m_used = mt;
-      }
-      float alpha_o = alpha;
-      if constexpr (!C::V16) {
-        if (vmt > 0.f) {
-          const int need = max(-100, min(100, ((__float_as_int(vmt) >> 23) & 0xFF) - 127 - 6));   // vmt 2^-need < 128
-          if (need > kp) {
-            if (kp > -1000) alpha_o *= pow2_diff((float)(kp - need), 0);
-            kp = need;
+          for (int i = 0; i < 2; ++i) {
+            const bool a = chunk_sees(p, qpos[i], key0 + 8 * k + c2), b = chunk_sees(p, qpos[i], key0 + 8 * k + c2 + 1);
+            sv[i][k].x = a ? sv[i][k].x * x.x : -INFINITY;
+            sv[i][k].y = b ? sv[i][k].y * x.y : -INFINITY;
+            vm[i] = fmaxf(vm[i], fmaxf(a ? v.x : 0.f, b ? v.y : 0.f));
           }
         }
-      }
-      const int kpr = kp > -1000 ? kp : 0;
-      const float neg_m = (m_used == -INFINITY ? 0.f : -m_used) - (float)kpr;
-      const float2 s22 = make_float2(s2, s2), nm2 = make_float2(neg_m, neg_m);
-      float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
-      uint32_t ph[32];
-#pragma unroll
-      for (int q4 = 0; q4 < 16; ++q4) {
-        const float2 a01 = __ffma2_rn(sv[2 * q4], s22, nm2), a23 = __ffma2_rn(sv[2 * q4 + 1], s22, nm2);
-        float2 p01 = make_float2(ex2_ftz(a01.x), ex2_ftz(a01.y));
-        float2 p23 = make_float2(ex2_ftz(a23.x), ex2_ftz(a23.y));
-        la = __fadd2_rn(la, p01);
-        lb = __fadd2_rn(lb, p23);
         if constexpr (!C::V16) {
-          const float4 vc = vc4[q4];
-          p01 = __fmul2_rn(p01, make_float2(vc.x, vc.y));
-          p23 = __fmul2_rn(p23, make_float2(vc.z, vc.w));
-        }
-        if constexpr (C::V16) {
-          const __nv_bfloat162 x = __floats2bfloat162_rn(p01.x, p01.y), y = __floats2bfloat162_rn(p23.x, p23.y);
-          ph[2 * q4] = *reinterpret_cast<const uint32_t*>(&x);
-          ph[2 * q4 + 1] = *reinterpret_cast<const uint32_t*>(&y);
-        } else {
-          const __half2 x = __floats2half2_rn(p01.x, p01.y), y = __floats2half2_rn(p23.x, p23.y);
-          ph[2 * q4] = *reinterpret_cast<const uint32_t*>(&x);
-          ph[2 * q4 + 1] = *reinterpret_cast<const uint32_t*>(&y);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            vm[i] = fmaxf(vm[i], __shfl_xor_sync(0xffffffffu, vm[i], 1));
+            vm[i] = fmaxf(vm[i], __shfl_xor_sync(0xffffffffu, vm[i], 2));
+          }
         }
       }
-      l = l * alpha + ((la.x + la.y) + (lb.x + lb.y)) * pow2i(kpr);
-      tmem_st16(s_col, ph);
-      tmem_st16(s_col + 16, ph + 16);
+      // each row's maximum by three-input max, joined over the quad
+      float mt[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        mt[i] = max3(max3(max3(sv[i][0].x, sv[i][0].y, sv[i][1].x), max3(sv[i][1].y, sv[i][2].x, sv[i][2].y),
+                          max3(sv[i][3].x, sv[i][3].y, sv[i][4].x)),
+                     max3(sv[i][4].y, sv[i][5].x, sv[i][5].y), max3(max3(sv[i][6].x, sv[i][6].y, sv[i][7].x), sv[i][7].y, -INFINITY));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 1));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 2)) * s2[i];
+      // The reference maximum moves only when it grows by more than 2^8 (P stays
+      // within 2^8 of it), kp only up; l (in units of 2^m) and O (2^(m + kp))
+      // move with them.  Rare behind the first tile: one vote skips it.
+      bool moved = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) moved = moved || mt[i] > m_used[i] + 8.f || (!C::V16 && vm[i] >= vm_top[i]);
+      moved = __any_sync(0xffffffffu, moved);
+      float alpha[2] = {1.f, 1.f};
+      if (moved) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (mt[i] > m_used[i] + 8.f) {
+            alpha[i] = ex2(m_used[i] - mt[i]);    // (0 for the first)
+            m_used[i] = mt[i];
+            l[i] *= alpha[i];
+          }
+          if (!C::V16 && vm[i] >= vm_top[i]) {
+            const int need = max(-100, min(100, ((__float_as_int(vm[i]) >> 23) & 0xFF) - 127 - 6));   // vm 2^-need < 2^7
+            alpha[i] *= pow2i(max(-126, (__float_as_int(up[i]) >> 23) - 127 - need));
+            up[i] = pow2i(need);
+            vm_top[i] = pow2i(need + 7);
+          }
+          neg_m[i] = (m_used[i] == -INFINITY ? 0.f : -m_used[i]) - (float)((__float_as_int(up[i]) >> 23) - 127);
+        }
+      }
+      float2 la[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      uint32_t ph[16];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 v = C::V16 ? make_float2(1.f, 1.f) : *reinterpret_cast<const float2*>(vc + 8 * k);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 a = __ffma2_rn(sv[i][k], make_float2(s2[i], s2[i]), make_float2(neg_m[i], neg_m[i]));
+          float2 x = make_float2(ex2_ftz(a.x), ex2_ftz(a.y));
+          la[i] = __fadd2_rn(la[i], x);
+          uint32_t& w = ph[2 * k + i];
+          if constexpr (C::V16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+            w = *reinterpret_cast<const uint32_t*>(&h);
+          } else {
+            x = __fmul2_rn(x, v);
+            const __half2 h = __floats2half2_rn(x.x, x.y);
+            w = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) l[i] = fmaf(la[i].x + la[i].y, up[i], l[i]);
+      tmem_st_128b_x8(s_col, ph);
       // O may be rescaled only when the previous P.V is done
       if (j > 0) {
         const bool done = wait_fast(pv_done, (j - 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, done)) { failed = true; break; }
       }
-      if (__any_sync(0xffffffffu, alpha_o != 1.f && j > 0)) {
+      if (moved && j > 0) {
         umma::fence_after_sync();
 #pragma unroll 1
-        for (int k = 0; k < 8; ++k) {
-          uint32_t rr[16];
-          umma::tmem_ld16_nowait(o_col + lane_off + 16 * k, rr);
+        for (int k = 0; k < 8; ++k) {             // 16 columns (head dims)
+          const uint32_t at = o_col + lane_off + 16 * k;
+          uint32_t rr[8];
+          tmem_ld_256b_x2(at, rr);
           umma::tmem_wait_ld();
 #pragma unroll
-          for (int u = 0; u < 16; ++u) rr[u] = __float_as_uint(__uint_as_float(rr[u]) * alpha_o);
-          tmem_st16(o_col + lane_off + 16 * k, rr);
+          for (int u = 0; u < 8; ++u) rr[u] = __float_as_uint(__uint_as_float(rr[u]) * (u & 2 ? alpha[1] : alpha[0]));
+          tmem_st_256b_x2(at, rr);
         }
       }
       tmem_wait_st();
@@ -577,20 +646,36 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       const bool done = wait_or_abort(pv_done, (n - 1) & 1, abort_flag);
       failed = !__all_sync(0xffffffffu, done);
     }
+    // one row and half of its dims per thread: the quads leave their rows'
+    // (m, l, 2^kp) in the query operand's place, which no product reads any more
+    float* st = reinterpret_cast<float*>(qop);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      const int row = row0 + g + 8 * i;
+      if (c2 == 0 && !failed) {
+        st[row] = m_used[i];
+        st[kCtRows + row] = l[i];
+        st[2 * kCtRows + row] = up[i];
+      }
+    }
+    failed = softmax_any(failed);                 // (a barrier of the eight warps)
     if (failed) {
-      if (lane == 0) raise_error(p.err, FP8KV_DEVERR_TIMEOUT);
+      if (tid == 0) raise_error(p.err, FP8KV_DEVERR_TIMEOUT);
     } else {
       umma::fence_after_sync();
-      const float of = C::V16 || kp <= -1000 ? 1.f : pow2i(kp);
+      const uint32_t lane_q = (uint32_t)(32 * (warp & 3)) << 16;
+      const float mr = st[r], lr = st[kCtRows + r], of = st[2 * kCtRows + r];
       const bool whole = p.num_splits == 1;
-      const float f = whole ? (l > 0.f ? of / l : l == l ? 0.f : l) : of;
+      const float f = !whole ? of : lr > 0.f ? of / lr : lr == lr ? 0.f : lr;
       const int64_t at = whole ? qrow : qrow * p.num_splits + split;
-      if (!whole && live) { p.part_m[at] = m_used; p.part_l[at] = l; }
+      if (!whole && live && hf == 0) { p.part_m[at] = mr; p.part_l[at] = lr; }
 #pragma unroll 1
-      for (int k = 0; k < 8; ++k) {
+      for (int k = 4 * hf; k < 4 * hf + 4; ++k) {
         uint32_t rr[16];
         if (n > 0) {
-          umma::tmem_ld16_nowait(o_col + lane_off + 16 * k, rr);
+          umma::tmem_ld16_nowait(o_col + lane_q + 16 * k, rr);
           umma::tmem_wait_ld();
         } else {
 #pragma unroll
@@ -621,7 +706,7 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  if (warp == 7) umma::tmem_dealloc(tmem, 256);
+  if (warp == 11) umma::tmem_dealloc(tmem, 256);
 }
 
 template <int KE, int VE>
