@@ -147,13 +147,15 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   uint64_t* op_free = op_full + OPN;                          // [OPN] P.V has read it
   uint64_t* col_full = op_free + OPN;                         // [NCOL] column scales written
   uint64_t* s_full = col_full + C::NCOL;                      // [2] scores ready
-  uint64_t* p_full = s_full + 2;                              // P written
-  uint64_t* pv_done = p_full + 1;                             // P.V finished
-  uint64_t* drained = pv_done + 1;
+  // P written, one barrier a buffer: a warp may be done with tile j + 1 before
+  // another is with tile j
+  uint64_t* p_full = s_full + 2;                              // [2]
+  uint64_t* pv_done = p_full + 2;                             // P.V finished
+  uint64_t* drained = pv_done + 1;                            // every product finished
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int8_t* kq_sh = reinterpret_cast<int8_t*>(bars) + 256;      // [128] exponent of each row's query operand
-  static_assert(8 * (2 * C::KN + 2 * C::VN + 2 * OPN + C::NCOL + 5) + 8 <= 256 && 256 + kCtRows <= C::MISC, "they fit");
+  static_assert(8 * (2 * C::KN + 2 * C::VN + 2 * OPN + C::NCOL + 6) + 8 <= 256 && 256 + kCtRows <= C::MISC, "they fit");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hk = blockIdx.y, split = blockIdx.z;
@@ -237,7 +239,8 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     for (int i = 0; i < C::NCOL; ++i) umma::mbar_init(&col_full[i], 2);
     umma::mbar_init(&s_full[0], 1);
     umma::mbar_init(&s_full[1], 1);
-    umma::mbar_init(p_full, 8);
+    umma::mbar_init(&p_full[0], 8);
+    umma::mbar_init(&p_full[1], 8);
     umma::mbar_init(pv_done, 1);
     umma::mbar_init(drained, 1);
     *abort_flag = 0;
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
         for (int j = 0; ok && j < n; ++j) {
           const int ob = j % OPN;
           if (!wait_fast(&op_full[ob], (j / OPN) & 1, abort_flag)) break;
-          if (!wait_fast(p_full, j & 1, abort_flag)) break;
+          if (!wait_fast(&p_full[j & 1], (j >> 1) & 1, abort_flag)) break;
           umma::fence_after_sync();
           const uint32_t va = umma::smem_u32(vop + ob * (C::V16 ? C::VST : C::OPT)), pa = tmem + 64 * (j & 1);
 #pragma unroll
@@ -411,9 +414,25 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       float* cc = cols + cb * C::CST;
       auto seen = [&](int k) { return !part || (key0 + k < t.kv_end && (key0 + k >= t.lo || key0 + k < p.sinks)); };
       const bool vis = seen(kr);
-      bool aside = false;                          // this key's V row holds something not finite
+      // per-key scales; in a tile that not every query sees whole they wait
+      // for the values: a row with one that is not finite marks its key's score
+      auto publish = [&](bool aside) {
+        const float vv = C::V16 || !vis ? 0.f : vsc[kr];
+        aside = (aside || !(fabsf(vv) < INFINITY)) && part && vis;
+        cc[kr] = aside ? NAN : C::K16 ? 1.f : vis ? ksc[kr] * p.scale_log2 : 0.f;
+        if constexpr (!C::V16) cc[kChunkKeys + kr] = aside ? 0.f : vv;
+        if (!C::V16 && warp == 8) {                // the tile's largest finite value scale
+          const float a = vsc[lane], b = vsc[lane + 32];
+          const float vm = warp_max_f32(fmaxf(seen(lane) && a < INFINITY ? a : 0.f, seen(lane + 32) && b < INFINITY ? b : 0.f));
+          if (lane == 0) cc[2 * kChunkKeys] = vm;
+        }
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&col_full[cb]);
+      };
+      if (!part) publish(false);
       if constexpr (C::V16) {
         if (part) {
+          bool aside = false;
           for (int ch = 0; ch < 16; ++ch) {
             uint4* at = reinterpret_cast<uint4*>(st + (ch >> 3) * (kChunkKeys * 128) + kr * 128 + (((ch & 7) ^ (kr & 7)) << 4));
             const uint4 w = *at;
@@ -430,41 +449,30 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
             if (bad || !vis) *at = make_uint4(ww[0], ww[1], ww[2], ww[3]);
           }
           umma::fence_proxy_async_smem();
+          publish(aside);
         }
+        if (lane == 0) umma::mbar_arrive(&op_full[vs]);
       }
-      uint32_t w[C::V16 ? 1 : 32];                 // e4m3: the key's 128 codes
       if constexpr (!C::V16) {
+        const int ob = j % C::NOP, ou = j / C::NOP;
+        uint32_t w[32];                            // the key's 128 codes
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch) {
           const uint4 x = *reinterpret_cast<const uint4*>(st + kr * 128 + ((ch ^ (kr & 7)) << 4));
           w[4 * ch] = x.x; w[4 * ch + 1] = x.y; w[4 * ch + 2] = x.z; w[4 * ch + 3] = x.w;
         }
         if (part) {
+          bool aside = false;
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
             const uint32_t nan = (((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 per NaN code
             aside = aside || nan != 0;
             w[k] = vis ? w[k] & ~(nan * 0xFFu) : 0u;
           }
+          publish(aside);
         }
-      }
-      const float vv = C::V16 || !vis ? 0.f : vsc[kr];
-      aside = (aside || !(fabsf(vv) < INFINITY)) && part && vis;
-      cc[kr] = aside ? NAN : C::K16 ? 1.f : vis ? ksc[kr] * p.scale_log2 : 0.f;
-      if constexpr (!C::V16) cc[kChunkKeys + kr] = aside ? 0.f : vv;
-      if (!C::V16 && warp == 8) {                  // the tile's largest finite value scale
-        const float a = vsc[lane], b = vsc[lane + 32];
-        const float vm = warp_max_f32(fmaxf(seen(lane) && a < INFINITY ? a : 0.f, seen(lane + 32) && b < INFINITY ? b : 0.f));
-        if (lane == 0) cc[2 * kChunkKeys] = vm;
-      }
-      __syncwarp();
-      if (lane == 0) {
-        umma::mbar_arrive(&col_full[cb]);
-        if constexpr (C::V16) umma::mbar_arrive(&op_full[vs]);
-        else umma::mbar_arrive(&vfree[vs]);
-      }
-      if constexpr (!C::V16) {
-        const int ob = j % C::NOP, ou = j / C::NOP;
+        __syncwarp();
+        if (lane == 0) umma::mbar_arrive(&vfree[vs]);
         if (ou > 0) {
           ok = wait_fast(&op_free[ob], (ou - 1) & 1, abort_flag);
           if (!__all_sync(0xffffffffu, ok)) break;
@@ -618,12 +626,12 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
 #pragma unroll
       for (int i = 0; i < 2; ++i) l[i] = fmaf(la[i].x + la[i].y, up[i], l[i]);
       tmem_st_128b_x8(s_col, ph);
-      // O may be rescaled only when the previous P.V is done
-      if (j > 0) {
+      if (moved && j > 0) {
+        // O may be rescaled only when the previous P.V is done.  (The parity is
+        // unambiguous: the scores of this tile were issued behind the P.V before
+        // that one, and the next P.V waits for this warp.)
         const bool done = wait_fast(pv_done, (j - 1) & 1, abort_flag);
         if (!__all_sync(0xffffffffu, done)) { failed = true; break; }
-      }
-      if (moved && j > 0) {
         umma::fence_after_sync();
 #pragma unroll 1
         for (int k = 0; k < 8; ++k) {             // 16 columns (head dims)
@@ -639,11 +647,13 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       tmem_wait_st();
       umma::fence_before_sync();
       __syncwarp();
-      if (lane == 0) umma::mbar_arrive(p_full);
+      if (lane == 0) umma::mbar_arrive(&p_full[j & 1]);
     }
     // ---------------------------------------------------------------- epilogue
     if (!failed && n > 0) {
-      const bool done = wait_or_abort(pv_done, (n - 1) & 1, abort_flag);
+      // (a barrier of its own: a late warp cannot tell by pv_done's parity
+      // whether the last phase or the one before it is over)
+      const bool done = wait_fast(drained, 0, abort_flag) && !*abort_flag;
       failed = !__all_sync(0xffffffffu, done);
     }
     // one row and half of its dims per thread: the quads leave their rows'
