@@ -31,7 +31,7 @@
 //               rows nobody sees are zeroed, and a row with non-finite values
 //               is cleared of them and its key scale set to NaN: queries that
 //               see it get NaN, the others nothing
-//   warp 10     TMA producer: K ring, and V ring with the scale rows
+//   warp 10     TMA producer: K ring and V ring
 //   warp 11     TMEM owner and MMA issuer
 // Every wait is bounded; one that runs out raises FP8KV_DEVERR_TIMEOUT.
 #include <cfloat>
@@ -50,15 +50,13 @@ struct CtCfg {
   static constexpr int QOP = kCtRows * 2 * D;                       // [hi, lo][128][128 B], or [2 halves of D][128][128 B]
   static constexpr int KT = kChunkKeys * D * (K16 ? 2 : 1);         // K tile
   static constexpr int VT = kChunkKeys * D * (V16 ? 2 : 1);         // V tile as stored
-  static constexpr int SCALES = K16 && V16 ? 0 : 2 * kChunkKeys * 4;
   static constexpr int KN = K16 ? 2 : 3, VN = K16 && !V16 ? 1 : 2;  // ring depths
   static constexpr int NOP = V16 ? 0 : 2;                           // f16 V operand buffers
   static constexpr int OPT = kChunkKeys * D * 2;
-  static constexpr int VST = VT + 1024 * (SCALES > 0);              // V stage: tile, scales (1024-byte aligned)
-  static constexpr int CST = 2 * kChunkKeys + 4;                    // floats: k, v column scales, largest v scale
+  static constexpr int CST = 2 * kChunkKeys + 4;                    // floats: k, v column scales, largest v scale of each half
   static constexpr int NCOL = 4;
   static constexpr int MISC = 512;
-  static constexpr int BYTES = 1024 + QOP + KN * KT + VN * VST + NOP * OPT + NCOL * CST * 4 + MISC;
+  static constexpr int BYTES = 1024 + QOP + KN * KT + VN * VT + NOP * OPT + NCOL * CST * 4 + MISC;
   static_assert(2 * (BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
@@ -106,6 +104,18 @@ __device__ __forceinline__ void tmem_st_128b_x8(uint32_t taddr, const uint32_t (
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+// One lane of the (converged) warp, the same at every call.  The issuing warps
+// run their loops with all lanes, and only the instruction itself belongs to
+// the elected one: addresses and descriptors are then uniform for the compiler.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e));
+  return e != 0;
+}
 // OR of `pred` over the 256 softmax threads (named barrier 1).
 __device__ __forceinline__ bool softmax_any(bool pred) {
   uint32_t r;
@@ -135,13 +145,13 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   uint8_t* qop = smem;
   uint8_t* kring = qop + C::QOP;
   uint8_t* vring = kring + C::KN * C::KT;
-  uint8_t* vop = C::V16 ? vring : vring + C::VN * C::VST;
-  float* cols = reinterpret_cast<float*>(vring + C::VN * C::VST + C::NOP * C::OPT);
+  uint8_t* vop = C::V16 ? vring : vring + C::VN * C::VT;
+  float* cols = reinterpret_cast<float*>(vring + C::VN * C::VT + C::NOP * C::OPT);
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(cols) + C::NCOL * C::CST * 4);
   constexpr int OPN = C::V16 ? C::VN : C::NOP;                // operand buffers of P.V
   uint64_t* kfull = bars;                                     // [KN] K tile landed
   uint64_t* kfree = kfull + C::KN;                            // [KN] QK has read it
-  uint64_t* vfull = kfree + C::KN;                            // [VN] V tile and scales landed
+  uint64_t* vfull = kfree + C::KN;                            // [VN] V tile landed
   uint64_t* vfree = vfull + C::VN;                            // [VN] converted (bf16: read by P.V)
   uint64_t* op_full = vfree + C::VN;                          // [OPN] operand of P.V ready
   uint64_t* op_free = op_full + OPN;                          // [OPN] P.V has read it
@@ -171,56 +181,61 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   auto page_needed = [&](int k0, int len) {                   // is any key of [k0, k0 + len) seen by a query?
     return k0 < t.kv_end && (k0 + len > t.lo || k0 < p.sinks);
   };
-  // The producer warp loads the K tiles and the V tiles with the scale rows.
-  // Paged: lane 4 i + k keeps the page id of page k of tile 8 q + i, fetched for eight
-  // tiles at once and one group ahead, so no copy waits for the page table.
+  // The producer warp loads the K tiles and the V tiles.  Paged: lane 4 i + k
+  // keeps the first cache row of page k of tile 8 q + i (-1: a page nobody
+  // sees, which may be gone), fetched for eight tiles at once and one group
+  // ahead, so no copy waits for the page table.
   const int pages = c.paged ? kChunkKeys / c.page_size : 0;
   auto fetch_ids = [&](int group) {
     const int j = 8 * group + (lane >> 2), k = lane & 3;
-    int page = 0;
+    int row = -1;
     if (k < pages && j < n) {
       const int key = chunk_key0(t, j0 + j) + k * c.page_size;
-      if (page_needed(key, c.page_size)) page = c.page_table[(int64_t)t.b * c.max_pages_per_seq + (key >> c.page_shift)];
-    }
-    return page;
-  };
-  auto load_tile = [&](int j, bool is_v, int ids) {
-    const int key0 = chunk_key0(t, j0 + j);
-    uint8_t* st = is_v ? vring + (j % C::VN) * C::VST : kring + (j % C::KN) * C::KT;
-    uint64_t* bar = is_v ? &vfull[j % C::VN] : &kfull[j % C::KN];
-    const CUtensorMap* map = is_v ? &tp.tmv : &tp.tmk;
-    const bool wide = is_v ? C::V16 : C::K16;
-    const uint32_t half = kChunkKeys * 128;                   // bf16: dims 64..127 behind dims 0..63
-    float* ksc = reinterpret_cast<float*>(st + C::VT);
-    float* vsc = ksc + kChunkKeys;
-    const int sides = is_v ? (C::K16 ? 0 : 1) + (C::V16 ? 0 : 1) : 0;   // scale rows beside the tile
-    if (!c.paged) {
-      if (lane != 0) return;
-      const int row = (int)(cont0 + key0);
-      const int nsc = min(kChunkKeys, (t.kv_end - key0 + 15) & ~15);
-      tma::arrive_expect_tx(bar, half * (wide ? 2 : 1) + (uint32_t)nsc * 4 * sides);
-      tma::load_2d(st, map, 0, row, bar);
-      if (wide) tma::load_2d(st + half, map, 64, row, bar);
-      if (is_v && !C::K16) tma::load_1d(ksc, c.k_scale + cont0 + key0, nsc * 4, bar);
-      if (is_v && !C::V16) tma::load_1d(vsc, c.v_scale + cont0 + key0, nsc * 4, bar);
-    } else {
-      const int P = c.page_size;
-      int page = __shfl_sync(0xffffffffu, ids, (j & 7) * 4 + (lane & 3));
-      const bool mine = lane < pages && page_needed(key0 + lane * P, P);   // a page nobody sees may be gone
-      const int np = __popc(__ballot_sync(0xffffffffu, mine));
-      if (lane == 0) tma::arrive_expect_tx(bar, np * (uint32_t)P * (128 * (wide ? 2 : 1) + 4 * sides));
-      __syncwarp();
-      if (mine) {
+      if (page_needed(key, c.page_size)) {
+        int page = c.page_table[(int64_t)t.b * c.max_pages_per_seq + (key >> c.page_shift)];
         if (page < 0 || page >= c.num_pages) {
           raise_error(p.err, FP8KV_DEVERR_BAD_PAGE);
           page = 0;
         }
-        const int64_t row = ((int64_t)page * c.kv_heads + hk) * P;
-        tma::load_2d(st + lane * P * 128, map, 0, (int)row, bar);
-        if (wide) tma::load_2d(st + half + lane * P * 128, map, 64, (int)row, bar);
-        if (is_v && !C::K16) tma::load_1d(ksc + lane * P, c.k_scale + row, P * 4, bar);
-        if (is_v && !C::V16) tma::load_1d(vsc + lane * P, c.v_scale + row, P * 4, bar);
+        row = (page * c.kv_heads + hk) * c.page_size;          // (rows of a cache fit 31 bits)
       }
+    }
+    return row;
+  };
+  auto load_tile = [&](int j, bool is_v, int ids) {
+    const int key0 = chunk_key0(t, j0 + j);
+    uint8_t* st = is_v ? vring + (j % C::VN) * C::VT : kring + (j % C::KN) * C::KT;
+    uint64_t* bar = is_v ? &vfull[j % C::VN] : &kfull[j % C::KN];
+    const CUtensorMap* map = is_v ? &tp.tmv : &tp.tmk;
+    const bool wide = is_v ? C::V16 : C::K16;
+    const uint32_t half = kChunkKeys * 128;                   // bf16: dims 64..127 behind dims 0..63
+    if (!c.paged) {
+      const int row = (int)(cont0 + key0);
+      if (elect_one()) {
+        tma::arrive_expect_tx(bar, half * (wide ? 2 : 1));
+        tma::load_2d(st, map, 0, row, bar);
+        if (wide) tma::load_2d(st + half, map, 64, row, bar);
+      }
+    } else {
+      const int P = c.page_size;
+      int row[4], np = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {                           // (four pages of 16 tokens at most)
+        // a reduction, not a shuffle: its result is uniform for the compiler,
+        // and a copy with uniform operands issues twice as fast
+        row[k] = __reduce_max_sync(0xffffffffu, lane == (j & 7) * 4 + k ? ids : -1);
+        np += row[k] >= 0;
+      }
+      if (elect_one()) {
+        tma::arrive_expect_tx(bar, np * (uint32_t)P * 128 * (wide ? 2 : 1));
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (row[k] >= 0) {
+            tma::load_2d(st + k * P * 128, map, 0, row[k], bar);
+            if (wide) tma::load_2d(st + half + k * P * 128, map, 64, row[k], bar);
+          }
+      }
+      __syncwarp();
     }
   };
 
@@ -350,66 +365,98 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       }
     } else {
       // ---------------------------------------------------------- MMA issuer
-      if (lane == 0) {
+      {
         constexpr uint32_t ID_QK = C::K16 ? umma::idesc(umma::FMT_BF16, umma::FMT_BF16, umma::MAJOR_K, umma::MAJOR_K, 128, 64)
                                           : umma::idesc(umma::FMT_E4M3, umma::FMT_E4M3, umma::MAJOR_K, umma::MAJOR_K, 128, 64);
         constexpr uint32_t FV = C::V16 ? umma::FMT_BF16 : umma::FMT_F16;
         constexpr uint32_t ID_PV = umma::idesc(FV, FV, umma::MAJOR_K, umma::MAJOR_MN, 128, 128);
         const uint32_t qa = umma::smem_u32(qop);
         auto issue_qk = [&](int j) {
-          if (!wait_fast(&kfull[j % C::KN], (j / C::KN) & 1, abort_flag)) return false;
+          const bool in = wait_fast(&kfull[j % C::KN], (j / C::KN) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, in)) return false;
           umma::fence_after_sync();
           const uint32_t ka = umma::smem_u32(kring + (j % C::KN) * C::KT), sd = tmem + 64 * (j & 1);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            // e4m3: 32 dims a step, the four steps of hi and of lo meet the same
-            // K; bf16: 16 dims a step, halves of 64 dims behind each other
-            const uint64_t a = umma::sdesc(qa + (kk >> 2) * (kCtRows * 128) + (kk & 3) * 32, 16, 1024, umma::SWIZZLE_128B);
-            const uint64_t b = umma::sdesc(ka + (C::K16 ? (kk >> 2) * (kChunkKeys * 128) : 0) + (kk & 3) * 32, 16, 1024,
-                                           umma::SWIZZLE_128B);
-            if constexpr (C::K16) umma::mma_f16_ss(sd, a, b, ID_QK, kk > 0);
-            else umma::mma_f8_ss(sd, a, b, ID_QK, kk > 0);
+            for (int kk = 0; kk < 8; ++kk) {
+              // e4m3: 32 dims a step, the four steps of hi and of lo meet the same
+              // K; bf16: 16 dims a step, halves of 64 dims behind each other
+              const uint64_t a = umma::sdesc(qa + (kk >> 2) * (kCtRows * 128) + (kk & 3) * 32, 16, 1024, umma::SWIZZLE_128B);
+              const uint64_t b = umma::sdesc(ka + (C::K16 ? (kk >> 2) * (kChunkKeys * 128) : 0) + (kk & 3) * 32, 16, 1024,
+                                             umma::SWIZZLE_128B);
+              if constexpr (C::K16) umma::mma_f16_ss(sd, a, b, ID_QK, kk > 0);
+              else umma::mma_f8_ss(sd, a, b, ID_QK, kk > 0);
+            }
+            umma::mma_commit(&s_full[j & 1]);
+            umma::mma_commit(&kfree[j % C::KN]);
           }
-          umma::mma_commit(&s_full[j & 1]);
-          umma::mma_commit(&kfree[j % C::KN]);
+          __syncwarp();
           return true;
         };
         bool ok = n > 0 && issue_qk(0);
         if (ok && n > 1) ok = issue_qk(1);
         for (int j = 0; ok && j < n; ++j) {
           const int ob = j % OPN;
-          if (!wait_fast(&op_full[ob], (j / OPN) & 1, abort_flag)) break;
-          if (!wait_fast(&p_full[j & 1], (j >> 1) & 1, abort_flag)) break;
+          bool in = wait_fast(&op_full[ob], (j / OPN) & 1, abort_flag);
+          in = in && wait_fast(&p_full[j & 1], (j >> 1) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, in)) break;
           umma::fence_after_sync();
-          const uint32_t va = umma::smem_u32(vop + ob * (C::V16 ? C::VST : C::OPT)), pa = tmem + 64 * (j & 1);
+          const uint32_t va = umma::smem_u32(vop + ob * (C::V16 ? C::VT : C::OPT)), pa = tmem + 64 * (j & 1);
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ts(o_col, pa + 8 * kk, umma::sdesc(va + kk * 2048, kChunkKeys * 128, 1024, umma::SWIZZLE_128B), ID_PV,
-                       (j > 0 || kk > 0) ? 1u : 0u);
-          umma::mma_commit(pv_done);
-          umma::mma_commit(&op_free[ob]);
-          if constexpr (C::V16) umma::mma_commit(&vfree[ob]);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ts(o_col, pa + 8 * kk, umma::sdesc(va + kk * 2048, kChunkKeys * 128, 1024, umma::SWIZZLE_128B), ID_PV,
+                         (j > 0 || kk > 0) ? 1u : 0u);
+            umma::mma_commit(pv_done);
+            if constexpr (C::V16) umma::mma_commit(&vfree[ob]);
+            else umma::mma_commit(&op_free[ob]);
+          }
+          __syncwarp();
           if (j + 2 < n) {
             // the scores of tile j + 2 go where P of tile j was
-            if (!wait_fast(pv_done, j & 1, abort_flag)) break;
+            in = wait_fast(pv_done, j & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, in)) break;
             ok = issue_qk(j + 2);
           }
         }
         // all issued MMAs complete before TMEM is released
-        umma::mma_commit(drained);
+        __syncwarp();
+        if (elect_one()) umma::mma_commit(drained);
         (void)umma::mbar_wait(drained, 0, 100000000ull);
       }
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ preparation
     const int kr = tid - 256;                     // this thread's key of the tile
+    // its scales come straight from the cache, a tile ahead, and the page id
+    // (paged) two tiles ahead
+    float next_k = 0.f, next_v = 0.f;
+    auto key_seen = [&](int j) {
+      const int key = j < n ? chunk_key0(t, j0 + j) + kr : INT32_MAX;
+      return key < t.kv_end && (key >= t.lo || key < p.sinks) ? key : -1;
+    };
+    auto fetch_page = [&](int j) {
+      const int key = c.paged ? key_seen(j) : -1;
+      return key < 0 ? 0 : c.page_table[(int64_t)t.b * c.max_pages_per_seq + (key >> c.page_shift)];
+    };
+    auto fetch_scales = [&](int j, int page) {
+      const int key = C::K16 && C::V16 ? -1 : key_seen(j);
+      if (key < 0) return;
+      if (page < 0 || page >= c.num_pages) page = 0;          // (reported by the producer)
+      const int64_t row = c.paged ? ((int64_t)page * c.kv_heads + hk) * c.page_size + (key & (c.page_size - 1)) : cont0 + key;
+      if constexpr (!C::K16) next_k = c.k_scale[row];
+      if constexpr (!C::V16) next_v = c.v_scale[row];
+    };
+    fetch_scales(0, fetch_page(0));
+    int page = fetch_page(1);
     for (int j = 0; j < n; ++j) {
       const int vs = j % C::VN, cb = j % C::NCOL, key0 = chunk_key0(t, j0 + j);
       bool ok = wait_fast(&vfull[vs], (j / C::VN) & 1, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
-      uint8_t* st = vring + vs * C::VST;
-      const float* ksc = reinterpret_cast<const float*>(st + C::VT);
-      const float* vsc = ksc + kChunkKeys;
+      uint8_t* st = vring + vs * C::VT;
+      const float k_scale = next_k, v_scale = next_v;
+      fetch_scales(j + 1, page);
+      page = fetch_page(j + 2);
       const bool part = !chunk_all_seen(p, t, key0);
       float* cc = cols + cb * C::CST;
       auto seen = [&](int k) { return !part || (key0 + k < t.kv_end && (key0 + k >= t.lo || key0 + k < p.sinks)); };
@@ -417,14 +464,13 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       // per-key scales; in a tile that not every query sees whole they wait
       // for the values: a row with one that is not finite marks its key's score
       auto publish = [&](bool aside) {
-        const float vv = C::V16 || !vis ? 0.f : vsc[kr];
+        const float vv = C::V16 || !vis ? 0.f : v_scale;
         aside = (aside || !(fabsf(vv) < INFINITY)) && part && vis;
-        cc[kr] = aside ? NAN : C::K16 ? 1.f : vis ? ksc[kr] * p.scale_log2 : 0.f;
+        cc[kr] = aside ? NAN : C::K16 ? 1.f : vis ? k_scale * p.scale_log2 : 0.f;
         if constexpr (!C::V16) cc[kChunkKeys + kr] = aside ? 0.f : vv;
-        if (!C::V16 && warp == 8) {                // the tile's largest finite value scale
-          const float a = vsc[lane], b = vsc[lane + 32];
-          const float vm = warp_max_f32(fmaxf(seen(lane) && a < INFINITY ? a : 0.f, seen(lane + 32) && b < INFINITY ? b : 0.f));
-          if (lane == 0) cc[2 * kChunkKeys] = vm;
+        if constexpr (!C::V16) {                   // the largest finite value scale of these 32 keys
+          const float vm = warp_max_f32(vv < INFINITY ? vv : 0.f);
+          if (lane == 0) cc[2 * kChunkKeys + warp - 8] = vm;
         }
         __syncwarp();
         if (lane == 0) umma::mbar_arrive(&col_full[cb]);
@@ -541,7 +587,7 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
           for (int i = 0; i < 2; ++i) sv[i][k] = __fmul2_rn(sv[i][k], x);
         }
       }
-      const float vmt = C::V16 ? 0.f : cols[cb * C::CST + 2 * kChunkKeys];
+      const float vmt = C::V16 ? 0.f : fmaxf(cols[cb * C::CST + 2 * kChunkKeys], cols[cb * C::CST + 2 * kChunkKeys + 1]);
       float vm[2] = {vmt, vmt};                   // largest value scale that the row sees
       if (!chunk_all_seen(p, t, key0)) {          // some query of the tile does not see all of its keys
 #pragma unroll
