@@ -330,22 +330,30 @@ def fp8kv_prefill_attention(q: torch.Tensor, cache: Fp8KVCache, q_pos0: torch.Te
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 
 
-def _here(t: torch.Tensor, dtype, name, shape=None, contiguous=True):
-    """A CUDA tensor of `dtype` on the current device (the launch goes to that
-    device's stream), contiguous unless said otherwise; returns its address."""
+def _refuse(t, dtype, name, shape, contiguous):
     if t.dtype is not dtype or not t.is_cuda or (contiguous and not t.is_contiguous()):
         raise ValueError(f"{name}: expected a {'contiguous ' if contiguous else ''}CUDA {dtype} tensor, got "
                          f"{t.dtype} on {t.device} (contiguous={t.is_contiguous()})")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    if shape is not None and tuple(t.shape) != shape:
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: on {t.device}, but the call runs on cuda:{torch.cuda.current_device()}, the current device")
+
+
+def _here(t: torch.Tensor, dtype, name, dev, shape=None):
+    """Address of a contiguous CUDA tensor of `dtype` on device `dev` (the
+    current one: the launch goes to that device's stream)."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        _refuse(t, dtype, name, shape, True)
     return t.data_ptr()
 
 
-def _cache_here(cache: Fp8KVCache):
-    if cache.k.get_device() != torch.cuda.current_device():
-        raise ValueError(f"cache: on {cache.k.device}, but the current device is cuda:{torch.cuda.current_device()}")
+def _current(cache: Fp8KVCache) -> int:
+    """The current device, which has to be the cache's."""
+    dev = cache.k.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"cache: on {cache.k.device}, but the current device is "
+                         f"{torch.cuda.current_device() if torch.cuda.is_available() else 'none'}")
+    return dev
 
 
 def _on(stream):
@@ -353,8 +361,8 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _raw_stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def fp8kv_build_tables(cache: Fp8KVCache, cached_lens: torch.Tensor, new_lens: torch.Tensor, n_rows: int,
@@ -372,13 +380,11 @@ def fp8kv_build_tables(cache: Fp8KVCache, cached_lens: torch.Tensor, new_lens: t
     paged = cache.layout == LAYOUT_PAGED
     if paged != (free_pages is not None) or paged != (free_head is not None):
         raise ValueError("free_pages and free_head come with a paged cache, and only with one")
-    _cache_here(cache)
-    a_cached = _here(cached_lens, torch.int32, "cached_lens", (B,))
-    a_new = _here(new_lens, torch.int32, "new_lens", (B,))
-    F, a_free, a_head = 0, None, None
+    dev, i32 = _current(cache), torch.int32
+    F, a_free, a_head, a_out = 0, None, None, None
     if paged:
         F = free_pages.numel()
-        a_free, a_head = _here(free_pages, torch.int32, "free_pages", (F,)), _here(free_head, torch.int32, "free_head", (1,))
+        a_free, a_head = _here(free_pages, i32, "free_pages", dev, (F,)), _here(free_head, i32, "free_head", dev, (1,))
     if cu_new is None or seq_lens is None or seq_idx is None or pos is None or slots is None or \
             (paged and free_head_out is None):
         with _on(stream):
@@ -387,12 +393,15 @@ def fp8kv_build_tables(cache: Fp8KVCache, cached_lens: torch.Tensor, new_lens: t
             cu_new, seq_lens, seq_idx, pos = new(cu_new, B + 1), new(seq_lens, B), new(seq_idx, N), new(pos, N)
             slots = new(slots, N, torch.int64)
             free_head_out = new(free_head_out, 1) if paged else free_head_out
-    a_out = None if free_head_out is None else _here(free_head_out, torch.int32, "free_head_out", (1,))
+    if paged:
+        a_out = _here(free_head_out, i32, "free_head_out", dev, (1,))
+    elif free_head_out is not None:
+        raise ValueError("free_head_out comes with a paged cache")
     _check(get_lib().fp8kv_build_tables(
-        cache.struct_ref, a_cached, a_new, a_free, F, a_head, N, _here(cu_new, torch.int32, "cu_new", (B + 1,)),
-        _here(seq_lens, torch.int32, "seq_lens", (B,)), _here(seq_idx, torch.int32, "seq_idx", (N,)),
-        _here(pos, torch.int32, "pos", (N,)), _here(slots, torch.int64, "slots", (N,)), a_out, _raw_stream(stream)),
-        "fp8kv_build_tables")
+        cache.struct_ref, _here(cached_lens, i32, "cached_lens", dev, (B,)), _here(new_lens, i32, "new_lens", dev, (B,)), a_free, F,
+        a_head, N, _here(cu_new, i32, "cu_new", dev, (B + 1,)), _here(seq_lens, i32, "seq_lens", dev, (B,)),
+        _here(seq_idx, i32, "seq_idx", dev, (N,)), _here(pos, i32, "pos", dev, (N,)), _here(slots, torch.int64, "slots", dev, (N,)),
+        a_out, _raw_stream(stream, dev)), "fp8kv_build_tables")
     return {"cu_new": cu_new, "seq_lens": seq_lens, "seq_idx": seq_idx, "pos": pos, "slots": slots,
             "free_head": free_head_out}
 
@@ -409,22 +418,23 @@ def fp8kv_rope_tables(positions: int, rot_dim: int, base: float = 10000.0, facto
             shape = (int(positions), int(rot_dim) // 2)
             cos = torch.empty(shape, device="cuda") if cos is None else cos
             sin = torch.empty(shape, device="cuda") if sin is None else sin
-    shape = (positions, rot_dim // 2)
+    shape, dev = (positions, rot_dim // 2), torch.cuda.current_device()
     _check(get_lib().fp8kv_rope_tables(
         positions, rot_dim, base, factor, original_positions, ramp[0], ramp[1], amplitude,
-        _here(cos, torch.float32, "cos", shape), _here(sin, torch.float32, "sin", shape), _raw_stream(stream)),
+        _here(cos, torch.float32, "cos", dev, shape), _here(sin, torch.float32, "sin", dev, shape), _raw_stream(stream, dev)),
         "fp8kv_rope_tables")
     return cos, sin
 
 
-def _rows(t, heads, dim, n, name):
+def _rows(t, heads, dim, n, name, dev):
     """[n, heads, dim] bf16 whose tokens may lie apart (a slice of a fused
     projection): address and token stride."""
-    a = _here(t, torch.bfloat16, name, (n, heads, dim), contiguous=False)
+    if t.dtype is not torch.bfloat16 or t.get_device() != dev or t.shape != (n, heads, dim):
+        _refuse(t, torch.bfloat16, name, (n, heads, dim), False)
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name}: heads of a token must lie side by side, got strides {t.stride()}")
-    return a, (s0 if n > 1 else max(s0, heads * dim))
+    return t.data_ptr(), (s0 if n > 1 else max(s0, heads * dim))
 
 
 def fp8kv_rope_append(cache: Fp8KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,
@@ -442,19 +452,19 @@ def fp8kv_rope_append(cache: Fp8KVCache, q: torch.Tensor, k: torch.Tensor, v: to
         raise ValueError(f"cos: expected [positions, rot_dim / 2], got {tuple(cos.shape)}")
     if D != cache.head_dim:
         raise ValueError(f"q: head dim {D}, but the cache's is {cache.head_dim}")
-    _cache_here(cache)
-    a_q, s_q = _rows(q, Hq, D, n, "q")
-    a_k, s_k = _rows(k, cache.kv_heads, D, n, "k")
-    a_v, s_v = _rows(v, cache.kv_heads, D, n, "v")
+    dev = _current(cache)
+    a_q, s_q = _rows(q, Hq, D, n, "q", dev)
+    a_k, s_k = _rows(k, cache.kv_heads, D, n, "k", dev)
+    a_v, s_v = _rows(v, cache.kv_heads, D, n, "v", dev)
     if q_out is None:
         with _on(stream):
             q_out = torch.empty((n, Hq, D), dtype=torch.bfloat16, device=q.device)
     T, half = cos.shape
     _check(get_lib().fp8kv_rope_append(
-        cache.struct_ref, a_q, s_q, a_k, s_k, a_v, s_v, Hq, _here(pos, torch.int32, "pos", (n,)),
-        _here(slots, torch.int64, "slots", (n,)), n, _here(cos, torch.float32, "cos"),
-        _here(sin, torch.float32, "sin", (T, half)), T, 2 * half, ROPE_LAYOUTS[layout],
-        _here(q_out, torch.bfloat16, "q_out", (n, Hq, D)), _raw_stream(stream)), "fp8kv_rope_append")
+        cache.struct_ref, a_q, s_q, a_k, s_k, a_v, s_v, Hq, _here(pos, torch.int32, "pos", dev, (n,)),
+        _here(slots, torch.int64, "slots", dev, (n,)), n, _here(cos, torch.float32, "cos", dev),
+        _here(sin, torch.float32, "sin", dev, (T, half)), T, 2 * half, ROPE_LAYOUTS[layout],
+        _here(q_out, torch.bfloat16, "q_out", dev, (n, Hq, D)), _raw_stream(stream, dev)), "fp8kv_rope_append")
     return q_out
 
 
@@ -484,8 +494,7 @@ def fp8kv_chunk_attention(q: torch.Tensor, cache: Fp8KVCache, cu_q: Optional[tor
     total_q, Hq, D = q.shape
     if D != cache.head_dim:
         raise ValueError(f"q: head dim {D}, but the cache's is {cache.head_dim}")
-    _cache_here(cache)
-    a_q = _here(q, torch.bfloat16, "q")
+    dev = _current(cache)
     k = _kernel(kernel)
     if out is None or workspace is None:
         with _on(stream):
@@ -494,14 +503,16 @@ def fp8kv_chunk_attention(q: torch.Tensor, cache: Fp8KVCache, cu_q: Optional[tor
             if workspace is None:
                 need = fp8kv_chunk_workspace_bytes(cache, total_q, Hq, window, sinks, num_splits, k)
                 workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    if out.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"out: expected bf16 or fp32, got {out.dtype}")
+    odt = out.dtype
+    if odt is not torch.bfloat16 and odt is not torch.float32:
+        raise ValueError(f"out: expected bf16 or fp32, got {odt}")
     _check(get_lib().fp8kv_chunk_attention(
-        a_q, cache.struct_ref, None if cu_q is None else _here(cu_q, torch.int32, "cu_q", (cache.batch + 1,)),
-        _here(seq_lens, torch.int32, "seq_lens", (cache.batch,)), total_q, Hq,
+        _here(q, torch.bfloat16, "q", dev), cache.struct_ref,
+        None if cu_q is None else _here(cu_q, torch.int32, "cu_q", dev, (cache.batch + 1,)),
+        _here(seq_lens, torch.int32, "seq_lens", dev, (cache.batch,)), total_q, Hq,
         1.0 / math.sqrt(D) if sm_scale is None else sm_scale, window, sinks, num_splits, k,
-        _here(workspace, torch.uint8, "workspace"), workspace.numel(), _here(out, out.dtype, "out", (total_q, Hq, D)),
-        OUT_F32 if out.dtype == torch.float32 else OUT_BF16, _raw_stream(stream)), "fp8kv_chunk_attention")
+        _here(workspace, torch.uint8, "workspace", dev), workspace.numel(), _here(out, odt, "out", dev, (total_q, Hq, D)),
+        OUT_F32 if odt is torch.float32 else OUT_BF16, _raw_stream(stream, dev)), "fp8kv_chunk_attention")
     return out
 
 

@@ -20,7 +20,7 @@ bool overlap(const Range& a, const Range& b) {
 
 bool misaligned(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; }
 
-struct ChunkPlan { int kernel, row_warps, tile_tokens, tiles, splits; };
+struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 
 // How a chunk call runs.  Tiles: rows per tile by the average number of query
 // rows (queries x heads of a group) a sequence has, so that short chunks do
@@ -41,8 +41,8 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   if (kernel == FP8KV_KERNEL_TENSOR_CORES && !tc_built) return FP8KV_ERR_UNSUPPORTED;
   const bool tc = kernel == FP8KV_KERNEL_TENSOR_CORES || (kernel == FP8KV_KERNEL_AUTO && tc_built && rows > 32);
   plan->kernel = tc ? FP8KV_KERNEL_TENSOR_CORES : FP8KV_KERNEL_WARP_MMA;
-  plan->row_warps = tc ? 8 : rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  plan->tile_tokens = 16 * plan->row_warps / G;
+  plan->tile_rows = tc ? 128 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  plan->tile_tokens = plan->tile_rows / G;
   const int64_t tiles = total_q / plan->tile_tokens + c->batch;
   if (tiles > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
   plan->tiles = (int)tiles;
@@ -242,7 +242,8 @@ fp8kv_status fp8kv_chunk_attention(const void* q, const fp8kv_cache* cache, cons
   cudaStream_t s = (cudaStream_t)stream;
   const int tiles = cu_q ? plan.tiles : cache->batch;
   cudaError_t e = plan.kernel == FP8KV_KERNEL_TENSOR_CORES ? launch_chunk_tc(p, cache->dtype, tiles, s)
-                                                            : launch_chunk_mma(p, cache->dtype, plan.row_warps, tiles, s);
+                  : plan.tile_rows == 8 ? launch_chunk_rows(p, cache->dtype, tiles, s)
+                                        : launch_chunk_mma(p, cache->dtype, plan.tile_rows / 16, tiles, s);
   if (e == cudaSuccess && plan.splits > 1) e = launch_chunk_merge(p, s);
   return cuda_status(e);
 }

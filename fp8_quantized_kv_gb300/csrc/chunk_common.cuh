@@ -11,10 +11,12 @@
 #pragma once
 
 #include "params.cuh"
+#include "tc_common.cuh"
 
 namespace fp8kv {
 
 constexpr int kChunkKeys = 64;     // keys per KV tile
+constexpr int kChunkThreads = 128; // of the kernels on warp-level matrix instructions
 
 struct ChunkTile {
   int b;           // sequence
@@ -108,6 +110,95 @@ __device__ __forceinline__ int chunk_row(const ChunkParams& p, const ChunkTile& 
 __device__ __forceinline__ float chunk_weight(float m, float l, float M) {
   if (m == -INFINITY) return l == l ? 0.f : l;
   return exp2f(m - M);
+}
+
+// ------------------------------------- warp-level matrix instructions --
+// 16-byte chunk of a K row in shared memory.  A lane reads 16 (MX: 8) bytes of
+// row lane / 4, four lanes side by side: neighbouring rows swap their 64-byte
+// (MX: 32-byte) parts so that a quarter warp (half warp) meets every bank once.
+template <int KE, int KB>
+__device__ __forceinline__ int k_chunk(int ch, int row) {
+  if constexpr (KE == ELEM_MX) return ch ^ ((row & 3) << 1);
+  return KB >= 128 ? ch ^ ((row & 1) << 2) : ch;
+}
+// 16-byte chunk of a V row: eight rows' chunks of the same column lie in
+// different banks (ldmatrix).
+template <int VB>
+__device__ __forceinline__ int v_chunk(int ch, int row) {
+  return VB >= 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
+}
+
+__device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4_z(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool BF16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float x, float y) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// Non-finite 16-bit values of a B fragment register: `clean` has zeros in
+// their place, the others 1.0 at each NaN, +inf or -inf.
+template <bool BF16>
+struct SetAside {
+  uint32_t clean, nan, pinf, ninf;
+  __device__ __forceinline__ explicit SetAside(uint32_t w) : clean(w), nan(0), pinf(0), ninf(0) {
+    constexpr uint32_t INF = BF16 ? 0x7F80u : 0x7C00u, ONE = BF16 ? 0x3F80u : 0x3C00u;
+#pragma unroll
+    for (int sh = 0; sh < 32; sh += 16) {
+      const uint32_t h = (w >> sh) & 0xFFFFu, m = h & 0x7FFFu;
+      if (m < INF) continue;
+      clean &= ~(0xFFFFu << sh);
+      if (m > INF) nan |= ONE << sh;
+      else if (h & 0x8000u) ninf |= ONE << sh;
+      else pinf |= ONE << sh;
+    }
+  }
+};
+
+
+// Elements d .. d + 3 of an unnormalised row of out with its maximum and sum:
+// normalised into out, or kept as this split's share.
+__device__ __forceinline__ void chunk_store(const ChunkParams& p, int64_t row, int split, int D, int d, const float (&x)[4],
+                                            float m, float l) {
+  if (p.num_splits > 1) {
+    const int64_t at = row * p.num_splits + split;
+    *reinterpret_cast<float4*>(p.part_o + at * D + d) = make_float4(x[0], x[1], x[2], x[3]);
+    if (d == 0) { p.part_m[at] = m; p.part_l[at] = l; }
+    return;
+  }
+  const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
+  if (p.out_f32)
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + row * D + d) =
+        make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+  else
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + row * D + d) =
+        make_uint2(pack16<true>(x[0] * inv, x[1] * inv), pack16<true>(x[2] * inv, x[3] * inv));
 }
 
 }  // namespace fp8kv

@@ -30,11 +30,8 @@
 // only some of the queries see, non-finite values are set aside and added
 // to the queries that see them (a zero weight times NaN would not be zero).
 #include "chunk_common.cuh"
-#include "tc_common.cuh"
 
 namespace fp8kv {
-
-constexpr int kChunkThreads = 128;
 
 template <int D, int KE, int VE>
 struct ChunkCfg {
@@ -46,74 +43,6 @@ struct ChunkCfg {
   static constexpr int OS = D + 4;                             // fp32 row stride of the join buffer
   static constexpr int JOIN = 64 * OS * 4 + 2 * 64 * 4;
   static constexpr int BYTES = (NS * STAGE > JOIN ? NS * STAGE : JOIN) + 4 * kChunkKeys * 4;
-};
-
-// 16-byte chunk of a K row in shared memory.  A lane reads 16 (MX: 8) bytes of
-// row lane / 4, four lanes side by side: neighbouring rows swap their 64-byte
-// (MX: 32-byte) parts so that a quarter warp (half warp) meets every bank once.
-template <int KE, int KB>
-__device__ __forceinline__ int k_chunk(int ch, int row) {
-  if constexpr (KE == ELEM_MX) return ch ^ ((row & 3) << 1);
-  return KB >= 128 ? ch ^ ((row & 1) << 2) : ch;
-}
-// 16-byte chunk of a V row: eight rows' chunks of the same column lie in
-// different banks (ldmatrix).
-template <int VB>
-__device__ __forceinline__ int v_chunk(int ch, int row) {
-  return VB >= 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3);
-}
-
-__device__ __forceinline__ void cp_async16_z(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4_z(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-template <bool BF16>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (BF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack16(float x, float y) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-
-// Non-finite 16-bit values of a B fragment register: `clean` has zeros in
-// their place, the others 1.0 at each NaN, +inf or -inf.
-template <bool BF16>
-struct SetAside {
-  uint32_t clean, nan, pinf, ninf;
-  __device__ __forceinline__ explicit SetAside(uint32_t w) : clean(w), nan(0), pinf(0), ninf(0) {
-    constexpr uint32_t INF = BF16 ? 0x7F80u : 0x7C00u, ONE = BF16 ? 0x3F80u : 0x3C00u;
-#pragma unroll
-    for (int sh = 0; sh < 32; sh += 16) {
-      const uint32_t h = (w >> sh) & 0xFFFFu, m = h & 0x7FFFu;
-      if (m < INF) continue;
-      clean &= ~(0xFFFFu << sh);
-      if (m > INF) nan |= ONE << sh;
-      else if (h & 0x8000u) ninf |= ONE << sh;
-      else pinf |= ONE << sh;
-    }
-  }
 };
 
 template <int D, int KE, int VE, int MW>
@@ -492,22 +421,6 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
   }
   // four neighbouring elements of row g + 8 i: e4m3 values interleave two
   // accumulator tiles, bf16 values have two neighbours in each
-  auto store = [&](int64_t row, int d, const float (&x)[4], float mm, float ll) {
-    if (p.num_splits > 1) {
-      const int64_t at = row * p.num_splits + split;
-      *reinterpret_cast<float4*>(p.part_o + at * D + d) = make_float4(x[0], x[1], x[2], x[3]);
-      if (d == 0) { p.part_m[at] = mm; p.part_l[at] = ll; }
-      return;
-    }
-    const float inv = ll > 0.f ? 1.f / ll : 0.f;
-    if (p.out_f32) {
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + row * D + d) =
-          make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-    } else {
-      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + row * D + d) =
-          make_uint2(pack16<true>(x[0] * inv, x[1] * inv), pack16<true>(x[2] * inv, x[3] * inv));
-    }
-  };
   if constexpr (MW == 4 && !VB16) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
@@ -515,7 +428,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
 #pragma unroll
         for (int u = 0; u < D / 16; ++u) {
           const float x[4] = {o[2 * u][2 * i], o[2 * u + 1][2 * i], o[2 * u][2 * i + 1], o[2 * u + 1][2 * i + 1]};
-          store(qrow[i], 16 * u + 4 * c4, x, m[i], l[i]);
+          chunk_store(p, qrow[i], split, D, 16 * u + 4 * c4, x, m[i], l[i]);
         }
   } else {
     cp_async_wait<0>();
@@ -557,7 +470,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
         x[0] = fmaf(w, v.x, x[0]); x[1] = fmaf(w, v.y, x[1]);
         x[2] = fmaf(w, v.z, x[2]); x[3] = fmaf(w, v.w, x[3]);
       }
-      store((int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G), d, x, M, L);
+      chunk_store(p, (int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G), split, D, d, x, M, L);
     }
   }
 }

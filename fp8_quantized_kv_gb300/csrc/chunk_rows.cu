@@ -1,0 +1,435 @@
+// chunk_rows.cu -- ragged chunk attention for tiles of at most eight query
+// rows (single tokens of a group of up to eight heads, a few drafted tokens):
+// the cache is read once and nothing else takes as long, so the kernel is
+// built around keeping loads in flight.
+//
+// The products are turned around so that the eight queries are the narrow side
+// of the matrix instruction: S^T = K Q^T (16 keys x 8 queries per instruction)
+// and O^T = V^T P^T (16 head dims x 8 queries).  A warp owns groups of 16 keys:
+// it copies their K and V rows and scales into its own ring (cp.async, no
+// barrier between warps), and keeps its own running maximum m, sum l and O^T;
+// the four warps of a CTA, and the splits of a long sequence, are joined at the
+// end.  A group never crosses a page (pages hold 16 tokens or more), so a page
+// id is looked up once per group, an iteration before its copy.
+//
+// Arithmetic as in chunk_mma.cu: f16 operands for e4m3 sides (codes exact,
+// query scaled by a power of two, P by 2^-kp and the value scale), bf16 for
+// bf16 sides, m, l and O in fp32.
+#include "chunk_common.cuh"
+
+namespace fp8kv {
+
+constexpr int kRowKeys = 16;       // keys of a group
+
+template <int D, int KE, int VE>
+struct RowsCfg {
+  static constexpr int KB = KE == ELEM_BF16 ? 2 * D : D;
+  static constexpr int VB = VE == ELEM_BF16 ? 2 * D : D;
+  static constexpr int STAGE = kRowKeys * (KB + VB) + 2 * kRowKeys * 4;    // rows, key scales, value scales
+  static constexpr int NS = KB + VB > 256 ? 3 : 4;
+  static constexpr int OS = D + 4;
+  static constexpr int JOIN = 32 * OS * 4 + 2 * 32 * 4;
+  static constexpr int RING = 4 * NS * STAGE;
+  static constexpr int BYTES = RING > JOIN ? RING : JOIN;
+};
+
+// 8x8 transposition of 16-bit elements held as a matrix fragment.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, int KE, int VE>
+__global__ void __launch_bounds__(kChunkThreads) chunk_rows(const ChunkParams p) {
+  using C = RowsCfg<D, KE, VE>;
+  constexpr bool KB16 = KE == ELEM_BF16, VB16 = VE == ELEM_BF16;
+  constexpr int KS = D / 16;                   // k steps of QK, m tiles of PV
+  extern __shared__ __align__(128) uint8_t rsm[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
+  const int hk = blockIdx.y, split = blockIdx.z;
+  ChunkTile t;
+  if (!chunk_tile(p, gridDim.x - 1 - blockIdx.x, tid == 0 && hk == 0 && split == 0, t)) return;
+  const CacheView& c = p.c;
+  const int G = p.group;
+  // groups of 16 keys: those of the first tokens, then the window's
+  const int first = t.lo / kRowKeys;
+  const int n_sink = p.window > 0 ? min((min(p.sinks, t.kv_end) + kRowKeys - 1) / kRowKeys, first) : 0;
+  const int all = n_sink + max(0, (t.kv_end + kRowKeys - 1) / kRowKeys - first);
+  const int per = (all + p.num_splits - 1) / p.num_splits;
+  const int j0 = min(all, split * per) + warp, j1 = min(all, (split + 1) * per);
+  const int n = j1 > j0 ? (j1 - j0 + 3) / 4 : 0;                 // this warp's groups j0, j0 + 4, ...
+  auto group_key0 = [&](int it) {
+    const int j = j0 + 4 * it;
+    return (j < n_sink ? j : first + j - n_sink) * kRowKeys;
+  };
+  const int64_t cont0 = ((int64_t)t.b * c.kv_heads + hk) * c.max_tokens;
+  auto fetch_page = [&](int it) {
+    return c.paged && it < n ? c.page_table[(int64_t)t.b * c.max_pages_per_seq + (group_key0(it) >> c.page_shift)] : 0;
+  };
+  uint8_t* ring = rsm + warp * C::NS * C::STAGE;
+  auto issue = [&](int it, int page) {
+    if (it < n) {
+      const int key0 = group_key0(it);
+      int64_t row = cont0 + key0;
+      bool ok = true;
+      if (c.paged) {
+        ok = page >= 0 && page < c.num_pages;
+        if (!ok && lane == 0) raise_error(p.err, FP8KV_DEVERR_BAD_PAGE);
+        row = ((int64_t)(ok ? page : 0) * c.kv_heads + hk) * c.page_size + (key0 & (c.page_size - 1));
+      }
+      // rows nobody sees are zero-filled, not read: they may hold anything
+      auto live = [&](int r) { return ok && key0 + r < t.kv_end && (key0 + r >= t.lo || key0 + r < p.sinks); };
+      const uint32_t ks = umma::smem_u32(ring + (it % C::NS) * C::STAGE), vs = ks + kRowKeys * C::KB, sc = vs + kRowKeys * C::VB;
+      constexpr int KC = C::KB / 16, VC = C::VB / 16;
+#pragma unroll
+      for (int i = 0; i < KC / 2; ++i) {
+        const int e = lane + 32 * i, r = e / KC, ch = e % KC;
+        cp_async16_z(ks + r * C::KB + k_chunk<KE, C::KB>(ch, r) * 16, c.k + (row + r) * C::KB + ch * 16, live(r));
+      }
+#pragma unroll
+      for (int i = 0; i < VC / 2; ++i) {
+        const int e = lane + 32 * i, r = e / VC, ch = e % VC;
+        cp_async16_z(vs + r * C::VB + v_chunk<C::VB>(ch, r) * 16, c.v + (row + r) * C::VB + ch * 16, live(r));
+      }
+      const int r = lane & 15;
+      if (lane < 16 ? !KB16 : !VB16) cp_async4_z(sc + lane * 4, (lane < 16 ? c.k_scale : c.v_scale) + row + r, live(r));
+    }
+    cp_async_commit();
+  };
+  {
+    int page[C::NS - 1];
+#pragma unroll
+    for (int it = 0; it < C::NS - 1; ++it) page[it] = fetch_page(it);
+#pragma unroll
+    for (int it = 0; it < C::NS - 1; ++it) issue(it, page[it]);
+  }
+  int next_page = fetch_page(C::NS - 1);
+
+  // query row g as B fragments; positions of this thread's score columns
+  const int tokg = g / G;
+  const bool liveg = tokg < t.ntok && g < p.tile_tokens * G;
+  const uint4* qsrc = reinterpret_cast<const uint4*>(
+      p.q + (liveg ? (int64_t)(t.row0 + tokg) * p.q_heads + hk * G + (g - tokg * G) : 0) * D);
+  uint32_t qb[KS][2];
+#pragma unroll
+  for (int u = 0; u < D / 32; ++u) {
+    const int at = KE == ELEM_E4M3 ? 8 * (u >> 1) + 2 * c4 + (u & 1) : 4 * u + c4;
+    const uint4 x = liveg ? qsrc[at] : make_uint4(0, 0, 0, 0);
+    qb[2 * u][0] = x.x; qb[2 * u][1] = x.y; qb[2 * u + 1][0] = x.z; qb[2 * u + 1][1] = x.w;
+  }
+  float qf[2] = {1.f, 1.f};                    // what the scaled query leaves to undo, per score column
+  if constexpr (!KB16) {
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float f[2];
+        bf16x2_to_f32(qb[k][u], f);
+        amax = fmaxf(amax, fmaxf(fabsf(f[0]), fabsf(f[1])));
+      }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int e = ((__float_as_int(amax) >> 23) & 0xFF) - 127;
+    const int up = amax > 0.f && e < 128 ? min(14 - e, 126) : 0;   // amax 2^up in [2^14, 2^15)
+    const float sc = pow2i(up), down = pow2i(-up);
+#pragma unroll
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float f[2];
+        bf16x2_to_f32(qb[k][u], f);
+        qb[k][u] = pack16<false>(f[0] * sc, f[1] * sc);
+      }
+    qf[0] = __shfl_sync(0xffffffffu, down, 8 * c4);
+    qf[1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
+  }
+  int qpos[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = 2 * c4 + i, tk = r / G;
+    qpos[i] = tk < t.ntok && r < p.tile_tokens * G ? t.pos0 + tk : -1;
+    qf[i] *= p.scale_log2;
+  }
+
+  float o[KS][4];
+#pragma unroll
+  for (int u = 0; u < KS; ++u)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[u][e] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  int kp[2] = {-1000, -1000};
+
+#pragma unroll 1
+  for (int it = 0; it < n; ++it) {
+    cp_async_wait<C::NS - 2>();
+    __syncwarp();
+    issue(it + C::NS - 1, next_page);
+    next_page = fetch_page(it + C::NS);
+    const uint8_t* st = ring + (it % C::NS) * C::STAGE;
+    const uint8_t* vst = st + kRowKeys * C::KB;
+    const float* ksc = reinterpret_cast<const float*>(vst + kRowKeys * C::VB);
+    const float* vsc = ksc + kRowKeys;
+    const int key0 = group_key0(it);
+    // s[e]: key g + 8 (e >> 1), query 2 c4 + (e & 1); two chains of products
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (KE == ELEM_E4M3) {
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        const uint4 x = *reinterpret_cast<const uint4*>(st + g * C::KB + k_chunk<KE, C::KB>(4 * h + c4, g) * 16);
+        const uint4 y = *reinterpret_cast<const uint4*>(st + (g + 8) * C::KB + k_chunk<KE, C::KB>(4 * h + c4, g + 8) * 16);
+        const uint32_t xx[4] = {x.x, x.y, x.z, x.w}, yy[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)xx[u]), e4m3x2_to_f16x2((uint16_t)yy[u]),
+                                 e4m3x2_to_f16x2((uint16_t)(xx[u] >> 16)), e4m3x2_to_f16x2((uint16_t)(yy[u] >> 16))};
+          mma16816<false>(u & 1 ? s1 : s, a, qb[4 * h + u][0], qb[4 * h + u][1]);
+        }
+      }
+      const float k0 = ksc[g], k1 = ksc[g + 8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = (s[e] + s1[e]) * ((e >> 1 ? k1 : k0) * qf[e & 1]);
+    } else if constexpr (KE == ELEM_MX) {
+      const uint32_t e0 = reinterpret_cast<const uint32_t*>(ksc)[g], e1 = reinterpret_cast<const uint32_t*>(ksc)[g + 8];
+#pragma unroll
+      for (int blk = 0; blk < D / 32; ++blk) {
+        const int ch = 2 * blk + (c4 >> 1), in = (c4 & 1) * 8;
+        const uint2 x = *reinterpret_cast<const uint2*>(st + g * C::KB + k_chunk<KE, C::KB>(ch, g) * 16 + in);
+        const uint2 y = *reinterpret_cast<const uint2*>(st + (g + 8) * C::KB + k_chunk<KE, C::KB>(ch, g + 8) * 16 + in);
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)x.x), e4m3x2_to_f16x2((uint16_t)y.x),
+                               e4m3x2_to_f16x2((uint16_t)(x.x >> 16)), e4m3x2_to_f16x2((uint16_t)(y.x >> 16))};
+        const uint32_t b[4] = {e4m3x2_to_f16x2((uint16_t)x.y), e4m3x2_to_f16x2((uint16_t)y.y),
+                               e4m3x2_to_f16x2((uint16_t)(x.y >> 16)), e4m3x2_to_f16x2((uint16_t)(y.y >> 16))};
+        mma16816<false>(part, a, qb[2 * blk][0], qb[2 * blk][1]);
+        mma16816<false>(part, b, qb[2 * blk + 1][0], qb[2 * blk + 1][1]);
+        const float f0 = pow2_exact((int)((e0 >> (8 * blk)) & 0xFF) - 127), f1 = pow2_exact((int)((e1 >> (8 * blk)) & 0xFF) - 127);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = fmaf(part[e], e >> 1 ? f1 : f0, s[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] *= qf[e & 1];
+    } else {
+#pragma unroll
+      for (int u = 0; u < D / 32; ++u) {
+        const uint4 x = *reinterpret_cast<const uint4*>(st + g * C::KB + k_chunk<KE, C::KB>(4 * u + c4, g) * 16);
+        const uint4 y = *reinterpret_cast<const uint4*>(st + (g + 8) * C::KB + k_chunk<KE, C::KB>(4 * u + c4, g + 8) * 16);
+        const uint32_t a[4] = {x.x, y.x, x.y, y.y}, b[4] = {x.z, y.z, x.w, y.w};
+        mma16816<true>(s, a, qb[2 * u][0], qb[2 * u][1]);
+        mma16816<true>(s1, b, qb[2 * u + 1][0], qb[2 * u + 1][1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] = (s[e] + s1[e]) * qf[e & 1];
+    }
+    // does every query see all 16 keys?
+    const int last = key0 + kRowKeys - 1;
+    const bool part = !(last <= t.pos0 && (p.window <= 0 || key0 > t.pos0 + t.ntok - 1 - p.window || last < p.sinks));
+    bool see[4] = {true, true, true, true};
+    if (part) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        see[e] = chunk_sees(p, qpos[e & 1], key0 + g + 8 * (e >> 1));
+        if (!see[e]) s[e] = -INFINITY;
+      }
+    }
+    float mt[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], x));
+    float alpha[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float mn = fmaxf(m[i], mt[i]), ref = mn == -INFINITY ? 0.f : mn;
+      alpha[i] = m[i] == -INFINITY ? 1.f : ex2_ftz(m[i] - ref);
+      m[i] = mn;
+      s[i] = ex2_ftz(s[i] - ref);
+      s[2 + i] = ex2_ftz(s[2 + i] - ref);
+      l[i] = l[i] * alpha[i] + (s[i] + s[2 + i]);
+    }
+    if constexpr (!VB16) {
+      const float v0 = vsc[g], v1 = vsc[g + 8];
+      auto finite = [](float v) { return v < INFINITY ? v : 0.f; };
+      float vm[2];
+      if (!part) {
+        vm[0] = vm[1] = warp_max_f32(fmaxf(finite(v0), finite(v1)));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) vm[i] = fmaxf(see[i] ? finite(v0) : 0.f, see[2 + i] ? finite(v1) : 0.f);
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) vm[i] = fmaxf(vm[i], __shfl_xor_sync(0xffffffffu, vm[i], x));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int need = max(-100, min(100, ((__float_as_int(vm[i]) >> 23) & 0xFF) - 127 - 14));   // vm 2^-need < 2^15
+        if (vm[i] > 0.f && need > kp[i]) {
+          if (kp[i] > -1000) alpha[i] *= pow2_diff((float)(kp[i] - need), 0);
+          kp[i] = need;
+        }
+        const float vf = kp[i] > -1000 ? pow2i(-kp[i]) : 1.f;
+        // (an unseen key's scale may be anything)
+        s[i] = see[i] ? s[i] * (v0 * vf) : 0.f;
+        s[2 + i] = see[2 + i] ? s[2 + i] * (v1 * vf) : 0.f;
+      }
+    }
+    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+      for (int u = 0; u < KS; ++u) {
+        o[u][0] *= alpha[0]; o[u][1] *= alpha[1];
+        o[u][2] *= alpha[0]; o[u][3] *= alpha[1];
+      }
+    }
+    // P^T as a B fragment: keys 2 c4, + 1 (and + 8) of query g
+    const uint32_t b0 = transpose8(pack16<VB16>(s[0], s[1])), b1 = transpose8(pack16<VB16>(s[2], s[3]));
+    bool aside = false;                        // values that must not meet an unseeing query's zero weight
+    if (part && t.ntok > 1) {
+      constexpr int VC = C::VB / 16;
+      for (int e = lane; e < kRowKeys * VC; e += 32) {
+        const uint4 w = *reinterpret_cast<const uint4*>(vst + e * 16);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if constexpr (VB16)
+            aside = aside || (ww[u] & 0x7F800000u) == 0x7F800000u || (ww[u] & 0x7F80u) == 0x7F80u;
+          else
+            aside = aside || (((ww[u] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+        }
+      }
+      aside = __any_sync(0xffffffffu, aside);
+    }
+    const uint32_t vaddr = umma::smem_u32(vst);
+    const int vr = lane & 15;
+    // the two 16-dim A fragments of 32 bytes of V rows
+    auto load_v = [&](int u, uint32_t (&a)[2][4]) {
+      uint32_t r[4];
+      ldsm_x4_trans(vaddr + vr * C::VB + v_chunk<C::VB>(2 * u + (lane >> 4), vr) * 16, r);
+      if constexpr (VB16) {
+        a[0][0] = r[0]; a[0][1] = r[2]; a[0][2] = r[1]; a[0][3] = r[3];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          // two keys x two dims of codes -> the two keys of each dim
+          const uint32_t w = __byte_perm(r[k], 0, 0x3120);
+          a[k >> 1][2 * (k & 1)] = e4m3x2_to_f16x2((uint16_t)w);
+          a[k >> 1][2 * (k & 1) + 1] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+        }
+      }
+    };
+    constexpr int MT = VB16 ? 1 : 2;           // m tiles per 32 bytes of a row
+#pragma unroll
+    for (int u = 0; u < C::VB / 32; ++u) {
+      uint32_t a[2][4];
+      load_v(u, a);
+#pragma unroll
+      for (int k = 0; k < MT; ++k) {
+        if (aside) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[k][e] = SetAside<VB16>(a[k][e]).clean;
+        }
+        mma16816<VB16>(o[MT * u + k], a[k], b0, b1);
+      }
+    }
+    if (aside) {                               // rare: which queries see the values set aside
+      const uint32_t z0 = transpose8(pack16<VB16>(see[0] ? 1.f : 0.f, see[1] ? 1.f : 0.f));
+      const uint32_t z1 = transpose8(pack16<VB16>(see[2] ? 1.f : 0.f, see[3] ? 1.f : 0.f));
+#pragma unroll
+      for (int u = 0; u < C::VB / 32; ++u) {
+        uint32_t a[2][4];
+        load_v(u, a);
+#pragma unroll
+        for (int k = 0; k < MT; ++k) {
+          uint32_t an[4], ap[4], am[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const SetAside<VB16> x(a[k][e]);
+            an[e] = x.nan; ap[e] = x.pinf; am[e] = x.ninf;
+          }
+          float nan[4] = {0.f, 0.f, 0.f, 0.f}, pinf[4] = {0.f, 0.f, 0.f, 0.f}, ninf[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816<VB16>(nan, an, z0, z1);
+          mma16816<VB16>(pinf, ap, z0, z1);
+          mma16816<VB16>(ninf, am, z0, z1);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float& acc = o[MT * u + k][e];
+            if (pinf[e] > 0.f) acc += INFINITY;
+            if (ninf[e] > 0.f) acc -= INFINITY;
+            if (nan[e] > 0.f) acc = NAN;
+          }
+        }
+      }
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+  // the four warps meet: [warp][query][D] in the rings' place
+  cp_async_wait<0>();
+  __syncthreads();
+  float* osh = reinterpret_cast<float*>(rsm);
+  float* msh = osh + 32 * C::OS;
+  float* lsh = msh + 32;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = warp * 8 + 2 * c4 + i;
+    const float f = !VB16 && kp[i] > -1000 ? pow2i(kp[i]) : 1.f;
+    if (g == 0) { msh[r] = m[i]; lsh[r] = l[i]; }
+#pragma unroll
+    for (int u = 0; u < KS; ++u) {
+      if constexpr (VB16) {
+        osh[r * C::OS + 16 * u + g] = o[u][i];
+        osh[r * C::OS + 16 * u + 8 + g] = o[u][2 + i];
+      } else {
+        *reinterpret_cast<float2*>(osh + r * C::OS + 16 * u + 2 * g) = make_float2(o[u][i] * f, o[u][2 + i] * f);
+      }
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < 8 * (D / 4); e += kChunkThreads) {
+    const int r = e / (D / 4), d = (e % (D / 4)) * 4, tk = r / G;
+    if (tk >= t.ntok || r >= p.tile_tokens * G) continue;
+    float M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) M = fmaxf(M, msh[8 * k + r]);
+    float L = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float w = chunk_weight(msh[8 * k + r], lsh[8 * k + r], M);
+      const float4 v = *reinterpret_cast<const float4*>(osh + (8 * k + r) * C::OS + d);
+      L = fmaf(w, lsh[8 * k + r], L);
+      x[0] = fmaf(w, v.x, x[0]); x[1] = fmaf(w, v.y, x[1]);
+      x[2] = fmaf(w, v.z, x[2]); x[3] = fmaf(w, v.w, x[3]);
+    }
+    chunk_store(p, (int64_t)(t.row0 + tk) * p.q_heads + hk * G + (r - tk * G), split, D, d, x, M, L);
+  }
+}
+
+template <int D, int KE, int VE>
+static cudaError_t launch_one(const ChunkParams& p, dim3 grid, cudaStream_t st) {
+  constexpr int smem = RowsCfg<D, KE, VE>::BYTES;
+  const cudaError_t e = ensure_smem_optin((const void*)chunk_rows<D, KE, VE>, smem);
+  if (e != cudaSuccess) return e;
+  chunk_rows<D, KE, VE><<<grid, kChunkThreads, smem, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_types(const ChunkParams& p, int dtype, dim3 grid, cudaStream_t st) {
+  if constexpr (D == 128)     // (MXFP8 keys are built for head_dim 128)
+    if (dtype == FP8KV_MXK8V8) return launch_one<D, ELEM_MX, ELEM_E4M3>(p, grid, st);
+  if (dtype == FP8KV_K8V8) return launch_one<D, ELEM_E4M3, ELEM_E4M3>(p, grid, st);
+  if (dtype == FP8KV_K16V8) return launch_one<D, ELEM_BF16, ELEM_E4M3>(p, grid, st);
+  if (dtype == FP8KV_K8V16) return launch_one<D, ELEM_E4M3, ELEM_BF16>(p, grid, st);
+  return launch_one<D, ELEM_BF16, ELEM_BF16>(p, grid, st);
+}
+
+cudaError_t launch_chunk_rows(const ChunkParams& p, int dtype, int tiles, cudaStream_t st) {
+  const dim3 grid(tiles, p.c.kv_heads, p.num_splits);
+  return p.c.head_dim == 128 ? launch_types<128>(p, dtype, grid, st) : launch_types<64>(p, dtype, grid, st);
+}
+
+}  // namespace fp8kv

@@ -131,7 +131,7 @@ def test_python_argument_checks():
     """The binding turns wrong tensors down by name."""
     t = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError, match="pos: expected a contiguous CUDA"):
-        fk._here(t, torch.int32, "pos")
+        fk._here(t, torch.int32, "pos", 0)
     with pytest.raises(ValueError, match="free_pages and free_head"):
         cache = type("C", (), dict(layout=fk.LAYOUT_PAGED, batch=4))()
         fk.fp8kv_build_tables(cache, t, t, 4)
