@@ -15,6 +15,8 @@
 // Arithmetic as in chunk_mma.cu: f16 operands for e4m3 sides (codes exact,
 // query scaled by a power of two, P by 2^-kp and the value scale), bf16 for
 // bf16 sides, m, l and O in fp32.
+#include <cfloat>
+
 #include "chunk_common.cuh"
 
 namespace fp8kv {
@@ -38,6 +40,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
   return y;
+}
+
+__device__ __forceinline__ void cp_async16_u(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
 
 template <int D, int KE, int VE>
@@ -78,19 +84,38 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows(const ChunkParams p)
         if (!ok && lane == 0) raise_error(p.err, FP8KV_DEVERR_BAD_PAGE);
         row = ((int64_t)(ok ? page : 0) * c.kv_heads + hk) * c.page_size + (key0 & (c.page_size - 1));
       }
-      // rows nobody sees are zero-filled, not read: they may hold anything
-      auto live = [&](int r) { return ok && key0 + r < t.kv_end && (key0 + r >= t.lo || key0 + r < p.sinks); };
       const uint32_t ks = umma::smem_u32(ring + (it % C::NS) * C::STAGE), vs = ks + kRowKeys * C::KB, sc = vs + kRowKeys * C::VB;
       constexpr int KC = C::KB / 16, VC = C::VB / 16;
+      // the 16 rows lie together: chunk e of the group is 16 e bytes from its start
+      const uint8_t* ksrc = c.k + row * C::KB + lane * 16;
+      const uint8_t* vsrc = c.v + row * C::VB + lane * 16;
+      // rows nobody sees are zero-filled, not read: they may hold anything
+      const bool whole = ok && key0 + kRowKeys <= t.kv_end && (key0 >= t.lo || key0 + kRowKeys <= p.sinks);
+      auto live = [&](int r) {
+        return whole || (ok && key0 + r < t.kv_end && (key0 + r >= t.lo || key0 + r < p.sinks));
+      };
+      if (whole) {
 #pragma unroll
-      for (int i = 0; i < KC / 2; ++i) {
-        const int e = lane + 32 * i, r = e / KC, ch = e % KC;
-        cp_async16_z(ks + r * C::KB + k_chunk<KE, C::KB>(ch, r) * 16, c.k + (row + r) * C::KB + ch * 16, live(r));
-      }
+        for (int i = 0; i < KC / 2; ++i) {
+          const int e = lane + 32 * i, r = e / KC, ch = e % KC;
+          cp_async16_u(ks + r * C::KB + k_chunk<KE, C::KB>(ch, r) * 16, ksrc + 512 * i);
+        }
 #pragma unroll
-      for (int i = 0; i < VC / 2; ++i) {
-        const int e = lane + 32 * i, r = e / VC, ch = e % VC;
-        cp_async16_z(vs + r * C::VB + v_chunk<C::VB>(ch, r) * 16, c.v + (row + r) * C::VB + ch * 16, live(r));
+        for (int i = 0; i < VC / 2; ++i) {
+          const int e = lane + 32 * i, r = e / VC, ch = e % VC;
+          cp_async16_u(vs + r * C::VB + v_chunk<C::VB>(ch, r) * 16, vsrc + 512 * i);
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < KC / 2; ++i) {
+          const int e = lane + 32 * i, r = e / KC, ch = e % KC;
+          cp_async16_z(ks + r * C::KB + k_chunk<KE, C::KB>(ch, r) * 16, ksrc + 512 * i, live(r));
+        }
+#pragma unroll 1
+        for (int i = 0; i < VC / 2; ++i) {
+          const int e = lane + 32 * i, r = e / VC, ch = e % VC;
+          cp_async16_z(vs + r * C::VB + v_chunk<C::VB>(ch, r) * 16, vsrc + 512 * i, live(r));
+        }
       }
       const int r = lane & 15;
       if (lane < 16 ? !KB16 : !VB16) cp_async4_z(sc + lane * 4, (lane < 16 ? c.k_scale : c.v_scale) + row + r, live(r));
@@ -158,8 +183,10 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows(const ChunkParams p)
   for (int u = 0; u < KS; ++u)
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[u][e] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  int kp[2] = {-1000, -1000};
+  // the reference maximum, the sum in units of 2^m, -m - kp, 2^kp, and the
+  // value scale from which on kp has to rise
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, neg_m[2] = {0.f, 0.f}, up2[2] = {1.f, 1.f};
+  float vm_top[2] = {FLT_MIN, FLT_MIN};
 
 #pragma unroll 1
   for (int it = 0; it < n; ++it) {
@@ -238,48 +265,51 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows(const ChunkParams p)
     for (int x = 4; x < 32; x <<= 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i) mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], x));
-    float alpha[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float mn = fmaxf(m[i], mt[i]), ref = mn == -INFINITY ? 0.f : mn;
-      alpha[i] = m[i] == -INFINITY ? 1.f : ex2_ftz(m[i] - ref);
-      m[i] = mn;
-      s[i] = ex2_ftz(s[i] - ref);
-      s[2 + i] = ex2_ftz(s[2 + i] - ref);
-      l[i] = l[i] * alpha[i] + (s[i] + s[2 + i]);
-    }
-    if constexpr (!VB16) {
-      const float v0 = vsc[g], v1 = vsc[g + 8];
-      auto finite = [](float v) { return v < INFINITY ? v : 0.f; };
-      float vm[2];
-      if (!part) {
-        vm[0] = vm[1] = warp_max_f32(fmaxf(finite(v0), finite(v1)));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) vm[i] = fmaxf(see[i] ? finite(v0) : 0.f, see[2 + i] ? finite(v1) : 0.f);
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) vm[i] = fmaxf(vm[i], __shfl_xor_sync(0xffffffffu, vm[i], x));
-      }
+    // The reference moves only when the maximum grows by more than 2^8, kp only
+    // up, and O with them: rare behind the first groups, one vote skips it.
+    const float v0 = VB16 ? 0.f : vsc[g], v1 = VB16 ? 0.f : vsc[g + 8];
+    bool moved = mt[0] > m[0] + 8.f || mt[1] > m[1] + 8.f;
+    if constexpr (!VB16) moved = moved || fmaxf(v0, v1) >= fminf(vm_top[0], vm_top[1]);
+    if (__any_sync(0xffffffffu, moved)) {
+      float alpha[2] = {1.f, 1.f};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int need = max(-100, min(100, ((__float_as_int(vm[i]) >> 23) & 0xFF) - 127 - 14));   // vm 2^-need < 2^15
-        if (vm[i] > 0.f && need > kp[i]) {
-          if (kp[i] > -1000) alpha[i] *= pow2_diff((float)(kp[i] - need), 0);
-          kp[i] = need;
+        if (mt[i] > m[i] + 8.f) {
+          alpha[i] = ex2(m[i] - mt[i]);        // (0 for the first)
+          m[i] = mt[i];
+          l[i] *= alpha[i];
         }
-        const float vf = kp[i] > -1000 ? pow2i(-kp[i]) : 1.f;
-        // (an unseen key's scale may be anything)
-        s[i] = see[i] ? s[i] * (v0 * vf) : 0.f;
-        s[2 + i] = see[2 + i] ? s[2 + i] * (v1 * vf) : 0.f;
+        if constexpr (!VB16) {                 // the largest finite value scale among the keys the query sees
+          float vm = fmaxf(see[i] && v0 < INFINITY ? v0 : 0.f, see[2 + i] && v1 < INFINITY ? v1 : 0.f);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, x));
+          if (vm >= vm_top[i]) {
+            const int need = max(-100, min(100, ((__float_as_int(vm) >> 23) & 0xFF) - 127 - 6));   // vm 2^-need < 2^7
+            alpha[i] *= pow2i(max(-126, (__float_as_int(up2[i]) >> 23) - 127 - need));
+            up2[i] = pow2i(need);
+            vm_top[i] = pow2i(need + 7);
+          }
+        }
+        neg_m[i] = (m[i] == -INFINITY ? 0.f : -m[i]) - (float)((__float_as_int(up2[i]) >> 23) - 127);
       }
-    }
-    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
       for (int u = 0; u < KS; ++u) {
         o[u][0] *= alpha[0]; o[u][1] *= alpha[1];
         o[u][2] *= alpha[0]; o[u][3] *= alpha[1];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      s[i] = ex2_ftz(s[i] + neg_m[i]);
+      s[2 + i] = ex2_ftz(s[2 + i] + neg_m[i]);
+      l[i] = fmaf(s[i] + s[2 + i], up2[i], l[i]);
+      if constexpr (!VB16) {
+        s[i] *= v0;
+        s[2 + i] *= v1;
+        if (part) {                            // an unseen key's scale may be anything
+          s[i] = see[i] ? s[i] : 0.f;
+          s[2 + i] = see[2 + i] ? s[2 + i] : 0.f;
+        }
       }
     }
     // P^T as a B fragment: keys 2 c4, + 1 (and + 8) of query g
@@ -376,12 +406,12 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_rows(const ChunkParams p)
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = warp * 8 + 2 * c4 + i;
-    const float f = !VB16 && kp[i] > -1000 ? pow2i(kp[i]) : 1.f;
+    const float f = up2[i];
     if (g == 0) { msh[r] = m[i]; lsh[r] = l[i]; }
 #pragma unroll
     for (int u = 0; u < KS; ++u) {
       if constexpr (VB16) {
-        osh[r * C::OS + 16 * u + g] = o[u][i];
+        osh[r * C::OS + 16 * u + g] = o[u][i];      // (2^kp is 1)
         osh[r * C::OS + 16 * u + 8 + g] = o[u][2 + i];
       } else {
         *reinterpret_cast<float2*>(osh + r * C::OS + 16 * u + 2 * g) = make_float2(o[u][i] * f, o[u][2 + i] * f);
