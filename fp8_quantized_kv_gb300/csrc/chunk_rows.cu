@@ -28,7 +28,7 @@ struct RowsCfg {
   static constexpr int KB = KE == ELEM_BF16 ? 2 * D : D;
   static constexpr int VB = VE == ELEM_BF16 ? 2 * D : D;
   static constexpr int STAGE = kRowKeys * (KB + VB) + 2 * kRowKeys * 4;    // rows, key scales, value scales
-  static constexpr int NS = KB + VB > 256 ? 3 : 4;
+  static constexpr int NS = KB + VB > 256 ? 2 : 3;
   static constexpr int OS = D + 4;
   static constexpr int JOIN = 32 * OS * 4 + 2 * 32 * 4;
   static constexpr int RING = 4 * NS * STAGE;
@@ -47,7 +47,7 @@ __device__ __forceinline__ void cp_async16_u(uint32_t dst, const void* src) {
 }
 
 template <int D, int KE, int VE>
-__global__ void __launch_bounds__(kChunkThreads) chunk_rows(const ChunkParams p) {
+__global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams p) {
   using C = RowsCfg<D, KE, VE>;
   constexpr bool KB16 = KE == ELEM_BF16, VB16 = VE == ELEM_BF16;
   constexpr int KS = D / 16;                   // k steps of QK, m tiles of PV

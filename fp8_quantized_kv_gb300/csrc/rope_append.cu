@@ -19,8 +19,7 @@
 
 namespace fp8kv {
 
-__device__ __forceinline__ void load4(const __nv_bfloat16* src, float (&x)[4]) {
-  const uint2 u = *reinterpret_cast<const uint2*>(src);
+__device__ __forceinline__ void unpack4(uint2 u, float (&x)[4]) {
   x[0] = __uint_as_float(u.x << 16);
   x[1] = __uint_as_float(u.x & 0xFFFF0000u);
   x[2] = __uint_as_float(u.y << 16);
@@ -98,27 +97,30 @@ __device__ __forceinline__ void store_row(uint8_t* base, float* scales, int64_t 
 }
 
 // One warp per (token, group of row passes); a pass is 256 / D rows of one
-// kind (queries, keys or values).
-template <int D, int KE, int VE>
+// kind (queries, keys or values).  UR passes are loaded before the first is
+// used, so a warp keeps UR x 512 bytes in flight.
+template <int D, int KE, int VE, int UR>
 __global__ void __launch_bounds__(256) rope_append_kernel(const RopeAppendParams p) {
   constexpr int LPR = D / 8, RPP = 32 / LPR;      // lanes per row, rows per pass
   const int lane = threadIdx.x & 31, s = lane & (LPR - 1), sub = lane / LPR;
   const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int64_t tok = w / p.groups;
+  const int64_t tok = p.groups == 1 ? w : w / p.groups;
   const int grp = (int)(w - tok * p.groups);
   if (tok >= p.n) return;
   const int64_t slot = p.slots[tok];
+  const int t = p.pos[tok];
   if (slot < 0) return;                            // padding: nothing of the row is read or written
   const CacheView& c = p.c;
-  const int t = p.pos[tok];
-  const int span = c.paged ? c.page_size : c.max_tokens;
-  const int64_t unit = slot / span;
-  const int off = (int)(slot - unit * span);
-  const bool bad_slot = unit >= (c.paged ? c.num_pages : c.batch);
+  // (a cache has fewer than 2^31 rows, so a slot inside it fits 32 bits)
+  const int64_t slots = c.paged ? (int64_t)c.num_pages << c.page_shift : (int64_t)c.batch * c.max_tokens;
+  const bool bad_slot = slot >= slots;
   if (t < 0 || t >= p.positions || bad_slot) {
     if (lane == 0) raise_error(p.err, bad_slot ? FP8KV_DEVERR_BAD_PAGE : FP8KV_DEVERR_SEQ_TOO_LONG);
     return;
   }
+  const unsigned span = c.paged ? c.page_size : c.max_tokens;
+  const unsigned unit = c.paged ? (unsigned)slot >> c.page_shift : (unsigned)slot / span;
+  const unsigned off = (unsigned)slot - unit * span;
   const int R8 = p.rot >> 3;
   const bool turn = s < R8;
   const int d0 = turn && !p.interleaved ? 4 * s : 8 * s;
@@ -131,71 +133,92 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeAppendParams
   }
   const int pq = (p.q_heads + RPP - 1) / RPP, pk = (c.kv_heads + RPP - 1) / RPP;
   const int end = min(pq + 2 * pk, (grp + 1) * p.per_group);
-  for (int pass = grp * p.per_group; pass < end; ++pass) {
-    const int kind = pass < pq ? 0 : pass < pq + pk ? 1 : 2;
-    const int h0 = (kind == 0 ? pass : kind == 1 ? pass - pq : pass - pq - pk) * RPP + sub;
-    const int heads = kind == 0 ? p.q_heads : c.kv_heads;
-    const bool live = h0 < heads;
-    const int h = live ? h0 : heads - 1;
-    const __nv_bfloat16* src = (kind == 0 ? p.q + tok * p.q_stride : kind == 1 ? p.k + tok * p.k_stride
-                                                                               : p.v + tok * p.v_stride) + h * D;
-    float x[4], y[4];
-    load4(src + d0, x);
-    load4(src + d1, y);
-    if (kind < 2 && turn) {
-      if (p.interleaved) {
-        rotate1(x[0], x[1], cs.x, sn.x);
-        rotate1(x[2], x[3], cs.y, sn.y);
-        rotate1(y[0], y[1], cs.z, sn.z);
-        rotate1(y[2], y[3], cs.w, sn.w);
-      } else {
-        rotate1(x[0], y[0], cs.x, sn.x);
-        rotate1(x[1], y[1], cs.y, sn.y);
-        rotate1(x[2], y[2], cs.z, sn.z);
-        rotate1(x[3], y[3], cs.w, sn.w);
-      }
-    }
-    if (kind == 0) {
-      __nv_bfloat16* out = p.q_out + (tok * p.q_heads + h) * D;
-      __syncwarp();                                // q_out may be q itself: the row is read before it is written
-      if (live) { store4(out + d0, x); store4(out + d1, y); }
-      continue;
-    }
-    const int64_t dst = (unit * c.kv_heads + h) * span + off;
-    if (kind == 1) {
-      if (KE == ELEM_E4M3 && c.k_bias != nullptr) {
+  const __nv_bfloat16 *qrow = p.q + tok * p.q_stride, *krow = p.k + tok * p.k_stride, *vrow = p.v + tok * p.v_stride;
+  for (int pass0 = grp * p.per_group; pass0 < end; pass0 += UR) {
+    uint2 raw[UR][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] -= c.rope_cos != nullptr ? rope_bias(c, h, t, d0 + i) : c.k_bias[h * D + d0 + i];
-          y[i] -= c.rope_cos != nullptr ? rope_bias(c, h, t, d1 + i) : c.k_bias[h * D + d1 + i];
+    for (int u = 0; u < UR; ++u) {
+      const int pass = min(pass0 + u, end - 1);
+      const int kind = pass < pq ? 0 : pass < pq + pk ? 1 : 2;
+      const int h0 = (kind == 0 ? pass : kind == 1 ? pass - pq : pass - pq - pk) * RPP + sub;
+      const int h = min(h0, (kind == 0 ? p.q_heads : c.kv_heads) - 1);
+      const __nv_bfloat16* src = (kind == 0 ? qrow : kind == 1 ? krow : vrow) + h * D;
+      raw[u][0] = *reinterpret_cast<const uint2*>(src + d0);
+      raw[u][1] = *reinterpret_cast<const uint2*>(src + d1);
+    }
+    __syncwarp();                                  // q_out may be q itself: rows are read before they are written
+#pragma unroll
+    for (int u = 0; u < UR; ++u) {
+      const int pass = pass0 + u;
+      if (pass >= end) break;
+      const int kind = pass < pq ? 0 : pass < pq + pk ? 1 : 2;
+      const int h = (kind == 0 ? pass : kind == 1 ? pass - pq : pass - pq - pk) * RPP + sub;
+      const bool live = h < (kind == 0 ? p.q_heads : c.kv_heads);
+      float x[4], y[4];
+      unpack4(raw[u][0], x);
+      unpack4(raw[u][1], y);
+      if (kind < 2 && turn) {
+        if (p.interleaved) {
+          rotate1(x[0], x[1], cs.x, sn.x);
+          rotate1(x[2], x[3], cs.y, sn.y);
+          rotate1(y[0], y[1], cs.z, sn.z);
+          rotate1(y[2], y[3], cs.w, sn.w);
+        } else {
+          rotate1(x[0], y[0], cs.x, sn.x);
+          rotate1(x[1], y[1], cs.y, sn.y);
+          rotate1(x[2], y[2], cs.z, sn.z);
+          rotate1(x[3], y[3], cs.w, sn.w);
         }
       }
-      store_row<D, KE>(const_cast<uint8_t*>(c.k), const_cast<float*>(c.k_scale), dst, d0, d1, x, y, live);
-    } else {
-      store_row<D, VE>(const_cast<uint8_t*>(c.v), const_cast<float*>(c.v_scale), dst, d0, d1, x, y, live);
+      if (kind == 0) {
+        if (live) {
+          __nv_bfloat16* out = p.q_out + (tok * p.q_heads + h) * D;
+          store4(out + d0, x);
+          store4(out + d1, y);
+        }
+        continue;
+      }
+      const int64_t dst = ((int64_t)unit * c.kv_heads + h) * span + off;
+      if (kind == 1) {
+        if (KE == ELEM_E4M3 && c.k_bias != nullptr && live) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] -= c.rope_cos != nullptr ? rope_bias(c, h, t, d0 + i) : c.k_bias[h * D + d0 + i];
+            y[i] -= c.rope_cos != nullptr ? rope_bias(c, h, t, d1 + i) : c.k_bias[h * D + d1 + i];
+          }
+        }
+        store_row<D, KE>(const_cast<uint8_t*>(c.k), const_cast<float*>(c.k_scale), dst, d0, d1, x, y, live);
+      } else {
+        store_row<D, VE>(const_cast<uint8_t*>(c.v), const_cast<float*>(c.v_scale), dst, d0, d1, x, y, live);
+      }
     }
   }
+}
+
+template <int D, int KE, int VE>
+static cudaError_t launch_one(const RopeAppendParams& p, unsigned grid, cudaStream_t s) {
+  if (p.per_group == 1) rope_append_kernel<D, KE, VE, 1><<<grid, 256, 0, s>>>(p);
+  else rope_append_kernel<D, KE, VE, 4><<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError();
 }
 
 template <int D>
 static cudaError_t dispatch(const RopeAppendParams& p, int dtype, unsigned grid, cudaStream_t s) {
   if constexpr (D == 128)
-    if (dtype == FP8KV_MXK8V8) {
-      rope_append_kernel<D, ELEM_MX, ELEM_E4M3><<<grid, 256, 0, s>>>(p);
-      return cudaGetLastError();
-    }
-  if (dtype == FP8KV_K8V8) rope_append_kernel<D, ELEM_E4M3, ELEM_E4M3><<<grid, 256, 0, s>>>(p);
-  else if (dtype == FP8KV_K16V8) rope_append_kernel<D, ELEM_BF16, ELEM_E4M3><<<grid, 256, 0, s>>>(p);
-  else if (dtype == FP8KV_K8V16) rope_append_kernel<D, ELEM_E4M3, ELEM_BF16><<<grid, 256, 0, s>>>(p);
-  else rope_append_kernel<D, ELEM_BF16, ELEM_BF16><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+    if (dtype == FP8KV_MXK8V8) return launch_one<D, ELEM_MX, ELEM_E4M3>(p, grid, s);
+  if (dtype == FP8KV_K8V8) return launch_one<D, ELEM_E4M3, ELEM_E4M3>(p, grid, s);
+  if (dtype == FP8KV_K16V8) return launch_one<D, ELEM_BF16, ELEM_E4M3>(p, grid, s);
+  if (dtype == FP8KV_K8V16) return launch_one<D, ELEM_E4M3, ELEM_BF16>(p, grid, s);
+  return launch_one<D, ELEM_BF16, ELEM_BF16>(p, grid, s);
 }
 
 cudaError_t launch_rope_append(RopeAppendParams& p, int dtype, cudaStream_t s) {
   if (p.n == 0) return cudaSuccess;
   const int rpp = 256 / p.c.head_dim;
   const int passes = (p.q_heads + rpp - 1) / rpp + 2 * ((p.c.kv_heads + rpp - 1) / rpp);
-  p.per_group = 1;
+  // few tokens: a warp per pass, as many warps as there is work; many: eight
+  // passes a warp, which shares the token's table row among them
+  p.per_group = p.n * passes <= 64 * (int64_t)sm_count() ? 1 : 8;
   p.groups = (passes + p.per_group - 1) / p.per_group;
   const int64_t warps = p.n * p.groups;
   const unsigned grid = (unsigned)((warps + 7) / 8);

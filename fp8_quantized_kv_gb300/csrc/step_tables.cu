@@ -194,8 +194,11 @@ cudaError_t launch_build_tables(const CacheView& c, const int32_t* cached, const
 // With w_i in turns as a 64-bit binary fraction W_i (host, fp64), the phase
 // t W_i mod 2^64 is exact integer arithmetic: far positions lose nothing but
 // t 2^-56 turns, the rounding of W_i itself.  Its top two bits (after adding
-// an eighth of a turn) pick the quadrant, the rest is an angle in
-// [-pi/4, pi/4] whose sine and cosine are taken in fp32.
+// an eighth of a turn) pick the quadrant; the rest is an angle x in
+// [-pi/4, pi/4], and there the Taylor polynomials through x^9 and x^10 are
+// within 2^-28 and 2^-31 of sine and cosine, so rounding to fp32 is what is
+// left.  A thread keeps VEC pairs and walks down the positions: the tables are
+// written once, 16 bytes a thread, and nothing is read.
 struct RopeTablesParams {
   unsigned long long w[kRopeMaxPairs];
   float *cos, *sin;
@@ -203,19 +206,37 @@ struct RopeTablesParams {
   int positions, pairs;
 };
 
+__device__ __forceinline__ void sincos_phase(unsigned int phase, float amplitude, float& c, float& s) {
+  const unsigned int quad = (phase + 0x20000000u) >> 30;
+  const float x = (float)(int)(phase - (quad << 30)) * 1.4629180792671596e-09f;      // 2 pi / 2^32
+  const float z = x * x;
+  const float sn = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 2.7557319e-6f, -1.9841270e-4f), 8.3333333e-3f), -1.6666667e-1f), x);
+  const float cs = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.7557319e-7f, 2.4801587e-5f), -1.3888889e-3f), 4.1666667e-2f), -0.5f), 1.f);
+  const float a = quad & 1 ? sn : cs, b = quad & 1 ? cs : sn;
+  c = (quad == 1 || quad == 2 ? -a : a) * amplitude;
+  s = (quad & 2 ? -b : b) * amplitude;
+}
+
+template <int VEC>
 __global__ void __launch_bounds__(256) rope_tables_kernel(const __grid_constant__ RopeTablesParams p) {
-  const long long n = (long long)p.positions * p.pairs;
-  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (long long)gridDim.x * blockDim.x) {
-    const int t = (int)(e / p.pairs), i = (int)(e - (long long)t * p.pairs);
-    const unsigned int phase = (unsigned int)(((unsigned long long)(unsigned int)t * p.w[i]) >> 32);
-    const unsigned int quad = (phase + 0x20000000u) >> 30;
-    const int rest = (int)(phase - (quad << 30));
-    float sn, cs;
-    sincosf((float)rest * 1.4629180792671596e-09f, &sn, &cs);      // 2 pi / 2^32
-    const float c = quad == 0 ? cs : quad == 1 ? -sn : quad == 2 ? -cs : sn;
-    const float s = quad == 0 ? sn : quad == 1 ? cs : quad == 2 ? -sn : -cs;
-    p.cos[e] = c * p.amplitude;
-    p.sin[e] = s * p.amplitude;
+  const int cols = p.pairs / VEC;                  // threads along a position
+  const int col = threadIdx.x % cols, rows = blockDim.x / cols;
+  if (threadIdx.x >= cols * rows) return;
+  unsigned long long w[VEC];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) w[k] = p.w[VEC * col + k];
+  for (long long t = (long long)blockIdx.x * rows + threadIdx.x / cols; t < p.positions; t += (long long)gridDim.x * rows) {
+    float c[VEC], s[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) sincos_phase((unsigned int)(((unsigned long long)t * w[k]) >> 32), p.amplitude, c[k], s[k]);
+    const long long at = t * p.pairs + VEC * col;
+    if constexpr (VEC == 4) {
+      *reinterpret_cast<float4*>(p.cos + at) = make_float4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<float4*>(p.sin + at) = make_float4(s[0], s[1], s[2], s[3]);
+    } else {
+      p.cos[at] = c[0];
+      p.sin[at] = s[0];
+    }
   }
 }
 
@@ -229,8 +250,13 @@ cudaError_t launch_rope_tables(int positions, int pairs, const unsigned long lon
   p.amplitude = amplitude;
   p.positions = positions;
   p.pairs = pairs;
-  const long long blocks = ((long long)positions * pairs + 255) / 256;
-  rope_tables_kernel<<<(unsigned)(blocks < 4864 ? blocks : 4864), 256, 0, s>>>(p);
+  // 16-byte stores where every row of the tables starts on one
+  const bool vec = pairs % 4 == 0 && (((uintptr_t)cos | (uintptr_t)sin) & 15) == 0;
+  const int rows = 256 / (vec ? pairs / 4 : pairs);
+  const long long blocks = ((long long)positions + rows - 1) / rows, most = 8LL * sm_count();
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+  if (vec) rope_tables_kernel<4><<<grid, 256, 0, s>>>(p);
+  else rope_tables_kernel<1><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
