@@ -68,7 +68,8 @@ struct RopeAppendParams {
   unsigned int* err;
   int64_t n, q_stride, k_stride, v_stride;
   int q_heads, rot, positions, interleaved;
-  int groups, per_group;            // warps per token, row passes per warp
+  int groups, q_groups, k_groups;   // warps per token: of queries, of keys (and as many of values)
+  int q_per, k_per;                 // row passes per warp
 };
 
 struct ChunkParams {

@@ -96,21 +96,42 @@ __device__ __forceinline__ void store_row(uint8_t* base, float* scales, int64_t 
   }
 }
 
-// One warp per (token, group of row passes); a pass is 256 / D rows of one
-// kind (queries, keys or values).  UR passes are loaded before the first is
-// used, so a warp keeps UR x 512 bytes in flight.
-template <int D, int KE, int VE, int UR>
+// A pass is 256 / D rows of one kind; a warp takes up to QU passes of a token's
+// queries, or up to KU of its keys or of its values.  All its rows are loaded
+// before the token's slot and position have arrived (a padding row is loaded
+// and dropped): two memory latencies a warp, the second for the table row.
+template <int D, int KE, int VE, int QU, int KU>
 __global__ void __launch_bounds__(256) rope_append_kernel(const RopeAppendParams p) {
   constexpr int LPR = D / 8, RPP = 32 / LPR;      // lanes per row, rows per pass
   const int lane = threadIdx.x & 31, s = lane & (LPR - 1), sub = lane / LPR;
   const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int64_t tok = p.groups == 1 ? w : w / p.groups;
-  const int grp = (int)(w - tok * p.groups);
+  const int64_t tok = w / p.groups;
   if (tok >= p.n) return;
+  const CacheView& c = p.c;
+  // which rows: groups of queries, then of keys, then of values
+  int grp = (int)(w - tok * p.groups);
+  const int kind = grp < p.q_groups ? 0 : grp < p.q_groups + p.k_groups ? 1 : 2;
+  if (kind > 0) grp -= p.q_groups + (kind - 1) * p.k_groups;
+  const int heads = kind == 0 ? p.q_heads : c.kv_heads;
+  const int h0 = grp * (kind == 0 ? p.q_per : p.k_per) * RPP + sub;              // first row of this lane
+  const int h1 = min(heads, (grp + 1) * (kind == 0 ? p.q_per : p.k_per) * RPP);   // rows of the group end here
+  const __nv_bfloat16* src = (kind == 0 ? p.q + tok * p.q_stride : kind == 1 ? p.k + tok * p.k_stride
+                                                                             : p.v + tok * p.v_stride) + h0 * D;
+  const int R8 = p.rot >> 3;
+  const bool turn = s < R8 && kind < 2;
+  const int d0 = turn && !p.interleaved ? 4 * s : 8 * s;
+  const int d1 = turn && !p.interleaved ? 4 * s + (p.rot >> 1) : 8 * s + 4;
+  constexpr int U = QU > KU ? QU : KU;
+  uint2 raw[U][2];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const bool in = h0 + u * RPP < h1;
+    raw[u][0] = in ? *reinterpret_cast<const uint2*>(src + u * RPP * D + d0) : make_uint2(0, 0);
+    raw[u][1] = in ? *reinterpret_cast<const uint2*>(src + u * RPP * D + d1) : make_uint2(0, 0);
+  }
   const int64_t slot = p.slots[tok];
   const int t = p.pos[tok];
-  if (slot < 0) return;                            // padding: nothing of the row is read or written
-  const CacheView& c = p.c;
+  if (slot < 0) return;                            // padding
   // (a cache has fewer than 2^31 rows, so a slot inside it fits 32 bits)
   const int64_t slots = c.paged ? (int64_t)c.num_pages << c.page_shift : (int64_t)c.batch * c.max_tokens;
   const bool bad_slot = slot >= slots;
@@ -118,87 +139,72 @@ __global__ void __launch_bounds__(256) rope_append_kernel(const RopeAppendParams
     if (lane == 0) raise_error(p.err, bad_slot ? FP8KV_DEVERR_BAD_PAGE : FP8KV_DEVERR_SEQ_TOO_LONG);
     return;
   }
-  const unsigned span = c.paged ? c.page_size : c.max_tokens;
-  const unsigned unit = c.paged ? (unsigned)slot >> c.page_shift : (unsigned)slot / span;
-  const unsigned off = (unsigned)slot - unit * span;
-  const int R8 = p.rot >> 3;
-  const bool turn = s < R8;
-  const int d0 = turn && !p.interleaved ? 4 * s : 8 * s;
-  const int d1 = turn && !p.interleaved ? 4 * s + (p.rot >> 1) : 8 * s + 4;
   float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
   if (turn) {
     const int64_t at = (int64_t)t * (p.rot >> 1) + 4 * s;
     cs = *reinterpret_cast<const float4*>(p.cos + at);
     sn = *reinterpret_cast<const float4*>(p.sin + at);
   }
-  const int pq = (p.q_heads + RPP - 1) / RPP, pk = (c.kv_heads + RPP - 1) / RPP;
-  const int end = min(pq + 2 * pk, (grp + 1) * p.per_group);
-  const __nv_bfloat16 *qrow = p.q + tok * p.q_stride, *krow = p.k + tok * p.k_stride, *vrow = p.v + tok * p.v_stride;
-  for (int pass0 = grp * p.per_group; pass0 < end; pass0 += UR) {
-    uint2 raw[UR][2];
-#pragma unroll
-    for (int u = 0; u < UR; ++u) {
-      const int pass = min(pass0 + u, end - 1);
-      const int kind = pass < pq ? 0 : pass < pq + pk ? 1 : 2;
-      const int h0 = (kind == 0 ? pass : kind == 1 ? pass - pq : pass - pq - pk) * RPP + sub;
-      const int h = min(h0, (kind == 0 ? p.q_heads : c.kv_heads) - 1);
-      const __nv_bfloat16* src = (kind == 0 ? qrow : kind == 1 ? krow : vrow) + h * D;
-      raw[u][0] = *reinterpret_cast<const uint2*>(src + d0);
-      raw[u][1] = *reinterpret_cast<const uint2*>(src + d1);
+  auto row = [&](int u, float (&x)[4], float (&y)[4]) {
+    unpack4(raw[u][0], x);
+    unpack4(raw[u][1], y);
+    if (!turn) return;
+    if (p.interleaved) {
+      rotate1(x[0], x[1], cs.x, sn.x);
+      rotate1(x[2], x[3], cs.y, sn.y);
+      rotate1(y[0], y[1], cs.z, sn.z);
+      rotate1(y[2], y[3], cs.w, sn.w);
+    } else {
+      rotate1(x[0], y[0], cs.x, sn.x);
+      rotate1(x[1], y[1], cs.y, sn.y);
+      rotate1(x[2], y[2], cs.z, sn.z);
+      rotate1(x[3], y[3], cs.w, sn.w);
     }
-    __syncwarp();                                  // q_out may be q itself: rows are read before they are written
+  };
+  if (kind == 0) {
+    // (q_out may be q itself: a lane writes the elements that it read)
+    __nv_bfloat16* dst = p.q_out + (tok * p.q_heads + h0) * D;
 #pragma unroll
-    for (int u = 0; u < UR; ++u) {
-      const int pass = pass0 + u;
-      if (pass >= end) break;
-      const int kind = pass < pq ? 0 : pass < pq + pk ? 1 : 2;
-      const int h = (kind == 0 ? pass : kind == 1 ? pass - pq : pass - pq - pk) * RPP + sub;
-      const bool live = h < (kind == 0 ? p.q_heads : c.kv_heads);
-      float x[4], y[4];
-      unpack4(raw[u][0], x);
-      unpack4(raw[u][1], y);
-      if (kind < 2 && turn) {
-        if (p.interleaved) {
-          rotate1(x[0], x[1], cs.x, sn.x);
-          rotate1(x[2], x[3], cs.y, sn.y);
-          rotate1(y[0], y[1], cs.z, sn.z);
-          rotate1(y[2], y[3], cs.w, sn.w);
-        } else {
-          rotate1(x[0], y[0], cs.x, sn.x);
-          rotate1(x[1], y[1], cs.y, sn.y);
-          rotate1(x[2], y[2], cs.z, sn.z);
-          rotate1(x[3], y[3], cs.w, sn.w);
-        }
+    for (int u = 0; u < QU; ++u)
+      if (h0 + u * RPP < h1) {
+        float x[4], y[4];
+        row(u, x, y);
+        store4(dst + u * RPP * D + d0, x);
+        store4(dst + u * RPP * D + d1, y);
       }
-      if (kind == 0) {
-        if (live) {
-          __nv_bfloat16* out = p.q_out + (tok * p.q_heads + h) * D;
-          store4(out + d0, x);
-          store4(out + d1, y);
-        }
-        continue;
-      }
-      const int64_t dst = ((int64_t)unit * c.kv_heads + h) * span + off;
-      if (kind == 1) {
-        if (KE == ELEM_E4M3 && c.k_bias != nullptr && live) {
+    return;
+  }
+  const unsigned span = c.paged ? c.page_size : c.max_tokens;
+  const unsigned unit = c.paged ? (unsigned)slot >> c.page_shift : (unsigned)slot / span;
+  const unsigned off = (unsigned)slot - unit * span;
+  // every lane of the warp takes part in a row's maximum
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] -= c.rope_cos != nullptr ? rope_bias(c, h, t, d0 + i) : c.k_bias[h * D + d0 + i];
-            y[i] -= c.rope_cos != nullptr ? rope_bias(c, h, t, d1 + i) : c.k_bias[h * D + d1 + i];
-          }
+  for (int u = 0; u < KU; ++u) {
+    const int h = h0 + u * RPP;
+    if (h - sub >= h1) break;
+    const bool live = h < h1;
+    const int64_t dst = ((int64_t)unit * c.kv_heads + h) * span + off;
+    float x[4], y[4];
+    row(u, x, y);
+    if (kind == 1) {
+      if (KE == ELEM_E4M3 && c.k_bias != nullptr && live) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] -= c.rope_cos != nullptr ? rope_bias(c, h, t, d0 + i) : c.k_bias[h * D + d0 + i];
+          y[i] -= c.rope_cos != nullptr ? rope_bias(c, h, t, d1 + i) : c.k_bias[h * D + d1 + i];
         }
-        store_row<D, KE>(const_cast<uint8_t*>(c.k), const_cast<float*>(c.k_scale), dst, d0, d1, x, y, live);
-      } else {
-        store_row<D, VE>(const_cast<uint8_t*>(c.v), const_cast<float*>(c.v_scale), dst, d0, d1, x, y, live);
       }
+      store_row<D, KE>(const_cast<uint8_t*>(c.k), const_cast<float*>(c.k_scale), dst, d0, d1, x, y, live);
+    } else {
+      store_row<D, VE>(const_cast<uint8_t*>(c.v), const_cast<float*>(c.v_scale), dst, d0, d1, x, y, live);
     }
   }
 }
 
 template <int D, int KE, int VE>
 static cudaError_t launch_one(const RopeAppendParams& p, unsigned grid, cudaStream_t s) {
-  if (p.per_group == 1) rope_append_kernel<D, KE, VE, 1><<<grid, 256, 0, s>>>(p);
-  else rope_append_kernel<D, KE, VE, 4><<<grid, 256, 0, s>>>(p);
+  if (p.q_per == 1 && p.k_per == 1) rope_append_kernel<D, KE, VE, 1, 1><<<grid, 256, 0, s>>>(p);
+  else rope_append_kernel<D, KE, VE, 8, 2><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -215,12 +221,17 @@ static cudaError_t dispatch(const RopeAppendParams& p, int dtype, unsigned grid,
 cudaError_t launch_rope_append(RopeAppendParams& p, int dtype, cudaStream_t s) {
   if (p.n == 0) return cudaSuccess;
   const int rpp = 256 / p.c.head_dim;
-  const int passes = (p.q_heads + rpp - 1) / rpp + 2 * ((p.c.kv_heads + rpp - 1) / rpp);
-  // few tokens: a warp per pass, as many warps as there is work; many: eight
-  // passes a warp, which shares the token's table row among them
-  p.per_group = p.n * passes <= 64 * (int64_t)sm_count() ? 1 : 8;
-  p.groups = (passes + p.per_group - 1) / p.per_group;
+  const int pq = (p.q_heads + rpp - 1) / rpp, pk = (p.c.kv_heads + rpp - 1) / rpp;
+  // few tokens: a warp per pass, as many warps as there is work; many: up to
+  // eight query passes or two key or value passes a warp
+  const bool few = p.n * (pq + 2 * pk) <= 64 * (int64_t)sm_count();
+  p.q_groups = few ? pq : (pq + 7) / 8;
+  p.k_groups = few ? pk : (pk + 1) / 2;
+  p.q_per = (pq + p.q_groups - 1) / p.q_groups;
+  p.k_per = (pk + p.k_groups - 1) / p.k_groups;
+  p.groups = p.q_groups + 2 * p.k_groups;
   const int64_t warps = p.n * p.groups;
+  if (warps > (int64_t)INT32_MAX * 8) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)((warps + 7) / 8);
   return p.c.head_dim == 128 ? dispatch<128>(p, dtype, grid, s) : dispatch<64>(p, dtype, grid, s);
 }

@@ -428,7 +428,7 @@ typedef enum {
  *   rot_dim:       a multiple of 8 from 8 to head_dim (else UNSUPPORTED)
  *   q_out:         [n][q_heads][head_dim] bf16; may be q itself if
  *                  q_stride = q_heads * head_dim
- * A row with a negative slot is padding: nothing of it is read or written.
+ * A row with a negative slot is padding: nothing is written for it.
  * A row whose position has no table entry or whose slot lies outside the
  * cache is skipped and raises SEQ_TOO_LONG or BAD_PAGE.  Two rows of one call
  * may not share a slot (which row's codes and scale stay is not defined). */
