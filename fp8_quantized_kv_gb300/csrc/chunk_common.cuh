@@ -97,12 +97,38 @@ __device__ __forceinline__ bool chunk_sees(const ChunkParams& p, int pos, int ke
   return key <= pos && (p.window <= 0 || key > pos - p.window || key < p.sinks);
 }
 
+// The 64 keys from key0 on that a query sees, as bits.
+__device__ __forceinline__ unsigned long long chunk_seen_mask(const ChunkParams& p, int pos, int key0) {
+  const int hi = min(pos - key0, 63);              // last key in reach
+  if (hi < 0) return 0;
+  const unsigned long long upto = ~0ull >> (63 - hi);
+  if (p.window <= 0) return upto;
+  const int lo = pos - p.window + 1 - key0, first = p.sinks - key0;
+  unsigned long long out = lo > 63 ? 0ull : ~0ull << max(lo, 0);
+  if (first > 0) out |= ~0ull >> (64 - min(first, 64));
+  return out & upto;
+}
+
 // Cache row of a key of the tile's sequence, or -1: a key that no query of
 // the tile can see (its row is never read: it may hold anything) or a bad
-// page (reported).
-__device__ __forceinline__ int chunk_row(const ChunkParams& p, const ChunkTile& t, int hk, int key) {
-  if (key >= t.kv_end || (key < t.lo && key >= p.sinks)) return -1;
-  return (int)cache_row(p.c, t.b, hk, key, p.err);
+// page (reported).  In two steps, so that the page id's latency can be spent
+// on other work: chunk_page fetches it, chunk_row makes the row of it.
+__device__ __forceinline__ bool chunk_wanted(const ChunkParams& p, const ChunkTile& t, int key) {
+  return key < t.kv_end && (key >= t.lo || key < p.sinks);
+}
+__device__ __forceinline__ int chunk_page(const ChunkParams& p, const ChunkTile& t, int key) {
+  if (!p.c.paged || !chunk_wanted(p, t, key)) return 0;
+  return p.c.page_table[(int64_t)t.b * p.c.max_pages_per_seq + (key >> p.c.page_shift)];
+}
+__device__ __forceinline__ int chunk_row(const ChunkParams& p, const ChunkTile& t, int hk, int key, int page) {
+  if (!chunk_wanted(p, t, key)) return -1;
+  const CacheView& c = p.c;
+  if (!c.paged) return (t.b * c.kv_heads + hk) * c.max_tokens + key;      // (rows of a cache fit 31 bits)
+  if (page < 0 || page >= c.num_pages) {
+    raise_error(p.err, FP8KV_DEVERR_BAD_PAGE);
+    return -1;
+  }
+  return (page * c.kv_heads + hk) * c.page_size + (key & (c.page_size - 1));
 }
 
 // Weight of a split's (m, l): zero for a split that saw nothing, NaN for one

@@ -65,9 +65,10 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
   const int j0 = min(t.n, split * per), nt = min(t.n, j0 + per) - j0;
   const int G = p.group;
 
-  auto find_rows = [&](int it) {               // threads 0..63
-    return it < nt ? chunk_row(p, t, hk, chunk_key0(t, j0 + it) + tid) : -1;
-  };
+  // threads 0..63: this thread's key of tile `it`, its page and its cache row
+  auto tile_key = [&](int it) { return chunk_key0(t, j0 + it) + tid; };
+  auto find_page = [&](int it) { return tid < kChunkKeys && it < nt ? chunk_page(p, t, tile_key(it)) : 0; };
+  auto find_row = [&](int it, int page) { return it < nt ? chunk_row(p, t, hk, tile_key(it), page) : -1; };
   auto issue = [&](int it) {
     if (it < nt) {
       uint8_t* st = csm + (it % C::NS) * C::STAGE;
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
 
   // prologue: cache rows of the first NS tiles, loads of the first NS - 1
   if (tid < kChunkKeys)
-    for (int it = 0; it < C::NS; ++it) rows_sh[(it & 3) * kChunkKeys + tid] = find_rows(it);
+    for (int it = 0; it < C::NS; ++it) rows_sh[(it & 3) * kChunkKeys + tid] = find_row(it, find_page(it));
   __syncthreads();
   for (int it = 0; it < C::NS - 1; ++it) issue(it);
 
@@ -170,7 +171,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
     cp_async_wait<C::NS - 2>();
     __syncthreads();                           // tile `it` has landed; every warp is done with tile it - 1
     issue(it + C::NS - 1);
-    const int next_row = tid < kChunkKeys ? find_rows(it + C::NS) : -1;
+    const int next_page = find_page(it + C::NS);
     const uint8_t* st = csm + (it % C::NS) * C::STAGE;
     const uint8_t* vst = st + kChunkKeys * C::KB;
     const float* ksc = reinterpret_cast<const float*>(vst + kChunkKeys * C::VB);
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
         }
       }
     }
-    if (tid < kChunkKeys) rows_sh[((it + C::NS) & 3) * kChunkKeys + tid] = next_row;
+    if (tid < kChunkKeys) rows_sh[((it + C::NS) & 3) * kChunkKeys + tid] = find_row(it + C::NS, next_page);
   }
 
 #pragma unroll

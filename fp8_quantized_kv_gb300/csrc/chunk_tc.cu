@@ -591,17 +591,18 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       float vm[2] = {vmt, vmt};                   // largest value scale that the row sees
       if (!chunk_all_seen(p, t, key0)) {          // some query of the tile does not see all of its keys
 #pragma unroll
-        for (int i = 0; i < 2; ++i) vm[i] = 0.f;
+        for (int i = 0; i < 2; ++i) {
+          const unsigned long long seen = chunk_seen_mask(p, qpos[i], key0) >> c2;
+          const uint32_t bits[2] = {(uint32_t)seen, (uint32_t)(seen >> 32)};
+          vm[i] = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 x = C::K16 ? *reinterpret_cast<const float2*>(kc + 8 * k) : make_float2(1.f, 1.f);
-          const float2 v = C::V16 ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(vc + 8 * k);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const bool a = chunk_sees(p, qpos[i], key0 + 8 * k + c2), b = chunk_sees(p, qpos[i], key0 + 8 * k + c2 + 1);
+          for (int k = 0; k < 8; ++k) {
+            const float2 x = C::K16 ? *reinterpret_cast<const float2*>(kc + 8 * k) : make_float2(1.f, 1.f);
+            const float2 v = C::V16 ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(vc + 8 * k);
+            const bool a = bits[k >> 2] & (1u << (8 * (k & 3))), b = bits[k >> 2] & (2u << (8 * (k & 3)));
             sv[i][k].x = a ? sv[i][k].x * x.x : -INFINITY;
             sv[i][k].y = b ? sv[i][k].y * x.y : -INFINITY;
-            vm[i] = fmaxf(vm[i], fmaxf(a ? v.x : 0.f, b ? v.y : 0.f));
+            if constexpr (!C::V16) vm[i] = fmaxf(vm[i], fmaxf(a ? v.x : 0.f, b ? v.y : 0.f));
           }
         }
         if constexpr (!C::V16) {
