@@ -44,9 +44,10 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
   const int T = p.tile_tokens, lane = threadIdx.x & 31;
   int b = x, q0 = x, q1 = x + 1, i0 = 0;           // one query per sequence
   if (p.cu_q == nullptr && x >= p.c.batch) return false;
+  int len = 0;
   if (p.cu_q != nullptr) {
     int lo = 0, n = p.c.batch;
-    while (n > 1) {
+    while (n > 32) {
       const int step = (n + 31) >> 5, at = lane * step;
       const bool le = at < n && (at == 0 || (long long)p.cu_q[lo + at] / T + lo + at <= x);
       // le is monotone for offsets that do not decrease; for others the
@@ -55,9 +56,15 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
       lo += k * step;
       n = min(step, n - k * step);
     }
-    b = lo;
-    q0 = p.cu_q[b];
-    q1 = p.cu_q[b + 1];
+    // the last step's lanes hold all there is to know of their sequence
+    const int at = min(lane, n - 1) + lo;
+    const int c0 = p.cu_q[at], c1 = p.cu_q[at + 1], ln = p.seq_lens[at];
+    const bool le = lane < n && (lane == 0 || (long long)c0 / T + at <= x);
+    const int k = max(__popc(__ballot_sync(0xffffffffu, le)), 1) - 1;
+    b = lo + k;
+    q0 = __shfl_sync(0xffffffffu, c0, k);
+    q1 = __shfl_sync(0xffffffffu, c1, k);
+    len = __shfl_sync(0xffffffffu, ln, k);
     if (q0 < 0 || q1 < q0 || q1 > p.total_q) {
       if (lead) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
       return false;
@@ -65,8 +72,9 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
     const long long i = ((long long)x - ((long long)q0 / T + b)) * T;
     if (i < 0 || i >= q1 - q0) return false;
     i0 = (int)i;
+  } else {
+    len = p.seq_lens[b];
   }
-  int len = p.seq_lens[b];
   if (len < 0 || len > cache_capacity(p.c)) {      // reported; the sequence's queries see nothing
     if (lead) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
     len = 0;

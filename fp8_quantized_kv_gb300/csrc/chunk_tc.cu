@@ -261,60 +261,69 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     *abort_flag = 0;
     umma::mbar_fence_init();
   }
+  // the first tiles' copies start before the query operand is made
+  constexpr int LEAD = C::KN - C::VN;
+  const int first_k = min(n, C::KN), first_v = min(n, C::VN);
+  if (warp == 10) {
+    __syncwarp();
+    for (int j = 0; j < first_k; ++j) load_tile(j, false, ids);
+    for (int j = 0; j < first_v; ++j) load_tile(j, true, ids);
+  }
   if (warp == 11) {
     umma::tmem_alloc(tslot, 256);
     umma::tmem_relinquish();
   }
-  // softmax warps: half of this thread's query row -> QK operand
-  const int r = tid & 127;                        // row of the tile, TMEM lane
-  const int tok = r / G;
-  const bool live = warp < 8 && tok < t.ntok && r < p.tile_tokens * G;
-  const int64_t qrow = live ? (int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G) : -1;
-  const int hf = (tid >> 7) & 1;                  // softmax warps: dims 64 hf .. of the query, of O
+  // softmax warps: query rows -> QK operand, 16 lanes a row (16 bytes each), so
+  // that a row is read in one piece; all eight loads of a thread in flight
+  const int hf = (tid >> 7) & 1;                  // softmax warps: which half of its lanes, and of O's dims
   if (warp < 8) {
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + (live ? qrow : 0) * D);
-    if constexpr (C::K16) {
+    const int ch = tid & 15;
+    uint4 x[8];
 #pragma unroll
-      for (int ch = 8 * hf; ch < 8 * hf + 8; ++ch) {
-        uint4 w = live && p.scale_log2 != 0.f ? src[ch] : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 8; ++i) {
+      const int row = 16 * i + (tid >> 4), tk = row / G;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (tk < t.ntok && row < p.tile_tokens * G)
+        x[i] = reinterpret_cast<const uint4*>(p.q + ((int64_t)(t.row0 + tk) * p.q_heads + hk * G + (row - tk * G)) * D)[ch];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = 16 * i + (tid >> 4);
+      if constexpr (C::K16) {
+        uint4 w = p.scale_log2 != 0.f ? x[i] : make_uint4(0, 0, 0, 0);
         if (p.scale_log2 < 0.f) w = make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
-        *reinterpret_cast<uint4*>(qop + (ch >> 3) * (kCtRows * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = w;
-      }
-    } else {
-      float amax = 0.f;
-#pragma unroll
-      for (int ch = 0; ch < 16; ++ch) {
-        const uint4 w = live ? src[ch] : make_uint4(0, 0, 0, 0);
-        const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+        *reinterpret_cast<uint4*>(qop + (ch >> 3) * (kCtRows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = w;
+      } else {
+        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        float f[8], amax = 0.f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          float f[2];
-          bf16x2_to_f32(w4[u], f);
-          amax = fmaxf(amax, fmaxf(fabsf(f[0]), fabsf(f[1])));
+          float f2[2];
+          bf16x2_to_f32(w[u], f2);
+          f[2 * u] = f2[0];
+          f[2 * u + 1] = f2[1];
+          amax = fmaxf(amax, fmaxf(fabsf(f2[0]), fabsf(f2[1])));
         }
-      }
-      const int kq = amax < INFINITY ? max(-100, min(120, e4m3_row_exp(amax))) : 0;
-      kq_sh[r] = (int8_t)kq;
-      const float qsc = pow2i(-kq);
-#pragma unroll 2
-      for (int ch = 4 * hf; ch < 4 * hf + 4; ++ch) {   // 16 dims (one 16-byte e4m3 chunk) each
-        const uint4 a = live ? src[2 * ch] : make_uint4(0, 0, 0, 0), b = live ? src[2 * ch + 1] : make_uint4(0, 0, 0, 0);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float f[2], g[2], hv[4];
-          bf16x2_to_f32(w[2 * u], f);
-          bf16x2_to_f32(w[2 * u + 1], g);
-          const float x0 = f[0] * qsc, x1 = f[1] * qsc, x2 = g[0] * qsc, x3 = g[1] * qsc;
+        for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // smallest power of two that brings the row within 448 = 1.75 * 2^8
+        const int ab = __float_as_int(amax);
+        const int kq = ab < 0x7F800000 ? max(-100, min(120, (ab >> 23) - 127 - 8 + ((ab & 0x7FFFFF) > 0x600000))) : 0;
+        if (ch == 0) kq_sh[row] = (int8_t)kq;
+        const float qsc = pow2i(-kq);
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float x0 = f[4 * u] * qsc, x1 = f[4 * u + 1] * qsc, x2 = f[4 * u + 2] * qsc, x3 = f[4 * u + 3] * qsc;
+          float hv[4];
           hi[u] = e4m3x2_rn(x0, x1) | (e4m3x2_rn(x2, x3) << 16);
           e4m3x4_to_f32_scaled(hi[u], hv);
           lo[u] = e4m3x2_rn(x0 - hv[0] * kTwoPow120, x1 - hv[1] * kTwoPow120) |
                   (e4m3x2_rn(x2 - hv[2] * kTwoPow120, x3 - hv[3] * kTwoPow120) << 16);
         }
-        const int off = r * 128 + ((ch ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(qop + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(qop + kCtRows * 128 + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        const int off = row * 128 + (((ch >> 1) ^ (row & 7)) << 4) + (ch & 1) * 8;
+        *reinterpret_cast<uint2*>(qop + off) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(qop + kCtRows * 128 + off) = make_uint2(lo[0], lo[1]);
       }
     }
     umma::fence_proxy_async_smem();
@@ -330,15 +339,12 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       // ---------------------------------------------------------- producer
       // V tile j goes out behind K tile j + KN - VN (the K ring is the deeper
       // one); a V tile's page ids may be those of the group before
-      constexpr int LEAD = C::KN - C::VN;
-      int old_ids = ids, kdone = 0, vdone = 0;
-      for (int i = 0; i < n + LEAD; ++i) {
+      int old_ids = ids, kdone = first_k, vdone = first_v;
+      for (int i = first_k; i < n + LEAD; ++i) {
         if (i < n) {
-          if (i >= C::KN) {
-            const bool ok = wait_fast(&kfree[i % C::KN], (i / C::KN - 1) & 1, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) break;
-          }
-          if (i > 0 && (i & 7) == 0) {
+          const bool ok = wait_fast(&kfree[i % C::KN], (i / C::KN - 1) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          if ((i & 7) == 0) {
             old_ids = ids;
             ids = next_ids;
             next_ids = fetch_ids((i >> 3) + 1);
@@ -347,11 +353,9 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
           kdone = i + 1;
         }
         const int j = i - LEAD;
-        if (j >= 0) {
-          if (j >= C::VN) {
-            const bool ok = wait_fast(&vfree[j % C::VN], (j / C::VN - 1) & 1, abort_flag);
-            if (!__all_sync(0xffffffffu, ok)) break;
-          }
+        if (j >= first_v) {
+          const bool ok = wait_fast(&vfree[j % C::VN], (j / C::VN - 1) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) break;
           load_tile(j, true, (j >> 3) == (min(i, n - 1) >> 3) ? ids : old_ids);
           vdone = j + 1;
         }
@@ -722,6 +726,9 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       if (tid == 0) raise_error(p.err, FP8KV_DEVERR_TIMEOUT);
     } else {
       umma::fence_after_sync();
+      const int r = tid & 127, tok = r / G;        // row of the tile, TMEM lane
+      const bool live = tok < t.ntok && r < p.tile_tokens * G;
+      const int64_t qrow = live ? (int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G) : -1;
       const uint32_t lane_q = (uint32_t)(32 * (warp & 3)) << 16;
       const float mr = st[r], lr = st[kCtRows + r], of = st[2 * kCtRows + r];
       const bool whole = p.num_splits == 1;
