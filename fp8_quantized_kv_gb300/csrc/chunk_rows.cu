@@ -74,6 +74,16 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
     return c.paged && it < n ? c.page_table[(int64_t)t.b * c.max_pages_per_seq + (group_key0(it) >> c.page_shift)] : 0;
   };
   uint8_t* ring = rsm + warp * C::NS * C::STAGE;
+  // Where a lane's chunks of a group go: chunk lane + 32 i lies 512 i bytes
+  // behind chunk lane, with one placement (K) or two that alternate (V), since
+  // 512 bytes hold a whole number of the rows after which the placement repeats
+  constexpr int KC = C::KB / 16, VC = C::VB / 16, VALT = 32 / VC < 8 ? 8 / (32 / VC) : 1;
+  static_assert(VALT <= 4, "rows of 64 bytes or more");
+  const uint32_t kdst = (lane / KC) * C::KB + k_chunk<KE, C::KB>(lane % KC, lane / KC) * 16;
+  uint32_t vdst[VALT];
+#pragma unroll
+  for (int i = 0; i < VALT; ++i)
+    vdst[i] = ((lane + 32 * i) / VC) * C::VB + v_chunk<C::VB>(lane % VC, (lane + 32 * i) / VC) * 16 - 512 * i;
   auto issue = [&](int it, int page) {
     if (it < n) {
       const int key0 = group_key0(it);
@@ -85,7 +95,6 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
         row = ((int64_t)(ok ? page : 0) * c.kv_heads + hk) * c.page_size + (key0 & (c.page_size - 1));
       }
       const uint32_t ks = umma::smem_u32(ring + (it % C::NS) * C::STAGE), vs = ks + kRowKeys * C::KB, sc = vs + kRowKeys * C::VB;
-      constexpr int KC = C::KB / 16, VC = C::VB / 16;
       // the 16 rows lie together: chunk e of the group is 16 e bytes from its start
       const uint8_t* ksrc = c.k + row * C::KB + lane * 16;
       const uint8_t* vsrc = c.v + row * C::VB + lane * 16;
@@ -96,26 +105,15 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
       };
       if (whole) {
 #pragma unroll
-        for (int i = 0; i < KC / 2; ++i) {
-          const int e = lane + 32 * i, r = e / KC, ch = e % KC;
-          cp_async16_u(ks + r * C::KB + k_chunk<KE, C::KB>(ch, r) * 16, ksrc + 512 * i);
-        }
+        for (int i = 0; i < KC / 2; ++i) cp_async16_u(ks + kdst + 512 * i, ksrc + 512 * i);
 #pragma unroll
-        for (int i = 0; i < VC / 2; ++i) {
-          const int e = lane + 32 * i, r = e / VC, ch = e % VC;
-          cp_async16_u(vs + r * C::VB + v_chunk<C::VB>(ch, r) * 16, vsrc + 512 * i);
-        }
+        for (int i = 0; i < VC / 2; ++i) cp_async16_u(vs + vdst[i % VALT] + 512 * i, vsrc + 512 * i);
       } else {
-#pragma unroll 1
-        for (int i = 0; i < KC / 2; ++i) {
-          const int e = lane + 32 * i, r = e / KC, ch = e % KC;
-          cp_async16_z(ks + r * C::KB + k_chunk<KE, C::KB>(ch, r) * 16, ksrc + 512 * i, live(r));
-        }
-#pragma unroll 1
-        for (int i = 0; i < VC / 2; ++i) {
-          const int e = lane + 32 * i, r = e / VC, ch = e % VC;
-          cp_async16_z(vs + r * C::VB + v_chunk<C::VB>(ch, r) * 16, vsrc + 512 * i, live(r));
-        }
+#pragma unroll
+        for (int i = 0; i < KC / 2; ++i) cp_async16_z(ks + kdst + 512 * i, ksrc + 512 * i, live((lane + 32 * i) / KC));
+#pragma unroll
+        for (int i = 0; i < VC / 2; ++i)
+          cp_async16_z(vs + vdst[i % VALT] + 512 * i, vsrc + 512 * i, live((lane + 32 * i) / VC));
       }
       const int r = lane & 15;
       if (lane < 16 ? !KB16 : !VB16) cp_async4_z(sc + lane * 4, (lane < 16 ? c.k_scale : c.v_scale) + row + r, live(r));
