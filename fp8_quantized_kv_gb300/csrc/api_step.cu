@@ -22,10 +22,19 @@ bool misaligned(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) !
 
 struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 
-// How a chunk call runs.  Tiles: rows per tile by the average number of query
-// rows (queries x heads of a group) a sequence has, so that short chunks do
-// not carry empty rows.  Splits: only when there are fewer tiles than the GPU
-// can hold CTAs.
+// How a chunk call runs, from its sizes (lengths are on the device).
+// Kernel, by the average number of query rows (queries x heads of a group) a
+// sequence has: up to 8 rows the few-row kernel (one token of 64 sequences
+// under a 1024-token window: 36 us, against 81 us on tcgen05 and 58 us on the
+// warp-level kernel's 16-row tiles); above, tcgen05 where it is built (8 tokens x
+// 4 heads over 8,000 tokens, 4 sequences: 40 us against 45 us at the best split
+// counts; 256 x 4 over 16,000: 108 against 447), else the warp-level kernel.
+// Splits: tiles are few -> enough of them for every CTA the GPU holds (four an
+// SM for the few-row kernel, two otherwise), each at least 256 (few rows) or
+// 512 keys long.  Without a window lengths can differ widely: shares of about
+// 4,096 keys then even them out (64 sequences of 1K-16K tokens: 268 us in 4
+// shares, 355 us whole; sequences of 700 tokens in the same cache pay 35 us
+// instead of 23), as long as that makes no more than 16 CTAs an SM.
 fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int window, int sinks, int num_splits,
                         int kernel, ChunkPlan* plan) {
   if (total_q < 0 || q_heads <= 0 || q_heads % c->kv_heads != 0 || window < 0 || sinks < 0 || num_splits < 0)
@@ -39,21 +48,29 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   const int64_t rows = (total_q + B - 1) / B * G;
   const bool tc_built = c->head_dim == 128 && c->dtype != FP8KV_MXK8V8;
   if (kernel == FP8KV_KERNEL_TENSOR_CORES && !tc_built) return FP8KV_ERR_UNSUPPORTED;
-  const bool tc = kernel == FP8KV_KERNEL_TENSOR_CORES || (kernel == FP8KV_KERNEL_AUTO && tc_built && rows > 32);
+  const int cap = capacity_of(c);
+  // (a cache without room has no tensor map; its calls only write zero rows)
+  const bool tc = cap > 0 && (kernel == FP8KV_KERNEL_TENSOR_CORES || (kernel == FP8KV_KERNEL_AUTO && tc_built && rows > 8));
   plan->kernel = tc ? FP8KV_KERNEL_TENSOR_CORES : FP8KV_KERNEL_WARP_MMA;
   plan->tile_rows = tc ? 128 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   plan->tile_tokens = plan->tile_rows / G;
-  const int64_t tiles = total_q / plan->tile_tokens + c->batch;
+  const int64_t tiles = total_q / plan->tile_tokens + c->batch;      // at most (chunk_common.cuh)
   if (tiles > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
   plan->tiles = (int)tiles;
-  const int cap = capacity_of(c);
   const int64_t seen = window > 0 && window < cap ? (int64_t)window + plan->tile_tokens + (sinks < cap ? sinks : cap) : cap;
   const int64_t kv_tiles = ((seen < cap ? seen : cap) + 63) / 64 + 1;
   int64_t want = num_splits;
   if (want == 0) {
-    const int64_t units = tiles * c->kv_heads, target = 2 * (int64_t)sm_count();
-    want = units > 0 ? target / units : 1;
-    if (want > kv_tiles / (tc ? 8 : 4)) want = kv_tiles / (tc ? 8 : 4);
+    // tiles if every sequence had the average number of queries
+    const int64_t units = B * (((total_q + B - 1) / B + plan->tile_tokens - 1) / plan->tile_tokens) * c->kv_heads;
+    const int64_t sms = sm_count(), least = tc ? 8 : 4;
+    want = units > 0 ? (plan->tile_rows == 8 ? 4 : 2) * sms / units : 1;
+    if (want > kv_tiles / least) want = kv_tiles / least;
+    if (plan->tile_rows == 8 && seen == cap && units > 0) {
+      int64_t even = (kv_tiles + 63) / 64;
+      if (even > 16 * sms / units) even = 16 * sms / units;
+      if (want < even) want = even;
+    }
   }
   if (want > kv_tiles) want = kv_tiles;
   if (want > 4096) want = 4096;
@@ -81,6 +98,11 @@ fp8kv_status fp8kv_build_tables(const fp8kv_cache* cache, const int32_t* cached_
   } else if (free_pages || num_free || free_head || free_head_out) {
     return FP8KV_ERR_INVALID_ARG;
   }
+  for (const void* a : {(const void*)cached_lens, (const void*)new_lens, (const void*)free_pages, (const void*)free_head,
+                        (const void*)cu_new, (const void*)seq_lens, (const void*)seq_idx, (const void*)pos,
+                        (const void*)free_head_out})
+    if (misaligned(a, 4)) return FP8KV_ERR_INVALID_ARG;
+  if (misaligned(slots, 8)) return FP8KV_ERR_INVALID_ARG;
   const size_t B = (size_t)cache->batch, N = (size_t)n_rows;
   const Range in[] = {{cached_lens, 4 * B}, {new_lens, 4 * B}, {free_pages, 4 * (size_t)num_free}, {free_head, 4},
                       {view.page_table, 4 * B * (size_t)view.max_pages_per_seq}};
@@ -111,7 +133,7 @@ fp8kv_status fp8kv_rope_tables(int64_t positions, int32_t rot_dim, double base, 
     return FP8KV_ERR_INVALID_ARG;
   if (rot_dim % 2 != 0 || rot_dim > 2 * kRopeMaxPairs || positions > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
   if (positions == 0) return FP8KV_OK;
-  if (!cos || !sin) return FP8KV_ERR_INVALID_ARG;
+  if (!cos || !sin || misaligned(cos, 4) || misaligned(sin, 4)) return FP8KV_ERR_INVALID_ARG;
   const size_t bytes = (size_t)positions * (rot_dim / 2) * sizeof(float);
   if (overlap({cos, bytes}, {sin, bytes})) return FP8KV_ERR_INVALID_ARG;
   constexpr double kTwoPi = 6.283185307179586476925;
@@ -180,7 +202,8 @@ fp8kv_status fp8kv_rope_append(const fp8kv_cache* cache, const void* q, int64_t 
   p.v_stride = v_stride;
   p.q_heads = q_heads;
   p.rot = rot_dim;
-  p.positions = positions;
+  // a turning key bias has its own table, one row per position of the cache
+  p.positions = cache->rope_cos != nullptr && cache->rope_positions < positions ? cache->rope_positions : positions;
   p.interleaved = layout == FP8KV_ROPE_INTERLEAVED;
   return cuda_status(launch_rope_append(p, cache->dtype, (cudaStream_t)stream));
 }
@@ -217,7 +240,10 @@ fp8kv_status fp8kv_chunk_attention(const void* q, const fp8kv_cache* cache, cons
   if (cu_q == nullptr && total_q != cache->batch) return FP8KV_ERR_INVALID_ARG;
   if (cache->batch == 0 || total_q == 0) return FP8KV_OK;
   if (!q || !seq_lens || !out || misaligned(q, 16) || misaligned(out, 16)) return FP8KV_ERR_INVALID_ARG;
+  if (misaligned(cu_q, 4) || misaligned(seq_lens, 4)) return FP8KV_ERR_INVALID_ARG;
   const int64_t rows = total_q * q_heads;
+  const size_t values = (size_t)rows * cache->head_dim;
+  if (overlap({q, 2 * values}, {out, (out_dtype == FP8KV_OUT_F32 ? 4 : 2) * values})) return FP8KV_ERR_INVALID_ARG;
   const size_t need = fp8kv_chunk_workspace_bytes(cache, total_q, q_heads, window, sinks, num_splits, kernel);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FP8KV_ERR_WORKSPACE;
   if (need > 0 && misaligned(workspace, 16)) return FP8KV_ERR_INVALID_ARG;

@@ -521,8 +521,6 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
           }
           publish(aside);
         }
-        __syncwarp();
-        if (lane == 0) umma::mbar_arrive(&vfree[vs]);
         if (ou > 0) {
           ok = wait_fast(&op_free[ob], (ou - 1) & 1, abort_flag);
           if (!__all_sync(0xffffffffu, ok)) break;
@@ -535,7 +533,13 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
                          e4m3x2_to_f16x2((uint16_t)(w[2 * ch + 1] & 0xFFFF)), e4m3x2_to_f16x2((uint16_t)(w[2 * ch + 1] >> 16)));
         umma::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) umma::mbar_arrive(&op_full[ob]);
+        // The stage is handed back only here, when the codes have been used.
+        // (Handed back right behind the reads, it could be overwritten while
+        // some were still pending: results differed from run to run.)
+        if (lane == 0) {
+          umma::mbar_arrive(&op_full[ob]);
+          umma::mbar_arrive(&vfree[vs]);
+        }
       }
     }
   } else {

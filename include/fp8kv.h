@@ -429,8 +429,8 @@ typedef enum {
  *   q_out:         [n][q_heads][head_dim] bf16; may be q itself if
  *                  q_stride = q_heads * head_dim
  * A row with a negative slot is padding: nothing is written for it.
- * A row whose position has no table entry or whose slot lies outside the
- * cache is skipped and raises SEQ_TOO_LONG or BAD_PAGE.  Two rows of one call
+ * A row whose position has no table entry (of cos and sin, or of the cache's
+ * rope_cos if it has one) or whose slot lies outside the cache is skipped and raises SEQ_TOO_LONG or BAD_PAGE.  Two rows of one call
  * may not share a slot (which row's codes and scale stay is not defined). */
 FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q, int64_t q_stride,
                                          const void *k, int64_t k_stride, const void *v,
@@ -466,7 +466,7 @@ FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q
  *               need be zero; NULL if that is 0.  Calls that may run at once
  *               need one each.
  *   out:        [total_q][q_heads][head_dim], bf16 or fp32 per out_dtype,
- *               16-byte aligned
+ *               16-byte aligned, apart from q
  * A query that sees no key (its position is negative: seq_lens[b] is less than
  * its sequence's queries) gets a zero row.  Keys that a query does not see
  * have no influence on it, whatever they hold (NaN included; pages that no

@@ -15,8 +15,8 @@ weights p (sum 1) and values v:
   - an f16 weight is held relative to the largest value scale, absolute step
     2^-39 of the largest value, at most one per key.
 So |o - exact| <= (u_P + 4 (d + 2^-19)) sum p |v| + keys 2^-38 max |v|.  The
-tcgen05 kernel's query operand adds 2^-18 max |q| sum |k| sm_scale to d.  A
-bf16 output adds its rounding, 2^-8 of the value."""
+tcgen05 kernel's query operand adds 2^-18 max |q| sum |k| sm_scale to d ("auto"
+may pick that kernel).  A bf16 output adds its rounding, 2^-8 of the value."""
 import math
 
 import numpy as np
@@ -130,7 +130,7 @@ def check(out, cache, want, rows, kernel):
     o, pv, qk, qs, keys, vmax = (x[rows] for x in want)
     v16 = cache.v.dtype == torch.bfloat16
     d = cache.head_dim * 2.0 ** -23 * qk + 2.0 ** -19
-    if kernel == "tensor_cores":
+    if kernel != "warp_mma":
         d = d + 2.0 ** -18 * qs
     tol = (2.0 ** (-8 if v16 else -11) + 4 * d)[..., None] * pv + (keys[:, None] * vmax * 2.0 ** -38)[..., None]
     got = out[rows].double().cpu()
@@ -195,9 +195,9 @@ def test_score_scale(dtype, sm):
 
 
 @pytest.mark.parametrize("dtype,D", [("k8v8", 128), ("k8v8", 64), ("k16v16", 128), ("mxk8v8", 128), ("k8v16", 64)])
-@pytest.mark.parametrize("new", [1, 2, 3])
+@pytest.mark.parametrize("new", [1, 2, 3, 6])
 def test_few_rows(dtype, D, new):
-    """Single and drafted tokens: the 16- and 32-row tiles, whose warps split
+    """Single and drafted tokens: the 8-, 16- and 32-row tiles, whose warps split
     the keys; one sequence holds the new tokens only."""
     run_case(dtype, D, 8, 2, [0, 15, 200, 63, 64], [new] * 5, 16, seed=2, kernel="warp_mma")
 
@@ -328,6 +328,39 @@ def test_reported_lengths_offsets_and_pages():
     out = fk.fp8kv_chunk_attention(q, cache, _i32([0, 2, 4, 6]), _i32([40, 40, 40]), out_dtype=torch.float32)
     assert fk.fp8kv_get_device_error() == fk.DEVERR_BAD_PAGE
     assert torch.equal(out[:2], good[:2]) and torch.equal(out[4:], good[4:])
+
+
+def test_large_calls_repeat():
+    """Calls of many CTAs, over and over: no wait runs out, and every run gives
+    the same bits (nothing depends on the order in which warps arrive)."""
+    rng = np.random.default_rng(31)
+    new, cached = rng.integers(100, 400, 12).tolist(), rng.integers(500, 3000, 12).tolist()
+    lens = [c + n for c, n in zip(cached, new)]
+    cu = np.concatenate([[0], np.cumsum(new)]).tolist()
+    for dtype in ("k8v8", "k16v16", "k16v8"):
+        cache = make_cache(dtype, 128, 4, lens, 16, seed=31, poison=False)
+        q = torch.randn(cu[-1], 28, 128, device="cuda").to(torch.bfloat16)
+        args = (q, cache, _i32(cu), _i32(lens))
+        for window in (0, 200):
+            ref = fk.fp8kv_chunk_attention(*args, window=window, sinks=5)
+            for _ in range(20):
+                assert torch.equal(fk.fp8kv_chunk_attention(*args, window=window, sinks=5), ref)
+            other = fk.fp8kv_chunk_attention(*args, window=window, sinks=5, kernel="warp_mma")
+            # two roundings of the weights on either side of values below 4.6, and bf16 outputs
+            assert (ref.float() - other.float()).abs().max() <= 2 * 2.0 ** -8 * 4.6 + 2.0 ** -8 * 4.6
+    assert fk.fp8kv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["k8v8", "k16v16"])
+def test_smallest_caches(dtype):
+    """A cache of 16 rows in all: fewer than a tile has keys.  One without room
+    has no storage and is refused, as by the other calls."""
+    for kernel in KERNELS:
+        run_case(dtype, 128, 2, 1, [0], [11], 0, seed=17, kernel=kernel)
+        cache = fk.Fp8KVCache.contiguous(2, 1, 128, 0, dtype)
+        q = torch.randn(30, 2, 128, device="cuda").to(torch.bfloat16)
+        with pytest.raises(fk.Fp8KVError):
+            fk.fp8kv_chunk_attention(q, cache, _i32([0, 20, 30]), _i32([0, 0]), kernel=kernel)
 
 
 def test_many_sequences():

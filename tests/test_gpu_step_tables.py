@@ -347,6 +347,20 @@ def test_rope_append_k_bias():
     assert fk.fp8kv_get_device_error() == 0
 
 
+def test_rope_append_turning_bias_has_its_own_table():
+    """A position past the cache's own rotary table is reported, however long
+    the call's table is."""
+    D = 64
+    cos, sin = fk.fp8kv_rope_tables(32, D)
+    long_cos, long_sin = fk.fp8kv_rope_tables(4096, D)
+    cache = fk.Fp8KVCache.contiguous(1, 1, D, 32, "k8v8", k_bias=torch.zeros(1, D, device="cuda"), rope_cos=cos, rope_sin=sin)
+    q = torch.randn(2, 1, D, device="cuda").to(torch.bfloat16)
+    out = torch.full_like(q, 9.0)
+    fk.fp8kv_rope_append(cache, q, q, q, _i32([3, 4000]), torch.tensor([3, 4], device="cuda"), long_cos, long_sin, q_out=out)
+    assert fk.fp8kv_get_device_error() == fk.DEVERR_SEQ_TOO_LONG
+    assert bool((out[1] == 9.0).all()) and not bool((out[0] == 9.0).any())
+
+
 def test_rope_append_padding_and_bad_rows():
     """Rows with a negative slot are left alone, rows without a table entry or
     with a slot past the cache are skipped and reported."""

@@ -44,6 +44,7 @@ def _tables(lib, cache, **kw):
     (INVALID, dict(free=None)), (INVALID, dict(head=None)), (INVALID, dict(head_out=None)),
     (INVALID, dict(lens=0x10000)), (INVALID, dict(head_out=0x13000)),      # outputs over inputs
     (INVALID, dict(pos=0x16004)), (INVALID, dict(cu=0x5000)), (INVALID, dict(cached=0x5000)),
+    (INVALID, dict(slots=0x18004)), (INVALID, dict(cached=0x10002)), (INVALID, dict(head=0x13001)),
     (UNSUPPORTED, dict(rows=1 << 31)),
 ])
 def test_tables_refusals(lib, want, kw):
@@ -61,7 +62,7 @@ def test_tables_refusals_by_cache(lib):
     (INVALID, dict(positions=-1)), (INVALID, dict(rot=0)), (INVALID, dict(base=0.0)), (INVALID, dict(base=float("inf"))),
     (INVALID, dict(factor=0.0)), (INVALID, dict(factor=float("nan"))), (INVALID, dict(amplitude=float("inf"))),
     (INVALID, dict(original=-1)), (INVALID, dict(original=64, lo=2.0, hi=2.0)), (INVALID, dict(original=64, lo=float("nan"))),
-    (INVALID, dict(cos=None)), (INVALID, dict(sin=0x20010)), (UNSUPPORTED, dict(rot=7)), (UNSUPPORTED, dict(rot=258)),
+    (INVALID, dict(cos=None)), (INVALID, dict(sin=0x20010)), (INVALID, dict(cos=0x20002)), (UNSUPPORTED, dict(rot=7)), (UNSUPPORTED, dict(rot=258)),
     (UNSUPPORTED, dict(positions=1 << 31)),
 ])
 def test_rope_tables_refusals(lib, want, kw):
@@ -89,6 +90,7 @@ def test_rope_append_refusals(lib, want, kw):
     (INVALID, dict(splits=-1)), (INVALID, dict(kernel=1)), (INVALID, dict(kernel=7)), (INVALID, dict(out_dtype=2)),
     (INVALID, dict(sm=float("nan"))), (INVALID, dict(q=None)), (INVALID, dict(lens=None)), (INVALID, dict(out=None)),
     (INVALID, dict(q=0x10008)), (INVALID, dict(out=0x40008)), (INVALID, dict(cu=None)), (INVALID, dict(ws=0x30008)),
+    (INVALID, dict(out=0x10000)), (INVALID, dict(out=0x10100)), (INVALID, dict(cu=0x20002)), (INVALID, dict(lens=0x21002)),
     (WORKSPACE, dict(ws=None)), (WORKSPACE, dict(ws_bytes=100)), (UNSUPPORTED, dict(q_heads=34)), (UNSUPPORTED, dict(total=1 << 31)),
     (UNSUPPORTED, dict(splits=5000)),
 ])
