@@ -259,12 +259,9 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
       }
     }
     float mt[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], x));
     // The reference moves only when the maximum grows by more than 2^8, kp only
-    // up, and O with them: rare behind the first groups, one vote skips it.
+    // up, and O with them: rare behind the first groups, one vote on what each
+    // lane sees skips it, and the query's maximum is joined only then.
     const float v0 = VB16 ? 0.f : vsc[g], v1 = VB16 ? 0.f : vsc[g + 8];
     bool moved = mt[0] > m[0] + 8.f || mt[1] > m[1] + 8.f;
     if constexpr (!VB16) moved = moved || fmaxf(v0, v1) >= fminf(vm_top[0], vm_top[1]);
@@ -272,6 +269,8 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
       float alpha[2] = {1.f, 1.f};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], x));
         if (mt[i] > m[i] + 8.f) {
           alpha[i] = ex2(m[i] - mt[i]);        // (0 for the first)
           m[i] = mt[i];

@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
           }
         }
       }
-      // each row's maximum by three-input max, joined over the quad
+      // the maximum of this thread's part of each row, by three-input max
       float mt[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -629,12 +629,11 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
                           max3(sv[i][3].x, sv[i][3].y, sv[i][4].x)),
                      max3(sv[i][4].y, sv[i][5].x, sv[i][5].y), max3(max3(sv[i][6].x, sv[i][6].y, sv[i][7].x), sv[i][7].y, -INFINITY));
 #pragma unroll
-      for (int i = 0; i < 2; ++i) mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 1));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 2)) * s2[i];
+      for (int i = 0; i < 2; ++i) mt[i] *= s2[i];
       // The reference maximum moves only when it grows by more than 2^8 (P stays
       // within 2^8 of it), kp only up; l (in units of 2^m) and O (2^(m + kp))
-      // move with them.  Rare behind the first tile: one vote skips it.
+      // move with them.  Rare behind the first tile: one vote on what each
+      // thread sees skips it, and the row's maximum is joined only then.
       bool moved = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i) moved = moved || mt[i] > m_used[i] + 8.f || (!C::V16 && vm[i] >= vm_top[i]);
@@ -643,6 +642,8 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       if (moved) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 1));
+          mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], 2));
           if (mt[i] > m_used[i] + 8.f) {
             alpha[i] = ex2(m_used[i] - mt[i]);    // (0 for the first)
             m_used[i] = mt[i];
