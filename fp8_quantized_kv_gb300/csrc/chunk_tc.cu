@@ -48,8 +48,10 @@
 //   rows read by the preparation warps                      295 us
 //   maxima joined only when a reference moves               281 us
 // Measured and not kept: four preparation warps (72 registers, spills: 351 us),
-// preparation warps on alternate tiles (315 us), waits with a suspend hint (as
-// fast).
+// preparation warps on alternate tiles (315 us), scores of two tiles by one
+// 128-key product (fewer reads of Q, but the pair waits for both P.V: 309 us),
+// key scales loaded while the scores arrive (287 us), waits with a suspend hint
+// (as fast).
 #include <cfloat>
 
 #include "chunk_common.cuh"
@@ -192,7 +194,6 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   const CacheView& c = p.c;
   const int G = p.group;
 
-  // loads of K tile / V tile j (one thread)
   const int64_t cont0 = ((int64_t)t.b * c.kv_heads + hk) * c.max_tokens;
   auto page_needed = [&](int k0, int len) {                   // is any key of [k0, k0 + len) seen by a query?
     return k0 < t.kv_end && (k0 + len > t.lo || k0 < p.sinks);
@@ -385,65 +386,63 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       }
     } else {
       // ---------------------------------------------------------- MMA issuer
-      {
-        constexpr uint32_t ID_QK = C::K16 ? umma::idesc(umma::FMT_BF16, umma::FMT_BF16, umma::MAJOR_K, umma::MAJOR_K, 128, 64)
-                                          : umma::idesc(umma::FMT_E4M3, umma::FMT_E4M3, umma::MAJOR_K, umma::MAJOR_K, 128, 64);
-        constexpr uint32_t FV = C::V16 ? umma::FMT_BF16 : umma::FMT_F16;
-        constexpr uint32_t ID_PV = umma::idesc(FV, FV, umma::MAJOR_K, umma::MAJOR_MN, 128, 128);
-        const uint32_t qa = umma::smem_u32(qop);
-        auto issue_qk = [&](int j) {
-          const bool in = wait_fast(&kfull[j % C::KN], (j / C::KN) & 1, abort_flag);
-          if (!__all_sync(0xffffffffu, in)) return false;
-          umma::fence_after_sync();
-          const uint32_t ka = umma::smem_u32(kring + (j % C::KN) * C::KT), sd = tmem + 64 * (j & 1);
-          if (elect_one()) {
+      constexpr uint32_t ID_QK = C::K16 ? umma::idesc(umma::FMT_BF16, umma::FMT_BF16, umma::MAJOR_K, umma::MAJOR_K, 128, 64)
+                                        : umma::idesc(umma::FMT_E4M3, umma::FMT_E4M3, umma::MAJOR_K, umma::MAJOR_K, 128, 64);
+      constexpr uint32_t FV = C::V16 ? umma::FMT_BF16 : umma::FMT_F16;
+      constexpr uint32_t ID_PV = umma::idesc(FV, FV, umma::MAJOR_K, umma::MAJOR_MN, 128, 128);
+      const uint32_t qa = umma::smem_u32(qop);
+      auto issue_qk = [&](int j) {
+        const bool in = wait_fast(&kfull[j % C::KN], (j / C::KN) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, in)) return false;
+        umma::fence_after_sync();
+        const uint32_t ka = umma::smem_u32(kring + (j % C::KN) * C::KT), sd = tmem + 64 * (j & 1);
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              // e4m3: 32 dims a step, the four steps of hi and of lo meet the same
-              // K; bf16: 16 dims a step, halves of 64 dims behind each other
-              const uint64_t a = umma::sdesc(qa + (kk >> 2) * (kCtRows * 128) + (kk & 3) * 32, 16, 1024, umma::SWIZZLE_128B);
-              const uint64_t b = umma::sdesc(ka + (C::K16 ? (kk >> 2) * (kChunkKeys * 128) : 0) + (kk & 3) * 32, 16, 1024,
-                                             umma::SWIZZLE_128B);
-              if constexpr (C::K16) umma::mma_f16_ss(sd, a, b, ID_QK, kk > 0);
-              else umma::mma_f8_ss(sd, a, b, ID_QK, kk > 0);
-            }
-            umma::mma_commit(&s_full[j & 1]);
-            umma::mma_commit(&kfree[j % C::KN]);
+          for (int kk = 0; kk < 8; ++kk) {
+            // e4m3: 32 dims a step, the four steps of hi and of lo meet the same
+            // K; bf16: 16 dims a step, halves of 64 dims behind each other
+            const uint64_t a = umma::sdesc(qa + (kk >> 2) * (kCtRows * 128) + (kk & 3) * 32, 16, 1024, umma::SWIZZLE_128B);
+            const uint64_t b = umma::sdesc(ka + (C::K16 ? (kk >> 2) * (kChunkKeys * 128) : 0) + (kk & 3) * 32, 16, 1024,
+                                           umma::SWIZZLE_128B);
+            if constexpr (C::K16) umma::mma_f16_ss(sd, a, b, ID_QK, kk > 0);
+            else umma::mma_f8_ss(sd, a, b, ID_QK, kk > 0);
           }
-          __syncwarp();
-          return true;
-        };
-        bool ok = n > 0 && issue_qk(0);
-        if (ok && n > 1) ok = issue_qk(1);
-        for (int j = 0; ok && j < n; ++j) {
-          const int ob = j % OPN;
-          bool in = wait_fast(&op_full[ob], (j / OPN) & 1, abort_flag);
-          in = in && wait_fast(&p_full[j & 1], (j >> 1) & 1, abort_flag);
-          if (!__all_sync(0xffffffffu, in)) break;
-          umma::fence_after_sync();
-          const uint32_t va = umma::smem_u32(vop + ob * (C::V16 ? C::VT : C::OPT)), pa = tmem + 64 * (j & 1);
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_f16_ts(o_col, pa + 8 * kk, umma::sdesc(va + kk * 2048, kChunkKeys * 128, 1024, umma::SWIZZLE_128B), ID_PV,
-                         (j > 0 || kk > 0) ? 1u : 0u);
-            umma::mma_commit(pv_done);
-            if constexpr (C::V16) umma::mma_commit(&vfree[ob]);
-            else umma::mma_commit(&op_free[ob]);
-          }
-          __syncwarp();
-          if (j + 2 < n) {
-            // the scores of tile j + 2 go where P of tile j was
-            in = wait_fast(pv_done, j & 1, abort_flag);
-            if (!__all_sync(0xffffffffu, in)) break;
-            ok = issue_qk(j + 2);
-          }
+          umma::mma_commit(&s_full[j & 1]);
+          umma::mma_commit(&kfree[j % C::KN]);
         }
-        // all issued MMAs complete before TMEM is released
         __syncwarp();
-        if (elect_one()) umma::mma_commit(drained);
-        (void)umma::mbar_wait(drained, 0, 100000000ull);
+        return true;
+      };
+      bool ok = n > 0 && issue_qk(0);
+      if (ok && n > 1) ok = issue_qk(1);
+      for (int j = 0; ok && j < n; ++j) {
+        const int ob = j % OPN;
+        bool in = wait_fast(&op_full[ob], (j / OPN) & 1, abort_flag);
+        in = in && wait_fast(&p_full[j & 1], (j >> 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, in)) break;
+        umma::fence_after_sync();
+        const uint32_t va = umma::smem_u32(vop + ob * (C::V16 ? C::VT : C::OPT)), pa = tmem + 64 * (j & 1);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ts(o_col, pa + 8 * kk, umma::sdesc(va + kk * 2048, kChunkKeys * 128, 1024, umma::SWIZZLE_128B), ID_PV,
+                       (j > 0 || kk > 0) ? 1u : 0u);
+          umma::mma_commit(pv_done);
+          if constexpr (C::V16) umma::mma_commit(&vfree[ob]);
+          else umma::mma_commit(&op_free[ob]);
+        }
+        __syncwarp();
+        if (j + 2 < n) {
+          // the scores of tile j + 2 go where P of tile j was
+          in = wait_fast(pv_done, j & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, in)) break;
+          ok = issue_qk(j + 2);
+        }
       }
+      // all issued MMAs complete before TMEM is released
+      __syncwarp();
+      if (elect_one()) umma::mma_commit(drained);
+      (void)umma::mbar_wait(drained, 0, 100000000ull);
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------ preparation

@@ -351,6 +351,26 @@ def test_large_calls_repeat():
     assert fk.fp8kv_get_device_error() == 0
 
 
+@pytest.mark.parametrize("dtype,D,new", [("k8v8", 128, [40, 3]), ("k8v8", 128, [1, 1]), ("k8v16", 64, [30, 1])])
+def test_residual_keys(dtype, D, new):
+    """A cache of keys less a fixed bias: the bias adds the same to every score of
+    a query, so the outputs are those of the whole keys."""
+    lens, Hkv = [100, 70], 2
+    g = torch.Generator(device="cuda").manual_seed(40)
+    bias = 5 * torch.randn(Hkv, D, generator=g, device="cuda")
+    cache = fk.Fp8KVCache.contiguous(2, Hkv, D, 112, dtype, k_bias=bias)
+    n = sum(lens)
+    k = (torch.randn(n, Hkv, D, generator=g, device="cuda") + bias).to(torch.bfloat16)
+    v = torch.randn(n, Hkv, D, generator=g, device="cuda").to(torch.bfloat16)
+    fk.fp8kv_append(cache, k, v, _i32([0] * 100 + [1] * 70), _i32(list(range(100)) + list(range(70))))
+    cu = [0, new[0], sum(new)]
+    q = torch.randn(cu[-1], 8, D, generator=g, device="cuda").to(torch.bfloat16)
+    out = fk.fp8kv_chunk_attention(q, cache, _i32(cu), _i32(lens), out_dtype=torch.float32)
+    assert fk.fp8kv_get_device_error() == 0
+    kv = [[x + bias.cpu().double(), y] for x, y in cache_values(cache, lens)]
+    check(out, cache, definition(q, kv, cu, lens, 0, 0, D ** -0.5), slice(0, cu[-1]), "auto")
+
+
 @pytest.mark.parametrize("dtype", ["k8v8", "k16v16"])
 def test_smallest_caches(dtype):
     """A cache of 16 rows in all: fewer than a tile has keys.  One without room
