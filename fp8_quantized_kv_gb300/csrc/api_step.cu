@@ -24,17 +24,29 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 
 // How a chunk call runs, from its sizes (lengths are on the device).
 // Kernel, by the average number of query rows (queries x heads of a group) a
-// sequence has: up to 8 rows the few-row kernel (one token of 64 sequences
-// under a 1024-token window: 36 us, against 81 us on tcgen05 and 58 us on the
-// warp-level kernel's 16-row tiles); above, tcgen05 where it is built (8 tokens x
-// 4 heads over 8,000 tokens, 4 sequences: 40 us against 45 us at the best split
-// counts; 256 x 4 over 16,000: 108 against 447), else the warp-level kernel.
-// Splits: tiles are few -> enough of them for every CTA the GPU holds (four an
-// SM for the few-row kernel, two otherwise), each at least 256 (few rows) or
-// 512 keys long.  Without a window lengths can differ widely: shares of about
-// 4,096 keys then even them out (64 sequences of 1K-16K tokens: 268 us in 4
-// shares, 355 us whole; sequences of 700 tokens in the same cache pay 35 us
-// instead of 23), as long as that makes no more than 16 CTAs an SM.
+// sequence has: up to 16 rows the few-row kernel, in tiles of 8 or 16 (one token
+// of 64 sequences under a 1,024-token window: 36 us, against 81 us on tcgen05; two
+// tokens x 8 heads of 64 sequences of 2K-4K tokens: 75 us, against 101 us);
+// above, tcgen05 where it is built (8 tokens x 4 heads over 8,000 tokens, 4
+// sequences: 40 us against 45 us at the best split counts; 256 x 4 over 16,000:
+// 108 against 447), else the warp-level kernel.
+//
+// Splits of the few-row kernel: an SM holds four of its CTAs (three of 16 rows,
+// or of 32 KiB stages), and a call takes as many waves of them as they need,
+// each as long as one share and the 8 tiles' time that a CTA spends on its
+// start and end.  So the counts that fill one, two or three waves are compared:
+// 256 units of 32-64 tiles (16 rows) take 100 us whole, 84 us in 2 shares (1.1
+// waves), 75 us in 3 (1.7), 79 us in 4.  Shares are 256 keys or longer.
+// Without a window lengths can differ widely: shares of about 4,096 keys at most
+// then even them out (64 sequences of 1K-16K tokens: 268 us in 4 shares, 355 us
+// whole; sequences of 700 tokens in the same cache pay 35 us instead of 23), as
+// long as that makes no more than 16 CTAs an SM.
+//
+// Splits of the others: tiles are few -> one wave.  tcgen05: two CTAs an SM,
+// shares of 512 keys or longer.  Warp-level kernel: two an SM and 256 keys, at
+// head dim 64 three (by their registers) and 128 (2-4 tokens x 8 heads, 16
+// sequences of 4K-8K tokens: 62 us in 4 shares, 51 us in 6, 43 us in 8; 32-64 x 8
+// of 2 sequences of 2K-4K: 36 us in 4, 31 us in 6, 37 us in 9, past one wave).
 fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int window, int sinks, int num_splits,
                         int kernel, ChunkPlan* plan) {
   if (total_q < 0 || q_heads <= 0 || q_heads % c->kv_heads != 0 || window < 0 || sinks < 0 || num_splits < 0)
@@ -50,7 +62,7 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   if (kernel == FP8KV_KERNEL_TENSOR_CORES && !tc_built) return FP8KV_ERR_UNSUPPORTED;
   const int cap = capacity_of(c);
   // (a cache without room has no tensor map; its calls only write zero rows)
-  const bool tc = cap > 0 && (kernel == FP8KV_KERNEL_TENSOR_CORES || (kernel == FP8KV_KERNEL_AUTO && tc_built && rows > 8));
+  const bool tc = cap > 0 && (kernel == FP8KV_KERNEL_TENSOR_CORES || (kernel == FP8KV_KERNEL_AUTO && tc_built && rows > 16));
   plan->kernel = tc ? FP8KV_KERNEL_TENSOR_CORES : FP8KV_KERNEL_WARP_MMA;
   plan->tile_rows = tc ? 128 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   plan->tile_tokens = plan->tile_rows / G;
@@ -63,13 +75,25 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   if (want == 0) {
     // tiles if every sequence had the average number of queries
     const int64_t units = B * (((total_q + B - 1) / B + plan->tile_tokens - 1) / plan->tile_tokens) * c->kv_heads;
-    const int64_t sms = sm_count(), least = tc ? 8 : 4;
-    want = units > 0 ? (plan->tile_rows == 8 ? 4 : 2) * sms / units : 1;
-    if (want > kv_tiles / least) want = kv_tiles / least;
-    if (plan->tile_rows == 8 && seen == cap && units > 0) {
-      int64_t even = (kv_tiles + 63) / 64;
+    const int64_t sms = sm_count();
+    if (plan->tile_rows > 16) {
+      const bool narrow = c->head_dim == 64;
+      want = units > 0 ? (narrow ? 3 : 2) * sms / units : 1;
+      const int64_t most = kv_tiles / (tc ? 8 : narrow ? 2 : 4);
+      if (want > most) want = most;
+    } else if (units > 0) {
+      const bool wide = c->head_dim == 128 && c->dtype == FP8KV_K16V16;
+      const int64_t held = (plan->tile_rows == 8 && !wide ? 4 : 3) * sms, most = kv_tiles / 4;
+      int64_t even = seen == cap ? (kv_tiles + 63) / 64 : 1;
       if (even > 16 * sms / units) even = 16 * sms / units;
-      if (want < even) want = even;
+      if (even < 1) even = 1;
+      want = even;
+      auto cost = [&](int64_t s) { return (double)((units * s + held - 1) / held) * ((double)kv_tiles / s + 8); };
+      for (int64_t waves = 1; waves <= 3; ++waves) {
+        int64_t s = waves * held / units;
+        if (s > most) s = most;
+        if (s > want && cost(s) < cost(want)) want = s;
+      }
     }
   }
   if (want > kv_tiles) want = kv_tiles;
@@ -268,7 +292,7 @@ fp8kv_status fp8kv_chunk_attention(const void* q, const fp8kv_cache* cache, cons
   cudaStream_t s = (cudaStream_t)stream;
   const int tiles = cu_q ? plan.tiles : cache->batch;
   cudaError_t e = plan.kernel == FP8KV_KERNEL_TENSOR_CORES ? launch_chunk_tc(p, cache->dtype, tiles, s)
-                  : plan.tile_rows == 8 ? launch_chunk_rows(p, cache->dtype, tiles, s)
+                  : plan.tile_rows <= 16 ? launch_chunk_rows(p, cache->dtype, tiles, s)
                                         : launch_chunk_mma(p, cache->dtype, plan.tile_rows / 16, tiles, s);
   if (e == cudaSuccess && plan.splits > 1) e = launch_chunk_merge(p, s);
   return cuda_status(e);

@@ -1,16 +1,16 @@
 // chunk_mma.cu -- ragged chunk attention over the cache on warp-level matrix
 // instructions, for every cache type and head dim: the form for what the
 // tcgen05 kernel is not built for (head dim 64, block-scaled keys) and the
-// few-row kernel does not take (more than eight query rows a tile).
+// few-row kernel does not take (more than sixteen query rows a sequence).
 //
 // One pass over the keys with a running maximum m, sum l and output O:
 //   s = (q . k) k_scale sm_scale log2(e),  m' = max(m, max s),
 //   l = l 2^(m - m') + sum 2^(s - m'),     O = O 2^(m - m') + 2^(s - m') V
 // 128 threads; a CTA owns 16 MW query rows of one KV head (rows = tokens x
 // heads of the group) and walks 64-key tiles through a ring of NS cp.async
-// stages.  MW = 4: a warp owns 16 rows and all keys of a tile.  MW = 1 and 2:
-// the warps split a tile's keys and join their (m, l, O) at the end, so a
-// tile with few rows still keeps four warps busy.
+// stages.  MW = 4: a warp owns 16 rows and all keys of a tile.  MW = 2: two warps
+// split a tile's keys and join their (m, l, O) at the end, so a tile with few
+// rows still keeps four warps busy.
 //
 // Operands.  e4m3 codes convert to f16 exactly, so QK runs in f16 with each
 // bf16 query row scaled by a power of two to put its largest element in
@@ -26,7 +26,7 @@
 // bf16 values.  m, l and O are fp32.
 //
 // What bounds it: instruction issue.  3,727 queries over 2,000-8,000 tokens (28 /
-// 4 heads, head dim 128, e4m3) take 1.2 ms, 160 TFLOP/s (conversions of codes
+// 4 heads, head dim 128, e4m3) take 1.28 ms, 151 TFLOP/s (conversions of codes
 // are repeated by each of a tile's four warps); 16 queries over 100 tokens at
 // head dim 64 take 7.2 us, the latency of a launch and a few dependent loads.
 //
@@ -554,7 +554,6 @@ static cudaError_t launch_one(const ChunkParams& p, dim3 grid, cudaStream_t st) 
 
 template <int D, int KE, int VE>
 static cudaError_t launch_rows(const ChunkParams& p, int row_warps, dim3 grid, cudaStream_t st) {
-  if (row_warps == 1) return launch_one<D, KE, VE, 1>(p, grid, st);
   if (row_warps == 2) return launch_one<D, KE, VE, 2>(p, grid, st);
   return launch_one<D, KE, VE, 4>(p, grid, st);
 }

@@ -1,16 +1,17 @@
-// chunk_rows.cu -- ragged chunk attention for tiles of at most eight query
-// rows (single tokens of a group of up to eight heads, a few drafted tokens):
-// the cache is read once and nothing else takes as long, so the kernel is
-// built around keeping loads in flight.
+// chunk_rows.cu -- ragged chunk attention for tiles of at most sixteen query
+// rows (single tokens of a group of heads, a few drafted tokens): the cache is
+// read once and nothing else takes as long, so the kernel is built around
+// keeping loads in flight.
 //
-// The products are turned around so that the eight queries are the narrow side
-// of the matrix instruction: S^T = K Q^T (16 keys x 8 queries per instruction)
-// and O^T = V^T P^T (16 head dims x 8 queries).  A warp owns groups of 16 keys:
-// it copies their K and V rows and scales into its own ring (cp.async, no
-// barrier between warps), and keeps its own running maximum m, sum l and O^T;
-// the four warps of a CTA, and the splits of a long sequence, are joined at the
-// end.  A group never crosses a page (pages hold 16 tokens or more), so a page
-// id is looked up once per group, an iteration before its copy.
+// The products are turned around so that the queries are the narrow side of the
+// matrix instruction: S^T = K Q^T (16 keys x 8 queries per instruction) and
+// O^T = V^T P^T (16 head dims x 8 queries).  A tile has one or two sets of eight
+// queries (QT); two share the loads and conversions of K and V.  A warp owns
+// groups of 16 keys: it copies their K and V rows and scales into its own ring
+// (cp.async, no barrier between warps), and keeps its own running maximum m, sum
+// l and O^T; the four warps of a CTA, and the splits of a long sequence, are
+// joined at the end.  A group never crosses a page (pages hold 16 tokens or
+// more), so a page id is looked up once per group, an iteration before its copy.
 //
 // Arithmetic as in chunk_mma.cu: f16 operands for e4m3 sides (codes exact,
 // query scaled by a power of two, P by 2^-kp and the value scale), bf16 for
@@ -21,11 +22,18 @@
 // TB/s, 57 % of the measured copy rate); 2,048 more tokens of window cost at 5.4
 // TB/s, so what is left is the fixed part (about 5 us to find the tile, load the
 // first groups and join) and the issue slots (46 % busy: 430 instructions a
-// group, 80 of them the conversion of 4,096 codes).  Queries on the wide side of
-// the instruction, one warp per 16 keys of a shared tile: 58 us; a reference
-// that moves at every new maximum: 46 us; three CTAs an SM at four ring stages:
-// 46 us, five at two: 40 us, four at three (this): 36.5 us.  QK on e4m3
+// group, 80 of them the conversion of 4,096 codes).  On the way there: 58 us with
+// a reference that moves at every new maximum and checked row copies; 46 us with
+// one vote for both and whole-group copies, three CTAs an SM at four ring stages;
+// 40 us with five CTAs at two; 36.5 us with four at three (this).  QK on e4m3
 // instructions without conversion (mma.sync m16n8k32) was slower, 39 us.
+//
+// Sixteen rows (two tokens x 8 heads, 4 KV heads, 64 sequences of 2K-4K tokens,
+// 210 MB): 75 us, three CTAs an SM at 168 registers; 59 us for one token.  The
+// second set costs its products, exponentials and transposes, not the codes'
+// conversion.  On the warp-level kernel, whose four warps share a tile, the call took
+// 90 us at the best split count, on tcgen05's 128-row tiles 101 us; 16 heads on one
+// KV head at head dim 64 (64 sequences of 4K-8K tokens) take 31 us, 53 us there.
 #include <cfloat>
 
 #include "chunk_common.cuh"
@@ -34,14 +42,15 @@ namespace fp8kv {
 
 constexpr int kRowKeys = 16;       // keys of a group
 
-template <int D, int KE, int VE>
+// QT: tiles of eight query rows (1 or 2)
+template <int D, int KE, int VE, int QT>
 struct RowsCfg {
   static constexpr int KB = KE == ELEM_BF16 ? 2 * D : D;
   static constexpr int VB = VE == ELEM_BF16 ? 2 * D : D;
   static constexpr int STAGE = kRowKeys * (KB + VB) + 2 * kRowKeys * 4;    // rows, key scales, value scales
   static constexpr int NS = KB + VB > 256 ? 2 : 3;
   static constexpr int OS = D + 4;
-  static constexpr int JOIN = 32 * OS * 4 + 2 * 32 * 4;
+  static constexpr int JOIN = 32 * QT * OS * 4 + 2 * 32 * QT * 4;
   static constexpr int RING = 4 * NS * STAGE;
   static constexpr int BYTES = RING > JOIN ? RING : JOIN;
 };
@@ -57,9 +66,11 @@ __device__ __forceinline__ void cp_async16_u(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
 
-template <int D, int KE, int VE>
-__global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams p) {
-  using C = RowsCfg<D, KE, VE>;
+template <int D, int KE, int VE, int QT>
+__global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(const ChunkParams p) {
+  using C = RowsCfg<D, KE, VE, QT>;
+  constexpr int QC = 2 * QT;                   // score columns (queries) of a thread
+  constexpr int QR = 8 * QT;                   // query rows of the tile
   constexpr bool KB16 = KE == ELEM_BF16, VB16 = VE == ELEM_BF16;
   constexpr int KS = D / 16;                   // k steps of QK, m tiles of PV
   extern __shared__ __align__(128) uint8_t rsm[];
@@ -140,62 +151,76 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
   }
   int next_page = fetch_page(C::NS - 1);
 
-  // query row g as B fragments; positions of this thread's score columns
-  const int tokg = g / G;
-  const bool liveg = tokg < t.ntok && g < p.tile_tokens * G;
-  const uint4* qsrc = reinterpret_cast<const uint4*>(
-      p.q + (liveg ? (int64_t)(t.row0 + tokg) * p.q_heads + hk * G + (g - tokg * G) : 0) * D);
-  uint32_t qb[KS][2];
+  // query rows g and g + 8 as B fragments; positions of this thread's score
+  // columns, queries col(i)
+  auto col = [&](int i) { return 8 * (i >> 1) + 2 * c4 + (i & 1); };
+  uint32_t qb[QT][KS][2];
+  float qf[QC];                                // what the scaled query leaves to undo, per score column
 #pragma unroll
-  for (int u = 0; u < D / 32; ++u) {
-    const int at = KE == ELEM_E4M3 ? 8 * (u >> 1) + 2 * c4 + (u & 1) : 4 * u + c4;
-    const uint4 x = liveg ? qsrc[at] : make_uint4(0, 0, 0, 0);
-    qb[2 * u][0] = x.x; qb[2 * u][1] = x.y; qb[2 * u + 1][0] = x.z; qb[2 * u + 1][1] = x.w;
+  for (int w = 0; w < QT; ++w) {
+    const int r = g + 8 * w, tokr = r / G;
+    const bool live = tokr < t.ntok && r < p.tile_tokens * G;
+    const uint4* qsrc = reinterpret_cast<const uint4*>(
+        p.q + (live ? (int64_t)(t.row0 + tokr) * p.q_heads + hk * G + (r - tokr * G) : 0) * D);
+#pragma unroll
+    for (int u = 0; u < D / 32; ++u) {
+      const int at = KE == ELEM_E4M3 ? 8 * (u >> 1) + 2 * c4 + (u & 1) : 4 * u + c4;
+      const uint4 x = live ? qsrc[at] : make_uint4(0, 0, 0, 0);
+      qb[w][2 * u][0] = x.x; qb[w][2 * u][1] = x.y; qb[w][2 * u + 1][0] = x.z; qb[w][2 * u + 1][1] = x.w;
+    }
+    qf[2 * w] = qf[2 * w + 1] = 1.f;
+    if constexpr (!KB16) {
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float f[2];
+          bf16x2_to_f32(qb[w][k][u], f);
+          amax = fmaxf(amax, fmaxf(fabsf(f[0]), fabsf(f[1])));
+        }
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+      const int e = ((__float_as_int(amax) >> 23) & 0xFF) - 127;
+      const int up = amax > 0.f && e < 128 ? min(14 - e, 126) : 0;   // amax 2^up in [2^14, 2^15)
+      const float sc = pow2i(up), down = pow2i(-up);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float f[2];
+          bf16x2_to_f32(qb[w][k][u], f);
+          qb[w][k][u] = pack16<false>(f[0] * sc, f[1] * sc);
+        }
+      qf[2 * w] = __shfl_sync(0xffffffffu, down, 8 * c4);
+      qf[2 * w + 1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
+    }
   }
-  float qf[2] = {1.f, 1.f};                    // what the scaled query leaves to undo, per score column
-  if constexpr (!KB16) {
-    float amax = 0.f;
+  int qpos[QC];
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float f[2];
-        bf16x2_to_f32(qb[k][u], f);
-        amax = fmaxf(amax, fmaxf(fabsf(f[0]), fabsf(f[1])));
-      }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const int e = ((__float_as_int(amax) >> 23) & 0xFF) - 127;
-    const int up = amax > 0.f && e < 128 ? min(14 - e, 126) : 0;   // amax 2^up in [2^14, 2^15)
-    const float sc = pow2i(up), down = pow2i(-up);
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float f[2];
-        bf16x2_to_f32(qb[k][u], f);
-        qb[k][u] = pack16<false>(f[0] * sc, f[1] * sc);
-      }
-    qf[0] = __shfl_sync(0xffffffffu, down, 8 * c4);
-    qf[1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
-  }
-  int qpos[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = 2 * c4 + i, tk = r / G;
+  for (int i = 0; i < QC; ++i) {
+    const int r = col(i), tk = r / G;
     qpos[i] = tk < t.ntok && r < p.tile_tokens * G ? t.pos0 + tk : -1;
     qf[i] *= p.scale_log2;
   }
 
-  float o[KS][4];
+  float o[QT][KS][4];
 #pragma unroll
-  for (int u = 0; u < KS; ++u)
+  for (int w = 0; w < QT; ++w)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[u][e] = 0.f;
+    for (int u = 0; u < KS; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[w][u][e] = 0.f;
   // the reference maximum, the sum in units of 2^m, -m - kp, 2^kp, and the
   // value scale from which on kp has to rise
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, neg_m[2] = {0.f, 0.f}, up2[2] = {1.f, 1.f};
-  float vm_top[2] = {FLT_MIN, FLT_MIN};
+  float m[QC], l[QC], neg_m[QC], up2[QC], vm_top[QC];
+#pragma unroll
+  for (int i = 0; i < QC; ++i) {
+    m[i] = -INFINITY;
+    l[i] = neg_m[i] = 0.f;
+    up2[i] = 1.f;
+    vm_top[i] = FLT_MIN;
+  }
 
 #pragma unroll 1
   for (int it = 0; it < n; ++it) {
@@ -208,8 +233,12 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
     const float* ksc = reinterpret_cast<const float*>(vst + kRowKeys * C::VB);
     const float* vsc = ksc + kRowKeys;
     const int key0 = group_key0(it);
-    // s[e]: key g + 8 (e >> 1), query 2 c4 + (e & 1); two chains of products
-    float s[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+    // s[w][e]: key g + 8 (e >> 1), query col(2 w + (e & 1)); two chains of products
+    float s[QT][4], s1[QT][4];
+#pragma unroll
+    for (int w = 0; w < QT; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[w][e] = s1[w][e] = 0.f;
     if constexpr (KE == ELEM_E4M3) {
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
@@ -220,12 +249,16 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
         for (int u = 0; u < 4; ++u) {
           const uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)xx[u]), e4m3x2_to_f16x2((uint16_t)yy[u]),
                                  e4m3x2_to_f16x2((uint16_t)(xx[u] >> 16)), e4m3x2_to_f16x2((uint16_t)(yy[u] >> 16))};
-          mma16816<false>(u & 1 ? s1 : s, a, qb[4 * h + u][0], qb[4 * h + u][1]);
+#pragma unroll
+          for (int w = 0; w < QT; ++w)
+            mma16816<false>(u & 1 ? s1[w] : s[w], a, qb[w][4 * h + u][0], qb[w][4 * h + u][1]);
         }
       }
       const float k0 = ksc[g], k1 = ksc[g + 8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = (s[e] + s1[e]) * ((e >> 1 ? k1 : k0) * qf[e & 1]);
+      for (int w = 0; w < QT; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[w][e] = (s[w][e] + s1[w][e]) * ((e >> 1 ? k1 : k0) * qf[2 * w + (e & 1)]);
     } else if constexpr (KE == ELEM_MX) {
       const uint32_t e0 = reinterpret_cast<const uint32_t*>(ksc)[g], e1 = reinterpret_cast<const uint32_t*>(ksc)[g + 8];
 #pragma unroll
@@ -233,95 +266,121 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
         const int ch = 2 * blk + (c4 >> 1), in = (c4 & 1) * 8;
         const uint2 x = *reinterpret_cast<const uint2*>(st + g * C::KB + k_chunk<KE, C::KB>(ch, g) * 16 + in);
         const uint2 y = *reinterpret_cast<const uint2*>(st + (g + 8) * C::KB + k_chunk<KE, C::KB>(ch, g + 8) * 16 + in);
-        float part[4] = {0.f, 0.f, 0.f, 0.f};
         const uint32_t a[4] = {e4m3x2_to_f16x2((uint16_t)x.x), e4m3x2_to_f16x2((uint16_t)y.x),
                                e4m3x2_to_f16x2((uint16_t)(x.x >> 16)), e4m3x2_to_f16x2((uint16_t)(y.x >> 16))};
         const uint32_t b[4] = {e4m3x2_to_f16x2((uint16_t)x.y), e4m3x2_to_f16x2((uint16_t)y.y),
                                e4m3x2_to_f16x2((uint16_t)(x.y >> 16)), e4m3x2_to_f16x2((uint16_t)(y.y >> 16))};
-        mma16816<false>(part, a, qb[2 * blk][0], qb[2 * blk][1]);
-        mma16816<false>(part, b, qb[2 * blk + 1][0], qb[2 * blk + 1][1]);
         const float f0 = pow2_exact((int)((e0 >> (8 * blk)) & 0xFF) - 127), f1 = pow2_exact((int)((e1 >> (8 * blk)) & 0xFF) - 127);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = fmaf(part[e], e >> 1 ? f1 : f0, s[e]);
+        for (int w = 0; w < QT; ++w) {
+          float part[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816<false>(part, a, qb[w][2 * blk][0], qb[w][2 * blk][1]);
+          mma16816<false>(part, b, qb[w][2 * blk + 1][0], qb[w][2 * blk + 1][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[w][e] = fmaf(part[e], e >> 1 ? f1 : f0, s[w][e]);
+        }
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] *= qf[e & 1];
+      for (int w = 0; w < QT; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[w][e] *= qf[2 * w + (e & 1)];
     } else {
 #pragma unroll
       for (int u = 0; u < D / 32; ++u) {
         const uint4 x = *reinterpret_cast<const uint4*>(st + g * C::KB + k_chunk<KE, C::KB>(4 * u + c4, g) * 16);
         const uint4 y = *reinterpret_cast<const uint4*>(st + (g + 8) * C::KB + k_chunk<KE, C::KB>(4 * u + c4, g + 8) * 16);
         const uint32_t a[4] = {x.x, y.x, x.y, y.y}, b[4] = {x.z, y.z, x.w, y.w};
-        mma16816<true>(s, a, qb[2 * u][0], qb[2 * u][1]);
-        mma16816<true>(s1, b, qb[2 * u + 1][0], qb[2 * u + 1][1]);
+#pragma unroll
+        for (int w = 0; w < QT; ++w) {
+          mma16816<true>(s[w], a, qb[w][2 * u][0], qb[w][2 * u][1]);
+          mma16816<true>(s1[w], b, qb[w][2 * u + 1][0], qb[w][2 * u + 1][1]);
+        }
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] = (s[e] + s1[e]) * qf[e & 1];
+      for (int w = 0; w < QT; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[w][e] = (s[w][e] + s1[w][e]) * qf[2 * w + (e & 1)];
     }
     // does every query see all 16 keys?
     const int last = key0 + kRowKeys - 1;
     const bool part = !(last <= t.pos0 && (p.window <= 0 || key0 > t.pos0 + t.ntok - 1 - p.window || last < p.sinks));
-    bool see[4] = {true, true, true, true};
+    bool see[QT][4];
+#pragma unroll
+    for (int w = 0; w < QT; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) see[w][e] = true;
     if (part) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        see[e] = chunk_sees(p, qpos[e & 1], key0 + g + 8 * (e >> 1));
-        if (!see[e]) s[e] = -INFINITY;
-      }
+      for (int w = 0; w < QT; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          see[w][e] = chunk_sees(p, qpos[2 * w + (e & 1)], key0 + g + 8 * (e >> 1));
+          if (!see[w][e]) s[w][e] = -INFINITY;
+        }
     }
-    float mt[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
     // The reference moves only when the maximum grows by more than 2^8, kp only
     // up, and O with them: rare behind the first groups, one vote on what each
     // lane sees skips it, and the query's maximum is joined only then.
     const float v0 = VB16 ? 0.f : vsc[g], v1 = VB16 ? 0.f : vsc[g + 8];
-    bool moved = mt[0] > m[0] + 8.f || mt[1] > m[1] + 8.f;
-    if constexpr (!VB16) moved = moved || fmaxf(v0, v1) >= fminf(vm_top[0], vm_top[1]);
+    bool moved = false;
+#pragma unroll
+    for (int i = 0; i < QC; ++i) {
+      moved = moved || fmaxf(s[i >> 1][i & 1], s[i >> 1][2 + (i & 1)]) > m[i] + 8.f;
+      if constexpr (!VB16) moved = moved || fmaxf(v0, v1) >= vm_top[i];
+    }
     if (__any_sync(0xffffffffu, moved)) {
-      float alpha[2] = {1.f, 1.f};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < QC; ++i) {
+        const int w = i >> 1, j = i & 1;
+        float alpha = 1.f, mt = fmaxf(s[w][j], s[w][2 + j]);
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) mt[i] = fmaxf(mt[i], __shfl_xor_sync(0xffffffffu, mt[i], x));
-        if (mt[i] > m[i] + 8.f) {
-          alpha[i] = ex2(m[i] - mt[i]);        // (0 for the first)
-          m[i] = mt[i];
-          l[i] *= alpha[i];
+        for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+        if (mt > m[i] + 8.f) {
+          alpha = ex2(m[i] - mt);              // (0 for the first)
+          m[i] = mt;
+          l[i] *= alpha;
         }
         if constexpr (!VB16) {                 // the largest finite value scale among the keys the query sees
-          float vm = fmaxf(see[i] && v0 < INFINITY ? v0 : 0.f, see[2 + i] && v1 < INFINITY ? v1 : 0.f);
+          float vm = fmaxf(see[w][j] && v0 < INFINITY ? v0 : 0.f, see[w][2 + j] && v1 < INFINITY ? v1 : 0.f);
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, x));
           if (vm >= vm_top[i]) {
             const int need = max(-100, min(100, ((__float_as_int(vm) >> 23) & 0xFF) - 127 - 6));   // vm 2^-need < 2^7
-            alpha[i] *= pow2i(max(-126, (__float_as_int(up2[i]) >> 23) - 127 - need));
+            alpha *= pow2i(max(-126, (__float_as_int(up2[i]) >> 23) - 127 - need));
             up2[i] = pow2i(need);
             vm_top[i] = pow2i(need + 7);
           }
         }
         neg_m[i] = (m[i] == -INFINITY ? 0.f : -m[i]) - (float)((__float_as_int(up2[i]) >> 23) - 127);
-      }
 #pragma unroll
-      for (int u = 0; u < KS; ++u) {
-        o[u][0] *= alpha[0]; o[u][1] *= alpha[1];
-        o[u][2] *= alpha[0]; o[u][3] *= alpha[1];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      s[i] = ex2_ftz(s[i] + neg_m[i]);
-      s[2 + i] = ex2_ftz(s[2 + i] + neg_m[i]);
-      l[i] = fmaf(s[i] + s[2 + i], up2[i], l[i]);
-      if constexpr (!VB16) {
-        s[i] *= v0;
-        s[2 + i] *= v1;
-        if (part) {                            // an unseen key's scale may be anything
-          s[i] = see[i] ? s[i] : 0.f;
-          s[2 + i] = see[2 + i] ? s[2 + i] : 0.f;
+        for (int u = 0; u < KS; ++u) {
+          o[w][u][j] *= alpha;
+          o[w][u][2 + j] *= alpha;
         }
       }
     }
-    // P^T as a B fragment: keys 2 c4, + 1 (and + 8) of query g
-    const uint32_t b0 = transpose8(pack16<VB16>(s[0], s[1])), b1 = transpose8(pack16<VB16>(s[2], s[3]));
+#pragma unroll
+    for (int i = 0; i < QC; ++i) {
+      const int w = i >> 1, j = i & 1;
+      s[w][j] = ex2_ftz(s[w][j] + neg_m[i]);
+      s[w][2 + j] = ex2_ftz(s[w][2 + j] + neg_m[i]);
+      l[i] = fmaf(s[w][j] + s[w][2 + j], up2[i], l[i]);
+      if constexpr (!VB16) {
+        s[w][j] *= v0;
+        s[w][2 + j] *= v1;
+        if (part) {                            // an unseen key's scale may be anything
+          s[w][j] = see[w][j] ? s[w][j] : 0.f;
+          s[w][2 + j] = see[w][2 + j] ? s[w][2 + j] : 0.f;
+        }
+      }
+    }
+    // P^T as B fragments: keys 2 c4, + 1 (and + 8) of queries g (and g + 8)
+    uint32_t pb[QT][2];
+#pragma unroll
+    for (int w = 0; w < QT; ++w) {
+      pb[w][0] = transpose8(pack16<VB16>(s[w][0], s[w][1]));
+      pb[w][1] = transpose8(pack16<VB16>(s[w][2], s[w][3]));
+    }
     bool aside = false;                        // values that must not meet an unseeing query's zero weight
     if (part && t.ntok > 1) {
       constexpr int VC = C::VB / 16;
@@ -367,34 +426,38 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
 #pragma unroll
           for (int e = 0; e < 4; ++e) a[k][e] = SetAside<VB16>(a[k][e]).clean;
         }
-        mma16816<VB16>(o[MT * u + k], a[k], b0, b1);
+#pragma unroll
+        for (int w = 0; w < QT; ++w) mma16816<VB16>(o[w][MT * u + k], a[k], pb[w][0], pb[w][1]);
       }
     }
     if (aside) {                               // rare: which queries see the values set aside
-      const uint32_t z0 = transpose8(pack16<VB16>(see[0] ? 1.f : 0.f, see[1] ? 1.f : 0.f));
-      const uint32_t z1 = transpose8(pack16<VB16>(see[2] ? 1.f : 0.f, see[3] ? 1.f : 0.f));
 #pragma unroll
-      for (int u = 0; u < C::VB / 32; ++u) {
-        uint32_t a[2][4];
-        load_v(u, a);
+      for (int w = 0; w < QT; ++w) {
+        const uint32_t z0 = transpose8(pack16<VB16>(see[w][0] ? 1.f : 0.f, see[w][1] ? 1.f : 0.f));
+        const uint32_t z1 = transpose8(pack16<VB16>(see[w][2] ? 1.f : 0.f, see[w][3] ? 1.f : 0.f));
 #pragma unroll
-        for (int k = 0; k < MT; ++k) {
-          uint32_t an[4], ap[4], am[4];
+        for (int u = 0; u < C::VB / 32; ++u) {
+          uint32_t a[2][4];
+          load_v(u, a);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const SetAside<VB16> x(a[k][e]);
-            an[e] = x.nan; ap[e] = x.pinf; am[e] = x.ninf;
-          }
-          float nan[4] = {0.f, 0.f, 0.f, 0.f}, pinf[4] = {0.f, 0.f, 0.f, 0.f}, ninf[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816<VB16>(nan, an, z0, z1);
-          mma16816<VB16>(pinf, ap, z0, z1);
-          mma16816<VB16>(ninf, am, z0, z1);
+          for (int k = 0; k < MT; ++k) {
+            uint32_t an[4], ap[4], am[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float& acc = o[MT * u + k][e];
-            if (pinf[e] > 0.f) acc += INFINITY;
-            if (ninf[e] > 0.f) acc -= INFINITY;
-            if (nan[e] > 0.f) acc = NAN;
+            for (int e = 0; e < 4; ++e) {
+              const SetAside<VB16> x(a[k][e]);
+              an[e] = x.nan; ap[e] = x.pinf; am[e] = x.ninf;
+            }
+            float nan[4] = {0.f, 0.f, 0.f, 0.f}, pinf[4] = {0.f, 0.f, 0.f, 0.f}, ninf[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816<VB16>(nan, an, z0, z1);
+            mma16816<VB16>(pinf, ap, z0, z1);
+            mma16816<VB16>(ninf, am, z0, z1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float& acc = o[w][MT * u + k][e];
+              if (pinf[e] > 0.f) acc += INFINITY;
+              if (ninf[e] > 0.f) acc -= INFINITY;
+              if (nan[e] > 0.f) acc = NAN;
+            }
           }
         }
       }
@@ -402,43 +465,43 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
   }
 
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < QC; ++i)
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
   // the four warps meet: [warp][query][D] in the rings' place
   cp_async_wait<0>();
   __syncthreads();
   float* osh = reinterpret_cast<float*>(rsm);
-  float* msh = osh + 32 * C::OS;
-  float* lsh = msh + 32;
+  float* msh = osh + 4 * QR * C::OS;
+  float* lsh = msh + 4 * QR;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = warp * 8 + 2 * c4 + i;
+  for (int i = 0; i < QC; ++i) {
+    const int r = warp * QR + col(i), w = i >> 1, j = i & 1;
     const float f = up2[i];
     if (g == 0) { msh[r] = m[i]; lsh[r] = l[i]; }
 #pragma unroll
     for (int u = 0; u < KS; ++u) {
       if constexpr (VB16) {
-        osh[r * C::OS + 16 * u + g] = o[u][i];      // (2^kp is 1)
-        osh[r * C::OS + 16 * u + 8 + g] = o[u][2 + i];
+        osh[r * C::OS + 16 * u + g] = o[w][u][j];      // (2^kp is 1)
+        osh[r * C::OS + 16 * u + 8 + g] = o[w][u][2 + j];
       } else {
-        *reinterpret_cast<float2*>(osh + r * C::OS + 16 * u + 2 * g) = make_float2(o[u][i] * f, o[u][2 + i] * f);
+        *reinterpret_cast<float2*>(osh + r * C::OS + 16 * u + 2 * g) = make_float2(o[w][u][j] * f, o[w][u][2 + j] * f);
       }
     }
   }
   __syncthreads();
-  for (int e = tid; e < 8 * (D / 4); e += kChunkThreads) {
+  for (int e = tid; e < QR * (D / 4); e += kChunkThreads) {
     const int r = e / (D / 4), d = (e % (D / 4)) * 4, tk = r / G;
     if (tk >= t.ntok || r >= p.tile_tokens * G) continue;
     float M = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) M = fmaxf(M, msh[8 * k + r]);
+    for (int k = 0; k < 4; ++k) M = fmaxf(M, msh[QR * k + r]);
     float L = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float w = chunk_weight(msh[8 * k + r], lsh[8 * k + r], M);
-      const float4 v = *reinterpret_cast<const float4*>(osh + (8 * k + r) * C::OS + d);
-      L = fmaf(w, lsh[8 * k + r], L);
+      const float w = chunk_weight(msh[QR * k + r], lsh[QR * k + r], M);
+      const float4 v = *reinterpret_cast<const float4*>(osh + (QR * k + r) * C::OS + d);
+      L = fmaf(w, lsh[QR * k + r], L);
       x[0] = fmaf(w, v.x, x[0]); x[1] = fmaf(w, v.y, x[1]);
       x[2] = fmaf(w, v.z, x[2]); x[3] = fmaf(w, v.w, x[3]);
     }
@@ -446,28 +509,30 @@ __global__ void __launch_bounds__(kChunkThreads, 4) chunk_rows(const ChunkParams
   }
 }
 
-template <int D, int KE, int VE>
+template <int D, int KE, int VE, int QT>
 static cudaError_t launch_one(const ChunkParams& p, dim3 grid, cudaStream_t st) {
-  constexpr int smem = RowsCfg<D, KE, VE>::BYTES;
-  const cudaError_t e = ensure_smem_optin((const void*)chunk_rows<D, KE, VE>, smem);
+  constexpr int smem = RowsCfg<D, KE, VE, QT>::BYTES;
+  const cudaError_t e = ensure_smem_optin((const void*)chunk_rows<D, KE, VE, QT>, smem);
   if (e != cudaSuccess) return e;
-  chunk_rows<D, KE, VE><<<grid, kChunkThreads, smem, st>>>(p);
+  chunk_rows<D, KE, VE, QT><<<grid, kChunkThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
-template <int D>
+template <int D, int QT>
 static cudaError_t launch_types(const ChunkParams& p, int dtype, dim3 grid, cudaStream_t st) {
   if constexpr (D == 128)     // (MXFP8 keys are built for head_dim 128)
-    if (dtype == FP8KV_MXK8V8) return launch_one<D, ELEM_MX, ELEM_E4M3>(p, grid, st);
-  if (dtype == FP8KV_K8V8) return launch_one<D, ELEM_E4M3, ELEM_E4M3>(p, grid, st);
-  if (dtype == FP8KV_K16V8) return launch_one<D, ELEM_BF16, ELEM_E4M3>(p, grid, st);
-  if (dtype == FP8KV_K8V16) return launch_one<D, ELEM_E4M3, ELEM_BF16>(p, grid, st);
-  return launch_one<D, ELEM_BF16, ELEM_BF16>(p, grid, st);
+    if (dtype == FP8KV_MXK8V8) return launch_one<D, ELEM_MX, ELEM_E4M3, QT>(p, grid, st);
+  if (dtype == FP8KV_K8V8) return launch_one<D, ELEM_E4M3, ELEM_E4M3, QT>(p, grid, st);
+  if (dtype == FP8KV_K16V8) return launch_one<D, ELEM_BF16, ELEM_E4M3, QT>(p, grid, st);
+  if (dtype == FP8KV_K8V16) return launch_one<D, ELEM_E4M3, ELEM_BF16, QT>(p, grid, st);
+  return launch_one<D, ELEM_BF16, ELEM_BF16, QT>(p, grid, st);
 }
 
 cudaError_t launch_chunk_rows(const ChunkParams& p, int dtype, int tiles, cudaStream_t st) {
   const dim3 grid(tiles, p.c.kv_heads, p.num_splits);
-  return p.c.head_dim == 128 ? launch_types<128>(p, dtype, grid, st) : launch_types<64>(p, dtype, grid, st);
+  if (p.tile_tokens * p.group > 8)
+    return p.c.head_dim == 128 ? launch_types<128, 2>(p, dtype, grid, st) : launch_types<64, 2>(p, dtype, grid, st);
+  return p.c.head_dim == 128 ? launch_types<128, 1>(p, dtype, grid, st) : launch_types<64, 1>(p, dtype, grid, st);
 }
 
 }  // namespace fp8kv

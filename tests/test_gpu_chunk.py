@@ -210,6 +210,48 @@ def test_groups(Hq, Hkv, kernel):
         run_case("k8v8", 128, Hq, Hkv, [70, 3, 0], new, 32, seed=3, kernel=kernel)
 
 
+@pytest.mark.parametrize("dtype,D", [("k8v8", 128), ("k16v8", 64), ("k8v16", 128), ("k16v16", 64), ("mxk8v8", 128)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (3, 1), (17, 40)])
+def test_nine_to_sixteen_rows(dtype, D, window, sinks):
+    """Tiles of two times eight query rows: 15 rows of 5 tokens x 3 heads, 11 and
+    16 of one token, 14 of 2 x 7, with scales that differ widely."""
+    for (Hq, Hkv), new in (((6, 2), [5, 4, 5, 5]), ((11, 1), [1] * 4), ((16, 1), [1, 0, 1, 2]), ((14, 2), [2] * 4)):
+        run_case(dtype, D, Hq, Hkv, [0, 200, 63, 530], new, 16, seed=41, window=window, sinks=sinks, spread=6.0)
+    run_case(dtype, D, 6, 2, [0, 200, 63, 530], [5, 4, 5, 5], 0, seed=42, window=window, sinks=sinks, splits=3,
+             out_dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", ["k8v8", "k16v16"])
+@pytest.mark.parametrize("Hq", [1, 2])
+@pytest.mark.parametrize("what", ["nan", "inf", "scale"])
+def test_few_rows_unseen_values(dtype, Hq, what):
+    """Values that are not finite at a position that some queries of an 8- or
+    16-row tile see and others do not; a huge value scale there."""
+    lens, new, window = [203], [8], 5
+    cache = make_cache(dtype, 128, 1, lens, 0, seed=43, poison=False)
+    q = torch.randn(8, Hq, 128, device="cuda").to(torch.bfloat16)
+    f = lambda: fk.fp8kv_chunk_attention(q, cache, _i32([0, 8]), _i32(lens), window=window, out_dtype=torch.float32)
+    ref = f().clone()
+    coded = dtype == "k8v8"
+    if what == "scale":
+        if not coded:
+            pytest.skip("bf16 values have no scales")
+        cache.v_scale[0, 0, 197] = float("inf")
+        cache.v[0, 0, 197] = 0x38
+    else:
+        cache.v[0, 0, 197, 5] = 0xFF if coded else float(what)
+    out = f()
+    assert fk.fp8kv_get_device_error() == 0
+    pos = torch.arange(195, 203)
+    sees = (pos >= 197) & (pos < 197 + window)
+    # the weights' two roundings (2^-11 or 2^-8 each) against other references
+    assert torch.isfinite(out[~sees]).all() and (out[~sees] - ref[~sees]).abs().max() <= 2.0 ** -7 * 4.5
+    assert not torch.isfinite(out[sees][..., 5]).any()
+    if what != "scale":
+        rest = [d for d in range(128) if d != 5]
+        assert (out[sees][..., rest] - ref[sees][..., rest]).abs().max() <= 2.0 ** -7 * 4.5
+
+
 @pytest.mark.parametrize("kernel", KERNELS)
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (63, 0), (64, 4), (65, 64), (100, 65), (130, 1000), (5000, 2), (2, 200)])
 def test_windows(window, sinks, kernel):
