@@ -434,7 +434,7 @@ def _rows(t, heads, dim, n, name, dev):
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != dim):
         raise ValueError(f"{name}: heads of a token must lie side by side, got strides {t.stride()}")
-    return t.data_ptr(), (s0 if n > 1 else max(s0, heads * dim))
+    return t.data_ptr(), (s0 if n > 1 else heads * dim)
 
 
 def fp8kv_rope_append(cache: Fp8KVCache, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos: torch.Tensor,

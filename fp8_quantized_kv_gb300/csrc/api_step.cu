@@ -20,6 +20,11 @@ bool overlap(const Range& a, const Range& b) {
 
 bool misaligned(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; }
 
+// Positions are 32-bit: a page table row may not hold more tokens.
+bool capacity_fits(const fp8kv_cache* c) {
+  return c->layout != FP8KV_LAYOUT_PAGED || (int64_t)c->max_pages_per_seq * c->page_size <= INT32_MAX;
+}
+
 struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 
 // How a chunk call runs, from its sizes (lengths are on the device).
@@ -54,7 +59,7 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   if (kernel != FP8KV_KERNEL_AUTO && kernel != FP8KV_KERNEL_WARP_MMA && kernel != FP8KV_KERNEL_TENSOR_CORES)
     return FP8KV_ERR_INVALID_ARG;
   const int G = q_heads / c->kv_heads;
-  if (G > 16 || c->rope_cos != nullptr || c->kv_heads > 65535 || num_splits > 4096) return FP8KV_ERR_UNSUPPORTED;
+  if (!capacity_fits(c) || G > 16 || c->rope_cos != nullptr || c->kv_heads > 65535 || num_splits > 4096) return FP8KV_ERR_UNSUPPORTED;
   if (total_q > INT32_MAX || (double)total_q * q_heads > 8.0 * INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
   const int64_t B = c->batch > 0 ? c->batch : 1;
   const int64_t rows = (total_q + B - 1) / B * G;
@@ -114,7 +119,7 @@ fp8kv_status fp8kv_build_tables(const fp8kv_cache* cache, const int32_t* cached_
   const fp8kv_status st = check_cache(cache, &view);
   if (st != FP8KV_OK) return st;
   if (n_rows < 0 || num_free < 0 || cu_new == nullptr) return FP8KV_ERR_INVALID_ARG;
-  if (cache->batch > kTablesMaxBatch || n_rows > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
+  if (!capacity_fits(cache) || cache->batch > kTablesMaxBatch || n_rows > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
   if (cache->batch > 0 && (!cached_lens || !new_lens || !seq_lens)) return FP8KV_ERR_INVALID_ARG;
   if (n_rows > 0 && (!seq_idx || !pos || !slots)) return FP8KV_ERR_INVALID_ARG;
   if (view.paged) {
@@ -271,6 +276,8 @@ fp8kv_status fp8kv_chunk_attention(const void* q, const fp8kv_cache* cache, cons
   const size_t need = fp8kv_chunk_workspace_bytes(cache, total_q, q_heads, window, sinks, num_splits, kernel);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FP8KV_ERR_WORKSPACE;
   if (need > 0 && misaligned(workspace, 16)) return FP8KV_ERR_INVALID_ARG;
+  for (const Range& r : {Range{q, 2 * values}, Range{out, (out_dtype == FP8KV_OUT_F32 ? 4 : 2) * values}})
+    if (overlap(r, {workspace, need})) return FP8KV_ERR_INVALID_ARG;
   p.err = device_error_ptr();
   if (!p.err) return FP8KV_ERR_CUDA;
   p.q = static_cast<const __nv_bfloat16*>(q);

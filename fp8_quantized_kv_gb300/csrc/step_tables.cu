@@ -111,8 +111,9 @@ __global__ void __launch_bounds__(kTablesThreads) build_tables_kernel(const Tabl
     }
   }
   const int i = blockIdx.x * kTablesThreads + tid;
-  // fresh page f
-  for (long long f = i; paged && f < base[p.batch]; f += (long long)gridDim.x * kTablesThreads) {
+  // fresh page f (placed sequences' pages end within the list)
+  const int pages = min(base[p.batch], avail);
+  for (long long f = i; paged && f < pages; f += (long long)gridDim.x * kTablesThreads) {
     int lo = 0, hi = p.batch - 1;                      // sequence with base[b] <= f < base[b + 1]
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;

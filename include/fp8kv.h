@@ -430,8 +430,9 @@ typedef enum {
  *                  q_stride = q_heads * head_dim
  * A row with a negative slot is padding: nothing is written for it.
  * A row whose position has no table entry (of cos and sin, or of the cache's
- * rope_cos if it has one) or whose slot lies outside the cache is skipped and raises SEQ_TOO_LONG or BAD_PAGE.  Two rows of one call
- * may not share a slot (which row's codes and scale stay is not defined). */
+ * rope_cos if it has one) or whose slot lies outside the cache is skipped and
+ * raises SEQ_TOO_LONG or BAD_PAGE.  Two rows of one call may not share a slot
+ * (which row's codes and scale stay is not defined). */
 FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q, int64_t q_stride,
                                          const void *k, int64_t k_stride, const void *v,
                                          int64_t v_stride, int32_t q_heads, const int32_t *pos,
@@ -463,8 +464,8 @@ FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q
  *               16); or _TENSOR_CORES (128-row tiles on tcgen05: head_dim 128,
  *               not FP8KV_MXK8V8, else FP8KV_ERR_UNSUPPORTED)
  *   workspace:  fp8kv_chunk_workspace_bytes() bytes, 16-byte aligned, nothing
- *               need be zero; NULL if that is 0.  Calls that may run at once
- *               need one each.
+ *               need be zero; NULL if that is 0; apart from q and out.
+ *               Calls that may run at once need one each.
  *   out:        [total_q][q_heads][head_dim], bf16 or fp32 per out_dtype,
  *               16-byte aligned, apart from q
  * A query that sees no key (its position is negative: seq_lens[b] is less than
@@ -472,8 +473,7 @@ FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q
  * have no influence on it, whatever they hold (NaN included; pages that no
  * query sees need not exist).  A seen value that is not finite makes that
  * element of the row not finite; the tensor-core kernel may make the whole row
- * NaN.  A length below
- * 0 or past the capacity raises SEQ_TOO_LONG and gives zero rows; offsets that
+ * NaN.  A length below 0 or past the capacity raises SEQ_TOO_LONG and gives zero rows; offsets that
  * decrease or pass total_q raise it and leave their rows as they were. */
 FP8KV_API fp8kv_status fp8kv_chunk_attention(const void *q, const fp8kv_cache *cache,
                                              const int32_t *cu_q, const int32_t *seq_lens,

@@ -146,6 +146,17 @@ def test_tables_out_of_pages():
     assert min(s[:20]) >= 0 and set(s[20:60]) == {-1} and min(s[60:63]) >= 0 and s[63] == -1
 
 
+def test_tables_far_more_pages_than_free():
+    """Requests for 2^23 pages with three free: nothing is placed, and the
+    pages that do not exist are not walked."""
+    table = torch.full((8, 1 << 20), -7, dtype=torch.int32)
+    cache = fk.Fp8KVCache.paged(table, 4, 1, 64, 16)
+    got = fk.fp8kv_build_tables(cache, _i32([0] * 8), _i32([16 << 20] * 8), 8, _i32([1, 2, 3]), _i32([0]))
+    assert fk.fp8kv_get_device_error() == fk.DEVERR_NO_PAGES | fk.DEVERR_SEQ_TOO_LONG
+    assert got["seq_lens"].tolist() == [0] * 8 and got["free_head"].tolist() == [0] and got["slots"].tolist() == [-1] * 8
+    assert bool((cache.page_table == -7).all())
+
+
 def test_tables_bad_ids_and_short_rows():
     page = 16
     cache = fk.Fp8KVCache.paged(torch.tensor([[99, -1], [0, -1]], dtype=torch.int32), 4, 1, 64, page)

@@ -54,6 +54,7 @@ def test_tables_refusals(lib, want, kw):
 def test_tables_refusals_by_cache(lib):
     assert _tables(lib, _paged(batch=16385)) == UNSUPPORTED
     assert _tables(lib, _paged(page_size=8)) == UNSUPPORTED
+    assert _tables(lib, _paged(max_pages_per_seq=1 << 27)) == UNSUPPORTED  # positions past 31 bits
     assert _tables(lib, _cache()) == INVALID                               # a free list with a contiguous cache
     assert _tables(lib, None) == INVALID
 
@@ -92,7 +93,7 @@ def test_rope_append_refusals(lib, want, kw):
     (INVALID, dict(q=0x10008)), (INVALID, dict(out=0x40008)), (INVALID, dict(cu=None)), (INVALID, dict(ws=0x30008)),
     (INVALID, dict(out=0x10000)), (INVALID, dict(out=0x10100)), (INVALID, dict(cu=0x20002)), (INVALID, dict(lens=0x21002)),
     (WORKSPACE, dict(ws=None)), (WORKSPACE, dict(ws_bytes=100)), (UNSUPPORTED, dict(q_heads=34)), (UNSUPPORTED, dict(total=1 << 31)),
-    (UNSUPPORTED, dict(splits=5000)),
+    (UNSUPPORTED, dict(splits=5000)), (INVALID, dict(ws=0x3f000)), (INVALID, dict(ws=0xf000)),      # workspace over out, over q
 ])
 def test_chunk_refusals(lib, want, kw):
     a = dict(q=0x10000, cu=0x20000, lens=0x21000, total=10, q_heads=4, sm=0.1, window=0, sinks=0, splits=2, kernel=0, ws=0x30000,
@@ -107,6 +108,7 @@ def test_chunk_refusals_by_cache(lib):
     turning = _cache(k_bias=0x8000, rope_cos=0x9000, rope_sin=0xA000, rope_positions=2048)
     assert lib.fp8kv_chunk_attention(0x10000, turning, *args) == UNSUPPORTED
     assert lib.fp8kv_chunk_attention(0x10000, None, *args) == INVALID
+    assert lib.fp8kv_chunk_attention(0x10000, _paged(max_pages_per_seq=1 << 27), *args) == UNSUPPORTED
     tc = args[:8] + (2,) + args[9:]
     for kw in (dict(head_dim=64), dict(dtype=4)):
         assert lib.fp8kv_chunk_attention(0x10000, _cache(**kw), *tc) == UNSUPPORTED
@@ -139,3 +141,9 @@ def test_python_argument_checks():
         fk.fp8kv_build_tables(cache, t, t, 4)
     with pytest.raises(ValueError, match="layout"):
         fk.fp8kv_rope_append(None, torch.zeros(1, 2, 64), None, None, t, t, t, t, layout="quarter")
+
+
+def test_stride_of_one_row():
+    """A single token's stride is never used: any slice of it will do."""
+    t = torch.zeros(256, dtype=torch.bfloat16).as_strided((1, 2, 128), (4100, 128, 1))
+    assert t.stride(0) == 4100 and fk._rows(t, 2, 128, 1, "k", -1)[1] == 256
