@@ -41,7 +41,8 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // each as long as one share and the 8 tiles' time that a CTA spends on its
 // start and end.  So the counts that fill one, two or three waves are compared:
 // 256 units of 32-64 tiles (16 rows) take 100 us whole, 84 us in 2 shares (1.1
-// waves), 75 us in 3 (1.7), 79 us in 4.  Shares are 256 keys or longer.
+// waves), 75 us in 3 (1.7), 79 us in 4.  Shares are 192 keys or longer (one token of
+// 32 / 8 heads over 6,200: 10.6 us in 32 shares, 11.1 in 24, 12.1 in 64).
 // Without a window lengths can differ widely: shares of about 4,096 keys at most
 // then even them out (64 sequences of 1K-16K tokens: 268 us in 4 shares, 355 us
 // whole; sequences of 700 tokens in the same cache pay 35 us instead of 23), as
@@ -88,7 +89,7 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
       if (want > most) want = most;
     } else if (units > 0) {
       const bool wide = c->head_dim == 128 && c->dtype == FP8KV_K16V16;
-      const int64_t held = (plan->tile_rows == 8 && !wide ? 4 : 3) * sms, most = kv_tiles / 4;
+      const int64_t held = (plan->tile_rows == 8 && !wide ? 4 : 3) * sms, most = kv_tiles / 3;
       int64_t even = seen == cap ? (kv_tiles + 63) / 64 : 1;
       if (even > 16 * sms / units) even = 16 * sms / units;
       if (even < 1) even = 1;

@@ -272,6 +272,15 @@ def test_splits(splits, kernel):
     assert (out[:33] - one[:33]).abs().max() <= 2.0 ** -10 * 4.5
 
 
+@pytest.mark.parametrize("dtype,D", [("k8v8", 64), ("k16v16", 128)])
+@pytest.mark.parametrize("splits", [4, 9, 33, 70])
+def test_joined_splits(dtype, D, splits):
+    """Few rows of many splits (a CTA's warps share a row's splits, some of them
+    empty), and many rows of as many (a warp a row)."""
+    run_case(dtype, D, 4, 2, [2000, 0, 90], [1, 0, 3], 16, seed=44, splits=splits)
+    run_case(dtype, D, 4, 1, [40, 900], [700, 30], 16, seed=45, splits=splits, out_dtype=torch.bfloat16)
+
+
 def test_bf16_output_and_no_offsets():
     """cu_q None is one query per sequence; a bf16 output is the fp32 one rounded."""
     lens = [1, 77, 640, 0, 129]
