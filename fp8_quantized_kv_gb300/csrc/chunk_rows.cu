@@ -468,8 +468,10 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
   for (int i = 0; i < QC; ++i)
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-  // (the kernel that joins the splits may be set up from here on: it waits for this one's end)
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  // The kernel that joins the splits may be set up from here on: it waits for
+  // this one's end.  Without splits the next kernel is a stranger, which may
+  // count on this one's results as soon as it starts.
+  if (p.num_splits > 1) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   // the four warps meet: [warp][query][D] in the rings' place
   cp_async_wait<0>();
   __syncthreads();

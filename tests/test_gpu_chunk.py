@@ -477,6 +477,36 @@ def test_offsets_past_32_bits():
     assert fk.fp8kv_get_device_error() == 0
 
 
+@pytest.mark.parametrize("splits", [1, 3, 9])
+def test_calls_in_a_chain(splits):
+    """Each call's queries are the last one's output and its workspace is shared:
+    a call starts when the one before is done, eager and from a graph."""
+    lens = [300, 17, 1200, 64]
+    cache = make_cache("k8v8", 128, 2, lens, 16, seed=46)
+    q = torch.randn(4, 8, 128, device="cuda").to(torch.bfloat16)
+    a, b = torch.empty_like(q), torch.empty_like(q)
+    ws = torch.empty(fk.fp8kv_chunk_workspace_bytes(cache, 4, 8, num_splits=splits) + 16, dtype=torch.uint8, device="cuda")
+    sl = _i32(lens)
+
+    def chain(wait):
+        x = q
+        for i in range(12):
+            x = fk.fp8kv_chunk_attention(x, cache, None, sl, num_splits=splits, out=(a, b)[i & 1], workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        return x
+
+    want = chain(True).clone()
+    assert torch.equal(chain(False), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = chain(False)
+    for _ in range(20):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and fk.fp8kv_get_device_error() == 0
+
+
 def test_graphs_and_streams():
     """Two captured calls with a workspace each, replayed on two streams, with
     lengths that change between replays."""
