@@ -31,10 +31,15 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // Kernel, by the average number of query rows (queries x heads of a group) a
 // sequence has: up to 16 rows the few-row kernel, in tiles of 8 or 16 (one token
 // of 64 sequences under a 1,024-token window: 36 us, against 81 us on tcgen05; two
-// tokens x 8 heads of 64 sequences of 2K-4K tokens: 75 us, against 101 us);
+// tokens x 8 heads of 64 sequences of 2K-4K tokens: 74 us, against 101 us);
 // above, tcgen05 where it is built (8 tokens x 4 heads over 8,000 tokens, 4
 // sequences: 40 us against 45 us at the best split counts; 256 x 4 over 16,000:
-// 108 against 447), else the warp-level kernel.
+// 108 against 447).  Block-scaled keys stay on the few-row kernel (2-4 x 8 over
+// 4K-8K, 16 sequences: 63 us, 88 us on the form that the warp-level kernel had for
+// them; 256-512 x 8, 4 sequences: 1.15 ms against 1.33), head dim 64 does up to 32
+// rows (2-4 x 8 of 64 sequences of 2K-4K, bf16: 64 us against 71 on 64-row tiles at
+// the best split count), with more it runs on the warp-level kernel (256-512 x 8 over
+// 4K-8K, 4 sequences: 0.56 ms against 0.70; around 64 rows either can be faster).
 //
 // Splits of the few-row kernel: an SM holds four of its CTAs (three of 16 rows,
 // or of 32 KiB stages), and a call takes as many waves of them as they need,
@@ -49,10 +54,9 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // long as that makes no more than 16 CTAs an SM.
 //
 // Splits of the others: tiles are few -> one wave.  tcgen05: two CTAs an SM,
-// shares of 512 keys or longer.  Warp-level kernel: two an SM and 256 keys, at
-// head dim 64 three (by their registers) and 128 (2-4 tokens x 8 heads, 16
-// sequences of 4K-8K tokens: 62 us in 4 shares, 51 us in 6, 43 us in 8; 32-64 x 8
-// of 2 sequences of 2K-4K: 36 us in 4, 31 us in 6, 37 us in 9, past one wave).
+// shares of 512 keys or longer.  Warp-level kernel: three an SM (by their
+// registers) and 128 keys (32-64 x 8 of 2 sequences of 2K-4K tokens: 36 us in 4
+// shares, 31 us in 6, 37 us in 9, past one wave).
 fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int window, int sinks, int num_splits,
                         int kernel, ChunkPlan* plan) {
   if (total_q < 0 || q_heads <= 0 || q_heads % c->kv_heads != 0 || window < 0 || sinks < 0 || num_splits < 0)
@@ -70,7 +74,7 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   // (a cache without room has no tensor map; its calls only write zero rows)
   const bool tc = cap > 0 && (kernel == FP8KV_KERNEL_TENSOR_CORES || (kernel == FP8KV_KERNEL_AUTO && tc_built && rows > 16));
   plan->kernel = tc ? FP8KV_KERNEL_TENSOR_CORES : FP8KV_KERNEL_WARP_MMA;
-  plan->tile_rows = tc ? 128 : rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  plan->tile_rows = tc ? 128 : rows <= 8 ? 8 : c->head_dim == 128 || rows <= 32 ? 16 : 64;
   plan->tile_tokens = plan->tile_rows / G;
   const int64_t tiles = total_q / plan->tile_tokens + c->batch;      // at most (chunk_common.cuh)
   if (tiles > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
@@ -79,13 +83,14 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   const int64_t kv_tiles = ((seen < cap ? seen : cap) + 63) / 64 + 1;
   int64_t want = num_splits;
   if (want == 0) {
-    // tiles if every sequence had the average number of queries
-    const int64_t units = B * (((total_q + B - 1) / B + plan->tile_tokens - 1) / plan->tile_tokens) * c->kv_heads;
+    // tiles if every sequence had the average number of queries, or, if that is
+    // not a whole number, as many more or fewer of them as it says
+    const int64_t T = plan->tile_tokens, even_q = (total_q / B + T - 1) / T * B, some_q = (total_q + T - 1) / T;
+    const int64_t units = (total_q % B == 0 ? even_q : some_q > B ? some_q : B) * c->kv_heads;
     const int64_t sms = sm_count();
     if (plan->tile_rows > 16) {
-      const bool narrow = c->head_dim == 64;
-      want = units > 0 ? (narrow ? 3 : 2) * sms / units : 1;
-      const int64_t most = kv_tiles / (tc ? 8 : narrow ? 2 : 4);
+      want = units > 0 ? (tc ? 2 : 3) * sms / units : 1;
+      const int64_t most = kv_tiles / (tc ? 8 : 2);
       if (want > most) want = most;
     } else if (units > 0) {
       const bool wide = c->head_dim == 128 && c->dtype == FP8KV_K16V16;
@@ -301,7 +306,7 @@ fp8kv_status fp8kv_chunk_attention(const void* q, const fp8kv_cache* cache, cons
   const int tiles = cu_q ? plan.tiles : cache->batch;
   cudaError_t e = plan.kernel == FP8KV_KERNEL_TENSOR_CORES ? launch_chunk_tc(p, cache->dtype, tiles, s)
                   : plan.tile_rows <= 16 ? launch_chunk_rows(p, cache->dtype, tiles, s)
-                                        : launch_chunk_mma(p, cache->dtype, plan.tile_rows / 16, tiles, s);
+                                        : launch_chunk_mma(p, cache->dtype, tiles, s);
   if (e == cudaSuccess && plan.splits > 1) e = launch_chunk_merge(p, s);
   return cuda_status(e);
 }

@@ -1,34 +1,32 @@
 // chunk_mma.cu -- ragged chunk attention over the cache on warp-level matrix
-// instructions, for every cache type and head dim: the form for what the
-// tcgen05 kernel is not built for (head dim 64, block-scaled keys) and the
-// few-row kernel does not take (more than sixteen query rows a sequence).
+// instructions, for head dim 64 and many query rows (more than 32 a sequence);
+// and the kernel that joins the splits of all chunk kernels.
 //
 // One pass over the keys with a running maximum m, sum l and output O:
 //   s = (q . k) k_scale sm_scale log2(e),  m' = max(m, max s),
 //   l = l 2^(m - m') + sum 2^(s - m'),     O = O 2^(m - m') + 2^(s - m') V
-// 128 threads; a CTA owns 16 MW query rows of one KV head (rows = tokens x
-// heads of the group) and walks 64-key tiles through a ring of NS cp.async
-// stages.  MW = 4: a warp owns 16 rows and all keys of a tile.  MW = 2: two warps
-// split a tile's keys and join their (m, l, O) at the end, so a tile with few
-// rows still keeps four warps busy.
+// 128 threads; a CTA owns 64 query rows of one KV head (rows = tokens x heads of
+// the group), a warp 16 of them, and walks 64-key tiles through a ring of three
+// cp.async stages.
 //
 // Operands.  e4m3 codes convert to f16 exactly, so QK runs in f16 with each
 // bf16 query row scaled by a power of two to put its largest element in
 // [2^14, 2^15): elements 2^-29 and more below it lose bits, an error of 2^-39
 // of the largest.  The scale comes back in fp32.  bf16 keys meet the bf16
-// query as they are.  Block-scaled keys: the four 32-element partial products
-// are scaled in fp32 and added.  The order of a row's elements inside a dot
-// product is free, so a lane takes the 16 (or 8) bytes that lie together and
-// the query fragments use the same order: no shuffles, no transposition of K.
+// query as they are.  The order of a row's elements inside a dot product is
+// free, so a lane takes the 16 bytes that lie together and the query fragments
+// use the same order: no shuffles, no transposition of K.
 // P (16 bits, the one rounding of the softmax) is f16 next to e4m3 values,
 // with the value scale folded in and a power of two 2^-kp that follows the
 // largest value scale the row sees (O is rescaled when it rises), and bf16 next to
 // bf16 values.  m, l and O are fp32.
 //
-// What bounds it: instruction issue.  3,727 queries over 2,000-8,000 tokens (28 /
-// 4 heads, head dim 128, e4m3) take 1.28 ms, 151 TFLOP/s (conversions of codes
-// are repeated by each of a tile's four warps); 16 queries over 100 tokens at
-// head dim 64 take 7.2 us, the latency of a launch and a few dependent loads.
+// What bounds it: instruction issue (conversions of codes are repeated by each
+// of a tile's four warps).  4 sequences of 256-512 queries over 4,000-8,000 tokens
+// (32 / 4 heads, e4m3) take 0.56 ms; the few-row kernel, whose 16-row tiles read
+// the cache four times as often, 0.70 ms.  (At head dim 128, block-scaled keys,
+// the same call took 1.33 ms in this form and 1.15 ms there: 128 fp32 of O and
+// wider fragments left two CTAs an SM, so that form is gone.)
 //
 // Keys that a query does not see get no weight, whatever their rows hold:
 // rows that no query of the tile sees are not read at all, and in a tile that
@@ -38,30 +36,26 @@
 
 namespace fp8kv {
 
-template <int D, int KE, int VE>
+template <int KE, int VE>
 struct ChunkCfg {
+  static constexpr int D = 64;
   static constexpr int KB = KE == ELEM_BF16 ? 2 * D : D;       // bytes of a K row
   static constexpr int VB = VE == ELEM_BF16 ? 2 * D : D;
   static constexpr int SC = KE == ELEM_BF16 && VE == ELEM_BF16 ? 0 : 2 * kChunkKeys * 4;
   static constexpr int STAGE = kChunkKeys * (KB + VB) + SC;
   static constexpr int NS = 3;
-  static constexpr int OS = D + 4;                             // fp32 row stride of the join buffer
-  static constexpr int JOIN = 64 * OS * 4 + 2 * 64 * 4;
-  static constexpr int BYTES = (NS * STAGE > JOIN ? NS * STAGE : JOIN) + 4 * kChunkKeys * 4;
+  static constexpr int BYTES = NS * STAGE + 4 * kChunkKeys * 4;
 };
 
-template <int D, int KE, int VE, int MW>
+template <int KE, int VE>
 __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) {
-  using C = ChunkCfg<D, KE, VE>;
-  constexpr int NKB = 4 / MW;                  // key blocks of a tile (warps that share rows)
-  constexpr int KPW = kChunkKeys / NKB;        // keys of a tile per warp
-  constexpr int NT = KPW / 8;                  // 8-key score tiles per warp
+  using C = ChunkCfg<KE, VE>;
+  constexpr int D = C::D, NT = kChunkKeys / 8; // 8-key score tiles
   constexpr bool KB16 = KE == ELEM_BF16, VB16 = VE == ELEM_BF16;
   extern __shared__ __align__(128) uint8_t csm[];
   int* rows_sh = reinterpret_cast<int*>(csm + (C::BYTES - 4 * kChunkKeys * 4));   // [4][64] cache rows of coming tiles
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
-  const int wm = warp % MW, kb0 = (warp / MW) * KPW;
   const int hk = blockIdx.y, split = blockIdx.z;
   ChunkTile t;
   // the last tiles of a sequence see the most keys: they start first
@@ -113,7 +107,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
   const uint4* qsrc[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int r = wm * 16 + g + 8 * i, tok = r / G;
+    const int r = warp * 16 + g + 8 * i, tok = r / G;
     const bool live = tok < t.ntok && r < p.tile_tokens * G;
     qpos[i] = live ? t.pos0 + tok : -1;
     qrow[i] = live ? (int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G) : -1;
@@ -183,11 +177,11 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
     const float* vsc = ksc + kChunkKeys;
     const int key0 = chunk_key0(t, j0 + it);
 
-    // scores: s[n] holds rows g, g + 8 and keys kb0 + 8 n + 2 c4, + 1
+    // scores: s[n] holds rows g, g + 8 and keys 8 n + 2 c4, + 1
     float s[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const int kr = kb0 + 8 * n + g, kc = kb0 + 8 * n + 2 * c4;
+      const int kr = 8 * n + g, kc = 8 * n + 2 * c4;
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
       if constexpr (KE == ELEM_E4M3) {
@@ -203,22 +197,6 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
         const float s0 = sc.x * p.scale_log2, s1 = sc.y * p.scale_log2;
         s[n][0] *= s0 * qf[0]; s[n][1] *= s1 * qf[0];
         s[n][2] *= s0 * qf[1]; s[n][3] *= s1 * qf[1];
-      } else if constexpr (KE == ELEM_MX) {
-        const uint2 e8 = *reinterpret_cast<const uint2*>(ksc + kc);
-#pragma unroll
-        for (int blk = 0; blk < D / 32; ++blk) {
-          const uint2 w = *reinterpret_cast<const uint2*>(st + kr * C::KB + k_chunk<KE, C::KB>(2 * blk + (c4 >> 1), kr) * 16 +
-                                                          (c4 & 1) * 8);
-          float part[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816<false>(part, qa[2 * blk], e4m3x2_to_f16x2((uint16_t)w.x), e4m3x2_to_f16x2((uint16_t)(w.x >> 16)));
-          mma16816<false>(part, qa[2 * blk + 1], e4m3x2_to_f16x2((uint16_t)w.y), e4m3x2_to_f16x2((uint16_t)(w.y >> 16)));
-          const float b0 = pow2_exact((int)((e8.x >> (8 * blk)) & 0xFF) - 127);
-          const float b1 = pow2_exact((int)((e8.y >> (8 * blk)) & 0xFF) - 127);
-          s[n][0] = fmaf(part[0], b0, s[n][0]); s[n][1] = fmaf(part[1], b1, s[n][1]);
-          s[n][2] = fmaf(part[2], b0, s[n][2]); s[n][3] = fmaf(part[3], b1, s[n][3]);
-        }
-        s[n][0] *= p.scale_log2 * qf[0]; s[n][1] *= p.scale_log2 * qf[0];
-        s[n][2] *= p.scale_log2 * qf[1]; s[n][3] *= p.scale_log2 * qf[1];
       } else {
 #pragma unroll
         for (int u = 0; u < D / 32; ++u) {
@@ -236,7 +214,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (!chunk_sees(p, qpos[e >> 1], key0 + kb0 + 8 * n + 2 * c4 + (e & 1))) s[n][e] = -INFINITY;
+          if (!chunk_sees(p, qpos[e >> 1], key0 + 8 * n + 2 * c4 + (e & 1))) s[n][e] = -INFINITY;
     }
     // running maximum and weights
     float alpha[2];
@@ -264,9 +242,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
       auto finite = [](float v) { return v < INFINITY ? v : 0.f; };
       float vm[2];
       if (!part) {
-        float v = finite(vsc[kb0 + (lane & (KPW - 1))]);
-        if constexpr (KPW == 64) v = fmaxf(v, finite(vsc[lane + 32]));
-        vm[0] = vm[1] = warp_max_f32(v);
+        vm[0] = vm[1] = warp_max_f32(fmaxf(finite(vsc[lane]), finite(vsc[lane + 32])));
       } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -275,7 +251,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int kc = kb0 + 8 * n + 2 * c4 + e;
+              const int kc = 8 * n + 2 * c4 + e;
               if (chunk_sees(p, qpos[i], key0 + kc)) vm[i] = fmaxf(vm[i], finite(vsc[kc]));
             }
           vm[i] = fmaxf(vm[i], __shfl_xor_sync(0xffffffffu, vm[i], 1));
@@ -294,12 +270,12 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float2 v = *reinterpret_cast<const float2*>(vsc + kb0 + 8 * n + 2 * c4);
+        const float2 v = *reinterpret_cast<const float2*>(vsc + 8 * n + 2 * c4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float w = s[n][e] * ((e & 1 ? v.y : v.x) * vf[e >> 1]);
           // a scale that is not finite would turn an unseen key's zero into NaN
-          s[n][e] = part && !chunk_sees(p, qpos[e >> 1], key0 + kb0 + 8 * n + 2 * c4 + (e & 1)) ? 0.f : w;
+          s[n][e] = part && !chunk_sees(p, qpos[e >> 1], key0 + 8 * n + 2 * c4 + (e & 1)) ? 0.f : w;
         }
       }
     }
@@ -315,8 +291,8 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
     bool aside = false;
     if (part && t.ntok > 1) {
       constexpr int VC = C::VB / 16;
-      for (int e = lane; e < KPW * VC; e += 32) {
-        const uint4 w = *reinterpret_cast<const uint4*>(vst + (kb0 + e / VC) * C::VB + (e % VC) * 16);
+      for (int e = lane; e < kChunkKeys * VC; e += 32) {
+        const uint4 w = *reinterpret_cast<const uint4*>(vst + e / VC * C::VB + (e % VC) * 16);
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -331,10 +307,10 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
     // O += P V: 16 keys at a time
     const uint32_t vaddr = umma::smem_u32(vst);
 #pragma unroll
-    for (int j = 0; j < KPW / 16; ++j) {
+    for (int j = 0; j < kChunkKeys / 16; ++j) {
       const uint32_t pa[4] = {pack16<VB16>(s[2 * j][0], s[2 * j][1]), pack16<VB16>(s[2 * j][2], s[2 * j][3]),
                               pack16<VB16>(s[2 * j + 1][0], s[2 * j + 1][1]), pack16<VB16>(s[2 * j + 1][2], s[2 * j + 1][3])};
-      const int vr = kb0 + 16 * j + (lane & 15);       // row this lane addresses for ldmatrix
+      const int vr = 16 * j + (lane & 15);       // row this lane addresses for ldmatrix
 #pragma unroll
       for (int u = 0; u < C::VB / 32; ++u) {
         uint32_t r[4];
@@ -369,11 +345,11 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
     }
     if (aside) {                               // rare: which queries see the values set aside
 #pragma unroll
-      for (int j = 0; j < KPW / 16; ++j) {
+      for (int j = 0; j < kChunkKeys / 16; ++j) {
         uint32_t see[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int key = key0 + kb0 + 16 * j + 8 * (k >> 1) + 2 * c4, pos = qpos[k & 1];
+          const int key = key0 + 16 * j + 8 * (k >> 1) + 2 * c4, pos = qpos[k & 1];
           see[k] = pack16<VB16>(chunk_sees(p, pos, key) ? 1.f : 0.f, chunk_sees(p, pos, key + 1) ? 1.f : 0.f);
         }
         auto add = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
@@ -389,7 +365,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
             if (nan[e] > 0.f) acc[e] = NAN;
           }
         };
-        const int vr = kb0 + 16 * j + (lane & 15);
+        const int vr = 16 * j + (lane & 15);
 #pragma unroll
         for (int u = 0; u < C::VB / 32; ++u) {
           uint32_t r[4];
@@ -426,59 +402,25 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
       for (int e = 0; e < 4; ++e) o[n][e] *= f[e >> 1];
   }
   // four neighbouring elements of row g + 8 i: e4m3 values interleave two
-  // accumulator tiles, bf16 values have two neighbours in each
-  if constexpr (MW == 4 && !VB16) {
+  // accumulator tiles; bf16 values have two neighbours in each, and lanes 2 c
+  // and 2 c + 1 swap a pair
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (qrow[i] >= 0)
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int u = 0; u < D / 16; ++u) {
-          const float x[4] = {o[2 * u][2 * i], o[2 * u + 1][2 * i], o[2 * u][2 * i + 1], o[2 * u + 1][2 * i + 1]};
-          chunk_store(p, qrow[i], split, D, 16 * u + 4 * c4, x, m[i], l[i]);
-        }
-  } else {
-    cp_async_wait<0>();
-    __syncthreads();                           // the ring is free: rows of all warps meet in shared memory
-    float* osh = reinterpret_cast<float*>(csm);
-    float* msh = osh + 64 * C::OS;
-    float* lsh = msh + 64;
-    const int at = (warp / MW) * 16 * MW + wm * 16;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = at + g + 8 * i;
-      float* dst = osh + r * C::OS;
-      if (c4 == 0) { msh[r] = m[i]; lsh[r] = l[i]; }
+    for (int u = 0; u < D / 16; ++u) {
+      float x[4] = {o[2 * u][2 * i], o[2 * u + 1][2 * i], o[2 * u][2 * i + 1], o[2 * u + 1][2 * i + 1]};
+      int d = 16 * u + 4 * c4;
       if constexpr (VB16) {
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-          *reinterpret_cast<float2*>(dst + 8 * n + 2 * c4) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
-      } else {
-#pragma unroll
-        for (int u = 0; u < D / 16; ++u)
-          *reinterpret_cast<float4*>(dst + 16 * u + 4 * c4) =
-              make_float4(o[2 * u][2 * i], o[2 * u + 1][2 * i], o[2 * u][2 * i + 1], o[2 * u + 1][2 * i + 1]);
+        const bool odd = c4 & 1;
+        const float a = __shfl_xor_sync(0xffffffffu, odd ? x[0] : x[1], 1);
+        const float b = __shfl_xor_sync(0xffffffffu, odd ? x[2] : x[3], 1);
+        const float own[2] = {odd ? x[1] : x[0], odd ? x[3] : x[2]};
+        x[0] = odd ? a : own[0]; x[1] = odd ? b : own[1];
+        x[2] = odd ? own[0] : a; x[3] = odd ? own[1] : b;
+        d = 16 * u + (odd ? 8 : 0) + 4 * (c4 >> 1);
       }
+      if (qrow[i] >= 0) chunk_store(p, qrow[i], split, D, d, x, m[i], l[i]);
     }
-    __syncthreads();
-    for (int e = tid; e < 16 * MW * (D / 4); e += kChunkThreads) {
-      const int r = e / (D / 4), d = (e % (D / 4)) * 4, tok = r / G;
-      if (tok >= t.ntok || r >= p.tile_tokens * G) continue;
-      float M = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < NKB; ++k) M = fmaxf(M, msh[k * 16 * MW + r]);
-      float L = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int k = 0; k < NKB; ++k) {
-        const int kr = k * 16 * MW + r;
-        const float w = chunk_weight(msh[kr], lsh[kr], M);
-        const float4 v = *reinterpret_cast<const float4*>(osh + kr * C::OS + d);
-        L = fmaf(w, lsh[kr], L);
-        x[0] = fmaf(w, v.x, x[0]); x[1] = fmaf(w, v.y, x[1]);
-        x[2] = fmaf(w, v.z, x[2]); x[3] = fmaf(w, v.w, x[3]);
-      }
-      chunk_store(p, (int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G), split, D, d, x, M, L);
-    }
-  }
 }
 
 // Joins the splits of each row of out.  Rows behind the last sequence stay as
@@ -571,35 +513,21 @@ cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, many ? chunk_merge<64, 8> : chunk_merge<64, 1>, p);
 }
 
-template <int D, int KE, int VE, int MW>
+template <int KE, int VE>
 static cudaError_t launch_one(const ChunkParams& p, dim3 grid, cudaStream_t st) {
-  constexpr int smem = ChunkCfg<D, KE, VE>::BYTES;
-  const cudaError_t e = ensure_smem_optin((const void*)chunk_mma<D, KE, VE, MW>, smem);
+  constexpr int smem = ChunkCfg<KE, VE>::BYTES;
+  const cudaError_t e = ensure_smem_optin((const void*)chunk_mma<KE, VE>, smem);
   if (e != cudaSuccess) return e;
-  chunk_mma<D, KE, VE, MW><<<grid, kChunkThreads, smem, st>>>(p);
+  chunk_mma<KE, VE><<<grid, kChunkThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 
-template <int D, int KE, int VE>
-static cudaError_t launch_rows(const ChunkParams& p, int row_warps, dim3 grid, cudaStream_t st) {
-  if (row_warps == 2) return launch_one<D, KE, VE, 2>(p, grid, st);
-  return launch_one<D, KE, VE, 4>(p, grid, st);
-}
-
-template <int D>
-static cudaError_t launch_types(const ChunkParams& p, int dtype, int row_warps, dim3 grid, cudaStream_t st) {
-  if constexpr (D == 128)     // (MXFP8 keys are built for head_dim 128)
-    if (dtype == FP8KV_MXK8V8) return launch_rows<D, ELEM_MX, ELEM_E4M3>(p, row_warps, grid, st);
-  if (dtype == FP8KV_K8V8) return launch_rows<D, ELEM_E4M3, ELEM_E4M3>(p, row_warps, grid, st);
-  if (dtype == FP8KV_K16V8) return launch_rows<D, ELEM_BF16, ELEM_E4M3>(p, row_warps, grid, st);
-  if (dtype == FP8KV_K8V16) return launch_rows<D, ELEM_E4M3, ELEM_BF16>(p, row_warps, grid, st);
-  return launch_rows<D, ELEM_BF16, ELEM_BF16>(p, row_warps, grid, st);
-}
-
-cudaError_t launch_chunk_mma(const ChunkParams& p, int dtype, int row_warps, int tiles, cudaStream_t st) {
+cudaError_t launch_chunk_mma(const ChunkParams& p, int dtype, int tiles, cudaStream_t st) {
   const dim3 grid(tiles, p.c.kv_heads, p.num_splits);
-  return p.c.head_dim == 128 ? launch_types<128>(p, dtype, row_warps, grid, st)
-                             : launch_types<64>(p, dtype, row_warps, grid, st);
+  if (dtype == FP8KV_K8V8) return launch_one<ELEM_E4M3, ELEM_E4M3>(p, grid, st);
+  if (dtype == FP8KV_K16V8) return launch_one<ELEM_BF16, ELEM_E4M3>(p, grid, st);
+  if (dtype == FP8KV_K8V16) return launch_one<ELEM_E4M3, ELEM_BF16>(p, grid, st);
+  return launch_one<ELEM_BF16, ELEM_BF16>(p, grid, st);
 }
 
 }  // namespace fp8kv

@@ -1,7 +1,9 @@
-// chunk_rows.cu -- ragged chunk attention for tiles of at most sixteen query
-// rows (single tokens of a group of heads, a few drafted tokens): the cache is
-// read once and nothing else takes as long, so the kernel is built around
-// keeping loads in flight.
+// chunk_rows.cu -- ragged chunk attention in tiles of at most sixteen query
+// rows, for single tokens of a group of heads and a few drafted tokens: the cache
+// is read once and nothing else takes as long, so the kernel is built around
+// keeping loads in flight.  Also the form of block-scaled keys at any length
+// (256-512 tokens x 8 heads, 4 sequences of 4K-8K: 1.15 ms, conversions and the
+// four fp32 partial products of a score).
 //
 // The products are turned around so that the queries are the narrow side of the
 // matrix instruction: S^T = K Q^T (16 keys x 8 queries per instruction) and
@@ -15,7 +17,8 @@
 //
 // Arithmetic as in chunk_mma.cu: f16 operands for e4m3 sides (codes exact,
 // query scaled by a power of two, P by 2^-kp and the value scale), bf16 for
-// bf16 sides, m, l and O in fp32.
+// bf16 sides, m, l and O in fp32.  Block-scaled keys: the four 32-element partial
+// products are scaled in fp32 and added.
 //
 // Measured on one GB300 (64 sequences, 32 query / 8 KV heads, head dim 128,
 // e4m3, 16-token pages, device time): a 1,024-token window 36 us (140 MB: 3.9
@@ -26,14 +29,16 @@
 // a reference that moves at every new maximum and checked row copies; 46 us with
 // one vote for both and whole-group copies, three CTAs an SM at four ring stages;
 // 40 us with five CTAs at two; 36.5 us with four at three (this).  QK on e4m3
-// instructions without conversion (mma.sync m16n8k32) was slower, 39 us.
+// instructions without conversion (mma.sync m16n8k32) was slower, 39 us.  Two groups
+// a step, which share the vote and the loop: 46 us (67 KB of rings, three CTAs an
+// SM, one wave and a bit; the same 59 us as below where shares can even that out).
 //
 // Sixteen rows (two tokens x 8 heads, 4 KV heads, 64 sequences of 2K-4K tokens,
-// 210 MB): 75 us, three CTAs an SM at 168 registers; 59 us for one token.  The
+// 210 MB): 74 us, three CTAs an SM at 168 registers; 59 us for one token.  The
 // second set costs its products, exponentials and transposes, not the codes'
 // conversion.  On the warp-level kernel, whose four warps share a tile, the call took
 // 90 us at the best split count, on tcgen05's 128-row tiles 101 us; 16 heads on one
-// KV head at head dim 64 (64 sequences of 4K-8K tokens) take 31 us, 53 us there.
+// KV head at head dim 64 (64 sequences of 4K-8K tokens) take 30 us, 53 us there.
 #include <cfloat>
 
 #include "chunk_common.cuh"

@@ -110,7 +110,7 @@ cudaError_t launch_build_tables(const CacheView& c, const int32_t* cached, const
                                 int32_t* head_out, unsigned int* err, cudaStream_t s);
 cudaError_t launch_rope_tables(int positions, int pairs, const unsigned long long* w, float amplitude, float* cos,
                                float* sin, cudaStream_t s);
-cudaError_t launch_chunk_mma(const ChunkParams& p, int dtype, int row_warps, int tiles, cudaStream_t st);
+cudaError_t launch_chunk_mma(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
 cudaError_t launch_chunk_rows(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
 cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t st);

@@ -252,6 +252,49 @@ def test_few_rows_unseen_values(dtype, Hq, what):
         assert (out[sees][..., rest] - ref[sees][..., rest]).abs().max() <= 2.0 ** -7 * 4.5
 
 
+@pytest.mark.parametrize("dtype", ["k8v8", "k16v8", "k8v16", "k16v16"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 1), (64, 4), (100, 65), (2, 200)])
+def test_many_rows_head_dim_64(dtype, window, sinks):
+    """64-row tiles, full and ragged, of groups that do and do not divide them,
+    with scales that differ widely and splits that are empty."""
+    for Hq, Hkv, splits in ((4, 2, 0), (7, 1, 3), (16, 1, 0)):
+        run_case(dtype, 64, Hq, Hkv, [0, 300, 129, 511], [150, 70, 1, 65], 16, seed=47, window=window, sinks=sinks, spread=6.0,
+                 splits=splits)
+    # the first queries come before the sequence's first token
+    run_case(dtype, 64, 4, 1, [-20, 0], [90, 60], 0, seed=48, window=window, sinks=sinks, out_dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", ["k8v8", "k16v16", "k8v16"])
+@pytest.mark.parametrize("what", ["nan", "inf", "scale"])
+def test_unseen_values_head_dim_64(dtype, what):
+    """Values that are not finite where some queries of a 64-row tile see them and
+    others do not."""
+    lens, window = [200], 40
+    cache = make_cache(dtype, 64, 1, lens, 0, seed=49, poison=False)
+    q = torch.randn(120, 2, 64, device="cuda").to(torch.bfloat16)
+    f = lambda: fk.fp8kv_chunk_attention(q, cache, _i32([0, 120]), _i32(lens), window=window, out_dtype=torch.float32)
+    ref = f().clone()
+    coded = dtype == "k8v8"
+    for j in (100, 150):
+        if what == "scale":
+            if not coded:
+                pytest.skip("bf16 values have no scales")
+            cache.v_scale[0, 0, j] = float("inf")
+            cache.v[0, 0, j] = 0x38
+        else:
+            cache.v[0, 0, j, 5] = 0xFF if coded else float(what)
+    out = f()
+    assert fk.fp8kv_get_device_error() == 0
+    pos = torch.arange(80, 200)
+    sees = torch.stack([(pos >= j) & (pos < j + window) for j in (100, 150)]).any(0)
+    # the weights' two roundings (2^-11 or 2^-8 each) against other references
+    assert torch.isfinite(out[~sees]).all() and (out[~sees] - ref[~sees]).abs().max() <= 2.0 ** -7 * 4.5
+    assert not torch.isfinite(out[sees][..., 5]).any()
+    if what != "scale":
+        rest = [d for d in range(64) if d != 5]
+        assert (out[sees][..., rest] - ref[sees][..., rest]).abs().max() <= 2.0 ** -7 * 4.5
+
+
 @pytest.mark.parametrize("kernel", KERNELS)
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (63, 0), (64, 4), (65, 64), (100, 65), (130, 1000), (5000, 2), (2, 200)])
 def test_windows(window, sinks, kernel):
