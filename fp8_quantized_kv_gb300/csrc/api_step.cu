@@ -67,7 +67,8 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   if (!capacity_fits(c) || G > 16 || c->rope_cos != nullptr || c->kv_heads > 65535 || num_splits > 4096) return FP8KV_ERR_UNSUPPORTED;
   if (total_q > INT32_MAX || (double)total_q * q_heads > 8.0 * INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
   const int64_t B = c->batch > 0 ? c->batch : 1;
-  const int64_t rows = (total_q + B - 1) / B * G;
+  // (an idle step, total_q 0, plans like one of single tokens: a tile holds one at least)
+  const int64_t rows = total_q > 0 ? (total_q + B - 1) / B * G : G;
   const bool tc_built = c->head_dim == 128 && c->dtype != FP8KV_MXK8V8;
   if (kernel == FP8KV_KERNEL_TENSOR_CORES && !tc_built) return FP8KV_ERR_UNSUPPORTED;
   const int cap = capacity_of(c);

@@ -147,3 +147,22 @@ def test_stride_of_one_row():
     """A single token's stride is never used: any slice of it will do."""
     t = torch.zeros(256, dtype=torch.bfloat16).as_strided((1, 2, 128), (4100, 128, 1))
     assert t.stride(0) == 4100 and fk._rows(t, 2, 128, 1, "k", -1)[1] == 256
+
+
+@pytest.mark.parametrize("layout", ["contiguous", "paged"])
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("group", [1, 8, 9, 16])
+def test_chunk_idle_step(lib, group, head_dim, layout):
+    """A step without a query, and one without a sequence, plans and returns like
+    any other, whatever the group's size."""
+    for batch, kernels in ((4, (0, 5, 2)), (0, (0, 5))):
+        kw = dict(batch=batch, kv_heads=1, head_dim=head_dim)
+        cache = _paged(**kw) if layout == "paged" else _cache(**kw)
+        for kernel in kernels:
+            if kernel == 2 and head_dim == 64:
+                continue
+            for window, splits in ((0, 0), (0, 3), (128, 0)):
+                assert lib.fp8kv_chunk_num_splits(cache, 0, group, window, 0, splits, kernel) >= 1
+                assert lib.fp8kv_chunk_workspace_bytes(cache, 0, group, window, 0, splits, kernel) == 0
+                assert lib.fp8kv_chunk_attention(None, cache, 0x20000, None, 0, group, 0.1, window, 0, splits, kernel, None, 0, None, 0,
+                                                 None) == 0
