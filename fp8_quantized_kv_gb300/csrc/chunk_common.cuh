@@ -38,34 +38,61 @@ __device__ __forceinline__ int chunk_key0(const ChunkTile& t, int j) {
 // Tiles are numbered so that a CTA finds its own without a scan over the
 // batch: sequence b owns the numbers from start(b) = cu_q[b] / T + b on,
 // because it has at most (cu_q[b+1] / T - cu_q[b] / T) + 1 tiles of T tokens.
-// The last sequence with start(b) <= x is found by a 32-way search of the
-// warp.  Returns false for a number that no tile has.  `lead`: raise errors.
+//
+// The last sequence b with start(b) <= x (TILE), or with cu_q[b] <= x, found by
+// a 32-way search of the warp; its offsets, and its length (TILE).  Offsets that
+// decrease give some sequence of the batch (the right one, up to 32 sequences,
+// before the first that decreases: the lanes in front count, not all).
+template <bool TILE>
+__device__ __forceinline__ int chunk_search(const ChunkParams& p, int x, int& q0, int& q1, int& len) {
+  const int lane = threadIdx.x & 31;
+  auto last_of = [](unsigned m) { return max(__clz(__brev(~m)), 1) - 1; };     // last lane of those in front
+  auto before = [&](int b, int first) { return TILE ? (long long)first / p.tile_tokens + b <= x : first <= x; };
+  int lo = 0, n = p.c.batch;
+  while (n > 32) {
+    const int step = (n + 31) >> 5, at = lane * step;
+    const bool le = at < n && (at == 0 || before(lo + at, p.cu_q[lo + at]));
+    const int k = last_of(__ballot_sync(0xffffffffu, le));
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  // the last step's lanes hold all there is to know of their sequence
+  const int at = min(lane, n - 1) + lo;
+  const int c0 = p.cu_q[at], c1 = p.cu_q[at + 1], ln = TILE ? p.seq_lens[at] : 0;
+  const bool le = lane < n && (lane == 0 || before(at, c0));
+  const int k = last_of(__ballot_sync(0xffffffffu, le));
+  q0 = __shfl_sync(0xffffffffu, c0, k);
+  q1 = __shfl_sync(0xffffffffu, c1, k);
+  if (TILE) len = __shfl_sync(0xffffffffu, ln, k);
+  return lo + k;
+}
+__device__ __forceinline__ bool chunk_offsets_ok(const ChunkParams& p, int q0, int q1) {
+  return q0 >= 0 && q1 >= q0 && q1 <= p.total_q;
+}
+
+// Whether the row of query `row` has been computed: it belongs to a sequence
+// with good offsets, and its tile number leads to that sequence (it does, unless
+// offsets decrease somewhere).  The tile's shares are then all written.
+__device__ __forceinline__ bool chunk_row_live(const ChunkParams& p, int row) {
+  if (p.cu_q == nullptr) return true;
+  int q0, q1, none;
+  const int b = chunk_search<false>(p, row, q0, q1, none);
+  if (!chunk_offsets_ok(p, q0, q1) || row < q0 || row >= q1) return false;
+  const int x = q0 / p.tile_tokens + b + (row - q0) / p.tile_tokens;
+  int c0, c1;
+  return chunk_search<true>(p, x, c0, c1, none) == b;
+}
+
+// The CTA's tile.  Returns false for a number that no tile has.  `lead`: raise
+// errors.
 __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lead, ChunkTile& t) {
-  const int T = p.tile_tokens, lane = threadIdx.x & 31;
+  const int T = p.tile_tokens;
   int b = x, q0 = x, q1 = x + 1, i0 = 0;           // one query per sequence
   if (p.cu_q == nullptr && x >= p.c.batch) return false;
   int len = 0;
   if (p.cu_q != nullptr) {
-    int lo = 0, n = p.c.batch;
-    while (n > 32) {
-      const int step = (n + 31) >> 5, at = lane * step;
-      const bool le = at < n && (at == 0 || (long long)p.cu_q[lo + at] / T + lo + at <= x);
-      // le is monotone for offsets that do not decrease; for others the
-      // count still lands on a sequence of the batch
-      const int k = max(__popc(__ballot_sync(0xffffffffu, le)), 1) - 1;
-      lo += k * step;
-      n = min(step, n - k * step);
-    }
-    // the last step's lanes hold all there is to know of their sequence
-    const int at = min(lane, n - 1) + lo;
-    const int c0 = p.cu_q[at], c1 = p.cu_q[at + 1], ln = p.seq_lens[at];
-    const bool le = lane < n && (lane == 0 || (long long)c0 / T + at <= x);
-    const int k = max(__popc(__ballot_sync(0xffffffffu, le)), 1) - 1;
-    b = lo + k;
-    q0 = __shfl_sync(0xffffffffu, c0, k);
-    q1 = __shfl_sync(0xffffffffu, c1, k);
-    len = __shfl_sync(0xffffffffu, ln, k);
-    if (q0 < 0 || q1 < q0 || q1 > p.total_q) {
+    b = chunk_search<true>(p, x, q0, q1, len);
+    if (!chunk_offsets_ok(p, q0, q1)) {
       if (lead) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
       return false;
     }

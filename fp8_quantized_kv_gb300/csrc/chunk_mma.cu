@@ -423,8 +423,9 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
     }
 }
 
-// Joins the splits of each row of out.  Rows behind the last sequence stay as
-// they were.  Many rows or few splits: a warp a row (W 1); few rows of more than
+// Joins the splits of each row of out.  Rows that no tile holds (padding, and
+// those of a sequence with bad offsets) have no shares and stay as they were.
+// Many rows or few splits: a warp a row (W 1); few rows of more than
 // three splits: the eight warps of a CTA take every eighth split each and add
 // their sums in order.  A chain of loads bounds it: one token of 32 heads over
 // 32,000 tokens in 76 splits took 33 us with a warp a row, 18 us so; 3,000 rows of
@@ -434,10 +435,10 @@ template <int D, int W>
 __global__ void __launch_bounds__(256) chunk_merge(const ChunkParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, S = p.num_splits;
   const int64_t row = W == 1 ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x;
+  // (the offsets are an input of the kernel before as well: they can be read now)
+  const bool live = row < (int64_t)p.total_q * p.q_heads && chunk_row_live(p, (int)(row / p.q_heads));
   asm volatile("griddepcontrol.wait;\n" ::: "memory");    // the shares are written
-  if (row >= (int64_t)p.total_q * p.q_heads) return;
-  const int tok = (int)(row / p.q_heads);
-  if (p.cu_q != nullptr && (tok < p.cu_q[0] || tok >= p.cu_q[p.c.batch])) return;
+  if (!live) return;
   const float* pm = p.part_m + row * S;
   const float* pl = p.part_l + row * S;
   constexpr int E = D / 32;

@@ -1,0 +1,72 @@
+"""Chunk attention at its edges: offsets that are refused, in calls with splits."""
+import pytest
+import torch
+
+import fp8_quantized_kv_gb300 as fk
+from test_gpu_chunk import _i32, make_cache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _clear_device_error():
+    fk.fp8kv_get_device_error(clear=True)
+    yield
+
+
+# (dtype, head dim, kernel, query heads): the few-row kernel with one and two sets
+# of rows, the warp-level kernel's 64-row tiles, tcgen05
+FORMS = [("k8v8", 128, "warp_mma", 2), ("k16v16", 64, "warp_mma", 2), ("mxk8v8", 128, "warp_mma", 4), ("k8v16", 64, "rows64", 4),
+         ("k8v8", 64, "rows64", 2), ("k8v8", 128, "tensor_cores", 2), ("k16v16", 128, "tensor_cores", 4)]
+
+
+def _call(q, cache, cu, lens, kernel, **kw):
+    return fk.fp8kv_chunk_attention(q, cache, _i32(cu), _i32(lens), kernel="warp_mma" if kernel == "rows64" else kernel, **kw)
+
+
+# --------------------------------------------------------- refused offsets --
+@pytest.mark.parametrize("splits", [1, 3, 9])
+@pytest.mark.parametrize("dtype,D,kernel,Hq", FORMS)
+def test_refused_offsets_leave_their_rows(dtype, D, kernel, Hq, splits):
+    """Rows of a sequence whose offsets decrease or pass total_q stay as they
+    were, with and without splits, whatever the workspace holds.  The others' rows
+    are those of a call without it; where offsets decrease some may be left too."""
+    lens, step = [700, 700, 700], 40 if kernel == "rows64" else 2
+    cache = make_cache(dtype, D, 1, lens, 16, seed=60)
+    total = 3 * step
+    q = torch.randn(total, Hq, D, device="cuda").to(torch.bfloat16)
+    good = _call(q, cache, [0, step, 2 * step, total], lens, kernel, num_splits=splits, out_dtype=torch.float32)
+    assert fk.fp8kv_get_device_error() == 0
+    need = fk.fp8kv_chunk_workspace_bytes(cache, total, Hq, num_splits=splits, kernel="warp_mma" if kernel == "rows64" else kernel)
+    for cu, kept in (([0, step, total + 3, total], slice(0, step)),           # past total_q, then back
+                     ([0, step, 2 * step, total + 1], slice(0, 2 * step)),    # past total_q at the end
+                     ([0, step, -1, -1], slice(0, step))):                    # below zero
+        out = torch.full((total, Hq, D), 3.0, device="cuda")
+        ws = torch.full((max(need, 16) // 4,), 0.5, device="cuda").view(torch.uint8)       # finite, so that it would show
+        _call(q, cache, cu, lens, kernel, num_splits=splits, out=out, workspace=ws)
+        assert fk.fp8kv_get_device_error() == fk.DEVERR_SEQ_TOO_LONG
+        same = (out[kept] == good[kept]) | ((out[kept] == 3.0) if sorted(cu) != cu else False)
+        assert bool(same.all()) and bool((out[:1] == good[:1]).all())
+        rest = torch.ones(total, dtype=torch.bool)
+        rest[kept] = False
+        assert bool((out[rest.cuda()] == 3.0).all())
+
+
+def test_more_rows_than_a_step_holds():
+    """fp8kv_build_tables reports more new rows than n_rows; the attention of that
+    step leaves the cut sequence's rows alone, in the splits that it chooses."""
+    B, D, Hq, n_rows = 3, 128, 2, 4
+    cache = fk.Fp8KVCache.paged(torch.full((B, 256), -1, dtype=torch.int32), 700, 1, D, 16)
+    t = fk.fp8kv_build_tables(cache, _i32([0] * B), _i32([1000, 1000, 1000]), 3000, _i32(list(range(700))), _i32([0]))
+    k = torch.randn(3000, 1, D, device="cuda").to(torch.bfloat16)
+    fk.fp8kv_append(cache, k, k, t["seq_idx"], t["pos"])
+    t = fk.fp8kv_build_tables(cache, t["seq_lens"], _i32([1, 1, 5]), n_rows, _i32(list(range(700))), t["free_head"])
+    assert fk.fp8kv_get_device_error() == fk.DEVERR_SEQ_TOO_LONG
+    # (the tokens themselves, out of this test's way: any finite values do)
+    q = torch.randn(n_rows, Hq, D, device="cuda").to(torch.bfloat16)
+    assert fk.fp8kv_chunk_num_splits(cache, n_rows, Hq) > 1
+    ws = torch.full((fk.fp8kv_chunk_workspace_bytes(cache, n_rows, Hq) // 4,), 0.5, device="cuda").view(torch.uint8)
+    out = torch.full((n_rows, Hq, D), 3.0, device="cuda")
+    fk.fp8kv_chunk_attention(q, cache, t["cu_new"], t["seq_lens"], out=out, workspace=ws)
+    assert fk.fp8kv_get_device_error() == fk.DEVERR_SEQ_TOO_LONG
+    assert bool((out[2:] == 3.0).all()) and not bool((out[:2] == 3.0).any())
