@@ -91,11 +91,13 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
   if (p.cu_q == nullptr && x >= p.c.batch) return false;
   int len = 0;
   if (p.cu_q != nullptr) {
+    // there are as many tile numbers as sequences, or more: each looks at one pair of
+    // offsets, so that every bad one is reported, found by the search or not
+    int a0 = 0, a1 = 0;
+    if (lead && x < p.c.batch) { a0 = p.cu_q[x]; a1 = p.cu_q[x + 1]; }
     b = chunk_search<true>(p, x, q0, q1, len);
-    if (!chunk_offsets_ok(p, q0, q1)) {
-      if (lead) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
-      return false;
-    }
+    if (!chunk_offsets_ok(p, a0, a1)) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
+    if (!chunk_offsets_ok(p, q0, q1)) return false;
     const long long i = ((long long)x - ((long long)q0 / T + b)) * T;
     if (i < 0 || i >= q1 - q0) return false;
     i0 = (int)i;

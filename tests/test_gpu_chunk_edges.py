@@ -70,3 +70,23 @@ def test_more_rows_than_a_step_holds():
     fk.fp8kv_chunk_attention(q, cache, t["cu_new"], t["seq_lens"], out=out, workspace=ws)
     assert fk.fp8kv_get_device_error() == fk.DEVERR_SEQ_TOO_LONG
     assert bool((out[2:] == 3.0).all()) and not bool((out[:2] == 3.0).any())
+
+
+@pytest.mark.parametrize("cu", [[0, 4, 3, 8], [0, 7, 3, 8], [0, 9, 3, 8], [0, 5, 3, 3, 8], [0, 8, 0, 8], [5, 3, 4, 8],
+                                [0] * 40 + [6, 5] + [6] * 40 + [8]])
+@pytest.mark.parametrize("splits", [1, 5])
+def test_every_decrease_is_reported(cu, splits):
+    """Offsets that decrease anywhere are reported, and no row gets anything that
+    this call did not write: a share of the workspace as it was would bring 1e9.
+    (A row that two sequences claim can mix their shares, whose references differ
+    by less than 2^16 here.)"""
+    B = len(cu) - 1
+    cache = make_cache("k8v8", 64, 1, [200] * B, 16, seed=61)
+    q = torch.randn(8, 1, 64, device="cuda").to(torch.bfloat16)
+    out = torch.full((8, 1, 64), 3.0, device="cuda")
+    need = fk.fp8kv_chunk_workspace_bytes(cache, 8, 1, num_splits=splits)
+    ws = torch.ones(max(need, 16) // 4, device="cuda")
+    ws[:8 * splits * 64] = 1e9
+    fk.fp8kv_chunk_attention(q, cache, _i32(cu), _i32([200] * B), num_splits=splits, out=out, workspace=ws.view(torch.uint8))
+    assert fk.fp8kv_get_device_error() == fk.DEVERR_SEQ_TOO_LONG
+    assert out.abs().max() <= 1e6
