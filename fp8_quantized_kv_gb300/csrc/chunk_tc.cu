@@ -33,7 +33,8 @@
 //               see it get NaN, the others nothing
 //   warp 10     TMA producer: K ring and V ring
 //   warp 11     TMEM owner and MMA issuer
-// Every wait is bounded; one that runs out raises FP8KV_DEVERR_TIMEOUT.
+// Every wait is bounded; one that runs out raises FP8KV_DEVERR_TIMEOUT, and the
+// tile's rows come out as if they saw no key (an empty share, a row of zeros).
 //
 // Measured on one GB300: 3,727 queries over 2,000-8,000 tokens (28 query / 4 KV
 // heads, e4m3, 16-token pages) 281 us, 691 TFLOP/s, 36 % of the measured bf16
@@ -742,48 +743,46 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       }
     }
     failed = softmax_any(failed);                 // (a barrier of the eight warps)
-    if (failed) {
-      if (tid == 0) raise_error(p.err, FP8KV_DEVERR_TIMEOUT);
-    } else {
-      umma::fence_after_sync();
-      const int r = tid & 127, tok = r / G;        // row of the tile, TMEM lane
-      const bool live = tok < t.ntok && r < p.tile_tokens * G;
-      const int64_t qrow = live ? (int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G) : -1;
-      const uint32_t lane_q = (uint32_t)(32 * (warp & 3)) << 16;
-      const float mr = st[r], lr = st[kCtRows + r], of = st[2 * kCtRows + r];
-      const bool whole = p.num_splits == 1;
-      const float f = !whole ? of : lr > 0.f ? of / lr : lr == lr ? 0.f : lr;
-      const int64_t at = whole ? qrow : qrow * p.num_splits + split;
-      if (!whole && live && hf == 0) { p.part_m[at] = mr; p.part_l[at] = lr; }
+    if (failed && tid == 0) raise_error(p.err, FP8KV_DEVERR_TIMEOUT);
+    const bool empty = failed || n == 0;          // O and the quads' values are not read
+    umma::fence_after_sync();
+    const int r = tid & 127, tok = r / G;          // row of the tile, TMEM lane
+    const bool live = tok < t.ntok && r < p.tile_tokens * G;
+    const int64_t qrow = live ? (int64_t)(t.row0 + tok) * p.q_heads + hk * G + (r - tok * G) : -1;
+    const uint32_t lane_q = (uint32_t)(32 * (warp & 3)) << 16;
+    const float mr = empty ? -INFINITY : st[r], lr = empty ? 0.f : st[kCtRows + r], of = empty ? 0.f : st[2 * kCtRows + r];
+    const bool whole = p.num_splits == 1;
+    const float f = !whole ? of : lr > 0.f ? of / lr : lr == lr ? 0.f : lr;
+    const int64_t at = whole ? qrow : qrow * p.num_splits + split;
+    if (!whole && live && hf == 0) { p.part_m[at] = mr; p.part_l[at] = lr; }
 #pragma unroll 1
-      for (int k = 4 * hf; k < 4 * hf + 4; ++k) {
-        uint32_t rr[16];
-        if (n > 0) {
-          umma::tmem_ld16_nowait(o_col + lane_q + 16 * k, rr);
-          umma::tmem_wait_ld();
-        } else {
+    for (int k = 4 * hf; k < 4 * hf + 4; ++k) {
+      uint32_t rr[16];
+      if (!empty) {
+        umma::tmem_ld16_nowait(o_col + lane_q + 16 * k, rr);
+        umma::tmem_wait_ld();
+      } else {
 #pragma unroll
-          for (int u = 0; u < 16; ++u) rr[u] = 0u;
+        for (int u = 0; u < 16; ++u) rr[u] = 0u;
+      }
+      if (!live) continue;
+      float o[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) o[u] = __uint_as_float(rr[u]) * f;
+      if (!whole || p.out_f32) {
+        float4* dst = reinterpret_cast<float4*>((whole ? reinterpret_cast<float*>(p.out) : p.part_o) + at * D + 16 * k);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+      } else {
+        uint32_t h[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(o[2 * u], o[2 * u + 1]);
+          h[u] = *reinterpret_cast<const uint32_t*>(&x);
         }
-        if (!live) continue;
-        float o[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u) o[u] = __uint_as_float(rr[u]) * f;
-        if (!whole || p.out_f32) {
-          float4* dst = reinterpret_cast<float4*>((whole ? reinterpret_cast<float*>(p.out) : p.part_o) + at * D + 16 * k);
-#pragma unroll
-          for (int u = 0; u < 4; ++u) dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-        } else {
-          uint32_t h[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(o[2 * u], o[2 * u + 1]);
-            h[u] = *reinterpret_cast<const uint32_t*>(&x);
-          }
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at * D + 16 * k);
-          dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
-          dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
-        }
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at * D + 16 * k);
+        dst[0] = make_uint4(h[0], h[1], h[2], h[3]);
+        dst[1] = make_uint4(h[4], h[5], h[6], h[7]);
       }
     }
   }

@@ -476,7 +476,9 @@ FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q
  * NaN.  A length below 0 or past the capacity raises SEQ_TOO_LONG and gives zero rows; offsets that
  * decrease or pass total_q raise it and leave their rows as they were.  (Where
  * offsets decrease, rows of other sequences may be left as they were too, and a
- * row that two sequences claim holds nothing defined.) */
+ * row that two sequences claim holds nothing defined.)  A wait of the
+ * tensor-core kernel that runs out raises TIMEOUT; its rows are zero, or lack
+ * that split's keys. */
 FP8KV_API fp8kv_status fp8kv_chunk_attention(const void *q, const fp8kv_cache *cache,
                                              const int32_t *cu_q, const int32_t *seq_lens,
                                              int64_t total_q, int32_t q_heads, float sm_scale,
