@@ -61,6 +61,7 @@
 namespace fp8kv {
 
 constexpr int kCtRows = 128, kCtThreads = 384;
+constexpr int kNotFinite = 127;    // in place of a query row's exponent: an element is infinite
 
 template <int KE, int VE>
 struct CtCfg {
@@ -324,9 +325,10 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
         }
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // smallest power of two that brings the row within 448 = 1.75 * 2^8
+        // smallest power of two that brings the row within 448 = 1.75 * 2^8;
+        // e4m3 has no infinity, so a row with one is marked (a NaN stays one)
         const int ab = __float_as_int(amax);
-        const int kq = ab < 0x7F800000 ? max(-100, min(120, (ab >> 23) - 127 - 8 + ((ab & 0x7FFFFF) > 0x600000))) : 0;
+        const int kq = ab < 0x7F800000 ? max(-100, min(120, (ab >> 23) - 127 - 8 + ((ab & 0x7FFFFF) > 0x600000))) : kNotFinite;
         if (ch == 0) kq_sh[row] = (int8_t)kq;
         const float qsc = pow2i(-kq);
         uint32_t hi[2], lo[2];
@@ -576,6 +578,9 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       // what is left of the score's scale, positive (bf16 keys: the query
       // operand carries the sign, and is zero for a scale of zero)
       s2[i] = !C::K16 ? pow2i(kq_sh[row]) : p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1.f;
+      // an infinite element: every score is +-inf or NaN, and the softmax of such
+      // scores NaN (a row before the first token sees none and stays zero)
+      if (!C::K16 && kq_sh[row] == kNotFinite) s2[i] = qpos[i] >= 0 ? NAN : 1.f;
       up[i] = 1.f;
       m_used[i] = -INFINITY;
       l[i] = neg_m[i] = 0.f;

@@ -1,4 +1,5 @@
-"""Chunk attention at its edges: offsets that are refused, in calls with splits."""
+"""Chunk attention at its edges: offsets that are refused, in calls with splits;
+queries that are not finite."""
 import pytest
 import torch
 
@@ -90,3 +91,34 @@ def test_every_decrease_is_reported(cu, splits):
     fk.fp8kv_chunk_attention(q, cache, _i32(cu), _i32([200] * B), num_splits=splits, out=out, workspace=ws.view(torch.uint8))
     assert fk.fp8kv_get_device_error() == fk.DEVERR_SEQ_TOO_LONG
     assert out.abs().max() <= 1e6
+
+
+# ------------------------------------------------ queries that are not finite --
+@pytest.mark.parametrize("splits", [1, 4])
+@pytest.mark.parametrize("dtype,D,kernel,Hq", FORMS + [("k16v8", 128, "tensor_cores", 2), ("k8v16", 128, "tensor_cores", 2)])
+def test_queries_that_are_not_finite(dtype, D, kernel, Hq, splits):
+    """An infinite or NaN element makes every score of its query +-inf or NaN, and
+    the softmax of such scores NaN (all -inf among them): that row is NaN on every
+    kernel, the others keep their bits, and one that sees no key stays zero."""
+    n = 80 if kernel == "rows64" else 7
+    lens, cu = [300, n - 3], [0, n, 2 * n]               # sequence 1's first three queries see nothing
+    cache = make_cache(dtype, D, 1, lens, 16, seed=62)
+    q = torch.randn(2 * n, Hq, D, device="cuda").to(torch.bfloat16)
+    args = dict(num_splits=splits, out_dtype=torch.float32)
+    ref = _call(q, cache, cu, lens, kernel, **args)
+    bad = q.clone()
+    bad[0, 0, 3] = float("inf")
+    bad[2, 1, D - 1] = float("-inf")
+    bad[3, 0, 17] = float("nan")
+    bad[n - 1, 1] = float("inf")
+    bad[5, 1, 9], bad[5, 1, 40] = float("inf"), 3.0e38
+    bad[n + 1, 0, 0], bad[n + 2, 1, 5] = float("inf"), float("nan")      # see nothing
+    out = _call(bad, cache, cu, lens, kernel, **args)
+    assert fk.fp8kv_get_device_error() == 0
+    rows = [(0, 0), (2, 1), (3, 0), (n - 1, 1), (5, 1)]
+    nan = torch.zeros(2 * n, Hq, dtype=torch.bool, device="cuda")
+    for r, h in rows:
+        nan[r, h] = True
+    assert bool(torch.isnan(out[nan]).all())
+    assert torch.equal(out[~nan], ref[~nan])
+    assert bool((out[n:n + 3] == 0).all())
