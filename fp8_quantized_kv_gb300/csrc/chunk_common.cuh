@@ -168,6 +168,16 @@ __device__ __forceinline__ int chunk_row(const ChunkParams& p, const ChunkTile& 
   return (page * c.kv_heads + hk) * c.page_size + (key & (c.page_size - 1));
 }
 
+// Whether one of eight bf16 elements is infinite or NaN.  The score of a query
+// that has one is +-inf or NaN at every key, and the softmax of such scores NaN,
+// all of them -inf among these: its operand, or its scores' factor, is made NaN,
+// since a score of -inf alone reads as a key that is not seen.
+__device__ __forceinline__ bool has_inf_nan(uint4 x) {
+  bool odd = false;
+  for (uint32_t w : {x.x, x.y, x.z, x.w}) odd = odd || (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+  return odd;
+}
+
 // Weight of a split's (m, l): zero for a split that saw nothing, NaN for one
 // whose scores were all NaN.
 __device__ __forceinline__ float chunk_weight(float m, float l, float M) {

@@ -120,10 +120,12 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
   for (int i = 0; i < 2; ++i) {
     uint32_t w[KS][2];                         // four elements of each step
     constexpr bool WIDE = KE == ELEM_E4M3;     // 16 elements together per lane (else 8)
+    bool odd = false;
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) {
       const int at = WIDE ? 8 * (u >> 1) + 2 * c4 + (u & 1) : 4 * u + c4;
       const uint4 x = qrow[i] >= 0 ? qsrc[i][at] : make_uint4(0, 0, 0, 0);
+      odd = odd || has_inf_nan(x);
       w[2 * u][0] = x.x; w[2 * u][1] = x.y; w[2 * u + 1][0] = x.z; w[2 * u + 1][1] = x.w;
     }
     float sc = 1.f;
@@ -143,6 +145,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
       const int up = min(14 - e, 126);
       if (amax > 0.f && e < 128) { sc = pow2i(up); qf[i] = pow2i(-up); }
     }
+    if ((__ballot_sync(0xffffffffu, odd) >> (lane & 28)) & 0xFu) qf[i] = NAN;    // (any lane of the row's quad)
 #pragma unroll
     for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
           mma16816<true>(s[n], qa[2 * u + 1], w.z, w.w);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] *= p.scale_log2;
+        for (int e = 0; e < 4; ++e) s[n][e] *= p.scale_log2 * qf[e >> 1];
       }
     }
     const bool part = !chunk_all_seen(p, t, key0);

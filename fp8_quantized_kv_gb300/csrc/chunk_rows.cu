@@ -167,10 +167,12 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
     const bool live = tokr < t.ntok && r < p.tile_tokens * G;
     const uint4* qsrc = reinterpret_cast<const uint4*>(
         p.q + (live ? (int64_t)(t.row0 + tokr) * p.q_heads + hk * G + (r - tokr * G) : 0) * D);
+    bool odd = false;
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) {
       const int at = KE == ELEM_E4M3 ? 8 * (u >> 1) + 2 * c4 + (u & 1) : 4 * u + c4;
       const uint4 x = live ? qsrc[at] : make_uint4(0, 0, 0, 0);
+      odd = odd || has_inf_nan(x);
       qb[w][2 * u][0] = x.x; qb[w][2 * u][1] = x.y; qb[w][2 * u + 1][0] = x.z; qb[w][2 * u + 1][1] = x.w;
     }
     qf[2 * w] = qf[2 * w + 1] = 1.f;
@@ -200,6 +202,9 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
       qf[2 * w] = __shfl_sync(0xffffffffu, down, 8 * c4);
       qf[2 * w + 1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
     }
+    const unsigned who = __ballot_sync(0xffffffffu, odd) >> (8 * c4);     // the quads of score columns 2 w, 2 w + 1
+    if (who & 0x0Fu) qf[2 * w] = NAN;
+    if (who & 0xF0u) qf[2 * w + 1] = NAN;
   }
   int qpos[QC];
 #pragma unroll

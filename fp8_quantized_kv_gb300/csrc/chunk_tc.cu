@@ -61,7 +61,6 @@
 namespace fp8kv {
 
 constexpr int kCtRows = 128, kCtThreads = 384;
-constexpr int kNotFinite = 127;    // in place of a query row's exponent: an element is infinite
 
 template <int KE, int VE>
 struct CtCfg {
@@ -309,8 +308,10 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     for (int i = 0; i < 8; ++i) {
       const int row = 16 * i + (tid >> 4);
       if constexpr (C::K16) {
+        const unsigned odd = __ballot_sync(0xffffffffu, has_inf_nan(x[i])) >> (lane & 16);
         uint4 w = p.scale_log2 != 0.f ? x[i] : make_uint4(0, 0, 0, 0);
         if (p.scale_log2 < 0.f) w = make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
+        if (odd & 0xFFFFu) w = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);      // NaN scores (has_inf_nan)
         *reinterpret_cast<uint4*>(qop + (ch >> 3) * (kCtRows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = w;
       } else {
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -325,12 +326,12 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
         }
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        // smallest power of two that brings the row within 448 = 1.75 * 2^8;
-        // e4m3 has no infinity, so a row with one is marked (a NaN stays one)
+        // smallest power of two that brings the row within 448 = 1.75 * 2^8; e4m3
+        // has no infinity: a row with one becomes NaN (has_inf_nan; a NaN stays one)
         const int ab = __float_as_int(amax);
-        const int kq = ab < 0x7F800000 ? max(-100, min(120, (ab >> 23) - 127 - 8 + ((ab & 0x7FFFFF) > 0x600000))) : kNotFinite;
+        const int kq = ab < 0x7F800000 ? max(-100, min(120, (ab >> 23) - 127 - 8 + ((ab & 0x7FFFFF) > 0x600000))) : 0;
         if (ch == 0) kq_sh[row] = (int8_t)kq;
-        const float qsc = pow2i(-kq);
+        const float qsc = ab < 0x7F800000 ? pow2i(-kq) : NAN;
         uint32_t hi[2], lo[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -578,9 +579,6 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       // what is left of the score's scale, positive (bf16 keys: the query
       // operand carries the sign, and is zero for a scale of zero)
       s2[i] = !C::K16 ? pow2i(kq_sh[row]) : p.scale_log2 != 0.f ? fabsf(p.scale_log2) : 1.f;
-      // an infinite element: every score is +-inf or NaN, and the softmax of such
-      // scores NaN (a row before the first token sees none and stays zero)
-      if (!C::K16 && kq_sh[row] == kNotFinite) s2[i] = qpos[i] >= 0 ? NAN : 1.f;
       up[i] = 1.f;
       m_used[i] = -INFINITY;
       l[i] = neg_m[i] = 0.f;

@@ -122,3 +122,29 @@ def test_queries_that_are_not_finite(dtype, D, kernel, Hq, splits):
     assert bool(torch.isnan(out[nan]).all())
     assert torch.equal(out[~nan], ref[~nan])
     assert bool((out[n:n + 3] == 0).all())
+
+
+@pytest.mark.parametrize("dtype,D,kernel,Hq", FORMS + [("k16v8", 128, "tensor_cores", 2)])
+def test_query_with_all_scores_below_every_number(dtype, D, kernel, Hq):
+    """Keys on one side of a query's infinite element give it scores of -inf alone."""
+    n = 80 if kernel == "rows64" else 5
+    cache = fk.Fp8KVCache.contiguous(1, 1, D, 96, dtype)
+    k = torch.randn(90, 1, D, device="cuda").abs().add(0.5).to(torch.bfloat16)
+    fk.fp8kv_append(cache, k, k, _i32([0] * 90), _i32(list(range(90))))
+    q = torch.zeros(n, Hq, D, device="cuda", dtype=torch.bfloat16)
+    q[1, 0] = float("-inf")
+    out = _call(q, cache, [0, n], [90], kernel, out_dtype=torch.float32)
+    assert fk.fp8kv_get_device_error() == 0
+    assert bool(torch.isnan(out[1, 0]).all()) and torch.isfinite(out[:1]).all() and torch.isfinite(out[1, 1:]).all()
+
+
+def test_infinite_query_with_a_score_scale_of_zero():
+    """0 inf is NaN, on bf16 keys too, whose operand carries the scale's sign."""
+    for dtype in ("k8v8", "k16v16"):
+        cache = make_cache(dtype, 128, 1, [90], 16, seed=64)
+        q = torch.randn(40, 2, 128, device="cuda").to(torch.bfloat16)
+        q[7, 1, 3] = float("inf")
+        for kernel in ("warp_mma", "tensor_cores"):
+            out = _call(q, cache, [0, 40], [90], kernel, sm_scale=0.0, out_dtype=torch.float32)
+            assert bool(torch.isnan(out[7, 1]).all()) and torch.isfinite(out[7, 0]).all() and torch.isfinite(out[8:]).all()
+    assert fk.fp8kv_get_device_error() == 0
