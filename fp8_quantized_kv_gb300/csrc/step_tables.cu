@@ -196,14 +196,16 @@ cudaError_t launch_build_tables(const CacheView& c, const int32_t* cached, const
 // Rotary tables.  cos and sin of theta = t w_i for positions t and pairs i.
 // With w_i in turns as a 64-bit binary fraction W_i (host, fp64), the phase
 // t W_i mod 2^64 is exact integer arithmetic: far positions lose nothing but
-// t 2^-56 turns, the rounding of W_i itself.  Its top two bits (after adding
-// an eighth of a turn) pick the quadrant; the rest is an angle x in
-// [-pi/4, pi/4], and there the Taylor polynomials through x^9 and x^10 are
+// t times the rounding of W_i itself.  Its top two bits (after adding an eighth
+// of a turn) pick the quadrant; the rest is an angle x in [-pi/4, pi/4], turned
+// to fp32 in two 32-bit parts, so that a small angle keeps its leading digits (a
+// small negative one loses 2^-56 of a turn to their sum).  There the Taylor polynomials through x^9 and x^10 are
 // within 2^-28 and 2^-31 of sine and cosine, so rounding to fp32 is what is
 // left.  A thread keeps VEC pairs and walks down the positions: the tables are
 // written once, 16 bytes a thread, and nothing is read.  131,072 positions of 32
-// pairs (34 MB) take 7.0 us on the device, 4.8 TB/s (71 % of the measured copy
-// rate; one pair a thread, a 64-bit division each and CUDA's sincosf: 35 us).
+// pairs (34 MB) take 7.1 us on the device, 4.7 TB/s (69 % of the measured copy
+// rate; 6.8 us with the upper 32 bits of the phase alone, which left a sine of a
+// millionth with two digits; one pair a thread, a 64-bit division each and CUDA's sincosf: 35 us).
 struct RopeTablesParams {
   unsigned long long w[kRopeMaxPairs];
   float *cos, *sin;
@@ -211,9 +213,11 @@ struct RopeTablesParams {
   int positions, pairs;
 };
 
-__device__ __forceinline__ void sincos_phase(unsigned int phase, float amplitude, float& c, float& s) {
-  const unsigned int quad = (phase + 0x20000000u) >> 30;
-  const float x = (float)(int)(phase - (quad << 30)) * 1.4629180792671596e-09f;      // 2 pi / 2^32
+// (phase: a 64-bit binary fraction of a turn)
+__device__ __forceinline__ void sincos_phase(unsigned long long phase, float amplitude, float& c, float& s) {
+  const unsigned int top = (unsigned int)(phase >> 32), quad = (top + 0x20000000u) >> 30;
+  const float x = fmaf((float)(unsigned int)phase, 3.4061215800865545e-19f,      // 2 pi / 2^64, 2 pi / 2^32
+                       (float)(int)(top - (quad << 30)) * 1.4629180792671596e-09f);
   const float z = x * x;
   const float sn = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 2.7557319e-6f, -1.9841270e-4f), 8.3333333e-3f), -1.6666667e-1f), x);
   const float cs = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -2.7557319e-7f, 2.4801587e-5f), -1.3888889e-3f), 4.1666667e-2f), -0.5f), 1.f);
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(256) rope_tables_kernel(const __grid_constant_
   for (long long t = (long long)blockIdx.x * rows + threadIdx.x / cols; t < p.positions; t += (long long)gridDim.x * rows) {
     float c[VEC], s[VEC];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) sincos_phase((unsigned int)(((unsigned long long)t * w[k]) >> 32), p.amplitude, c[k], s[k]);
+    for (int k = 0; k < VEC; ++k) sincos_phase((unsigned long long)t * w[k], p.amplitude, c[k], s[k]);
     const long long at = t * p.pairs + VEC * col;
     if constexpr (VEC == 4) {
       *reinterpret_cast<float4*>(p.cos + at) = make_float4(c[0], c[1], c[2], c[3]);

@@ -398,8 +398,10 @@ FP8KV_API fp8kv_status fp8kv_build_tables(const fp8kv_cache *cache, const int32_
  *   turns within the trained length) and g_i = (turns_i - ramp_low) /
  *   (ramp_high - ramp_low) clamped to [0, 1]: w_i (g_i + (1 - g_i) / factor),
  *   so fast pairs stay and slow ones are stretched.
- * The angle at position t is off by at most t * 2^-55 of a turn (w_i is held
- * as a binary fraction of a turn, so far positions lose nothing else).
+ * With w_i <= 1 the angle at position t is off by at most t * 2^-53 + 2^-56 of a
+ * turn (w_i, from 64-bit floats, is held as a 64-bit binary fraction of a turn,
+ * so far positions lose nothing else); from there sine and cosine are within
+ * 2^-21 of their value.
  *   rot_dim:  even, 2 to 256 (else FP8KV_ERR_UNSUPPORTED)
  *   cos, sin: [positions][rot_dim / 2] fp32 */
 FP8KV_API fp8kv_status fp8kv_rope_tables(int64_t positions, int32_t rot_dim, double base, double factor,

@@ -237,6 +237,28 @@ def test_rope_tables_far_positions():
             assert abs(sin[t, i].item() - math.sin(angle)) <= 2.0 ** -22
 
 
+@pytest.mark.parametrize("rot,kw", [(64, {"base": 500000.0, "factor": 8.0}), (128, {"base": 1e6}), (256, {"base": 1e8, "factor": 40.0}),
+                                    (6, {"base": 1e7})])
+def test_rope_tables_small_angles(rot, kw):
+    """Sines keep their leading digits: a sine is off by its own roundings, relative
+    to it.  The angle is a 64-bit phase converted to fp32 in two parts (each part
+    and each product rounded, the constants too, and the sum: 6 roundings of 2^-24
+    at most), sine's polynomial adds 2^-27 and its last sum 2^-24: 8 x 2^-24 =
+    2^-21 in all.  Beside it the frequency's own error, t 2^-53 of a turn."""
+    n = 4096
+    cos, sin = fk.fp8kv_rope_tables(n, rot, **kw)
+    base, factor = kw["base"], kw.get("factor", 1.0)
+    w = np.array([base ** (-2.0 * i / rot) / factor for i in range(rot // 2)])
+    t = np.arange(n)[:, None]
+    want = np.sin(t * w)
+    # (numpy's own product t w and sine: 2^-52 of the angle)
+    tol = 2.0 ** -21 * np.abs(want) + t * (2 * math.pi * 2.0 ** -53 + 2.0 ** -52 * w)
+    assert np.all(np.abs(sin.cpu().numpy() - want) <= tol)
+    want = np.cos(t * w)
+    tol = 2.0 ** -21 * np.abs(want) + t * (2 * math.pi * 2.0 ** -53 + 2.0 ** -52 * w)
+    assert np.all(np.abs(cos.cpu().numpy() - want) <= tol)
+
+
 # ------------------------------------------------------------- rope append --
 def _f32(t):
     return t.float().cpu().numpy()
