@@ -30,6 +30,12 @@ struct ChunkTile {
   int n;           // KV tiles in all
 };
 
+// Whether KV tiles j0 .. j1 - 1 of the tile's list hold the key at position `pos`.
+__device__ __forceinline__ bool chunk_own(const ChunkTile& t, int pos, int j0, int j1) {
+  const int j = pos / kChunkKeys - t.first + t.n_sink;
+  return pos >= 0 && j >= j0 && j < j1;
+}
+
 // The first key of KV tile j of the tile's list.
 __device__ __forceinline__ int chunk_key0(const ChunkTile& t, int j) {
   return (j < t.n_sink ? j : t.first + j - t.n_sink) * kChunkKeys;
@@ -39,15 +45,14 @@ __device__ __forceinline__ int chunk_key0(const ChunkTile& t, int j) {
 // batch: sequence b owns the numbers from start(b) = cu_q[b] / T + b on,
 // because it has at most (cu_q[b+1] / T - cu_q[b] / T) + 1 tiles of T tokens.
 //
-// The last sequence b with start(b) <= x (TILE), or with cu_q[b] <= x, found by
-// a 32-way search of the warp; its offsets, and its length (TILE).  Offsets that
-// decrease give some sequence of the batch (the right one, up to 32 sequences,
-// before the first that decreases: the lanes in front count, not all).
-template <bool TILE>
+// The last sequence b with start(b) <= x, found by a 32-way search of the warp;
+// its offsets and its length.  Offsets that decrease give some sequence of the
+// batch (the right one, up to 32 sequences, before the first that decreases: the
+// lanes in front count, not all).
 __device__ __forceinline__ int chunk_search(const ChunkParams& p, int x, int& q0, int& q1, int& len) {
   const int lane = threadIdx.x & 31;
   auto last_of = [](unsigned m) { return max(__clz(__brev(~m)), 1) - 1; };     // last lane of those in front
-  auto before = [&](int b, int first) { return TILE ? (long long)first / p.tile_tokens + b <= x : first <= x; };
+  auto before = [&](int b, int first) { return (long long)first / p.tile_tokens + b <= x; };
   int lo = 0, n = p.c.batch;
   while (n > 32) {
     const int step = (n + 31) >> 5, at = lane * step;
@@ -58,33 +63,39 @@ __device__ __forceinline__ int chunk_search(const ChunkParams& p, int x, int& q0
   }
   // the last step's lanes hold all there is to know of their sequence
   const int at = min(lane, n - 1) + lo;
-  const int c0 = p.cu_q[at], c1 = p.cu_q[at + 1], ln = TILE ? p.seq_lens[at] : 0;
+  const int c0 = p.cu_q[at], c1 = p.cu_q[at + 1], ln = p.seq_lens[at];
   const bool le = lane < n && (lane == 0 || before(at, c0));
   const int k = last_of(__ballot_sync(0xffffffffu, le));
   q0 = __shfl_sync(0xffffffffu, c0, k);
   q1 = __shfl_sync(0xffffffffu, c1, k);
-  if (TILE) len = __shfl_sync(0xffffffffu, ln, k);
+  len = __shfl_sync(0xffffffffu, ln, k);
   return lo + k;
 }
 __device__ __forceinline__ bool chunk_offsets_ok(const ChunkParams& p, int q0, int q1) {
   return q0 >= 0 && q1 >= q0 && q1 <= p.total_q;
 }
 
-// Whether the row of query `row` has been computed: it belongs to a sequence
-// with good offsets, and its tile number leads to that sequence (it does, unless
-// offsets decrease somewhere).  The tile's shares are then all written.
-__device__ __forceinline__ bool chunk_row_live(const ChunkParams& p, int row) {
-  if (p.cu_q == nullptr) return true;
-  int q0, q1, none;
-  const int b = chunk_search<false>(p, row, q0, q1, none);
-  if (!chunk_offsets_ok(p, q0, q1) || row < q0 || row >= q1) return false;
-  const int x = q0 / p.tile_tokens + b + (row - q0) / p.tile_tokens;
-  int c0, c1;
-  return chunk_search<true>(p, x, c0, c1, none) == b;
+// Splits: rows of a sequence with bad offsets have no shares.  The whole CTA that
+// looks at them (pair x) marks those rows for the joining kernel, in the sum of
+// their first share, which is never below zero otherwise.  Where the pair
+// decreases, any row from the largest offset so far on may be without shares, and
+// in a batch past one step of the search any row at all: all of these are marked,
+// and a tile that holds some writes its sum over the mark, or has it marked.
+constexpr float kChunkNoRow = -1.f;
+static __device__ __noinline__ void chunk_mark_rows(const int32_t* cu_q, float* part_l, int batch, int total_q, int q_heads,
+                                                    int num_splits, int x, int a0, int a1) {
+  int first = max(a0, 0);
+  if (a0 < 0 || a1 < a0) {
+    first = 0;
+    if (batch <= 32)
+      for (int i = 0; i <= x; ++i) first = max(first, cu_q[i]);
+  }
+  const int64_t rows = (int64_t)total_q * q_heads;
+  for (int64_t r = (int64_t)first * q_heads + threadIdx.x; r < rows; r += blockDim.x) part_l[r * num_splits] = kChunkNoRow;
 }
 
-// The CTA's tile.  Returns false for a number that no tile has.  `lead`: raise
-// errors.
+// The CTA's tile.  Returns false for a number that no tile has.  `lead` (the same
+// for the whole CTA): report errors.
 __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lead, ChunkTile& t) {
   const int T = p.tile_tokens;
   int b = x, q0 = x, q1 = x + 1, i0 = 0;           // one query per sequence
@@ -95,8 +106,11 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
     // offsets, so that every bad one is reported, found by the search or not
     int a0 = 0, a1 = 0;
     if (lead && x < p.c.batch) { a0 = p.cu_q[x]; a1 = p.cu_q[x + 1]; }
-    b = chunk_search<true>(p, x, q0, q1, len);
-    if (!chunk_offsets_ok(p, a0, a1)) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
+    b = chunk_search(p, x, q0, q1, len);
+    if (!chunk_offsets_ok(p, a0, a1)) {
+      if (threadIdx.x == 0) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
+      if (p.num_splits > 1) chunk_mark_rows(p.cu_q, p.part_l, p.c.batch, p.total_q, p.q_heads, p.num_splits, x, a0, a1);
+    }
     if (!chunk_offsets_ok(p, q0, q1)) return false;
     const long long i = ((long long)x - ((long long)q0 / T + b)) * T;
     if (i < 0 || i >= q1 - q0) return false;
@@ -105,7 +119,7 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
     len = p.seq_lens[b];
   }
   if (len < 0 || len > cache_capacity(p.c)) {      // reported; the sequence's queries see nothing
-    if (lead) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
+    if (lead && threadIdx.x == 0) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
     len = 0;
   }
   t.b = b;
@@ -166,16 +180,6 @@ __device__ __forceinline__ int chunk_row(const ChunkParams& p, const ChunkTile& 
     return -1;
   }
   return (page * c.kv_heads + hk) * c.page_size + (key & (c.page_size - 1));
-}
-
-// Whether one of eight bf16 elements is infinite or NaN.  The score of a query
-// that has one is +-inf or NaN at every key, and the softmax of such scores NaN,
-// all of them -inf among these: its operand, or its scores' factor, is made NaN,
-// since a score of -inf alone reads as a key that is not seen.
-__device__ __forceinline__ bool has_inf_nan(uint4 x) {
-  bool odd = false;
-  for (uint32_t w : {x.x, x.y, x.z, x.w}) odd = odd || (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-  return odd;
 }
 
 // Weight of a split's (m, l): zero for a split that saw nothing, NaN for one
@@ -255,17 +259,29 @@ struct SetAside {
 };
 
 
+// A row that sees no key is zero.  One whose seen keys all score -inf (an infinite
+// query or key) has a sum of zero too, but the softmax of such scores is NaN.  The
+// two are told apart by the row's own key, the one at its position, which it sees
+// whatever the window: a share that holds that key (`own`) and has a sum of zero
+// keeps it as -0.  (Once a finite score has been seen the sum is at least 1.)
+//
+// Factor from a whole row's unnormalised O to out, from its sum.
+__device__ __forceinline__ float chunk_inverse(float l, bool own) {
+  return l > 0.f ? 1.f / l : l == 0.f && !own ? 0.f : NAN;
+}
+__device__ __forceinline__ float chunk_share_sum(float l, bool own) { return l == 0.f && own ? -0.f : l; }
+
 // Elements d .. d + 3 of an unnormalised row of out with its maximum and sum:
 // normalised into out, or kept as this split's share.
 __device__ __forceinline__ void chunk_store(const ChunkParams& p, int64_t row, int split, int D, int d, const float (&x)[4],
-                                            float m, float l) {
+                                            float m, float l, bool own) {
   if (p.num_splits > 1) {
     const int64_t at = row * p.num_splits + split;
     *reinterpret_cast<float4*>(p.part_o + at * D + d) = make_float4(x[0], x[1], x[2], x[3]);
-    if (d == 0) { p.part_m[at] = m; p.part_l[at] = l; }
+    if (d == 0) { p.part_m[at] = m; p.part_l[at] = chunk_share_sum(l, own); }
     return;
   }
-  const float inv = l > 0.f ? 1.f / l : l == l ? 0.f : l;
+  const float inv = chunk_inverse(l, own);
   if (p.out_f32)
     *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + row * D + d) =
         make_float4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
   const int hk = blockIdx.y, split = blockIdx.z;
   ChunkTile t;
   // the last tiles of a sequence see the most keys: they start first
-  if (!chunk_tile(p, gridDim.x - 1 - blockIdx.x, tid == 0 && hk == 0 && split == 0, t)) return;
+  if (!chunk_tile(p, gridDim.x - 1 - blockIdx.x, hk == 0 && split == 0, t)) return;
   const int per = (t.n + p.num_splits - 1) / p.num_splits;
   const int j0 = min(t.n, split * per), nt = min(t.n, j0 + per) - j0;
   const int G = p.group;
@@ -120,12 +120,10 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
   for (int i = 0; i < 2; ++i) {
     uint32_t w[KS][2];                         // four elements of each step
     constexpr bool WIDE = KE == ELEM_E4M3;     // 16 elements together per lane (else 8)
-    bool odd = false;
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) {
       const int at = WIDE ? 8 * (u >> 1) + 2 * c4 + (u & 1) : 4 * u + c4;
       const uint4 x = qrow[i] >= 0 ? qsrc[i][at] : make_uint4(0, 0, 0, 0);
-      odd = odd || has_inf_nan(x);
       w[2 * u][0] = x.x; w[2 * u][1] = x.y; w[2 * u + 1][0] = x.z; w[2 * u + 1][1] = x.w;
     }
     float sc = 1.f;
@@ -145,7 +143,6 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
       const int up = min(14 - e, 126);
       if (amax > 0.f && e < 128) { sc = pow2i(up); qf[i] = pow2i(-up); }
     }
-    if ((__ballot_sync(0xffffffffu, odd) >> (lane & 28)) & 0xFu) qf[i] = NAN;    // (any lane of the row's quad)
 #pragma unroll
     for (int k = 0; k < KS; ++k)
 #pragma unroll
@@ -208,7 +205,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
           mma16816<true>(s[n], qa[2 * u + 1], w.z, w.w);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] *= p.scale_log2 * qf[e >> 1];
+        for (int e = 0; e < 4; ++e) s[n][e] *= p.scale_log2;
       }
     }
     const bool part = !chunk_all_seen(p, t, key0);
@@ -422,7 +419,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
         x[2] = odd ? own[0] : a; x[3] = odd ? own[1] : b;
         d = 16 * u + (odd ? 8 : 0) + 4 * (c4 >> 1);
       }
-      if (qrow[i] >= 0) chunk_store(p, qrow[i], split, D, d, x, m[i], l[i]);
+      if (qrow[i] >= 0) chunk_store(p, qrow[i], split, D, d, x, m[i], l[i], chunk_own(t, qpos[i], j0, j0 + nt));
     }
 }
 
@@ -435,11 +432,18 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
 // 12 splits 34 us with a warp a row, 38 us with eight.  It is launched as a
 // programmatic dependent, set up while the kernel before it drains (1 us).
 template <int D, int W>
-__global__ void __launch_bounds__(256) chunk_merge(const ChunkParams p) {
+__global__ void __launch_bounds__(256, 8) chunk_merge(const ChunkParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, S = p.num_splits;
   const int64_t row = W == 1 ? (int64_t)blockIdx.x * 8 + warp : blockIdx.x;
-  // (the offsets are an input of the kernel before as well: they can be read now)
-  const bool live = row < (int64_t)p.total_q * p.q_heads && chunk_row_live(p, (int)(row / p.q_heads));
+  const int tok = (int)(row / p.q_heads);
+  // padding in front of and behind the sequences (the offsets are an input of the
+  // kernel before as well: they can be read now); an end before the start has its
+  // rows marked (chunk_mark_rows)
+  bool live = row < (int64_t)p.total_q * p.q_heads;
+  if (live && p.cu_q != nullptr) {
+    const int start = p.cu_q[0], end = p.cu_q[p.c.batch];
+    live = tok >= start && (tok < end || end < start);
+  }
   asm volatile("griddepcontrol.wait;\n" ::: "memory");    // the shares are written
   if (!live) return;
   const float* pm = p.part_m + row * S;
@@ -448,8 +452,13 @@ __global__ void __launch_bounds__(256) chunk_merge(const ChunkParams p) {
   float M = -INFINITY, L = 0.f, x[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) x[e] = 0.f;
+  const bool marked = pl[0] == kChunkNoRow;
   for (int s = lane; s < S; s += 32) M = fmaxf(M, pm[s]);
   M = warp_max(M);
+  if (marked) return;
+  bool minus = false;                          // no finite score: did a share see some (its sum is -0)?
+  if (M == -INFINITY)
+    for (int s = 0; s < S; ++s) minus = minus || __float_as_uint(pl[s]) == 0x80000000u;
   // splits k W + warp (W 1: all)
   for (int k0 = 0; k0 * W < S; k0 += 32) {
     const int s = W == 1 ? k0 + lane : (k0 + lane) * W + warp;
@@ -487,7 +496,7 @@ __global__ void __launch_bounds__(256) chunk_merge(const ChunkParams p) {
       for (int e = 0; e < E; ++e) x[e] += sx[k][lane * E + e];
     }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = chunk_inverse(L, minus);
 #pragma unroll
   for (int e = 0; e < E; ++e) x[e] *= inv;
   if (p.out_f32) {

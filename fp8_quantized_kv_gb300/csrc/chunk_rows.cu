@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
   const int hk = blockIdx.y, split = blockIdx.z;
   ChunkTile t;
-  if (!chunk_tile(p, gridDim.x - 1 - blockIdx.x, tid == 0 && hk == 0 && split == 0, t)) return;
+  if (!chunk_tile(p, gridDim.x - 1 - blockIdx.x, hk == 0 && split == 0, t)) return;
   const CacheView& c = p.c;
   const int G = p.group;
   // groups of 16 keys: those of the first tokens, then the window's
@@ -167,12 +167,10 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
     const bool live = tokr < t.ntok && r < p.tile_tokens * G;
     const uint4* qsrc = reinterpret_cast<const uint4*>(
         p.q + (live ? (int64_t)(t.row0 + tokr) * p.q_heads + hk * G + (r - tokr * G) : 0) * D);
-    bool odd = false;
 #pragma unroll
     for (int u = 0; u < D / 32; ++u) {
       const int at = KE == ELEM_E4M3 ? 8 * (u >> 1) + 2 * c4 + (u & 1) : 4 * u + c4;
       const uint4 x = live ? qsrc[at] : make_uint4(0, 0, 0, 0);
-      odd = odd || has_inf_nan(x);
       qb[w][2 * u][0] = x.x; qb[w][2 * u][1] = x.y; qb[w][2 * u + 1][0] = x.z; qb[w][2 * u + 1][1] = x.w;
     }
     qf[2 * w] = qf[2 * w + 1] = 1.f;
@@ -202,9 +200,6 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
       qf[2 * w] = __shfl_sync(0xffffffffu, down, 8 * c4);
       qf[2 * w + 1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
     }
-    const unsigned who = __ballot_sync(0xffffffffu, odd) >> (8 * c4);     // the quads of score columns 2 w, 2 w + 1
-    if (who & 0x0Fu) qf[2 * w] = NAN;
-    if (who & 0xF0u) qf[2 * w + 1] = NAN;
   }
   int qpos[QC];
 #pragma unroll
@@ -519,7 +514,9 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
       x[0] = fmaf(w, v.x, x[0]); x[1] = fmaf(w, v.y, x[1]);
       x[2] = fmaf(w, v.z, x[2]); x[3] = fmaf(w, v.w, x[3]);
     }
-    chunk_store(p, (int64_t)(t.row0 + tk) * p.q_heads + hk * G + (r - tk * G), split, D, d, x, M, L);
+    const int pos = t.pos0 + tk, jpos = pos / kRowKeys - first + n_sink;         // the group of the row's own key
+    const bool own = pos >= 0 && jpos >= split * per && jpos < (split + 1) * per;
+    chunk_store(p, (int64_t)(t.row0 + tk) * p.q_heads + hk * G + (r - tk * G), split, D, d, x, M, L, own);
   }
 }
 

@@ -148,6 +148,10 @@ __device__ __forceinline__ bool softmax_any(bool pred) {
       : "memory");
   return r != 0;
 }
+// Two bf16 elements times zero: 0, or NaN for one that is infinite or NaN.
+__device__ __forceinline__ uint32_t times_zero(uint32_t w) {
+  return ((w & 0x7F80u) == 0x7F80u ? 0x7FFFu : 0u) | ((w & 0x7F800000u) == 0x7F800000u ? 0x7FFF0000u : 0u);
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -184,12 +188,13 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   int8_t* kq_sh = reinterpret_cast<int8_t*>(bars) + 256;      // [128] exponent of each row's query operand
-  static_assert(8 * (2 * C::KN + 2 * C::VN + 2 * OPN + C::NCOL + 6) + 8 <= 256 && 256 + kCtRows <= C::MISC, "they fit");
+  int8_t* own_sh = kq_sh + kCtRows;               // [128] is the row's own key in this share?
+  static_assert(8 * (2 * C::KN + 2 * C::VN + 2 * OPN + C::NCOL + 6) + 8 <= 256 && 256 + 2 * kCtRows <= C::MISC, "they fit");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hk = blockIdx.y, split = blockIdx.z;
   ChunkTile t;
-  if (!chunk_tile(p, gridDim.x - 1 - blockIdx.x, tid == 0 && hk == 0 && split == 0, t)) return;
+  if (!chunk_tile(p, gridDim.x - 1 - blockIdx.x, hk == 0 && split == 0, t)) return;
   const int per = (t.n + p.num_splits - 1) / p.num_splits;
   const int j0 = min(t.n, split * per), n = min(t.n, j0 + per) - j0;
   const CacheView& c = p.c;
@@ -296,6 +301,7 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   const int hf = (tid >> 7) & 1;                  // softmax warps: which half of its lanes, and of O's dims
   if (warp < 8) {
     const int ch = tid & 15;
+    if (tid < kCtRows) own_sh[tid] = chunk_own(t, t.pos0 + tid / G, j0, j0 + n);
     uint4 x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -308,10 +314,9 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     for (int i = 0; i < 8; ++i) {
       const int row = 16 * i + (tid >> 4);
       if constexpr (C::K16) {
-        const unsigned odd = __ballot_sync(0xffffffffu, has_inf_nan(x[i])) >> (lane & 16);
-        uint4 w = p.scale_log2 != 0.f ? x[i] : make_uint4(0, 0, 0, 0);
+        uint4 w = x[i];
         if (p.scale_log2 < 0.f) w = make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
-        if (odd & 0xFFFFu) w = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);      // NaN scores (has_inf_nan)
+        if (p.scale_log2 == 0.f) w = make_uint4(times_zero(w.x), times_zero(w.y), times_zero(w.z), times_zero(w.w));
         *reinterpret_cast<uint4*>(qop + (ch >> 3) * (kCtRows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = w;
       } else {
         const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         // smallest power of two that brings the row within 448 = 1.75 * 2^8; e4m3
-        // has no infinity: a row with one becomes NaN (has_inf_nan; a NaN stays one)
+        // has no infinity: a row with one becomes NaN, as its softmax is
         const int ab = __float_as_int(amax);
         const int kq = ab < 0x7F800000 ? max(-100, min(120, (ab >> 23) - 127 - 8 + ((ab & 0x7FFFFF) > 0x600000))) : 0;
         if (ch == 0) kq_sh[row] = (int8_t)kq;
@@ -755,9 +760,10 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     const uint32_t lane_q = (uint32_t)(32 * (warp & 3)) << 16;
     const float mr = empty ? -INFINITY : st[r], lr = empty ? 0.f : st[kCtRows + r], of = empty ? 0.f : st[2 * kCtRows + r];
     const bool whole = p.num_splits == 1;
-    const float f = !whole ? of : lr > 0.f ? of / lr : lr == lr ? 0.f : lr;
+    const bool own = !failed && own_sh[r];
+    const float f = whole ? of * chunk_inverse(lr, own) : of;
     const int64_t at = whole ? qrow : qrow * p.num_splits + split;
-    if (!whole && live && hf == 0) { p.part_m[at] = mr; p.part_l[at] = lr; }
+    if (!whole && live && hf == 0) { p.part_m[at] = mr; p.part_l[at] = chunk_share_sum(lr, own); }
 #pragma unroll 1
     for (int k = 4 * hf; k < 4 * hf + 4; ++k) {
       uint32_t rr[16];

@@ -475,12 +475,15 @@ FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q
  * have no influence on it, whatever they hold (NaN included; pages that no
  * query sees need not exist).  A seen value that is not finite makes that
  * element of the row not finite; the tensor-core kernel may make the whole row
- * NaN.  A length below 0 or past the capacity raises SEQ_TOO_LONG and gives zero rows; offsets that
- * decrease or pass total_q raise it and leave their rows as they were.  (Where
- * offsets decrease, rows of other sequences may be left as they were too, and a
- * row that two sequences claim holds nothing defined.)  A wait of the
- * tensor-core kernel that runs out raises TIMEOUT; its rows are zero, or lack
- * that split's keys. */
+ * NaN.  Queries and seen keys that are not finite count as in the definition: a
+ * score of -inf weighs nothing beside a finite one, and +inf, NaN or -inf alone
+ * make the row NaN.
+ * A length below 0 or past the capacity, of a sequence with queries, raises
+ * SEQ_TOO_LONG and gives zero rows; offsets that decrease or pass total_q raise
+ * it and leave their rows as they were.  (Where offsets decrease, rows of other
+ * sequences may be left as they were too, and a row that two sequences claim
+ * holds nothing defined.)  A wait of the tensor-core kernel that runs out raises
+ * TIMEOUT; its rows are zero, or lack that split's keys. */
 FP8KV_API fp8kv_status fp8kv_chunk_attention(const void *q, const fp8kv_cache *cache,
                                              const int32_t *cu_q, const int32_t *seq_lens,
                                              int64_t total_q, int32_t q_heads, float sm_scale,

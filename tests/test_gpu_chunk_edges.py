@@ -148,3 +148,56 @@ def test_infinite_query_with_a_score_scale_of_zero():
             out = _call(q, cache, [0, 40], [90], kernel, sm_scale=0.0, out_dtype=torch.float32)
             assert bool(torch.isnan(out[7, 1]).all()) and torch.isfinite(out[7, 0]).all() and torch.isfinite(out[8:]).all()
     assert fk.fp8kv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("splits", [1, 5])
+@pytest.mark.parametrize("dtype,D,kernel,Hq", [f for f in FORMS if f[0] != "mxk8v8"] + [("k8v16", 128, "tensor_cores", 2)])
+def test_scores_of_minus_infinity(dtype, D, kernel, Hq, splits):
+    """An infinite key on the far side of a query scores -inf: it weighs nothing
+    beside keys with finite scores, and a query that sees such keys alone is NaN,
+    whichever share holds them; queries before the first token stay zero."""
+    n, T, bad = (80, 300, (250, 251, 252, 299)) if kernel == "rows64" else (9, 300, (293, 294, 295, 299))
+    cache = fk.Fp8KVCache.contiguous(2, 1, D, 304, dtype)
+    g = torch.Generator(device="cuda").manual_seed(66)
+    k = (torch.rand(T + 4, 1, D, generator=g, device="cuda") + 0.5).to(torch.bfloat16)
+    v = torch.randn(T + 4, 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    fk.fp8kv_append(cache, k, v, _i32([0] * T + [1] * 4), _i32(list(range(T)) + list(range(4))))
+    q = torch.zeros(2 * n, Hq, D, device="cuda", dtype=torch.bfloat16)
+    q[:, :, 0] = -1.0
+    for j in bad:
+        if dtype in ("k8v8", "k8v16"):
+            cache.k_scale[0, 0, j] = float("inf")
+        else:
+            cache.k[0, 0, j, 0] = float("inf")
+    args = dict(num_splits=splits, out_dtype=torch.float32)
+    pos = torch.arange(T - n, T)
+    for window, sinks in ((0, 0), (1, 0), (2, 0), (3, 0), (2, 1)):
+        out = _call(q, cache, [0, n, 2 * n], [T, 4], kernel, window=window, sinks=sinks, **args)
+        assert fk.fp8kv_get_device_error() == 0
+        seen = [[j for j in range(int(p) + 1) if window == 0 or j > p - window or j < sinks] for p in pos]
+        alone = torch.tensor([all(j in bad for j in s) for s in seen], device="cuda")
+        assert bool(torch.isnan(out[:n][alone]).all()) and bool(torch.isfinite(out[:n][~alone]).all())
+        assert bool((out[n:2 * n - 4] == 0).all()) and bool(torch.isfinite(out[2 * n - 4:]).all())
+        # a weight of zero: the value of such a key does not matter
+        old = cache.v[0, 0, 299].clone()
+        cache.v[0, 0, 299] = cache.v[0, 0, 17]
+        again = _call(q, cache, [0, n, 2 * n], [T, 4], kernel, window=window, sinks=sinks, **args)
+        cache.v[0, 0, 299] = old
+        assert torch.equal(again[:n][~alone], out[:n][~alone])
+
+
+@pytest.mark.parametrize("dtype,D,kernel,Hq", FORMS)
+def test_query_with_all_scores_below_every_number_in_splits(dtype, D, kernel, Hq):
+    """As without splits, in shares that hold the query's own key and in others."""
+    n = 80 if kernel == "rows64" else 5
+    cache = fk.Fp8KVCache.contiguous(1, 1, D, 608, dtype)
+    k = torch.randn(600, 1, D, device="cuda").abs().add(0.5).to(torch.bfloat16)
+    fk.fp8kv_append(cache, k, k, _i32([0] * 600), _i32(list(range(600))))
+    q = torch.zeros(n, Hq, D, device="cuda", dtype=torch.bfloat16)
+    q[1, 0] = float("-inf")
+    for splits in (2, 6):
+        for window, sinks in ((0, 0), (100, 70)):
+            out = _call(q, cache, [0, n], [600], kernel, out_dtype=torch.float32, num_splits=splits, window=window, sinks=sinks)
+            assert bool(torch.isnan(out[1, 0]).all()) and torch.isfinite(out[:1]).all() and torch.isfinite(out[1, 1:]).all()
+            assert torch.isfinite(out[2:]).all()
+    assert fk.fp8kv_get_device_error() == 0
