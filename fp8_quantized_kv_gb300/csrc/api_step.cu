@@ -1,6 +1,7 @@
 // api_step.cu -- the extern "C" boundary of the serving-step calls: argument
 // checks, launch plans, status codes.  As in api.cu, every entry validates on
 // the host, launches on the caller's stream and allocates nothing.
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -163,16 +164,12 @@ fp8kv_status fp8kv_rope_tables(int64_t positions, int32_t rot_dim, double base, 
                                int32_t original_positions, double ramp_low, double ramp_high, double amplitude,
                                float* cos, float* sin, fp8kv_stream_t stream) {
   if (positions < 0 || rot_dim <= 0 || original_positions < 0) return FP8KV_ERR_INVALID_ARG;
-  if (!(base > 0) || !std::isfinite(base) || !(factor > 0) || !std::isfinite(factor) || !std::isfinite(amplitude))
+  if (!(base > 0) || !std::isfinite(base) || !(factor > 0) || !std::isfinite(factor) || !(std::fabs(amplitude) <= FLT_MAX))
     return FP8KV_ERR_INVALID_ARG;
   if (original_positions > 0 && !(std::isfinite(ramp_low) && std::isfinite(ramp_high) && ramp_low < ramp_high))
     return FP8KV_ERR_INVALID_ARG;
   if (rot_dim % 2 != 0 || rot_dim > 2 * kRopeMaxPairs || positions > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
-  if (positions == 0) return FP8KV_OK;
-  if (!cos || !sin || misaligned(cos, 4) || misaligned(sin, 4)) return FP8KV_ERR_INVALID_ARG;
-  const size_t bytes = (size_t)positions * (rot_dim / 2) * sizeof(float);
-  if (overlap({cos, bytes}, {sin, bytes})) return FP8KV_ERR_INVALID_ARG;
-  constexpr double kTwoPi = 6.283185307179586476925;
+  constexpr double kTwoPi = 6.283185307179586476925, kMostRadians = 1048576.0;
   unsigned long long w[kRopeMaxPairs];
   for (int i = 0; i < rot_dim / 2; ++i) {
     double f = std::pow(base, -2.0 * i / rot_dim);
@@ -183,6 +180,8 @@ fp8kv_status fp8kv_rope_tables(int64_t positions, int32_t rot_dim, double base, 
     } else {
       f /= factor;
     }
+    // (a 64-bit float has no fraction of a turn left where the turns are many)
+    if (!(f <= kMostRadians)) return FP8KV_ERR_INVALID_ARG;
     // the frequency in turns per position, modulo one turn (positions are
     // whole numbers), as a 64-bit binary fraction
     double turns = f / kTwoPi;
@@ -190,6 +189,10 @@ fp8kv_status fp8kv_rope_tables(int64_t positions, int32_t rot_dim, double base, 
     const double scaled = std::ldexp(turns, 64);
     w[i] = scaled >= 18446744073709551616.0 ? 0 : (unsigned long long)scaled;
   }
+  if (positions == 0) return FP8KV_OK;
+  if (!cos || !sin || misaligned(cos, 4) || misaligned(sin, 4)) return FP8KV_ERR_INVALID_ARG;
+  const size_t bytes = (size_t)positions * (rot_dim / 2) * sizeof(float);
+  if (overlap({cos, bytes}, {sin, bytes})) return FP8KV_ERR_INVALID_ARG;
   return cuda_status(launch_rope_tables((int)positions, rot_dim / 2, w, (float)amplitude, cos, sin,
                                         (cudaStream_t)stream));
 }

@@ -401,7 +401,8 @@ FP8KV_API fp8kv_status fp8kv_build_tables(const fp8kv_cache *cache, const int32_
  * With w_i <= 1 the angle at position t is off by at most t * 2^-53 + 2^-56 of a
  * turn (w_i, from 64-bit floats, is held as a 64-bit binary fraction of a turn,
  * so far positions lose nothing else); from there sine and cosine are within
- * 2^-21 of their value.
+ * 2^-21 of their value.  A frequency past 2^20 radians a position (a base below 1,
+ * a factor near 0) or an amplitude past fp32 is refused (FP8KV_ERR_INVALID_ARG).
  *   rot_dim:  even, 2 to 256 (else FP8KV_ERR_UNSUPPORTED)
  *   cos, sin: [positions][rot_dim / 2] fp32 */
 FP8KV_API fp8kv_status fp8kv_rope_tables(int64_t positions, int32_t rot_dim, double base, double factor,

@@ -166,3 +166,17 @@ def test_chunk_idle_step(lib, group, head_dim, layout):
                 assert lib.fp8kv_chunk_workspace_bytes(cache, 0, group, window, 0, splits, kernel) == 0
                 assert lib.fp8kv_chunk_attention(None, cache, 0x20000, None, 0, group, 0.1, window, 0, splits, kernel, None, 0, None, 0,
                                                  None) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(base=1e-300), dict(base=1e-12, rot=2 * 128), dict(factor=1e-300), dict(factor=1e-7),
+                                dict(factor=1e-310, original=4096, lo=1.0, hi=4.0), dict(amplitude=1e39), dict(amplitude=-1e300),
+                                dict(base=5e-324), dict(base=1e-300, positions=0)])
+def test_rope_tables_refuse_what_no_table_holds(lib, kw):
+    """Frequencies that are not finite, or so high that no fraction of a turn is
+    left of them, and amplitudes that overflow fp32."""
+    a = dict(positions=100, rot=64, base=1e4, factor=1.0, original=0, lo=1.0, hi=4.0, amplitude=1.0, cos=0x20000, sin=0x80000)
+    a.update(kw)
+    assert lib.fp8kv_rope_tables(*a.values(), None) == INVALID
+    # slow frequencies, down to none at all, have tables
+    for base in (1.0, 0.3, 1e300):
+        assert lib.fp8kv_rope_tables(0, 64, base, 1.0, 0, 1.0, 4.0, 1.0, None, None, None) == 0
