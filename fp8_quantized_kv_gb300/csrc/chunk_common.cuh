@@ -30,6 +30,9 @@ struct ChunkTile {
   int n;           // KV tiles in all
 };
 
+// KV tiles that `keys` keys (>= 0, up to 2^31 - 16) take.
+__device__ __forceinline__ int chunk_tiles(int keys) { return (int)(((unsigned)keys + kChunkKeys - 1) / kChunkKeys); }
+
 // Whether KV tiles j0 .. j1 - 1 of the tile's list hold the key at position `pos`.
 __device__ __forceinline__ bool chunk_own(const ChunkTile& t, int pos, int j0, int j1) {
   const int j = pos / kChunkKeys - t.first + t.n_sink;
@@ -132,10 +135,10 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
   if (p.window > 0) {
     const long long lo = (long long)t.pos0 - p.window + 1;
     t.lo = lo > 0 ? (int)lo : 0;
-    t.n_sink = min((min(p.sinks, t.kv_end) + kChunkKeys - 1) / kChunkKeys, t.lo / kChunkKeys);
+    t.n_sink = min(chunk_tiles(min(p.sinks, t.kv_end)), t.lo / kChunkKeys);
   }
   t.first = t.lo / kChunkKeys;
-  t.n = t.n_sink + max(0, (t.kv_end + kChunkKeys - 1) / kChunkKeys - t.first);
+  t.n = t.n_sink + max(0, chunk_tiles(t.kv_end) - t.first);
   return true;
 }
 

@@ -1,5 +1,5 @@
 """Chunk attention at its edges: offsets that are refused, in calls with splits;
-queries that are not finite."""
+queries and keys that are not finite; positions close to 2^31."""
 import pytest
 import torch
 
@@ -201,3 +201,20 @@ def test_query_with_all_scores_below_every_number_in_splits(dtype, D, kernel, Hq
             assert bool(torch.isnan(out[1, 0]).all()) and torch.isfinite(out[:1]).all() and torch.isfinite(out[1, 1:]).all()
             assert torch.isfinite(out[2:]).all()
     assert fk.fp8kv_get_device_error() == 0
+
+
+# --------------------------------------------------- positions close to 2^31 --
+@pytest.mark.parametrize("D,kernel,new", [(128, "warp_mma", 1), (128, "tensor_cores", 40), (64, "rows64", 70)])
+def test_positions_up_to_31_bits(D, kernel, new):
+    """A table row for 2^31 - 16 tokens, full, under a window: the last tile's end
+    is past 31 bits when rounded up.  Tiles lie as in a sequence of 112 tokens."""
+    cols, window = (1 << 27) - 1, 15
+    small = make_cache("k8v8", D, 1, [112], 16, seed=65, poison=False)
+    q = torch.randn(new, 2, D, device="cuda").to(torch.bfloat16)
+    want = _call(q, small, [0, new], [112], kernel, window=window, num_splits=1, out_dtype=torch.float32)
+    big = fk.Fp8KVCache.paged(torch.full((1, cols), -1, dtype=torch.int32), small.num_pages, 1, D, 16)
+    for side in ("k", "v", "k_scale", "v_scale"):
+        getattr(big, side).copy_(getattr(small, side))
+    big.page_table[0, cols - 7:] = small.page_table[0, :7]
+    out = _call(q, big, [0, new], [cols * 16], kernel, window=window, num_splits=1, out_dtype=torch.float32)
+    assert fk.fp8kv_get_device_error() == 0 and torch.equal(out, want)
