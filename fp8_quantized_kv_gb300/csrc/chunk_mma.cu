@@ -18,8 +18,9 @@
 // use the same order: no shuffles, no transposition of K.
 // P (16 bits, the one rounding of the softmax) is f16 next to e4m3 values,
 // with the value scale folded in and a power of two 2^-kp that follows the
-// largest value scale the row sees (O is rescaled when it rises), and bf16 next to
-// bf16 values.  m, l and O are fp32.
+// largest value scale the row sees (to [2^14, 2^15): the step below 2^-28 of that is
+// 2^-39 of the largest value; O is rescaled when it rises), and bf16 next to bf16
+// values, since the instruction takes one 16-bit type.  m, l and O are fp32.
 //
 // What bounds it: instruction issue (conversions of codes are repeated by each
 // of a tile's four warps).  4 sequences of 256-512 queries over 4,000-8,000 tokens

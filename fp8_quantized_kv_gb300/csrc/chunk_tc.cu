@@ -18,7 +18,8 @@
 //                                  e4m3 values converted to f16 (exact), bf16
 //                                  values as they landed
 // P carries the value scale and a power of two 2^-kp per row, as in
-// chunk_mma.cu: 16 bits, the one rounding of the softmax.
+// chunk_rows.cu: 16 bits, the one rounding of the softmax (f16 beside e4m3
+// values; bf16 beside bf16 ones, since the instruction takes one 16-bit type).
 //
 // The CTA keeps to 256 TMEM columns (two score buffers, one O) and at most 113
 // KB of shared memory, so two CTAs share an SM: one's softmax runs while the

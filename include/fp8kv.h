@@ -471,6 +471,12 @@ FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q
  *               Calls that may run at once need one each.
  *   out:        [total_q][q_heads][head_dim], bf16 or fp32 per out_dtype,
  *               16-byte aligned, apart from q
+ * Roundings: a weight is held in 16 bits once, f16 beside e4m3 values (2^-11 of
+ * it, or 2^-31 of the largest seen value where the weighted value is that small),
+ * bf16 beside bf16 values (2^-8: the matrix instructions take one 16-bit type).
+ * Beside e4m3 keys the tensor-core kernel holds a query's elements to 2^-18 of
+ * its largest (two e4m3 terms), the other kernels to 2^-39.  Sums, maxima and the
+ * output before its own rounding are fp32.
  * A query that sees no key (its position is negative: seq_lens[b] is less than
  * its sequence's queries) gets a zero row.  Keys that a query does not see
  * have no influence on it, whatever they hold (NaN included; pages that no

@@ -1,10 +1,11 @@
 """Chunk attention at its edges: offsets that are refused, in calls with splits;
-queries and keys that are not finite; positions close to 2^31."""
+queries and keys that are not finite; positions close to 2^31; value scales far
+apart."""
 import pytest
 import torch
 
 import fp8_quantized_kv_gb300 as fk
-from test_gpu_chunk import _i32, make_cache
+from test_gpu_chunk import _i32, cache_values, definition, make_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -218,3 +219,38 @@ def test_positions_up_to_31_bits(D, kernel, new):
     big.page_table[0, cols - 7:] = small.page_table[0, :7]
     out = _call(q, big, [0, new], [cols * 16], kernel, window=window, num_splits=1, out_dtype=torch.float32)
     assert fk.fp8kv_get_device_error() == 0 and torch.equal(out, want)
+
+
+# ------------------------------------------------------ range of the weights --
+@pytest.mark.parametrize("octaves", [10, 20, 24])
+@pytest.mark.parametrize("dtype,D,kernel,Hq", [f for f in FORMS if f[0] in ("k8v8", "mxk8v8")] + [("k16v8", 128, "tensor_cores", 2)])
+def test_small_value_scale_of_the_heaviest_key(dtype, D, kernel, Hq, octaves):
+    """A query's weight goes to keys whose value scale is 2^-octaves of another seen
+    key's, which weighs next to nothing.  The weight operand is an f16 number times
+    a power of two that puts the largest seen value scale in [2^6, 2^7) (64-row
+    tiles: [2^14, 2^15)).  Below 2^-14 its step is 2^-24, and half of that is, in
+    values (codes up to 448, scale = max |v| / 448), 2^-31 (2^-39) of the largest
+    seen |v| for each key; the sum that divides it is 1 at least.  The rest of the
+    tolerance is that of the other tests."""
+    n, T = (80, 84) if kernel == "rows64" else (3, 12)
+    cache = fk.Fp8KVCache.contiguous(1, 1, D, 96, dtype)
+    g = torch.Generator(device="cuda").manual_seed(67)
+    base = torch.randn(1, 1, D, generator=g, device="cuda")
+    k = (-2.0 * base).repeat(T, 1, 1)
+    k[1] = 1.5 * base                                       # the heaviest key (all queries see it), and the one beside it
+    k[2] = 1.5 * base + 0.01 * torch.randn(1, D, generator=g, device="cuda")
+    v = torch.randn(T, 1, D, generator=g, device="cuda")
+    v[1:3] *= 2.0 ** -octaves
+    k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    fk.fp8kv_append(cache, k, v, _i32([0] * T), _i32(list(range(T))))
+    # scores of about 1.5 |base|^2 sm (17 and 12 at these head dims), and -2 |base|^2 sm
+    q = base.expand(n, Hq, D).contiguous().to(torch.bfloat16)
+    lens, cu, sm = [T], [0, n], D ** -0.5
+    out = _call(q, cache, cu, lens, kernel, out_dtype=torch.float32)
+    assert fk.fp8kv_get_device_error() == 0
+    o, pv, qk, qs, keys, vmax = definition(q, cache_values(cache, lens), cu, lens, 0, 0, sm)
+    d = D * 2.0 ** -23 * qk + 2.0 ** -19 + (2.0 ** -18 * qs if kernel == "tensor_cores" else 0)
+    step = 2.0 ** (-39 if kernel == "rows64" else -31)
+    tol = (2.0 ** -11 + 4 * d)[..., None] * pv + (keys[:, None] * vmax * step)[..., None]
+    worst = ((out.double().cpu() - o).abs() - tol).max().item()
+    assert worst <= 0, f"past the tolerance by {worst:.3e}"
