@@ -31,11 +31,16 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // How a chunk call runs, from its sizes (lengths are on the device).
 // Kernel, by the average number of query rows (queries x heads of a group) a
 // sequence has: up to 16 rows the few-row kernel, in tiles of 8 or 16 (one token
-// of 64 sequences under a 1,024-token window: 36 us, against 81 us on tcgen05; two
+// of 64 sequences under a 1,024-token window: 35 us, against 81 us on tcgen05; two
 // tokens x 8 heads of 64 sequences of 2K-4K tokens: 74 us, against 101 us);
-// above, tcgen05 where it is built (8 tokens x 4 heads over 8,000 tokens, 4
-// sequences: 40 us against 45 us at the best split counts; 256 x 4 over 16,000:
-// 108 against 447).  Block-scaled keys stay on the few-row kernel (2-4 x 8 over
+// above, tcgen05 where it is built.  Between 17 and 32 rows neither is clearly ahead
+// (8 tokens x 4 heads over 8,000 tokens, 4 sequences: 40 us against 45 us at the best
+// split counts; 2-4 x 8 over 4K-8K, 16 sequences: 62 against 58 to 71), far above
+// it is (256 x 4 over 16,000: 108 against 447).  The average counts idle sequences
+// and rows of padding, and one kernel runs the whole call: batches of unlike
+// sequences (a prompt in many idle slots, or beside many single tokens) get the
+// form that suits only some of them.  Lengths of queries are on the device, so the
+// host knows no better.  Block-scaled keys stay on the few-row kernel (2-4 x 8 over
 // 4K-8K, 16 sequences: 63 us, 88 us on the form that the warp-level kernel had for
 // them; 256-512 x 8, 4 sequences: 1.15 ms against 1.33), head dim 64 does up to 32
 // rows (2-4 x 8 of 64 sequences of 2K-4K, bf16: 64 us against 71 on 64-row tiles at
@@ -50,8 +55,8 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // waves), 75 us in 3 (1.7), 79 us in 4.  Shares are 192 keys or longer (one token of
 // 32 / 8 heads over 6,200: 10.6 us in 32 shares, 11.1 in 24, 12.1 in 64).
 // Without a window lengths can differ widely: shares of about 4,096 keys at most
-// then even them out (64 sequences of 1K-16K tokens: 268 us in 4 shares, 355 us
-// whole; sequences of 700 tokens in the same cache pay 35 us instead of 23), as
+// then even them out (64 sequences of 1K-16K tokens, 32 / 8 heads: 249 us in 4
+// shares, 355 us whole; sequences of 700 tokens in the same cache pay 35 us instead of 23), as
 // long as that makes no more than 16 CTAs an SM.
 //
 // Splits of the others: tiles are few -> one wave.  tcgen05: two CTAs an SM,

@@ -426,12 +426,13 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
 
 // Joins the splits of each row of out.  Rows that no tile holds (padding, and
 // those of a sequence with bad offsets) have no shares and stay as they were.
-// Many rows or few splits: a warp a row (W 1); few rows of more than
-// three splits: the eight warps of a CTA take every eighth split each and add
-// their sums in order.  A chain of loads bounds it: one token of 32 heads over
-// 32,000 tokens in 76 splits took 33 us with a warp a row, 18 us so; 3,000 rows of
-// 12 splits 34 us with a warp a row, 38 us with eight.  It is launched as a
-// programmatic dependent, set up while the kernel before it drains (1 us).
+// Many rows or few splits: a warp a row (W 1); few rows of more than three splits:
+// the eight warps of a CTA take every eighth split each and add their sums in
+// order.  A chain of loads bounds it: one token of 32 heads over 24,000 tokens in
+// 76 splits takes 33 us with a warp a row, 17 us so; 3,000 rows of 12 splits 34 us
+// with a warp a row, 38 us with eight.  It is launched as a programmatic dependent,
+// set up while the kernel before it drains (1 us); at 32 registers 1,024 rows are
+// one wave (at 39 two, 1.5 us more).
 template <int D, int W>
 __global__ void __launch_bounds__(256, 8) chunk_merge(const ChunkParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, S = p.num_splits;

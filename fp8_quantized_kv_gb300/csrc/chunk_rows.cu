@@ -2,7 +2,7 @@
 // rows, for single tokens of a group of heads and a few drafted tokens: the cache
 // is read once and nothing else takes as long, so the kernel is built around
 // keeping loads in flight.  Also the form of block-scaled keys at any length
-// (256-512 tokens x 8 heads, 4 sequences of 4K-8K: 1.15 ms, conversions and the
+// (256-512 tokens x 8 heads, 4 sequences of 4K-8K: 1.14 ms, conversions and the
 // four fp32 partial products of a score).
 //
 // The products are turned around so that the queries are the narrow side of the
@@ -24,8 +24,8 @@
 // 32-element partial products are scaled in fp32 and added.
 //
 // Measured on one GB300 (64 sequences, 32 query / 8 KV heads, head dim 128,
-// e4m3, 16-token pages, device time): a 1,024-token window 36 us (140 MB: 3.9
-// TB/s, 57 % of the measured copy rate); 2,048 more tokens of window cost at 5.4
+// e4m3, 16-token pages, device time): a 1,024-token window 35 us (140 MB: 4.0
+// TB/s, 59 % of the measured copy rate); 2,048 more tokens of window cost at 5.4
 // TB/s, so what is left is the fixed part (about 5 us to find the tile, load the
 // first groups and join) and the issue slots (46 % busy: 430 instructions a
 // group, 80 of them the conversion of 4,096 codes).  On the way there: 58 us with
@@ -37,7 +37,7 @@
 // SM, one wave and a bit; the same 59 us as below where shares can even that out).
 //
 // Sixteen rows (two tokens x 8 heads, 4 KV heads, 64 sequences of 2K-4K tokens,
-// 210 MB): 74 us, three CTAs an SM at 168 registers; 59 us for one token.  The
+// 210 MB): 74 us, three CTAs an SM at 168 registers; 55 us for one token.  The
 // second set costs its products, exponentials and transposes, not the codes'
 // conversion.  On the warp-level kernel, whose four warps share a tile, the call took
 // 90 us at the best split count, on tcgen05's 128-row tiles 101 us; 16 heads on one

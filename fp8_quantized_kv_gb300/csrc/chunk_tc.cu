@@ -38,8 +38,8 @@
 // tile's rows come out as if they saw no key (an empty share, a row of zeros).
 //
 // Measured on one GB300: 3,727 queries over 2,000-8,000 tokens (28 query / 4 KV
-// heads, e4m3, 16-token pages) 281 us, 691 TFLOP/s, 36 % of the measured bf16
-// peak; 6,642 queries under a 512-token window (16 / 2 heads, bf16) 78 us.  What
+// heads, e4m3, 16-token pages) 280 us, 693 TFLOP/s, 36 % of the measured bf16
+// peak; 6,642 queries under a 512-token window (16 / 2 heads, bf16) 73 us.  What
 // bounds it: the chain of a tile through a softmax warp (TMEM load, scales,
 // maximum, exponentials, P store: about 2,500 cycles with two CTAs on the SM,
 // issue slots 60 % busy, tensor pipe 44 %, shared-memory port 49 %).  On the way:

@@ -10,7 +10,7 @@
 //
 // What bounds it: memory.  7,940 tokens of 28 query and 4 KV heads (143 MB)
 // take 26.8 us on the device, 5.3 TB/s (79 % of the measured copy rate); 64
-// tokens take 3.4 us, a launch and two dependent loads.  One row pass a warp
+// tokens take 2.7 us, a launch and two dependent loads.  One row pass a warp
 // took 73 us, eight behind the token's slot 41 us, eight loaded before it this.
 //
 // A row of D values takes D / 8 lanes; lane s holds two groups of four

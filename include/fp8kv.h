@@ -377,7 +377,7 @@ FP8KV_API fp8kv_status fp8kv_prefill_attention(const void *q, const fp8kv_cache 
  * to run steps from a graph, copy seq_lens and free_head_out back between
  * two steps.  At most 16384 sequences (else FP8KV_ERR_UNSUPPORTED).
  * A sequence that cannot be placed keeps its rows with slot and pos -1, gets
- * no page, has seq_lens = cached_lens, and raises a device error bit:
+ * no page, has seq_lens = cached_lens (0 for a negative one), and raises a device error bit:
  * SEQ_TOO_LONG for a negative length or one past the capacity, NO_PAGES when
  * the free list does not hold all of its pages (later sequences that need
  * pages fail too).  An invalid page id gives slot -1 and BAD_PAGE; new rows
