@@ -26,7 +26,7 @@ DTYPES = {"k8v8": K8V8, "k16v8": K16V8, "k16v16": K16V16, "k8v16": K8V16, "mxk8v
 LAYOUT_CONTIGUOUS, LAYOUT_PAGED = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 
-DEVERR_SEQ_TOO_LONG, DEVERR_BAD_PAGE, DEVERR_TIMEOUT, DEVERR_NO_PAGES = 0x1, 0x2, 0x4, 0x8
+DEVERR_SEQ_TOO_LONG, DEVERR_BAD_PAGE, DEVERR_TIMEOUT, DEVERR_NO_PAGES, DEVERR_BAD_TREE = 0x1, 0x2, 0x4, 0x8, 0x10
 STEP_EARLY_CACHE_READ = 0x1
 KERNEL_AUTO, KERNEL_CUDA_CORES, KERNEL_TENSOR_CORES = 0, 1, 2
 KERNEL_TENSOR_CORES_K_F16, KERNEL_TENSOR_CORES_K_F16_PRODUCER, KERNEL_WARP_MMA = 3, 4, 5
@@ -516,6 +516,97 @@ def fp8kv_chunk_attention(q: torch.Tensor, cache: Fp8KVCache, cu_q: Optional[tor
     return out
 
 
+def fp8kv_tree_tables(parents: torch.Tensor, cu_new: torch.Tensor, seq_lens: torch.Tensor, max_nodes: int,
+                      masks: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None, stream=None):
+    """Masks and positions of trees of drafted tokens: parents [n] int32 (of
+    row cu_new[b] + i: index of node i's parent within its tree, -1: none),
+    cu_new [B + 1], seq_lens [B] int32 (nodes counted).  max_nodes: nodes that a
+    row of bits has room for.  Returns masks [n, ceil(max_nodes / 32)] int32 (bit
+    i: node i, the node itself or an ancestor) and pos [n] int32 (context length +
+    depth); rows of no tree get no bits and -1."""
+    n, B, words, dev, i32 = parents.numel(), seq_lens.numel(), (int(max_nodes) + 31) // 32, torch.cuda.current_device(), torch.int32
+    if masks is None or pos is None:
+        with _on(stream):
+            masks = torch.empty((n, words), dtype=i32, device=parents.device) if masks is None else masks
+            pos = torch.empty(n, dtype=i32, device=parents.device) if pos is None else pos
+    _check(get_lib().fp8kv_tree_tables(
+        _here(parents, i32, "parents", dev, (n,)), _here(cu_new, i32, "cu_new", dev, (B + 1,)), _here(seq_lens, i32, "seq_lens", dev, (B,)),
+        B, n, words, _here(masks, i32, "masks", dev, (n, words)), _here(pos, i32, "pos", dev, (n,)), _raw_stream(stream, dev)),
+        "fp8kv_tree_tables")
+    return masks, pos
+
+
+def fp8kv_tree_workspace_bytes(cache: Fp8KVCache, total_q: int, q_heads: int, window: int = 0, sinks: int = 0,
+                               num_splits: int = 0, kernel=0) -> int:
+    return int(get_lib().fp8kv_tree_workspace_bytes(cache.struct_ref, total_q, q_heads, window, sinks, num_splits,
+                                                    _kernel(kernel)))
+
+
+def fp8kv_tree_attention(q: torch.Tensor, cache: Fp8KVCache, cu_q: torch.Tensor, seq_lens: torch.Tensor, masks: torch.Tensor,
+                         pos: Optional[torch.Tensor] = None, sm_scale: Optional[float] = None, window: int = 0, sinks: int = 0,
+                         num_splits: int = 0, out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                         workspace: Optional[torch.Tensor] = None, kernel="auto", stream=None):
+    """Attention of trees of drafted tokens: q [total_q, Hq, D] bf16, sequence
+    b's nodes in rows cu_q[b]..cu_q[b+1]-1 and in the cache as its last tokens.
+    A node sees the context, the nodes of its row of masks [total_q, words] int32
+    (fp8kv_tree_tables) and itself; window > 0: of the context the tokens above
+    pos - window and the first `sinks` (pos [total_q] int32, needed then).  The
+    rest as in fp8kv_chunk_attention."""
+    total_q, Hq, D = q.shape
+    if D != cache.head_dim:
+        raise ValueError(f"q: head dim {D}, but the cache's is {cache.head_dim}")
+    if masks.dim() != 2:
+        raise ValueError(f"masks: expected [total_q, words], got {tuple(masks.shape)}")
+    dev, i32 = _current(cache), torch.int32
+    k = _kernel(kernel)
+    if out is None or workspace is None:
+        with _on(stream):
+            if out is None:
+                out = torch.empty((total_q, Hq, D), dtype=out_dtype, device=q.device)
+            if workspace is None:
+                need = fp8kv_tree_workspace_bytes(cache, total_q, Hq, window, sinks, num_splits, k)
+                workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    odt, words = out.dtype, masks.shape[1]
+    if odt is not torch.bfloat16 and odt is not torch.float32:
+        raise ValueError(f"out: expected bf16 or fp32, got {odt}")
+    _check(get_lib().fp8kv_tree_attention(
+        _here(q, torch.bfloat16, "q", dev), cache.struct_ref, _here(cu_q, i32, "cu_q", dev, (cache.batch + 1,)),
+        _here(seq_lens, i32, "seq_lens", dev, (cache.batch,)), _here(masks, i32, "masks", dev, (total_q, words)), words,
+        None if pos is None else _here(pos, i32, "pos", dev, (total_q,)), total_q, Hq,
+        1.0 / math.sqrt(D) if sm_scale is None else sm_scale, window, sinks, num_splits, k,
+        _here(workspace, torch.uint8, "workspace", dev), workspace.numel(), _here(out, odt, "out", dev, (total_q, Hq, D)),
+        OUT_F32 if odt is torch.float32 else OUT_BF16, _raw_stream(stream, dev)), "fp8kv_tree_attention")
+    return out
+
+
+def fp8kv_tree_accept(caches, parents: torch.Tensor, tokens: torch.Tensor, choices: torch.Tensor, cu_new: torch.Tensor,
+                      seq_lens: torch.Tensor, max_path: int, path=None, accepted=None, next_tokens=None, new_lens=None,
+                      stream=None):
+    """The accepted nodes of every tree, and their rows moved behind the context
+    in every cache of `caches` (a list: the layers; may be empty).  parents [n],
+    cu_new [B + 1], seq_lens [B] int32 as in fp8kv_tree_tables; tokens, choices [n]
+    int64: drafted token of a node, the model's choice behind it.  Returns a dict
+    of path [B, max_path] int32 (-1 behind the last), accepted [B] int32,
+    next_tokens [B] int64 and lens [B] int32 (cached_lens of the next step)."""
+    n, B, M, dev, i32, i64 = parents.numel(), seq_lens.numel(), int(max_path), torch.cuda.current_device(), torch.int32, torch.int64
+    caches = list(caches)
+    for c in caches:
+        _current(c)
+    if path is None or accepted is None or next_tokens is None or new_lens is None:
+        with _on(stream):
+            def new(t, shape, dtype=torch.int32):
+                return torch.empty(shape, dtype=dtype, device=parents.device) if t is None else t
+            path, accepted, next_tokens, new_lens = new(path, (B, M)), new(accepted, B), new(next_tokens, B, i64), new(new_lens, B)
+    refs = (ctypes.POINTER(CacheStruct) * len(caches))(*[ctypes.pointer(c._struct) for c in caches])
+    _check(get_lib().fp8kv_tree_accept(
+        refs, len(caches), _here(parents, i32, "parents", dev, (n,)), _here(tokens, i64, "tokens", dev, (n,)),
+        _here(choices, i64, "choices", dev, (n,)), _here(cu_new, i32, "cu_new", dev, (B + 1,)), _here(seq_lens, i32, "seq_lens", dev, (B,)),
+        B, n, M, _here(path, i32, "path", dev, (B, M)), _here(accepted, i32, "accepted", dev, (B,)),
+        _here(next_tokens, i64, "next_tokens", dev, (B,)), _here(new_lens, i32, "new_lens", dev, (B,)), _raw_stream(stream, dev)),
+        "fp8kv_tree_accept")
+    return {"path": path, "accepted": accepted, "next_tokens": next_tokens, "lens": new_lens}
+
+
 def fp8kv_get_device_error(clear: bool = True) -> int:
     """Synchronise the device and return (optionally clearing) the device
     error word (bits DEVERR_*)."""
@@ -536,5 +627,6 @@ __all__ = ["Fp8KVCache", "Fp8KVError", "fp8kv_quantize", "fp8kv_quantize_mx", "f
            "fp8kv_decode_step_workspace_bytes",
            "fp8kv_prefill_attention", "fp8kv_build_tables", "fp8kv_rope_tables", "fp8kv_rope_append",
            "fp8kv_chunk_num_splits", "fp8kv_chunk_workspace_bytes", "fp8kv_chunk_attention",
+           "fp8kv_tree_tables", "fp8kv_tree_workspace_bytes", "fp8kv_tree_attention", "fp8kv_tree_accept",
            "fp8kv_get_device_error", "fp8kv_status_string",
            "EXPORTS", "K8V8", "K16V8", "K16V16", "K8V16", "MXK8V8"]

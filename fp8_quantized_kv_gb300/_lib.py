@@ -30,6 +30,10 @@ EXPORTS = (
     "fp8kv_chunk_num_splits",
     "fp8kv_chunk_workspace_bytes",
     "fp8kv_chunk_attention",
+    "fp8kv_tree_tables",
+    "fp8kv_tree_workspace_bytes",
+    "fp8kv_tree_attention",
+    "fp8kv_tree_accept",
     "fp8kv_get_device_error",
     "fp8kv_status_string",
 )
@@ -94,6 +98,10 @@ def get_lib() -> ctypes.CDLL:
         "fp8kv_chunk_num_splits": (i32, [cp, i64, i32, i32, i32, i32, i32]),
         "fp8kv_chunk_workspace_bytes": (sz, [cp, i64, i32, i32, i32, i32, i32]),
         "fp8kv_chunk_attention": (i32, [vp, cp, vp, vp, i64, i32, f32, i32, i32, i32, i32, vp, sz, vp, i32, vp]),
+        "fp8kv_tree_tables": (i32, [vp, vp, vp, i32, i64, i32, vp, vp, vp]),
+        "fp8kv_tree_workspace_bytes": (sz, [cp, i64, i32, i32, i32, i32, i32]),
+        "fp8kv_tree_attention": (i32, [vp, cp, vp, vp, vp, i32, vp, i64, i32, f32, i32, i32, i32, i32, vp, sz, vp, i32, vp]),
+        "fp8kv_tree_accept": (i32, [vp, i32, vp, vp, vp, vp, vp, i32, i64, i32, vp, vp, vp, vp, vp]),
         "fp8kv_get_device_error": (i32, [ctypes.POINTER(ctypes.c_uint32), i32]),
         "fp8kv_status_string": (ctypes.c_char_p, [i32]),
     }

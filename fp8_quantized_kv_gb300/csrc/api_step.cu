@@ -1,6 +1,7 @@
 // api_step.cu -- the extern "C" boundary of the serving-step calls: argument
 // checks, launch plans, status codes.  As in api.cu, every entry validates on
 // the host, launches on the caller's stream and allocates nothing.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -10,16 +11,6 @@
 using namespace fp8kv;
 
 namespace {
-
-struct Range { const void* p; size_t bytes; };
-
-bool overlap(const Range& a, const Range& b) {
-  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
-  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
-  return x < y + b.bytes && y < x + a.bytes;
-}
-
-bool misaligned(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; }
 
 // Positions are 32-bit: a page table row may not hold more tokens.
 bool capacity_fits(const fp8kv_cache* c) {
@@ -118,6 +109,78 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   if (want > 4096) want = 4096;
   plan->splits = want < 1 ? 1 : (int)want;
   return FP8KV_OK;
+}
+
+// The chunk and the tree call: causal without masks (null), else over trees.
+struct TreeArgs { const uint32_t* masks; const int32_t* pos; int32_t words; };
+
+fp8kv_status run_chunk(const void* q, const fp8kv_cache* cache, const int32_t* cu_q, const int32_t* seq_lens,
+                       const TreeArgs* tree, int64_t total_q, int32_t q_heads, float sm_scale, int32_t window,
+                       int32_t sinks, int32_t num_splits, int32_t kernel, void* workspace, size_t workspace_bytes,
+                       void* out, int32_t out_dtype, fp8kv_stream_t stream) {
+  ChunkParams p;
+  fp8kv_status st = check_cache(cache, &p.c);
+  if (st != FP8KV_OK) return st;
+  ChunkPlan plan;
+  st = plan_chunk(cache, total_q, q_heads, window, sinks, num_splits, kernel, &plan);
+  if (st != FP8KV_OK) return st;
+  if (out_dtype != FP8KV_OUT_BF16 && out_dtype != FP8KV_OUT_F32) return FP8KV_ERR_INVALID_ARG;
+  if (!std::isfinite(sm_scale)) return FP8KV_ERR_INVALID_ARG;
+  if (cu_q == nullptr && (tree != nullptr || total_q != cache->batch)) return FP8KV_ERR_INVALID_ARG;
+  if (tree != nullptr) {
+    if (tree->words < 1) return FP8KV_ERR_INVALID_ARG;
+    if (tree->words > kTreeMaxNodes / 32) return FP8KV_ERR_UNSUPPORTED;
+  }
+  if (cache->batch == 0 || total_q == 0) return FP8KV_OK;
+  if (!q || !seq_lens || !out || misaligned(q, 16) || misaligned(out, 16)) return FP8KV_ERR_INVALID_ARG;
+  if (misaligned(cu_q, 4) || misaligned(seq_lens, 4)) return FP8KV_ERR_INVALID_ARG;
+  const int64_t rows = total_q * q_heads;
+  const size_t values = (size_t)rows * cache->head_dim;
+  if (overlap({q, 2 * values}, {out, (out_dtype == FP8KV_OUT_F32 ? 4 : 2) * values})) return FP8KV_ERR_INVALID_ARG;
+  const size_t need = fp8kv_chunk_workspace_bytes(cache, total_q, q_heads, window, sinks, num_splits, kernel);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FP8KV_ERR_WORKSPACE;
+  if (need > 0 && misaligned(workspace, 16)) return FP8KV_ERR_INVALID_ARG;
+  const Range result = {out, (out_dtype == FP8KV_OUT_F32 ? 4 : 2) * values};
+  for (const Range& r : {Range{q, 2 * values}, result})
+    if (overlap(r, {workspace, need})) return FP8KV_ERR_INVALID_ARG;
+  p.window = window < capacity_of(cache) ? window : 0;
+  p.masks = nullptr;
+  p.tree_pos = nullptr;
+  p.mask_words = 0;
+  if (tree != nullptr) {
+    if (!tree->masks || misaligned(tree->masks, 4) || misaligned(tree->pos, 4)) return FP8KV_ERR_INVALID_ARG;
+    if (p.window > 0 && !tree->pos) return FP8KV_ERR_INVALID_ARG;
+    for (const Range& r : {Range{tree->masks, 4 * (size_t)total_q * tree->words}, Range{tree->pos, 4 * (size_t)total_q}})
+      if (overlap(r, result) || overlap(r, {workspace, need})) return FP8KV_ERR_INVALID_ARG;
+    p.masks = tree->masks;
+    p.tree_pos = tree->pos;
+    p.mask_words = tree->words;
+  }
+  p.err = device_error_ptr();
+  if (!p.err) return FP8KV_ERR_CUDA;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.cu_q = cu_q;
+  p.seq_lens = seq_lens;
+  p.out = out;
+  p.part_o = plan.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  p.part_m = plan.splits > 1 ? p.part_o + rows * plan.splits * cache->head_dim : nullptr;
+  p.part_l = plan.splits > 1 ? p.part_m + rows * plan.splits : nullptr;
+  p.total_q = (int)total_q;
+  p.q_heads = q_heads;
+  p.group = q_heads / cache->kv_heads;
+  p.out_f32 = out_dtype == FP8KV_OUT_F32;
+  p.sinks = sinks;
+  p.num_splits = plan.splits;
+  p.tile_tokens = plan.tile_tokens;
+  p.scale_log2 = sm_scale * kLog2e;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int tiles = cu_q ? plan.tiles : cache->batch;
+  auto* launch = plan.kernel == FP8KV_KERNEL_TENSOR_CORES ? (tree ? launch_tree_tc : launch_chunk_tc)
+                 : plan.tile_rows <= 16 ? (tree ? launch_tree_rows : launch_chunk_rows)
+                                        : (tree ? launch_tree_mma : launch_chunk_mma);
+  cudaError_t e = launch(p, cache->dtype, tiles, s);
+  if (e == cudaSuccess && plan.splits > 1) e = launch_chunk_merge(p, s);
+  return cuda_status(e);
 }
 
 }  // namespace
@@ -273,51 +336,146 @@ fp8kv_status fp8kv_chunk_attention(const void* q, const fp8kv_cache* cache, cons
                                    int32_t window, int32_t sinks, int32_t num_splits, int32_t kernel,
                                    void* workspace, size_t workspace_bytes, void* out, int32_t out_dtype,
                                    fp8kv_stream_t stream) {
-  ChunkParams p;
-  fp8kv_status st = check_cache(cache, &p.c);
-  if (st != FP8KV_OK) return st;
-  ChunkPlan plan;
-  st = plan_chunk(cache, total_q, q_heads, window, sinks, num_splits, kernel, &plan);
-  if (st != FP8KV_OK) return st;
-  if (out_dtype != FP8KV_OUT_BF16 && out_dtype != FP8KV_OUT_F32) return FP8KV_ERR_INVALID_ARG;
-  if (!std::isfinite(sm_scale)) return FP8KV_ERR_INVALID_ARG;
-  if (cu_q == nullptr && total_q != cache->batch) return FP8KV_ERR_INVALID_ARG;
-  if (cache->batch == 0 || total_q == 0) return FP8KV_OK;
-  if (!q || !seq_lens || !out || misaligned(q, 16) || misaligned(out, 16)) return FP8KV_ERR_INVALID_ARG;
-  if (misaligned(cu_q, 4) || misaligned(seq_lens, 4)) return FP8KV_ERR_INVALID_ARG;
-  const int64_t rows = total_q * q_heads;
-  const size_t values = (size_t)rows * cache->head_dim;
-  if (overlap({q, 2 * values}, {out, (out_dtype == FP8KV_OUT_F32 ? 4 : 2) * values})) return FP8KV_ERR_INVALID_ARG;
-  const size_t need = fp8kv_chunk_workspace_bytes(cache, total_q, q_heads, window, sinks, num_splits, kernel);
-  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FP8KV_ERR_WORKSPACE;
-  if (need > 0 && misaligned(workspace, 16)) return FP8KV_ERR_INVALID_ARG;
-  for (const Range& r : {Range{q, 2 * values}, Range{out, (out_dtype == FP8KV_OUT_F32 ? 4 : 2) * values}})
-    if (overlap(r, {workspace, need})) return FP8KV_ERR_INVALID_ARG;
+  return run_chunk(q, cache, cu_q, seq_lens, nullptr, total_q, q_heads, sm_scale, window, sinks, num_splits, kernel,
+                   workspace, workspace_bytes, out, out_dtype, stream);
+}
+
+size_t fp8kv_tree_workspace_bytes(const fp8kv_cache* cache, int64_t total_q, int32_t q_heads, int32_t window,
+                                  int32_t sinks, int32_t num_splits, int32_t kernel) {
+  return fp8kv_chunk_workspace_bytes(cache, total_q, q_heads, window, sinks, num_splits, kernel);
+}
+
+fp8kv_status fp8kv_tree_attention(const void* q, const fp8kv_cache* cache, const int32_t* cu_q,
+                                  const int32_t* seq_lens, const uint32_t* masks, int32_t mask_words,
+                                  const int32_t* pos, int64_t total_q, int32_t q_heads, float sm_scale, int32_t window,
+                                  int32_t sinks, int32_t num_splits, int32_t kernel, void* workspace,
+                                  size_t workspace_bytes, void* out, int32_t out_dtype, fp8kv_stream_t stream) {
+  const TreeArgs tree = {masks, pos, mask_words};
+  return run_chunk(q, cache, cu_q, seq_lens, &tree, total_q, q_heads, sm_scale, window, sinks, num_splits, kernel,
+                   workspace, workspace_bytes, out, out_dtype, stream);
+}
+
+fp8kv_status fp8kv_tree_tables(const int32_t* parents, const int32_t* cu_new, const int32_t* seq_lens, int32_t batch,
+                               int64_t n_rows, int32_t mask_words, uint32_t* masks, int32_t* pos,
+                               fp8kv_stream_t stream) {
+  if (batch < 0 || n_rows < 0 || mask_words < 1 || !cu_new) return FP8KV_ERR_INVALID_ARG;
+  if (mask_words > kTreeMaxNodes / 32 || n_rows > INT32_MAX || batch > INT32_MAX - 64) return FP8KV_ERR_UNSUPPORTED;
+  if (batch > 0 && !seq_lens) return FP8KV_ERR_INVALID_ARG;
+  if (n_rows == 0) return FP8KV_OK;
+  if (!parents || !masks || !pos) return FP8KV_ERR_INVALID_ARG;
+  const size_t N = (size_t)n_rows, B = (size_t)batch;
+  const Range in[] = {{parents, 4 * N}, {cu_new, 4 * (B + 1)}, {seq_lens, 4 * B}};
+  const Range out[] = {{masks, 4 * N * mask_words}, {pos, 4 * N}};
+  for (const Range& o : out) {
+    if (misaligned(o.p, 4)) return FP8KV_ERR_INVALID_ARG;
+    for (const Range& r : in)
+      if (misaligned(r.p, 4) || overlap(r, o)) return FP8KV_ERR_INVALID_ARG;
+  }
+  if (overlap(out[0], out[1])) return FP8KV_ERR_INVALID_ARG;
+  TreeTablesParams p;
   p.err = device_error_ptr();
   if (!p.err) return FP8KV_ERR_CUDA;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.cu_q = cu_q;
+  p.parents = parents;
+  p.cu = cu_new;
   p.seq_lens = seq_lens;
-  p.out = out;
-  p.part_o = plan.splits > 1 ? static_cast<float*>(workspace) : nullptr;
-  p.part_m = plan.splits > 1 ? p.part_o + rows * plan.splits * cache->head_dim : nullptr;
-  p.part_l = plan.splits > 1 ? p.part_m + rows * plan.splits : nullptr;
-  p.total_q = (int)total_q;
-  p.q_heads = q_heads;
-  p.group = q_heads / cache->kv_heads;
-  p.out_f32 = out_dtype == FP8KV_OUT_F32;
-  p.window = window < capacity_of(cache) ? window : 0;
-  p.sinks = sinks;
-  p.num_splits = plan.splits;
-  p.tile_tokens = plan.tile_tokens;
-  p.scale_log2 = sm_scale * kLog2e;
-  cudaStream_t s = (cudaStream_t)stream;
-  const int tiles = cu_q ? plan.tiles : cache->batch;
-  cudaError_t e = plan.kernel == FP8KV_KERNEL_TENSOR_CORES ? launch_chunk_tc(p, cache->dtype, tiles, s)
-                  : plan.tile_rows <= 16 ? launch_chunk_rows(p, cache->dtype, tiles, s)
-                                        : launch_chunk_mma(p, cache->dtype, tiles, s);
-  if (e == cudaSuccess && plan.splits > 1) e = launch_chunk_merge(p, s);
-  return cuda_status(e);
+  p.masks = masks;
+  p.pos = pos;
+  p.batch = batch;
+  p.rows = (int)n_rows;
+  p.words = mask_words;
+  return cuda_status(launch_tree_tables(p, (cudaStream_t)stream));
+}
+
+fp8kv_status fp8kv_tree_accept(const fp8kv_cache* const* caches, int32_t num_caches, const int32_t* parents,
+                               const int64_t* tokens, const int64_t* choices, const int32_t* cu_new,
+                               const int32_t* seq_lens, int32_t batch, int64_t n_rows, int32_t max_path, int32_t* path,
+                               int32_t* accepted, int64_t* next_tokens, int32_t* new_lens, fp8kv_stream_t stream) {
+  if (num_caches < 0 || batch < 0 || n_rows < 0 || max_path < 1 || (num_caches > 0 && !caches))
+    return FP8KV_ERR_INVALID_ARG;
+  if (num_caches > kTreeMostCaches || n_rows > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
+  TreeAcceptParams p;
+  const size_t N = (size_t)n_rows, B = (size_t)batch;
+  const Range out[] = {{path, 4 * B * max_path}, {accepted, 4 * B}, {next_tokens, 8 * B}, {new_lens, 4 * B}};
+  const Range in[] = {{parents, 4 * N}, {tokens, 8 * N}, {choices, 8 * N}, {cu_new, 4 * (B + 1)}, {seq_lens, 4 * B}};
+  // what the call moves rows of: no cache twice, none that shares memory with another, or with the other arguments
+  Range held[4 * kTreeMostCaches];
+  int n_held = 0;
+  const fp8kv_cache* c0 = nullptr;
+  for (int i = 0; i < num_caches; ++i) {
+    const fp8kv_cache* c = caches[i];
+    CacheView view;
+    const fp8kv_status st = check_cache(c, &view);
+    if (st != FP8KV_OK) return st;
+    if (!capacity_fits(c)) return FP8KV_ERR_UNSUPPORTED;
+    if (i == 0) c0 = c;
+    if (c->batch != batch || c->dtype != c0->dtype || c->layout != c0->layout || c->kv_heads != c0->kv_heads ||
+        c->head_dim != c0->head_dim || c->page_size != c0->page_size)
+      return FP8KV_ERR_INVALID_ARG;
+    const size_t rows = (size_t)c->kv_heads * (view.paged ? (size_t)c->num_pages * c->page_size : B * c->max_tokens);
+    held[n_held++] = {c->k, rows * c->head_dim * (c->k_scale ? 1 : 2)};
+    held[n_held++] = {c->v, rows * c->head_dim * (c->v_scale ? 1 : 2)};
+    if (c->k_scale) held[n_held++] = {c->k_scale, 4 * rows};
+    if (c->v_scale) held[n_held++] = {c->v_scale, 4 * rows};
+    const Range table = {view.page_table, 4 * B * (size_t)view.max_pages_per_seq};
+    for (const Range& o : out)
+      if (overlap(o, table)) return FP8KV_ERR_INVALID_ARG;
+  }
+  if (batch == 0) return FP8KV_OK;
+  if (!cu_new || !seq_lens || !path || !accepted || !next_tokens || !new_lens) return FP8KV_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!parents || !tokens || !choices)) return FP8KV_ERR_INVALID_ARG;
+  for (int i = 0; i < 4; ++i) {
+    if (misaligned(out[i].p, i == 2 ? 8 : 4)) return FP8KV_ERR_INVALID_ARG;
+    for (const Range& r : in)
+      if (overlap(r, out[i])) return FP8KV_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[j], out[i])) return FP8KV_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < 5; ++i)
+    if (misaligned(in[i].p, i == 1 || i == 2 ? 8 : 4)) return FP8KV_ERR_INVALID_ARG;
+  // in the order of their addresses only neighbours can overlap
+  std::sort(held, held + n_held, [](const Range& a, const Range& b) { return (uintptr_t)a.p < (uintptr_t)b.p; });
+  for (int i = 0; i < n_held; ++i) {
+    if (i > 0 && overlap(held[i - 1], held[i])) return FP8KV_ERR_INVALID_ARG;
+    for (const Range& o : out)
+      if (overlap(o, held[i])) return FP8KV_ERR_INVALID_ARG;
+  }
+  p.err = device_error_ptr();
+  if (!p.err) return FP8KV_ERR_CUDA;
+  p.parents = parents;
+  p.cu = cu_new;
+  p.seq_lens = seq_lens;
+  p.tokens = tokens;
+  p.choices = choices;
+  p.path = path;
+  p.accepted = accepted;
+  p.new_lens = new_lens;
+  p.next = next_tokens;
+  p.batch = batch;
+  p.rows = (int)n_rows;
+  p.max_path = max_path;
+  p.kv_heads = p.k_bytes = p.v_bytes = p.page_shift = p.paged = 0;
+  if (c0 != nullptr) {
+    p.kv_heads = c0->kv_heads;
+    p.k_bytes = c0->head_dim * (c0->k_scale ? 1 : 2);
+    p.v_bytes = c0->head_dim * (c0->v_scale ? 1 : 2);
+    p.paged = c0->layout == FP8KV_LAYOUT_PAGED;
+    while (p.paged && (1 << p.page_shift) < c0->page_size) ++p.page_shift;
+  }
+  int at = 0;
+  do {
+    p.first = at == 0;
+    p.layers = num_caches - at < kTreeMaxLayers ? num_caches - at : kTreeMaxLayers;
+    for (int i = 0; i < p.layers; ++i) {
+      const fp8kv_cache* c = caches[at + i];
+      p.layer[i] = {static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), reinterpret_cast<uint32_t*>(c->k_scale),
+                    reinterpret_cast<uint32_t*>(c->v_scale), c->page_table, c->num_pages, c->max_pages_per_seq,
+                    c->max_tokens};
+    }
+    const cudaError_t e = launch_tree_accept(p, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_status(e);
+    at += p.layers;
+  } while (at < num_caches);
+  return FP8KV_OK;
 }
 
 }  // extern "C"

@@ -8,6 +8,14 @@
 // that the heads of a group share the K and V tiles they read.  Query
 // position p sees key j if j <= p and, under a window W, j > p - W or
 // j < sinks.
+//
+// Trees (the kernels' TREE forms): the new tokens of a sequence are the nodes of a
+// tree, in the cache behind its ctx = seq_lens[b] - nodes cached tokens, node i
+// as key ctx + i.  Node i sees the cached tokens (under a window those with
+// j > pos - W or j < sinks, pos its position in the text, ctx + its depth), the
+// nodes of its row of bits, and itself.  So every KV tile that holds a node, or
+// whose first keys some node's window misses, is seen in part, and the bits are
+// looked up there alone: the context's tiles run as in the causal form.
 #pragma once
 
 #include "params.cuh"
@@ -28,6 +36,7 @@ struct ChunkTile {
   int n_sink;      // KV tiles that hold first tokens, before the window's
   int first;       // first KV tile of the window
   int n;           // KV tiles in all
+  int ctx;         // trees: tokens before the first node (negative: not all nodes are in the cache)
 };
 
 // KV tiles that `keys` keys (>= 0, up to 2^31 - 16) take.
@@ -99,6 +108,7 @@ static __device__ __noinline__ void chunk_mark_rows(const int32_t* cu_q, float* 
 
 // The CTA's tile.  Returns false for a number that no tile has.  `lead` (the same
 // for the whole CTA): report errors.
+template <bool TREE = false>
 __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lead, ChunkTile& t) {
   const int T = p.tile_tokens;
   int b = x, q0 = x, q1 = x + 1, i0 = 0;           // one query per sequence
@@ -121,7 +131,8 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
   } else {
     len = p.seq_lens[b];
   }
-  if (len < 0 || len > cache_capacity(p.c)) {      // reported; the sequence's queries see nothing
+  // reported; the sequence's queries see nothing
+  if (len < 0 || len > cache_capacity(p.c) || (TREE && q1 - q0 > 32 * p.mask_words)) {
     if (lead && threadIdx.x == 0) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
     len = 0;
   }
@@ -130,10 +141,16 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
   t.ntok = min(T, q1 - q0 - i0);
   t.pos0 = len - (q1 - q0) + i0;
   t.kv_end = max(0, t.pos0 + t.ntok);
+  t.ctx = 0;
+  int first_pos = t.pos0;                          // no query's window starts before this position's
+  if constexpr (TREE) {
+    t.ctx = first_pos = len - (q1 - q0);
+    if (t.kv_end > 0) t.kv_end = len;              // bits may name any node
+  }
   t.lo = 0;
   t.n_sink = 0;
   if (p.window > 0) {
-    const long long lo = (long long)t.pos0 - p.window + 1;
+    const long long lo = (long long)first_pos - p.window + 1;
     t.lo = lo > 0 ? (int)lo : 0;
     t.n_sink = min(chunk_tiles(min(p.sinks, t.kv_end)), t.lo / kChunkKeys);
   }
@@ -143,8 +160,12 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
 }
 
 // Whether every query of the tile sees all keys of the KV tile from key0 on.
+// (Trees: a node's position is below the end of its sequence.)
+template <bool TREE = false, int KEYS = kChunkKeys>
 __device__ __forceinline__ bool chunk_all_seen(const ChunkParams& p, const ChunkTile& t, int key0) {
-  const int last = key0 + kChunkKeys - 1;
+  const int last = key0 + KEYS - 1;
+  if constexpr (TREE)
+    return last < t.ctx && (p.window <= 0 || key0 > t.kv_end - 1 - p.window || last < p.sinks);
   return last <= t.pos0 && (p.window <= 0 || key0 > t.pos0 + t.ntok - 1 - p.window || last < p.sinks);
 }
 __device__ __forceinline__ bool chunk_sees(const ChunkParams& p, int pos, int key) {
@@ -161,6 +182,44 @@ __device__ __forceinline__ unsigned long long chunk_seen_mask(const ChunkParams&
   unsigned long long out = lo > 63 ? 0ull : ~0ull << max(lo, 0);
   if (first > 0) out |= ~0ull >> (64 - min(first, 64));
   return out & upto;
+}
+
+// Trees: the 64 keys from key0 on that the node at cache position `own` (-1: no
+// query) sees, as bits.  Its position in the text is taken within its sequence.
+__device__ __forceinline__ unsigned long long tree_seen_mask(const ChunkParams& p, const ChunkTile& t, int own, int key0) {
+  const int live = min(t.kv_end - key0, 64);       // keys in the cache
+  if (own < 0 || live <= 0) return 0;
+  const int64_t row = t.row0 + (own - t.pos0);
+  const int cached = t.ctx - key0;                 // keys before the first node
+  unsigned long long out = 0;
+  if (cached > 0) {
+    out = ~0ull >> (64 - min(cached, 64));
+    if (p.window > 0) {
+      const int pos = max(t.ctx, min(p.tree_pos[row], t.kv_end - 1));
+      const int lo = pos - p.window + 1 - key0, first = p.sinks - key0;
+      unsigned long long in = lo > 63 ? 0ull : ~0ull << max(lo, 0);
+      if (first > 0) in |= ~0ull >> (64 - min(first, 64));
+      out &= in;
+    }
+  }
+  if (cached < 64) {                               // bits -cached .. -cached + 63 of the node's row
+    const uint32_t* bits = p.masks + row * p.mask_words;
+    unsigned long long nodes;
+    if (cached > 0) {
+      nodes = bits[0];
+      if (p.mask_words > 1) nodes |= (unsigned long long)bits[1] << 32;
+      nodes <<= cached;
+    } else {
+      const int w = -cached >> 5, sh = -cached & 31;
+      auto word = [&](int i) { return i < p.mask_words ? bits[i] : 0u; };
+      const uint32_t a = word(w), b = word(w + 1), c = word(w + 2);
+      nodes = __funnelshift_r(a, b, sh) | (unsigned long long)__funnelshift_r(b, c, sh) << 32;
+    }
+    const int self = own - key0;
+    if (self >= 0 && self < 64) nodes |= 1ull << self;
+    out |= nodes & (~0ull >> (64 - live));
+  }
+  return out;
 }
 
 // Cache row of a key of the tile's sequence, or -1: a key that no query of

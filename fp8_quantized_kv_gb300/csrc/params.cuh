@@ -72,6 +72,38 @@ struct RopeAppendParams {
   int q_per, k_per;                 // row passes per warp
 };
 
+// Nodes of one sequence's tree.
+constexpr int kTreeMaxNodes = 1024;
+
+struct TreeTablesParams {
+  const int32_t *parents;           // [rows] parent within the tree, -1: none
+  const int32_t *cu, *seq_lens;     // [B + 1], [B]
+  uint32_t* masks;                  // [rows][words]
+  int32_t* pos;                     // [rows]
+  unsigned int* err;
+  int batch, rows, words;
+};
+
+// What the accepted rows of one layer's cache are moved in.
+struct TreeLayer {
+  uint8_t *k, *v;
+  uint32_t *k_scale, *v_scale;      // 4-byte scale slots (null: a bf16 side)
+  const int32_t* page_table;
+  int num_pages, max_pages, max_tokens;
+};
+constexpr int kTreeMaxLayers = 60;    // of one launch (4 KB of arguments)
+constexpr int kTreeMostCaches = 512;  // of one call
+struct TreeAcceptParams {
+  TreeLayer layer[kTreeMaxLayers];
+  const int32_t *parents, *cu, *seq_lens;
+  const int64_t *tokens, *choices;  // [rows] drafted token of a node, the model's choice behind it
+  int32_t *path, *accepted, *new_lens;
+  int64_t* next;
+  unsigned int* err;
+  int batch, rows, max_path, layers, first;      // first: the launch that writes the outputs
+  int kv_heads, k_bytes, v_bytes, page_shift, paged;
+};
+
 struct ChunkParams {
   CacheView c;
   const __nv_bfloat16* q;    // [total_q][Hq][D]
@@ -87,6 +119,10 @@ struct ChunkParams {
   int num_splits;            // CTAs that share a tile's keys
   int tile_tokens;           // queries of a sequence per tile
   float scale_log2;          // sm_scale * log2(e)
+  // trees of new tokens (the kernels' TREE forms; zero/null otherwise):
+  const uint32_t* masks;     // [total_q][mask_words] nodes that each node sees
+  const int32_t* tree_pos;   // [total_q] positions in the text (read under a window only)
+  int mask_words;
 };
 
 cudaError_t launch_quantize(const void* x, int64_t rows, int head_dim, uint8_t* codes, float* scales,
@@ -113,10 +149,25 @@ cudaError_t launch_rope_tables(int positions, int pairs, const unsigned long lon
 cudaError_t launch_chunk_mma(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
 cudaError_t launch_chunk_rows(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
+cudaError_t launch_tree_tables(const TreeTablesParams& p, cudaStream_t st);
+cudaError_t launch_tree_accept(const TreeAcceptParams& p, cudaStream_t st);
+cudaError_t launch_tree_mma(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
+cudaError_t launch_tree_rows(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
+cudaError_t launch_tree_tc(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
 cudaError_t launch_chunk_merge(const ChunkParams& p, cudaStream_t st);
 cudaError_t launch_rope_append(RopeAppendParams& p, int dtype, cudaStream_t s);
 
-// Host-side pieces of the C-ABI layer (api.cu).
+// Host-side pieces of the C-ABI layer: argument checks, and (api.cu) per-device values.
+struct Range { const void* p; size_t bytes; };
+
+inline bool overlap(const Range& a, const Range& b) {
+  if (a.p == nullptr || b.p == nullptr || a.bytes == 0 || b.bytes == 0) return false;
+  const uintptr_t x = (uintptr_t)a.p, y = (uintptr_t)b.p;
+  return x < y + b.bytes && y < x + a.bytes;
+}
+
+inline bool misaligned(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) != 0; }
+
 unsigned int* device_error_ptr();
 int sm_count();
 fp8kv_status check_cache(const fp8kv_cache* c, CacheView* view);

@@ -131,6 +131,7 @@ typedef enum {
 #define FP8KV_DEVERR_BAD_PAGE 0x2u       /* a page id outside [0, num_pages)    */
 #define FP8KV_DEVERR_TIMEOUT 0x4u        /* a bounded mbarrier wait ran out    */
 #define FP8KV_DEVERR_NO_PAGES 0x8u       /* a step needs more pages than are free */
+#define FP8KV_DEVERR_BAD_TREE 0x10u      /* a parent that does not come before its node */
 
 /* A KV cache.  The struct is read on the host at every call (pass it by
  * pointer; it may live on the stack).  All pointers are device pointers owned
@@ -507,6 +508,102 @@ FP8KV_API int32_t fp8kv_chunk_num_splits(const fp8kv_cache *cache, int64_t total
 FP8KV_API size_t fp8kv_chunk_workspace_bytes(const fp8kv_cache *cache, int64_t total_q, int32_t q_heads,
                                              int32_t window, int32_t sinks, int32_t num_splits,
                                              int32_t kernel);
+
+/* A step that verifies trees of drafted tokens.  The new tokens of a sequence
+ * are the nodes of a tree: node 0 is the token that follows the context (the
+ * last one that the model chose, not yet in the cache), every other node hangs
+ * under one before it.  With n nodes and L = seq_lens[b] tokens in the cache, the
+ * nodes' among them, the context is the first ctx = L - n, and node i is cached as
+ * token ctx + i (fp8kv_build_tables gives its slot) but stands at position
+ * ctx + depth of the text.  The calls of a step:
+ *   fp8kv_build_tables -> fp8kv_tree_tables -> per layer: fp8kv_rope_append with
+ *   the positions of fp8kv_tree_tables, fp8kv_tree_attention -> the model's choice
+ *   at every node -> fp8kv_tree_accept.
+ * A tree has at most 1024 nodes. */
+
+/* The nodes that each node sees, as bits, and its position, from the parents.
+ *   parents:    [n_rows] int32, for row cu_new[b] + i the index (below i) of node
+ *               i's parent within the tree; -1: none, depth 0 (node 0)
+ *   cu_new:     [batch + 1] int32, first row of each tree, not decreasing
+ *   seq_lens:   [batch] int32, tokens of each sequence, its nodes among them
+ *   mask_words: words of a row of bits, 1 to 32 (32 nodes each); more:
+ *               FP8KV_ERR_UNSUPPORTED
+ *   masks:      [n_rows][mask_words]; bit i % 32 of word i / 32 stands for node i:
+ *               the node itself and its ancestors
+ *   pos:        [n_rows] int32, ctx + depth
+ * Rows that belong to no tree (padding) get no bits and position -1, and so do those
+ * of a tree that has more nodes than bits or than its sequence has tokens
+ * (SEQ_TOO_LONG); offsets that decrease or pass n_rows raise it and leave their
+ * rows as they were (where offsets decrease, rows from the last offset on may
+ * count as padding, whoever claims them).  A parent outside [-1, i) counts as none (BAD_TREE).
+ * Outputs may not overlap inputs or each other (FP8KV_ERR_INVALID_ARG). */
+FP8KV_API fp8kv_status fp8kv_tree_tables(const int32_t *parents, const int32_t *cu_new,
+                                         const int32_t *seq_lens, int32_t batch, int64_t n_rows,
+                                         int32_t mask_words, uint32_t *masks, int32_t *pos,
+                                         fp8kv_stream_t stream);
+
+/* Attention of the nodes of trees over the cache, which must hold them already.
+ * Node i of a sequence sees the context (under a window W the tokens
+ * j > pos - W or j < sinks of it), the nodes of its row of masks, and itself,
+ * whether its own bit is set or not.  Bits may name later nodes too; those of
+ * nodes that the tree does not have are not looked at.  Nodes are never hidden by
+ * the window.
+ *   masks, mask_words: as fp8kv_tree_tables writes them
+ *   pos:        [total_q] int32, positions in the text (read under a window only,
+ *               else may be NULL); one outside [ctx, seq_lens[b]) counts as the
+ *               nearest in it
+ * All else as in fp8kv_chunk_attention, whose kernels run it: cu_q (not NULL here),
+ * seq_lens, num_splits, kernel, workspace (fp8kv_tree_workspace_bytes), roundings,
+ * values that are not finite, bad lengths and offsets.  A node whose key ctx + i
+ * would be negative gets a zero row, and so do the nodes of a tree with more of
+ * them than bits (SEQ_TOO_LONG).  Under a window the keys from
+ * ctx - window + 1 on may be read, whatever the nodes' depths. */
+FP8KV_API fp8kv_status fp8kv_tree_attention(const void *q, const fp8kv_cache *cache,
+                                            const int32_t *cu_q, const int32_t *seq_lens,
+                                            const uint32_t *masks, int32_t mask_words,
+                                            const int32_t *pos, int64_t total_q, int32_t q_heads,
+                                            float sm_scale, int32_t window, int32_t sinks,
+                                            int32_t num_splits, int32_t kernel, void *workspace,
+                                            size_t workspace_bytes, void *out, int32_t out_dtype,
+                                            fp8kv_stream_t stream);
+FP8KV_API size_t fp8kv_tree_workspace_bytes(const fp8kv_cache *cache, int64_t total_q, int32_t q_heads,
+                                            int32_t window, int32_t sinks, int32_t num_splits,
+                                            int32_t kernel);
+
+/* The nodes that the model accepts, and what the caches keep of a tree.  Node 0
+ * is accepted; from an accepted node the walk goes on to the child whose drafted
+ * token is the model's choice at that node (the lowest of several), up to
+ * max_path nodes in all.  In every cache given, the rows of the accepted nodes
+ * move to the places behind the context: the node of depth k from token
+ * ctx + path[k] to token ctx + k, codes, values and scales as they are.  The
+ * other nodes' tokens keep what they hold, behind the new length.
+ *   caches:      [num_caches] pointers, the layers' caches (0 to 512; none: only
+ *                the walk).  They agree in batch, layout, types and sizes of a
+ *                row and page, and share no memory (FP8KV_ERR_INVALID_ARG)
+ *   parents, cu_new, seq_lens: as in fp8kv_tree_tables (lengths before the walk)
+ *   tokens:      [n_rows] int64, the drafted token of each node
+ *   choices:     [n_rows] int64, the token that the model chose to follow each
+ *                node: its most likely one, or one sampled (the accepted tokens
+ *                are then distributed as the model's own)
+ *   path:        [batch][max_path] int32, the accepted nodes, -1 behind them
+ *   accepted:    [batch] int32, how many; 0 without nodes
+ *   next_tokens: [batch] int64, the choice at the last accepted node; -1 without
+ *   new_lens:    [batch] int32, ctx + accepted: the cached_lens of the next step
+ * Pages that hold only tokens from new_lens on stay in the page table; the next
+ * fp8kv_build_tables takes fresh pages in their place, so hand them back to the
+ * free list.
+ * A parent outside [-1, i) raises BAD_TREE and its node is not accepted.  A tree
+ * with bad offsets, more than 1024 nodes or more nodes than its sequence has
+ * tokens accepts nothing and keeps its length; one whose length passes a
+ * cache's capacity moves nothing there (SEQ_TOO_LONG).  A row on a bad page does
+ * not move (BAD_PAGE). */
+FP8KV_API fp8kv_status fp8kv_tree_accept(const fp8kv_cache *const *caches, int32_t num_caches,
+                                         const int32_t *parents, const int64_t *tokens,
+                                         const int64_t *choices, const int32_t *cu_new,
+                                         const int32_t *seq_lens, int32_t batch, int64_t n_rows,
+                                         int32_t max_path, int32_t *path, int32_t *accepted,
+                                         int64_t *next_tokens, int32_t *new_lens,
+                                         fp8kv_stream_t stream);
 
 /* Read (and, if `clear` is non-zero, reset) the device error word of the
  * current device.  Synchronous: waits for all work on the device. */

@@ -1,0 +1,96 @@
+"""Refusals of the tree calls, on the host: every call below is turned down by its
+argument checks, before any CUDA call.  No GPU."""
+import ctypes
+
+import pytest
+import torch
+
+import fp8_quantized_kv_gb300 as fk
+from test_step_host import INVALID, UNSUPPORTED, WORKSPACE, _cache, _paged, lib  # noqa: F401
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(batch=-1)), (INVALID, dict(rows=-1)), (INVALID, dict(words=0)), (INVALID, dict(parents=None)), (INVALID, dict(cu=None)),
+    (INVALID, dict(lens=None)), (INVALID, dict(masks=None)), (INVALID, dict(pos=None)), (INVALID, dict(masks=0x10004)),
+    (INVALID, dict(pos=0x11000)), (INVALID, dict(pos=0x12000)), (INVALID, dict(pos=0x13004)), (INVALID, dict(pos=0x14002)),
+    (INVALID, dict(parents=0x10001)), (UNSUPPORTED, dict(words=33)), (UNSUPPORTED, dict(rows=1 << 31)),
+])
+def test_tables_refusals(lib, want, kw):  # noqa: F811
+    a = dict(parents=0x10000, cu=0x11000, lens=0x12000, batch=4, rows=16, words=2, masks=0x13000, pos=0x14000)
+    a.update(kw)
+    assert lib.fp8kv_tree_tables(*a.values(), None) == want
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(total=-1)), (INVALID, dict(q_heads=3)), (INVALID, dict(window=-1)), (INVALID, dict(sinks=-1)),
+    (INVALID, dict(splits=-1)), (INVALID, dict(kernel=1)), (INVALID, dict(kernel=7)), (INVALID, dict(out_dtype=2)),
+    (INVALID, dict(sm=float("inf"))), (INVALID, dict(q=None)), (INVALID, dict(lens=None)), (INVALID, dict(out=None)),
+    (INVALID, dict(cu=None)), (INVALID, dict(masks=None)), (INVALID, dict(words=0)), (INVALID, dict(masks=0x22002)),
+    (INVALID, dict(pos=0x23002)), (INVALID, dict(pos=None, window=16)), (INVALID, dict(masks=0x40000)), (INVALID, dict(pos=0x30000)),
+    (INVALID, dict(out=0x10000)), (INVALID, dict(ws=0x30008)), (WORKSPACE, dict(ws=None)), (WORKSPACE, dict(ws_bytes=100)),
+    (UNSUPPORTED, dict(words=33)), (UNSUPPORTED, dict(q_heads=34)), (UNSUPPORTED, dict(total=1 << 31)), (UNSUPPORTED, dict(splits=5000)),
+])
+def test_attention_refusals(lib, want, kw):  # noqa: F811
+    a = dict(q=0x10000, cu=0x20000, lens=0x21000, masks=0x22000, words=1, pos=0x23000, total=10, q_heads=4, sm=0.1, window=0, sinks=0,
+             splits=2, kernel=0, ws=0x30000, ws_bytes=1 << 30, out=0x40000, out_dtype=0)
+    a.update(kw)
+    v = list(a.values())
+    assert lib.fp8kv_tree_attention(v[0], _paged(), *v[1:], None) == want
+
+
+def test_attention_refusals_by_cache(lib):  # noqa: F811
+    args = (0x20000, 0x21000, 0x22000, 1, 0x23000, 10, 4, 0.1, 0, 0, 0, 0, 0x30000, 1 << 30, 0x40000, 0, None)
+    turning = _cache(k_bias=0x8000, rope_cos=0x9000, rope_sin=0xA000, rope_positions=2048)
+    assert lib.fp8kv_tree_attention(0x10000, turning, *args) == UNSUPPORTED
+    assert lib.fp8kv_tree_attention(0x10000, None, *args) == INVALID
+    assert lib.fp8kv_tree_workspace_bytes(_paged(), 10, 4, 0, 0, 2, 0) == lib.fp8kv_chunk_workspace_bytes(_paged(), 10, 4, 0, 0, 2, 0) > 0
+    assert lib.fp8kv_tree_workspace_bytes(_paged(), 10, 3, 0, 0, 2, 0) == 0
+    # nothing to do
+    assert lib.fp8kv_tree_attention(0x10000, _paged(), *args[:5], 0, *args[6:]) == 0
+
+
+def _accept(lib, caches, n=None, **kw):  # noqa: F811
+    from fp8_quantized_kv_gb300._lib import CacheStruct
+    refs = (ctypes.POINTER(CacheStruct) * max(1, len(caches)))(*[ctypes.pointer(c._obj) for c in caches])
+    a = dict(parents=0x10000, tokens=0x11000, choices=0x12000, cu=0x13000, lens=0x14000, batch=4, rows=16, most=4, path=0x15000,
+             accepted=0x16000, next=0x17000, new_lens=0x18000)
+    a.update(kw)
+    return lib.fp8kv_tree_accept(refs if caches else None, len(caches) if n is None else n, *a.values(), None)
+
+
+@pytest.mark.parametrize("want,kw", [
+    (INVALID, dict(batch=-1)), (INVALID, dict(rows=-1)), (INVALID, dict(most=0)), (INVALID, dict(parents=None)), (INVALID, dict(tokens=None)),
+    (INVALID, dict(choices=None)), (INVALID, dict(cu=None)), (INVALID, dict(lens=None)), (INVALID, dict(path=None)),
+    (INVALID, dict(accepted=None)), (INVALID, dict(next=None)), (INVALID, dict(new_lens=None)), (INVALID, dict(new_lens=0x14000)),
+    (INVALID, dict(path=0x11010)), (INVALID, dict(accepted=0x15004)), (INVALID, dict(next=0x17004)), (INVALID, dict(tokens=0x11004)),
+    (INVALID, dict(lens=0x14001)), (UNSUPPORTED, dict(rows=1 << 31)),
+])
+def test_accept_refusals(lib, want, kw):  # noqa: F811
+    assert _accept(lib, [], **kw) == want
+
+
+def test_accept_refusals_by_caches(lib):  # noqa: F811
+    big = dict(max_tokens=16, k=0x100000, v=0x200000, k_scale=0x300000, v_scale=0x400000)
+    apart = dict(max_tokens=16, k=0x500000, v=0x600000, k_scale=0x700000, v_scale=0x800000)
+    one = _cache(**big)
+    assert _accept(lib, [], n=1) == INVALID and _accept(lib, [], n=-1) == INVALID
+    assert _accept(lib, [one, one]) == INVALID                                             # the same cache twice
+    assert _accept(lib, [one, _cache(**{**apart, "v": 0x100010})]) == INVALID              # shared rows
+    for kw in (dict(batch=5), dict(kv_heads=4), dict(head_dim=64), dict(dtype=3, v_scale=None),
+               dict(layout=1, max_tokens=0, page_size=16, num_pages=4, max_pages_per_seq=2, page_table=0x900000)):
+        assert _accept(lib, [one, _cache(**{**apart, **kw})]) == INVALID
+    assert _accept(lib, [_cache(**{**big, "batch": 5})]) == INVALID
+    assert _accept(lib, [one], path=0x100000) == INVALID                                   # outputs in a cache, in a page table
+    paged = dict(layout=1, max_tokens=0, page_size=16, num_pages=4, max_pages_per_seq=2, page_table=0x18000)
+    assert _accept(lib, [_cache(**{**big, **paged})]) == INVALID
+    assert _accept(lib, [_paged(max_pages_per_seq=1 << 27)]) == UNSUPPORTED
+    assert _accept(lib, [one] * 513) == UNSUPPORTED
+    assert _accept(lib, [], batch=0) == 0
+
+
+def test_binding_refusals():
+    i32 = torch.zeros(4, dtype=torch.int32)
+    if torch.cuda.is_available():
+        pytest.skip("the message differs with a device")
+    with pytest.raises((ValueError, RuntimeError, AssertionError)):
+        fk.fp8kv_tree_tables(i32, i32, i32, 32)
