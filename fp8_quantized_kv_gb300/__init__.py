@@ -607,6 +607,34 @@ def fp8kv_tree_accept(caches, parents: torch.Tensor, tokens: torch.Tensor, choic
     return {"path": path, "accepted": accepted, "next_tokens": next_tokens, "lens": new_lens}
 
 
+def fp8kv_block_matmul(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
+                       bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
+                       stream=None):
+    """Matrix product of e4m3 codes a [M, K] (activations; a_scales
+    [M, ceil(K / 128)] fp32) and b [N, K] (a weight; b_scales
+    [ceil(N / 128), ceil(K / 128)]): out [M, N] = the sum over blocks of 128 of
+    K of both scales times the codes' products, plus bias [N] fp32.  With K a
+    multiple of 128, fp8kv_quantize(x.view(M, K // 128, 128)) makes a and its
+    scales (view the codes as [M, K]).  K a multiple of 16."""
+    f32 = torch.float32
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError(f"a, b: expected [M, K] and [N, K], got {tuple(a.shape)} and {tuple(b.shape)}")
+    M, K = a.shape
+    N, KB, dev = b.shape[0], (K + 127) // 128, torch.cuda.current_device()
+    if out is None:
+        with _on(stream):
+            out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    odt = out.dtype
+    if odt is not torch.bfloat16 and odt is not f32:
+        raise ValueError(f"out: expected bf16 or fp32, got {odt}")
+    _check(get_lib().fp8kv_block_matmul(
+        _here(a, torch.uint8, "a", dev), _here(a_scales, f32, "a_scales", dev, (M, KB)), _here(b, torch.uint8, "b", dev, (N, K)),
+        _here(b_scales, f32, "b_scales", dev, ((N + 127) // 128, KB)), None if bias is None else _here(bias, f32, "bias", dev, (N,)),
+        M, N, K, _here(out, odt, "out", dev, (M, N)), OUT_F32 if odt is f32 else OUT_BF16, _raw_stream(stream, dev)),
+        "fp8kv_block_matmul")
+    return out
+
+
 def fp8kv_get_device_error(clear: bool = True) -> int:
     """Synchronise the device and return (optionally clearing) the device
     error word (bits DEVERR_*)."""
@@ -627,6 +655,6 @@ __all__ = ["Fp8KVCache", "Fp8KVError", "fp8kv_quantize", "fp8kv_quantize_mx", "f
            "fp8kv_decode_step_workspace_bytes",
            "fp8kv_prefill_attention", "fp8kv_build_tables", "fp8kv_rope_tables", "fp8kv_rope_append",
            "fp8kv_chunk_num_splits", "fp8kv_chunk_workspace_bytes", "fp8kv_chunk_attention",
-           "fp8kv_tree_tables", "fp8kv_tree_workspace_bytes", "fp8kv_tree_attention", "fp8kv_tree_accept",
+           "fp8kv_tree_tables", "fp8kv_tree_workspace_bytes", "fp8kv_tree_attention", "fp8kv_tree_accept", "fp8kv_block_matmul",
            "fp8kv_get_device_error", "fp8kv_status_string",
            "EXPORTS", "K8V8", "K16V8", "K16V16", "K8V16", "MXK8V8"]

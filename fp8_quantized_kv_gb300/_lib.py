@@ -34,6 +34,7 @@ EXPORTS = (
     "fp8kv_tree_workspace_bytes",
     "fp8kv_tree_attention",
     "fp8kv_tree_accept",
+    "fp8kv_block_matmul",
     "fp8kv_get_device_error",
     "fp8kv_status_string",
 )
@@ -102,6 +103,7 @@ def get_lib() -> ctypes.CDLL:
         "fp8kv_tree_workspace_bytes": (sz, [cp, i64, i32, i32, i32, i32, i32]),
         "fp8kv_tree_attention": (i32, [vp, cp, vp, vp, vp, i32, vp, i64, i32, f32, i32, i32, i32, i32, vp, sz, vp, i32, vp]),
         "fp8kv_tree_accept": (i32, [vp, i32, vp, vp, vp, vp, vp, i32, i64, i32, vp, vp, vp, vp, vp]),
+        "fp8kv_block_matmul": (i32, [vp, vp, vp, vp, vp, i64, i64, i64, vp, i32, vp]),
         "fp8kv_get_device_error": (i32, [ctypes.POINTER(ctypes.c_uint32), i32]),
         "fp8kv_status_string": (ctypes.c_char_p, [i32]),
     }

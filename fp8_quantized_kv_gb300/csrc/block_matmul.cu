@@ -1,0 +1,476 @@
+// block_matmul.cu -- matrix product of e4m3 codes with an fp32 scale for each block
+// of 128, on the tcgen05 tensor cores:
+//   y[m][n] = sum_j sa[m][j] sb[n / 128][j] sum_{k in block j} a[m][k] b[n][k]  (+ bias[n])
+// a: one scale per row and block of 128 elements of K (activations); b: one per
+// block of 128 x 128 (weights).
+//
+// The scales change with every block of K, so the tensor core sums one block at a
+// time (four kind::f8f6f4 products of 32 elements into a fresh TMEM buffer) and
+// fp32 registers sum the blocks: acc = fma(d, sa sb, acc), one rounding of the pair
+// of scales and one of each sum.  Two buffers, so that the tensor core fills one
+// while the other is read.
+#include "params.cuh"
+#include "tc_common.cuh"
+
+namespace fp8kv {
+
+constexpr int kMmBlock = 128;            // elements of a block of K: one 128-byte swizzled row
+
+struct MatmulParams {
+  CUtensorMap ta, tb;
+  MatmulArgs a;
+  int kb;                                // blocks of K
+  int tiles_m, tiles_n;
+};
+
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// Waits for this thread's TMEM loads; the values are named, so that nothing that
+// uses them moves in front.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
+// ---------------------------------------------------------- many rows of a --
+// A CTA owns tiles of 128 rows of a x BN rows of b, one after the other.
+//   warp 0      TMA producer: ring of a and b blocks
+//   warp 1      TMEM owner and MMA issuer
+//   warps 4-11  sums: a thread keeps one row of the tile and half of its columns
+template <int BN>
+struct MmCfg {
+  static constexpr int STAGE = (128 + BN) * kMmBlock;
+  static constexpr int NS = BN == 256 ? 4 : 6;
+  static constexpr int BYTES = 1024 + NS * STAGE + 256;
+  static constexpr int THREADS = 384;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_rows(const __grid_constant__ MatmulParams p) {
+  using C = MmCfg<BN>;
+  constexpr int HC = BN / 2;                                  // columns of a thread
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::NS * C::STAGE);
+  uint64_t* full = bars;                                      // [NS] blocks landed
+  uint64_t* empty = full + C::NS;                             // [NS] products have read them
+  uint64_t* d_full = empty + C::NS;                           // [2] a block's sums are in TMEM
+  uint64_t* d_free = d_full + 2;                              // [2] read
+  uint64_t* drained = d_free + 2;                             // every product finished
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tiles = p.tiles_m * p.tiles_n;
+  if (tid == 0) {
+    tma::prefetch_map(&p.ta);
+    tma::prefetch_map(&p.tb);
+    for (int i = 0; i < C::NS; ++i) { umma::mbar_init(&full[i], 1); umma::mbar_init(&empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { umma::mbar_init(&d_full[i], 1); umma::mbar_init(&d_free[i], 8); }
+    umma::mbar_init(drained, 1);
+    *abort_flag = 0;
+    umma::mbar_fence_init();
+  }
+  if (warp == 1) {
+    umma::tmem_alloc(tslot, 2 * BN);
+    umma::tmem_relinquish();
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  const uint32_t tmem = *tslot;
+
+  if (warp < 4) {
+    regs_dec<40>();
+    if (warp == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        const int m0 = tile % p.tiles_m * 128, n0 = tile / p.tiles_m * BN;
+        for (int j = 0; j < p.kb; ++j, ++it) {
+          const int s = it % C::NS;
+          if (it >= C::NS) {
+            ok = wait_fast(&empty[s], (it / C::NS - 1) & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          }
+          if (elect_one()) {
+            uint8_t* st = smem + s * C::STAGE;
+            tma::arrive_expect_tx(&full[s], C::STAGE);
+            tma::load_2d(st, &p.ta, j * kMmBlock, m0, &full[s]);
+            tma::load_2d(st + 128 * kMmBlock, &p.tb, j * kMmBlock, n0, &full[s]);
+          }
+          __syncwarp();
+        }
+      }
+      // no copy is in flight when the CTA ends (matters when a wait gave up)
+      if (lane == 0)
+        for (int i = max(0, it - C::NS); i < it; ++i) (void)umma::mbar_wait(&full[i % C::NS], (i / C::NS) & 1, 100000000ull);
+    } else if (warp == 1) {
+      constexpr uint32_t ID = umma::idesc(umma::FMT_E4M3, umma::FMT_E4M3, umma::MAJOR_K, umma::MAJOR_K, 128, BN);
+      int it = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+        for (int j = 0; j < p.kb; ++j, ++it) {
+          const int s = it % C::NS, d = it & 1;
+          ok = wait_fast(&full[s], (it / C::NS) & 1, abort_flag);
+          if (it >= 2) ok = ok && wait_fast(&d_free[d], (it / 2 - 1) & 1, abort_flag);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          umma::fence_after_sync();
+          const uint32_t aa = umma::smem_u32(smem + s * C::STAGE), ba = aa + 128 * kMmBlock;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma::mma_f8_ss(tmem + d * BN, umma::sdesc(aa + 32 * k, 16, 1024, umma::SWIZZLE_128B),
+                              umma::sdesc(ba + 32 * k, 16, 1024, umma::SWIZZLE_128B), ID, k > 0);
+            umma::mma_commit(&empty[s]);
+            umma::mma_commit(&d_full[d]);
+          }
+          __syncwarp();
+        }
+      }
+      // all issued products complete before TMEM is released
+      __syncwarp();
+      if (elect_one()) umma::mma_commit(drained);
+      (void)umma::mbar_wait(drained, 0, 100000000ull);
+    }
+  } else {
+    regs_inc<216>();
+    const int half = (warp - 4) >> 2, row_in = 32 * (warp & 3) + lane;
+    const uint32_t lane_col = ((uint32_t)(32 * (warp & 3)) << 16) + half * HC;
+    int it = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      const int m = tile % p.tiles_m * 128 + row_in, n0 = tile / p.tiles_m * BN + half * HC;
+      const bool live = m < p.a.M && n0 < p.a.N;
+      const float* sa = p.a.sa + (int64_t)(live ? m : 0) * p.kb;
+      const float* sb = p.a.sb + (int64_t)(live ? n0 / 128 : 0) * p.kb;
+      float2 acc[HC / 2];
+#pragma unroll
+      for (int c = 0; c < HC / 2; ++c) acc[c] = make_float2(0.f, 0.f);
+      float next_a = sa[0], next_b = sb[0];
+      for (int j = 0; j < p.kb; ++j, ++it) {
+        const int d = it & 1;
+        const float s = next_a * next_b;
+        if (j + 1 < p.kb) { next_a = sa[j + 1]; next_b = sb[j + 1]; }
+        ok = wait_fast(&d_full[d], (it / 2) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        umma::fence_after_sync();
+        const float2 s2 = make_float2(s, s);
+        uint32_t r[2][32];
+        const uint32_t at = tmem + d * BN + lane_col;
+        tmem_ld32_nowait(at, r[0]);
+#pragma unroll
+        for (int c = 0; c < HC / 32; ++c) {
+          tmem_wait_ld32(r[c & 1]);
+          if (c + 1 < HC / 32) tmem_ld32_nowait(at + 32 * (c + 1), r[(c + 1) & 1]);
+          else {
+            umma::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) umma::mbar_arrive(&d_free[d]);
+          }
+#pragma unroll
+          for (int u = 0; u < 16; ++u)
+            acc[16 * c + u] = __ffma2_rn(make_float2(__uint_as_float(r[c & 1][2 * u]), __uint_as_float(r[c & 1][2 * u + 1])), s2,
+                                         acc[16 * c + u]);
+        }
+      }
+      if (!ok || !live) continue;
+      const int cols = min(HC, p.a.N - n0);
+      if (p.a.bias != nullptr) {
+#pragma unroll
+        for (int c = 0; c < HC / 2; ++c) {
+          if (2 * c < cols) acc[c].x += p.a.bias[n0 + 2 * c];
+          if (2 * c + 1 < cols) acc[c].y += p.a.bias[n0 + 2 * c + 1];
+        }
+      }
+      const int64_t out = (int64_t)m * p.a.N + n0;
+      if (p.a.out_f32) {
+        float* y = reinterpret_cast<float*>(p.a.out) + out;
+        const bool vec = p.a.N % 4 == 0;
+#pragma unroll
+        for (int c = 0; c < HC / 2; c += 2) {
+          if (vec && 2 * c + 4 <= cols) *reinterpret_cast<float4*>(y + 2 * c) = make_float4(acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y);
+          else {
+            const float v[4] = {acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y};
+            for (int u = 0; u < 4; ++u)
+              if (2 * c + u < cols) y[2 * c + u] = v[u];
+          }
+        }
+      } else {
+        __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.a.out) + out;
+        const bool vec = p.a.N % 8 == 0;
+#pragma unroll
+        for (int c = 0; c < HC / 2; c += 4) {
+          __nv_bfloat162 h[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) h[u] = __floats2bfloat162_rn(acc[c + u].x, acc[c + u].y);
+          if (vec && 2 * c + 8 <= cols) *reinterpret_cast<uint4*>(y + 2 * c) = *reinterpret_cast<const uint4*>(h);
+          else {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              if (2 * c + u < cols) y[2 * c + u] = u & 1 ? h[u / 2].y : h[u / 2].x;
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (warp == 1) umma::tmem_dealloc(tmem, 2 * BN);
+}
+
+// ----------------------------------------------------------- few rows of a --
+// The weights' bytes bound it, so they are spread over all SMs: a CTA takes 128
+// rows of b (the tensor core's 128 lanes), up to MT rows of a (its columns), and a
+// share of the blocks of K; the CTAs of a cluster hold the shares of one tile.  Each
+// sums its blocks in registers, sends every column's sums to the CTA that owns the
+// column (distributed shared memory), and the owner adds the shares in rank order.
+template <int MT>
+struct MfCfg {
+  static constexpr int STAGE = (128 + MT) * kMmBlock;
+  static constexpr int NB = 512 / MT < 8 ? 512 / MT : 8;      // TMEM buffers
+  static constexpr int NS = MT == 128 ? 4 : MT == 64 ? 7 : 8;
+  static constexpr int PART = 128 * (MT + 8) * 4;             // shares received (columns rounded up per rank)
+  static constexpr int BYTES = 1024 + NS * STAGE + PART + 2 * MT * 4 + 512;
+  static constexpr int TCOLS = NB * MT < 32 ? 32 : NB * MT;
+  static constexpr int THREADS = 192;
+  static_assert(BYTES <= 227 * 1024, "shared memory of an SM");
+};
+
+template <int MT>
+__global__ void __launch_bounds__(MfCfg<MT>::THREADS, 1) block_matmul_few(const __grid_constant__ MatmulParams p) {
+  using C = MfCfg<MT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* part = reinterpret_cast<float*>(smem + C::NS * C::STAGE);       // [rank][own column][128]
+  float* scol = reinterpret_cast<float*>(smem + C::NS * C::STAGE + C::PART);   // [2][MT] scales of the columns
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scol + 2 * MT);
+  uint64_t* full = bars;
+  uint64_t* empty = full + C::NS;
+  uint64_t* d_full = empty + C::NS;                           // [NB]
+  uint64_t* d_free = d_full + C::NB;                          // [NB]
+  uint64_t* drained = d_free + C::NB;                         // every product finished
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int S, rank;
+  asm("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(S));
+  rank = (int)cluster_rank();
+  const int n0 = blockIdx.x / S * 128, m0 = blockIdx.y * MT;
+  const int j0 = (int)((int64_t)p.kb * rank / S), j1 = (int)((int64_t)p.kb * (rank + 1) / S);
+  if (tid == 0) {
+    tma::prefetch_map(&p.ta);
+    tma::prefetch_map(&p.tb);
+    for (int i = 0; i < C::NS; ++i) { umma::mbar_init(&full[i], 1); umma::mbar_init(&empty[i], 1); }
+    for (int i = 0; i < C::NB; ++i) { umma::mbar_init(&d_full[i], 1); umma::mbar_init(&d_free[i], 4); }
+    umma::mbar_init(drained, 1);
+    *abort_flag = 0;
+    umma::mbar_fence_init();
+  }
+  if (warp == 1) {
+    umma::tmem_alloc(tslot, C::TCOLS);
+    umma::tmem_relinquish();
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  cluster_arrive_relaxed();                                   // every CTA of the cluster runs before it is written to
+  const uint32_t tmem = *tslot;
+  const int per = (MT + S - 1) / S;                           // columns of a rank
+  if (warp == 0) {
+    int j = j0;
+    for (; j < j1; ++j) {
+      const int it = j - j0, s = it % C::NS;
+      if (it >= C::NS) {
+        const bool ok = wait_fast(&empty[s], (it / C::NS - 1) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) break;
+      }
+      if (elect_one()) {
+        uint8_t* st = smem + s * C::STAGE;
+        tma::arrive_expect_tx(&full[s], C::STAGE);
+        tma::load_2d(st, &p.tb, j * kMmBlock, n0, &full[s]);
+        tma::load_2d(st + 128 * kMmBlock, &p.ta, j * kMmBlock, m0, &full[s]);
+      }
+      __syncwarp();
+    }
+    if (lane == 0)
+      for (int i = max(0, j - j0 - C::NS); i < j - j0; ++i) (void)umma::mbar_wait(&full[i % C::NS], (i / C::NS) & 1, 100000000ull);
+    cluster_wait();
+  } else if (warp == 1) {
+    constexpr uint32_t ID = umma::idesc(umma::FMT_E4M3, umma::FMT_E4M3, umma::MAJOR_K, umma::MAJOR_K, 128, MT);
+    for (int it = 0; it < j1 - j0; ++it) {
+      const int s = it % C::NS, d = it % C::NB;
+      bool ok = wait_fast(&full[s], (it / C::NS) & 1, abort_flag);
+      if (it >= C::NB) ok = ok && wait_fast(&d_free[d], (it / C::NB - 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      umma::fence_after_sync();
+      const uint32_t wa = umma::smem_u32(smem + s * C::STAGE), xa = wa + 128 * kMmBlock;
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma::mma_f8_ss(tmem + d * MT, umma::sdesc(wa + 32 * k, 16, 1024, umma::SWIZZLE_128B),
+                          umma::sdesc(xa + 32 * k, 16, 1024, umma::SWIZZLE_128B), ID, k > 0);
+        umma::mma_commit(&empty[s]);
+        umma::mma_commit(&d_full[d]);
+      }
+      __syncwarp();
+    }
+    __syncwarp();
+    if (elect_one()) umma::mma_commit(drained);               // complete before TMEM is released
+    (void)umma::mbar_wait(drained, 0, 100000000ull);
+    cluster_wait();
+  } else {
+    const int t = tid - 64, quarter = warp & 3, row = 32 * quarter + lane;     // row of b, TMEM lane
+    const uint32_t lane_col = (uint32_t)(32 * quarter) << 16;
+    const float* sa = p.a.sa + (int64_t)min(m0 + t, p.a.M - 1) * p.kb;         // column t's scales (t < MT)
+    const float* sb = p.a.sb + (int64_t)(n0 / 128) * p.kb;
+    float2 acc[MT / 2];
+#pragma unroll
+    for (int c = 0; c < MT / 2; ++c) acc[c] = make_float2(0.f, 0.f);
+    float next = t < MT && j0 < j1 ? sa[j0] * sb[j0] : 0.f;
+    bool ok = true;
+    for (int j = j0; j < j1; ++j) {
+      const int it = j - j0, d = it % C::NB;
+      if (t < MT) scol[(it & 1) * MT + t] = next;
+      if (t < MT && j + 1 < j1) next = sa[j + 1] * sb[j + 1];
+      asm volatile("bar.sync 1, 128;\n" ::: "memory");        // (and every warp is done with the row before the last)
+      ok = ok && wait_fast(&d_full[d], (it / C::NB) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) continue;                                      // (the barrier's other warps go on as well)
+      umma::fence_after_sync();
+      const float4* sc = reinterpret_cast<const float4*>(scol + (it & 1) * MT);
+#pragma unroll
+      for (int c = 0; c < MT / 16; ++c) {
+        uint32_t r[16];
+        umma::tmem_ld16_nowait(tmem + d * MT + lane_col + 16 * c, r);
+        umma::tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 x = sc[4 * c + u];
+          acc[8 * c + 2 * u] = __ffma2_rn(make_float2(__uint_as_float(r[4 * u]), __uint_as_float(r[4 * u + 1])), make_float2(x.x, x.y),
+                                          acc[8 * c + 2 * u]);
+          acc[8 * c + 2 * u + 1] = __ffma2_rn(make_float2(__uint_as_float(r[4 * u + 2]), __uint_as_float(r[4 * u + 3])),
+                                              make_float2(x.z, x.w), acc[8 * c + 2 * u + 1]);
+        }
+      }
+      umma::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) umma::mbar_arrive(&d_free[d]);
+    }
+    if (!ok) {
+      if (lane == 0) raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
+#pragma unroll
+      for (int c = 0; c < MT / 2; ++c) acc[c] = make_float2(NAN, NAN);
+    }
+    cluster_wait();
+    // column c goes to rank c / per
+    const uint32_t mine = umma::smem_u32(part + (rank * per) * 128 + row);
+    int owner = 0, left = per;
+    uint32_t to = mapa_u32(mine, 0);
+#pragma unroll
+    for (int c = 0; c < MT; ++c) {
+      if (left == 0) {
+        to = mapa_u32(mine, ++owner);
+        left = per;
+      }
+      asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to), "f"(c & 1 ? acc[c / 2].y : acc[c / 2].x) : "memory");
+      to += 512;
+      --left;
+    }
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory");
+  // this rank's columns (rows of out); neighbouring threads, neighbouring columns of out
+  for (int e = tid; e < per * 128; e += C::THREADS) {
+    const int c = e >> 7, l = e & 127, m = m0 + rank * per + c, n = n0 + l;
+    if (rank * per + c >= MT || m >= p.a.M || n >= p.a.N) continue;
+    float y = 0.f;
+    for (int r = 0; r < S; ++r) y += part[(r * per + c) * 128 + l];
+    if (p.a.bias != nullptr) y += p.a.bias[n];
+    if (p.a.out_f32) reinterpret_cast<float*>(p.a.out)[(int64_t)m * p.a.N + n] = y;
+    else reinterpret_cast<__nv_bfloat16*>(p.a.out)[(int64_t)m * p.a.N + n] = __float2bfloat16_rn(y);
+  }
+  umma::fence_before_sync();
+  __syncthreads();
+  umma::fence_after_sync();
+  if (warp == 1) umma::tmem_dealloc(tmem, C::TCOLS);
+}
+
+// Codes viewed as [rows][K], boxes of `box` rows x 128 bytes; what lies outside
+// reads as zero codes.
+static bool make_codes_map(CUtensorMap* m, const uint8_t* base, int rows, int K, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)K};
+  const cuuint32_t box[2] = {kMmBlock, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int BN>
+static cudaError_t launch_rows(MatmulParams& p, cudaStream_t st) {
+  const cudaError_t e = ensure_smem_optin((const void*)block_matmul_rows<BN>, MmCfg<BN>::BYTES);
+  if (e != cudaSuccess) return e;
+  p.tiles_m = (p.a.M + 127) / 128;
+  p.tiles_n = (p.a.N + BN - 1) / BN;
+  if (!make_codes_map(&p.ta, p.a.a, p.a.M, p.a.K, 128) || !make_codes_map(&p.tb, p.a.b, p.a.N, p.a.K, BN)) return cudaErrorInvalidValue;
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, sms = sm_count();
+  block_matmul_rows<BN><<<(unsigned)(tiles < sms ? tiles : sms), MmCfg<BN>::THREADS, MmCfg<BN>::BYTES, st>>>(p);
+  return cudaGetLastError();
+}
+
+template <int MT>
+static cudaError_t launch_few(MatmulParams& p, cudaStream_t st) {
+  const cudaError_t e = ensure_smem_optin((const void*)block_matmul_few<MT>, MfCfg<MT>::BYTES);
+  if (e != cudaSuccess) return e;
+  p.tiles_m = (p.a.M + MT - 1) / MT;
+  p.tiles_n = (p.a.N + 127) / 128;
+  if (!make_codes_map(&p.ta, p.a.a, p.a.M, p.a.K, MT) || !make_codes_map(&p.tb, p.a.b, p.a.N, p.a.K, 128)) return cudaErrorInvalidValue;
+  const int64_t units = (int64_t)p.tiles_m * p.tiles_n;
+  int64_t S = sm_count() / units;
+  S = S < 1 ? 1 : S > 8 ? 8 : S;
+  if (S > p.kb) S = p.kb;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)S;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.tiles_n * S), p.tiles_m);
+  cfg.blockDim = dim3(MfCfg<MT>::THREADS);
+  cfg.dynamicSmemBytes = MfCfg<MT>::BYTES;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, block_matmul_few<MT>, p);
+  if (r != cudaSuccess) (void)cudaGetLastError();
+  return r;
+}
+
+cudaError_t launch_block_matmul(const MatmulArgs& a, cudaStream_t st) {
+  MatmulParams p;
+  p.a = a;
+  p.kb = (a.K + kMmBlock - 1) / kMmBlock;
+  if (a.M <= 16) return launch_few<16>(p, st);
+  if (a.M <= 32) return launch_few<32>(p, st);
+  if (a.M <= 64) return launch_few<64>(p, st);
+  const int64_t tiles = (int64_t)((a.M + 127) / 128) * ((a.N + 127) / 128);
+  if (2 * tiles <= sm_count()) return launch_few<128>(p, st);
+  return tiles > 2 * sm_count() || a.M > 512 ? launch_rows<256>(p, st) : launch_rows<128>(p, st);
+}
+
+}  // namespace fp8kv

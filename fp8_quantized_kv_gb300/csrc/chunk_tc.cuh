@@ -126,18 +126,6 @@ __device__ __forceinline__ void tmem_st_128b_x8(uint32_t taddr, const uint32_t (
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-// One lane of the (converged) warp, the same at every call.  The issuing warps
-// run their loops with all lanes, and only the instruction itself belongs to
-// the elected one: addresses and descriptors are then uniform for the compiler.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t e;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(e));
-  return e != 0;
-}
 // OR of `pred` over the 256 softmax threads (named barrier 1).
 __device__ __forceinline__ bool softmax_any(bool pred) {
   uint32_t r;

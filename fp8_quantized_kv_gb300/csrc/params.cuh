@@ -104,6 +104,16 @@ struct TreeAcceptParams {
   int kv_heads, k_bytes, v_bytes, page_shift, paged;
 };
 
+// y[m][n] = sum over 128-wide blocks j of K of sa[m][j] sb[n / 128][j] sum a[m][k] b[n][k], plus bias[n].
+struct MatmulArgs {
+  const uint8_t *a, *b;       // e4m3 codes [M][K], [N][K]
+  const float *sa, *sb;       // [M][KB], [ceil(N / 128)][KB], KB = ceil(K / 128)
+  const float* bias;          // [N] or null
+  void* out;                  // [M][N]
+  unsigned int* err;
+  int M, N, K, out_f32;
+};
+
 struct ChunkParams {
   CacheView c;
   const __nv_bfloat16* q;    // [total_q][Hq][D]
@@ -149,6 +159,7 @@ cudaError_t launch_rope_tables(int positions, int pairs, const unsigned long lon
 cudaError_t launch_chunk_mma(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
 cudaError_t launch_chunk_rows(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
 cudaError_t launch_chunk_tc(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);
+cudaError_t launch_block_matmul(const MatmulArgs& a, cudaStream_t st);
 cudaError_t launch_tree_tables(const TreeTablesParams& p, cudaStream_t st);
 cudaError_t launch_tree_accept(const TreeAcceptParams& p, cudaStream_t st);
 cudaError_t launch_tree_mma(const ChunkParams& p, int dtype, int tiles, cudaStream_t st);

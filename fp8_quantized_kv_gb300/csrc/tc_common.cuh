@@ -181,6 +181,19 @@ __device__ __forceinline__ bool wait_fast(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// One lane of the (converged) warp, the same at every call.  The issuing warps
+// run their loops with all lanes, and only the instruction itself belongs to
+// the elected one: addresses and descriptors are then uniform for the compiler.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e));
+  return e != 0;
+}
+
 // OR of `pred` over the 128 threads of softmax warpgroup `wg` (named barrier
 // 1 + wg), and a plain barrier over the same threads.
 __device__ __forceinline__ bool group_any(int wg, bool pred) {

@@ -605,6 +605,27 @@ FP8KV_API fp8kv_status fp8kv_tree_accept(const fp8kv_cache *const *caches, int32
                                          int64_t *next_tokens, int32_t *new_lens,
                                          fp8kv_stream_t stream);
 
+/* The projections on either side of the attention, in 8 bits: matrix product of
+ * e4m3 codes with an fp32 scale for each block of 128 elements of k,
+ *   out[i][j] = sum_c a_scales[i][c] b_scales[j / 128][c]
+ *               sum_{l in block c} a[i][l] b[j][l]  (+ bias[j]).
+ *   a_codes:  [m][k] uint8, rows of activations; a_scales: [m][ceil(k / 128)]:
+ *             what fp8kv_quantize makes of [m * k / 128] rows of 128
+ *   b_codes:  [n][k] uint8, a weight; b_scales: [ceil(n / 128)][ceil(k / 128)],
+ *             one for each block of 128 x 128
+ *   bias:     [n] fp32, or NULL
+ *   out:      [m][n], bf16 or fp32 per out_dtype; apart from the inputs
+ * k a multiple of 16 (else FP8KV_ERR_UNSUPPORTED), any m and n up to 2^30; the last
+ * blocks of k and n may be short.  Codes and out on 16 bytes.
+ * A block's sum is formed on the tensor cores in fp32; blocks are summed in fp32
+ * with one rounding of the product of their two scales, which has to be in fp32's
+ * range.  Codes and scales that are not finite count as in the definition.
+ * A wait that runs out raises TIMEOUT; its rows are left as they were, or NaN. */
+FP8KV_API fp8kv_status fp8kv_block_matmul(const uint8_t *a_codes, const float *a_scales,
+                                          const uint8_t *b_codes, const float *b_scales,
+                                          const float *bias, int64_t m, int64_t n, int64_t k,
+                                          void *out, int32_t out_dtype, fp8kv_stream_t stream);
+
 /* Read (and, if `clear` is non-zero, reset) the device error word of the
  * current device.  Synchronous: waits for all work on the device. */
 FP8KV_API fp8kv_status fp8kv_get_device_error(uint32_t *bits, int32_t clear);
