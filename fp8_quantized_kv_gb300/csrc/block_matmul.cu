@@ -23,6 +23,8 @@ struct MatmulParams {
   int tiles_m, tiles_n;
 };
 
+// Waits for this thread's TMEM loads; the values are named, so that nothing that
+// uses them moves in front.
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -30,13 +32,59 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[3
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-// Waits for this thread's TMEM loads; the values are named, so that nothing that
-// uses them moves in front.
 __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+// Columns n0 .. n0 + 63 of row m of out, as far as there are any.
+__device__ __forceinline__ void store_row64(const MatmulArgs& a, int m, int n0, float2* acc) {
+  const int cols = min(64, a.N - n0);
+  if (cols <= 0) return;
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      if (2 * c < cols) acc[c].x += a.bias[n0 + 2 * c];
+      if (2 * c + 1 < cols) acc[c].y += a.bias[n0 + 2 * c + 1];
+    }
+  }
+  const int64_t out = (int64_t)m * a.N + n0;
+  if (a.out_f32) {
+    float* y = reinterpret_cast<float*>(a.out) + out;
+    const bool vec = a.N % 4 == 0;
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      if (vec && 2 * c + 4 <= cols) *reinterpret_cast<float4*>(y + 2 * c) = make_float4(acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y);
+      else {
+        const float v[4] = {acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y};
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (2 * c + u < cols) y[2 * c + u] = v[u];
+      }
+    }
+  } else {
+    __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(a.out) + out;
+    const bool vec = a.N % 8 == 0;
+#pragma unroll
+    for (int c = 0; c < 32; c += 4) {
+      __nv_bfloat162 h[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) h[u] = __floats2bfloat162_rn(acc[c + u].x, acc[c + u].y);
+      if (vec && 2 * c + 8 <= cols) *reinterpret_cast<uint4*>(y + 2 * c) = *reinterpret_cast<const uint4*>(h);
+      else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (2 * c + u < cols) y[2 * c + u] = u & 1 ? h[u / 2].y : h[u / 2].x;
+      }
+    }
+  }
 }
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
@@ -44,49 +92,94 @@ template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 
 // ---------------------------------------------------------- many rows of a --
-// A CTA owns tiles of 128 rows of a x BN rows of b, one after the other.
-//   warp 0      TMA producer: ring of a and b blocks
-//   warp 1      TMEM owner and MMA issuer
+// A pair of CTAs (cta_group::2) owns tiles of 256 rows of a x BN rows of b, one after
+// the other: each CTA loads and keeps 128 rows of a and half of b's, the products read
+// b from both, and each CTA's TMEM holds its own 128 rows of the sums.
+//   warp 0      TMA producer: ring of a and b blocks; every copy counts on the first
+//               CTA's barrier
+//   warp 1      TMEM owner; the first CTA's issues the products
 //   warps 4-11  sums: a thread keeps one row of the tile and half of its columns
 template <int BN>
 struct MmCfg {
-  static constexpr int STAGE = (128 + BN) * kMmBlock;
-  static constexpr int NS = BN == 256 ? 4 : 6;
-  static constexpr int BYTES = 1024 + NS * STAGE + 256;
+  static constexpr int STAGE = (128 + BN / 2) * kMmBlock;     // of one CTA
+  static constexpr int NS = BN == 256 ? 6 : 8;
+  static constexpr int NB = 512 / BN;                         // TMEM buffers
   static constexpr int THREADS = 384;
+  static constexpr int BYTES = 1024 + NS * STAGE + 512;
 };
 
+namespace pair {
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(umma::smem_u32(dst_smem)), "r"(ncols));
+}
+__device__ __forceinline__ void tmem_relinquish() { asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::); }
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(ncols));
+}
+// D (both CTAs' TMEM) (+)= A x B^T, 256 rows; one thread of the first CTA issues.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(id), "r"(accumulate));
+}
+// Arrive on the barrier at this place in both CTAs when all products issued before are complete.
+__device__ __forceinline__ void mma_commit(uint64_t* mbar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+                   umma::smem_u32(mbar)),
+               "h"((uint16_t)3)
+               : "memory");
+}
+// Tile load into this CTA; its bytes count on the barrier of the first CTA, given
+// by its shared::cluster address.
+__device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];\n" ::"r"(umma::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// Arrive on a barrier of either CTA (shared::cluster address).  It orders reads of
+// TMEM, which the tcgen05 fence in front covers, and no shared memory: at cluster
+// scope the release costs a microsecond.
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+}  // namespace pair
+
 template <int BN>
-__global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_rows(const __grid_constant__ MatmulParams p) {
+__global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const __grid_constant__ MatmulParams p) {
   using C = MmCfg<BN>;
-  constexpr int HC = BN / 2;                                  // columns of a thread
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::NS * C::STAGE);
-  uint64_t* full = bars;                                      // [NS] blocks landed
+  uint64_t* full = bars;                                      // [NS] first CTA: both CTAs' blocks landed
   uint64_t* empty = full + C::NS;                             // [NS] products have read them
-  uint64_t* d_full = empty + C::NS;                           // [2] a block's sums are in TMEM
-  uint64_t* d_free = d_full + 2;                              // [2] read
-  uint64_t* drained = d_free + 2;                             // every product finished
+  uint64_t* d_full = empty + C::NS;                           // [NB] a block's sums are in TMEM
+  uint64_t* d_free = d_full + C::NB;                          // [NB] first CTA: both CTAs have read them
+  uint64_t* drained = d_free + C::NB;                         // every product finished
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int tiles = p.tiles_m * p.tiles_n;
+  const int rank = (int)cluster_rank(), tiles = p.tiles_m * p.tiles_n, first = blockIdx.x >> 1, step = gridDim.x >> 1;
   if (tid == 0) {
     tma::prefetch_map(&p.ta);
     tma::prefetch_map(&p.tb);
     for (int i = 0; i < C::NS; ++i) { umma::mbar_init(&full[i], 1); umma::mbar_init(&empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { umma::mbar_init(&d_full[i], 1); umma::mbar_init(&d_free[i], 8); }
+    for (int i = 0; i < C::NB; ++i) { umma::mbar_init(&d_full[i], 1); umma::mbar_init(&d_free[i], 16); }
     umma::mbar_init(drained, 1);
     *abort_flag = 0;
     umma::mbar_fence_init();
   }
   if (warp == 1) {
-    umma::tmem_alloc(tslot, 2 * BN);
-    umma::tmem_relinquish();
+    pair::tmem_alloc(tslot, 512);
+    pair::tmem_relinquish();
   }
   umma::fence_before_sync();
   __syncthreads();
+  cluster_arrive_relaxed();                                   // (barriers initialised: fence above)
+  cluster_wait();
   umma::fence_after_sync();
   const uint32_t tmem = *tslot;
 
@@ -95,8 +188,8 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_rows(const
     if (warp == 0) {
       int it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-        const int m0 = tile % p.tiles_m * 128, n0 = tile / p.tiles_m * BN;
+      for (int tile = first; ok && tile < tiles; tile += step) {
+        const int m0 = tile % p.tiles_m * 256 + 128 * rank, n0 = tile / p.tiles_m * BN + BN / 2 * rank;
         for (int j = 0; j < p.kb; ++j, ++it) {
           const int s = it % C::NS;
           if (it >= C::NS) {
@@ -105,78 +198,98 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_rows(const
           }
           if (elect_one()) {
             uint8_t* st = smem + s * C::STAGE;
-            tma::arrive_expect_tx(&full[s], C::STAGE);
-            tma::load_2d(st, &p.ta, j * kMmBlock, m0, &full[s]);
-            tma::load_2d(st + 128 * kMmBlock, &p.tb, j * kMmBlock, n0, &full[s]);
+            const uint32_t bar = mapa_u32(umma::smem_u32(&full[s]), 0);
+            if (rank == 0) tma::arrive_expect_tx(&full[s], 2 * C::STAGE);
+            pair::load_2d(st, &p.ta, j * kMmBlock, m0, bar);
+            pair::load_2d(st + 128 * kMmBlock, &p.tb, j * kMmBlock, n0, bar);
           }
           __syncwarp();
         }
       }
-      // no copy is in flight when the CTA ends (matters when a wait gave up)
-      if (lane == 0)
+      // no copy is in flight when the pair ends (matters when a wait gave up)
+      if (lane == 0 && rank == 0)
         for (int i = max(0, it - C::NS); i < it; ++i) (void)umma::mbar_wait(&full[i % C::NS], (i / C::NS) & 1, 100000000ull);
-    } else if (warp == 1) {
-      constexpr uint32_t ID = umma::idesc(umma::FMT_E4M3, umma::FMT_E4M3, umma::MAJOR_K, umma::MAJOR_K, 128, BN);
+    } else if (warp == 1 && rank == 0) {
+      constexpr uint32_t ID = umma::idesc(umma::FMT_E4M3, umma::FMT_E4M3, umma::MAJOR_K, umma::MAJOR_K, 256, BN);
+      // The next block's barriers are tested while this one's products go out: the
+      // tensor pipe runs dry if they are looked at only behind them.
       int it = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      bool ok = true, full_ok = false, free_ok = true;
+      for (int tile = first; ok && tile < tiles; tile += step) {
         for (int j = 0; j < p.kb; ++j, ++it) {
-          const int s = it % C::NS, d = it & 1;
-          ok = wait_fast(&full[s], (it / C::NS) & 1, abort_flag);
-          if (it >= 2) ok = ok && wait_fast(&d_free[d], (it / 2 - 1) & 1, abort_flag);
+          const int s = it % C::NS, d = it % C::NB, next = it + 1;
+          if (!full_ok) ok = wait_fast(&full[s], (it / C::NS) & 1, abort_flag);
+          if (!free_ok) ok = ok && wait_fast(&d_free[d], (it / C::NB - 1) & 1, abort_flag);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           umma::fence_after_sync();
           const uint32_t aa = umma::smem_u32(smem + s * C::STAGE), ba = aa + 128 * kMmBlock;
-          if (elect_one()) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma::mma_f8_ss(tmem + d * BN, umma::sdesc(aa + 32 * k, 16, 1024, umma::SWIZZLE_128B),
-                              umma::sdesc(ba + 32 * k, 16, 1024, umma::SWIZZLE_128B), ID, k > 0);
-            umma::mma_commit(&empty[s]);
-            umma::mma_commit(&d_full[d]);
+          const bool leader = elect_one();
+          auto product = [&](int k) {
+            pair::mma_f8(tmem + d * BN, umma::sdesc(aa + 32 * k, 16, 1024, umma::SWIZZLE_128B),
+                         umma::sdesc(ba + 32 * k, 16, 1024, umma::SWIZZLE_128B), ID, k > 0);
+          };
+          if (leader) {
+            product(0);
+            product(1);
+          }
+          free_ok = next < C::NB || umma::mbar_test(&d_free[next % C::NB], (next / C::NB - 1) & 1);
+          full_ok = umma::mbar_test(&full[next % C::NS], (next / C::NS) & 1);
+          if (leader) {
+            product(2);
+            product(3);
+            pair::mma_commit(&d_full[d]);
+            pair::mma_commit(&empty[s]);
           }
           __syncwarp();
         }
       }
       // all issued products complete before TMEM is released
       __syncwarp();
-      if (elect_one()) umma::mma_commit(drained);
+      if (elect_one()) pair::mma_commit(drained);
       (void)umma::mbar_wait(drained, 0, 100000000ull);
     }
   } else {
-    regs_inc<216>();
-    const int half = (warp - 4) >> 2, row_in = 32 * (warp & 3) + lane;
-    const uint32_t lane_col = ((uint32_t)(32 * (warp & 3)) << 16) + half * HC;
+    regs_inc<232>();
+    constexpr int HC = BN / 2, PC = HC / 32;                  // columns of a thread, and in pieces of 32
+    const int part = (warp - 4) >> 2, row_in = 32 * (warp & 3) + lane;
+    const uint32_t base = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + HC * part;
+    const uint32_t free0 = mapa_u32(umma::smem_u32(d_free), 0);
+    const int blocks = (tiles - first + step - 1) / step * p.kb;             // of all this pair's tiles
     int it = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-      const int m = tile % p.tiles_m * 128 + row_in, n0 = tile / p.tiles_m * BN + half * HC;
-      const bool live = m < p.a.M && n0 < p.a.N;
-      const float* sa = p.a.sa + (int64_t)(live ? m : 0) * p.kb;
-      const float* sb = p.a.sb + (int64_t)(live ? n0 / 128 : 0) * p.kb;
+    bool ok = true, ready = false;
+    uint32_t r[2][32];
+    // the first piece of block i, behind its barrier (`ready`: found complete before)
+    auto start = [&](int i) {
+      if (!ready) ok = wait_fast(&d_full[i % C::NB], (i / C::NB) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      umma::fence_after_sync();
+      tmem_ld32_nowait(base + BN * (i % C::NB), r[0]);
+    };
+    start(0);
+    for (int tile = first; ok && tile < tiles; tile += step) {
+      const int m = tile % p.tiles_m * 256 + 128 * rank + row_in, n0 = tile / p.tiles_m * BN + HC * part;
+      const float* sa = p.a.sa + (int64_t)min(m, p.a.M - 1) * p.kb;
+      const float* sb = p.a.sb + (int64_t)(n0 < p.a.N ? n0 / 128 : 0) * p.kb;
       float2 acc[HC / 2];
 #pragma unroll
       for (int c = 0; c < HC / 2; ++c) acc[c] = make_float2(0.f, 0.f);
       float next_a = sa[0], next_b = sb[0];
-      for (int j = 0; j < p.kb; ++j, ++it) {
-        const int d = it & 1;
-        const float s = next_a * next_b;
+      for (int j = 0; ok && j < p.kb; ++j, ++it) {
+        const int d = it % C::NB, next = it + 1;
+        const float2 s2 = make_float2(next_a * next_b, next_a * next_b);
         if (j + 1 < p.kb) { next_a = sa[j + 1]; next_b = sb[j + 1]; }
-        ok = wait_fast(&d_full[d], (it / 2) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        umma::fence_after_sync();
-        const float2 s2 = make_float2(s, s);
-        uint32_t r[2][32];
-        const uint32_t at = tmem + d * BN + lane_col;
-        tmem_ld32_nowait(at, r[0]);
+        // a piece of 32 columns is multiplied while the next is on its way
 #pragma unroll
-        for (int c = 0; c < HC / 32; ++c) {
+        for (int c = 0; c < PC; ++c) {
           tmem_wait_ld32(r[c & 1]);
-          if (c + 1 < HC / 32) tmem_ld32_nowait(at + 32 * (c + 1), r[(c + 1) & 1]);
-          else {
+          if (c == PC - 2) ready = umma::mbar_test(&d_full[next % C::NB], (next / C::NB) & 1);
+          if (c < PC - 1) {
+            tmem_ld32_nowait(base + BN * d + 32 * (c + 1), r[(c + 1) & 1]);
+          } else {
             umma::fence_before_sync();
             __syncwarp();
-            if (lane == 0) umma::mbar_arrive(&d_free[d]);
+            if (lane == 0) pair::arrive_remote(free0 + 8 * d);
+            if (next < blocks) start(next);
           }
 #pragma unroll
           for (int u = 0; u < 16; ++u)
@@ -184,51 +297,19 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_rows(const
                                          acc[16 * c + u]);
         }
       }
-      if (!ok || !live) continue;
-      const int cols = min(HC, p.a.N - n0);
-      if (p.a.bias != nullptr) {
+      if (!ok || m >= p.a.M) continue;
 #pragma unroll
-        for (int c = 0; c < HC / 2; ++c) {
-          if (2 * c < cols) acc[c].x += p.a.bias[n0 + 2 * c];
-          if (2 * c + 1 < cols) acc[c].y += p.a.bias[n0 + 2 * c + 1];
-        }
-      }
-      const int64_t out = (int64_t)m * p.a.N + n0;
-      if (p.a.out_f32) {
-        float* y = reinterpret_cast<float*>(p.a.out) + out;
-        const bool vec = p.a.N % 4 == 0;
-#pragma unroll
-        for (int c = 0; c < HC / 2; c += 2) {
-          if (vec && 2 * c + 4 <= cols) *reinterpret_cast<float4*>(y + 2 * c) = make_float4(acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y);
-          else {
-            const float v[4] = {acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y};
-            for (int u = 0; u < 4; ++u)
-              if (2 * c + u < cols) y[2 * c + u] = v[u];
-          }
-        }
-      } else {
-        __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(p.a.out) + out;
-        const bool vec = p.a.N % 8 == 0;
-#pragma unroll
-        for (int c = 0; c < HC / 2; c += 4) {
-          __nv_bfloat162 h[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) h[u] = __floats2bfloat162_rn(acc[c + u].x, acc[c + u].y);
-          if (vec && 2 * c + 8 <= cols) *reinterpret_cast<uint4*>(y + 2 * c) = *reinterpret_cast<const uint4*>(h);
-          else {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              if (2 * c + u < cols) y[2 * c + u] = u & 1 ? h[u / 2].y : h[u / 2].x;
-          }
-        }
-      }
+      for (int c = 0; c < HC / 64; ++c) store_row64(p.a, m, n0 + 64 * c, acc + 32 * c);
     }
     if (!ok && lane == 0) raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
   }
+  // neither CTA's shared memory or TMEM is in use by the other any more
   umma::fence_before_sync();
-  __syncthreads();
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");
+  cluster_wait();
   umma::fence_after_sync();
-  if (warp == 1) umma::tmem_dealloc(tmem, 2 * BN);
+  if (warp == 1) pair::tmem_dealloc(tmem, 512);
 }
 
 // ----------------------------------------------------------- few rows of a --
@@ -423,15 +504,28 @@ static bool make_codes_map(CUtensorMap* m, const uint8_t* base, int rows, int K,
 }
 
 template <int BN>
-static cudaError_t launch_rows(MatmulParams& p, cudaStream_t st) {
-  const cudaError_t e = ensure_smem_optin((const void*)block_matmul_rows<BN>, MmCfg<BN>::BYTES);
+static cudaError_t launch_pair(MatmulParams& p, cudaStream_t st) {
+  using C = MmCfg<BN>;
+  const cudaError_t e = ensure_smem_optin((const void*)block_matmul_pair<BN>, C::BYTES);
   if (e != cudaSuccess) return e;
-  p.tiles_m = (p.a.M + 127) / 128;
+  p.tiles_m = (p.a.M + 255) / 256;
   p.tiles_n = (p.a.N + BN - 1) / BN;
-  if (!make_codes_map(&p.ta, p.a.a, p.a.M, p.a.K, 128) || !make_codes_map(&p.tb, p.a.b, p.a.N, p.a.K, BN)) return cudaErrorInvalidValue;
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, sms = sm_count();
-  block_matmul_rows<BN><<<(unsigned)(tiles < sms ? tiles : sms), MmCfg<BN>::THREADS, MmCfg<BN>::BYTES, st>>>(p);
-  return cudaGetLastError();
+  if (!make_codes_map(&p.ta, p.a.a, p.a.M, p.a.K, 128) || !make_codes_map(&p.tb, p.a.b, p.a.N, p.a.K, BN / 2)) return cudaErrorInvalidValue;
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, pairs = sm_count() / 2;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::BYTES;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, block_matmul_pair<BN>, p);
+  if (r != cudaSuccess) (void)cudaGetLastError();
+  return r;
 }
 
 template <int MT>
@@ -468,9 +562,9 @@ cudaError_t launch_block_matmul(const MatmulArgs& a, cudaStream_t st) {
   if (a.M <= 16) return launch_few<16>(p, st);
   if (a.M <= 32) return launch_few<32>(p, st);
   if (a.M <= 64) return launch_few<64>(p, st);
-  const int64_t tiles = (int64_t)((a.M + 127) / 128) * ((a.N + 127) / 128);
-  if (2 * tiles <= sm_count()) return launch_few<128>(p, st);
-  return tiles > 2 * sm_count() || a.M > 512 ? launch_rows<256>(p, st) : launch_rows<128>(p, st);
+  if (a.M <= 128) return launch_few<128>(p, st);
+  const int64_t wide = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+  return 2 * wide > sm_count() / 2 ? launch_pair<256>(p, st) : launch_pair<128>(p, st);
 }
 
 }  // namespace fp8kv
