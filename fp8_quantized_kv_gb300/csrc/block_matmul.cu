@@ -312,6 +312,110 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
   if (warp == 1) pair::tmem_dealloc(tmem, 512);
 }
 
+// --------------------------------------------------- at most sixteen rows of a --
+// The weights are read once and nothing else takes as long, so no operand is staged:
+// a warp takes 16 rows of b and every eighth block of K, and its lanes load their
+// matrix fragments straight from memory (mma.sync, b's rows on the long side, a's
+// as the eight columns; NT sets of those).  The order of a dot product's elements is
+// free, so a lane takes 16 bytes that lie together, of b and of a alike.  The eight
+// warps of a CTA join in shared memory in their order.
+constexpr int kMwRows = 16, kMwWarps = 8;
+
+__device__ __forceinline__ void mma16832_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint4 load_once(const uint8_t* p) {
+  uint4 x;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+  return x;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(32 * kMwWarps, NT == 1 ? 3 : 2) block_matmul_warp(const MatmulArgs a, int kb) {
+  constexpr int U = 2;                                        // blocks of K loaded at once
+  __shared__ float part[kMwWarps][8 * NT][kMwRows + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
+  const int n0 = blockIdx.x * kMwRows;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint8_t* brow[2];
+  const uint8_t* arow[NT];
+  bool blive[2], alive[NT];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int n = n0 + g + 8 * i;
+    blive[i] = n < a.N;
+    brow[i] = a.b + (int64_t)(blive[i] ? n : 0) * a.K + 16 * c4;
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int m = 8 * t + g;
+    alive[t] = m < a.M;
+    arow[t] = a.a + (int64_t)(alive[t] ? m : 0) * a.K + 16 * c4;
+  }
+  const float* sb = a.sb + (int64_t)(n0 / 128) * kb;
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+  for (int j0 = warp; j0 < kb; j0 += U * kMwWarps) {
+    uint4 bx[U][2][2], ax[U][NT][2];                          // [block][row][64-byte half]
+    float s[U][NT][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * kMwWarps;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t k = (int64_t)j * kMmBlock + 64 * h;
+        const bool in = j < kb && k + 16 * c4 < a.K;          // (K is a multiple of 16)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) bx[u][i][h] = in && blive[i] ? load_once(brow[i] + k) : zero;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) ax[u][t][h] = in && alive[t] ? *reinterpret_cast<const uint4*>(arow[t] + k) : zero;
+      }
+      const float b = j < kb ? sb[j] : 0.f;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int m = 8 * t + 2 * c4 + i;
+          s[u][t][i] = j < kb && m < a.M ? a.sa[(int64_t)m * kb + j] * b : 0.f;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mma16832_e4m3(d, bx[u][0][h].x, bx[u][1][h].x, bx[u][0][h].y, bx[u][1][h].y, ax[u][t][h].x, ax[u][t][h].y);
+          mma16832_e4m3(d, bx[u][0][h].z, bx[u][1][h].z, bx[u][0][h].w, bx[u][1][h].w, ax[u][t][h].z, ax[u][t][h].w);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(d[e], s[u][t][e & 1], acc[t][e]);
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[warp][8 * t + 2 * c4 + (e & 1)][g + 8 * (e >> 1)] = acc[t][e];
+  __syncthreads();
+  if (tid < 8 * NT * kMwRows) {
+    const int m = tid / kMwRows, n = n0 + tid % kMwRows;
+    if (m >= a.M || n >= a.N) return;
+    float y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMwWarps; ++w) y += part[w][m][tid % kMwRows];
+    if (a.bias != nullptr) y += a.bias[n];
+    if (a.out_f32) reinterpret_cast<float*>(a.out)[(int64_t)m * a.N + n] = y;
+    else reinterpret_cast<__nv_bfloat16*>(a.out)[(int64_t)m * a.N + n] = __float2bfloat16_rn(y);
+  }
+}
+
 // ----------------------------------------------------------- few rows of a --
 // The weights' bytes bound it, so they are spread over all SMs: a CTA takes 128
 // rows of b (the tensor core's 128 lanes), up to MT rows of a (its columns), and a
@@ -559,7 +663,12 @@ cudaError_t launch_block_matmul(const MatmulArgs& a, cudaStream_t st) {
   MatmulParams p;
   p.a = a;
   p.kb = (a.K + kMmBlock - 1) / kMmBlock;
-  if (a.M <= 16) return launch_few<16>(p, st);
+  if (a.M <= 16) {
+    const unsigned grid = (unsigned)((a.N + kMwRows - 1) / kMwRows);
+    if (a.M <= 8) block_matmul_warp<1><<<grid, 32 * kMwWarps, 0, st>>>(a, p.kb);
+    else block_matmul_warp<2><<<grid, 32 * kMwWarps, 0, st>>>(a, p.kb);
+    return cudaGetLastError();
+  }
   if (a.M <= 32) return launch_few<32>(p, st);
   if (a.M <= 64) return launch_few<64>(p, st);
   if (a.M <= 128) return launch_few<128>(p, st);
