@@ -86,6 +86,33 @@ __device__ __forceinline__ void store_row64(const MatmulArgs& a, int m, int n0, 
     }
   }
 }
+// Columns n .. n + 3 of row m of out (n a multiple of 4), as far as there are any.
+__device__ __forceinline__ void store_row4(const MatmulArgs& a, int m, int n, float4 y) {
+  const int cols = a.N - n;
+  if (a.bias != nullptr) {
+    y.x += a.bias[n];
+    if (cols > 1) y.y += a.bias[n + 1];
+    if (cols > 2) y.z += a.bias[n + 2];
+    if (cols > 3) y.w += a.bias[n + 3];
+  }
+  const int64_t at = (int64_t)m * a.N + n;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+  if (a.N % 4 == 0) {
+    if (a.out_f32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = y;
+    else
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    return;
+  }
+  const float v[4] = {y.x, y.y, y.z, y.w};
+  const __nv_bfloat16 w[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (u < cols) {
+      if (a.out_f32) reinterpret_cast<float*>(a.out)[at + u] = v[u];
+      else reinterpret_cast<__nv_bfloat16*>(a.out)[at + u] = w[u];
+    }
+}
 template <int N>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
 template <int N>
@@ -303,10 +330,11 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
     }
     if (!ok && lane == 0) raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
   }
-  // neither CTA's shared memory or TMEM is in use by the other any more
+  // neither CTA's shared memory or TMEM is in use by the other any more (nothing is
+  // published: a release would wait for the stores of out)
   umma::fence_before_sync();
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");
+  cluster_arrive_relaxed();
   cluster_wait();
   umma::fence_after_sync();
   if (warp == 1) pair::tmem_dealloc(tmem, 512);
@@ -334,8 +362,8 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
 }
 
 template <int NT>
-__global__ void __launch_bounds__(32 * kMwWarps, NT == 1 ? 3 : 2) block_matmul_warp(const MatmulArgs a, int kb) {
-  constexpr int U = 2;                                        // blocks of K loaded at once
+__global__ void __launch_bounds__(32 * kMwWarps, 3) block_matmul_warp(const MatmulArgs a, int kb) {
+  constexpr int U = NT == 1 ? 2 : 1;                          // blocks of K loaded at once
   __shared__ float part[kMwWarps][8 * NT][kMwRows + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
   const int n0 = blockIdx.x * kMwRows;
@@ -420,49 +448,61 @@ __global__ void __launch_bounds__(32 * kMwWarps, NT == 1 ? 3 : 2) block_matmul_w
 // The weights' bytes bound it, so they are spread over all SMs: a CTA takes 128
 // rows of b (the tensor core's 128 lanes), up to MT rows of a (its columns), and a
 // share of the blocks of K; the CTAs of a cluster hold the shares of one tile.  Each
-// sums its blocks in registers, sends every column's sums to the CTA that owns the
-// column (distributed shared memory), and the owner adds the shares in rank order.
+// sums its blocks in registers, copies every column's sums to the CTA that owns the
+// column (one bulk copy a CTA through distributed shared memory), and the owner adds
+// the shares in rank order.
 template <int MT>
 struct MfCfg {
   static constexpr int STAGE = (128 + MT) * kMmBlock;
-  static constexpr int NB = 512 / MT < 8 ? 512 / MT : 8;      // TMEM buffers
-  static constexpr int NS = MT == 128 ? 4 : MT == 64 ? 7 : 8;
-  static constexpr int PART = 128 * (MT + 8) * 4;             // shares received (columns rounded up per rank)
-  static constexpr int BYTES = 1024 + NS * STAGE + PART + 2 * MT * 4 + 512;
-  static constexpr int TCOLS = NB * MT < 32 ? 32 : NB * MT;
+  static constexpr int CTAS = MT <= 64 ? 2 : 1;               // of an SM
+  static constexpr int NB = 256 * (3 - CTAS) / MT < 8 ? 256 * (3 - CTAS) / MT : 8;      // TMEM buffers
+  static constexpr int NS = MT == 128 ? 6 : MT == 64 ? 4 : 5;
+  static constexpr int SK = 16;                               // blocks whose scales are held
+  static constexpr int SUMS = MT * 128 * 4;                   // a tile's sums, as they are sent
+  static constexpr int BYTES = 1024 + NS * STAGE + SK * MT * 4 + 512;
+  static constexpr int TCOLS = NB * MT;
   static constexpr int THREADS = 192;
-  static_assert(BYTES <= 227 * 1024, "shared memory of an SM");
+  static_assert(2 * SUMS <= NS * STAGE, "sent and received sums take the ring's place");
+  static_assert(CTAS * (BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 template <int MT>
-__global__ void __launch_bounds__(MfCfg<MT>::THREADS, 1) block_matmul_few(const __grid_constant__ MatmulParams p) {
+__global__ void __launch_bounds__(MfCfg<MT>::THREADS, MfCfg<MT>::CTAS) block_matmul_few(const __grid_constant__ MatmulParams p) {
   using C = MfCfg<MT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* part = reinterpret_cast<float*>(smem + C::NS * C::STAGE);       // [rank][own column][128]
-  float* scol = reinterpret_cast<float*>(smem + C::NS * C::STAGE + C::PART);   // [2][MT] scales of the columns
-  uint64_t* bars = reinterpret_cast<uint64_t*>(scol + 2 * MT);
+  float* scol = reinterpret_cast<float*>(smem + C::NS * C::STAGE);       // [SK][MT] scales of the columns
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scol + C::SK * MT);
   uint64_t* full = bars;
   uint64_t* empty = full + C::NS;
   uint64_t* d_full = empty + C::NS;                           // [NB]
   uint64_t* d_free = d_full + C::NB;                          // [NB]
   uint64_t* drained = d_free + C::NB;                         // every product finished
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
+  uint64_t* landed = drained + 1;                             // the other shares of this CTA's columns
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(landed + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int S, rank;
+  int S;
   asm("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(S));
-  rank = (int)cluster_rank();
+  const int rank = (int)cluster_rank(), per = MT / S;         // columns of a rank (S is 1, 2, 4 or 8)
   const int n0 = blockIdx.x / S * 128, m0 = blockIdx.y * MT;
   const int j0 = (int)((int64_t)p.kb * rank / S), j1 = (int)((int64_t)p.kb * (rank + 1) / S);
+  auto load = [&](int it) {                                   // block j0 + it
+    const int s = it % C::NS;
+    uint8_t* st = smem + s * C::STAGE;
+    tma::arrive_expect_tx(&full[s], C::STAGE);
+    tma::load_2d(st, &p.tb, (j0 + it) * kMmBlock, n0, &full[s]);
+    tma::load_2d(st + 128 * kMmBlock, &p.ta, (j0 + it) * kMmBlock, m0, &full[s]);
+  };
   if (tid == 0) {
-    tma::prefetch_map(&p.ta);
-    tma::prefetch_map(&p.tb);
     for (int i = 0; i < C::NS; ++i) { umma::mbar_init(&full[i], 1); umma::mbar_init(&empty[i], 1); }
     for (int i = 0; i < C::NB; ++i) { umma::mbar_init(&d_full[i], 1); umma::mbar_init(&d_free[i], 4); }
     umma::mbar_init(drained, 1);
+    umma::mbar_init(landed, 1);
     *abort_flag = 0;
     umma::mbar_fence_init();
+    if (S > 1) tma::arrive_expect_tx(landed, (S - 1) * per * 512);
+    for (int it = 0; it < C::NS && it < j1 - j0; ++it) load(it);         // the first copies do not wait for the rest
   }
   if (warp == 1) {
     umma::tmem_alloc(tslot, C::TCOLS);
@@ -471,35 +511,27 @@ __global__ void __launch_bounds__(MfCfg<MT>::THREADS, 1) block_matmul_few(const 
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
-  cluster_arrive_relaxed();                                   // every CTA of the cluster runs before it is written to
   const uint32_t tmem = *tslot;
-  const int per = (MT + S - 1) / S;                           // columns of a rank
+  float2 acc[MT / 2];
+  bool ok = true;
   if (warp == 0) {
-    int j = j0;
-    for (; j < j1; ++j) {
-      const int it = j - j0, s = it % C::NS;
-      if (it >= C::NS) {
-        const bool ok = wait_fast(&empty[s], (it / C::NS - 1) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) break;
-      }
-      if (elect_one()) {
-        uint8_t* st = smem + s * C::STAGE;
-        tma::arrive_expect_tx(&full[s], C::STAGE);
-        tma::load_2d(st, &p.tb, j * kMmBlock, n0, &full[s]);
-        tma::load_2d(st + 128 * kMmBlock, &p.ta, j * kMmBlock, m0, &full[s]);
-      }
+    int it = min(C::NS, j1 - j0);
+    for (; it < j1 - j0; ++it) {
+      const bool free = wait_fast(&empty[it % C::NS], (it / C::NS - 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, free)) break;
+      if (elect_one()) load(it);
       __syncwarp();
     }
+    // no copy is in flight when the ring is used for the sums (matters when a wait gave up)
     if (lane == 0)
-      for (int i = max(0, j - j0 - C::NS); i < j - j0; ++i) (void)umma::mbar_wait(&full[i % C::NS], (i / C::NS) & 1, 100000000ull);
-    cluster_wait();
+      for (int i = max(0, it - C::NS); i < it; ++i) (void)umma::mbar_wait(&full[i % C::NS], (i / C::NS) & 1, 100000000ull);
   } else if (warp == 1) {
     constexpr uint32_t ID = umma::idesc(umma::FMT_E4M3, umma::FMT_E4M3, umma::MAJOR_K, umma::MAJOR_K, 128, MT);
     for (int it = 0; it < j1 - j0; ++it) {
       const int s = it % C::NS, d = it % C::NB;
-      bool ok = wait_fast(&full[s], (it / C::NS) & 1, abort_flag);
-      if (it >= C::NB) ok = ok && wait_fast(&d_free[d], (it / C::NB - 1) & 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      bool go = wait_fast(&full[s], (it / C::NS) & 1, abort_flag);
+      if (it >= C::NB) go = go && wait_fast(&d_free[d], (it / C::NB - 1) & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, go)) break;
       umma::fence_after_sync();
       const uint32_t wa = umma::smem_u32(smem + s * C::STAGE), xa = wa + 128 * kMmBlock;
       if (elect_one()) {
@@ -513,83 +545,112 @@ __global__ void __launch_bounds__(MfCfg<MT>::THREADS, 1) block_matmul_few(const 
       __syncwarp();
     }
     __syncwarp();
-    if (elect_one()) umma::mma_commit(drained);               // complete before TMEM is released
+    if (elect_one()) umma::mma_commit(drained);               // complete before TMEM and the ring are used otherwise
     (void)umma::mbar_wait(drained, 0, 100000000ull);
-    cluster_wait();
   } else {
-    const int t = tid - 64, quarter = warp & 3, row = 32 * quarter + lane;     // row of b, TMEM lane
-    const uint32_t lane_col = (uint32_t)(32 * quarter) << 16;
-    const float* sa = p.a.sa + (int64_t)min(m0 + t, p.a.M - 1) * p.kb;         // column t's scales (t < MT)
+    const int t = tid - 64;
+    const uint32_t base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const float* sb = p.a.sb + (int64_t)(n0 / 128) * p.kb;
-    float2 acc[MT / 2];
 #pragma unroll
     for (int c = 0; c < MT / 2; ++c) acc[c] = make_float2(0.f, 0.f);
-    float next = t < MT && j0 < j1 ? sa[j0] * sb[j0] : 0.f;
-    bool ok = true;
     for (int j = j0; j < j1; ++j) {
       const int it = j - j0, d = it % C::NB;
-      if (t < MT) scol[(it & 1) * MT + t] = next;
-      if (t < MT && j + 1 < j1) next = sa[j + 1] * sb[j + 1];
-      asm volatile("bar.sync 1, 128;\n" ::: "memory");        // (and every warp is done with the row before the last)
+      if (it % C::SK == 0) {                                  // scales of the next blocks: both factors multiplied once
+        asm volatile("bar.sync 1, 128;\n" ::: "memory");      // (the others are done with the last ones)
+        constexpr int EACH = C::SK * MT / 128;                // of a thread: loaded at once, one block of K
+        const int i = t % C::SK;
+        const float b = j + i < j1 ? sb[j + i] : 0.f;
+        float x[EACH];
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+          const int m = min(m0 + t / C::SK + e * (128 / C::SK), p.a.M - 1);
+          x[e] = j + i < j1 ? p.a.sa[(int64_t)m * p.kb + j + i] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) scol[i * MT + t / C::SK + e * (128 / C::SK)] = x[e] * b;
+        asm volatile("bar.sync 1, 128;\n" ::: "memory");
+      }
       ok = ok && wait_fast(&d_full[d], (it / C::NB) & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) continue;                                      // (the barrier's other warps go on as well)
+      if (!ok) continue;                                      // (the barriers' other warps go on as well)
       umma::fence_after_sync();
-      const float4* sc = reinterpret_cast<const float4*>(scol + (it & 1) * MT);
+      const float4* sc = reinterpret_cast<const float4*>(scol + it % C::SK * MT);
 #pragma unroll
-      for (int c = 0; c < MT / 16; ++c) {
-        uint32_t r[16];
-        umma::tmem_ld16_nowait(tmem + d * MT + lane_col + 16 * c, r);
-        umma::tmem_wait_ld();
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float4 x = sc[4 * c + u];
-          acc[8 * c + 2 * u] = __ffma2_rn(make_float2(__uint_as_float(r[4 * u]), __uint_as_float(r[4 * u + 1])), make_float2(x.x, x.y),
-                                          acc[8 * c + 2 * u]);
-          acc[8 * c + 2 * u + 1] = __ffma2_rn(make_float2(__uint_as_float(r[4 * u + 2]), __uint_as_float(r[4 * u + 3])),
-                                              make_float2(x.z, x.w), acc[8 * c + 2 * u + 1]);
+      for (int c = 0; c < MT / 32; c += 2) {                  // two pieces of 32 columns in flight
+        uint32_t r[2][32];
+        tmem_ld32_nowait(base + d * MT + 32 * c, r[0]);
+        if (c + 1 < MT / 32) tmem_ld32_nowait(base + d * MT + 32 * (c + 1), r[1]);
+        tmem_wait_ld32(r[0]);
+        if (c + 1 < MT / 32) tmem_wait_ld32(r[1]);
+        if (c + 2 >= MT / 32) {
+          umma::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) umma::mbar_arrive(&d_free[d]);
         }
-      }
-      umma::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) umma::mbar_arrive(&d_free[d]);
-    }
-    if (!ok) {
-      if (lane == 0) raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
 #pragma unroll
-      for (int c = 0; c < MT / 2; ++c) acc[c] = make_float2(NAN, NAN);
-    }
-    cluster_wait();
-    // column c goes to rank c / per
-    const uint32_t mine = umma::smem_u32(part + (rank * per) * 128 + row);
-    int owner = 0, left = per;
-    uint32_t to = mapa_u32(mine, 0);
+        for (int k = 0; k < 2 && c + k < MT / 32; ++k)
 #pragma unroll
-    for (int c = 0; c < MT; ++c) {
-      if (left == 0) {
-        to = mapa_u32(mine, ++owner);
-        left = per;
+          for (int u = 0; u < 8; ++u) {
+            const float4 x = sc[8 * (c + k) + u];
+            float2* y = acc + 16 * (c + k) + 2 * u;
+            y[0] = __ffma2_rn(make_float2(__uint_as_float(r[k][4 * u]), __uint_as_float(r[k][4 * u + 1])), make_float2(x.x, x.y), y[0]);
+            y[1] = __ffma2_rn(make_float2(__uint_as_float(r[k][4 * u + 2]), __uint_as_float(r[k][4 * u + 3])), make_float2(x.z, x.w), y[1]);
+          }
       }
-      asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(to), "f"(c & 1 ? acc[c / 2].y : acc[c / 2].x) : "memory");
-      to += 512;
-      --left;
     }
   }
+  // Every CTA of the cluster is done with its ring: sums to send go to its front,
+  // [column][row of b], those received behind them, [rank][own column][row of b].
   __syncwarp();
-  asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire;\n" ::: "memory");
-  // this rank's columns (rows of out); neighbouring threads, neighbouring columns of out
-  for (int e = tid; e < per * 128; e += C::THREADS) {
-    const int c = e >> 7, l = e & 127, m = m0 + rank * per + c, n = n0 + l;
-    if (rank * per + c >= MT || m >= p.a.M || n >= p.a.N) continue;
-    float y = 0.f;
-    for (int r = 0; r < S; ++r) y += part[(r * per + c) * 128 + l];
-    if (p.a.bias != nullptr) y += p.a.bias[n];
-    if (p.a.out_f32) reinterpret_cast<float*>(p.a.out)[(int64_t)m * p.a.N + n] = y;
-    else reinterpret_cast<__nv_bfloat16*>(p.a.out)[(int64_t)m * p.a.N + n] = __float2bfloat16_rn(y);
+  if (S > 1) {
+    asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");
+    cluster_wait();
+  } else {
+    __syncthreads();
   }
-  umma::fence_before_sync();
+  float* sent = reinterpret_cast<float*>(smem);
+  float* got = sent + MT * 128;
+  if (warp >= 2) {
+    const int row = 32 * (warp & 3) + lane;                   // of b, TMEM lane
+    if (!ok && lane == 0) raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
+#pragma unroll
+    for (int c = 0; c < MT; ++c) sent[c * 128 + row] = !ok ? NAN : c & 1 ? acc[c / 2].y : acc[c / 2].x;
+    umma::fence_proxy_async_smem();
+  }
   __syncthreads();
+  if (S > 1) {
+    if (tid < S && tid != rank)
+      asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                       mapa_u32(umma::smem_u32(got + rank * per * 128), tid)),
+                   "r"(umma::smem_u32(sent + tid * per * 128)), "r"(per * 512), "r"(mapa_u32(umma::smem_u32(landed), tid))
+                   : "memory");
+    ok = wait_cluster(landed, 0, abort_flag);
+    if (!ok) {                                                // (and nothing lands behind this CTA's end)
+      raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
+      (void)umma::mbar_wait(landed, 0, 100000000ull);
+    }
+  }
+  // this rank's columns (rows of out), four neighbouring columns of out a thread
+  for (int e = tid; e < per * 32; e += C::THREADS) {
+    const int c = e >> 5, l = 4 * (e & 31), m = m0 + rank * per + c, n = n0 + l;
+    if ((S > 1 && !ok) || m >= p.a.M || n >= p.a.N) continue;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int r = 0; r < S; ++r) {
+      const float4 x = *reinterpret_cast<const float4*>(r == rank ? sent + (rank * per + c) * 128 + l : got + (r * per + c) * 128 + l);
+      y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+    }
+    store_row4(p.a, m, n, y);
+  }
+  // the copies out of this CTA have arrived when their readers are here
+  umma::fence_before_sync();
+  if (S > 1) {
+    __syncwarp();
+    cluster_arrive_relaxed();                                 // (a release would wait for the stores of out)
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
   umma::fence_after_sync();
   if (warp == 1) umma::tmem_dealloc(tmem, C::TCOLS);
 }
@@ -640,15 +701,14 @@ static cudaError_t launch_few(MatmulParams& p, cudaStream_t st) {
   p.tiles_n = (p.a.N + 127) / 128;
   if (!make_codes_map(&p.ta, p.a.a, p.a.M, p.a.K, MT) || !make_codes_map(&p.tb, p.a.b, p.a.N, p.a.K, 128)) return cudaErrorInvalidValue;
   const int64_t units = (int64_t)p.tiles_m * p.tiles_n;
-  int64_t S = sm_count() / units;
-  S = S < 1 ? 1 : S > 8 ? 8 : S;
-  if (S > p.kb) S = p.kb;
+  int S = 1;                                                  // shares while every CTA runs at once
+  while (S < 8 && 2 * S * units <= MfCfg<MT>::CTAS * sm_count() && 2 * S <= p.kb) S *= 2;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)S;
+  attr.val.clusterDim.x = S;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.tiles_n * S), p.tiles_m);
+  cfg.gridDim = dim3(p.tiles_n * S, p.tiles_m);
   cfg.blockDim = dim3(MfCfg<MT>::THREADS);
   cfg.dynamicSmemBytes = MfCfg<MT>::BYTES;
   cfg.stream = st;
