@@ -591,13 +591,14 @@ def fp8kv_tree_accept(caches, parents: torch.Tensor, tokens: torch.Tensor, choic
     n, B, M, dev, i32, i64 = parents.numel(), seq_lens.numel(), int(max_path), torch.cuda.current_device(), torch.int32, torch.int64
     caches = list(caches)
     for c in caches:
-        _current(c)
+        if c.k.get_device() != dev:
+            raise ValueError(f"cache: on {c.k.device}, but the current device is {dev}")
     if path is None or accepted is None or next_tokens is None or new_lens is None:
         with _on(stream):
             def new(t, shape, dtype=torch.int32):
                 return torch.empty(shape, dtype=dtype, device=parents.device) if t is None else t
             path, accepted, next_tokens, new_lens = new(path, (B, M)), new(accepted, B), new(next_tokens, B, i64), new(new_lens, B)
-    refs = (ctypes.POINTER(CacheStruct) * len(caches))(*[ctypes.pointer(c._struct) for c in caches])
+    refs = (ctypes.c_void_p * len(caches))(*[ctypes.addressof(c._struct) for c in caches])
     _check(get_lib().fp8kv_tree_accept(
         refs, len(caches), _here(parents, i32, "parents", dev, (n,)), _here(tokens, i64, "tokens", dev, (n,)),
         _here(choices, i64, "choices", dev, (n,)), _here(cu_new, i32, "cu_new", dev, (B + 1,)), _here(seq_lens, i32, "seq_lens", dev, (B,)),

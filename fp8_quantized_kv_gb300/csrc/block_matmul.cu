@@ -17,10 +17,11 @@ namespace fp8kv {
 constexpr int kMmBlock = 128;            // elements of a block of K: one 128-byte swizzled row
 
 struct MatmulParams {
-  CUtensorMap ta, tb;
+  CUtensorMap ta, tb, to;
   MatmulArgs a;
   int kb;                                // blocks of K
   int tiles_m, tiles_n;
+  int bulk_out;                          // rows of out start on 16 bytes: stored by TMA (map `to`)
 };
 
 // Waits for this thread's TMEM loads; the values are named, so that nothing that
@@ -118,6 +119,74 @@ __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.a
 template <int N>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
 
+// A warp's 32 rows of out from row m0 on, HC columns from n0 on (lane: row), staged in
+// `buf` (8 KB, two boxes of 32 rows x 128 bytes, swizzled) and stored by TMA, which
+// cuts what lies outside.  (Stored by the threads, 16 bytes of 32 rows an
+// instruction, a tile's end took 2.5 us.)  The warp goes on while the stores run.
+template <int HC>
+__device__ __forceinline__ void store_rows(const MatmulParams& p, uint8_t* buf, int lane, int m0, int n0, float2* acc) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");     // the last stores have read the buffer
+  __syncwarp();
+  if (p.a.bias != nullptr) {                                  // (in the buffer for as long as it is added)
+    float* b = reinterpret_cast<float*>(buf);
+#pragma unroll
+    for (int c = 0; c < HC / 32; ++c) b[32 * c + lane] = n0 + 32 * c + lane < p.a.N ? p.a.bias[n0 + 32 * c + lane] : 0.f;
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < HC / 4; ++c) {
+      const float4 x = reinterpret_cast<const float4*>(b)[c];
+      acc[2 * c].x += x.x; acc[2 * c].y += x.y; acc[2 * c + 1].x += x.z; acc[2 * c + 1].y += x.w;
+    }
+    __syncwarp();
+  }
+  auto put = [&](int box, int chunk, uint4 v) { *reinterpret_cast<uint4*>(buf + box * 4096 + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v; };
+  auto send = [&](int box, int n) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
+                     reinterpret_cast<uint64_t>(&p.to)),
+                 "r"(n), "r"(m0), "r"(umma::smem_u32(buf + box * 4096))
+                 : "memory");
+  };
+  if (!p.a.out_f32) {
+#pragma unroll
+    for (int c = 0; c < HC / 8; ++c) {
+      __nv_bfloat162 h[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) h[u] = __floats2bfloat162_rn(acc[4 * c + u].x, acc[4 * c + u].y);
+      put(c / 8, c % 8, *reinterpret_cast<const uint4*>(h));
+    }
+    umma::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && m0 < p.a.M) {
+#pragma unroll
+      for (int b = 0; b < HC / 64; ++b)
+        if (n0 + 64 * b < p.a.N) send(b, n0 + 64 * b);
+      asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < HC / 64; ++q) {                       // two boxes of 32 columns at a time
+      if (q > 0) {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+        __syncwarp();
+      }
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float2 x = acc[32 * q + 2 * c], y = acc[32 * q + 2 * c + 1];
+        const float4 v = make_float4(x.x, x.y, y.x, y.y);
+        put(c / 8, c % 8, *reinterpret_cast<const uint4*>(&v));
+      }
+      umma::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && m0 < p.a.M) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          if (n0 + 64 * q + 32 * b < p.a.N) send(b, n0 + 64 * q + 32 * b);
+        asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------- many rows of a --
 // A pair of CTAs (cta_group::2) owns tiles of 256 rows of a x BN rows of b, one after
 // the other: each CTA loads and keeps 128 rows of a and half of b's, the products read
@@ -129,10 +198,12 @@ __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.a
 template <int BN>
 struct MmCfg {
   static constexpr int STAGE = (128 + BN / 2) * kMmBlock;     // of one CTA
-  static constexpr int NS = BN == 256 ? 6 : 8;
+  static constexpr int NS = BN == 256 ? 5 : 6;
   static constexpr int NB = 512 / BN;                         // TMEM buffers
   static constexpr int THREADS = 384;
-  static constexpr int BYTES = 1024 + NS * STAGE + 512;
+  static constexpr int OUT = 8 * 8192;                        // staged output, 8 KB a warp of sums
+  static constexpr int BYTES = 1024 + NS * STAGE + OUT + 512;
+  static_assert(BYTES <= 227 * 1024, "shared memory of an SM");
 };
 
 namespace pair {
@@ -180,7 +251,8 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
   using C = MmCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::NS * C::STAGE);
+  uint8_t* staged = smem + C::NS * C::STAGE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staged + C::OUT);
   uint64_t* full = bars;                                      // [NS] first CTA: both CTAs' blocks landed
   uint64_t* empty = full + C::NS;                             // [NS] products have read them
   uint64_t* d_full = empty + C::NS;                           // [NB] a block's sums are in TMEM
@@ -324,10 +396,15 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
                                          acc[16 * c + u]);
         }
       }
-      if (!ok || m >= p.a.M) continue;
+      if (!ok) continue;
+      if (p.bulk_out) {
+        store_rows<HC>(p, staged + (warp - 4) * 8192, lane, m - lane, n0, acc);
+      } else if (m < p.a.M) {
 #pragma unroll
-      for (int c = 0; c < HC / 64; ++c) store_row64(p.a, m, n0 + 64 * c, acc + 32 * c);
+        for (int c = 0; c < HC / 64; ++c) store_row64(p.a, m, n0 + 64 * c, acc + 32 * c);
+      }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
     if (!ok && lane == 0) raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
   }
   // neither CTA's shared memory or TMEM is in use by the other any more (nothing is
@@ -668,6 +745,19 @@ static bool make_codes_map(CUtensorMap* m, const uint8_t* base, int rows, int K,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// out viewed as [rows][N], boxes of 32 rows x 128 bytes.
+static bool make_out_map(CUtensorMap* m, const MatmulArgs& a) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int size = a.out_f32 ? 4 : 2;
+  const cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.M};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.N * size};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / size), 32}, estr[2] = {1, 1};
+  return fn(m, a.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int BN>
 static cudaError_t launch_pair(MatmulParams& p, cudaStream_t st) {
   using C = MmCfg<BN>;
@@ -676,6 +766,8 @@ static cudaError_t launch_pair(MatmulParams& p, cudaStream_t st) {
   p.tiles_m = (p.a.M + 255) / 256;
   p.tiles_n = (p.a.N + BN - 1) / BN;
   if (!make_codes_map(&p.ta, p.a.a, p.a.M, p.a.K, 128) || !make_codes_map(&p.tb, p.a.b, p.a.N, p.a.K, BN / 2)) return cudaErrorInvalidValue;
+  p.bulk_out = p.a.N % (p.a.out_f32 ? 4 : 8) == 0;
+  if (p.bulk_out && !make_out_map(&p.to, p.a)) return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, pairs = sm_count() / 2;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;

@@ -11,18 +11,18 @@ namespace fp8kv {
 // before their children, so the walk ends) and writes its words from the highest
 // down: ancestors only get lower.  Latency bounds it: offsets, parents, then a
 // step of the walk every 30 cycles or so.
-constexpr int kTreeThreads = 128;
+constexpr int kTreeThreads = 256;
 
 __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTablesParams p) {
   __shared__ int16_t up[kTreeMaxNodes];
   const int tid = threadIdx.x;
   if (blockIdx.x >= p.batch) {                     // rows that belong to no sequence
-    const int first = p.cu[0], end = p.cu[p.batch];
-    for (int64_t i = (int64_t)(blockIdx.x - p.batch) * kTreeThreads + tid; i < p.rows;
+    const int first = min(max(p.cu[0], 0), p.rows), end = min(max(p.cu[p.batch], first), p.rows);
+    for (int64_t i = (int64_t)(blockIdx.x - p.batch) * kTreeThreads + tid; i < first + p.rows - end;
          i += (int64_t)(gridDim.x - p.batch) * kTreeThreads) {
-      if (i >= first && i < end) continue;
-      p.pos[i] = -1;
-      for (int w = 0; w < p.words; ++w) p.masks[i * p.words + w] = 0;
+      const int64_t r = i < first ? i : end + (i - first);
+      p.pos[r] = -1;
+      for (int w = 0; w < p.words; ++w) p.masks[r * p.words + w] = 0;
     }
     return;
   }
