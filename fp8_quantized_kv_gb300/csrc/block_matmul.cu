@@ -533,13 +533,13 @@ struct MfCfg {
   static constexpr int STAGE = (128 + MT) * kMmBlock;
   static constexpr int CTAS = MT <= 64 ? 2 : 1;               // of an SM
   static constexpr int NB = 256 * (3 - CTAS) / MT < 8 ? 256 * (3 - CTAS) / MT : 8;      // TMEM buffers
-  static constexpr int NS = MT == 128 ? 6 : MT == 64 ? 4 : 5;
+  static constexpr int NS = MT == 128 ? 4 : MT == 64 ? 3 : 4;
   static constexpr int SK = 16;                               // blocks whose scales are held
   static constexpr int SUMS = MT * 128 * 4;                   // a tile's sums, as they are sent
-  static constexpr int BYTES = 1024 + NS * STAGE + SK * MT * 4 + 512;
+  static constexpr int BYTES = 1024 + NS * STAGE + SUMS + SK * MT * 4 + 512;
   static constexpr int TCOLS = NB * MT;
   static constexpr int THREADS = 192;
-  static_assert(2 * SUMS <= NS * STAGE, "sent and received sums take the ring's place");
+  static_assert(SUMS <= NS * STAGE, "sums to send take the ring's place");
   static_assert(CTAS * (BYTES + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
@@ -548,7 +548,9 @@ __global__ void __launch_bounds__(MfCfg<MT>::THREADS, MfCfg<MT>::CTAS) block_mat
   using C = MfCfg<MT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* scol = reinterpret_cast<float*>(smem + C::NS * C::STAGE);       // [SK][MT] scales of the columns
+  float* sent = reinterpret_cast<float*>(smem);               // sums, [column][row of b], in the ring's place
+  float* got = reinterpret_cast<float*>(smem + C::NS * C::STAGE);        // received, [rank][own column][row of b]
+  float* scol = got + C::SUMS / 4;                            // [SK][MT] scales of the columns
   uint64_t* bars = reinterpret_cast<uint64_t*>(scol + C::SK * MT);
   uint64_t* full = bars;
   uint64_t* empty = full + C::NS;
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(MfCfg<MT>::THREADS, MfCfg<MT>::CTAS) block_mat
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int S;
   asm("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(S));
-  const int rank = (int)cluster_rank(), per = MT / S;         // columns of a rank (S is 1, 2, 4 or 8)
+  const int rank = (int)cluster_rank(), per = MT / S;         // columns of a rank (S is 1, 2 or 4)
   const int n0 = blockIdx.x / S * 128, m0 = blockIdx.y * MT;
   const int j0 = (int)((int64_t)p.kb * rank / S), j1 = (int)((int64_t)p.kb * (rank + 1) / S);
   auto load = [&](int it) {                                   // block j0 + it
@@ -588,6 +590,7 @@ __global__ void __launch_bounds__(MfCfg<MT>::THREADS, MfCfg<MT>::CTAS) block_mat
   umma::fence_before_sync();
   __syncthreads();
   umma::fence_after_sync();
+  cluster_arrive_relaxed();                                   // every CTA runs, its barriers ready, before sums are sent to it
   const uint32_t tmem = *tslot;
   float2 acc[MT / 2];
   bool ok = true;
@@ -676,17 +679,8 @@ __global__ void __launch_bounds__(MfCfg<MT>::THREADS, MfCfg<MT>::CTAS) block_mat
       }
     }
   }
-  // Every CTA of the cluster is done with its ring: sums to send go to its front,
-  // [column][row of b], those received behind them, [rank][own column][row of b].
-  __syncwarp();
-  if (S > 1) {
-    asm volatile("barrier.cluster.arrive.release;\n" ::: "memory");
-    cluster_wait();
-  } else {
-    __syncthreads();
-  }
-  float* sent = reinterpret_cast<float*>(smem);
-  float* got = sent + MT * 128;
+  // every product is complete and every copy has landed: the sums take the ring's place
+  __syncthreads();
   if (warp >= 2) {
     const int row = 32 * (warp & 3) + lane;                   // of b, TMEM lane
     if (!ok && lane == 0) raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
@@ -694,6 +688,7 @@ __global__ void __launch_bounds__(MfCfg<MT>::THREADS, MfCfg<MT>::CTAS) block_mat
     for (int c = 0; c < MT; ++c) sent[c * 128 + row] = !ok ? NAN : c & 1 ? acc[c / 2].y : acc[c / 2].x;
     umma::fence_proxy_async_smem();
   }
+  cluster_wait();
   __syncthreads();
   if (S > 1) {
     if (tid < S && tid != rank)
@@ -794,7 +789,7 @@ static cudaError_t launch_few(MatmulParams& p, cudaStream_t st) {
   if (!make_codes_map(&p.ta, p.a.a, p.a.M, p.a.K, MT) || !make_codes_map(&p.tb, p.a.b, p.a.N, p.a.K, 128)) return cudaErrorInvalidValue;
   const int64_t units = (int64_t)p.tiles_m * p.tiles_n;
   int S = 1;                                                  // shares while every CTA runs at once
-  while (S < 8 && 2 * S * units <= MfCfg<MT>::CTAS * sm_count() && 2 * S <= p.kb) S *= 2;
+  while (S < 4 && 2 * S * units <= MfCfg<MT>::CTAS * sm_count() && 2 * S <= p.kb) S *= 2;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = S;
