@@ -54,8 +54,13 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // shares of 512 keys or longer.  Warp-level kernel: three an SM (by their
 // registers) and 128 keys (32-64 x 8 of 2 sequences of 2K-4K tokens: 36 us in 4
 // shares, 31 us in 6, 37 us in 9, past one wave).
+// Trees: the same, with shares of 1,024 keys or longer on tcgen05 (64 nodes x 4 heads,
+// 8 KV heads, 4 sequences of 8,000 tokens: 138 us whole, 71 in 4 shares, 91 in 5, past
+// one wave; under a window of 4,096 35 us in 4, 40 in 6).  Where whole tiles fill two
+// thirds of a wave or less and there is no window, lengths can differ, and halves even
+// them out (33-64 x 7, 4 KV heads, 16 sequences of 2K-8K: 180 us whole, 150 in 2 or 3).
 fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int window, int sinks, int num_splits,
-                        int kernel, ChunkPlan* plan) {
+                        int kernel, bool tree, ChunkPlan* plan) {
   if (total_q < 0 || q_heads <= 0 || q_heads % c->kv_heads != 0 || window < 0 || sinks < 0 || num_splits < 0)
     return FP8KV_ERR_INVALID_ARG;
   if (kernel != FP8KV_KERNEL_AUTO && kernel != FP8KV_KERNEL_WARP_MMA && kernel != FP8KV_KERNEL_TENSOR_CORES)
@@ -83,12 +88,15 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   if (want == 0) {
     // tiles if every sequence had the average number of queries, or, if that is
     // not a whole number, as many more or fewer of them as it says
-    const int64_t T = plan->tile_tokens, even_q = (total_q / B + T - 1) / T * B, some_q = (total_q + T - 1) / T;
+    // (trees are rarely of one size: half a tile more each)
+    const int64_t T = plan->tile_tokens, even_q = (total_q / B + T - 1) / T * B;
+    const int64_t some_q = tree ? total_q / T + B / 2 : (total_q + T - 1) / T;
     const int64_t units = (total_q % B == 0 ? even_q : some_q > B ? some_q : B) * c->kv_heads;
     const int64_t sms = sm_count();
     if (plan->tile_rows > 16) {
       want = units > 0 ? (tc ? 2 : 3) * sms / units : 1;
-      const int64_t most = kv_tiles / (tc ? 8 : 2);
+      if (tree && tc && window == 0 && want == 1 && 14 * units <= 10 * 2 * sms) want = 2;
+      const int64_t most = kv_tiles / (tc ? (tree ? 16 : 8) : 2);
       if (want > most) want = most;
     } else if (units > 0) {
       const bool wide = c->head_dim == 128 && c->dtype == FP8KV_K16V16;
@@ -111,6 +119,11 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   return FP8KV_OK;
 }
 
+// The fp32 partials (O, m, l) of every (row, split); nothing without splits.
+size_t share_bytes(const fp8kv_cache* c, int64_t total_q, int q_heads, int splits) {
+  return splits <= 1 ? 0 : (size_t)total_q * q_heads * splits * ((size_t)c->head_dim + 2) * sizeof(float);
+}
+
 // The chunk and the tree call: causal without masks (null), else over trees.
 struct TreeArgs { const uint32_t* masks; const int32_t* pos; int32_t words; };
 
@@ -122,7 +135,7 @@ fp8kv_status run_chunk(const void* q, const fp8kv_cache* cache, const int32_t* c
   fp8kv_status st = check_cache(cache, &p.c);
   if (st != FP8KV_OK) return st;
   ChunkPlan plan;
-  st = plan_chunk(cache, total_q, q_heads, window, sinks, num_splits, kernel, &plan);
+  st = plan_chunk(cache, total_q, q_heads, window, sinks, num_splits, kernel, tree != nullptr, &plan);
   if (st != FP8KV_OK) return st;
   if (out_dtype != FP8KV_OUT_BF16 && out_dtype != FP8KV_OUT_F32) return FP8KV_ERR_INVALID_ARG;
   if (!std::isfinite(sm_scale)) return FP8KV_ERR_INVALID_ARG;
@@ -137,7 +150,7 @@ fp8kv_status run_chunk(const void* q, const fp8kv_cache* cache, const int32_t* c
   const int64_t rows = total_q * q_heads;
   const size_t values = (size_t)rows * cache->head_dim;
   if (overlap({q, 2 * values}, {out, (out_dtype == FP8KV_OUT_F32 ? 4 : 2) * values})) return FP8KV_ERR_INVALID_ARG;
-  const size_t need = fp8kv_chunk_workspace_bytes(cache, total_q, q_heads, window, sinks, num_splits, kernel);
+  const size_t need = share_bytes(cache, total_q, q_heads, plan.splits);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FP8KV_ERR_WORKSPACE;
   if (need > 0 && misaligned(workspace, 16)) return FP8KV_ERR_INVALID_ARG;
   const Range result = {out, (out_dtype == FP8KV_OUT_F32 ? 4 : 2) * values};
@@ -320,15 +333,13 @@ int32_t fp8kv_chunk_num_splits(const fp8kv_cache* cache, int64_t total_q, int32_
   CacheView view;
   ChunkPlan plan;
   if (check_cache(cache, &view) != FP8KV_OK) return 0;
-  if (plan_chunk(cache, total_q, q_heads, window, sinks, num_splits, kernel, &plan) != FP8KV_OK) return 0;
+  if (plan_chunk(cache, total_q, q_heads, window, sinks, num_splits, kernel, false, &plan) != FP8KV_OK) return 0;
   return plan.splits;
 }
 
 size_t fp8kv_chunk_workspace_bytes(const fp8kv_cache* cache, int64_t total_q, int32_t q_heads, int32_t window,
                                    int32_t sinks, int32_t num_splits, int32_t kernel) {
-  const int S = fp8kv_chunk_num_splits(cache, total_q, q_heads, window, sinks, num_splits, kernel);
-  if (S <= 1) return 0;
-  return (size_t)total_q * q_heads * S * ((size_t)cache->head_dim + 2) * sizeof(float);
+  return share_bytes(cache, total_q, q_heads, fp8kv_chunk_num_splits(cache, total_q, q_heads, window, sinks, num_splits, kernel));
 }
 
 fp8kv_status fp8kv_chunk_attention(const void* q, const fp8kv_cache* cache, const int32_t* cu_q,
@@ -342,7 +353,11 @@ fp8kv_status fp8kv_chunk_attention(const void* q, const fp8kv_cache* cache, cons
 
 size_t fp8kv_tree_workspace_bytes(const fp8kv_cache* cache, int64_t total_q, int32_t q_heads, int32_t window,
                                   int32_t sinks, int32_t num_splits, int32_t kernel) {
-  return fp8kv_chunk_workspace_bytes(cache, total_q, q_heads, window, sinks, num_splits, kernel);
+  CacheView view;
+  ChunkPlan plan;
+  if (check_cache(cache, &view) != FP8KV_OK) return 0;
+  if (plan_chunk(cache, total_q, q_heads, window, sinks, num_splits, kernel, true, &plan) != FP8KV_OK) return 0;
+  return share_bytes(cache, total_q, q_heads, plan.splits);
 }
 
 fp8kv_status fp8kv_tree_attention(const void* q, const fp8kv_cache* cache, const int32_t* cu_q,

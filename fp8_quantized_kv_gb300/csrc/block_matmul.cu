@@ -531,9 +531,9 @@ __global__ void __launch_bounds__(32 * kMwWarps, 3) block_matmul_warp(const Matm
 template <int MT>
 struct MfCfg {
   static constexpr int STAGE = (128 + MT) * kMmBlock;
-  static constexpr int CTAS = MT <= 64 ? 2 : 1;               // of an SM
-  static constexpr int NB = 256 * (3 - CTAS) / MT < 8 ? 256 * (3 - CTAS) / MT : 8;      // TMEM buffers
-  static constexpr int NS = MT == 128 ? 4 : MT == 64 ? 3 : 4;
+  static constexpr int CTAS = 2;                              // of an SM
+  static constexpr int NB = 256 / MT;                         // TMEM buffers
+  static constexpr int NS = MT == 64 ? 3 : 4;
   static constexpr int SK = 16;                               // blocks whose scales are held
   static constexpr int SUMS = MT * 128 * 4;                   // a tile's sums, as they are sent
   static constexpr int BYTES = 1024 + NS * STAGE + SUMS + SK * MT * 4 + 512;
@@ -817,8 +817,7 @@ cudaError_t launch_block_matmul(const MatmulArgs& a, cudaStream_t st) {
     return cudaGetLastError();
   }
   if (a.M <= 32) return launch_few<32>(p, st);
-  if (a.M <= 64) return launch_few<64>(p, st);
-  if (a.M <= 128) return launch_few<128>(p, st);
+  if (a.M <= 128) return launch_few<64>(p, st);
   const int64_t wide = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
   return 2 * wide > sm_count() / 2 ? launch_pair<256>(p, st) : launch_pair<128>(p, st);
 }
