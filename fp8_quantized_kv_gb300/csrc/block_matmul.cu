@@ -353,18 +353,8 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
     const int part = (warp - 4) >> 2, row_in = 32 * (warp & 3) + lane;
     const uint32_t base = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + HC * part;
     const uint32_t free0 = mapa_u32(umma::smem_u32(d_free), 0);
-    const int blocks = (tiles - first + step - 1) / step * p.kb;             // of all this pair's tiles
     int it = 0;
     bool ok = true, ready = false;
-    uint32_t r[2][32];
-    // the first piece of block i, behind its barrier (`ready`: found complete before)
-    auto start = [&](int i) {
-      if (!ready) ok = wait_fast(&d_full[i % C::NB], (i / C::NB) & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
-      umma::fence_after_sync();
-      tmem_ld32_nowait(base + BN * (i % C::NB), r[0]);
-    };
-    start(0);
     for (int tile = first; ok && tile < tiles; tile += step) {
       const int m = tile % p.tiles_m * 256 + 128 * rank + row_in, n0 = tile / p.tiles_m * BN + HC * part;
       const float* sa = p.a.sa + (int64_t)min(m, p.a.M - 1) * p.kb;
@@ -373,28 +363,41 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
 #pragma unroll
       for (int c = 0; c < HC / 2; ++c) acc[c] = make_float2(0.f, 0.f);
       float next_a = sa[0], next_b = sb[0];
-      for (int j = 0; ok && j < p.kb; ++j, ++it) {
+      for (int j = 0; j < p.kb; ++j, ++it) {
         const int d = it % C::NB, next = it + 1;
+        const uint32_t at = base + BN * d;
+        if (!ready) ok = wait_fast(&d_full[d], (it / C::NB) & 1, abort_flag);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        umma::fence_after_sync();
+        // The buffer is handed back as soon as it is read: two pieces of 32 columns are
+        // on their way at once, and the last two are multiplied behind the hand-back.
+        uint32_t r[2][32];
+        tmem_ld32_nowait(at, r[0]);
+        tmem_ld32_nowait(at + 32, r[1]);
         const float2 s2 = make_float2(next_a * next_b, next_a * next_b);
         if (j + 1 < p.kb) { next_a = sa[j + 1]; next_b = sb[j + 1]; }
-        // a piece of 32 columns is multiplied while the next is on its way
-#pragma unroll
-        for (int c = 0; c < PC; ++c) {
-          tmem_wait_ld32(r[c & 1]);
-          if (c == PC - 2) ready = umma::mbar_test(&d_full[next % C::NB], (next / C::NB) & 1);
-          if (c < PC - 1) {
-            tmem_ld32_nowait(base + BN * d + 32 * (c + 1), r[(c + 1) & 1]);
-          } else {
-            umma::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) pair::arrive_remote(free0 + 8 * d);
-            if (next < blocks) start(next);
-          }
+        auto sum = [&](int c) {
 #pragma unroll
           for (int u = 0; u < 16; ++u)
             acc[16 * c + u] = __ffma2_rn(make_float2(__uint_as_float(r[c & 1][2 * u]), __uint_as_float(r[c & 1][2 * u + 1])), s2,
                                          acc[16 * c + u]);
+        };
+        tmem_wait_ld32(r[0]);
+        tmem_wait_ld32(r[1]);
+        if constexpr (PC == 4) {
+          sum(0);
+          tmem_ld32_nowait(at + 64, r[0]);
+          sum(1);
+          tmem_ld32_nowait(at + 96, r[1]);
+          tmem_wait_ld32(r[0]);
+          tmem_wait_ld32(r[1]);
         }
+        umma::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) pair::arrive_remote(free0 + 8 * d);
+        ready = umma::mbar_test(&d_full[next % C::NB], (next / C::NB) & 1);
+        sum(PC - 2);
+        sum(PC - 1);
       }
       if (!ok) continue;
       if (p.bulk_out) {
