@@ -7,8 +7,13 @@
 // The scales change with every block of K, so the tensor core sums one block at a
 // time (four kind::f8f6f4 products of 32 elements into a fresh TMEM buffer) and
 // fp32 registers sum the blocks: acc = fma(d, sa sb, acc), one rounding of the pair
-// of scales and one of each sum.  Two buffers, so that the tensor core fills one
-// while the other is read.
+// of scales and one of each sum.  While one buffer is read the tensor core fills
+// another.  Three kernels: a few rows of a are bound by the bytes of b (fragments
+// straight from memory, or shares of K in clusters), many by the products and by the
+// hand-over of each block's sums (pairs of CTAs).  Measured on one GB300, device time:
+// 1 x 2560 x 2048 2.5 us; 64 x 6144 x 4096 10.8 us (25 MB: 2.4 TB/s; 4.9 TB/s at 32,768
+// columns); 997 x 4608 x 3584 18.0 us (1,820 TFLOP/s); 7940 x 6144 x 4096 170 us (2,350
+// TFLOP/s, 1.23 times the measured bf16 rate); 8192^3 412 us (2,670 TFLOP/s).
 #include "params.cuh"
 #include "tc_common.cuh"
 
@@ -24,8 +29,8 @@ struct MatmulParams {
   int bulk_out;                          // rows of out start on 16 bytes: stored by TMA (map `to`)
 };
 
-// Waits for this thread's TMEM loads; the values are named, so that nothing that
-// uses them moves in front.
+// 32 columns of TMEM into registers, and the wait for this thread's loads: the values
+// are named there, so that nothing that uses them moves in front.
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -36,12 +41,6 @@ __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t (&r)[3
 __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
 }
@@ -195,6 +194,21 @@ __device__ __forceinline__ void store_rows(const MatmulParams& p, uint8_t* buf, 
 //               CTA's barrier
 //   warp 1      TMEM owner; the first CTA's issues the products
 //   warps 4-11  sums: a thread keeps one row of the tile and half of its columns
+//
+// What bounds 256 columns: a block's products take about 640 cycles back to back, but
+// with two TMEM buffers a block also waits for half of the way round a buffer: products
+// until their sums are seen (820 cycles), reading (450), hand-back to the issuer (250).
+// On the way (997 x 4608 x 3584 and 8192^3, us):
+//   one CTA, 128 x 256, sums of a whole row's half in pieces of 32       23.5   572
+//   pairs (8192^3 without any hand-over: 302)                            21.3   461
+//   output by TMA instead of 16-byte stores of 32 rows                   18.7   430
+//   two pieces on their way at once, hand-back before the last products  18.0   425
+//   one thread each for copies and products                              18.0   412
+// Measured and not kept: sixteen warps of sums with 64 columns each (22.1, 571: twice the
+// instructions around the sums), buffers of 128 columns (26.4, 610: products of 128
+// columns take 116 cycles instead of 160 for 256), scalar sums instead of packed pairs
+// (23.6, 623), barriers tested without suspension (18.6, 437), a release at cluster scope
+// for the hand-back (36, 1150).
 template <int BN>
 struct MmCfg {
   static constexpr int STAGE = (128 + BN / 2) * kMmBlock;     // of one CTA
@@ -271,16 +285,20 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
     *abort_flag = 0;
     umma::mbar_fence_init();
   }
+  cluster_arrive_relaxed();                                   // (thread 0's barriers are initialised: fence above)
+  cluster_wait();
+  // TMEM is there before it is used, not before the first copies
+  uint32_t tmem = 0;
   if (warp == 1) {
     pair::tmem_alloc(tslot, 512);
     pair::tmem_relinquish();
+    umma::fence_before_sync();
   }
-  umma::fence_before_sync();
-  __syncthreads();
-  cluster_arrive_relaxed();                                   // (barriers initialised: fence above)
-  cluster_wait();
-  umma::fence_after_sync();
-  const uint32_t tmem = *tslot;
+  if (warp == 1 || warp >= 4) {
+    asm volatile("bar.sync 1, 288;\n" ::: "memory");
+    umma::fence_after_sync();
+    tmem = *tslot;
+  }
 
   if (warp < 4) {
     regs_dec<40>();
@@ -337,7 +355,6 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
           }
         }
       }
-      __syncwarp();
       // all issued products complete before TMEM is released
       __syncwarp();
       if (elect_one()) pair::mma_commit(drained);
@@ -422,7 +439,9 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
 // matrix fragments straight from memory (mma.sync, b's rows on the long side, a's
 // as the eight columns; NT sets of those).  The order of a dot product's elements is
 // free, so a lane takes 16 bytes that lie together, of b and of a alike.  The eight
-// warps of a CTA join in shared memory in their order.
+// warps of a CTA join in shared memory in their order.  8 x 6144 x 4096 take 6.7 us (3.8
+// TB/s): three CTAs an SM, two blocks of K in flight a warp; with four blocks and fewer
+// CTAs, or CTAs of four warps, 7 to 8.4 us.
 constexpr int kMwRows = 16, kMwWarps = 8;
 
 __device__ __forceinline__ void mma16832_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -438,7 +457,7 @@ __device__ __forceinline__ uint4 load_once(const uint8_t* p) {
 }
 
 template <int NT>
-__global__ void __launch_bounds__(32 * kMwWarps, 3) block_matmul_warp(const MatmulArgs a, int kb) {
+__global__ void __launch_bounds__(32 * kMwWarps, NT == 1 ? 3 : 2) block_matmul_warp(const MatmulArgs a, int kb) {
   constexpr int U = NT == 1 ? 2 : 1;                          // blocks of K loaded at once
   __shared__ float part[kMwWarps][8 * NT][kMwRows + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
@@ -526,7 +545,11 @@ __global__ void __launch_bounds__(32 * kMwWarps, 3) block_matmul_warp(const Matm
 // share of the blocks of K; the CTAs of a cluster hold the shares of one tile.  Each
 // sums its blocks in registers, copies every column's sums to the CTA that owns the
 // column (one bulk copy a CTA through distributed shared memory), and the owner adds
-// the shares in rank order.
+// the shares in rank order.  Of the 10.8 us of 64 x 6144 x 4096 about 2.5 pass until the
+// first blocks land, 4.3 with them (25 MB at the measured copy rate: 3.9) and 3 with the
+// join and the stores.  One CTA an SM with a deeper ring is slower (12.0 us), and so are
+// eight shares (64 x 2560 x 2048: 8.1 us, 6.7 in four) and clusters of three (a cluster
+// takes whole pairs of SMs: 26 us).
 template <int MT>
 struct MfCfg {
   static constexpr int STAGE = (128 + MT) * kMmBlock;
@@ -804,18 +827,30 @@ static cudaError_t launch_few(MatmulParams& p, cudaStream_t st) {
   return r;
 }
 
+// Which kernel, by the rows of a (times in us on one GB300, inputs from memory):
+//   up to 8      fragments from memory (8 x 6144 x 4096: 6.7, in clusters 8.5; 8 x 1000 x
+//                2048: 2.2 and 4.9; from 20,000 columns on clusters are 8 % faster)
+//   up to 16     the same while the strips of 16 columns fill the SMs once (12 x 4608 x
+//                3584: 6.4, in clusters 7.5), beyond it clusters (16 x 6144 x 4096: 8.9, 10.7)
+//   up to 64     clusters (64 x 6144 x 4096: 10.8, on pairs 12.6)
+//   up to 128    clusters while four shares of every tile run at once (100 x 4608 x 3584:
+//                10.7, on pairs 11.7), else pairs (128 x 6144 x 4096: 12.9, 14.9)
+//   more         pairs, 128 columns a tile while those fit the SMs at once (200 x 6144 x
+//                4096: 12.9, 256 columns 20; 512 x 2560 x 2048: 8.1 and 12.3), else 256
+//                (512 x 6144 x 4096: 19.7, 128 columns 26.7; 2000 x 2560 x 2048: 21.1, 21.7)
 cudaError_t launch_block_matmul(const MatmulArgs& a, cudaStream_t st) {
   MatmulParams p;
   p.a = a;
   p.kb = (a.K + kMmBlock - 1) / kMmBlock;
-  if (a.M <= 16) {
-    const unsigned grid = (unsigned)((a.N + kMwRows - 1) / kMwRows);
-    if (a.M <= 8) block_matmul_warp<1><<<grid, 32 * kMwWarps, 0, st>>>(a, p.kb);
-    else block_matmul_warp<2><<<grid, 32 * kMwWarps, 0, st>>>(a, p.kb);
+  const int64_t strips = ((int64_t)a.N + kMwRows - 1) / kMwRows;
+  if (a.M <= 8 || (a.M <= 16 && strips <= 2 * sm_count())) {
+    if (a.M <= 8) block_matmul_warp<1><<<(unsigned)strips, 32 * kMwWarps, 0, st>>>(a, p.kb);
+    else block_matmul_warp<2><<<(unsigned)strips, 32 * kMwWarps, 0, st>>>(a, p.kb);
     return cudaGetLastError();
   }
   if (a.M <= 32) return launch_few<32>(p, st);
-  if (a.M <= 128) return launch_few<64>(p, st);
+  const int64_t units = 2 * (((int64_t)a.N + 127) / 128);
+  if (a.M <= 64 || (a.M <= 128 && 4 * units <= 2 * sm_count())) return launch_few<64>(p, st);
   const int64_t wide = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
   return 2 * wide > sm_count() / 2 ? launch_pair<256>(p, st) : launch_pair<128>(p, st);
 }

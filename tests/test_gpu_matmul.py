@@ -70,9 +70,10 @@ def test_sizes(M, N, K):
     check(fk.fp8kv_block_matmul(a, sa, b, sb, bias=bias), a, sa, b, sb, bias)
 
 
-@pytest.mark.parametrize("M,N,K", [(640, 4608, 896), (1500, 2560, 2048), (997, 4609, 272), (2100, 1111, 512), (5000, 6144, 384)])
+@pytest.mark.parametrize("M,N,K", [(640, 4608, 896), (1500, 2560, 2048), (997, 4609, 272), (2100, 1111, 512), (5000, 6144, 384),
+                                   (12, 5003, 272), (100, 6144, 272), (128, 9001, 128), (600, 2568, 16)])
 def test_many_rows(M, N, K):
-    """Several tiles a CTA, ragged at both ends."""
+    """Several tiles a CTA, ragged at both ends; few rows beside many columns."""
     a, sa, b, sb, bias = make(M, N, K, seed=M, spread=8.0)
     check(fk.fp8kv_block_matmul(a, sa, b, sb, bias=bias, out_dtype=torch.float32), a, sa, b, sb, bias)
     check(fk.fp8kv_block_matmul(a, sa, b, sb), a, sa, b, sb)
@@ -91,7 +92,7 @@ def test_each_block_has_its_scales(M):
     assert fk.fp8kv_get_device_error() == 0 and torch.equal(out.double(), want)
 
 
-@pytest.mark.parametrize("M", [5, 600])
+@pytest.mark.parametrize("M", [5, 12, 50, 600])
 def test_not_finite(M):
     """NaN codes and infinite or NaN scales reach the rows and columns that they belong to, and no others."""
     N, K = 260, 384
