@@ -54,11 +54,14 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // shares of 512 keys or longer.  Warp-level kernel: three an SM (by their
 // registers) and 128 keys (32-64 x 8 of 2 sequences of 2K-4K tokens: 36 us in 4
 // shares, 31 us in 6, 37 us in 9, past one wave).
-// Trees: the same, with shares of 1,024 keys or longer on tcgen05 (64 nodes x 4 heads,
-// 8 KV heads, 4 sequences of 8,000 tokens: 138 us whole, 71 in 4 shares, 91 in 5, past
-// one wave; under a window of 4,096 35 us in 4, 40 in 6).  Where whole tiles fill two
-// thirds of a wave or less and there is no window, lengths can differ, and halves even
-// them out (33-64 x 7, 4 KV heads, 16 sequences of 2K-8K: 180 us whole, 150 in 2 or 3).
+// Trees on tcgen05: tiles see whole contexts, and two CTAs of an SM slow each other
+// down, so one CTA an SM with shares of 256 keys or longer, or two with 1,024 or
+// longer, whichever is more shares (5-31 nodes x 8 heads, 2 KV heads, 16 sequences,
+// window 1,024: 32 us whole, 26 in 2 shares, 29 in 4; of 4 sequences 32, 25 and 20;
+// 64 x 4, 8 KV heads, 4 sequences of 8,000 tokens: 138 whole, 80 in 2, 71 in 4, 91 in
+// 5, past one wave).  Where whole tiles fill seven tenths of a wave or less and there is
+// no window, lengths can differ, and halves even them out (33-64 x 7, 4 KV heads, 16
+// sequences of 2K-8K: 180 us whole, 150 in 2 or 3).
 fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int window, int sinks, int num_splits,
                         int kernel, bool tree, ChunkPlan* plan) {
   if (total_q < 0 || q_heads <= 0 || q_heads % c->kv_heads != 0 || window < 0 || sinks < 0 || num_splits < 0)
@@ -88,16 +91,24 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   if (want == 0) {
     // tiles if every sequence had the average number of queries, or, if that is
     // not a whole number, as many more or fewer of them as it says
-    // (trees are rarely of one size: half a tile more each)
+    // (trees are rarely of one size: half a tile more each, and a little over, since a
+    // wave that is just missed costs as much as a whole one)
     const int64_t T = plan->tile_tokens, even_q = (total_q / B + T - 1) / T * B;
-    const int64_t some_q = tree ? total_q / T + B / 2 : (total_q + T - 1) / T;
+    const int64_t some_q = tree ? (total_q / T + B / 2) * 21 / 20 : (total_q + T - 1) / T;
     const int64_t units = (total_q % B == 0 ? even_q : some_q > B ? some_q : B) * c->kv_heads;
     const int64_t sms = sm_count();
     if (plan->tile_rows > 16) {
-      want = units > 0 ? (tc ? 2 : 3) * sms / units : 1;
-      if (tree && tc && window == 0 && want == 1 && 14 * units <= 10 * 2 * sms) want = 2;
-      const int64_t most = kv_tiles / (tc ? (tree ? 16 : 8) : 2);
-      if (want > most) want = most;
+      auto shares = [&](int64_t held, int64_t tiles) {        // fill `held` CTAs with shares of `tiles` KV tiles or more
+        const int64_t s = units > 0 ? held / units : 1;
+        return s < kv_tiles / tiles ? s : kv_tiles / tiles;
+      };
+      if (tc && tree) {
+        want = shares(sms, 4);
+        if (shares(2 * sms, 16) > want) want = shares(2 * sms, 16);
+        if (window == 0 && want <= 1 && kv_tiles >= 32 && 14 * units <= 10 * 2 * sms) want = 2;
+      } else {
+        want = tc ? shares(2 * sms, 8) : shares(3 * sms, 2);
+      }
     } else if (units > 0) {
       const bool wide = c->head_dim == 128 && c->dtype == FP8KV_K16V16;
       const int64_t held = (plan->tile_rows == 8 && !wide ? 4 : 3) * sms, most = kv_tiles / 3;

@@ -324,8 +324,17 @@ def test_chain_is_causal():
         assert pos.tolist() == list(range(300 - n, 300)) + list(range(n))
         a = fk.fp8kv_tree_attention(q, cache, cu, lens, masks, out_dtype=torch.float32)
         b = fk.fp8kv_chunk_attention(q, cache, cu, lens, out_dtype=torch.float32)
-        # the same scores and weights; only the order of rescalings can differ
-        assert fk.fp8kv_get_device_error() == 0 and (a - b).abs().max().item() <= 1e-5
+        # Each is the definition's row up to the rounding of its weights: u sum p |v| <= u max |v|,
+        # u = 2^-11 beside e4m3 values and 2^-8 beside bf16 ones, relative to a reference that
+        # depends on the share of keys (the two calls may split them differently).  Two rows
+        # differ by twice that; fp32 sums add far less than the 1e-5 here.
+        u = 2.0 ** (-8 if cache.v.dtype == torch.bfloat16 else -11)
+        most = max(float(v.abs().max()) for _, v in cache_values(cache, [300, n]))
+        assert fk.fp8kv_get_device_error() == 0 and (a - b).abs().max().item() <= 2 * u * most + 1e-5
+        c = fk.fp8kv_tree_attention(q, cache, cu, lens, masks, out_dtype=torch.float32, num_splits=1)
+        b = fk.fp8kv_chunk_attention(q, cache, cu, lens, out_dtype=torch.float32, num_splits=1)
+        # one share each: the same scores and weights, only the order of rescalings can differ
+        assert (c - b).abs().max().item() <= 1e-5
 
 
 def test_graph_and_stream():
