@@ -464,6 +464,8 @@ fp8kv_status fp8kv_tree_accept(const fp8kv_cache* const* caches, int32_t num_cac
     if (i > 0 && overlap(held[i - 1], held[i])) return FP8KV_ERR_INVALID_ARG;
     for (const Range& o : out)
       if (overlap(o, held[i])) return FP8KV_ERR_INVALID_ARG;
+    for (const Range& r : in)
+      if (overlap(r, held[i])) return FP8KV_ERR_INVALID_ARG;
   }
   p.err = device_error_ptr();
   if (!p.err) return FP8KV_ERR_CUDA;

@@ -80,6 +80,7 @@ def test_accept_refusals_by_caches(lib):  # noqa: F811
                dict(layout=1, max_tokens=0, page_size=16, num_pages=4, max_pages_per_seq=2, page_table=0x900000)):
         assert _accept(lib, [one, _cache(**{**apart, **kw})]) == INVALID
     assert _accept(lib, [_cache(**{**big, "batch": 5})]) == INVALID
+    assert _accept(lib, [one], lens=0x200100) == INVALID                                   # an input among a cache's rows
     assert _accept(lib, [one], path=0x100000) == INVALID                                   # outputs in a cache, in a page table
     paged = dict(layout=1, max_tokens=0, page_size=16, num_pages=4, max_pages_per_seq=2, page_table=0x18000)
     assert _accept(lib, [_cache(**{**big, **paged})]) == INVALID
