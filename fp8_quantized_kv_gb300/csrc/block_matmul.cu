@@ -724,17 +724,29 @@ __global__ void __launch_bounds__(MfCfg<MT>::THREADS, MfCfg<MT>::CTAS) block_mat
       (void)umma::mbar_wait(landed, 0, 100000000ull);
     }
   }
-  // this rank's columns (rows of out), four neighbouring columns of out a thread
-  for (int e = tid; e < per * 32; e += C::THREADS) {
-    const int c = e >> 5, l = 4 * (e & 31), m = m0 + rank * per + c, n = n0 + l;
-    if ((S > 1 && !ok) || m >= p.a.M || n >= p.a.N) continue;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int r = 0; r < S; ++r) {
-      const float4 x = *reinterpret_cast<const float4*>(r == rank ? sent + (rank * per + c) * 128 + l : got + (r * per + c) * 128 + l);
-      y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+  // this rank's columns (rows of out), four neighbouring columns of out a thread; the
+  // warps of sums have each four of them at once
+  if (warp >= 2 && (S == 1 || ok)) {
+    const int l = 4 * lane, n = n0 + l, c0 = warp - 2;        // columns c0, c0 + 4, ...
+    for (int c = c0; c < per; c += 16) {
+      float4 y[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        y[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c + 4 * u >= per) continue;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {                         // (four ranks at most)
+          if (r >= S) continue;
+          const float4 x = *reinterpret_cast<const float4*>((r == rank ? sent : got) + (r * per + c + 4 * u) * 128 + l);
+          y[u].x += x.x; y[u].y += x.y; y[u].z += x.z; y[u].w += x.w;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int m = m0 + rank * per + c + 4 * u;
+        if (c + 4 * u < per && m < p.a.M && n < p.a.N) store_row4(p.a, m, n, y[u]);
+      }
     }
-    store_row4(p.a, m, n, y);
   }
   // the copies out of this CTA have arrived when their readers are here
   umma::fence_before_sync();
