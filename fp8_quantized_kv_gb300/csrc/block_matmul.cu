@@ -12,8 +12,10 @@
 // straight from memory, or shares of K in clusters), many by the products and by the
 // hand-over of each block's sums (pairs of CTAs).  Measured on one GB300, device time:
 // 1 x 2560 x 2048 2.5 us; 64 x 6144 x 4096 10.8 us (25 MB: 2.4 TB/s; 4.9 TB/s at 32,768
-// columns); 997 x 4608 x 3584 18.0 us (1,820 TFLOP/s); 7940 x 6144 x 4096 170 us (2,350
+// columns); 997 x 4608 x 3584 17.7 us (1,860 TFLOP/s); 7940 x 6144 x 4096 170 us (2,350
 // TFLOP/s, 1.23 times the measured bf16 rate); 8192^3 412 us (2,670 TFLOP/s).
+#include <type_traits>
+
 #include "params.cuh"
 #include "tc_common.cuh"
 
@@ -23,9 +25,11 @@ constexpr int kMmBlock = 128;            // elements of a block of K: one 128-by
 
 struct MatmulParams {
   CUtensorMap ta, tb, to;
+  CUtensorMap th;                        // b for half tiles
   MatmulArgs a;
   int kb;                                // blocks of K
   int tiles_m, tiles_n;
+  int whole;                             // pairs of CTAs: tiles before the first that is cut into halves
   int bulk_out;                          // rows of out start on 16 bytes: stored by TMA (map `to`)
 };
 
@@ -194,6 +198,8 @@ __device__ __forceinline__ void store_rows(const MatmulParams& p, uint8_t* buf, 
 //               CTA's barrier
 //   warp 1      TMEM owner; the first CTA's issues the products
 //   warps 4-11  sums: a thread keeps one row of the tile and half of its columns
+// Where the last wave would leave half of the pairs or more without a tile, its tiles
+// are cut into halves of 128 columns (launch_pair).
 //
 // What bounds 256 columns: a block's products take about 640 cycles back to back, but
 // with two TMEM buffers a block also waits for half of the way round a buffer: products
@@ -260,7 +266,28 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar) {
 }
 }  // namespace pair
 
-template <int BN>
+// The tiles of a pair: tile first, first + step, ... of the whole ones, then (CUT) a half.
+template <bool CUT>
+struct MmTile {
+  int m0, n0;
+  bool half;
+  __device__ __forceinline__ bool get(const MatmulParams& p, int bn, int i) {
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1, tiles = p.tiles_m * p.tiles_n;
+    int t = first + i * step, side = 0;
+    half = CUT && t >= p.whole;
+    if (half) {
+      t -= p.whole;
+      side = t & 1;
+      t = p.whole + (t >> 1);
+    }
+    if (t >= tiles) return false;
+    m0 = t % p.tiles_m * 256;
+    n0 = t / p.tiles_m * bn + 128 * side;
+    return true;
+  }
+};
+
+template <int BN, bool CUT>
 __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const __grid_constant__ MatmulParams p) {
   using C = MmCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
@@ -275,7 +302,8 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = (int)cluster_rank(), tiles = p.tiles_m * p.tiles_n, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int rank = (int)cluster_rank();
+  MmTile<CUT> tile;
   if (tid == 0) {
     tma::prefetch_map(&p.ta);
     tma::prefetch_map(&p.tb);
@@ -307,17 +335,18 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
         const uint32_t full0 = mapa_u32(umma::smem_u32(full), 0);
         int it = 0;
         bool ok = true;
-        for (int tile = first; ok && tile < tiles; tile += step) {
-          const int m0 = tile % p.tiles_m * 256 + 128 * rank, n0 = tile / p.tiles_m * BN + BN / 2 * rank;
+        for (int i = 0; ok && tile.get(p, BN, i); ++i) {
+          const bool half = CUT && tile.half;
+          const int m0 = tile.m0 + 128 * rank, n0 = tile.n0 + (half ? 64 : BN / 2) * rank;
           for (int j = 0; j < p.kb; ++j, ++it) {
             const int s = it % C::NS;
             if (it >= C::NS) ok = wait_fast(&empty[s], (it / C::NS - 1) & 1, abort_flag);
             if (!ok) break;
             uint8_t* st = smem + s * C::STAGE;
             const uint32_t bar = full0 + 8 * s;
-            if (rank == 0) tma::arrive_expect_tx(&full[s], 2 * C::STAGE);
+            if (rank == 0) tma::arrive_expect_tx(&full[s], half ? 2 * (128 + 64) * kMmBlock : 2 * C::STAGE);
             pair::load_2d(st, &p.ta, j * kMmBlock, m0, bar);
-            pair::load_2d(st + 128 * kMmBlock, &p.tb, j * kMmBlock, n0, bar);
+            pair::load_2d(st + 128 * kMmBlock, half ? &p.th : &p.tb, j * kMmBlock, n0, bar);
           }
         }
         // no copy is in flight when the pair ends (matters when a wait gave up)
@@ -332,7 +361,8 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
       if (elect_one()) {
         int it = 0;
         bool ok = true, full_ok = false, free_ok = true;
-        for (int tile = first; ok && tile < tiles; tile += step) {
+        for (int i = 0; ok && tile.get(p, BN, i); ++i) {
+          const uint32_t id = CUT && tile.half ? umma::idesc(umma::FMT_E4M3, umma::FMT_E4M3, umma::MAJOR_K, umma::MAJOR_K, 256, 128) : ID;
           for (int j = 0; j < p.kb; ++j, ++it) {
             const int s = it % C::NS, d = it % C::NB;
             const int next = it + 1;
@@ -348,7 +378,7 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
                 full_ok = umma::mbar_test(&full[next % C::NS], (next / C::NS) & 1);
               }
               pair::mma_f8(tmem + d * BN, umma::sdesc(aa + 32 * k, 16, 1024, umma::SWIZZLE_128B),
-                           umma::sdesc(ba + 32 * k, 16, 1024, umma::SWIZZLE_128B), ID, k > 0);
+                           umma::sdesc(ba + 32 * k, 16, 1024, umma::SWIZZLE_128B), id, k > 0);
             }
             pair::mma_commit(&d_full[d]);
             pair::mma_commit(&empty[s]);
@@ -362,14 +392,16 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
     }
   } else {
     regs_inc<232>();
-    constexpr int HC = BN / 2, PC = HC / 32;                  // columns of a thread, and in pieces of 32
     const int part = (warp - 4) >> 2, row_in = 32 * (warp & 3) + lane;
-    const uint32_t base = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + HC * part;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t free0 = mapa_u32(umma::smem_u32(d_free), 0);
     int it = 0;
     bool ok = true, ready = false;
-    for (int tile = first; ok && tile < tiles; tile += step) {
-      const int m = tile % p.tiles_m * 256 + 128 * rank + row_in, n0 = tile / p.tiles_m * BN + HC * part;
+    // a tile of which a thread keeps HC columns
+    auto run = [&](auto columns) {
+      constexpr int HC = decltype(columns)::value, PC = HC / 32;             // in pieces of 32
+      const int m = tile.m0 + 128 * rank + row_in, n0 = tile.n0 + HC * part;
+      const uint32_t base = lanes + HC * part;
       const float* sa = p.a.sa + (int64_t)min(m, p.a.M - 1) * p.kb;
       const float* sb = p.a.sb + (int64_t)(n0 < p.a.N ? n0 / 128 : 0) * p.kb;
       float2 acc[HC / 2];
@@ -380,7 +412,7 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
         const int d = it % C::NB, next = it + 1;
         const uint32_t at = base + BN * d;
         if (!ready) ok = wait_fast(&d_full[d], (it / C::NB) & 1, abort_flag);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; return; }
         umma::fence_after_sync();
         // The buffer is handed back as soon as it is read: two pieces of 32 columns are
         // on their way at once, and the last two are multiplied behind the hand-back.
@@ -412,13 +444,21 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
         sum(PC - 2);
         sum(PC - 1);
       }
-      if (!ok) continue;
       if (p.bulk_out) {
         store_rows<HC>(p, staged + (warp - 4) * 8192, lane, m - lane, n0, acc);
       } else if (m < p.a.M) {
 #pragma unroll
         for (int c = 0; c < HC / 64; ++c) store_row64(p.a, m, n0 + 64 * c, acc + 32 * c);
       }
+    };
+    for (int i = 0; ok && tile.get(p, BN, i); ++i) {
+      if constexpr (CUT) {
+        if (tile.half) {
+          run(std::integral_constant<int, 64>());
+          continue;
+        }
+      }
+      run(std::integral_constant<int, BN / 2>());
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
     if (!ok && lane == 0) raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
@@ -787,31 +827,47 @@ static bool make_out_map(CUtensorMap* m, const MatmulArgs& a) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN>
-static cudaError_t launch_pair(MatmulParams& p, cudaStream_t st) {
+template <int BN, bool CUT>
+static cudaError_t launch_pair_one(const MatmulParams& p, unsigned pairs, cudaStream_t st) {
   using C = MmCfg<BN>;
-  const cudaError_t e = ensure_smem_optin((const void*)block_matmul_pair<BN>, C::BYTES);
+  const cudaError_t e = ensure_smem_optin((const void*)block_matmul_pair<BN, CUT>, C::BYTES);
   if (e != cudaSuccess) return e;
-  p.tiles_m = (p.a.M + 255) / 256;
-  p.tiles_n = (p.a.N + BN - 1) / BN;
-  if (!make_codes_map(&p.ta, p.a.a, p.a.M, p.a.K, 128) || !make_codes_map(&p.tb, p.a.b, p.a.N, p.a.K, BN / 2)) return cudaErrorInvalidValue;
-  p.bulk_out = p.a.N % (p.a.out_f32 ? 4 : 8) == 0;
-  if (p.bulk_out && !make_out_map(&p.to, p.a)) return cudaErrorInvalidValue;
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, pairs = sm_count() / 2;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = 2;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+  cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::BYTES;
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t r = cudaLaunchKernelEx(&cfg, block_matmul_pair<BN>, p);
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, block_matmul_pair<BN, CUT>, p);
   if (r != cudaSuccess) (void)cudaGetLastError();
   return r;
+}
+
+template <int BN>
+static cudaError_t launch_pair(MatmulParams& p, cudaStream_t st) {
+  p.tiles_m = (p.a.M + 255) / 256;
+  p.tiles_n = (p.a.N + BN - 1) / BN;
+  if (!make_codes_map(&p.ta, p.a.a, p.a.M, p.a.K, 128) || !make_codes_map(&p.tb, p.a.b, p.a.N, p.a.K, BN / 2)) return cudaErrorInvalidValue;
+  p.bulk_out = p.a.N % (p.a.out_f32 ? 4 : 8) == 0;
+  if (p.bulk_out && !make_out_map(&p.to, p.a)) return cudaErrorInvalidValue;
+  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n, pairs = sm_count() / 2, rest = tiles % pairs;
+  p.whole = (int)tiles;
+  if constexpr (BN == 256) {
+    // Half tiles in the last wave: 1000 x 6144 x 4096 (96 tiles) 33.8 -> 30.1 us, 4000 x 2560 x
+    // 2048 (160) 28.4 -> 26.5, 5000 x 6144 x 4096 (480) 109.5 -> 108; the form that can cut
+    // takes 2.5 % more a tile, so from eight waves on nothing is won (768 tiles: 169 us both).
+    if (tiles > pairs && tiles < 8 * pairs && rest > 0 && 2 * rest <= pairs) {
+      p.whole = (int)(tiles - rest);
+      if (!make_codes_map(&p.th, p.a.b, p.a.N, p.a.K, 64)) return cudaErrorInvalidValue;
+      return launch_pair_one<256, true>(p, (unsigned)pairs, st);
+    }
+  }
+  return launch_pair_one<BN, false>(p, (unsigned)(tiles < pairs ? tiles : pairs), st);
 }
 
 template <int MT>
@@ -849,8 +905,8 @@ static cudaError_t launch_few(MatmulParams& p, cudaStream_t st) {
 //   up to 128    clusters while four shares of every tile run at once (100 x 4608 x 3584:
 //                10.7, on pairs 11.7), else pairs (128 x 6144 x 4096: 12.9, 14.9)
 //   more         pairs, 128 columns a tile while those fit the SMs at once (200 x 6144 x
-//                4096: 12.9, 256 columns 20; 512 x 2560 x 2048: 8.1 and 12.3), else 256
-//                (512 x 6144 x 4096: 19.7, 128 columns 26.7; 2000 x 2560 x 2048: 21.1, 21.7)
+//                4096: 12.4, 256 columns 20; 512 x 2560 x 2048: 8.1 and 12.3), else 256
+//                (512 x 6144 x 4096: 19.4, 128 columns 26.7; 2000 x 2560 x 2048: 21.1, 21.7)
 cudaError_t launch_block_matmul(const MatmulArgs& a, cudaStream_t st) {
   MatmulParams p;
   p.a = a;

@@ -71,9 +71,10 @@ def test_sizes(M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(640, 4608, 896), (1500, 2560, 2048), (997, 4609, 272), (2100, 1111, 512), (5000, 6144, 384),
-                                   (12, 5003, 272), (100, 6144, 272), (128, 9001, 128), (600, 2568, 16)])
+                                   (12, 5003, 272), (100, 6144, 272), (128, 9001, 128), (600, 2568, 16),
+                                   (4100, 1217, 144), (2600, 2056, 400), (20000, 250, 160)])
 def test_many_rows(M, N, K):
-    """Several tiles a CTA, ragged at both ends; few rows beside many columns."""
+    """Several tiles a CTA, ragged at both ends, last waves cut into half tiles; few rows beside many columns."""
     a, sa, b, sb, bias = make(M, N, K, seed=M, spread=8.0)
     check(fk.fp8kv_block_matmul(a, sa, b, sb, bias=bias, out_dtype=torch.float32), a, sa, b, sb, bias)
     check(fk.fp8kv_block_matmul(a, sa, b, sb), a, sa, b, sb)
