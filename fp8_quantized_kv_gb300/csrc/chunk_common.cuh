@@ -159,6 +159,62 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
   return true;
 }
 
+// Trees: the number of the tile that comes `at`-th when those of long sequences go
+// first, in four classes by length; a permutation of the numbers.  Each lane counts
+// the tiles of batch / 32 sequences in 16 bits a class (the host sees to it that they
+// fit).  Bad offsets: as they come.
+__device__ __forceinline__ int tree_order(const ChunkParams& p, int at) {
+  const int lane = threadIdx.x & 31, B = p.c.batch, T = p.tile_tokens, each = (B + 31) / 32;
+  const int b0 = min(B, lane * each), b1 = min(B, b0 + each);
+  int longest = 0;
+#pragma unroll 4
+  for (int b = b0; b < b1; ++b) longest = max(longest, p.seq_lens[b]);
+  const unsigned step = (unsigned)__reduce_max_sync(0xffffffffu, longest) / 4 + 1;
+  auto shift = [&](int b) { return 48 - 16 * (int)((unsigned)max(p.seq_lens[b], 0) / step); };
+  auto start = [&](int b) { return p.cu_q[b] / T + b; };
+  bool ok = true;
+  unsigned long long own = 0;
+#pragma unroll 2
+  for (int b = b0; b < b1; ++b) {
+    ok = ok && chunk_offsets_ok(p, p.cu_q[b], p.cu_q[b + 1]);
+    own += (unsigned long long)(unsigned)(start(b + 1) - start(b)) << shift(b);
+  }
+  if (!__all_sync(0xffffffffu, ok)) return at;
+  unsigned long long upto = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += x;
+  }
+  const unsigned long long all = __shfl_sync(0xffffffffu, upto, 31);
+  int y = at, sh = 0;
+  for (; sh < 64 && y >= (int)(all >> sh & 0xFFFF); sh += 16) y -= (int)(all >> sh & 0xFFFF);
+  if (sh == 64) return y < start(0) ? y : at;      // numbers in front of the first sequence, and behind the last
+  int e = (int)((upto - own) >> sh & 0xFFFF), x = -1;
+  for (int b = b0; b < b1; ++b) {
+    if (shift(b) != sh) continue;
+    const int n = start(b + 1) - start(b);
+    if (y >= e && y < e + n) x = start(b) + y - e;
+    e += n;
+  }
+  return __reduce_max_sync(0xffffffffu, x);
+}
+
+// What a CTA works at: tile number, KV head, share.  The last tiles of a sequence see
+// the most keys (trees: all see as many): they start first, or, for trees, with
+// `longest_first`, those of long sequences in all their heads and shares.
+struct ChunkPlace { int x, hk, split; };
+
+template <bool TREE>
+__device__ __forceinline__ ChunkPlace chunk_place(const ChunkParams& p) {
+  ChunkPlace a = {(int)(gridDim.x - 1 - blockIdx.x), (int)blockIdx.y, (int)blockIdx.z};
+  if (TREE && p.longest_first) {
+    const unsigned i = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z), each = gridDim.y * gridDim.z, r = i % each;
+    a = {tree_order(p, (int)(i / each)), (int)(r % gridDim.y), (int)(r / gridDim.y)};
+  }
+  return a;
+}
+
 // Whether every query of the tile sees all keys of the KV tile from key0 on.
 // (Trees: a node's position is below the end of its sequence.)
 template <bool TREE = false, int KEYS = kChunkKeys>

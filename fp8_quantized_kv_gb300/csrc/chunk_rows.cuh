@@ -15,7 +15,7 @@
 // joined at the end.  A group never crosses a page (pages hold 16 tokens or
 // more), so a page id is looked up once per group, an iteration before its copy.
 //
-// Arithmetic as in chunk_mma.cuhh: f16 operands for e4m3 sides (codes exact,
+// Arithmetic as in chunk_mma.cuh: f16 operands for e4m3 sides (codes exact,
 // query scaled by a power of two, P by 2^-kp and the value scale), bf16 for
 // bf16 sides, m, l and O in fp32.  Here kp puts the largest value scale a row sees
 // in [2^6, 2^7) (the reference may lag by 2^8), so a weight of 1 on a key whose
@@ -85,9 +85,10 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
   constexpr int KS = D / 16;                   // k steps of QK, m tiles of PV
   extern __shared__ __align__(128) uint8_t rsm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
-  const int hk = blockIdx.y, split = blockIdx.z;
+  const ChunkPlace at = chunk_place<TREE>(p);
+  const int hk = at.hk, split = at.split;
   ChunkTile t;
-  if (!chunk_tile<TREE>(p, gridDim.x - 1 - blockIdx.x, hk == 0 && split == 0, t)) return;
+  if (!chunk_tile<TREE>(p, at.x, hk == 0 && split == 0, t)) return;
   const CacheView& c = p.c;
   const int G = p.group;
   // groups of 16 keys: those of the first tokens, then the window's

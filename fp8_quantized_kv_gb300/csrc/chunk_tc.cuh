@@ -183,9 +183,10 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   static_assert(8 * (2 * C::KN + 2 * C::VN + 2 * OPN + C::NCOL + 6) + 8 <= 256 && 256 + 2 * kCtRows <= C::MISC, "they fit");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int hk = blockIdx.y, split = blockIdx.z;
+  const ChunkPlace at = chunk_place<TREE>(p);
+  const int hk = at.hk, split = at.split;
   ChunkTile t;
-  if (!chunk_tile<TREE>(p, gridDim.x - 1 - blockIdx.x, hk == 0 && split == 0, t)) return;
+  if (!chunk_tile<TREE>(p, at.x, hk == 0 && split == 0, t)) return;
   const int per = (t.n + p.num_splits - 1) / p.num_splits;
   const int j0 = min(t.n, split * per), n = min(t.n, j0 + per) - j0;
   const CacheView& c = p.c;

@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTab
   const int tid = threadIdx.x;
   if (blockIdx.x >= p.batch) {                     // rows that belong to no sequence
     const int first = min(max(p.cu[0], 0), p.rows), end = min(max(p.cu[p.batch], first), p.rows);
-    for (int64_t i = (int64_t)(blockIdx.x - p.batch) * kTreeThreads + tid; i < first + p.rows - end;
+    for (int64_t i = (int64_t)(blockIdx.x - p.batch) * kTreeThreads + tid; i < (int64_t)first + p.rows - end;
          i += (int64_t)(gridDim.x - p.batch) * kTreeThreads) {
       const int64_t r = i < first ? i : end + (i - first);
       p.pos[r] = -1;
@@ -26,11 +26,12 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTab
     }
     return;
   }
-  const int b = blockIdx.x, q0 = p.cu[b], q1 = p.cu[b + 1], len = p.seq_lens[b], n = q1 - q0;
+  const int b = blockIdx.x, q0 = p.cu[b], q1 = p.cu[b + 1], len = p.seq_lens[b];
   if (q0 < 0 || q1 < q0 || q1 > p.rows) {
     if (tid == 0) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
     return;
   }
+  const int n = q1 - q0;
   const bool fits = n <= 32 * p.words && len >= n;
   if (!fits) {
     if (tid == 0) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
@@ -84,11 +85,12 @@ __global__ void __launch_bounds__(kAcceptThreads) tree_accept_kernel(const __gri
   __shared__ int taken_sh;
   const int tid = threadIdx.x, b = blockIdx.x;
   const bool lead = blockIdx.y == 0 && p.first;
-  const int q0 = p.cu[b], q1 = p.cu[b + 1], len = p.seq_lens[b], n = q1 - q0;
+  const int q0 = p.cu[b], q1 = p.cu[b + 1], len = p.seq_lens[b];
   const bool offsets = q0 >= 0 && q1 >= q0 && q1 <= p.rows;
+  const int n = offsets ? q1 - q0 : 0;
   const bool fits = offsets && n <= kTreeMaxNodes && len >= n;
   if (!fits && lead && tid == 0) raise_error(p.err, FP8KV_DEVERR_SEQ_TOO_LONG);
-  const int nodes = fits ? n : 0, ctx = len - n;
+  const int nodes = fits ? n : 0, ctx = fits ? len - n : 0;
   for (int i = tid; i < nodes; i += kAcceptThreads) best[i] = INT32_MAX;
   __syncthreads();
   bool bad = false;

@@ -593,11 +593,11 @@ FP8KV_API size_t fp8kv_tree_workspace_bytes(const fp8kv_cache *cache, int64_t to
  * Pages that hold only tokens from new_lens on stay in the page table; the next
  * fp8kv_build_tables takes fresh pages in their place, so hand them back to the
  * free list.
- * A parent outside [-1, i) raises BAD_TREE and its node is not accepted.  A tree
- * with bad offsets, more than 1024 nodes or more nodes than its sequence has
- * tokens accepts nothing and keeps its length; one whose length passes a
- * cache's capacity moves nothing there (SEQ_TOO_LONG).  A row on a bad page does
- * not move (BAD_PAGE). */
+ * A parent outside [-1, i) raises BAD_TREE and its node, unless it is node 0, is not
+ * accepted.  A tree with bad offsets, more than 1024 nodes or more nodes than its
+ * sequence has tokens accepts nothing and keeps its length; one whose length
+ * passes a cache's capacity moves nothing there (SEQ_TOO_LONG).  A row on a bad
+ * page does not move (BAD_PAGE). */
 FP8KV_API fp8kv_status fp8kv_tree_accept(const fp8kv_cache *const *caches, int32_t num_caches,
                                          const int32_t *parents, const int64_t *tokens,
                                          const int64_t *choices, const int32_t *cu_new,

@@ -180,3 +180,52 @@ def test_captured_layer(nodes):
             results.append([y.clone()] + [t.clone() for t in kept.values()] + cache_copy(cache))
         assert all(torch.equal(a, b) for a, b in zip(*results))
         assert torch.isfinite(results[0][0]).all() and fk.fp8kv_get_device_error() == 0
+
+
+def many_trees(seed, batch, context, nodes):
+    """Contexts of all lengths up to `context`, some empty, and trees of up to `nodes`, some without any."""
+    r = random.Random(seed)
+    ctx = [r.choice([0, 1, r.randint(1, context), context]) for _ in range(batch)]
+    return ctx, [r.choice([0, 1, nodes, r.randint(1, nodes)]) for _ in range(batch)]
+
+
+@pytest.mark.parametrize("dtype,D,kernel,batch,Hkv,nodes,splits", [
+    ("k8v8", 128, "warp_mma", 40, 2, 5, 4), ("k16v16", 64, "warp_mma", 33, 1, 40, 8), ("k8v8", 128, "tensor_cores", 31, 2, 40, 4),
+    ("k8v16", 128, "warp_mma", 300, 1, 3, 2), ("k8v8", 64, "auto", 1024, 1, 2, 1), ("k8v8", 64, "auto", 1025, 1, 2, 1),
+    ("k16v8", 128, "tensor_cores", 2, 4, 1024, 3)])
+def test_long_sequences_first(dtype, D, kernel, batch, Hkv, nodes, splits):
+    """More tiles than run at once, in the order of the sequences' lengths: every row is some tile's."""
+    ctx, new = many_trees(batch, batch, 40 if batch > 100 else 200, nodes)
+    if batch == 2:
+        ctx, new = [700, 30], [600, 1024]
+    cache, lens, cu, q, masks, seen, pos, _ = make_step(dtype, D, 2 * Hkv, Hkv, ctx, new, 16, seed=81, pad=4,
+                                                        words=max(1, -(-max(new) // 32)))
+    front = 3
+    gap = [c + front for c in cu]
+    q = torch.cat([q[-3:], q])
+    masks = torch.cat([masks[-3:], masks])
+    out = torch.full((gap[-1] + 4, 2 * Hkv, D), 6.0, device="cuda")
+    fk.fp8kv_tree_attention(q, cache, _i32(gap), _i32(lens), masks, out=out, kernel=kernel, num_splits=splits)
+    assert fk.fp8kv_get_device_error() == 0
+    assert bool((out[:front] == 6).all()) and bool((out[gap[-1]:] == 6).all())
+    want = tree_definition(q[front:], cache_values(cache, lens), cu, lens, seen, pos, 0, 0, 1 / math.sqrt(D))
+    check(out[front:], cache, want, slice(0, cu[-1]), kernel)
+
+
+def test_long_sequences_first_beside_bad_offsets():
+    """Offsets that decrease leave the order as it comes; a row in front is right or as it was."""
+    ctx, new = many_trees(5, 40, 200, 5)
+    cache, lens, cu, q, masks, *_ = make_step("k8v8", 128, 4, 2, ctx, new, 16, seed=83)
+    want = fk.fp8kv_tree_attention(q, cache, _i32(cu), _i32(lens), masks, num_splits=4)
+    bad = cu[:31] + [cu[30] - 1] + cu[32:]
+    out = torch.full_like(want, 6.0)
+    fk.fp8kv_tree_attention(q, cache, _i32(bad), _i32(lens), masks, num_splits=4, out=out)
+    assert fk.fp8kv_get_device_error() == fk.DEVERR_SEQ_TOO_LONG
+    assert bool(((out == want) | (out == 6)).all(-1).all(-1)[:cu[30] - 1].all()) and bool((out[cu[-1]:] == 6).all())
+
+
+def test_node_0_with_a_bad_parent_is_accepted():
+    cache = make_cache("k8v8", 128, 1, [40], 16, seed=85, poison=False)
+    tokens = torch.ones(3, dtype=torch.int64, device="cuda")
+    got = fk.fp8kv_tree_accept([cache], _i32([0, 0, 1]), tokens, tokens, _i32([0, 3]), _i32([40]), 4)
+    assert fk.fp8kv_get_device_error() == fk.DEVERR_BAD_TREE and got["path"].tolist() == [[0, 1, 2, -1]]
