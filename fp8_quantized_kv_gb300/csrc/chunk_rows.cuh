@@ -2,7 +2,7 @@
 // rows, for single tokens of a group of heads and a few drafted tokens: the cache
 // is read once and nothing else takes as long, so the kernel is built around
 // keeping loads in flight.  Also the form of block-scaled keys at any length
-// (256-512 tokens x 8 heads, 4 sequences of 4K-8K: 1.14 ms, conversions and the
+// (256-512 tokens x 8 heads, 4 sequences of 4K-8K: 0.71 ms, conversions and the
 // four fp32 partial products of a score).
 //
 // The products are turned around so that the queries are the narrow side of the
@@ -24,27 +24,33 @@
 // 32-element partial products are scaled in fp32 and added.
 //
 // Measured on one GB300 (64 sequences, 32 query / 8 KV heads, head dim 128,
-// e4m3, 16-token pages, device time): a 1,024-token window 35 us (140 MB: 4.0
-// TB/s, 59 % of the measured copy rate); 2,048 more tokens of window cost at 5.4
-// TB/s, so what is left is the fixed part (about 5 us to find the tile, load the
-// first groups and join) and the issue slots (46 % busy: 430 instructions a
-// group, 80 of them the conversion of 4,096 codes).  On the way there: 58 us with
+// e4m3, 16-token pages, device time): a 1,024-token window 30 us (140 MB: 4.6
+// TB/s, 68 % of the measured copy rate); whole contexts of 1K-16K tokens, 2-4 tokens
+// each, 186 us of a call's 194 (1.06 GB: 5.7 TB/s, 84 %).  What is left is the fixed
+// part (about 5 us to find the tile, load the first groups and join) and latency: three
+// to four warps a scheduler, 470 instructions a group of sixteen rows, 64 of them the
+// conversion of 4,096 codes.  On the way there (the window): 58 us with
 // a reference that moves at every new maximum and checked row copies; 46 us with
 // one vote for both and whole-group copies, three CTAs an SM at four ring stages;
-// 40 us with five CTAs at two; 36.5 us with four at three (this).  QK on e4m3
-// instructions without conversion (mma.sync m16n8k32) was slower, 39 us.  Two groups
-// a step, which share the vote and the loop: 46 us (67 KB of rings, three CTAs an
-// SM, one wave and a bit; the same 59 us as below where shares can even that out).
+// 40 us with five CTAs at two; 36.5 us with four at three; 30.5 us with groups that
+// every query sees in a form of their own (`weigh`: 33 instructions less, and the
+// registers of the other form) and copies whose addresses take 32-bit row numbers
+// (100 instructions instead of 158; sixteen rows 217 -> 194 us).  QK on e4m3
+// instructions without conversion (mma.sync m16n8k32) was slower.  Two groups
+// a step, which share the vote and the loop: slower too (67 KB of rings, three CTAs an
+// SM, one wave and a bit).
 //
 // Sixteen rows (two tokens x 8 heads, 4 KV heads, 64 sequences of 2K-4K tokens,
-// 210 MB): 74 us, three CTAs an SM at 168 registers; 55 us for one token.  The
-// second set costs its products, exponentials and transposes, not the codes'
-// conversion.  On the warp-level kernel, whose four warps share a tile, the call took
-// 90 us at the best split count, on tcgen05's 128-row tiles 101 us; 16 heads on one
-// KV head at head dim 64 (64 sequences of 4K-8K tokens) take 30 us, 53 us there.
+// 210 MB): 56 us, three CTAs an SM at 168 registers (four at 128 registers leave 9 KB
+// of first-level cache, where spilled registers and scales are lost: 25 % slower);
+// 45 us for one token.  The second set costs its products, exponentials and transposes,
+// not the codes' conversion.  The query's fragments in shared memory take 8 loads a
+// group and give back 32 registers: 0.7 % faster, not kept.  16 heads on one KV head at
+// head dim 64 (64 sequences of 4K-8K tokens) take 24 us.
 #pragma once
 
 #include <cfloat>
+#include <type_traits>
 
 #include "chunk_common.cuh"
 
@@ -75,6 +81,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __device__ __forceinline__ void cp_async16_u(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async4_u(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+}
 
 template <bool TREE, int D, int KE, int VE, int QT>
 __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(const ChunkParams p) {
@@ -96,17 +105,28 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
   const int n_sink = p.window > 0 ? min((min(p.sinks, t.kv_end) + kRowKeys - 1) / kRowKeys, first) : 0;
   const int all = n_sink + max(0, (t.kv_end + kRowKeys - 1) / kRowKeys - first);
   const int per = (all + p.num_splits - 1) / p.num_splits;
-  const int j0 = min(all, split * per) + warp, j1 = min(all, (split + 1) * per);
-  const int n = j1 > j0 ? (j1 - j0 + 3) / 4 : 0;                 // this warp's groups j0, j0 + 4, ...
-  auto group_key0 = [&](int it) {
-    const int j = j0 + 4 * it;
-    return (j < n_sink ? j : first + j - n_sink) * kRowKeys;
-  };
-  const int64_t cont0 = ((int64_t)t.b * c.kv_heads + hk) * c.max_tokens;
-  auto fetch_page = [&](int it) {
-    return c.paged && it < n ? c.page_table[(int64_t)t.b * c.max_pages_per_seq + (group_key0(it) >> c.page_shift)] : 0;
+  const int j0 = min(all, split * per) + warp, j1 = min(all, (split + 1) * per);      // this warp's groups j0, j0 + 4, ...
+  const int skip = first - n_sink;
+  auto group_key0 = [&](int j) { return (j < n_sink ? j : j + skip) * kRowKeys; };
+  // The copies of a group take a third of the loop's instructions unless their addresses
+  // are little work: rows are 31-bit numbers (of a page: page * row_step + row0 + its
+  // token; contiguous: row0 + key), and a lane's three pointers to row 0 are kept.
+  const unsigned row_step = c.kv_heads * c.page_size, num_pages = c.paged ? c.num_pages : 1;
+  const unsigned row0 = c.paged ? hk * c.page_size : (unsigned)(t.b * c.kv_heads + hk) * c.max_tokens;
+  const int key_mask = c.paged ? c.page_size - 1 : INT32_MAX;
+  const int32_t* table = c.paged ? c.page_table + (int64_t)t.b * c.max_pages_per_seq : nullptr;
+  int jf = j0;                                 // next group whose page is fetched
+  auto fetch = [&](int& key0, int& page) {     // its first key (-1: none) and page
+    key0 = -1;
+    page = 0;
+    if (jf < j1) {
+      key0 = group_key0(jf);
+      if (c.paged) page = table[key0 >> c.page_shift];
+    }
+    jf += 4;
   };
   uint8_t* ring = rsm + warp * C::NS * C::STAGE;
+  const uint32_t ring_at = umma::smem_u32(ring);
   // Where a lane's chunks of a group go: chunk lane + 32 i lies 512 i bytes
   // behind chunk lane, with one placement (K) or two that alternate (V), since
   // 512 bytes hold a whole number of the rows after which the placement repeats
@@ -117,50 +137,45 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
 #pragma unroll
   for (int i = 0; i < VALT; ++i)
     vdst[i] = ((lane + 32 * i) / VC) * C::VB + v_chunk<C::VB>(lane % VC, (lane + 32 * i) / VC) * 16 - 512 * i;
-  auto issue = [&](int it, int page) {
-    if (it < n) {
-      const int key0 = group_key0(it);
-      int64_t row = cont0 + key0;
-      bool ok = true;
-      if (c.paged) {
-        ok = page >= 0 && page < c.num_pages;
-        if (!ok && lane == 0) raise_error(p.err, FP8KV_DEVERR_BAD_PAGE);
-        row = ((int64_t)(ok ? page : 0) * c.kv_heads + hk) * c.page_size + (key0 & (c.page_size - 1));
-      }
-      const uint32_t ks = umma::smem_u32(ring + (it % C::NS) * C::STAGE), vs = ks + kRowKeys * C::KB, sc = vs + kRowKeys * C::VB;
+  auto issue = [&](uint32_t stage, int key0, int page) {      // stage: byte offset in the ring
+    if (key0 >= 0) {
+      const bool ok = (unsigned)page < num_pages;
+      if (!ok && lane == 0) raise_error(p.err, FP8KV_DEVERR_BAD_PAGE);
+      const unsigned row = (ok ? page : 0) * row_step + row0 + (unsigned)(key0 & key_mask);
+      const uint32_t ks = ring_at + stage, vs = ks + kRowKeys * C::KB, sc = vs + kRowKeys * C::VB;
       // the 16 rows lie together: chunk e of the group is 16 e bytes from its start
-      const uint8_t* ksrc = c.k + row * C::KB + lane * 16;
-      const uint8_t* vsrc = c.v + row * C::VB + lane * 16;
+      const uint8_t* ksrc = c.k + ((uint64_t)row * C::KB + lane * 16);
+      const uint8_t* vsrc = c.v + ((uint64_t)row * C::VB + lane * 16);
+      const float* ssrc = (lane < 16 ? c.k_scale : c.v_scale) + ((uint64_t)row + (lane & 15));
       // rows nobody sees are zero-filled, not read: they may hold anything
       const bool whole = ok && key0 + kRowKeys <= t.kv_end && (key0 >= t.lo || key0 + kRowKeys <= p.sinks);
-      auto live = [&](int r) {
-        return whole || (ok && key0 + r < t.kv_end && (key0 + r >= t.lo || key0 + r < p.sinks));
-      };
       if (whole) {
 #pragma unroll
         for (int i = 0; i < KC / 2; ++i) cp_async16_u(ks + kdst + 512 * i, ksrc + 512 * i);
 #pragma unroll
         for (int i = 0; i < VC / 2; ++i) cp_async16_u(vs + vdst[i % VALT] + 512 * i, vsrc + 512 * i);
+        if (lane < 16 ? !KB16 : !VB16) cp_async4_u(sc + lane * 4, ssrc);
       } else {
+        auto live = [&](int r) { return ok && key0 + r < t.kv_end && (key0 + r >= t.lo || key0 + r < p.sinks); };
 #pragma unroll
         for (int i = 0; i < KC / 2; ++i) cp_async16_z(ks + kdst + 512 * i, ksrc + 512 * i, live((lane + 32 * i) / KC));
 #pragma unroll
         for (int i = 0; i < VC / 2; ++i)
           cp_async16_z(vs + vdst[i % VALT] + 512 * i, vsrc + 512 * i, live((lane + 32 * i) / VC));
+        if (lane < 16 ? !KB16 : !VB16) cp_async4_z(sc + lane * 4, ssrc, live(lane & 15));
       }
-      const int r = lane & 15;
-      if (lane < 16 ? !KB16 : !VB16) cp_async4_z(sc + lane * 4, (lane < 16 ? c.k_scale : c.v_scale) + row + r, live(r));
     }
     cp_async_commit();
   };
   {
-    int page[C::NS - 1];
+    int key0[C::NS - 1], page[C::NS - 1];
 #pragma unroll
-    for (int it = 0; it < C::NS - 1; ++it) page[it] = fetch_page(it);
+    for (int it = 0; it < C::NS - 1; ++it) fetch(key0[it], page[it]);
 #pragma unroll
-    for (int it = 0; it < C::NS - 1; ++it) issue(it, page[it]);
+    for (int it = 0; it < C::NS - 1; ++it) issue(it * C::STAGE, key0[it], page[it]);
   }
-  int next_page = fetch_page(C::NS - 1);
+  int next_key, next_page;
+  fetch(next_key, next_page);
 
   // query rows g and g + 8 as B fragments; positions of this thread's score
   // columns, queries col(i)
@@ -207,13 +222,12 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
       qf[2 * w + 1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
     }
   }
-  int qpos[QC];
-#pragma unroll
-  for (int i = 0; i < QC; ++i) {
+  auto qpos = [&](int i) {                     // (asked in the few groups that are seen in part)
     const int r = col(i), tk = r / G;
-    qpos[i] = tk < t.ntok && r < p.tile_tokens * G ? t.pos0 + tk : -1;
-    qf[i] *= p.scale_log2;
-  }
+    return tk < t.ntok && r < p.tile_tokens * G ? t.pos0 + tk : -1;
+  };
+#pragma unroll
+  for (int i = 0; i < QC; ++i) qf[i] *= p.scale_log2;
 
   float o[QT][KS][4];
 #pragma unroll
@@ -224,26 +238,28 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
       for (int e = 0; e < 4; ++e) o[w][u][e] = 0.f;
   // the reference maximum, the sum in units of 2^m, -m - kp, 2^kp, and the
   // value scale from which on kp has to rise
-  float m[QC], l[QC], neg_m[QC], up2[QC], vm_top[QC];
+  float m[QC], l[QC], neg_m[QC], up2[QC];
 #pragma unroll
   for (int i = 0; i < QC; ++i) {
     m[i] = -INFINITY;
-    l[i] = neg_m[i] = 0.f;
-    up2[i] = 1.f;
-    vm_top[i] = FLT_MIN;
+    l[i] = 0.f;
+    neg_m[i] = VB16 ? 0.f : 100.f;
+    up2[i] = VB16 ? 1.f : pow2i(-100);
   }
 
+  uint32_t stage = 0;                          // byte offset of the group's place in the ring
 #pragma unroll 1
-  for (int it = 0; it < n; ++it) {
+  for (int jr = j0; jr < j1; jr += 4) {
     cp_async_wait<C::NS - 2>();
     __syncwarp();
-    issue(it + C::NS - 1, next_page);
-    next_page = fetch_page(it + C::NS);
-    const uint8_t* st = ring + (it % C::NS) * C::STAGE;
+    issue(stage == 0 ? (C::NS - 1) * C::STAGE : stage - C::STAGE, next_key, next_page);
+    fetch(next_key, next_page);
+    const uint8_t* st = ring + stage;
+    stage = stage == (C::NS - 1) * C::STAGE ? 0 : stage + C::STAGE;
     const uint8_t* vst = st + kRowKeys * C::KB;
     const float* ksc = reinterpret_cast<const float*>(vst + kRowKeys * C::VB);
     const float* vsc = ksc + kRowKeys;
-    const int key0 = group_key0(it);
+    const int key0 = group_key0(jr);
     // s[w][e]: key g + 8 (e >> 1), query col(2 w + (e & 1)); two chains of products
     float s[QT][4], s1[QT][4];
 #pragma unroll
@@ -312,170 +328,173 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[w][e] = (s[w][e] + s1[w][e]) * qf[2 * w + (e & 1)];
     }
-    // does every query see all 16 keys?
-    const bool part = !chunk_all_seen<TREE, kRowKeys>(p, t, key0);
-    bool see[QT][4];
-#pragma unroll
-    for (int w = 0; w < QT; ++w)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) see[w][e] = true;
-    if (part) {
-      unsigned bits[QC];
-#pragma unroll
-      for (int i = 0; i < QC; ++i) bits[i] = TREE ? (unsigned)tree_seen_mask(p, t, qpos[i], key0) >> g : 0u;
+    // `part`: not every query sees all 16 keys
+    auto weigh = [&](auto cut) {
+      constexpr bool part = decltype(cut)::value;
+      bool see[QT][4];
 #pragma unroll
       for (int w = 0; w < QT; ++w)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (TREE) see[w][e] = bits[2 * w + (e & 1)] >> (8 * (e >> 1)) & 1;
-          else see[w][e] = chunk_sees(p, qpos[2 * w + (e & 1)], key0 + g + 8 * (e >> 1));
-          if (!see[w][e]) s[w][e] = -INFINITY;
-        }
-    }
-    // The reference moves only when the maximum grows by more than 2^8, kp only
-    // up, and O with them: rare behind the first groups, one vote on what each
-    // lane sees skips it, and the query's maximum is joined only then.
-    const float v0 = VB16 ? 0.f : vsc[g], v1 = VB16 ? 0.f : vsc[g + 8];
-    bool moved = false;
+        for (int e = 0; e < 4; ++e) see[w][e] = true;
+      if (part) {
+        unsigned bits[QC];
 #pragma unroll
-    for (int i = 0; i < QC; ++i) {
-      moved = moved || fmaxf(s[i >> 1][i & 1], s[i >> 1][2 + (i & 1)]) > m[i] + 8.f;
-      if constexpr (!VB16) moved = moved || fmaxf(v0, v1) >= vm_top[i];
-    }
-    if (__any_sync(0xffffffffu, moved)) {
+        for (int i = 0; i < QC; ++i) bits[i] = TREE ? (unsigned)tree_seen_mask(p, t, qpos(i), key0) >> g : 0u;
+#pragma unroll
+        for (int w = 0; w < QT; ++w)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (TREE) see[w][e] = bits[2 * w + (e & 1)] >> (8 * (e >> 1)) & 1;
+            else see[w][e] = chunk_sees(p, qpos(2 * w + (e & 1)), key0 + g + 8 * (e >> 1));
+            if (!see[w][e]) s[w][e] = -INFINITY;
+          }
+      }
+      // The reference moves only when the maximum grows by more than 2^8, kp only
+      // up, and O with them: rare behind the first groups, one vote on what each
+      // lane sees skips it, and the query's maximum is joined only then.
+      [[maybe_unused]] const float v0 = VB16 ? 0.f : vsc[g], v1 = VB16 ? 0.f : vsc[g + 8];
+      bool moved = false;
+#pragma unroll
+      for (int i = 0; i < QC; ++i) {
+        moved = moved || fmaxf(s[i >> 1][i & 1], s[i >> 1][2 + (i & 1)]) > m[i] + 8.f;
+        if constexpr (!VB16) moved = moved || fmaxf(v0, v1) * 0.0078125f >= up2[i];
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int i = 0; i < QC; ++i) {
+          const int w = i >> 1, j = i & 1;
+          float alpha = 1.f, mt = fmaxf(s[w][j], s[w][2 + j]);
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+          if (mt > m[i] + 8.f) {
+            alpha = ex2(m[i] - mt);              // (0 for the first)
+            m[i] = mt;
+            l[i] *= alpha;
+          }
+          if constexpr (!VB16) {                 // the largest finite value scale among the keys the query sees
+            float vm = fmaxf(see[w][j] && v0 < INFINITY ? v0 : 0.f, see[w][2 + j] && v1 < INFINITY ? v1 : 0.f);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, x));
+            if (vm * 0.0078125f >= up2[i]) {
+              const int need = max(-100, min(100, ((__float_as_int(vm) >> 23) & 0xFF) - 127 - 6));   // vm 2^-need < 2^7
+              alpha *= pow2i(max(-126, (__float_as_int(up2[i]) >> 23) - 127 - need));
+              up2[i] = pow2i(need);
+            }
+          }
+          neg_m[i] = (m[i] == -INFINITY ? 0.f : -m[i]) - (float)((__float_as_int(up2[i]) >> 23) - 127);
+#pragma unroll
+          for (int u = 0; u < KS; ++u) {
+            o[w][u][j] *= alpha;
+            o[w][u][2 + j] *= alpha;
+          }
+        }
+      }
 #pragma unroll
       for (int i = 0; i < QC; ++i) {
         const int w = i >> 1, j = i & 1;
-        float alpha = 1.f, mt = fmaxf(s[w][j], s[w][2 + j]);
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-        if (mt > m[i] + 8.f) {
-          alpha = ex2(m[i] - mt);              // (0 for the first)
-          m[i] = mt;
-          l[i] *= alpha;
-        }
-        if constexpr (!VB16) {                 // the largest finite value scale among the keys the query sees
-          float vm = fmaxf(see[w][j] && v0 < INFINITY ? v0 : 0.f, see[w][2 + j] && v1 < INFINITY ? v1 : 0.f);
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, x));
-          if (vm >= vm_top[i]) {
-            const int need = max(-100, min(100, ((__float_as_int(vm) >> 23) & 0xFF) - 127 - 6));   // vm 2^-need < 2^7
-            alpha *= pow2i(max(-126, (__float_as_int(up2[i]) >> 23) - 127 - need));
-            up2[i] = pow2i(need);
-            vm_top[i] = pow2i(need + 7);
+        s[w][j] = ex2_ftz(s[w][j] + neg_m[i]);
+        s[w][2 + j] = ex2_ftz(s[w][2 + j] + neg_m[i]);
+        l[i] = fmaf(s[w][j] + s[w][2 + j], up2[i], l[i]);
+        if constexpr (!VB16) {
+          s[w][j] *= v0;
+          s[w][2 + j] *= v1;
+          if (part) {                            // an unseen key's scale may be anything
+            s[w][j] = see[w][j] ? s[w][j] : 0.f;
+            s[w][2 + j] = see[w][2 + j] ? s[w][2 + j] : 0.f;
           }
         }
-        neg_m[i] = (m[i] == -INFINITY ? 0.f : -m[i]) - (float)((__float_as_int(up2[i]) >> 23) - 127);
+      }
+      // P^T as B fragments: keys 2 c4, + 1 (and + 8) of queries g (and g + 8)
+      uint32_t pb[QT][2];
 #pragma unroll
-        for (int u = 0; u < KS; ++u) {
-          o[w][u][j] *= alpha;
-          o[w][u][2 + j] *= alpha;
+      for (int w = 0; w < QT; ++w) {
+        pb[w][0] = transpose8(pack16<VB16>(s[w][0], s[w][1]));
+        pb[w][1] = transpose8(pack16<VB16>(s[w][2], s[w][3]));
+      }
+      bool aside = false;                        // values that must not meet an unseeing query's zero weight
+      if (part && (TREE || t.ntok > 1)) {
+        constexpr int VC = C::VB / 16;
+        for (int e = lane; e < kRowKeys * VC; e += 32) {
+          const uint4 w = *reinterpret_cast<const uint4*>(vst + e * 16);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if constexpr (VB16)
+              aside = aside || (ww[u] & 0x7F800000u) == 0x7F800000u || (ww[u] & 0x7F80u) == 0x7F80u;
+            else
+              aside = aside || (((ww[u] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+          }
+        }
+        aside = __any_sync(0xffffffffu, aside);
+      }
+      const uint32_t vaddr = umma::smem_u32(vst);
+      const int vr = lane & 15;
+      // the two 16-dim A fragments of 32 bytes of V rows
+      auto load_v = [&](int u, uint32_t (&a)[2][4]) {
+        uint32_t r[4];
+        ldsm_x4_trans(vaddr + vr * C::VB + v_chunk<C::VB>(2 * u + (lane >> 4), vr) * 16, r);
+        if constexpr (VB16) {
+          a[0][0] = r[0]; a[0][1] = r[2]; a[0][2] = r[1]; a[0][3] = r[3];
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            // two keys x two dims of codes -> the two keys of each dim
+            const uint32_t w = __byte_perm(r[k], 0, 0x3120);
+            a[k >> 1][2 * (k & 1)] = e4m3x2_to_f16x2((uint16_t)w);
+            a[k >> 1][2 * (k & 1) + 1] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+          }
+        }
+      };
+      constexpr int MT = VB16 ? 1 : 2;           // m tiles per 32 bytes of a row
+#pragma unroll
+      for (int u = 0; u < C::VB / 32; ++u) {
+        uint32_t a[2][4];
+        load_v(u, a);
+#pragma unroll
+        for (int k = 0; k < MT; ++k) {
+          if (aside) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[k][e] = SetAside<VB16>(a[k][e]).clean;
+          }
+#pragma unroll
+          for (int w = 0; w < QT; ++w) mma16816<VB16>(o[w][MT * u + k], a[k], pb[w][0], pb[w][1]);
         }
       }
-    }
+      if (aside) {                               // rare: which queries see the values set aside
 #pragma unroll
-    for (int i = 0; i < QC; ++i) {
-      const int w = i >> 1, j = i & 1;
-      s[w][j] = ex2_ftz(s[w][j] + neg_m[i]);
-      s[w][2 + j] = ex2_ftz(s[w][2 + j] + neg_m[i]);
-      l[i] = fmaf(s[w][j] + s[w][2 + j], up2[i], l[i]);
-      if constexpr (!VB16) {
-        s[w][j] *= v0;
-        s[w][2 + j] *= v1;
-        if (part) {                            // an unseen key's scale may be anything
-          s[w][j] = see[w][j] ? s[w][j] : 0.f;
-          s[w][2 + j] = see[w][2 + j] ? s[w][2 + j] : 0.f;
-        }
-      }
-    }
-    // P^T as B fragments: keys 2 c4, + 1 (and + 8) of queries g (and g + 8)
-    uint32_t pb[QT][2];
+        for (int w = 0; w < QT; ++w) {
+          const uint32_t z0 = transpose8(pack16<VB16>(see[w][0] ? 1.f : 0.f, see[w][1] ? 1.f : 0.f));
+          const uint32_t z1 = transpose8(pack16<VB16>(see[w][2] ? 1.f : 0.f, see[w][3] ? 1.f : 0.f));
 #pragma unroll
-    for (int w = 0; w < QT; ++w) {
-      pb[w][0] = transpose8(pack16<VB16>(s[w][0], s[w][1]));
-      pb[w][1] = transpose8(pack16<VB16>(s[w][2], s[w][3]));
-    }
-    bool aside = false;                        // values that must not meet an unseeing query's zero weight
-    if (part && (TREE || t.ntok > 1)) {
-      constexpr int VC = C::VB / 16;
-      for (int e = lane; e < kRowKeys * VC; e += 32) {
-        const uint4 w = *reinterpret_cast<const uint4*>(vst + e * 16);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          for (int u = 0; u < C::VB / 32; ++u) {
+            uint32_t a[2][4];
+            load_v(u, a);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if constexpr (VB16)
-            aside = aside || (ww[u] & 0x7F800000u) == 0x7F800000u || (ww[u] & 0x7F80u) == 0x7F80u;
-          else
-            aside = aside || (((ww[u] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-        }
-      }
-      aside = __any_sync(0xffffffffu, aside);
-    }
-    const uint32_t vaddr = umma::smem_u32(vst);
-    const int vr = lane & 15;
-    // the two 16-dim A fragments of 32 bytes of V rows
-    auto load_v = [&](int u, uint32_t (&a)[2][4]) {
-      uint32_t r[4];
-      ldsm_x4_trans(vaddr + vr * C::VB + v_chunk<C::VB>(2 * u + (lane >> 4), vr) * 16, r);
-      if constexpr (VB16) {
-        a[0][0] = r[0]; a[0][1] = r[2]; a[0][2] = r[1]; a[0][3] = r[3];
-      } else {
+            for (int k = 0; k < MT; ++k) {
+              uint32_t an[4], ap[4], am[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          // two keys x two dims of codes -> the two keys of each dim
-          const uint32_t w = __byte_perm(r[k], 0, 0x3120);
-          a[k >> 1][2 * (k & 1)] = e4m3x2_to_f16x2((uint16_t)w);
-          a[k >> 1][2 * (k & 1) + 1] = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+              for (int e = 0; e < 4; ++e) {
+                const SetAside<VB16> x(a[k][e]);
+                an[e] = x.nan; ap[e] = x.pinf; am[e] = x.ninf;
+              }
+              float nan[4] = {0.f, 0.f, 0.f, 0.f}, pinf[4] = {0.f, 0.f, 0.f, 0.f}, ninf[4] = {0.f, 0.f, 0.f, 0.f};
+              mma16816<VB16>(nan, an, z0, z1);
+              mma16816<VB16>(pinf, ap, z0, z1);
+              mma16816<VB16>(ninf, am, z0, z1);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float& acc = o[w][MT * u + k][e];
+                if (pinf[e] > 0.f) acc += INFINITY;
+                if (ninf[e] > 0.f) acc -= INFINITY;
+                if (nan[e] > 0.f) acc = NAN;
+              }
+            }
+          }
         }
       }
     };
-    constexpr int MT = VB16 ? 1 : 2;           // m tiles per 32 bytes of a row
-#pragma unroll
-    for (int u = 0; u < C::VB / 32; ++u) {
-      uint32_t a[2][4];
-      load_v(u, a);
-#pragma unroll
-      for (int k = 0; k < MT; ++k) {
-        if (aside) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) a[k][e] = SetAside<VB16>(a[k][e]).clean;
-        }
-#pragma unroll
-        for (int w = 0; w < QT; ++w) mma16816<VB16>(o[w][MT * u + k], a[k], pb[w][0], pb[w][1]);
-      }
-    }
-    if (aside) {                               // rare: which queries see the values set aside
-#pragma unroll
-      for (int w = 0; w < QT; ++w) {
-        const uint32_t z0 = transpose8(pack16<VB16>(see[w][0] ? 1.f : 0.f, see[w][1] ? 1.f : 0.f));
-        const uint32_t z1 = transpose8(pack16<VB16>(see[w][2] ? 1.f : 0.f, see[w][3] ? 1.f : 0.f));
-#pragma unroll
-        for (int u = 0; u < C::VB / 32; ++u) {
-          uint32_t a[2][4];
-          load_v(u, a);
-#pragma unroll
-          for (int k = 0; k < MT; ++k) {
-            uint32_t an[4], ap[4], am[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const SetAside<VB16> x(a[k][e]);
-              an[e] = x.nan; ap[e] = x.pinf; am[e] = x.ninf;
-            }
-            float nan[4] = {0.f, 0.f, 0.f, 0.f}, pinf[4] = {0.f, 0.f, 0.f, 0.f}, ninf[4] = {0.f, 0.f, 0.f, 0.f};
-            mma16816<VB16>(nan, an, z0, z1);
-            mma16816<VB16>(pinf, ap, z0, z1);
-            mma16816<VB16>(ninf, am, z0, z1);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float& acc = o[w][MT * u + k][e];
-              if (pinf[e] > 0.f) acc += INFINITY;
-              if (ninf[e] > 0.f) acc -= INFINITY;
-              if (nan[e] > 0.f) acc = NAN;
-            }
-          }
-        }
-      }
-    }
+    if (chunk_all_seen<TREE, kRowKeys>(p, t, key0)) weigh(std::false_type());
+    else weigh(std::true_type());
   }
 
 #pragma unroll

@@ -72,8 +72,12 @@ struct CtCfg {
   static constexpr int QOP = kCtRows * 2 * D;                       // [hi, lo][128][128 B], or [2 halves of D][128][128 B]
   static constexpr int KT = kChunkKeys * D * (K16 ? 2 : 1);         // K tile
   static constexpr int VT = kChunkKeys * D * (V16 ? 2 : 1);         // V tile as stored
-  static constexpr int KN = K16 ? 2 : 3, VN = K16 && !V16 ? 1 : 2;  // ring depths
-  static constexpr int NOP = V16 ? 0 : 2;                           // f16 V operand buffers
+  static constexpr int KN = K16 ? 2 : 3, VN = 2;                    // ring depths
+  // f16 V operand buffers.  Beside bf16 keys there is room for a second one or for a
+  // second V stage, and the copy takes longer than the conversion: four sequences of
+  // 512-1,024 queries over 2K-8K tokens (28 / 4 heads) 339 us with one stage and two
+  // buffers, 294 so (three stages: 294); beside e4m3 keys one buffer makes 300 us 333.
+  static constexpr int NOP = V16 ? 0 : K16 ? 1 : 2;
   static constexpr int OPT = kChunkKeys * D * 2;
   static constexpr int CST = 2 * kChunkKeys + 4;                    // floats: k, v column scales, largest v scale of each half
   static constexpr int NCOL = 4;
