@@ -22,19 +22,22 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // How a chunk call runs, from its sizes (lengths are on the device).
 // Kernel, by the average number of query rows (queries x heads of a group) a
 // sequence has: up to 16 rows the few-row kernel, in tiles of 8 or 16 (one token
-// of 64 sequences under a 1,024-token window: 35 us, against 81 us on tcgen05; two
-// tokens x 8 heads of 64 sequences of 2K-4K tokens: 74 us, against 101 us);
-// above, tcgen05 where it is built.  Between 17 and 32 rows neither is clearly ahead
-// (8 tokens x 4 heads over 8,000 tokens, 4 sequences: 40 us against 45 us at the best
-// split counts; 2-4 x 8 over 4K-8K, 16 sequences: 62 against 58 to 71), far above
-// it is (256 x 4 over 16,000: 108 against 447).  The average counts idle sequences
+// of 64 sequences under a 1,024-token window: 30 us, against 81 us on tcgen05; two
+// tokens x 8 heads of 64 sequences of 2K-4K tokens: 56 us, against 101 us);
+// above, tcgen05 where it is built, which far above is ahead (256 x 4 over 16,000: 107
+// against 323).  Between 17 and 32 rows the few-row kernel is, beside e4m3 values (8
+// tokens x 4 heads over 8,000 tokens, 4 sequences: 33 us against 39 us at the best
+// split counts; 2-4 x 8 over 4K-8K, 16 sequences: 45 against 61; trees of 3-4 x 8 over
+// 100-2,000, 300 sequences: 179 against 227; but 50 against 46 under a window of 1,024
+// of 64), beside bf16 ones either (188 against 180, 127 against 159): trees take it
+// there, chunk calls stay with tcgen05 and its roundings.  The average counts idle sequences
 // and rows of padding, and one kernel runs the whole call: batches of unlike
 // sequences (a prompt in many idle slots, or beside many single tokens) get the
 // form that suits only some of them.  Lengths of queries are on the device, so the
 // host knows no better.  Block-scaled keys stay on the few-row kernel (2-4 x 8 over
-// 4K-8K, 16 sequences: 63 us, 88 us on the form that the warp-level kernel had for
-// them; 256-512 x 8, 4 sequences: 1.15 ms against 1.33), head dim 64 does up to 32
-// rows (2-4 x 8 of 64 sequences of 2K-4K, bf16: 64 us against 71 on 64-row tiles at
+// 4K-8K, 16 sequences: 49 us, 88 us on the form that the warp-level kernel had for
+// them; 256-512 x 8, 4 sequences: 0.71 ms against 1.33), head dim 64 does up to 32
+// rows (2-4 x 8 of 64 sequences of 2K-4K, bf16: 56 us against 71 on 64-row tiles at
 // the best split count), with more it runs on the warp-level kernel (256-512 x 8 over
 // 4K-8K, 4 sequences: 0.56 ms against 0.70; around 64 rows either can be faster).
 //
@@ -42,12 +45,12 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // or of 32 KiB stages), and a call takes as many waves of them as they need,
 // each as long as one share and the 8 tiles' time that a CTA spends on its
 // start and end.  So the counts that fill one, two or three waves are compared:
-// 256 units of 32-64 tiles (16 rows) take 100 us whole, 84 us in 2 shares (1.1
-// waves), 75 us in 3 (1.7), 79 us in 4.  Shares are 192 keys or longer (one token of
-// 32 / 8 heads over 6,200: 10.6 us in 32 shares, 11.1 in 24, 12.1 in 64).
+// 256 units of 32-64 tiles (16 rows) take 72 us whole, 62 us in 2 shares (1.1
+// waves), 56 us in 3 (1.7), 60 us in 4.  Shares are 192 keys or longer (one token of
+// 32 / 8 heads over 6,200: 9.4 us in 32 shares, 9.7 in 24 and in 64).
 // Without a window lengths can differ widely: shares of about 4,096 keys at most
-// then even them out (64 sequences of 1K-16K tokens, 32 / 8 heads: 249 us in 4
-// shares, 355 us whole; sequences of 700 tokens in the same cache pay 35 us instead of 23), as
+// then even them out (64 sequences of 1K-16K tokens, 32 / 8 heads: 200 us in 4
+// shares, 246 us whole; sequences of 700 tokens in the same cache pay 34 us instead of 19), as
 // long as that makes no more than 16 CTAs an SM.
 //
 // Splits of the others: tiles are few -> one wave.  tcgen05: two CTAs an SM,
@@ -61,7 +64,8 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // 64 x 4, 8 KV heads, 4 sequences of 8,000 tokens: 138 whole, 80 in 2, 71 in 4, 91 in
 // 5, past one wave).  Where whole tiles fill seven tenths of a wave or less and there is
 // no window, lengths can differ, and halves even them out (33-64 x 7, 4 KV heads, 16
-// sequences of 2K-8K: 180 us whole, 150 in 2 or 3).
+// sequences of 2K-8K, longest first: 170 us whole, 133 in 2, 138 in 3; shares of 1,024 to
+// 3,000 keys, so that only long sequences have several, 132 to 162).
 fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int window, int sinks, int num_splits,
                         int kernel, bool tree, ChunkPlan* plan) {
   if (total_q < 0 || q_heads <= 0 || q_heads % c->kv_heads != 0 || window < 0 || sinks < 0 || num_splits < 0)
@@ -78,7 +82,8 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   if (kernel == FP8KV_KERNEL_TENSOR_CORES && !tc_built) return FP8KV_ERR_UNSUPPORTED;
   const int cap = capacity_of(c);
   // (a cache without room has no tensor map; its calls only write zero rows)
-  const bool tc = cap > 0 && (kernel == FP8KV_KERNEL_TENSOR_CORES || (kernel == FP8KV_KERNEL_AUTO && tc_built && rows > 16));
+  const int few = tree && (c->dtype == FP8KV_K8V8 || c->dtype == FP8KV_K16V8) ? 32 : 16;
+  const bool tc = cap > 0 && (kernel == FP8KV_KERNEL_TENSOR_CORES || (kernel == FP8KV_KERNEL_AUTO && tc_built && rows > few));
   plan->kernel = tc ? FP8KV_KERNEL_TENSOR_CORES : FP8KV_KERNEL_WARP_MMA;
   plan->tile_rows = tc ? 128 : rows <= 8 ? 8 : c->head_dim == 128 || rows <= 32 ? 16 : 64;
   plan->tile_tokens = plan->tile_rows / G;

@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
     for (int u = 0; u < KS; ++u)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[w][u][e] = 0.f;
-  // the reference maximum, the sum in units of 2^m, -m - kp, 2^kp, and the
-  // value scale from which on kp has to rise
+  // the reference maximum, the sum in units of 2^m, -m - kp, and 2^kp (a value scale
+  // of 2^(kp + 7) or more lets it rise)
   float m[QC], l[QC], neg_m[QC], up2[QC];
 #pragma unroll
   for (int i = 0; i < QC; ++i) {
