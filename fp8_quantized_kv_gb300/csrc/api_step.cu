@@ -206,7 +206,7 @@ fp8kv_status run_chunk(const void* q, const fp8kv_cache* cache, const int32_t* c
   const int tiles = cu_q ? plan.tiles : cache->batch;
   // (one wave starts at once anyway; under a window sequences are alike)
   const int64_t ctas = (int64_t)tiles * cache->kv_heads * plan.splits;
-  p.longest_first = tree && p.window == 0 && cache->batch > 1 && cache->batch <= 1024 && tiles <= 65535 && ctas <= INT32_MAX &&
+  p.longest_first = tree && p.window == 0 && cache->batch > 1 && cache->batch <= 256 && tiles <= 65535 && ctas <= INT32_MAX &&
                     ctas > 2 * sm_count();
   auto* launch = plan.kernel == FP8KV_KERNEL_TENSOR_CORES ? (tree ? launch_tree_tc : launch_chunk_tc)
                  : plan.tile_rows <= 16 ? (tree ? launch_tree_rows : launch_chunk_rows)

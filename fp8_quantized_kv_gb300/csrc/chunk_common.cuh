@@ -106,15 +106,113 @@ static __device__ __noinline__ void chunk_mark_rows(const int32_t* cu_q, float* 
   for (int64_t r = (int64_t)first * q_heads + threadIdx.x; r < rows; r += blockDim.x) part_l[r * num_splits] = kChunkNoRow;
 }
 
-// The CTA's tile.  Returns false for a number that no tile has.  `lead` (the same
-// for the whole CTA): report errors.
-template <bool TREE = false>
-__device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lead, ChunkTile& t) {
+// What a CTA works at: tile number, KV head, share.  The last tiles of a sequence see
+// the most keys (trees: all see as many): they start first, or, for trees, with
+// `longest_first`, those of long sequences in all their heads and shares.
+struct ChunkPlace {
+  int x, hk, split;
+  int b, q0, q1, len, i0;      // the sequence, where it is known already (else b is -1), and the tile's first query
+};
+
+// Trees: the tile that comes `at`-th when those of long sequences go first, in four
+// classes by length.  Each lane counts the tiles of batch / 32 sequences (eight at
+// most) in 16 bits a class (the host sees to it that they fit).  Returns false where no
+// tile has the number; bad offsets: as the search finds them.
+__device__ __forceinline__ bool tree_order(const ChunkParams& p, int at, ChunkPlace& a) {
+  const int lane = threadIdx.x & 31, B = p.c.batch, T = p.tile_tokens, each = (B + 31) / 32, b0 = lane * each;
+  int cu[9], len[8], longest = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (k >= each) break;
+    cu[k] = p.cu_q[min(b0 + k, B)];
+    len[k] = b0 + k < B ? p.seq_lens[b0 + k] : 0;
+    cu[k + 1] = p.cu_q[min(b0 + k + 1, B)];
+  }
+  bool ok = true;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (k >= each) break;
+    ok = ok && chunk_offsets_ok(p, cu[k], cu[k + 1]);
+    longest = max(longest, len[k]);
+  }
+  if (!__all_sync(0xffffffffu, ok)) {
+    a.x = at;
+    return true;
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  const int l1 = longest >> 2, l2 = longest >> 1, l3 = l1 + l2;
+  auto shift = [&](int k) { return len[k] > l3 ? 0 : len[k] > l2 ? 16 : len[k] > l1 ? 32 : 48; };
+  unsigned long long own = 0;
+  int first = cu[0] / T + b0;
+  auto tiles = [&](int k, int& start) {                // of sequence b0 + k, whose first number is `start`
+    const int end = cu[k + 1] / T + b0 + k + 1, n = b0 + k < B ? end - start : 0;
+    start = end;
+    return n;
+  };
+  int start = first;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (k >= each) break;
+    own += (unsigned long long)(unsigned)tiles(k, start) << shift(k);
+  }
+  unsigned long long upto = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += x;
+  }
+  const unsigned long long all = __shfl_sync(0xffffffffu, upto, 31);
+  int y = at, sh = 0;
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const int n = (int)(all >> sh & 0xFFFF);
+    if (sh == 16 * k && y >= n) { y -= n; sh += 16; }
+  }
+  if (y >= (int)(all >> sh & 0xFFFF)) return false;    // numbers in front of the first sequence, and behind the last
+  int e = (int)((upto - own) >> sh & 0xFFFF), mine = -1, i = 0;
+  start = first;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (k >= each) break;
+    const int n = tiles(k, start);
+    if (shift(k) == sh) {
+      if (y >= e && y < e + n) { mine = k; i = y - e; a.q0 = cu[k]; a.q1 = cu[k + 1]; a.len = len[k]; }
+      e += n;
+    }
+  }
+  const int from = __ffs(__ballot_sync(0xffffffffu, mine >= 0)) - 1;
+  a.b = __shfl_sync(0xffffffffu, b0 + mine, from);
+  a.q0 = __shfl_sync(0xffffffffu, a.q0, from);
+  a.q1 = __shfl_sync(0xffffffffu, a.q1, from);
+  a.len = __shfl_sync(0xffffffffu, a.len, from);
+  a.i0 = __shfl_sync(0xffffffffu, i, from) * T;
+  return a.i0 < a.q1 - a.q0;
+}
+
+// The CTA's place and tile.  Returns false for a number that no tile has.  The same
+// CTA of a tile reports errors (KV head 0, share 0).
+template <bool TREE>
+__device__ __forceinline__ bool chunk_tile(const ChunkParams& p, ChunkPlace& a, ChunkTile& t) {
   const int T = p.tile_tokens;
+  a = {(int)(gridDim.x - 1 - blockIdx.x), (int)blockIdx.y, (int)blockIdx.z, -1, 0, 0, 0, 0};
+  if (TREE && p.longest_first) {
+    const unsigned i = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z), each = gridDim.y * gridDim.z, r = i % each;
+    a.hk = (int)(r % gridDim.y);
+    a.split = (int)(r / gridDim.y);
+    if (!tree_order(p, (int)(i / each), a)) return false;
+  }
+  const bool lead = a.hk == 0 && a.split == 0;
+  const int x = a.x;
   int b = x, q0 = x, q1 = x + 1, i0 = 0;           // one query per sequence
   if (p.cu_q == nullptr && x >= p.c.batch) return false;
   int len = 0;
-  if (p.cu_q != nullptr) {
+  if (TREE && a.b >= 0) {
+    b = a.b;
+    q0 = a.q0;
+    q1 = a.q1;
+    len = a.len;
+    i0 = a.i0;
+  } else if (p.cu_q != nullptr) {
     // there are as many tile numbers as sequences, or more: each looks at one pair of
     // offsets, so that every bad one is reported, found by the search or not
     int a0 = 0, a1 = 0;
@@ -157,62 +255,6 @@ __device__ __forceinline__ bool chunk_tile(const ChunkParams& p, int x, bool lea
   t.first = t.lo / kChunkKeys;
   t.n = t.n_sink + max(0, chunk_tiles(t.kv_end) - t.first);
   return true;
-}
-
-// Trees: the number of the tile that comes `at`-th when those of long sequences go
-// first, in four classes by length; a permutation of the numbers.  Each lane counts
-// the tiles of batch / 32 sequences in 16 bits a class (the host sees to it that they
-// fit).  Bad offsets: as they come.
-__device__ __forceinline__ int tree_order(const ChunkParams& p, int at) {
-  const int lane = threadIdx.x & 31, B = p.c.batch, T = p.tile_tokens, each = (B + 31) / 32;
-  const int b0 = min(B, lane * each), b1 = min(B, b0 + each);
-  int longest = 0;
-#pragma unroll 4
-  for (int b = b0; b < b1; ++b) longest = max(longest, p.seq_lens[b]);
-  const unsigned step = (unsigned)__reduce_max_sync(0xffffffffu, longest) / 4 + 1;
-  auto shift = [&](int b) { return 48 - 16 * (int)((unsigned)max(p.seq_lens[b], 0) / step); };
-  auto start = [&](int b) { return p.cu_q[b] / T + b; };
-  bool ok = true;
-  unsigned long long own = 0;
-#pragma unroll 2
-  for (int b = b0; b < b1; ++b) {
-    ok = ok && chunk_offsets_ok(p, p.cu_q[b], p.cu_q[b + 1]);
-    own += (unsigned long long)(unsigned)(start(b + 1) - start(b)) << shift(b);
-  }
-  if (!__all_sync(0xffffffffu, ok)) return at;
-  unsigned long long upto = own;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long x = __shfl_up_sync(0xffffffffu, upto, d);
-    if (lane >= d) upto += x;
-  }
-  const unsigned long long all = __shfl_sync(0xffffffffu, upto, 31);
-  int y = at, sh = 0;
-  for (; sh < 64 && y >= (int)(all >> sh & 0xFFFF); sh += 16) y -= (int)(all >> sh & 0xFFFF);
-  if (sh == 64) return y < start(0) ? y : at;      // numbers in front of the first sequence, and behind the last
-  int e = (int)((upto - own) >> sh & 0xFFFF), x = -1;
-  for (int b = b0; b < b1; ++b) {
-    if (shift(b) != sh) continue;
-    const int n = start(b + 1) - start(b);
-    if (y >= e && y < e + n) x = start(b) + y - e;
-    e += n;
-  }
-  return __reduce_max_sync(0xffffffffu, x);
-}
-
-// What a CTA works at: tile number, KV head, share.  The last tiles of a sequence see
-// the most keys (trees: all see as many): they start first, or, for trees, with
-// `longest_first`, those of long sequences in all their heads and shares.
-struct ChunkPlace { int x, hk, split; };
-
-template <bool TREE>
-__device__ __forceinline__ ChunkPlace chunk_place(const ChunkParams& p) {
-  ChunkPlace a = {(int)(gridDim.x - 1 - blockIdx.x), (int)blockIdx.y, (int)blockIdx.z};
-  if (TREE && p.longest_first) {
-    const unsigned i = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z), each = gridDim.y * gridDim.z, r = i % each;
-    a = {tree_order(p, (int)(i / each)), (int)(r % gridDim.y), (int)(r / gridDim.y)};
-  }
-  return a;
 }
 
 // Whether every query of the tile sees all keys of the KV tile from key0 on.

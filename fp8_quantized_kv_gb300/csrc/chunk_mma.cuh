@@ -58,10 +58,10 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
   int* rows_sh = reinterpret_cast<int*>(csm + (C::BYTES - 4 * kChunkKeys * 4));   // [4][64] cache rows of coming tiles
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
-  const ChunkPlace at = chunk_place<TREE>(p);
-  const int hk = at.hk, split = at.split;
   ChunkTile t;
-  if (!chunk_tile<TREE>(p, at.x, hk == 0 && split == 0, t)) return;
+  ChunkPlace place;
+  if (!chunk_tile<TREE>(p, place, t)) return;
+  const int hk = place.hk, split = place.split;
   const int per = (t.n + p.num_splits - 1) / p.num_splits;
   const int j0 = min(t.n, split * per), nt = min(t.n, j0 + per) - j0;
   const int G = p.group;

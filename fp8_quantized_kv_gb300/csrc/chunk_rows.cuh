@@ -94,10 +94,10 @@ __global__ void __launch_bounds__(kChunkThreads, QT == 1 ? 4 : 3) chunk_rows(con
   constexpr int KS = D / 16;                   // k steps of QK, m tiles of PV
   extern __shared__ __align__(128) uint8_t rsm[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c4 = lane & 3;
-  const ChunkPlace at = chunk_place<TREE>(p);
-  const int hk = at.hk, split = at.split;
   ChunkTile t;
-  if (!chunk_tile<TREE>(p, at.x, hk == 0 && split == 0, t)) return;
+  ChunkPlace place;
+  if (!chunk_tile<TREE>(p, place, t)) return;
+  const int hk = place.hk, split = place.split;
   const CacheView& c = p.c;
   const int G = p.group;
   // groups of 16 keys: those of the first tokens, then the window's

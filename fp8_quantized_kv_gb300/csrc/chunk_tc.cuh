@@ -38,7 +38,7 @@
 // tile's rows come out as if they saw no key (an empty share, a row of zeros).
 //
 // Measured on one GB300: 3,727 queries over 2,000-8,000 tokens (28 query / 4 KV
-// heads, e4m3, 16-token pages) 280 us, 693 TFLOP/s, 36 % of the measured bf16
+// heads, e4m3, 16-token pages) 272 us, 714 TFLOP/s, 37 % of the measured bf16
 // peak; 6,642 queries under a 512-token window (16 / 2 heads, bf16) 73 us.  What
 // bounds it: the chain of a tile through a softmax warp (TMEM load, scales,
 // maximum, exponentials, P store: about 2,500 cycles with two CTAs on the SM,
@@ -53,7 +53,12 @@
 // preparation warps on alternate tiles (315 us), scores of two tiles by one
 // 128-key product (fewer reads of Q, but the pair waits for both P.V: 309 us),
 // key scales loaded while the scores arrive (287 us), waits with a suspend hint
-// (as fast).
+// (as fast), an empty path for warps without queries (2 % slower), rare paths marked
+// unlikely (as fast).
+// A CTA's start (with another on the SM): 2.3 us to its place, 4 to the query operand,
+// 1.2 to the first scores; its end 4.  The first scales fetched while the operand is
+// made, the operand's rows in a loop and trees' places without the search give the 16
+// sequences of 2K-8K tokens with 33-64 nodes x 7 heads 125 us instead of 133.
 #pragma once
 
 #include <cfloat>
@@ -187,10 +192,10 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
   static_assert(8 * (2 * C::KN + 2 * C::VN + 2 * OPN + C::NCOL + 6) + 8 <= 256 && 256 + 2 * kCtRows <= C::MISC, "they fit");
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const ChunkPlace at = chunk_place<TREE>(p);
-  const int hk = at.hk, split = at.split;
   ChunkTile t;
-  if (!chunk_tile<TREE>(p, at.x, hk == 0 && split == 0, t)) return;
+  ChunkPlace place;
+  if (!chunk_tile<TREE>(p, place, t)) return;
+  const int hk = place.hk, split = place.split;
   const int per = (t.n + p.num_splits - 1) / p.num_splits;
   const int j0 = min(t.n, split * per), n = min(t.n, j0 + per) - j0;
   const CacheView& c = p.c;
@@ -292,30 +297,57 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     umma::tmem_alloc(tslot, 256);
     umma::tmem_relinquish();
   }
+  // Preparation warps: the scales of the first tile's keys and the pages of the second's,
+  // while the query operand is made.  A thread leaves its own in the places of the third
+  // and fourth tile's column scales, which it writes later.
+  float* first_cols = cols + (C::NCOL - 2) * C::CST;
+  if (warp == 8 || warp == 9) {
+    const int k = tid - 256;
+    auto page_of = [&](int j, int& key) {
+      key = j < n ? chunk_key0(t, j0 + j) + k : INT32_MAX;
+      const bool seen = key < t.kv_end && (key >= t.lo || key < p.sinks);
+      if (!seen) key = -1;
+      return c.paged && seen ? c.page_table[(int64_t)t.b * c.max_pages_per_seq + (key >> c.page_shift)] : 0;
+    };
+    int key, key1;
+    int page = page_of(0, key);
+    reinterpret_cast<int*>(first_cols)[C::CST + k] = page_of(1, key1);
+    if (!(C::K16 && C::V16) && key >= 0) {
+      if (page < 0 || page >= c.num_pages) page = 0;          // (reported by the producer)
+      const int64_t row = c.paged ? ((int64_t)page * c.kv_heads + hk) * c.page_size + (key & (c.page_size - 1)) : cont0 + key;
+      if constexpr (!C::K16) first_cols[k] = c.k_scale[row];
+      if constexpr (!C::V16) first_cols[kChunkKeys + k] = c.v_scale[row];
+    }
+  }
   // softmax warps: query rows -> QK operand, 16 lanes a row (16 bytes each), so
   // that a row is read in one piece; all eight loads of a thread in flight
   const int hf = (tid >> 7) & 1;                  // softmax warps: which half of its lanes, and of O's dims
   if (warp < 8) {
     const int ch = tid & 15;
     if (tid < kCtRows) own_sh[tid] = chunk_own(t, t.pos0 + tid / G, j0, j0 + n);
+    const int inv_g = (65536 + G - 1) / G;        // row / G for rows below 128, groups up to 16
     uint4 x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int row = 16 * i + (tid >> 4), tk = row / G;
+      const int row = 16 * i + (tid >> 4), tk = row * inv_g >> 16;
       x[i] = make_uint4(0, 0, 0, 0);
       if (tk < t.ntok && row < p.tile_tokens * G)
         x[i] = reinterpret_cast<const uint4*>(p.q + ((int64_t)(t.row0 + tk) * p.q_heads + hk * G + (row - tk * G)) * D)[ch];
     }
-#pragma unroll
+    // (a loop: unrolled, code that runs once misses the instruction cache)
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) {
       const int row = 16 * i + (tid >> 4);
+      const uint4 x0 = x[0];
+#pragma unroll
+      for (int u = 0; u < 7; ++u) x[u] = x[u + 1];
       if constexpr (C::K16) {
-        uint4 w = x[i];
+        uint4 w = x0;
         if (p.scale_log2 < 0.f) w = make_uint4(w.x ^ 0x80008000u, w.y ^ 0x80008000u, w.z ^ 0x80008000u, w.w ^ 0x80008000u);
         if (p.scale_log2 == 0.f) w = make_uint4(times_zero(w.x), times_zero(w.y), times_zero(w.z), times_zero(w.w));
         *reinterpret_cast<uint4*>(qop + (ch >> 3) * (kCtRows * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) = w;
       } else {
-        const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        const uint32_t w[4] = {x0.x, x0.y, x0.z, x0.w};
         float f[8], amax = 0.f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -453,8 +485,8 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
     // ------------------------------------------------------------ preparation
     const int kr = tid - 256;                     // this thread's key of the tile
     // its scales come straight from the cache, a tile ahead, and the page id
-    // (paged) two tiles ahead
-    float next_k = 0.f, next_v = 0.f;
+    // (paged) two tiles ahead (the first ones from above)
+    float next_k = C::K16 ? 0.f : first_cols[kr], next_v = C::V16 ? 0.f : first_cols[kChunkKeys + kr];
     auto key_seen = [&](int j) {
       const int key = j < n ? chunk_key0(t, j0 + j) + kr : INT32_MAX;
       return key < t.kv_end && (key >= t.lo || key < p.sinks) ? key : -1;
@@ -471,8 +503,7 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
       if constexpr (!C::K16) next_k = c.k_scale[row];
       if constexpr (!C::V16) next_v = c.v_scale[row];
     };
-    fetch_scales(0, fetch_page(0));
-    int page = fetch_page(1);
+    int page = reinterpret_cast<const int*>(first_cols)[C::CST + kr];
     for (int j = 0; j < n; ++j) {
       const int vs = j % C::VN, cb = j % C::NCOL, key0 = chunk_key0(t, j0 + j);
       bool ok = wait_fast(&vfull[vs], (j / C::VN) & 1, abort_flag);

@@ -133,7 +133,7 @@ struct ChunkParams {
   const uint32_t* masks;     // [total_q][mask_words] nodes that each node sees
   const int32_t* tree_pos;   // [total_q] positions in the text (read under a window only)
   int mask_words;
-  int longest_first;         // CTAs in the order of their sequences' lengths (chunk_place)
+  int longest_first;         // CTAs in the order of their sequences' lengths (tree_order)
 };
 
 cudaError_t launch_quantize(const void* x, int64_t rows, int head_dim, uint8_t* codes, float* scales,

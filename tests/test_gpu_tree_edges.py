@@ -191,7 +191,8 @@ def many_trees(seed, batch, context, nodes):
 
 @pytest.mark.parametrize("dtype,D,kernel,batch,Hkv,nodes,splits", [
     ("k8v8", 128, "warp_mma", 40, 2, 5, 4), ("k16v16", 64, "warp_mma", 33, 1, 40, 8), ("k8v8", 128, "tensor_cores", 31, 2, 40, 4),
-    ("k8v16", 128, "warp_mma", 300, 1, 3, 2), ("k8v8", 64, "auto", 1024, 1, 2, 1), ("k8v8", 64, "auto", 1025, 1, 2, 1),
+    ("k8v16", 128, "warp_mma", 300, 1, 3, 2), ("k8v8", 64, "auto", 1024, 1, 2, 1), ("k8v8", 64, "auto", 1025, 1, 2, 1), ("k8v8", 128, "auto", 256, 1, 4, 2),
+    ("k8v8", 64, "auto", 257, 1, 2, 2), ("k16v16", 128, "warp_mma", 65, 2, 3, 3),
     ("k16v8", 128, "tensor_cores", 2, 4, 1024, 3)])
 def test_long_sequences_first(dtype, D, kernel, batch, Hkv, nodes, splits):
     """More tiles than run at once, in the order of the sequences' lengths: every row is some tile's."""
