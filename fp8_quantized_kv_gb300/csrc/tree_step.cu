@@ -9,12 +9,15 @@ namespace fp8kv {
 // Masks and positions.  Row i of sequence b: bits of node i and of its ancestors,
 // and ctx + depth.  A thread walks up from its node in shared memory (parents come
 // before their children, so the walk ends) and writes its words from the highest
-// down: ancestors only get lower.  Latency bounds it: offsets, parents, then a
-// step of the walk every 30 cycles or so.
+// down: ancestors only get lower.  Latency bounds it: offsets, parents, then the
+// steps of the walk, which read four ancestors at once (300 trees of up to 256 nodes
+// on 40 levels: 5.8 us, one at a time 6.6; 64 trees of 24-64 nodes: 2.5 and 2.3).
 constexpr int kTreeThreads = 256;
 
 __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTablesParams p) {
   __shared__ int16_t up[kTreeMaxNodes];
+  __shared__ short2 two[kTreeMaxNodes];            // parent and its parent, -1: none
+  __shared__ short4 four[kTreeMaxNodes];
   const int tid = threadIdx.x;
   if (blockIdx.x >= p.batch) {                     // rows that belong to no sequence
     const int first = min(max(p.cu[0], 0), p.rows), end = min(max(p.cu[p.batch], first), p.rows);
@@ -48,13 +51,28 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTab
   if (bad) raise_error(p.err, FP8KV_DEVERR_BAD_TREE);
   __syncthreads();
   for (int i = tid; i < n; i += kTreeThreads) {
+    const int16_t a = up[i];
+    two[i] = make_short2(a, a >= 0 ? up[a] : -1);
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kTreeThreads) {
+    const short2 a = two[i], b = a.y >= 0 ? two[a.y] : make_short2(-1, -1);
+    four[i] = make_short4(a.x, a.y, b.x, b.y);
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kTreeThreads) {
     uint32_t* row = p.masks + (int64_t)(q0 + i) * p.words;
     int w = p.words - 1, depth = -1;
     uint32_t bits = 0;
-    for (int a = i; a >= 0; a = up[a], ++depth) {
+    auto sees = [&](int a) {                       // (-1: no more)
+      if (a < 0) return false;
       for (; w > a >> 5; --w) { row[w] = bits; bits = 0; }
       bits |= 1u << (a & 31);
-    }
+      ++depth;
+      return true;
+    };
+    sees(i);
+    for (short4 a = four[i]; sees(a.x) && sees(a.y) && sees(a.z) && sees(a.w); a = four[a.w]) {}
     for (; w >= 0; --w) { row[w] = bits; bits = 0; }
     p.pos[q0 + i] = len - n + depth;
   }
