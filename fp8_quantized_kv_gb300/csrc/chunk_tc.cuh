@@ -777,6 +777,8 @@ __global__ void __launch_bounds__(kCtThreads, 2) chunk_tc(const __grid_constant_
         st[2 * kCtRows + row] = up[i];
       }
     }
+    // (the joining kernel may be set up; without splits the next kernel is a stranger)
+    if (p.num_splits > 1) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     failed = softmax_any(failed);                 // (a barrier of the eight warps)
     if (failed && tid == 0) raise_error(p.err, FP8KV_DEVERR_TIMEOUT);
     const bool empty = failed || n == 0;          // O and the quads' values are not read
