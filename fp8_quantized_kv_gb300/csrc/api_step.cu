@@ -64,8 +64,8 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // 64 x 4, 8 KV heads, 4 sequences of 8,000 tokens: 138 whole, 80 in 2, 71 in 4, 91 in
 // 5, past one wave).  Where whole tiles fill seven tenths of a wave or less and there is
 // no window, lengths can differ, and halves even them out (33-64 x 7, 4 KV heads, 16
-// sequences of 2K-8K, longest first: 170 us whole, 133 in 2, 138 in 3; shares of 1,024 to
-// 3,000 keys, so that only long sequences have several, 132 to 162).
+// sequences of 2K-8K, longest first: 168 us whole, 120 in 2, 126 in 3; shares of 1,024 to
+// 3,000 keys or more, so that only long sequences have several, were no better).
 fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int window, int sinks, int num_splits,
                         int kernel, bool tree, ChunkPlan* plan) {
   if (total_q < 0 || q_heads <= 0 || q_heads % c->kv_heads != 0 || window < 0 || sinks < 0 || num_splits < 0)

@@ -26,7 +26,7 @@
 // Measured on one GB300 (64 sequences, 32 query / 8 KV heads, head dim 128,
 // e4m3, 16-token pages, device time): a 1,024-token window 30 us (140 MB: 4.6
 // TB/s, 68 % of the measured copy rate); whole contexts of 1K-16K tokens, 2-4 tokens
-// each, 186 us of a call's 194 (1.06 GB: 5.7 TB/s, 84 %).  What is left is the fixed
+// each, 181 us of a call's 189 (1.06 GB: 5.8 TB/s, 86 %).  What is left is the fixed
 // part (about 5 us to find the tile, load the first groups and join) and latency: three
 // to four warps a scheduler, 470 instructions a group of sixteen rows, 64 of them the
 // conversion of 4,096 codes.  On the way there (the window): 58 us with
