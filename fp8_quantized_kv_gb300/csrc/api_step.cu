@@ -39,7 +39,8 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // them; 256-512 x 8, 4 sequences: 0.71 ms against 1.33), head dim 64 does up to 32
 // rows (2-4 x 8 of 64 sequences of 2K-4K, bf16: 56 us against 71 on 64-row tiles at
 // the best split count), with more it runs on the warp-level kernel (256-512 x 8 over
-// 4K-8K, 4 sequences: 0.56 ms against 0.70; around 64 rows either can be faster).
+// 4K-8K, 4 sequences: 0.39 ms; before both were made faster 0.56 against 0.70, and around
+// 64 rows either could be ahead).
 //
 // Splits of the few-row kernel: an SM holds four of its CTAs (three of 16 rows,
 // or of 32 KiB stages), and a call takes as many waves of them as they need,
@@ -55,8 +56,8 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 //
 // Splits of the others: tiles are few -> one wave.  tcgen05: two CTAs an SM,
 // shares of 512 keys or longer.  Warp-level kernel: three an SM (by their
-// registers) and 128 keys (32-64 x 8 of 2 sequences of 2K-4K tokens: 36 us in 4
-// shares, 31 us in 6, 37 us in 9, past one wave).
+// registers) and 128 keys (32-64 x 8 of 2 sequences of 2K-4K tokens, when it was slower:
+// 36 us in 4 shares, 31 us in 6, 37 us in 9, past one wave).
 // Trees on tcgen05: tiles see whole contexts, and two CTAs of an SM slow each other
 // down, so one CTA an SM with shares of 256 keys or longer, or two with 1,024 or
 // longer, whichever is more shares (5-31 nodes x 8 heads, 2 KV heads, 16 sequences,
@@ -66,6 +67,9 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // no window, lengths can differ, and halves even them out (33-64 x 7, 4 KV heads, 16
 // sequences of 2K-8K, longest first: 168 us whole, 120 in 2, 126 in 3; shares of 1,024 to
 // 3,000 keys or more, so that only long sequences have several, were no better).
+// Trees on the warp-level kernel, no window: up to four shares while that makes no more
+// than eight CTAs an SM, for the same reason (33-64 x 8, 4 KV heads, 2K-8K: 16 sequences
+// 200 us whole, 169 in 2; 8 sequences 93 in 2, 82 in 4).
 fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int window, int sinks, int num_splits,
                         int kernel, bool tree, ChunkPlan* plan) {
   if (total_q < 0 || q_heads <= 0 || q_heads % c->kv_heads != 0 || window < 0 || sinks < 0 || num_splits < 0)
@@ -113,6 +117,10 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
         if (window == 0 && want <= 1 && kv_tiles >= 32 && 14 * units <= 10 * 2 * sms) want = 2;
       } else {
         want = tc ? shares(2 * sms, 8) : shares(3 * sms, 2);
+        if (tree && window == 0 && kv_tiles >= 32) {
+          const int64_t more = shares(8 * sms, 2) < 4 ? shares(8 * sms, 2) : 4;
+          if (more > want) want = more;
+        }
       }
     } else if (units > 0) {
       const bool wide = c->head_dim == 128 && c->dtype == FP8KV_K16V16;

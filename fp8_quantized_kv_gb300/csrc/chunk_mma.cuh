@@ -32,7 +32,15 @@
 // rows that no query of the tile sees are not read at all, and in a tile that
 // only some of the queries see, non-finite values are set aside and added
 // to the queries that see them (a zero weight times NaN would not be zero).
+//
+// Measured on one GB300 (256-512 tokens x 8 heads of 4 sequences of 4K-8K tokens, 4 KV
+// heads, e4m3): 394 us, issue slots bound it; 490 us while one form of the loop served
+// tiles that every query sees and others alike.  Trees of 33-64 nodes x 8 heads, 16
+// sequences of 2K-8K tokens: 217 us in that shape (290), two CTAs an SM at 255 registers;
+// three at 168 with spills 221.
 #pragma once
+
+#include <type_traits>
 
 #include "chunk_common.cuh"
 
@@ -210,192 +218,198 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_mma(const ChunkParams p) 
         for (int e = 0; e < 4; ++e) s[n][e] *= p.scale_log2;
       }
     }
-    const bool part = !chunk_all_seen<TREE>(p, t, key0);
-    unsigned long long bits[2] = {0, 0};
-    if (TREE && part) {
+    // `part`: not every query sees all 64 keys (a form of its own: the other tiles then
+    // neither ask who sees what nor for values that must be set aside)
+    auto weigh = [&](auto cut) {
+      constexpr bool part = decltype(cut)::value;
+      unsigned long long bits[2] = {0, 0};
+      if (TREE && part) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) bits[i] = tree_seen_mask(p, t, qpos[i], key0);
-    }
-    auto sees = [&](int i, int key) {          // row i, key `key` of the tile (asked where it is seen in part)
-      return TREE ? (bool)(bits[i] >> key & 1) : chunk_sees(p, qpos[i], key0 + key);
-    };
-    if (part) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (!sees(e >> 1, 8 * n + 2 * c4 + (e & 1))) s[n][e] = -INFINITY;
-    }
-    // running maximum and weights
-    float alpha[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float mt = -INFINITY;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) mt = fmaxf(mt, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
-      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-      mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-      const float mn = fmaxf(m[i], mt), ref = mn == -INFINITY ? 0.f : mn;
-      alpha[i] = m[i] == -INFINITY ? 1.f : ex2_ftz(m[i] - ref);   // (nothing yet: O and l are zero)
-      m[i] = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        s[n][2 * i] = ex2_ftz(s[n][2 * i] - ref);
-        s[n][2 * i + 1] = ex2_ftz(s[n][2 * i + 1] - ref);
-        sum += s[n][2 * i] + s[n][2 * i + 1];
+        for (int i = 0; i < 2; ++i) bits[i] = tree_seen_mask(p, t, qpos[i], key0);
       }
-      l[i] = l[i] * alpha[i] + sum;
-    }
-    if constexpr (!VB16) {
-      // the largest value scale among the keys that the row sees
-      auto finite = [](float v) { return v < INFINITY ? v : 0.f; };
-      float vm[2];
-      if (!part) {
-        vm[0] = vm[1] = warp_max_f32(fmaxf(finite(vsc[lane]), finite(vsc[lane + 32])));
-      } else {
+      auto sees = [&](int i, int key) {          // row i, key `key` of the tile (asked where it is seen in part)
+        return TREE ? (bool)(bits[i] >> key & 1) : chunk_sees(p, qpos[i], key0 + key);
+      };
+      if (part) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          vm[i] = 0.f;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int kc = 8 * n + 2 * c4 + e;
-              if (sees(i, kc)) vm[i] = fmaxf(vm[i], finite(vsc[kc]));
-            }
-          vm[i] = fmaxf(vm[i], __shfl_xor_sync(0xffffffffu, vm[i], 1));
-          vm[i] = fmaxf(vm[i], __shfl_xor_sync(0xffffffffu, vm[i], 2));
-        }
+          for (int e = 0; e < 4; ++e)
+            if (!sees(e >> 1, 8 * n + 2 * c4 + (e & 1))) s[n][e] = -INFINITY;
       }
-      float vf[2];
+      // running maximum and weights
+      float alpha[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int need = max(-100, min(100, ((__float_as_int(vm[i]) >> 23) & 0xFF) - 127 - 14));   // vm 2^-need < 2^15
-        if (vm[i] > 0.f && need > kp[i]) {
-          if (kp[i] > -1000) alpha[i] *= pow2_diff((float)(kp[i] - need), 0);
-          kp[i] = need;
+        float mt = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mt = fmaxf(mt, fmaxf(s[n][2 * i], s[n][2 * i + 1]));
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+        const float mn = fmaxf(m[i], mt), ref = mn == -INFINITY ? 0.f : mn;
+        alpha[i] = m[i] == -INFINITY ? 1.f : ex2_ftz(m[i] - ref);   // (nothing yet: O and l are zero)
+        m[i] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          s[n][2 * i] = ex2_ftz(s[n][2 * i] - ref);
+          s[n][2 * i + 1] = ex2_ftz(s[n][2 * i + 1] - ref);
+          sum += s[n][2 * i] + s[n][2 * i + 1];
         }
-        vf[i] = kp[i] > -1000 ? pow2i(-kp[i]) : 1.f;
+        l[i] = l[i] * alpha[i] + sum;
       }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float2 v = *reinterpret_cast<const float2*>(vsc + 8 * n + 2 * c4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float w = s[n][e] * ((e & 1 ? v.y : v.x) * vf[e >> 1]);
-          // a scale that is not finite would turn an unseen key's zero into NaN
-          s[n][e] = part && !sees(e >> 1, 8 * n + 2 * c4 + (e & 1)) ? 0.f : w;
-        }
-      }
-    }
-    if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        o[n][0] *= alpha[0]; o[n][1] *= alpha[0];
-        o[n][2] *= alpha[1]; o[n][3] *= alpha[1];
-      }
-    }
-    // a tile seen by some of its queries only: are there values that must not
-    // meet the others' zero weights?
-    bool aside = false;
-    if (part && (TREE || t.ntok > 1)) {
-      constexpr int VC = C::VB / 16;
-      for (int e = lane; e < kChunkKeys * VC; e += 32) {
-        const uint4 w = *reinterpret_cast<const uint4*>(vst + e / VC * C::VB + (e % VC) * 16);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if constexpr (VB16)
-            aside = aside || (ww[u] & 0x7F800000u) == 0x7F800000u || (ww[u] & 0x7F80u) == 0x7F80u;
-          else
-            aside = aside || ((((ww[u] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0);
-        }
-      }
-      aside = __any_sync(0xffffffffu, aside);
-    }
-    // O += P V: 16 keys at a time
-    const uint32_t vaddr = umma::smem_u32(vst);
-#pragma unroll
-    for (int j = 0; j < kChunkKeys / 16; ++j) {
-      const uint32_t pa[4] = {pack16<VB16>(s[2 * j][0], s[2 * j][1]), pack16<VB16>(s[2 * j][2], s[2 * j][3]),
-                              pack16<VB16>(s[2 * j + 1][0], s[2 * j + 1][1]), pack16<VB16>(s[2 * j + 1][2], s[2 * j + 1][3])};
-      const int vr = 16 * j + (lane & 15);       // row this lane addresses for ldmatrix
-#pragma unroll
-      for (int u = 0; u < C::VB / 32; ++u) {
-        uint32_t r[4];
-        ldsm_x4_trans(vaddr + vr * C::VB + v_chunk<C::VB>(2 * u + (lane >> 4), vr) * 16, r);
-        if constexpr (VB16) {
-          if (aside) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) r[k] = SetAside<true>(r[k]).clean;
-          }
-          mma16816<true>(o[2 * u], pa, r[0], r[1]);
-          mma16816<true>(o[2 * u + 1], pa, r[2], r[3]);
+      if constexpr (!VB16) {
+        // the largest value scale among the keys that the row sees
+        auto finite = [](float v) { return v < INFINITY ? v : 0.f; };
+        float vm[2];
+        if (!part) {
+          vm[0] = vm[1] = warp_max_f32(fmaxf(finite(vsc[lane]), finite(vsc[lane + 32])));
         } else {
-          // two keys x two dims of e4m3 codes -> the two keys' pairs of each dim
 #pragma unroll
-          for (int k = 0; k < 4; ++k) r[k] = __byte_perm(r[k], 0, 0x3120);
-          uint32_t b[8];
+          for (int i = 0; i < 2; ++i) {
+            vm[i] = 0.f;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            b[2 * k] = e4m3x2_to_f16x2((uint16_t)r[k]);
-            b[2 * k + 1] = e4m3x2_to_f16x2((uint16_t)(r[k] >> 16));
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int kc = 8 * n + 2 * c4 + e;
+                if (sees(i, kc)) vm[i] = fmaxf(vm[i], finite(vsc[kc]));
+              }
+            vm[i] = fmaxf(vm[i], __shfl_xor_sync(0xffffffffu, vm[i], 1));
+            vm[i] = fmaxf(vm[i], __shfl_xor_sync(0xffffffffu, vm[i], 2));
           }
-          if (aside) {
+        }
+        float vf[2];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) b[k] = SetAside<false>(b[k]).clean;
+        for (int i = 0; i < 2; ++i) {
+          const int need = max(-100, min(100, ((__float_as_int(vm[i]) >> 23) & 0xFF) - 127 - 14));   // vm 2^-need < 2^15
+          if (vm[i] > 0.f && need > kp[i]) {
+            if (kp[i] > -1000) alpha[i] *= pow2_diff((float)(kp[i] - need), 0);
+            kp[i] = need;
           }
-          mma16816<false>(o[4 * u], pa, b[0], b[2]);
-          mma16816<false>(o[4 * u + 1], pa, b[1], b[3]);
-          mma16816<false>(o[4 * u + 2], pa, b[4], b[6]);
-          mma16816<false>(o[4 * u + 3], pa, b[5], b[7]);
+          vf[i] = kp[i] > -1000 ? pow2i(-kp[i]) : 1.f;
         }
-      }
-    }
-    if (aside) {                               // rare: which queries see the values set aside
 #pragma unroll
-      for (int j = 0; j < kChunkKeys / 16; ++j) {
-        uint32_t see[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int key = 16 * j + 8 * (k >> 1) + 2 * c4;
-          see[k] = pack16<VB16>(sees(k & 1, key) ? 1.f : 0.f, sees(k & 1, key + 1) ? 1.f : 0.f);
-        }
-        auto add = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
-          const SetAside<VB16> x(b0), y(b1);
-          float nan[4] = {0.f, 0.f, 0.f, 0.f}, pinf[4] = {0.f, 0.f, 0.f, 0.f}, ninf[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816<VB16>(nan, see, x.nan, y.nan);
-          mma16816<VB16>(pinf, see, x.pinf, y.pinf);
-          mma16816<VB16>(ninf, see, x.ninf, y.ninf);
+        for (int n = 0; n < NT; ++n) {
+          const float2 v = *reinterpret_cast<const float2*>(vsc + 8 * n + 2 * c4);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (pinf[e] > 0.f) acc[e] += INFINITY;
-            if (ninf[e] > 0.f) acc[e] -= INFINITY;
-            if (nan[e] > 0.f) acc[e] = NAN;
+            const float w = s[n][e] * ((e & 1 ? v.y : v.x) * vf[e >> 1]);
+            // a scale that is not finite would turn an unseen key's zero into NaN
+            s[n][e] = part && !sees(e >> 1, 8 * n + 2 * c4 + (e & 1)) ? 0.f : w;
           }
-        };
-        const int vr = 16 * j + (lane & 15);
+        }
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[n][0] *= alpha[0]; o[n][1] *= alpha[0];
+          o[n][2] *= alpha[1]; o[n][3] *= alpha[1];
+        }
+      }
+      // a tile seen by some of its queries only: are there values that must not
+      // meet the others' zero weights?
+      bool aside = false;
+      if (part && (TREE || t.ntok > 1)) {
+        constexpr int VC = C::VB / 16;
+        for (int e = lane; e < kChunkKeys * VC; e += 32) {
+          const uint4 w = *reinterpret_cast<const uint4*>(vst + e / VC * C::VB + (e % VC) * 16);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if constexpr (VB16)
+              aside = aside || (ww[u] & 0x7F800000u) == 0x7F800000u || (ww[u] & 0x7F80u) == 0x7F80u;
+            else
+              aside = aside || ((((ww[u] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0);
+          }
+        }
+        aside = __any_sync(0xffffffffu, aside);
+      }
+      // O += P V: 16 keys at a time
+      const uint32_t vaddr = umma::smem_u32(vst);
+#pragma unroll
+      for (int j = 0; j < kChunkKeys / 16; ++j) {
+        const uint32_t pa[4] = {pack16<VB16>(s[2 * j][0], s[2 * j][1]), pack16<VB16>(s[2 * j][2], s[2 * j][3]),
+                                pack16<VB16>(s[2 * j + 1][0], s[2 * j + 1][1]), pack16<VB16>(s[2 * j + 1][2], s[2 * j + 1][3])};
+        const int vr = 16 * j + (lane & 15);       // row this lane addresses for ldmatrix
 #pragma unroll
         for (int u = 0; u < C::VB / 32; ++u) {
           uint32_t r[4];
           ldsm_x4_trans(vaddr + vr * C::VB + v_chunk<C::VB>(2 * u + (lane >> 4), vr) * 16, r);
           if constexpr (VB16) {
-            add(o[2 * u], r[0], r[1]);
-            add(o[2 * u + 1], r[2], r[3]);
+            if (aside) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) r[k] = SetAside<true>(r[k]).clean;
+            }
+            mma16816<true>(o[2 * u], pa, r[0], r[1]);
+            mma16816<true>(o[2 * u + 1], pa, r[2], r[3]);
           } else {
+            // two keys x two dims of e4m3 codes -> the two keys' pairs of each dim
 #pragma unroll
             for (int k = 0; k < 4; ++k) r[k] = __byte_perm(r[k], 0, 0x3120);
+            uint32_t b[8];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              add(o[4 * u + 2 * k], e4m3x2_to_f16x2((uint16_t)r[2 * k]), e4m3x2_to_f16x2((uint16_t)r[2 * k + 1]));
-              add(o[4 * u + 2 * k + 1], e4m3x2_to_f16x2((uint16_t)(r[2 * k] >> 16)),
-                  e4m3x2_to_f16x2((uint16_t)(r[2 * k + 1] >> 16)));
+            for (int k = 0; k < 4; ++k) {
+              b[2 * k] = e4m3x2_to_f16x2((uint16_t)r[k]);
+              b[2 * k + 1] = e4m3x2_to_f16x2((uint16_t)(r[k] >> 16));
+            }
+            if (aside) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) b[k] = SetAside<false>(b[k]).clean;
+            }
+            mma16816<false>(o[4 * u], pa, b[0], b[2]);
+            mma16816<false>(o[4 * u + 1], pa, b[1], b[3]);
+            mma16816<false>(o[4 * u + 2], pa, b[4], b[6]);
+            mma16816<false>(o[4 * u + 3], pa, b[5], b[7]);
+          }
+        }
+      }
+      if (aside) {                               // rare: which queries see the values set aside
+#pragma unroll
+        for (int j = 0; j < kChunkKeys / 16; ++j) {
+          uint32_t see[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int key = 16 * j + 8 * (k >> 1) + 2 * c4;
+            see[k] = pack16<VB16>(sees(k & 1, key) ? 1.f : 0.f, sees(k & 1, key + 1) ? 1.f : 0.f);
+          }
+          auto add = [&](float (&acc)[4], uint32_t b0, uint32_t b1) {
+            const SetAside<VB16> x(b0), y(b1);
+            float nan[4] = {0.f, 0.f, 0.f, 0.f}, pinf[4] = {0.f, 0.f, 0.f, 0.f}, ninf[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816<VB16>(nan, see, x.nan, y.nan);
+            mma16816<VB16>(pinf, see, x.pinf, y.pinf);
+            mma16816<VB16>(ninf, see, x.ninf, y.ninf);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (pinf[e] > 0.f) acc[e] += INFINITY;
+              if (ninf[e] > 0.f) acc[e] -= INFINITY;
+              if (nan[e] > 0.f) acc[e] = NAN;
+            }
+          };
+          const int vr = 16 * j + (lane & 15);
+#pragma unroll
+          for (int u = 0; u < C::VB / 32; ++u) {
+            uint32_t r[4];
+            ldsm_x4_trans(vaddr + vr * C::VB + v_chunk<C::VB>(2 * u + (lane >> 4), vr) * 16, r);
+            if constexpr (VB16) {
+              add(o[2 * u], r[0], r[1]);
+              add(o[2 * u + 1], r[2], r[3]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) r[k] = __byte_perm(r[k], 0, 0x3120);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                add(o[4 * u + 2 * k], e4m3x2_to_f16x2((uint16_t)r[2 * k]), e4m3x2_to_f16x2((uint16_t)r[2 * k + 1]));
+                add(o[4 * u + 2 * k + 1], e4m3x2_to_f16x2((uint16_t)(r[2 * k] >> 16)),
+                    e4m3x2_to_f16x2((uint16_t)(r[2 * k + 1] >> 16)));
+              }
             }
           }
         }
       }
-    }
+    };
+    if (chunk_all_seen<TREE>(p, t, key0)) weigh(std::false_type());
+    else weigh(std::true_type());
     if (tid < kChunkKeys) rows_sh[((it + C::NS) & 3) * kChunkKeys + tid] = find_row(it + C::NS, next_page);
   }
 
