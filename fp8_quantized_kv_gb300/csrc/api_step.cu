@@ -63,10 +63,12 @@ struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 // longer, whichever is more shares (5-31 nodes x 8 heads, 2 KV heads, 16 sequences,
 // window 1,024: 32 us whole, 26 in 2 shares, 29 in 4; of 4 sequences 32, 25 and 20;
 // 64 x 4, 8 KV heads, 4 sequences of 8,000 tokens: 138 whole, 80 in 2, 71 in 4, 91 in
-// 5, past one wave).  Where whole tiles fill seven tenths of a wave or less and there is
-// no window, lengths can differ, and halves even them out (33-64 x 7, 4 KV heads, 16
-// sequences of 2K-8K, longest first: 168 us whole, 120 in 2, 126 in 3; shares of 1,024 to
-// 3,000 keys or more, so that only long sequences have several, were no better).
+// 5, past one wave).  Without a window lengths can differ, and shares even them out: two
+// where whole tiles fit one wave (12-24 x 4, 8 KV heads, 32 sequences of 1K-8K: 156 us
+// whole, 132 in 2; past one wave, 33-64 x 7 of 32 sequences of 2K-8K, 197 and 221), three
+// from 2.5 CTAs a tile on (33-64 x 8, 8 sequences of 1K-16K: 177 in 2, 138 in 3; with 1.5
+// CTAs a tile, 33-64 x 7 of 16 sequences of 2K-8K, 168 whole, 120 in 2, 126 in 3).  Shares
+// of 1,024 to 3,000 keys or more, so that only long sequences have several, were no better.
 // Trees on the warp-level kernel, no window: up to four shares while that makes no more
 // than eight CTAs an SM, for the same reason (33-64 x 8, 4 KV heads, 2K-8K: 16 sequences
 // 200 us whole, 169 in 2; 8 sequences 93 in 2, 82 in 4).
@@ -114,7 +116,8 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
       if (tc && tree) {
         want = shares(sms, 4);
         if (shares(2 * sms, 16) > want) want = shares(2 * sms, 16);
-        if (window == 0 && want <= 1 && kv_tiles >= 32 && 14 * units <= 10 * 2 * sms) want = 2;
+        if (window == 0 && want <= 1 && kv_tiles >= 32 && units <= 2 * sms) want = 2;
+        if (window == 0 && want == 2 && kv_tiles >= 48 && 5 * units <= 2 * 2 * sms) want = 3;
       } else {
         want = tc ? shares(2 * sms, 8) : shares(3 * sms, 2);
         if (tree && window == 0 && kv_tiles >= 32) {
