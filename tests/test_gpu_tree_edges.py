@@ -230,3 +230,49 @@ def test_node_0_with_a_bad_parent_is_accepted():
     tokens = torch.ones(3, dtype=torch.int64, device="cuda")
     got = fk.fp8kv_tree_accept([cache], _i32([0, 0, 1]), tokens, tokens, _i32([0, 3]), _i32([40]), 4)
     assert fk.fp8kv_get_device_error() == fk.DEVERR_BAD_TREE and got["path"].tolist() == [[0, 1, 2, -1]]
+
+
+@pytest.mark.parametrize("dtype,D,nodes,batch", [("k8v8", 128, (30, 60), 24), ("k16v8", 128, (30, 60), 24), ("k16v16", 128, (2, 5), 60),
+                                                 ("k8v8", 64, (30, 60), 24), ("mxk8v8", 128, (3, 9), 40)])
+def test_large_calls_repeat_and_follow_lengths(dtype, D, nodes, batch):
+    """More tiles than run at once: every run gives the same bits, on two streams at
+    once too, and a captured call orders its tiles by the lengths of each replay."""
+    r = random.Random(batch + D)
+    ctx, new = [r.randint(100, 2500) for _ in range(batch)], [r.randint(*nodes) for _ in range(batch)]
+    cache, lens, cu, q, masks, *_ = make_step(dtype, D, 16, 4, ctx, new, 16, seed=87, pad=0)
+    lens_t, cu_t, outs = _i32(lens), _i32(cu), [torch.empty_like(q) for _ in range(3)]
+    need = fk.fp8kv_tree_workspace_bytes(cache, q.shape[0], 16)
+    spaces = [torch.empty(max(need, 16), dtype=torch.uint8, device="cuda") for _ in range(3)]
+
+    def call(i, stream=None):
+        return fk.fp8kv_tree_attention(q, cache, cu_t, lens_t, masks, out=outs[i], workspace=spaces[i], stream=stream)
+
+    want = call(0).clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            call(i, s)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(2)
+    for shorter in ([n - min(c, 16 * (b % 5)) for b, (n, c) in enumerate(zip(lens, ctx))], [n if b % 2 else m + 7
+                                                                                           for b, (n, m) in enumerate(zip(lens, new))]):
+        lens_t.copy_(_i32(shorter))
+        graph.replay()
+        assert torch.equal(outs[2], call(0))
+    assert fk.fp8kv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("down", [-100, -60, 90])
+@pytest.mark.parametrize("D,nodes,kernel", [(128, 2, "warp_mma"), (128, 9, "warp_mma"), (128, 40, "tensor_cores"), (64, 60, "warp_mma")])
+def test_value_scales_far_from_one(D, nodes, kernel, down):
+    cache, lens, cu, q, masks, seen, pos, _ = make_step("k8v8", D, 4, 2, [300, 0, 41], [nodes, 1, nodes], 16, seed=89)
+    cache.v_scale.mul_(2.0 ** down)
+    cache.v_scale.view(-1)[::7] = 0
+    out = fk.fp8kv_tree_attention(q, cache, _i32(cu), _i32(lens), masks, kernel=kernel, out_dtype=torch.float32)
+    assert fk.fp8kv_get_device_error() == 0
+    want = tree_definition(q, cache_values(cache, lens), cu, lens, seen, pos, 0, 0, 1 / math.sqrt(D))
+    check(out, cache, want, slice(0, cu[-1]), kernel)
