@@ -201,6 +201,14 @@ __device__ __forceinline__ void store_rows(const MatmulParams& p, uint8_t* buf, 
 // Where the last wave would leave half of the pairs or more without a tile, its tiles
 // are cut into halves of 128 columns (launch_pair).
 //
+// The end.  Arrivals on the other CTA's barriers and copies that count there may still
+// be under way when a CTA has nothing left to do, and the cluster barrier alone (relaxed:
+// a release would wait for the stores of out) orders none of them.  So each CTA first
+// waits for everything that is sent to it: the producer for its last `empty` phases and
+// `drained`, the issuer for the last `d_free` phases, the warps of sums have seen every
+// `d_full`, and the products every `full`.  Where a wait gave up, either CTA tells the
+// other, and the first one then waits for the copies of both before the pair ends.
+//
 // What bounds 256 columns: a block's products take about 640 cycles back to back, but
 // with two TMEM buffers a block also waits for half of the way round a buffer: products
 // until their sums are seen (820 cycles), reading (450), hand-back to the issuer (250).
@@ -225,6 +233,10 @@ struct MmCfg {
   static constexpr int BYTES = 1024 + NS * STAGE + OUT + 512;
   static_assert(BYTES <= 227 * 1024, "shared memory of an SM");
 };
+
+// The last wait of a producer, in ns: longer than the waits of the issuer that it
+// depends on take to give up (kWaitLimitCycles, about 2 s).
+constexpr uint64_t kPairLastWait = 5000000000ull;
 
 namespace pair {
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
@@ -264,6 +276,15 @@ __device__ __forceinline__ void load_2d(void* dst, const CUtensorMap* map, int x
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
+// A word of either CTA's shared memory (this CTA's address of it).
+__device__ __forceinline__ void store_word(volatile int* at, uint32_t rank, int value) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(mapa_u32(umma::smem_u32(const_cast<int*>(at)), rank)), "r"(value) : "memory");
+}
+// Count `bytes` that never arrive as arrived.
+__device__ __forceinline__ void complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(umma::smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive_release() { asm volatile("barrier.cluster.arrive.release;\n" ::: "memory"); }
 }  // namespace pair
 
 // The tiles of a pair: tile first, first + step, ... of the whole ones, then (CUT) a half.
@@ -301,6 +322,8 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
   uint64_t* drained = d_free + C::NB;                         // every product finished
   uint32_t* tslot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
+  volatile int* issued = abort_flag + 1;                      // [2] blocks that each CTA has copied, in both
+  static_assert(8 * (2 * C::NS + 2 * C::NB + 1) + 4 * 4 <= 512, "they fit");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster_rank();
   MmTile<CUT> tile;
@@ -349,9 +372,11 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
             pair::load_2d(st + 128 * kMmBlock, half ? &p.th : &p.tb, j * kMmBlock, n0, bar);
           }
         }
-        // no copy is in flight when the pair ends (matters when a wait gave up)
-        if (rank == 0)
-          for (int i = max(0, it - C::NS); i < it; ++i) (void)umma::mbar_wait(&full[i % C::NS], (i / C::NS) & 1, 100000000ull);
+#pragma unroll 1
+        for (int i = max(0, it - C::NS); ok && i < it; ++i) ok = wait_fast(&empty[i % C::NS], (i / C::NS) & 1, abort_flag);
+        (void)umma::mbar_wait(drained, 0, kPairLastWait);
+        pair::store_word(issued + rank, 0, it);
+        pair::store_word(issued + rank, 1, it);
       }
     } else if (warp == 1 && rank == 0) {
       constexpr uint32_t ID = umma::idesc(umma::FMT_E4M3, umma::FMT_E4M3, umma::MAJOR_K, umma::MAJOR_K, 256, BN);
@@ -384,11 +409,12 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
             pair::mma_commit(&empty[s]);
           }
         }
+        // all issued products complete before TMEM is released
+        pair::mma_commit(drained);
+        (void)umma::mbar_wait(drained, 0, 100000000ull);
+#pragma unroll 1
+        for (int i = max(0, it - C::NB); ok && i < it; ++i) ok = wait_fast(&d_free[i % C::NB], (i / C::NB) & 1, abort_flag);
       }
-      // all issued products complete before TMEM is released
-      __syncwarp();
-      if (elect_one()) pair::mma_commit(drained);
-      (void)umma::mbar_wait(drained, 0, 100000000ull);
     }
   } else {
     regs_inc<232>();
@@ -463,12 +489,31 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
     if (!ok && lane == 0) raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
   }
-  // neither CTA's shared memory or TMEM is in use by the other any more (nothing is
-  // published: a release would wait for the stores of out)
+  // neither CTA's shared memory or TMEM is in use by the other any more
   umma::fence_before_sync();
   __syncwarp();
-  cluster_arrive_relaxed();
+  const bool gave_up = *abort_flag;
+  if (gave_up && lane == 0) pair::store_word(abort_flag, cluster_rank() ^ 1, 1);
+  if (gave_up || warp == 0) pair::cluster_arrive_release();   // (warp 0 has stored no rows of out)
+  else cluster_arrive_relaxed();
   cluster_wait();
+  if (*abort_flag) {                                          // (in both CTAs alike)
+    if (cluster_rank() == 0 && threadIdx.x == 0) {
+      const int n0 = issued[0], n1 = issued[1], top = max(n0, n1);
+#pragma unroll 1
+      for (int i = max(0, top - C::NS); i < top; ++i) {
+        const int s = i % C::NS;
+        (void)tile.get(p, BN, i / p.kb);
+        const uint32_t bytes = CUT && tile.half ? (128 + 64) * kMmBlock : C::STAGE;    // of one CTA
+        if (i >= n0) tma::arrive_expect_tx(&full[s], bytes);
+        else if (i >= n1) pair::complete_tx(&full[s], bytes);
+        (void)umma::mbar_wait(&full[s], (i / C::NS) & 1, 100000000ull);
+      }
+    }
+    __syncwarp();
+    pair::cluster_arrive_release();
+    cluster_wait();
+  }
   umma::fence_after_sync();
   if (warp == 1) pair::tmem_dealloc(tmem, 512);
 }
