@@ -22,6 +22,9 @@
 namespace fp8kv {
 
 constexpr int kMmBlock = 128;            // elements of a block of K: one 128-byte swizzled row
+// A CTA's last wait for what another of its cluster sends, in ns: longer than the other
+// takes to give up where its waits run out (kWaitLimitCycles, about 2 s) and send.
+constexpr uint64_t kMmLastWait = 5000000000ull;
 
 struct MatmulParams {
   CUtensorMap ta, tb, to;
@@ -234,10 +237,6 @@ struct MmCfg {
   static_assert(BYTES <= 227 * 1024, "shared memory of an SM");
 };
 
-// The last wait of a producer, in ns: longer than the waits of the issuer that it
-// depends on take to give up (kWaitLimitCycles, about 2 s).
-constexpr uint64_t kPairLastWait = 5000000000ull;
-
 namespace pair {
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(umma::smem_u32(dst_smem)), "r"(ncols));
@@ -374,7 +373,7 @@ __global__ void __launch_bounds__(MmCfg<BN>::THREADS, 1) block_matmul_pair(const
         }
 #pragma unroll 1
         for (int i = max(0, it - C::NS); ok && i < it; ++i) ok = wait_fast(&empty[i % C::NS], (i / C::NS) & 1, abort_flag);
-        (void)umma::mbar_wait(drained, 0, kPairLastWait);
+        (void)umma::mbar_wait(drained, 0, kMmLastWait);
         pair::store_word(issued + rank, 0, it);
         pair::store_word(issued + rank, 1, it);
       }
@@ -806,7 +805,7 @@ __global__ void __launch_bounds__(MfCfg<MT>::THREADS, MfCfg<MT>::CTAS) block_mat
     ok = wait_cluster(landed, 0, abort_flag);
     if (!ok) {                                                // (and nothing lands behind this CTA's end)
       raise_error(p.a.err, FP8KV_DEVERR_TIMEOUT);
-      (void)umma::mbar_wait(landed, 0, 100000000ull);
+      (void)umma::mbar_wait(landed, 0, kMmLastWait);
     }
   }
   // this rank's columns (rows of out), four neighbouring columns of out a thread; the
