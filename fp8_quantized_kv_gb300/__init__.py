@@ -517,22 +517,25 @@ def fp8kv_chunk_attention(q: torch.Tensor, cache: Fp8KVCache, cu_q: Optional[tor
 
 
 def fp8kv_tree_tables(parents: torch.Tensor, cu_new: torch.Tensor, seq_lens: torch.Tensor, max_nodes: int,
-                      masks: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None, stream=None):
+                      masks: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None, stream=None, window: int = 0,
+                      sinks: int = 0):
     """Masks and positions of trees of drafted tokens: parents [n] int32 (of
     row cu_new[b] + i: index of node i's parent within its tree, -1: none),
     cu_new [B + 1], seq_lens [B] int32 (nodes counted).  max_nodes: nodes that a
     row of bits has room for.  Returns masks [n, ceil(max_nodes / 32)] int32 (bit
     i: node i, the node itself or an ancestor) and pos [n] int32 (context length +
-    depth); rows of no tree get no bits and -1."""
+    depth); rows of no tree get no bits and -1.  window > 0: ancestors `window` or
+    more positions above a node have no bit, unless they are among the first `sinks`
+    tokens (fp8kv_tree_attention itself hides no node under a window)."""
     n, B, words, dev, i32 = parents.numel(), seq_lens.numel(), (int(max_nodes) + 31) // 32, torch.cuda.current_device(), torch.int32
     if masks is None or pos is None:
         with _on(stream):
             masks = torch.empty((n, words), dtype=i32, device=parents.device) if masks is None else masks
             pos = torch.empty(n, dtype=i32, device=parents.device) if pos is None else pos
-    _check(get_lib().fp8kv_tree_tables(
+    _check(get_lib().fp8kv_tree_tables_window(
         _here(parents, i32, "parents", dev, (n,)), _here(cu_new, i32, "cu_new", dev, (B + 1,)), _here(seq_lens, i32, "seq_lens", dev, (B,)),
-        B, n, words, _here(masks, i32, "masks", dev, (n, words)), _here(pos, i32, "pos", dev, (n,)), _raw_stream(stream, dev)),
-        "fp8kv_tree_tables")
+        B, n, words, window, sinks, _here(masks, i32, "masks", dev, (n, words)), _here(pos, i32, "pos", dev, (n,)),
+        _raw_stream(stream, dev)), "fp8kv_tree_tables")
     return masks, pos
 
 

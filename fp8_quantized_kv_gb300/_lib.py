@@ -31,6 +31,7 @@ EXPORTS = (
     "fp8kv_chunk_workspace_bytes",
     "fp8kv_chunk_attention",
     "fp8kv_tree_tables",
+    "fp8kv_tree_tables_window",
     "fp8kv_tree_workspace_bytes",
     "fp8kv_tree_attention",
     "fp8kv_tree_accept",
@@ -100,6 +101,7 @@ def get_lib() -> ctypes.CDLL:
         "fp8kv_chunk_workspace_bytes": (sz, [cp, i64, i32, i32, i32, i32, i32]),
         "fp8kv_chunk_attention": (i32, [vp, cp, vp, vp, i64, i32, f32, i32, i32, i32, i32, vp, sz, vp, i32, vp]),
         "fp8kv_tree_tables": (i32, [vp, vp, vp, i32, i64, i32, vp, vp, vp]),
+        "fp8kv_tree_tables_window": (i32, [vp, vp, vp, i32, i64, i32, i32, i32, vp, vp, vp]),
         "fp8kv_tree_workspace_bytes": (sz, [cp, i64, i32, i32, i32, i32, i32]),
         "fp8kv_tree_attention": (i32, [vp, cp, vp, vp, vp, i32, vp, i64, i32, f32, i32, i32, i32, i32, vp, sz, vp, i32, vp]),
         "fp8kv_tree_accept": (i32, [vp, i32, vp, vp, vp, vp, vp, i32, i64, i32, vp, vp, vp, vp, vp]),

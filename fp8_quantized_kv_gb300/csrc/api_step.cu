@@ -404,7 +404,13 @@ fp8kv_status fp8kv_tree_attention(const void* q, const fp8kv_cache* cache, const
 fp8kv_status fp8kv_tree_tables(const int32_t* parents, const int32_t* cu_new, const int32_t* seq_lens, int32_t batch,
                                int64_t n_rows, int32_t mask_words, uint32_t* masks, int32_t* pos,
                                fp8kv_stream_t stream) {
-  if (batch < 0 || n_rows < 0 || mask_words < 1 || !cu_new) return FP8KV_ERR_INVALID_ARG;
+  return fp8kv_tree_tables_window(parents, cu_new, seq_lens, batch, n_rows, mask_words, 0, 0, masks, pos, stream);
+}
+
+fp8kv_status fp8kv_tree_tables_window(const int32_t* parents, const int32_t* cu_new, const int32_t* seq_lens,
+                                      int32_t batch, int64_t n_rows, int32_t mask_words, int32_t window, int32_t sinks,
+                                      uint32_t* masks, int32_t* pos, fp8kv_stream_t stream) {
+  if (batch < 0 || n_rows < 0 || mask_words < 1 || window < 0 || sinks < 0 || !cu_new) return FP8KV_ERR_INVALID_ARG;
   if (mask_words > kTreeMaxNodes / 32 || n_rows > INT32_MAX || batch > INT32_MAX - 64) return FP8KV_ERR_UNSUPPORTED;
   if (batch > 0 && !seq_lens) return FP8KV_ERR_INVALID_ARG;
   if (n_rows == 0) return FP8KV_OK;
@@ -429,6 +435,8 @@ fp8kv_status fp8kv_tree_tables(const int32_t* parents, const int32_t* cu_new, co
   p.batch = batch;
   p.rows = (int)n_rows;
   p.words = mask_words;
+  p.window = window;
+  p.sinks = sinks;
   return cuda_status(launch_tree_tables(p, (cudaStream_t)stream));
 }
 

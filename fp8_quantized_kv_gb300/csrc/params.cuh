@@ -82,6 +82,7 @@ struct TreeTablesParams {
   int32_t* pos;                     // [rows]
   unsigned int* err;
   int batch, rows, words;
+  int window, sinks;                // 0: no window
 };
 
 // What the accepted rows of one layer's cache are moved in.

@@ -6,7 +6,8 @@
 
 namespace fp8kv {
 
-// Masks and positions.  Row i of sequence b: bits of node i and of its ancestors,
+// Masks and positions.  Row i of sequence b: bits of node i and of its ancestors (under
+// a window W those less than W positions above it or among the first `sinks` tokens),
 // and ctx + depth.  A thread walks up from its node in shared memory (parents come
 // before their children, so the walk ends) and writes its words from the highest
 // down: ancestors only get lower.  Latency bounds it: offsets, parents, then the
@@ -14,6 +15,7 @@ namespace fp8kv {
 // on 40 levels: 5.8 us, one at a time 6.6; 64 trees of 24-64 nodes: 2.5 and 2.3).
 constexpr int kTreeThreads = 256;
 
+template <bool WINDOW>
 __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTablesParams p) {
   __shared__ int16_t up[kTreeMaxNodes];
   __shared__ short2 two[kTreeMaxNodes];            // parent and its parent, -1: none
@@ -64,15 +66,27 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTab
     uint32_t* row = p.masks + (int64_t)(q0 + i) * p.words;
     int w = p.words - 1, depth = -1;
     uint32_t bits = 0;
-    auto sees = [&](int a) {                       // (-1: no more)
+    auto climb = [&](auto&& sees) {                // (-1: no more)
+      sees(i);
+      for (short4 a = four[i]; sees(a.x) && sees(a.y) && sees(a.z) && sees(a.w); a = four[a.w]) {}
+    };
+    // under a window: ancestors at depths from `reach` on, or below `early`, are seen
+    int reach = 0, early = 0;
+    if constexpr (WINDOW) {                        // (the node's own depth first)
+      climb([&](int a) { depth += a >= 0; return a >= 0; });
+      reach = depth - p.window + 1;
+      early = p.sinks - (len - n);
+    }
+    [[maybe_unused]] const int own = depth;
+    depth = -1;
+    climb([&](int a) {
       if (a < 0) return false;
+      ++depth;                                     // steps above the node
+      if (WINDOW && own - depth < reach && own - depth >= early) return true;
       for (; w > a >> 5; --w) { row[w] = bits; bits = 0; }
       bits |= 1u << (a & 31);
-      ++depth;
       return true;
-    };
-    sees(i);
-    for (short4 a = four[i]; sees(a.x) && sees(a.y) && sees(a.z) && sees(a.w); a = four[a.w]) {}
+    });
     for (; w >= 0; --w) { row[w] = bits; bits = 0; }
     p.pos[q0 + i] = len - n + depth;
   }
@@ -80,7 +94,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_tables_kernel(const TreeTab
 
 cudaError_t launch_tree_tables(const TreeTablesParams& p, cudaStream_t st) {
   const int pad = p.rows / 1024 < 8 ? p.rows / 1024 + 1 : 8;
-  tree_tables_kernel<<<p.batch + pad, kTreeThreads, 0, st>>>(p);
+  (p.window > 0 ? tree_tables_kernel<true> : tree_tables_kernel<false>)<<<p.batch + pad, kTreeThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -542,12 +542,23 @@ FP8KV_API fp8kv_status fp8kv_tree_tables(const int32_t *parents, const int32_t *
                                          int32_t mask_words, uint32_t *masks, int32_t *pos,
                                          fp8kv_stream_t stream);
 
+/* The same for a model with a sliding window (0: none): an ancestor has a bit only if
+ * its position is above pos - window or below `sinks`, as in fp8kv_chunk_attention.
+ * A tree that is no deeper than the window has the masks of fp8kv_tree_tables. */
+FP8KV_API fp8kv_status fp8kv_tree_tables_window(const int32_t *parents, const int32_t *cu_new,
+                                                const int32_t *seq_lens, int32_t batch,
+                                                int64_t n_rows, int32_t mask_words, int32_t window,
+                                                int32_t sinks, uint32_t *masks, int32_t *pos,
+                                                fp8kv_stream_t stream);
+
 /* Attention of the nodes of trees over the cache, which must hold them already.
  * Node i of a sequence sees the context (under a window W the tokens
  * j > pos - W or j < sinks of it), the nodes of its row of masks, and itself,
  * whether its own bit is set or not.  Bits may name later nodes too; those of
- * nodes that the tree does not have are not looked at.  Nodes are never hidden by
- * the window.
+ * nodes that the tree does not have are not looked at.  The window hides tokens of
+ * the context alone: which nodes a node sees is for its bits to say, and those of
+ * fp8kv_tree_tables_window give what decoding the same tokens one by one gives, in
+ * trees deeper than the window too.
  *   masks, mask_words: as fp8kv_tree_tables writes them
  *   pos:        [total_q] int32, positions in the text (read under a window only,
  *               else may be NULL); one outside [ctx, seq_lens[b]) counts as the

@@ -95,3 +95,11 @@ def test_binding_refusals():
         pytest.skip("the message differs with a device")
     with pytest.raises((ValueError, RuntimeError, AssertionError)):
         fk.fp8kv_tree_tables(i32, i32, i32, 32)
+
+
+@pytest.mark.parametrize("want,kw", [(INVALID, dict(window=-1)), (INVALID, dict(sinks=-1)), (INVALID, dict(words=0)),
+                                     (INVALID, dict(masks=0x10004)), (UNSUPPORTED, dict(words=33)), (0, dict(rows=0))])
+def test_windowed_tables_refusals(lib, want, kw):  # noqa: F811
+    a = dict(parents=0x10000, cu=0x11000, lens=0x12000, batch=4, rows=16, words=2, window=8, sinks=4, masks=0x13000, pos=0x14000)
+    a.update(kw)
+    assert lib.fp8kv_tree_tables_window(*a.values(), None) == want
