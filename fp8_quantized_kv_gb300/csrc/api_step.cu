@@ -495,6 +495,17 @@ fp8kv_status fp8kv_tree_accept(const fp8kv_cache* const* caches, int32_t num_cac
     for (const Range& r : in)
       if (overlap(r, held[i])) return FP8KV_ERR_INVALID_ARG;
   }
+  // a page table among rows would be written over while another layer's CTAs read it (the
+  // layers of a model share one table: looked at once)
+  for (int i = 0; i < num_caches; ++i) {
+    const fp8kv_cache* c = caches[i];
+    if (c->layout != FP8KV_LAYOUT_PAGED || (i > 0 && c->page_table == caches[i - 1]->page_table &&
+                                            c->max_pages_per_seq == caches[i - 1]->max_pages_per_seq)) continue;
+    const Range table = {c->page_table, 4 * B * (size_t)c->max_pages_per_seq};
+    const Range* next = std::upper_bound(held, held + n_held, table, [](const Range& a, const Range& b) { return (uintptr_t)a.p < (uintptr_t)b.p; });
+    if (next != held && overlap(next[-1], table)) return FP8KV_ERR_INVALID_ARG;
+    if (next != held + n_held && overlap(*next, table)) return FP8KV_ERR_INVALID_ARG;
+  }
   p.err = device_error_ptr();
   if (!p.err) return FP8KV_ERR_CUDA;
   p.parents = parents;

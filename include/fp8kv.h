@@ -590,8 +590,9 @@ FP8KV_API size_t fp8kv_tree_workspace_bytes(const fp8kv_cache *cache, int64_t to
  * other nodes' tokens keep what they hold, behind the new length.
  *   caches:      [num_caches] pointers, the layers' caches (0 to 512; none: only
  *                the walk).  They agree in batch, layout, types and sizes of a
- *                row and page, and share no memory with each other or the other
- *                arguments (FP8KV_ERR_INVALID_ARG)
+ *                row and page; their rows and scales share no memory with each
+ *                other, a page table or the other arguments
+ *                (FP8KV_ERR_INVALID_ARG)
  *   parents, cu_new, seq_lens: as in fp8kv_tree_tables (lengths before the walk)
  *   tokens:      [n_rows] int64, the drafted token of each node
  *   choices:     [n_rows] int64, the token that the model chose to follow each

@@ -103,3 +103,15 @@ def test_windowed_tables_refusals(lib, want, kw):  # noqa: F811
     a = dict(parents=0x10000, cu=0x11000, lens=0x12000, batch=4, rows=16, words=2, window=8, sinks=4, masks=0x13000, pos=0x14000)
     a.update(kw)
     assert lib.fp8kv_tree_tables_window(*a.values(), None) == want
+
+
+def test_accept_refuses_a_page_table_among_rows(lib):  # noqa: F811
+    """The table of one layer inside the rows or scales of another (or of its own cache): those are written."""
+    paged = dict(layout=1, max_tokens=0, page_size=16, num_pages=4, max_pages_per_seq=2)
+    a = dict(k=0x100000, v=0x200000, k_scale=0x300000, v_scale=0x400000)
+    b = dict(k=0x500000, v=0x600000, k_scale=0x700000, v_scale=0x800000)
+    rows = 4 * 2 * 16                                                   # of a cache: 128 bytes of codes, 4 of scales each
+    for at in (0x100000, 0x200010, 0x300000 + 4 * rows - 16, 0x400000, 0x500000 + 128 * rows - 16, 0x700000 - 16 + 4 * rows, 0x800000 - 16):
+        first, second = _cache(**a, **paged, page_table=0x900000), _cache(**b, **paged, page_table=at)
+        assert _accept(lib, [first, second]) == INVALID and _accept(lib, [second, first]) == INVALID
+        assert _accept(lib, [first, first]) == INVALID
