@@ -17,6 +17,22 @@ bool capacity_fits(const fp8kv_cache* c) {
   return c->layout != FP8KV_LAYOUT_PAGED || (int64_t)c->max_pages_per_seq * c->page_size <= INT32_MAX;
 }
 
+// The rows and scales of a cache, up to four ranges; returns how many.
+int cache_rows_of(const fp8kv_cache* c, Range* out) {
+  const size_t per = c->layout == FP8KV_LAYOUT_PAGED ? (size_t)c->num_pages * c->page_size : (size_t)c->batch * c->max_tokens;
+  const size_t rows = c->kv_heads * per;
+  int n = 0;
+  out[n++] = {c->k, rows * c->head_dim * (c->k_scale ? 1 : 2)};
+  out[n++] = {c->v, rows * c->head_dim * (c->v_scale ? 1 : 2)};
+  if (c->k_scale) out[n++] = {c->k_scale, 4 * rows};
+  if (c->v_scale) out[n++] = {c->v_scale, 4 * rows};
+  return n;
+}
+Range cache_table_of(const fp8kv_cache* c) {
+  if (c->layout != FP8KV_LAYOUT_PAGED) return {nullptr, 0};
+  return {c->page_table, 4 * (size_t)c->batch * (size_t)c->max_pages_per_seq};
+}
+
 struct ChunkPlan { int kernel, tile_rows, tile_tokens, tiles, splits; };
 
 // How a chunk call runs, from its sizes (lengths are on the device).
@@ -181,8 +197,16 @@ fp8kv_status run_chunk(const void* q, const fp8kv_cache* cache, const int32_t* c
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return FP8KV_ERR_WORKSPACE;
   if (need > 0 && misaligned(workspace, 16)) return FP8KV_ERR_INVALID_ARG;
   const Range result = {out, (out_dtype == FP8KV_OUT_F32 ? 4 : 2) * values};
-  for (const Range& r : {Range{q, 2 * values}, result})
-    if (overlap(r, {workspace, need})) return FP8KV_ERR_INVALID_ARG;
+  const Range shares = {workspace, need};
+  if (overlap(result, shares) || overlap({q, 2 * values}, shares)) return FP8KV_ERR_INVALID_ARG;
+  // (the joining kernel reads the offsets again, behind the first rows of out)
+  Range read[7];
+  int reads = cache_rows_of(cache, read);
+  read[reads++] = cache_table_of(cache);
+  read[reads++] = {seq_lens, 4 * (size_t)cache->batch};
+  read[reads++] = {cu_q, cu_q ? 4 * ((size_t)cache->batch + 1) : 0};
+  for (int i = 0; i < reads; ++i)
+    if (overlap(read[i], result) || overlap(read[i], shares)) return FP8KV_ERR_INVALID_ARG;
   p.window = window < capacity_of(cache) ? window : 0;
   p.masks = nullptr;
   p.tree_pos = nullptr;
@@ -191,7 +215,7 @@ fp8kv_status run_chunk(const void* q, const fp8kv_cache* cache, const int32_t* c
     if (!tree->masks || misaligned(tree->masks, 4) || misaligned(tree->pos, 4)) return FP8KV_ERR_INVALID_ARG;
     if (p.window > 0 && !tree->pos) return FP8KV_ERR_INVALID_ARG;
     for (const Range& r : {Range{tree->masks, 4 * (size_t)total_q * tree->words}, Range{tree->pos, 4 * (size_t)total_q}})
-      if (overlap(r, result) || overlap(r, {workspace, need})) return FP8KV_ERR_INVALID_ARG;
+      if (overlap(r, result) || overlap(r, shares)) return FP8KV_ERR_INVALID_ARG;
     p.masks = tree->masks;
     p.tree_pos = tree->pos;
     p.mask_words = tree->words;
@@ -465,14 +489,9 @@ fp8kv_status fp8kv_tree_accept(const fp8kv_cache* const* caches, int32_t num_cac
     if (c->batch != batch || c->dtype != c0->dtype || c->layout != c0->layout || c->kv_heads != c0->kv_heads ||
         c->head_dim != c0->head_dim || c->page_size != c0->page_size)
       return FP8KV_ERR_INVALID_ARG;
-    const size_t rows = (size_t)c->kv_heads * (view.paged ? (size_t)c->num_pages * c->page_size : B * c->max_tokens);
-    held[n_held++] = {c->k, rows * c->head_dim * (c->k_scale ? 1 : 2)};
-    held[n_held++] = {c->v, rows * c->head_dim * (c->v_scale ? 1 : 2)};
-    if (c->k_scale) held[n_held++] = {c->k_scale, 4 * rows};
-    if (c->v_scale) held[n_held++] = {c->v_scale, 4 * rows};
-    const Range table = {view.page_table, 4 * B * (size_t)view.max_pages_per_seq};
+    n_held += cache_rows_of(c, held + n_held);
     for (const Range& o : out)
-      if (overlap(o, table)) return FP8KV_ERR_INVALID_ARG;
+      if (overlap(o, cache_table_of(c))) return FP8KV_ERR_INVALID_ARG;
   }
   if (batch == 0) return FP8KV_OK;
   if (!cu_new || !seq_lens || !path || !accepted || !next_tokens || !new_lens) return FP8KV_ERR_INVALID_ARG;
@@ -501,7 +520,7 @@ fp8kv_status fp8kv_tree_accept(const fp8kv_cache* const* caches, int32_t num_cac
     const fp8kv_cache* c = caches[i];
     if (c->layout != FP8KV_LAYOUT_PAGED || (i > 0 && c->page_table == caches[i - 1]->page_table &&
                                             c->max_pages_per_seq == caches[i - 1]->max_pages_per_seq)) continue;
-    const Range table = {c->page_table, 4 * B * (size_t)c->max_pages_per_seq};
+    const Range table = cache_table_of(c);
     const Range* next = std::upper_bound(held, held + n_held, table, [](const Range& a, const Range& b) { return (uintptr_t)a.p < (uintptr_t)b.p; });
     if (next != held && overlap(next[-1], table)) return FP8KV_ERR_INVALID_ARG;
     if (next != held + n_held && overlap(*next, table)) return FP8KV_ERR_INVALID_ARG;

@@ -468,10 +468,11 @@ FP8KV_API fp8kv_status fp8kv_rope_append(const fp8kv_cache *cache, const void *q
  *               16); or _TENSOR_CORES (128-row tiles on tcgen05: head_dim 128,
  *               not FP8KV_MXK8V8, else FP8KV_ERR_UNSUPPORTED)
  *   workspace:  fp8kv_chunk_workspace_bytes() bytes, 16-byte aligned, nothing
- *               need be zero; NULL if that is 0; apart from q and out.
- *               Calls that may run at once need one each.
+ *               need be zero; NULL if that is 0; apart from out and all that
+ *               the call reads.  Calls that may run at once need one each.
  *   out:        [total_q][q_heads][head_dim], bf16 or fp32 per out_dtype,
- *               16-byte aligned, apart from q
+ *               16-byte aligned, apart from all that the call reads
+ *               (FP8KV_ERR_INVALID_ARG)
  * Roundings: a weight is held in 16 bits once, f16 beside e4m3 values (2^-11 of
  * it, or 2^-31 of the largest seen value where the weighted value is that small),
  * bf16 beside bf16 values (2^-8: the matrix instructions take one 16-bit type).

@@ -115,3 +115,23 @@ def test_accept_refuses_a_page_table_among_rows(lib):  # noqa: F811
         first, second = _cache(**a, **paged, page_table=0x900000), _cache(**b, **paged, page_table=at)
         assert _accept(lib, [first, second]) == INVALID and _accept(lib, [second, first]) == INVALID
         assert _accept(lib, [first, first]) == INVALID
+
+
+@pytest.mark.parametrize("what", ["cu", "lens", "table", "k", "v_scale"])
+@pytest.mark.parametrize("end", [0, 1])
+def test_out_and_workspace_apart_from_what_is_read(lib, end, what):  # noqa: F811
+    """Offsets, lengths, page table and cache rows that out or the workspace would write
+    over: refused, in the tree and in the chunk call."""
+    far = dict(k=0x1000000, v=0x2000000, k_scale=0x3000000, v_scale=0x4000000, page_table=0x5000000)
+    out_bytes, ws_bytes = 10 * 4 * 128 * 2, 10 * 4 * 2 * 130 * 4
+    for base, size in ((0x40000, out_bytes), (0x30000, ws_bytes)):
+        at = base + (size - 16 if end else 0)
+        a = dict(cu=0x20000, lens=0x21000)
+        cache = dict(far)
+        if what in a:
+            a[what] = at
+        else:
+            cache["page_table" if what == "table" else what] = at
+        tail = (10, 4, 0.1, 0, 0, 2, 0, 0x30000, 1 << 30, 0x40000, 0, None)
+        assert lib.fp8kv_tree_attention(0x10000, _paged(**cache), a["cu"], a["lens"], 0x22000, 1, 0x23000, *tail) == INVALID
+        assert lib.fp8kv_chunk_attention(0x10000, _paged(**cache), a["cu"], a["lens"], *tail) == INVALID
