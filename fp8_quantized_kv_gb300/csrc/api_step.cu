@@ -112,8 +112,16 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
   const int64_t tiles = total_q / plan->tile_tokens + c->batch;      // at most (chunk_common.cuh)
   if (tiles > INT32_MAX) return FP8KV_ERR_UNSUPPORTED;
   plan->tiles = (int)tiles;
-  const int64_t seen = window > 0 && window < cap ? (int64_t)window + plan->tile_tokens + (sinks < cap ? sinks : cap) : cap;
-  const int64_t kv_tiles = ((seen < cap ? seen : cap) + 63) / 64 + 1;
+  // KV tiles that a tile of queries sees: under a window those of its queries, or of all
+  // nodes of its tree, whatever part of them the tile holds (on average; a call's largest
+  // tree can have all rows)
+  auto seen_by = [&](int64_t queries) {
+    const int64_t seen = window > 0 && window < cap ? (int64_t)window + queries + (sinks < cap ? sinks : cap) : cap;
+    return seen < cap ? seen : cap;
+  };
+  const int64_t seen = seen_by(tree ? (total_q + B - 1) / B : plan->tile_tokens);
+  const int64_t kv_tiles = (seen + 63) / 64 + 1;
+  const int64_t most_tiles = tree ? (seen_by(total_q < kTreeMaxNodes ? total_q : kTreeMaxNodes) + 63) / 64 + 1 : kv_tiles;
   int64_t want = num_splits;
   if (want == 0) {
     // tiles if every sequence had the average number of queries, or, if that is
@@ -156,7 +164,7 @@ fp8kv_status plan_chunk(const fp8kv_cache* c, int64_t total_q, int q_heads, int 
       }
     }
   }
-  if (want > kv_tiles) want = kv_tiles;
+  if (want > (num_splits > 0 ? most_tiles : kv_tiles)) want = num_splits > 0 ? most_tiles : kv_tiles;
   if (want > 4096) want = 4096;
   plan->splits = want < 1 ? 1 : (int)want;
   return FP8KV_OK;

@@ -9,7 +9,7 @@ import torch
 
 import fp8_quantized_kv_gb300 as fk
 from test_gpu_chunk import _i32, cache_values, make_cache
-from test_gpu_tree import ancestors, bits_of, random_tree
+from test_gpu_tree import FORMS, ancestors, bits_of, random_tree, run_case
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +65,11 @@ def test_chain_under_a_window(kernel, window, sinks):
         a = fk.fp8kv_tree_attention(q, cache, cu, lens, masks, pos=pos, **kw)
         b = fk.fp8kv_chunk_attention(q, cache, cu, lens, **kw)
         assert fk.fp8kv_get_device_error() == 0 and (a - b).abs().max().item() <= 2 * 2.0 ** -11 * most + 1e-5
+
+
+@pytest.mark.parametrize("dtype,D,kernel", FORMS)
+@pytest.mark.parametrize("splits", [0, 5])
+def test_wide_tree_under_a_small_window(dtype, D, kernel, splits):
+    """A window far smaller than the tree: its nodes are most of the keys, and the shares
+    divide them."""
+    run_case(dtype, D, 4, 2, [200, 50], [300, 9], 16, seed=21, window=32, sinks=3, kernel=kernel, splits=splits)

@@ -135,3 +135,18 @@ def test_out_and_workspace_apart_from_what_is_read(lib, end, what):  # noqa: F81
         tail = (10, 4, 0.1, 0, 0, 2, 0, 0x30000, 1 << 30, 0x40000, 0, None)
         assert lib.fp8kv_tree_attention(0x10000, _paged(**cache), a["cu"], a["lens"], 0x22000, 1, 0x23000, *tail) == INVALID
         assert lib.fp8kv_chunk_attention(0x10000, _paged(**cache), a["cu"], a["lens"], *tail) == INVALID
+
+
+def test_plan_of_wide_trees_under_a_small_window(lib):  # noqa: F811
+    """A tile of a tree sees the window and all nodes of the tree, not its own alone:
+    the split count that is asked for is used, and an automatic one counts those tiles."""
+    cache = _cache(batch=1, max_tokens=65536)
+    share = 1024 * 4 * 130 * 4                                          # bytes of one share of every row
+    for kernel in (0, 5, 2):
+        assert lib.fp8kv_tree_workspace_bytes(cache, 1024, 4, 64, 0, 10, kernel) == 10 * share
+        assert lib.fp8kv_tree_workspace_bytes(cache, 1024, 4, 64, 0, 100, kernel) == 18 * share      # (64 + 1,024 tokens: 17 tiles, or 18)
+    assert lib.fp8kv_tree_workspace_bytes(cache, 1024, 4, 64, 0, 0, 0) >= 3 * share
+    # one tree among many small ones may hold most rows
+    assert lib.fp8kv_tree_workspace_bytes(_cache(batch=8, max_tokens=8192), 1031, 4, 64, 0, 10, 0) == 10 * 1031 * 4 * 130 * 4
+    # a chunk call's tile sees its own 64 queries only: (64 + 64) / 64 tiles, or one more
+    assert lib.fp8kv_chunk_num_splits(cache, 1024, 4, 64, 0, 10, 2) == 3
