@@ -51,7 +51,9 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
                :
                : "memory");
 }
-// Columns n0 .. n0 + 63 of row m of out, as far as there are any.
+// Columns n0 .. n0 + 63 of row m of out, as far as there are any: for widths whose rows do
+// not start on 16 bytes, element by element, 32 rows an instruction (others are stored by
+// TMA).  997 x 4609 x 3584: 63 us in bf16, 39 in fp32, where 4608 columns take 17.1 and 18.5.
 __device__ __forceinline__ void store_row64(const MatmulArgs& a, int m, int n0, float2* acc) {
   const int cols = min(64, a.N - n0);
   if (cols <= 0) return;
@@ -65,31 +67,16 @@ __device__ __forceinline__ void store_row64(const MatmulArgs& a, int m, int n0, 
   const int64_t out = (int64_t)m * a.N + n0;
   if (a.out_f32) {
     float* y = reinterpret_cast<float*>(a.out) + out;
-    const bool vec = a.N % 4 == 0;
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      if (vec && 2 * c + 4 <= cols) *reinterpret_cast<float4*>(y + 2 * c) = make_float4(acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y);
-      else {
-        const float v[4] = {acc[c].x, acc[c].y, acc[c + 1].x, acc[c + 1].y};
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (2 * c + u < cols) y[2 * c + u] = v[u];
-      }
-    }
+    for (int c = 0; c < 64; ++c)
+      if (c < cols) y[c] = c & 1 ? acc[c / 2].y : acc[c / 2].x;
   } else {
     __nv_bfloat16* y = reinterpret_cast<__nv_bfloat16*>(a.out) + out;
-    const bool vec = a.N % 8 == 0;
 #pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-      __nv_bfloat162 h[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) h[u] = __floats2bfloat162_rn(acc[c + u].x, acc[c + u].y);
-      if (vec && 2 * c + 8 <= cols) *reinterpret_cast<uint4*>(y + 2 * c) = *reinterpret_cast<const uint4*>(h);
-      else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-          if (2 * c + u < cols) y[2 * c + u] = u & 1 ? h[u / 2].y : h[u / 2].x;
-      }
+    for (int c = 0; c < 32; ++c) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(acc[c].x, acc[c].y);
+      if (2 * c < cols) y[2 * c] = h.x;
+      if (2 * c + 1 < cols) y[2 * c + 1] = h.y;
     }
   }
 }
