@@ -43,3 +43,33 @@ def test_kernels_that_follow_a_pair_of_ctas():
         for out in outs[:1 + turn % 2]:
             assert all(torch.equal(o, w) for o, w in zip(out, want))
     assert fk.fp8kv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("M", [3, 12, 20, 64, 100, 200])
+@pytest.mark.parametrize("N,K", [(4096, 14336), (1000, 8192), (2050, 14224)])
+def test_long_k(M, N, K):
+    """Dozens of blocks of K in a CTA's share: every ring goes round several times, and
+    the scales of the next blocks take the place of those before."""
+    a, sa, b, sb, bias = make(M, N, K, seed=M + K, spread=5.0)
+    check(fk.fp8kv_block_matmul(a, sa, b, sb, out_dtype=torch.float32), a, sa, b, sb)
+    check(fk.fp8kv_block_matmul(a, sa, b, sb, bias=bias), a, sa, b, sb, bias)
+
+
+@pytest.mark.parametrize("M", [8, 20, 64])
+def test_long_k_and_many_columns(M):
+    """So many columns that no share of K is split off: 64 blocks one after the other."""
+    a, sa, b, sb, _ = make(M, 28672, 8192, seed=M, spread=5.0)
+    check(fk.fp8kv_block_matmul(a, sa, b, sb, out_dtype=torch.float32), a, sa, b, sb)
+
+
+@pytest.mark.parametrize("M", [20, 100, 300])
+def test_long_k_each_block_has_its_scales(M):
+    """Ones everywhere: the sum of the pairs of scales, exactly (powers of two, 112 blocks)."""
+    N, K, kb = 300, 14336, 112
+    a, b = (torch.full((r, K), 0x38, dtype=torch.uint8, device="cuda") for r in (M, N))
+    g = torch.Generator(device="cuda").manual_seed(2)
+    sa = torch.exp2(torch.randint(-3, 4, (M, kb), generator=g, device="cuda").float())
+    sb = torch.exp2(torch.randint(-3, 4, (3, kb), generator=g, device="cuda").float())
+    out = fk.fp8kv_block_matmul(a, sa, b, sb, out_dtype=torch.float32)
+    want = 128 * (sa.double() @ sb.double().T).repeat_interleave(128, 1)[:, :N]
+    assert fk.fp8kv_get_device_error() == 0 and torch.equal(out.double(), want)
