@@ -532,10 +532,13 @@ def fp8kv_tree_tables(parents: torch.Tensor, cu_new: torch.Tensor, seq_lens: tor
         with _on(stream):
             masks = torch.empty((n, words), dtype=i32, device=parents.device) if masks is None else masks
             pos = torch.empty(n, dtype=i32, device=parents.device) if pos is None else pos
-    _check(get_lib().fp8kv_tree_tables_window(
-        _here(parents, i32, "parents", dev, (n,)), _here(cu_new, i32, "cu_new", dev, (B + 1,)), _here(seq_lens, i32, "seq_lens", dev, (B,)),
-        B, n, words, window, sinks, _here(masks, i32, "masks", dev, (n, words)), _here(pos, i32, "pos", dev, (n,)),
-        _raw_stream(stream, dev)), "fp8kv_tree_tables")
+    args = (_here(parents, i32, "parents", dev, (n,)), _here(cu_new, i32, "cu_new", dev, (B + 1,)), _here(seq_lens, i32, "seq_lens", dev, (B,)),
+            B, n, words)
+    outs = (_here(masks, i32, "masks", dev, (n, words)), _here(pos, i32, "pos", dev, (n,)), _raw_stream(stream, dev))
+    if window or sinks:
+        _check(get_lib().fp8kv_tree_tables_window(*args, window, sinks, *outs), "fp8kv_tree_tables_window")
+    else:
+        _check(get_lib().fp8kv_tree_tables(*args, *outs), "fp8kv_tree_tables")
     return masks, pos
 
 
