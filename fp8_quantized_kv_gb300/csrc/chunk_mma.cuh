@@ -22,11 +22,9 @@
 // values, since the instruction takes one 16-bit type.  m, l and O are fp32.
 //
 // What bounds it: instruction issue (conversions of codes are repeated by each
-// of a tile's four warps).  4 sequences of 256-512 queries over 4,000-8,000 tokens
-// (32 / 4 heads, e4m3) take 0.56 ms; the few-row kernel, whose 16-row tiles read
-// the cache four times as often, 0.70 ms.  (At head dim 128, block-scaled keys,
-// the same call took 1.33 ms in this form and 1.15 ms there: 128 fp32 of O and
-// wider fragments left two CTAs an SM, so that form is gone.)
+// of a tile's four warps).  The few-row kernel's 16-row tiles read the cache four times
+// as often; at head dim 128 with block-scaled keys it is ahead all the same (128 fp32 of
+// O and wider fragments leave two CTAs an SM here), so that form is gone.
 //
 // Keys that a query does not see get no weight, whatever their rows hold:
 // rows that no query of the tile sees are not read at all, and in a tile that
@@ -36,8 +34,9 @@
 // Measured on one GB300 (256-512 tokens x 8 heads of 4 sequences of 4K-8K tokens, 4 KV
 // heads, e4m3): 394 us, issue slots bound it; 490 us while one form of the loop served
 // tiles that every query sees and others alike.  Trees of 33-64 nodes x 8 heads, 16
-// sequences of 2K-8K tokens: 217 us in that shape (290), two CTAs an SM at 255 registers;
-// three at 168 with spills 221.
+// sequences of 2K-8K tokens: 217 us whole in that shape (290), 181 with the plan's shares;
+// two CTAs an SM at 255 registers beside e4m3 values (three at 168 with spills 221), three
+// beside bf16 ones and in chunk calls.
 #pragma once
 
 #include <type_traits>
